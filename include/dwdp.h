@@ -63,6 +63,8 @@ extern "C" {
 #define DWDP_MAX_TOPK 32
 #define DWDP_MAX_LAYERS 256
 #define DWDP_MAX_PEERS 64
+#define DWDP_MAX_GROUPS 32
+#define DWDP_MAX_LORA_RANK 128
 
 typedef struct dwdp_ctx dwdp_ctx;
 /* Same object as cudaStream_t; NULL = the legacy default stream. */
@@ -457,6 +459,116 @@ int32_t dwdp_plan_prefetch(int32_t n_experts, int32_t hidden, int32_t inter, int
  * Errors: INVALID_ARG. */
 int32_t dwdp_group_map(int32_t n_experts, int32_t n_ranks, int32_t rank, int32_t* local_slot, int32_t* peer_id,
                        int32_t* peer_slot);
+
+/* ---- the rest of a decoder block's second half --------------------------
+ * The three calls below surround dwdp_moe_layer in a decoder block: the
+ * adapters of the attention's output projection (the projection itself is
+ * dwdp_grouped_gemm with one group), the residual addition with the norm, and
+ * the router of the R1 models.  They serve (no gradients), for one token as
+ * for many, and can be captured into CUDA graphs. */
+
+/* Residual addition and root-mean-square norm, optionally also as E4M3 rows
+ * for dwdp_moe_layer_codes.  Per row of H elements, with h = x + residual
+ * (h = x when residual is NULL):
+ *   residual_out = bf16(h)                        (iff residual is given)
+ *   y   = h / sqrt(mean(h^2) + eps) * weight      binary32, from the unrounded h
+ *   out = bf16(y)
+ *   row_scale = max|y| / 448 (1 for an all-zero row),
+ *   codes = E4M3(y / row_scale)                   (iff codes is given)
+ * The codes come from the unrounded y: one rounding, to nearest even.  A row
+ * whose largest |h weight| is below 2^-100 is quantized as if it were 2^-100.
+ * The squares are summed in binary32, scaled where they would pass its range.
+ * A NaN makes its row of out, and its row_scale, NaN.
+ * x: bf16, row r at x + r * x_stride elements (x_stride >= H, a multiple of
+ * 8); residual, residual_out, out: bf16 [rows][H]; weight: bf16 [H]; codes:
+ * E4M3 bytes [rows][H]; row_scale: fp32 [rows].  Either of residual and
+ * residual_out NULL means both are; likewise codes and row_scale.
+ * residual_out may be residual, and out may be x when x_stride == H; no other
+ * overlap.  H a multiple of 8, 8 <= H <= 32768; eps >= 0 and finite; rows in
+ * [0, 2^31).  All pointers device, 16-byte aligned.  Enqueued on `stream`;
+ * needs no context.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int32_t dwdp_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, void* residual_out,
+                         const void* weight, float eps, int64_t rows, int32_t H, void* out, void* codes,
+                         float* row_scale, dwdp_stream_t stream);
+
+/* How dwdp_route_scored scores, chooses and weighs.
+ *   score        DWDP_SCORE_SOFTMAX (over all E) or DWDP_SCORE_SIGMOID
+ *   n_groups     experts e / (E / n_groups) form a group; divides E, 1 = none
+ *   top_groups   groups a token may choose from, 1..n_groups
+ *   group_score  DWDP_GROUP_MAX: a group's largest choice value;
+ *                DWDP_GROUP_TOP2: the sum of its two largest (of its one)
+ *   renormalize  1: the k weights are divided by their sum; 0: as scored
+ *   scale        factor on the weights, finite and > 0 */
+#define DWDP_SCORE_SOFTMAX 0
+#define DWDP_SCORE_SIGMOID 1
+#define DWDP_GROUP_MAX 0
+#define DWDP_GROUP_TOP2 1
+typedef struct {
+    int32_t score;
+    int32_t n_groups;
+    int32_t top_groups;
+    int32_t group_score;
+    int32_t renormalize;
+    float scale;
+} dwdp_scoring;
+
+/* Routing as the R1 models do it, with dwdp_route's outputs.  With the fp32
+ * logits z = x W^T:
+ *   s = softmax(z) or sigmoid(z);  c = s + choice_bias (NULL = 0)
+ *   the top_groups groups with the largest group score of c stay;
+ *   the k largest c in them are chosen; topk_w = s of the chosen
+ *   (divided by their sum if renormalize) * scale.
+ * Ties go to the lowest group and expert id.  choice_bias [E] fp32 (device)
+ * steers the choice only, not the weights; -inf takes an expert out: it is
+ * chosen only where fewer than k others are left, and then has weight 0.  The
+ * choice is the one these formulas give in binary64 on the fp32 logits (a
+ * token whose decision binary32 cannot tell apart is decided again in
+ * binary64), so it depends on the logits alone.  The logits are deterministic
+ * for a given device and shape; out->logits (NULL = not returned) gets them.
+ * A token with a logit that is not finite, or a bias that is NaN or +inf, is
+ * treated as in dwdp_route: k distinct experts, DEVICE_CHECK.
+ * x, w_router, out, ws, T as for dwdp_route; k <= top_groups * E / n_groups;
+ * n_groups <= DWDP_MAX_GROUPS.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router,
+                          const float* choice_bias, const dwdp_scoring* scoring, const dwdp_route_out* out,
+                          void* ws, size_t ws_bytes, dwdp_stream_t stream);
+
+/* Low-rank adapters of many requests beside a shared projection.  For token t
+ * with adapter i = adapter_ids[t]:
+ *   out[t] = bf16(base[t] + adapter_scale[i] * (x[t] A_i^T) B_i^T)
+ * and out[t] = base[t] where i is -1 (no adapter).  The inner product is
+ * summed in fp32, scaled and rounded once to bf16 (it is the second product's
+ * operand); the second is summed in fp32 on top of base, rounded once.
+ * a: bf16 [n_adapters][R][K]; b: bf16 [n_adapters][N][R]; adapter_scale fp32
+ * [n_adapters]; adapter_ids int32 [T] (all device).  Adapters of a smaller
+ * rank are padded with zero rows (columns).  Tokens may come in any order;
+ * tokens of one adapter next to each other are the cheap case.  x: row t at
+ * x + t * x_stride elements, K of them; base and out: row t at t *
+ * base_stride / t * out_stride, N of them; every stride a multiple of 8 and
+ * no smaller than the row.  out may be base (equal strides); no other
+ * overlap.  K, N multiples of 8; R a multiple of 8, 8..DWDP_MAX_LORA_RANK.  An id
+ * outside [-1, n_adapters) is not followed: the token gets base and the
+ * device error word reports a bad index (DEVICE_CHECK).  ws: at least
+ * dwdp_lora_workspace_bytes(T, K, N, R) bytes, device.  All pointers 16-byte
+ * aligned.  Enqueued on `stream`.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T, int32_t K, int32_t N,
+                      const void* a, const void* b, const float* adapter_scale, int32_t n_adapters, int32_t R,
+                      const int32_t* adapter_ids, const void* base, int64_t base_stride, void* out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, dwdp_stream_t stream);
+
+/* Workspace of dwdp_lora_add; 0 for sizes it refuses. */
+size_t dwdp_lora_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t R);
+
+/* dwdp_moe_layer of an E4M3 context on rows that are E4M3 already: xq [T][H]
+ * codes and sx [T] fp32 row scales (x = code * scale), e.g. those of
+ * dwdp_add_rmsnorm, which are the more exact ones (rounded once, from the
+ * norm's unrounded rows).  Everything else is as for dwdp_moe_layer; xq must
+ * be device memory of the context's device.  The workspace regions XQ and SX
+ * stay unwritten.  Errors: INVALID_ARG (also: the context is not E4M3),
+ * NOT_MAPPED, UNSUPPORTED, CUDA. */
+int32_t dwdp_moe_layer_codes(dwdp_ctx* ctx, int32_t layer, int32_t stage, const void* xq, const float* sx,
+                             int32_t T, const dwdp_route_out* route, void* out, void* ws, size_t ws_bytes,
+                             dwdp_stream_t stream);
 
 #ifdef __cplusplus
 }

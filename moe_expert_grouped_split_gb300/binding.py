@@ -21,6 +21,8 @@ EPI_BF16, EPI_SILU, EPI_F32 = 0, 1, 2
 DWDP_PHASE_EVENTS = 7  # dwdp_set_phase_events: route start/end, rows in expert order, stage waited for, gate/up, down, combine
 DTYPE_BF16, DTYPE_E4M3, DTYPE_NVFP4 = 0, 1, 2
 FLAG_WIDE_EPILOGUE = 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 
 
 def weight_slot_bytes(rows: int, K: int, weight_dtype: int) -> int:
@@ -53,6 +55,11 @@ class dwdp_route_out(ctypes.Structure):
     _fields_ = [("topk_ids", ctypes.c_void_p), ("topk_w", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("perm", ctypes.c_void_p), ("inv_perm", ctypes.c_void_p),
                 ("logits", ctypes.c_void_p)]
+
+
+class dwdp_scoring(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class dwdp_copy_slice(ctypes.Structure):
@@ -93,6 +100,15 @@ SIGNATURES = [
     ("dwdp_workspace_region", _I32, [_VP, _I32, _I32, ctypes.POINTER(ctypes.c_size_t),
                                      ctypes.POINTER(ctypes.c_size_t)]),
     ("dwdp_quantize_rows", _I32, [_I32, _VP, ctypes.c_int64, _I32, _VP, _VP, _VP, _VP]),
+    ("dwdp_add_rmsnorm", _I32, [_VP, ctypes.c_int64, _VP, _VP, _VP, ctypes.c_float, ctypes.c_int64, _I32, _VP, _VP,
+                                _VP, _VP]),
+    ("dwdp_route_scored", _I32, [_VP, _VP, _I32, _VP, _VP, ctypes.POINTER(dwdp_scoring),
+                                 ctypes.POINTER(dwdp_route_out), _VP, ctypes.c_size_t, _VP]),
+    ("dwdp_lora_add", _I32, [_VP, _VP, ctypes.c_int64, _I32, _I32, _I32, _VP, _VP, _VP, _I32, _I32, _VP, _VP,
+                             ctypes.c_int64, _VP, ctypes.c_int64, _VP, ctypes.c_size_t, _VP]),
+    ("dwdp_lora_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
+    ("dwdp_moe_layer_codes", _I32, [_VP, _I32, _I32, _VP, _VP, _I32, ctypes.POINTER(dwdp_route_out), _VP, _VP,
+                                    ctypes.c_size_t, _VP]),
     ("dwdp_plan_prefetch", _I32, [_I32, _I32, _I32, _I32, _I32P, _I32P, _I32P, _I32, ctypes.c_size_t,
                                   ctypes.POINTER(dwdp_copy_slice), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
 ]
@@ -209,6 +225,42 @@ def dwdp_prefetch_layer(ctx, layer, stage, chunk_bytes, copy_streams) -> None:
 def dwdp_moe_layer(ctx, layer, stage, x, T, route: dwdp_route_out, out, ws, ws_bytes, stream=None) -> None:
     _check(ctx, lib().dwdp_moe_layer(ctx, layer, stage, _ptr(x), T, ctypes.byref(route), _ptr(out), _ptr(ws),
                                      ws_bytes, _stream(stream)))
+
+
+def dwdp_moe_layer_codes(ctx, layer, stage, xq, sx, T, route: dwdp_route_out, out, ws, ws_bytes,
+                         stream=None) -> None:
+    _check(ctx, lib().dwdp_moe_layer_codes(ctx, layer, stage, _ptr(xq), _ptr(sx), T, ctypes.byref(route), _ptr(out),
+                                           _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dwdp_add_rmsnorm(x, rows, H, weight, eps, out, residual=None, residual_out=None, codes=None, row_scale=None,
+                     x_stride=None, stream=None) -> None:
+    """x_stride: elements between x's rows (None: H)."""
+    _check(None, lib().dwdp_add_rmsnorm(_ptr(x), H if x_stride is None else x_stride, _ptr(residual),
+                                        _ptr(residual_out), _ptr(weight), eps, rows, H, _ptr(out), _ptr(codes),
+                                        _ptr(row_scale), _stream(stream)))
+
+
+def scoring(score=SCORE_SOFTMAX, n_groups=1, top_groups=1, group_score=GROUP_MAX, renormalize=True,
+            scale=1.0) -> dwdp_scoring:
+    return dwdp_scoring(score, n_groups, top_groups, group_score, 1 if renormalize else 0, scale)
+
+
+def dwdp_route_scored(ctx, x, T, w_router, choice_bias, how: dwdp_scoring, out: dwdp_route_out, ws, ws_bytes,
+                      stream=None) -> None:
+    _check(ctx, lib().dwdp_route_scored(ctx, _ptr(x), T, _ptr(w_router), _ptr(choice_bias), ctypes.byref(how),
+                                        ctypes.byref(out), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dwdp_lora_workspace_bytes(T, K, N, R) -> int:
+    return lib().dwdp_lora_workspace_bytes(T, K, N, R)
+
+
+def dwdp_lora_add(ctx, x, x_stride, T, K, N, a, b, adapter_scale, n_adapters, R, adapter_ids, base, base_stride, out,
+                  out_stride, ws, ws_bytes, stream=None) -> None:
+    _check(ctx, lib().dwdp_lora_add(ctx, _ptr(x), x_stride, T, K, N, _ptr(a), _ptr(b), _ptr(adapter_scale),
+                                    n_adapters, R, _ptr(adapter_ids), _ptr(base), base_stride, _ptr(out), out_stride,
+                                    _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def dwdp_wait_stage(ctx, stage, timeout_ms) -> int:
@@ -343,10 +395,11 @@ class RouteBuffers:
 
 class Runtime:
     """One dwdp context with its stage buffers (two by default) and a
-    workspace (torch allocations); methods forward to the C ABI."""
+    workspace (torch allocations; at least min_ws_bytes, e.g. what
+    dwdp_lora_workspace_bytes asks for); methods forward to the C ABI."""
 
     def __init__(self, hidden, inter, n_experts, top_k, n_shared, max_tokens, n_layers, stage_slots,
-                 device="cuda", weight_dtype=DTYPE_BF16, n_stages=2, flags=0):
+                 device="cuda", weight_dtype=DTYPE_BF16, n_stages=2, flags=0, min_ws_bytes=0):
         import torch
         self.cfg = dict(hidden=hidden, inter=inter, n_experts=n_experts, top_k=top_k, n_shared=n_shared,
                         max_tokens=max_tokens, n_layers=n_layers, stage_slots=stage_slots)
@@ -363,7 +416,7 @@ class Runtime:
             self.stage_w2 = [None] * n_stages
         self.ctx = dwdp_create(hidden, inter, n_experts, top_k, n_shared, max_tokens, n_layers, stage_slots,
                                self.stage_w13, self.stage_w2, weight_dtype, n_stages, flags)
-        self.ws_bytes = max(256, dwdp_workspace_bytes(self.ctx, max_tokens))
+        self.ws_bytes = max(256, dwdp_workspace_bytes(self.ctx, max_tokens), min_ws_bytes)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self._keep = {}
 
@@ -383,6 +436,20 @@ class Runtime:
 
     def moe(self, layer, stage, x, rb: RouteBuffers, out, stream=None) -> None:
         dwdp_moe_layer(self.ctx, layer, stage, x, x.shape[0], rb.c, out, self.ws, self.ws_bytes, stream)
+
+    def route_scored(self, x, w_router, choice_bias, how: dwdp_scoring, rb: RouteBuffers, stream=None) -> None:
+        dwdp_route_scored(self.ctx, x, x.shape[0], w_router, choice_bias, how, rb.c, self.ws, self.ws_bytes, stream)
+
+    def moe_codes(self, layer, stage, xq, sx, rb: RouteBuffers, out, stream=None) -> None:
+        dwdp_moe_layer_codes(self.ctx, layer, stage, xq, sx, xq.shape[0], rb.c, out, self.ws, self.ws_bytes, stream)
+
+    def lora_add(self, x, a, b, adapter_scale, adapter_ids, base, out, stream=None) -> None:
+        """x [T, K], base and out [T, N] (row strides as the tensors have
+        them), a [n, R, K] and b [n, N, R] contiguous."""
+        T, K = x.shape
+        n, R, _ = a.shape
+        dwdp_lora_add(self.ctx, x, x.stride(0), T, K, b.shape[1], a, b, adapter_scale, n, R, adapter_ids, base,
+                      base.stride(0), out, out.stride(0), self.ws, self.ws_bytes, stream)
 
     def prefetch(self, layer, stage, chunk_bytes, copy_streams) -> None:
         dwdp_prefetch_layer(self.ctx, layer, stage, chunk_bytes, copy_streams)

@@ -308,6 +308,228 @@ int32_t check_device_error_word(dwdp_ctx* ctx) {
     return DWDP_OK;
 }
 
+// The argument checks dwdp_route and dwdp_route_scored share.  T = 0 is done
+// here (empty set): nothing is routed.
+int32_t check_route(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router, const float* bias,
+                    const dwdp_route_out* out, const void* ws, size_t ws_bytes, cudaStream_t stream, bool& empty) {
+    const dwdp_config& c = ctx->cfg;
+    if (T < 0 || T > c.max_tokens) return fail(ctx, DWDP_ERR_INVALID_ARG, "T=%d outside [0, max_tokens]", T);
+    if (!out || !out->topk_ids || !out->topk_w || !out->counts || !out->offsets || !out->perm || !out->inv_perm)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "route outputs must not be NULL (except logits)");
+    if (!aligned16(out->topk_ids) || !aligned16(out->topk_w) || !aligned16(out->counts) ||
+        !aligned16(out->offsets) || !aligned16(out->perm) || !aligned16(out->inv_perm) ||
+        (out->logits && !aligned16(out->logits)) || (bias && !aligned16(bias)))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "route pointers must be 16-byte aligned");
+    if (T == 0) {
+        empty = true;
+        DWDP_CUDA(ctx, cudaMemsetAsync(out->counts, 0, sizeof(int32_t) * c.n_experts, stream));
+        DWDP_CUDA(ctx, cudaMemsetAsync(out->offsets, 0, sizeof(int32_t) * (c.n_experts + 1), stream));
+        return DWDP_OK;
+    }
+    if (!x || !w_router || !aligned16(x) || !aligned16(w_router))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and w_router must be non-NULL, 16-byte aligned");
+    if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(w_router, ctx->device))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and w_router must be device memory of the context's device (%d)",
+                    ctx->device);
+    const size_t need = ws_layout(c, T).route_bytes;
+    if (!ws || ws_bytes < need || !aligned16(ws))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu) or unaligned", ws_bytes, need);
+    return DWDP_OK;
+}
+
+// The router GEMM on the grouped-GEMM kernel.  K split: with fewer 128-token
+// tiles than SMs the GEMM's K is cut into parts, each a tile writing its own
+// fp32 plane; the top-k kernel adds the planes in order (router_k_parts:
+// deterministic per shape).  The planes go to the workspace, a single one
+// straight to out_logits where the caller keeps the logits.
+int32_t router_gemm(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router, const float* col_bias,
+                    float* out_logits, void* ws, cudaStream_t stream, int& parts, float*& logits) {
+    const dwdp_config& c = ctx->cfg;
+    parts = router_k_parts(T, c.n_experts, c.hidden, ctx->n_sms, (size_t)kRouterMaxSplit * T * c.n_experts * 4);
+    logits = (out_logits && parts == 1) ? out_logits
+                                        : reinterpret_cast<float*>(static_cast<char*>(ws) + ws_layout(c, T).logits);
+    GemmArgs& a = *ctx->args;
+    if (!encode_rows(&a.tmA[0], x, T, c.hidden) ||
+        !encode_slots(&a.tmB[0], w_router, 1, c.n_experts, c.hidden))
+        return fail(ctx, DWDP_ERR_CUDA, "tensor map for the router GEMM");
+    a.tmA[1] = a.tmA[0];
+    a.tmB[1] = a.tmB[2] = a.tmB[0];
+    a.row_offsets = nullptr;
+    a.n_routed = 0;
+    a.shared_rows = T;
+    a.shared_a_row = 0;
+    a.shared_d_row = 0;
+    a.K = c.hidden;
+    a.N = c.n_experts;
+    a.ldd = c.n_experts;
+    a.d_rows = T;
+    a.D = logits;
+    a.col_bias = col_bias;
+    a.k_split = parts;
+    a.split_stride = (int64_t)T * c.n_experts;
+    a.err = ctx->d_err;
+    a.bsrc[0] = make_int2(0, 0);
+    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_F32, FMT_BF16, a, ctx->n_sms, stream));
+    return DWDP_OK;
+}
+
+// dwdp_moe_layer (given_sx NULL: x is bf16) and dwdp_moe_layer_codes (x is
+// E4M3 codes with row scales given_sx).
+int32_t moe_layer(dwdp_ctx* ctx, int32_t layer, int32_t stage, const void* x, const float* given_sx, int32_t T,
+                  const dwdp_route_out* route, void* out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    const dwdp_config& c = ctx->cfg;
+    if (layer < 0 || layer >= c.n_layers) return fail(ctx, DWDP_ERR_INVALID_ARG, "layer %d out of range", layer);
+    if (T < 0 || T > c.max_tokens) return fail(ctx, DWDP_ERR_INVALID_ARG, "T=%d outside [0, max_tokens]", T);
+    LayerMap& m = ctx->layers[layer];
+    if (!m.mapped) return fail(ctx, DWDP_ERR_NOT_MAPPED, "layer %d has no expert map", layer);
+    if (m.n_remote > 0) {
+        if (stage < 0 || stage >= ctx->n_stages)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "stage %d outside [0, %d)", stage, ctx->n_stages);
+        if (ctx->stage_layer[stage] != layer)
+            return fail(ctx, DWDP_ERR_NOT_MAPPED, "stage %d holds layer %d, not layer %d", stage,
+                        ctx->stage_layer[stage], layer);
+    }
+    if (T == 0) return DWDP_OK;
+    if (!route || !route->topk_w || !route->offsets || !route->perm || !route->inv_perm)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "route outputs must not be NULL");
+    if (!x || !out || !aligned16(x) || !aligned16(out) || !aligned16(route->offsets) ||
+        !aligned16(route->perm) || !aligned16(route->inv_perm) || !aligned16(route->topk_w))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "x, out and route pointers must be non-NULL, 16-byte aligned");
+    const WsLayout L = ws_layout(c, T);
+    if (!ws || ws_bytes < L.moe_bytes || !aligned16(ws))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu) or unaligned", ws_bytes, L.moe_bytes);
+    // x and the workspace (xp, a and their codes) are read through tensor maps
+    if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(ws, ctx->device))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and ws must be device memory of the context's device (%d)",
+                    ctx->device);
+    const int64_t k = c.top_k, S = c.n_shared, H = c.hidden, I = c.inter, E = c.n_experts;
+    const int64_t rows_r = (int64_t)T * k, rows_all = (int64_t)T * (k + S);
+    const int fmt = ctx->fmt;
+    const bool scaled = fmt != FMT_BF16;
+    if (scaled && m.scale13.size() != m.bsrc.size())
+        return fail(ctx, DWDP_ERR_NOT_MAPPED, "layer %d has no weight scales (dwdp_set_expert_scales)", layer);
+    char* w = static_cast<char*>(ws);
+    void* xp = w + L.xp;
+    void* act = w + L.a;
+    void* y = w + L.y;
+    void* xq = w + L.xq;
+    float* sx = reinterpret_cast<float*>(w + L.sx);
+    const void* shared_x = scaled ? xq : x;  // the shared expert's rows
+    const float* shared_sx = sx;
+    float* sxp = reinterpret_cast<float*>(w + L.sxp);
+    void* aq = w + L.aq;
+    float* sa = reinterpret_cast<float*>(w + L.sa);
+    uint8_t* sfx = reinterpret_cast<uint8_t*>(w + L.sfx);
+    uint8_t* sfa = reinterpret_cast<uint8_t*>(w + L.sfa);
+
+    // x goes into expert order first: only the GEMMs read the staged weights,
+    // so the copy into the stage may still run meanwhile
+    if (fmt == FMT_NVFP4) {
+        // x rows to NVFP4 once per token, written to each chosen expert's row
+        if (!route->topk_ids || !aligned16(route->topk_ids))
+            return fail(ctx, DWDP_ERR_INVALID_ARG, "NVFP4 layers need route->topk_ids");
+        DWDP_CUDA(ctx, launch_quantize_x_nvfp4(x, (int)H, (int)T, (int)k, route->topk_ids, route->inv_perm,
+                                               route->offsets, (int)E, S > 0, xq, sx, xp, sxp, sfx, L.sf_tiles,
+                                               ctx->d_err, stream));
+    } else if (given_sx) {
+        // codes and row scales into expert order; the shared expert reads the caller's
+        shared_x = x;
+        shared_sx = given_sx;
+        DWDP_CUDA(ctx, launch_gather_codes(x, (int)H, given_sx, route->inv_perm, (int)T, (int)k, xp, sxp, ctx->d_err,
+                                           stream));
+    } else if (fmt == FMT_E4M3) {
+        // x rows to E4M3 (per-token scales) once, written to xq and into
+        // expert order in the same pass
+        DWDP_CUDA(ctx, launch_quantize_x_e4m3(x, (int)H, route->inv_perm, (int)T, (int)k, xq, sx, xp, sxp, ctx->d_err,
+                                              stream));
+    } else {
+        DWDP_CUDA(ctx, launch_gather(x, (int)H, route->inv_perm, (int)T, (int)k, xp, ctx->d_err, stream));
+    }
+    DWDP_CUDA(ctx, mark(ctx, 2, stream));
+    if (m.n_remote > 0) DWDP_CUDA(ctx, cudaStreamWaitEvent(stream, ctx->ready[stage], 0));
+    DWDP_CUDA(ctx, mark(ctx, 3, stream));
+
+    GemmArgs& a = *ctx->args;
+    // B buffers: 0 = local pool, 1 = the stage, 2 = the shared expert.  Slots
+    // no group reads get a copy of a valid map.
+    auto set_b = [&](const CUtensorMap& local, const CUtensorMap& stg, const CUtensorMap& shared) {
+        const CUtensorMap* valid = m.has_local_map ? &local : (m.n_remote > 0 ? &stg : &shared);
+        a.tmB[0] = m.has_local_map ? local : *valid;
+        a.tmB[1] = m.n_remote > 0 ? stg : *valid;
+        a.tmB[2] = S ? shared : *valid;
+    };
+    // NVFP4: where each buffer's slot 0 keeps its block scales (after its
+    // rows x K / 2 bytes of codes); buffers no group reads get nullptr.
+    auto set_bsf = [&](const void* local, const void* stg, const void* shared, int64_t rows, int64_t K) {
+        const int64_t codes = rows * K / 2;
+        auto at = [&](const void* base) { return base ? static_cast<const uint8_t*>(base) + codes : nullptr; };
+        a.bsf[0] = m.has_local_map ? at(local) : nullptr;
+        a.bsf[1] = m.n_remote > 0 ? at(stg) : nullptr;
+        a.bsf[2] = S ? at(shared) : nullptr;
+        a.b_slot_bytes = weight_slot_bytes(rows, K, fmt);
+    };
+    // G1: a = SiLU(xp W_gate) * (xp W_up); the shared group reads x directly
+    // (E4M3: xp / x codes, dequantized in the epilogue by row scale * weight scale).
+    if (!encode_rows(&a.tmA[0], xp, rows_r, H, fmt) || !encode_rows(&a.tmA[1], shared_x, T, H, fmt))
+        return fail(ctx, DWDP_ERR_CUDA, "tensor maps for the gate/up GEMM");
+    a.row_scale[0] = sxp;
+    a.row_scale[1] = shared_sx;
+    set_b(m.local13, ctx->stage_map13[m.n_remote > 0 ? stage : 0], m.shared13);
+    a.sfa = sfx;
+    a.sfa_tiles = L.sf_tiles;
+    if (fmt == FMT_NVFP4)
+        set_bsf(m.local.w13, ctx->stage13[m.n_remote > 0 ? stage : 0], m.shared_w13, 2 * I, H);
+    a.row_offsets = route->offsets;
+    a.n_routed = (int32_t)E;
+    a.shared_rows = (int32_t)(T * S);
+    a.shared_a_row = 0;
+    a.shared_d_row = (int32_t)rows_r;
+    a.K = (int32_t)H;
+    a.N = (int32_t)I;
+    a.ldd = I;
+    a.d_rows = rows_all;
+    a.D = act;
+    a.col_bias = nullptr;
+    a.k_split = 1;
+    a.err = ctx->d_err;
+    for (size_t g = 0; g < m.bsrc.size(); ++g) {
+        a.bsrc[g] = m.bsrc[g];
+        if (scaled) a.gscale[g] = m.scale13[g];
+    }
+    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_SILU, fmt, a, ctx->n_sms, stream,
+                                       (c.flags & DWDP_FLAG_WIDE_EPILOGUE) != 0));
+    DWDP_CUDA(ctx, mark(ctx, 4, stream));
+    // G2: y = a W_down (E4M3 / NVFP4: a's rows quantized first; this phase includes it).
+    if (fmt == FMT_E4M3) DWDP_CUDA(ctx, launch_quantize_rows(act, rows_all, (int)I, aq, sa, stream));
+    if (fmt == FMT_NVFP4)
+        DWDP_CUDA(ctx, launch_quantize_a_nvfp4(act, (int)I, rows_r, rows_all, route->offsets, (int)E, aq, sa, sfa,
+                                               L.sf_tiles, ctx->d_err, stream));
+    if (!encode_rows(&a.tmA[0], scaled ? aq : act, rows_all, I, fmt))
+        return fail(ctx, DWDP_ERR_CUDA, "tensor map for the down GEMM");
+    a.tmA[1] = a.tmA[0];
+    a.row_scale[0] = a.row_scale[1] = sa;
+    if (scaled)
+        for (size_t g = 0; g < m.bsrc.size(); ++g) a.gscale[g] = m.scale2[g];
+    set_b(m.local2, ctx->stage_map2[m.n_remote > 0 ? stage : 0], m.shared2);
+    a.sfa = sfa;
+    if (fmt == FMT_NVFP4)
+        set_bsf(m.local.w2, ctx->stage2[m.n_remote > 0 ? stage : 0], m.shared_w2, H, I);
+    a.shared_a_row = (int32_t)rows_r;
+    a.shared_d_row = (int32_t)rows_r;
+    a.K = (int32_t)I;
+    a.N = (int32_t)H;
+    a.ldd = H;
+    a.d_rows = rows_all;
+    a.D = y;
+    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_BF16, fmt, a, ctx->n_sms, stream));
+    DWDP_CUDA(ctx, mark(ctx, 5, stream));
+    // The stage's weights have been read: the next prefetch into it may start.
+    if (m.n_remote > 0) DWDP_CUDA(ctx, cudaEventRecord(ctx->freed[stage], stream));
+    DWDP_CUDA(ctx, launch_combine(y, (int)H, route->inv_perm, route->topk_w, T, (int)k, rows_r, S > 0, out, ctx->d_err, stream));
+    DWDP_CUDA(ctx, mark(ctx, 6, stream));
+    return DWDP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -582,64 +804,145 @@ int32_t dwdp_route(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router
     const NvtxRange nvtx("dwdp_route T=%d", T);
     if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
     const dwdp_config& c = ctx->cfg;
-    if (T < 0 || T > c.max_tokens) return fail(ctx, DWDP_ERR_INVALID_ARG, "T=%d outside [0, max_tokens]", T);
-    if (!out || !out->topk_ids || !out->topk_w || !out->counts || !out->offsets || !out->perm || !out->inv_perm)
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "route outputs must not be NULL (except logits)");
-    if (!aligned16(out->topk_ids) || !aligned16(out->topk_w) || !aligned16(out->counts) ||
-        !aligned16(out->offsets) || !aligned16(out->perm) || !aligned16(out->inv_perm) ||
-        (out->logits && !aligned16(out->logits)) || (logit_bias && !aligned16(logit_bias)))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "route pointers must be 16-byte aligned");
-    if (T == 0) {
-        DWDP_CUDA(ctx, cudaMemsetAsync(out->counts, 0, sizeof(int32_t) * c.n_experts, stream));
-        DWDP_CUDA(ctx, cudaMemsetAsync(out->offsets, 0, sizeof(int32_t) * (c.n_experts + 1), stream));
-        return DWDP_OK;
-    }
-    if (!x || !w_router || !aligned16(x) || !aligned16(w_router))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and w_router must be non-NULL, 16-byte aligned");
-    if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(w_router, ctx->device))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and w_router must be device memory of the context's device (%d)",
-                    ctx->device);
+    bool empty = false;
+    const int32_t rc = check_route(ctx, x, T, w_router, logit_bias, out, ws, ws_bytes, stream, empty);
+    if (rc != DWDP_OK || empty) return rc;
     const WsLayout L = ws_layout(c, T);
-    if (!ws || ws_bytes < L.route_bytes || !aligned16(ws))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu) or unaligned", ws_bytes,
-                    L.route_bytes);
-    // K split: with fewer 128-token tiles than SMs the router GEMM's K is cut
-    // into parts, each a tile writing its own fp32 plane; the top-k kernel
-    // adds the planes in order (router_k_parts: deterministic per shape).
-    const int parts = router_k_parts(T, c.n_experts, c.hidden, ctx->n_sms,
-                                     (size_t)kRouterMaxSplit * T * c.n_experts * 4);
-    float* planes = reinterpret_cast<float*>(static_cast<char*>(ws) + L.logits);
-    float* logits = (out->logits && parts == 1) ? out->logits : planes;
     int32_t* group_scratch = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.group);
     DWDP_CUDA(ctx, mark(ctx, 0, stream));
-    GemmArgs& a = *ctx->args;
-    if (!encode_rows(&a.tmA[0], x, T, c.hidden) ||
-        !encode_slots(&a.tmB[0], w_router, 1, c.n_experts, c.hidden))
-        return fail(ctx, DWDP_ERR_CUDA, "tensor map for the router GEMM");
-    a.tmA[1] = a.tmA[0];
-    a.tmB[1] = a.tmB[2] = a.tmB[0];
-    a.row_offsets = nullptr;
-    a.n_routed = 0;
-    a.shared_rows = T;
-    a.shared_a_row = 0;
-    a.shared_d_row = 0;
-    a.K = c.hidden;
-    a.N = c.n_experts;
-    a.ldd = c.n_experts;
-    a.d_rows = T;
-    a.D = logits;
-    a.col_bias = logit_bias;
-    a.k_split = parts;
-    a.split_stride = (int64_t)T * c.n_experts;
-    a.err = ctx->d_err;
-    a.bsrc[0] = make_int2(0, 0);
-    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_F32, FMT_BF16, a, ctx->n_sms, stream));
+    int parts = 1;
+    float* logits = nullptr;
+    const int32_t rg = router_gemm(ctx, x, T, w_router, logit_bias, out->logits, ws, stream, parts, logits);
+    if (rg != DWDP_OK) return rg;
     DWDP_CUDA(ctx, launch_topk(logits, parts, (int64_t)T * c.n_experts, nullptr, T, c.n_experts, c.top_k,
                                out->topk_ids, out->topk_w, parts > 1 ? out->logits : nullptr, ctx->d_err,
                                stream));
     DWDP_CUDA(ctx, launch_group_chunked(out->topk_ids, T * c.top_k, c.n_experts, out->counts, out->offsets,
                                         out->perm, out->inv_perm, group_scratch, stream));
     DWDP_CUDA(ctx, mark(ctx, 1, stream));
+    return DWDP_OK;
+}
+
+int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router, const float* choice_bias,
+                          const dwdp_scoring* scoring, const dwdp_route_out* out, void* ws, size_t ws_bytes,
+                          dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_route_scored T=%d", T);
+    if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
+    const dwdp_config& c = ctx->cfg;
+    if (!scoring) return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring is NULL");
+    const dwdp_scoring& sc = *scoring;
+    if ((sc.score != DWDP_SCORE_SOFTMAX && sc.score != DWDP_SCORE_SIGMOID) ||
+        (sc.group_score != DWDP_GROUP_MAX && sc.group_score != DWDP_GROUP_TOP2) ||
+        (sc.renormalize != 0 && sc.renormalize != 1) || !std::isfinite(sc.scale) || !(sc.scale > 0.0f))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring: unknown score, group_score or renormalize, or a bad scale");
+    if (sc.n_groups < 1 || c.n_experts % sc.n_groups || sc.top_groups < 1 || sc.top_groups > sc.n_groups)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring: n_groups %d must divide E = %d, top_groups %d lie in 1..n_groups",
+                    sc.n_groups, c.n_experts, sc.top_groups);
+    if (sc.n_groups > DWDP_MAX_GROUPS)
+        return fail(ctx, DWDP_ERR_UNSUPPORTED, "scoring: at most %d groups", DWDP_MAX_GROUPS);
+    if (c.top_k > sc.top_groups * (c.n_experts / sc.n_groups))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring: %d groups of %d experts hold fewer than k = %d", sc.top_groups,
+                    c.n_experts / sc.n_groups, c.top_k);
+    bool empty = false;
+    const int32_t rc = check_route(ctx, x, T, w_router, choice_bias, out, ws, ws_bytes, stream, empty);
+    if (rc != DWDP_OK || empty) return rc;
+    DWDP_CUDA(ctx, mark(ctx, 0, stream));
+    ScoredArgs p{};
+    float* logits = nullptr;
+    const int32_t rg = router_gemm(ctx, x, T, w_router, nullptr, out->logits, ws, stream, p.parts, logits);
+    if (rg != DWDP_OK) return rg;
+    p.logits = logits;
+    p.part_stride = (int64_t)T * c.n_experts;
+    p.bias = choice_bias;
+    p.ids = out->topk_ids;
+    p.w = out->topk_w;
+    p.z_out = p.parts > 1 ? out->logits : nullptr;
+    p.err = ctx->d_err;
+    p.T = T;
+    p.E = c.n_experts;
+    p.k = c.top_k;
+    p.n_groups = sc.n_groups;
+    p.top_groups = sc.top_groups;
+    p.sigmoid = sc.score == DWDP_SCORE_SIGMOID;
+    p.group_top2 = sc.group_score == DWDP_GROUP_TOP2;
+    p.renorm = sc.renormalize != 0;
+    p.scale = sc.scale;
+    scored_layout(p);
+    DWDP_CUDA(ctx, launch_scored_topk(p, stream));
+    int32_t* group_scratch = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + ws_layout(c, T).group);
+    DWDP_CUDA(ctx, launch_group_chunked(out->topk_ids, T * c.top_k, c.n_experts, out->counts, out->offsets, out->perm,
+                                        out->inv_perm, group_scratch, stream));
+    DWDP_CUDA(ctx, mark(ctx, 1, stream));
+    return DWDP_OK;
+}
+
+int32_t dwdp_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, void* residual_out,
+                         const void* weight, float eps, int64_t rows, int32_t H, void* out, void* codes,
+                         float* row_scale, dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_add_rmsnorm rows=%lld", (long long)rows);
+    if (rows < 0 || rows >= ((int64_t)1 << 31)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "rows outside [0, 2^31)");
+    if (H <= 0 || H % 8 || H > 32768)
+        return fail(nullptr, DWDP_ERR_UNSUPPORTED, "H must be a multiple of 8 in 8..32768");
+    if (x_stride < H || x_stride % 8)
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least H");
+    if (!std::isfinite(eps) || eps < 0.0f) return fail(nullptr, DWDP_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!residual != !residual_out) return fail(nullptr, DWDP_ERR_INVALID_ARG, "residual and residual_out go together");
+    if (!codes != !row_scale) return fail(nullptr, DWDP_ERR_INVALID_ARG, "codes and row_scale go together");
+    if (rows == 0) return DWDP_OK;
+    if (!x || !weight || !out || !aligned16(x) || !aligned16(weight) || !aligned16(out) || !aligned16(residual) ||
+        !aligned16(residual_out) || !aligned16(codes) || !aligned16(row_scale))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "x, weight and out must be non-NULL; every pointer 16-byte aligned");
+    const cudaError_t e =
+        launch_add_rmsnorm(x, x_stride, residual, residual_out, weight, eps, rows, H, out, codes, row_scale, stream);
+    return e == cudaSuccess ? DWDP_OK : cuda_fail(nullptr, e, "dwdp_add_rmsnorm");
+}
+
+size_t dwdp_lora_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t R) {
+    if (T < 0 || K <= 0 || N <= 0 || K % 8 || N % 8 || R <= 0 || R % 8 || R > DWDP_MAX_LORA_RANK) return 0;
+    return std::max<size_t>(256, lora_workspace_bytes(T, K, N, R));
+}
+
+int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T, int32_t K, int32_t N,
+                      const void* a, const void* b, const float* adapter_scale, int32_t n_adapters, int32_t R,
+                      const int32_t* adapter_ids, const void* base, int64_t base_stride, void* out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_lora_add T=%d", T);
+    if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
+    if (T < 0 || n_adapters < 1) return fail(ctx, DWDP_ERR_INVALID_ARG, "T >= 0 and n_adapters >= 1");
+    const size_t need = dwdp_lora_workspace_bytes(T, K, N, R);
+    if (need == 0)
+        return fail(ctx, DWDP_ERR_UNSUPPORTED, "K, N and R must be positive multiples of 8, R <= %d",
+                    DWDP_MAX_LORA_RANK);
+    if (x_stride < K || x_stride % 8 || base_stride < N || base_stride % 8 || out_stride < N || out_stride % 8)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "strides must be multiples of 8, no smaller than the row");
+    if (out == base && out_stride != base_stride)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "out may be base only with base's stride");
+    if (T == 0) return DWDP_OK;
+    if (!x || !a || !b || !adapter_scale || !adapter_ids || !base || !out || !aligned16(x) || !aligned16(a) ||
+        !aligned16(b) || !aligned16(adapter_scale) || !aligned16(adapter_ids) || !aligned16(base) || !aligned16(out))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "pointers must be non-NULL, 16-byte aligned");
+    if (!ws || ws_bytes < need || !aligned16(ws))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu) or unaligned", ws_bytes, need);
+    LoraArgs p{};
+    p.x = x;
+    p.x_stride = x_stride;
+    p.T = T;
+    p.K = K;
+    p.N = N;
+    p.a = a;
+    p.b = b;
+    p.scale = adapter_scale;
+    p.n_adapters = n_adapters;
+    p.R = R;
+    p.ids = adapter_ids;
+    p.base = base;
+    p.base_stride = base_stride;
+    p.out = out;
+    p.out_stride = out_stride;
+    p.ws = ws;
+    p.err = ctx->d_err;
+    p.n_sms = ctx->n_sms;
+    DWDP_CUDA(ctx, launch_lora_add(p, stream));
     return DWDP_OK;
 }
 
@@ -706,149 +1009,18 @@ int32_t dwdp_moe_layer(dwdp_ctx* ctx, int32_t layer, int32_t stage, const void* 
                        const dwdp_route_out* route, void* out, void* ws, size_t ws_bytes, dwdp_stream_t stream) {
     const NvtxRange nvtx("dwdp_moe_layer layer %d stage %d T=%d", layer, stage, T);
     if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
-    const dwdp_config& c = ctx->cfg;
-    if (layer < 0 || layer >= c.n_layers) return fail(ctx, DWDP_ERR_INVALID_ARG, "layer %d out of range", layer);
-    if (T < 0 || T > c.max_tokens) return fail(ctx, DWDP_ERR_INVALID_ARG, "T=%d outside [0, max_tokens]", T);
-    LayerMap& m = ctx->layers[layer];
-    if (!m.mapped) return fail(ctx, DWDP_ERR_NOT_MAPPED, "layer %d has no expert map", layer);
-    if (m.n_remote > 0) {
-        if (stage < 0 || stage >= ctx->n_stages)
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "stage %d outside [0, %d)", stage, ctx->n_stages);
-        if (ctx->stage_layer[stage] != layer)
-            return fail(ctx, DWDP_ERR_NOT_MAPPED, "stage %d holds layer %d, not layer %d", stage,
-                        ctx->stage_layer[stage], layer);
-    }
-    if (T == 0) return DWDP_OK;
-    if (!route || !route->topk_w || !route->offsets || !route->perm || !route->inv_perm)
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "route outputs must not be NULL");
-    if (!x || !out || !aligned16(x) || !aligned16(out) || !aligned16(route->offsets) ||
-        !aligned16(route->perm) || !aligned16(route->inv_perm) || !aligned16(route->topk_w))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "x, out and route pointers must be non-NULL, 16-byte aligned");
-    const WsLayout L = ws_layout(c, T);
-    if (!ws || ws_bytes < L.moe_bytes || !aligned16(ws))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu) or unaligned", ws_bytes, L.moe_bytes);
-    // x and the workspace (xp, a and their codes) are read through tensor maps
-    if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(ws, ctx->device))
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and ws must be device memory of the context's device (%d)",
-                    ctx->device);
-    const int64_t k = c.top_k, S = c.n_shared, H = c.hidden, I = c.inter, E = c.n_experts;
-    const int64_t rows_r = (int64_t)T * k, rows_all = (int64_t)T * (k + S);
-    const int fmt = ctx->fmt;
-    const bool scaled = fmt != FMT_BF16;
-    if (scaled && m.scale13.size() != m.bsrc.size())
-        return fail(ctx, DWDP_ERR_NOT_MAPPED, "layer %d has no weight scales (dwdp_set_expert_scales)", layer);
-    char* w = static_cast<char*>(ws);
-    void* xp = w + L.xp;
-    void* act = w + L.a;
-    void* y = w + L.y;
-    void* xq = w + L.xq;
-    float* sx = reinterpret_cast<float*>(w + L.sx);
-    float* sxp = reinterpret_cast<float*>(w + L.sxp);
-    void* aq = w + L.aq;
-    float* sa = reinterpret_cast<float*>(w + L.sa);
-    uint8_t* sfx = reinterpret_cast<uint8_t*>(w + L.sfx);
-    uint8_t* sfa = reinterpret_cast<uint8_t*>(w + L.sfa);
+    return moe_layer(ctx, layer, stage, x, nullptr, T, route, out, ws, ws_bytes, stream);
+}
 
-    // x goes into expert order first: only the GEMMs read the staged weights,
-    // so the copy into the stage may still run meanwhile
-    if (fmt == FMT_NVFP4) {
-        // x rows to NVFP4 once per token, written to each chosen expert's row
-        if (!route->topk_ids || !aligned16(route->topk_ids))
-            return fail(ctx, DWDP_ERR_INVALID_ARG, "NVFP4 layers need route->topk_ids");
-        DWDP_CUDA(ctx, launch_quantize_x_nvfp4(x, (int)H, (int)T, (int)k, route->topk_ids, route->inv_perm,
-                                               route->offsets, (int)E, S > 0, xq, sx, xp, sxp, sfx, L.sf_tiles,
-                                               ctx->d_err, stream));
-    } else if (fmt == FMT_E4M3) {
-        // x rows to E4M3 (per-token scales) once, written to xq and into
-        // expert order in the same pass
-        DWDP_CUDA(ctx, launch_quantize_x_e4m3(x, (int)H, route->inv_perm, (int)T, (int)k, xq, sx, xp, sxp, ctx->d_err,
-                                              stream));
-    } else {
-        DWDP_CUDA(ctx, launch_gather(x, (int)H, route->inv_perm, (int)T, (int)k, xp, ctx->d_err, stream));
-    }
-    DWDP_CUDA(ctx, mark(ctx, 2, stream));
-    if (m.n_remote > 0) DWDP_CUDA(ctx, cudaStreamWaitEvent(stream, ctx->ready[stage], 0));
-    DWDP_CUDA(ctx, mark(ctx, 3, stream));
-
-    GemmArgs& a = *ctx->args;
-    // B buffers: 0 = local pool, 1 = the stage, 2 = the shared expert.  Slots
-    // no group reads get a copy of a valid map.
-    auto set_b = [&](const CUtensorMap& local, const CUtensorMap& stg, const CUtensorMap& shared) {
-        const CUtensorMap* valid = m.has_local_map ? &local : (m.n_remote > 0 ? &stg : &shared);
-        a.tmB[0] = m.has_local_map ? local : *valid;
-        a.tmB[1] = m.n_remote > 0 ? stg : *valid;
-        a.tmB[2] = S ? shared : *valid;
-    };
-    // NVFP4: where each buffer's slot 0 keeps its block scales (after its
-    // rows x K / 2 bytes of codes); buffers no group reads get nullptr.
-    auto set_bsf = [&](const void* local, const void* stg, const void* shared, int64_t rows, int64_t K) {
-        const int64_t codes = rows * K / 2;
-        auto at = [&](const void* base) { return base ? static_cast<const uint8_t*>(base) + codes : nullptr; };
-        a.bsf[0] = m.has_local_map ? at(local) : nullptr;
-        a.bsf[1] = m.n_remote > 0 ? at(stg) : nullptr;
-        a.bsf[2] = S ? at(shared) : nullptr;
-        a.b_slot_bytes = weight_slot_bytes(rows, K, fmt);
-    };
-    // G1: a = SiLU(xp W_gate) * (xp W_up); the shared group reads x directly
-    // (E4M3: xp / x codes, dequantized in the epilogue by row scale * weight scale).
-    if (!encode_rows(&a.tmA[0], xp, rows_r, H, fmt) || !encode_rows(&a.tmA[1], scaled ? xq : x, T, H, fmt))
-        return fail(ctx, DWDP_ERR_CUDA, "tensor maps for the gate/up GEMM");
-    a.row_scale[0] = sxp;
-    a.row_scale[1] = sx;
-    set_b(m.local13, ctx->stage_map13[m.n_remote > 0 ? stage : 0], m.shared13);
-    a.sfa = sfx;
-    a.sfa_tiles = L.sf_tiles;
-    if (fmt == FMT_NVFP4)
-        set_bsf(m.local.w13, ctx->stage13[m.n_remote > 0 ? stage : 0], m.shared_w13, 2 * I, H);
-    a.row_offsets = route->offsets;
-    a.n_routed = (int32_t)E;
-    a.shared_rows = (int32_t)(T * S);
-    a.shared_a_row = 0;
-    a.shared_d_row = (int32_t)rows_r;
-    a.K = (int32_t)H;
-    a.N = (int32_t)I;
-    a.ldd = I;
-    a.d_rows = rows_all;
-    a.D = act;
-    a.col_bias = nullptr;
-    a.k_split = 1;
-    a.err = ctx->d_err;
-    for (size_t g = 0; g < m.bsrc.size(); ++g) {
-        a.bsrc[g] = m.bsrc[g];
-        if (scaled) a.gscale[g] = m.scale13[g];
-    }
-    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_SILU, fmt, a, ctx->n_sms, stream,
-                                       (c.flags & DWDP_FLAG_WIDE_EPILOGUE) != 0));
-    DWDP_CUDA(ctx, mark(ctx, 4, stream));
-    // G2: y = a W_down (E4M3 / NVFP4: a's rows quantized first; this phase includes it).
-    if (fmt == FMT_E4M3) DWDP_CUDA(ctx, launch_quantize_rows(act, rows_all, (int)I, aq, sa, stream));
-    if (fmt == FMT_NVFP4)
-        DWDP_CUDA(ctx, launch_quantize_a_nvfp4(act, (int)I, rows_r, rows_all, route->offsets, (int)E, aq, sa, sfa,
-                                               L.sf_tiles, ctx->d_err, stream));
-    if (!encode_rows(&a.tmA[0], scaled ? aq : act, rows_all, I, fmt))
-        return fail(ctx, DWDP_ERR_CUDA, "tensor map for the down GEMM");
-    a.tmA[1] = a.tmA[0];
-    a.row_scale[0] = a.row_scale[1] = sa;
-    if (scaled)
-        for (size_t g = 0; g < m.bsrc.size(); ++g) a.gscale[g] = m.scale2[g];
-    set_b(m.local2, ctx->stage_map2[m.n_remote > 0 ? stage : 0], m.shared2);
-    a.sfa = sfa;
-    if (fmt == FMT_NVFP4)
-        set_bsf(m.local.w2, ctx->stage2[m.n_remote > 0 ? stage : 0], m.shared_w2, H, I);
-    a.shared_a_row = (int32_t)rows_r;
-    a.shared_d_row = (int32_t)rows_r;
-    a.K = (int32_t)I;
-    a.N = (int32_t)H;
-    a.ldd = H;
-    a.d_rows = rows_all;
-    a.D = y;
-    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_BF16, fmt, a, ctx->n_sms, stream));
-    DWDP_CUDA(ctx, mark(ctx, 5, stream));
-    // The stage's weights have been read: the next prefetch into it may start.
-    if (m.n_remote > 0) DWDP_CUDA(ctx, cudaEventRecord(ctx->freed[stage], stream));
-    DWDP_CUDA(ctx, launch_combine(y, (int)H, route->inv_perm, route->topk_w, T, (int)k, rows_r, S > 0, out, ctx->d_err, stream));
-    DWDP_CUDA(ctx, mark(ctx, 6, stream));
-    return DWDP_OK;
+int32_t dwdp_moe_layer_codes(dwdp_ctx* ctx, int32_t layer, int32_t stage, const void* xq, const float* sx,
+                             int32_t T, const dwdp_route_out* route, void* out, void* ws, size_t ws_bytes,
+                             dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_moe_layer_codes layer %d stage %d T=%d", layer, stage, T);
+    if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
+    if (ctx->fmt != FMT_E4M3) return fail(ctx, DWDP_ERR_INVALID_ARG, "the context is not DWDP_DTYPE_E4M3");
+    if (T > 0 && (!sx || !aligned16(sx)))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "sx must be non-NULL, 16-byte aligned");
+    return moe_layer(ctx, layer, stage, xq, sx, T, route, out, ws, ws_bytes, stream);
 }
 
 int32_t dwdp_quantize_rows(int32_t weight_dtype, const void* x, int64_t rows, int32_t K, void* codes,

@@ -187,6 +187,10 @@ cudaError_t launch_group_chunked(const int32_t* ids, int n, int E, int32_t* coun
 // here and in the combine.
 cudaError_t launch_gather(const void* x, int H, const int32_t* inv, int T, int k, void* xp, int* err,
                           cudaStream_t s);
+// The same for rows that are E4M3 codes (H bytes) with row scales sx, which
+// go to sxp[inv[t k + j]].
+cudaError_t launch_gather_codes(const void* xq, int H, const float* sx, const int32_t* inv, int T, int k, void* xp,
+                                float* sxp, int* err, cudaStream_t s);
 // E4M3 rows: codes[r][:] and scale[r] of bf16 rows (scale = amax / 448).
 cudaError_t launch_quantize_rows(const void* in, int64_t rows, int cols, void* codes, float* scale, cudaStream_t s);
 // x rows to E4M3 as launch_quantize_rows does (xq, sx), each also written to
@@ -207,5 +211,52 @@ cudaError_t launch_quantize_a_nvfp4(const void* act, int I, int64_t rows_r, int6
                                     cudaStream_t s);
 cudaError_t launch_combine(const void* y, int H, const int32_t* inv, const float* w, int T, int k,
                            int64_t shared_row0, bool has_shared, void* out, int* err, cudaStream_t s);
+
+// norm.cu: dwdp_add_rmsnorm's kernel (arguments as there, checked).
+cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, void* residual_out,
+                               const void* weight, float eps, int64_t rows, int H, void* out, void* codes,
+                               float* row_scale, cudaStream_t s);
+
+// route_scored.cu: the choice of dwdp_route_scored.  logits: `parts` fp32
+// planes [T][E] part_stride apart, summed in plane order; z_out, if not null,
+// receives the sums.  The members after `err` are filled by scored_layout.
+struct ScoredArgs {
+    const float* logits;
+    int64_t part_stride;
+    const float* bias;
+    int32_t* ids;
+    float* w;
+    float* z_out;
+    int* err;
+    int parts, T, E, k;
+    int n_groups, top_groups;
+    bool sigmoid, group_top2, renorm;
+    float scale;
+    int lanes, group_size, per_lane;
+    bool vector_loads;
+};
+void scored_layout(ScoredArgs& p);
+cudaError_t launch_scored_topk(const ScoredArgs& p, cudaStream_t s);
+
+// lora.cu: dwdp_lora_add (arguments as there, checked).
+struct LoraArgs {
+    const void* x;
+    int64_t x_stride;
+    int32_t T, K, N;
+    const void* a;
+    const void* b;
+    const float* scale;
+    int32_t n_adapters, R;
+    const int32_t* ids;
+    const void* base;
+    int64_t base_stride;
+    void* out;
+    int64_t out_stride;
+    void* ws;
+    int* err;
+    int n_sms;
+};
+size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R);
+cudaError_t launch_lora_add(const LoraArgs& p, cudaStream_t s);
 
 }  // namespace dwdp

@@ -1041,6 +1041,11 @@ cudaError_t launch_gather(const void* x, int H, const int32_t* inv, int T, int k
     return scatter_rows(x, H / 8, inv, T, k, xp, nullptr, nullptr, err, s);
 }
 
+cudaError_t launch_gather_codes(const void* xq, int H, const float* sx, const int32_t* inv, int T, int k, void* xp,
+                                float* sxp, int* err, cudaStream_t s) {
+    return scatter_rows(xq, H / 16, inv, T, k, xp, sx, sxp, err, s);
+}
+
 cudaError_t launch_combine(const void* y, int H, const int32_t* inv, const float* w, int T, int k,
                            int64_t shared_row0, bool has_shared, void* out, int* err, cudaStream_t s) {
     if (T <= 0) return cudaSuccess;

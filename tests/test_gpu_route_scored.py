@@ -1,0 +1,269 @@
+"""dwdp_route_scored: the logits against x W^T in 64 bits, and everything that
+follows them against the formulas in 64 bits on the returned fp32 logits.
+
+The chosen ids have to be equal for every token (the call promises the choice
+of the formulas in binary64); weights are a few binary32 operations on the
+chosen logits: within 2^-19 of their value, exponents of up to 2^7 adding
+2^-24 * 2^7 = 2^-17 more."""
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_grouped_split_gb300 import binding as B
+from moe_expert_grouped_split_gb300 import inputs as I
+from moe_expert_grouped_split_gb300.build import build
+
+pytestmark = pytest.mark.gpu
+
+W_TOL = 2.0 ** -16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build()
+
+
+def formula(z, bias, how, k):
+    """(ids ascending, weights, choice values) of fp32 logits z in 64 bits."""
+    z = z.astype(np.float64)
+    T, E = z.shape
+    e = np.exp(-np.abs(z))
+    if how.score == B.SCORE_SIGMOID:
+        s = np.where(z >= 0, 1.0, e) / (1.0 + e)
+    else:
+        s = np.exp(z - z.max(axis=1, keepdims=True))
+        s = s / s.sum(axis=1, keepdims=True)
+    c = s if bias is None else s + bias.astype(np.float64)
+    G = how.n_groups
+    left = c
+    if how.top_groups < G:
+        by = np.sort(c.reshape(T, G, E // G), axis=2)
+        v = by[:, :, -1]
+        if how.group_score == B.GROUP_TOP2 and E // G > 1:
+            v = by[:, :, -1] + by[:, :, -2]
+        kept = np.argsort(-v, axis=1, kind="stable")[:, :how.top_groups]
+        in_kept = np.zeros((T, G), bool)
+        np.put_along_axis(in_kept, kept, True, axis=1)
+        mask = np.repeat(in_kept, E // G, axis=1)
+    else:
+        mask = np.ones((T, E), bool)
+    ids = np.empty((T, k), np.int64)
+    for t in range(T):
+        at = np.nonzero(mask[t])[0]
+        ids[t] = np.sort(at[np.argsort(-left[t, at], kind="stable")[:k]])
+    w = np.take_along_axis(s, ids, axis=1)
+    if bias is not None:
+        w = np.where(np.isneginf(bias[ids]), 0.0, w)
+    if how.renormalize:
+        total = w.sum(axis=1, keepdims=True)
+        w = np.divide(w, total, out=np.zeros_like(w), where=total > 0)
+    return ids, w * np.float64(np.float32(how.scale)), c
+
+
+def route(T, H, E, k, how, x=None, wr=None, bias=None, seed=0, std=None, keep_logits=True, status=0):
+    rt = B.Runtime(H, 64, E, k, 0, T, 1, 0)
+    try:
+        if x is None:
+            x = I.make_tokens(T, H, seed).cuda()
+        if wr is None:
+            wr = I.randn_bf16((E, H), std or I.sqrt_inv(H), I.seed_for(seed, "Wr")).cuda()
+        rb = B.RouteBuffers(T, E, k, keep_logits=keep_logits)
+        for t in (rb.topk_ids, rb.counts, rb.offsets, rb.perm, rb.inv_perm):
+            t.fill_(-7)
+        rb.topk_w.fill_(float("nan"))
+        torch.cuda.synchronize()
+        rt.route_scored(x, wr, torch.from_numpy(bias).cuda() if bias is not None else None, how, rb)
+        torch.cuda.synchronize()
+        assert rt.device_status() == status
+        return x, wr, rb
+    finally:
+        rt.close()
+
+
+def check(T, E, k, how, bias, rb):
+    z = rb.logits.cpu().numpy()
+    ids, w, _ = formula(z, bias, how, k)
+    got = rb.topk_ids.cpu().numpy()
+    bad = np.nonzero((got != ids).any(axis=1))[0]
+    assert bad.size == 0, f"{bad.size} of {T} tokens, first {bad[0]}: {got[bad[0]]} for {ids[bad[0]]}"
+    dw = np.abs(rb.topk_w.cpu().numpy().astype(np.float64) - w)
+    assert (dw <= W_TOL * w + 1e-37).all(), dw.max()
+    flat = ids.reshape(-1)
+    counts = np.bincount(flat, minlength=E)
+    perm = np.argsort(flat, kind="stable")
+    inv = np.empty_like(perm)
+    inv[perm] = np.arange(T * k)
+    assert np.array_equal(rb.counts.cpu().numpy(), counts)
+    assert np.array_equal(rb.offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(counts)]))
+    assert np.array_equal(rb.perm.cpu().numpy(), perm) and np.array_equal(rb.inv_perm.cpu().numpy(), inv)
+
+
+def how_of(score, G=1, top=1, gs=B.GROUP_MAX, renorm=True, scale=1.0):
+    return B.scoring(score, G, top, gs, renorm, scale)
+
+
+SIG, SOFT = B.SCORE_SIGMOID, B.SCORE_SOFTMAX
+CASES = [
+    # T, H, E, k, how, biased
+    (1, 7168, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (2, 7168, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (17, 7168, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (64, 1024, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (129, 1024, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (1003, 512, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (4099, 256, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, False, 1.0), True),
+    (300, 512, 160, 6, how_of(SOFT, 8, 3, B.GROUP_MAX, False, 16.0), False),
+    (300, 512, 160, 6, how_of(SOFT, 8, 3, B.GROUP_TOP2, True, 1.0), True),
+    (77, 128, 64, 6, how_of(SOFT), False),
+    (77, 128, 64, 1, how_of(SOFT, renorm=False), False),
+    (77, 128, 60, 4, how_of(SIG), True),
+    (50, 128, 300, 16, how_of(SIG, 5, 2, B.GROUP_TOP2), True),
+    (40, 128, 1020, 32, how_of(SIG, 17, 9, B.GROUP_TOP2), True),
+    (40, 128, 1024, 32, how_of(SOFT, 32, 2, B.GROUP_MAX), True),
+    (40, 128, 1024, 32, how_of(SOFT), False),
+    (40, 128, 992, 3, how_of(SIG, 31, 1, B.GROUP_TOP2), False),
+    (9, 64, 32, 2, how_of(SIG, 32, 2, B.GROUP_TOP2), True),      # groups of one expert
+    (9, 64, 8, 8, how_of(SIG, 4, 4, B.GROUP_TOP2), True),        # everything is chosen
+    (9, 64, 8, 4, how_of(SOFT, 4, 2, B.GROUP_TOP2), True),       # everything in the kept groups
+    (5, 64, 1, 1, how_of(SIG), False),
+    (33, 64, 7, 3, how_of(SOFT, 7, 3, B.GROUP_MAX), False),
+]
+
+
+@pytest.mark.parametrize("T, H, E, k, how, biased", CASES,
+                         ids=[f"T{c[0]}_H{c[1]}_E{c[2]}_k{c[3]}_G{c[4].n_groups}" + f"_{i}" for i, c in enumerate(CASES)])
+def test_routes_as_the_formulas_say(T, H, E, k, how, biased):
+    bias = np.random.default_rng(E + k).normal(0, 0.1, E).astype(np.float32) if biased else None
+    x, wr, rb = route(T, H, E, k, how, bias=bias, seed=T + E)
+    z = rb.logits.cpu().numpy().astype(np.float64)
+    ref = (x.double() @ wr.double().t()).cpu().numpy()
+    # fp32 sums of H products: each step off by 2^-24 of a partial sum at most
+    mag = (x.double().abs() @ wr.double().abs().t()).cpu().numpy()
+    assert (np.abs(z - ref) <= 2.0 ** -24 * np.sqrt(H) * mag + 1e-30).all()
+    check(T, E, k, how, bias, rb)
+    _, _, again = route(T, H, E, k, how, x=x, wr=wr, bias=bias, keep_logits=False)
+    for name in ("topk_ids", "topk_w", "counts", "offsets", "perm", "inv_perm"):
+        assert torch.equal(getattr(rb, name), getattr(again, name)), name
+
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("G, top", [(1, 1), (4, 2)])
+def test_equal_scores_tie_to_the_lowest_group_and_id(score, G, top):
+    T, H, E, k = 37, 128, 64, 6
+    wr = torch.zeros((E, H), dtype=torch.bfloat16, device="cuda")
+    how = how_of(score, G, top, B.GROUP_TOP2)
+    _, _, rb = route(T, H, E, k, how, wr=wr)
+    assert (rb.topk_ids.cpu().numpy() == np.arange(k)).all()
+    check(T, E, k, how, None, rb)
+
+
+@pytest.mark.parametrize("std", [0.5, 3.0, 20.0])
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_saturated_scores(score, std):
+    """Logits so far out that binary32 scores are 0 or 1 for many experts."""
+    T, H, E, k = 200, 128, 64, 6
+    for how in (how_of(score, 4, 2, B.GROUP_TOP2), how_of(score, renorm=False)):
+        _, _, rb = route(T, H, E, k, how, std=std, seed=3)
+        check(T, E, k, how, None, rb)
+
+
+def test_choices_next_to_each_other():
+    """Biases that differ by less than binary32's rounding of a score: the
+    decision is the one in 64 bits."""
+    T, H, E, k = 400, 128, 64, 6
+    rng = np.random.default_rng(1)
+    bias = (rng.integers(0, 3, E) * 1e-8).astype(np.float32)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = torch.from_numpy(rng.integers(-3, 4, T).astype(np.float32)).cuda()
+    wr = torch.zeros((E, H), dtype=torch.bfloat16, device="cuda")
+    wr[:, 0] = torch.from_numpy(rng.integers(-1, 2, E).astype(np.float32)).cuda()
+    for how in (how_of(SIG), how_of(SIG, 8, 3, B.GROUP_TOP2), how_of(SOFT, 8, 3, B.GROUP_MAX)):
+        _, _, rb = route(T, H, E, k, how, x=x, wr=wr, bias=bias)
+        check(T, E, k, how, bias, rb)
+
+
+def test_experts_taken_out():
+    T, H, E, k = 100, 128, 32, 4
+    rng = np.random.default_rng(2)
+    for left, G, top in ((20, 1, 1), (20, 4, 2), (2, 1, 1), (0, 1, 1), (0, 4, 2)):
+        bias = np.full(E, -np.inf, np.float32)
+        bias[rng.permutation(E)[:left]] = rng.normal(0, 0.1, left)
+        for renorm in (True, False):
+            how = how_of(SIG, G, top, B.GROUP_MAX, renorm, 2.5)
+            _, _, rb = route(T, H, E, k, how, bias=bias)
+            check(T, E, k, how, bias, rb)
+            w = rb.topk_w.cpu().numpy()
+            assert (w[np.isneginf(bias[rb.topk_ids.cpu().numpy()])] == 0).all()
+
+
+def test_non_finite_logits_and_biases_are_reported():
+    T, H, E, k = 200, 256, 16, 4
+    x = I.make_tokens(T, H, 9).cuda()
+    x[17, 3] = float("nan")
+    how = how_of(SIG, 4, 2, B.GROUP_TOP2)
+    x, wr, rb = route(T, H, E, k, how, x=x, status=-6)
+    ids = rb.topk_ids.cpu().numpy()
+    assert all(len(set(r.tolist())) == k and r.min() >= 0 and r.max() < E for r in ids)
+    clean = x.clone()
+    clean[17, 3] = 0.0
+    _, _, ok = route(T, H, E, k, how, x=clean, wr=wr)
+    good = np.arange(T) != 17
+    assert np.array_equal(ids[good], ok.topk_ids.cpu().numpy()[good])
+    for v in (float("nan"), float("inf")):
+        bias = np.zeros(E, np.float32)
+        bias[5] = v
+        _, _, rb = route(T, H, E, k, how, x=clean, wr=wr, bias=bias, status=-6)
+        assert all(len(set(r.tolist())) == k for r in rb.topk_ids.cpu().numpy())
+
+
+def test_no_tokens():
+    rt = B.Runtime(256, 64, 16, 4, 0, 8, 1, 0)
+    rb = B.RouteBuffers(0, 16, 4)
+    rb.counts.fill_(3)
+    rb.offsets.fill_(3)
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    rt.route_scored(x, torch.zeros((16, 256), dtype=torch.bfloat16, device="cuda"), None, how_of(SIG), rb)
+    torch.cuda.synchronize()
+    assert (rb.counts == 0).all() and (rb.offsets == 0).all()
+    rt.close()
+
+
+def test_refusals():
+    T, H, E, k = 8, 256, 16, 4
+    rt = B.Runtime(H, 64, E, k, 0, T, 1, 0)
+    try:
+        x = I.make_tokens(T, H, 1).cuda()
+        wr = I.randn_bf16((E, H), 0.02, 2).cuda()
+        rb = B.RouteBuffers(T, E, k)
+        bad = [(how_of(2), -1), (how_of(SIG, 0, 1), -1), (how_of(SIG, 3, 1), -1), (how_of(SIG, 4, 0), -1),
+               (how_of(SIG, 4, 5), -1), (how_of(SIG, 8, 1), -1), (how_of(SIG, 1, 1, 2), -1),
+               (how_of(SIG, scale=0.0), -1), (how_of(SIG, scale=float("nan")), -1),
+               (how_of(SIG, scale=float("inf")), -1), (how_of(SIG, scale=-1.0), -1)]
+        for how, code in bad:
+            with pytest.raises(B.DwdpError) as ei:
+                rt.route_scored(x, wr, None, how, rb)
+            assert ei.value.code == code
+        how = how_of(SIG)
+        how.renormalize = 2
+        with pytest.raises(B.DwdpError):
+            rt.route_scored(x, wr, None, how, rb)
+        for args in ((x.cpu().pin_memory(), wr, None), (x, wr.cpu().pin_memory(), None), (None, wr, None)):
+            with pytest.raises(B.DwdpError) as ei:
+                B.dwdp_route_scored(rt.ctx, args[0], T, args[1], args[2], how_of(SIG), rb.c, rt.ws, rt.ws_bytes)
+            assert ei.value.code == -1
+        with pytest.raises(B.DwdpError):
+            B.dwdp_route_scored(rt.ctx, x, T + 1, wr, None, how_of(SIG), rb.c, rt.ws, rt.ws_bytes)
+        with pytest.raises(B.DwdpError):
+            B.dwdp_route_scored(rt.ctx, x, T, wr, None, how_of(SIG), rb.c, rt.ws, 16)
+        torch.cuda.synchronize()
+        assert rt.device_status() == 0
+    finally:
+        rt.close()
+    big = B.Runtime(256, 64, 64, 1, 0, T, 1, 0)
+    try:
+        with pytest.raises(B.DwdpError) as ei:
+            big.route_scored(x, torch.zeros((64, 256), dtype=torch.bfloat16, device="cuda"), None,
+                             how_of(SIG, 64, 1), B.RouteBuffers(T, 64, 1))
+        assert ei.value.code == -5
+    finally:
+        big.close()
