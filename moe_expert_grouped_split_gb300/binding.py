@@ -139,10 +139,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current_raw_stream = None
+
+
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a torch.cuda.Stream object
+        # around it (0.2 us a call instead of 2.9 us)
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            import torch
+            torch.cuda.init()
+            get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_raw_stream = lambda: get(device())
+        return _current_raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -898,7 +898,9 @@ int32_t dwdp_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, 
 }
 
 size_t dwdp_lora_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t R) {
-    if (T < 0 || K <= 0 || N <= 0 || K % 8 || N % 8 || R <= 0 || R % 8 || R > DWDP_MAX_LORA_RANK) return 0;
+    if (T < 0 || T > (1 << 30) || K <= 0 || N <= 0 || K > (1 << 20) || N > (1 << 20) || K % 8 || N % 8 || R <= 0 ||
+        R % 8 || R > DWDP_MAX_LORA_RANK)
+        return 0;
     return std::max<size_t>(256, lora_workspace_bytes(T, K, N, R));
 }
 
@@ -911,7 +913,7 @@ int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T,
     if (T < 0 || n_adapters < 1) return fail(ctx, DWDP_ERR_INVALID_ARG, "T >= 0 and n_adapters >= 1");
     const size_t need = dwdp_lora_workspace_bytes(T, K, N, R);
     if (need == 0)
-        return fail(ctx, DWDP_ERR_UNSUPPORTED, "K, N and R must be positive multiples of 8, R <= %d",
+        return fail(ctx, DWDP_ERR_UNSUPPORTED, "K, N and R must be positive multiples of 8, K, N <= 2^20, R <= %d; T <= 2^30",
                     DWDP_MAX_LORA_RANK);
     if (x_stride < K || x_stride % 8 || base_stride < N || base_stride % 8 || out_stride < N || out_stride % 8)
         return fail(ctx, DWDP_ERR_INVALID_ARG, "strides must be multiples of 8, no smaller than the row");

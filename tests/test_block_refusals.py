@@ -44,7 +44,7 @@ def test_add_rmsnorm_of_no_rows_reads_nothing(lib):
 
 def test_lora_workspace(lib):
     for bad in ((-1, 64, 64, 16), (4, 60, 64, 16), (4, 64, 0, 16), (4, 64, 64, 0), (4, 64, 64, 12),
-                (4, 64, 64, 136)):
+                (4, 64, 64, 136), (4, (1 << 20) + 8, 64, 16), (4, 64, (1 << 20) + 8, 16), ((1 << 30) + 1, 64, 64, 16)):
         assert B.dwdp_lora_workspace_bytes(*bad) == 0
     last = 0
     for T in (0, 1, 17, 128, 129, 8192, 100000):
