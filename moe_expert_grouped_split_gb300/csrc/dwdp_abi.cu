@@ -204,7 +204,8 @@ WsLayout ws_layout(const dwdp_config& c, int64_t T) {
     const int fmt = c.weight_dtype;
     L.logits = 0;  // up to kRouterMaxSplit partial-sum planes of the router GEMM
     L.group = align_up((size_t)(kRouterMaxSplit * T * E * 4), 256);
-    L.route_bytes = L.group + align_up(group_chunked_scratch_bytes((int)(T * k), (int)E), 256);
+    L.route_bytes = L.group + align_up(std::max(group_chunked_scratch_bytes((int)(T * k), (int)E),
+                                                scored_scratch_bytes(T, E, k)), 256);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -849,8 +850,14 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     DWDP_CUDA(ctx, mark(ctx, 0, stream));
     ScoredArgs p{};
     float* logits = nullptr;
-    const int32_t rg = router_gemm(ctx, x, T, w_router, nullptr, out->logits, ws, stream, p.parts, logits);
-    if (rg != DWDP_OK) return rg;
+    if (T <= kRouterSmallTokens) {
+        p.parts = 1;
+        logits = out->logits ? out->logits : reinterpret_cast<float*>(static_cast<char*>(ws) + ws_layout(c, T).logits);
+        DWDP_CUDA(ctx, launch_router_small(x, w_router, T, c.n_experts, c.hidden, logits, stream));
+    } else {
+        const int32_t rg = router_gemm(ctx, x, T, w_router, nullptr, out->logits, ws, stream, p.parts, logits);
+        if (rg != DWDP_OK) return rg;
+    }
     p.logits = logits;
     p.part_stride = (int64_t)T * c.n_experts;
     p.bias = choice_bias;
@@ -867,11 +874,12 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     p.group_top2 = sc.group_score == DWDP_GROUP_TOP2;
     p.renorm = sc.renormalize != 0;
     p.scale = sc.scale;
-    scored_layout(p);
-    DWDP_CUDA(ctx, launch_scored_topk(p, stream));
-    int32_t* group_scratch = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + ws_layout(c, T).group);
-    DWDP_CUDA(ctx, launch_group_chunked(out->topk_ids, T * c.top_k, c.n_experts, out->counts, out->offsets, out->perm,
-                                        out->inv_perm, group_scratch, stream));
+    p.counts = out->counts;
+    p.offsets = out->offsets;
+    p.perm = out->perm;
+    p.inv_perm = out->inv_perm;
+    p.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + ws_layout(c, T).group);
+    DWDP_CUDA(ctx, launch_scored_choice(p, stream));
     DWDP_CUDA(ctx, mark(ctx, 1, stream));
     return DWDP_OK;
 }

@@ -217,26 +217,39 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* resi
                                const void* weight, float eps, int64_t rows, int H, void* out, void* codes,
                                float* row_scale, cudaStream_t s);
 
-// route_scored.cu: the choice of dwdp_route_scored.  logits: `parts` fp32
+// router.cu: z [T][E] = x [T][H] W [E][H]^T in fp32 for T <= kRouterSmallTokens.
+constexpr int kRouterSmallTokens = 256;
+cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s);
+
+// route_scored.cu: dwdp_route_scored from the logits on.  logits: `parts` fp32
 // planes [T][E] part_stride apart, summed in plane order; z_out, if not null,
-// receives the sums.  The members after `err` are filled by scored_layout.
+// receives the sums; hist: scored_scratch_bytes(T, E, k) of scratch.  The
+// members after `scale` are filled by launch_scored_choice.
 struct ScoredArgs {
     const float* logits;
     int64_t part_stride;
     const float* bias;
     int32_t* ids;
     float* w;
+    int32_t* counts;
+    int32_t* offsets;
+    int32_t* perm;
+    int32_t* inv_perm;
+    int32_t* hist;
     float* z_out;
     int* err;
     int parts, T, E, k;
     int n_groups, top_groups;
     bool sigmoid, group_top2, renorm;
     float scale;
-    int lanes, group_size, per_lane;
+    int lanes, group_size, per_lane, chunk_tokens;
     bool vector_loads;
 };
-void scored_layout(ScoredArgs& p);
-cudaError_t launch_scored_topk(const ScoredArgs& p, cudaStream_t s);
+size_t scored_scratch_bytes(int64_t T, int64_t E, int64_t k);
+cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s);
+// route.cu's chunk_scan_kernel on its own: hist [n_chunks][E] counts to each
+// chunk's first rows, counts [E] and offsets [E + 1].
+cudaError_t launch_chunk_scan(int32_t* hist, int n_chunks, int E, int32_t* counts, int32_t* offsets, cudaStream_t s);
 
 // lora.cu: dwdp_lora_add (arguments as there, checked).
 struct LoraArgs {

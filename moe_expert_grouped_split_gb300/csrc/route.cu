@@ -1019,6 +1019,11 @@ size_t group_chunked_scratch_bytes(int n, int E) {
     return sizeof(int32_t) * (size_t)((n + kChunk - 1) / kChunk) * (size_t)E;
 }
 
+cudaError_t launch_chunk_scan(int32_t* hist, int n_chunks, int E, int32_t* counts, int32_t* offsets, cudaStream_t s) {
+    chunk_scan_kernel<<<1, 1024, 0, s>>>(hist, n_chunks, E, counts, offsets);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_group_chunked(const int32_t* ids, int n, int E, int32_t* counts, int32_t* offsets, int32_t* perm,
                                  int32_t* inv, int32_t* scratch, cudaStream_t s) {
     const int n_chunks = (n + kChunk - 1) / kChunk;

@@ -1,0 +1,133 @@
+// router.cu: the router's logits for few tokens (dwdp_route_scored):
+// z [T][E] = x W^T, fp32.
+//
+// Few tokens read W once and little else, so what counts is that the whole
+// GPU loads at once and how few round trips a launch needs: a tile of 16 or
+// 32 tokens x 16 or 32 experts is a cluster of 8 CTAs of 8 warps, 64 parts of
+// K, all of a part's loads issued before its first product; the parts meet in
+// shared memory, then across the cluster, in order.
+#include <cuda_bf16.h>
+
+#include "dwdp_internal.h"
+
+namespace dwdp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// MT m16 tiles of tokens x NT n8 tiles of experts.  A step is 32 elements of
+// K: thread q of a row's four takes 8 neighbours, 16 bytes, as the operands
+// of two MMAs (the order of k is free as long as both operands share it).
+template <int MT, int NT, int U>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+    router_small_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w, int T, int E, int H,
+                        float* __restrict__ z) {
+    constexpr int kTile = MT * 16 * NT * 8;
+    __shared__ __align__(16) float part[kWarps][kTile];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int rank = blockIdx.x % kCluster;
+    const int t0 = (int)(blockIdx.x / kCluster) * MT * 16, e0 = (int)blockIdx.y * NT * 8;
+    const int hv = H / 8, steps = H / 32;
+    const int at = rank * kWarps + warp;
+    const int step0 = steps * at / (kCluster * kWarps), step1 = steps * (at + 1) / (kCluster * kWarps);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    float acc[MT][NT][4] = {};
+    for (int st = step0; st < step1; st += U) {
+        uint4 xv[U][2 * MT], wv[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (st + u) * 4 + q;
+            const bool in = st + u < step1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int e = e0 + j * 8 + g;
+                wv[u][j] = in && e < E ? __ldg(w + (int64_t)e * hv + k) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                const int t = t0 + i * 8 + g;
+                xv[u][i] = in && t < T ? __ldg(x + (int64_t)t * hv + k) : make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint4 &lo = xv[u][2 * m], &hi = xv[u][2 * m + 1], &b = wv[u][j];
+                    mma16816(acc[m][j], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+                    mma16816(acc[m][j], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+                }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(&part[warp][(m * 16 + h * 8 + g) * NT * 8 + j * 8 + 2 * q]) =
+                    make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile; i += kThreads) {
+        float s = part[0][i];
+#pragma unroll
+        for (int v = 1; v < kWarps; ++v) s += part[v][i];
+        part[0][i] = s;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int i = rank * (kTile / kCluster) + threadIdx.x; i < (rank + 1) * (kTile / kCluster); i += kThreads) {
+        const uint32_t here = (uint32_t)__cvta_generic_to_shared(&part[0][i]);
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            uint32_t there;
+            float v;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(c));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+            s += v;
+        }
+        const int t = t0 + i / (NT * 8), e = e0 + i % (NT * 8);
+        if (t < T && e < E) z[(int64_t)t * E + e] = s;
+    }
+    // nobody leaves while another rank may still read its shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int MT, int NT, int U>
+cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((T + MT * 16 - 1) / (MT * 16) * kCluster, (E + NT * 8 - 1) / (NT * 8));
+    c.blockDim = dim3(kThreads);
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, router_small_kernel<MT, NT, U>, static_cast<const uint4*>(x),
+                              static_cast<const uint4*>(w), T, E, H, z);
+}
+
+}  // namespace
+
+cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
+    if (T <= 16) return launch<1, 2, 4>(x, w, T, E, H, z, s);
+    return launch<2, 4, 2>(x, w, T, E, H, z, s);
+}
+
+}  // namespace dwdp

@@ -126,6 +126,11 @@ CASES = [
     (9, 64, 8, 8, how_of(SIG, 4, 4, B.GROUP_TOP2), True),        # everything is chosen
     (9, 64, 8, 4, how_of(SOFT, 4, 2, B.GROUP_TOP2), True),       # everything in the kept groups
     (5, 64, 1, 1, how_of(SIG), False),
+    (17003, 64, 64, 8, how_of(SIG, 8, 4, B.GROUP_TOP2), True),   # more chunks of pairs than the placing blocks sum up
+    (129, 7168, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2), True),
+    (255, 576, 40, 3, how_of(SOFT), True),
+    (31, 7168, 24, 3, how_of(SIG), False),
+    (700, 7168, 512, 8, how_of(SIG, 8, 4, B.GROUP_TOP2), True),
     (33, 64, 7, 3, how_of(SOFT, 7, 3, B.GROUP_MAX), False),
 ]
 
