@@ -243,7 +243,6 @@ struct ScoredArgs {
     bool sigmoid, group_top2, renorm;
     float scale;
     int lanes, group_size, per_lane, chunk_tokens;
-    bool vector_loads;
 };
 size_t scored_scratch_bytes(int64_t T, int64_t E, int64_t k);
 cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s);

@@ -12,24 +12,24 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Order-preserving keys: a > b iff key(a) > key(b); -0 folds into +0, every
-// NaN is above +inf, and no value has key 0, which marks "not a candidate".
+// Order-preserving keys: a > b iff key(a) > key(b).  Made of results of
+// arithmetic only: a sum never gives -0 here (scores are not negative), and a
+// NaN is the positive one, above +inf.  No value has key 0, which marks "not
+// a candidate".
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x) return 0xFFFFFFFFu;
-    const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+    return __uint_as_float(k ^ (((k >> 31) - 1u) | 0x80000000u));
 }
 constexpr uint64_t kSign64 = 0x8000000000000000ull;
 __device__ __forceinline__ uint64_t order_key(double x) {
-    if (x != x) return ~0ull;
-    const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
-    return (u & kSign64) ? ~u : (u | kSign64);
+    const uint64_t u = (uint64_t)__double_as_longlong(x);
+    return u ^ ((uint64_t)((int64_t)u >> 63) | kSign64);
 }
 __device__ __forceinline__ double key_value(uint64_t k) {
-    return __longlong_as_double((long long)((k & kSign64) ? (k & ~kSign64) : ~k));
+    return __longlong_as_double((long long)(k ^ (((k >> 63) - 1ull) | kSign64)));
 }
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kFull, k); }
@@ -38,6 +38,26 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return ((uint64_t)hi << 32) | lo;
 }
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// 2^x, and 1 / x: a few units in the last place, results below the normal
+// range are 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
@@ -64,41 +84,49 @@ struct Lane {
     }
 };
 
-// z[j] = the token's logit of expert first + j: the partial-sum planes of a
-// K-split router GEMM added in plane order.  Whole runs in 16-byte loads.
-template <int P>
-__device__ __forceinline__ void load_logits(const ScoredArgs& p, int64_t t, const Lane& ln, float (&z)[P]) {
-    const float* src = p.logits + t * p.E + ln.first;
-    if (P >= 4 && p.vector_loads) {
+// The kernels come in two forms.  FULL: every lane holds exactly P experts
+// (32 P = E and whole groups), so nothing asks whether expert j exists; and
+// runs are read in 16-byte pieces (8 for P = 2).  In the other form a lane
+// holds n <= P of them.
+template <int P, bool FULL>
+__device__ __forceinline__ bool has(const Lane& ln, int j) {
+    return FULL || j < ln.n;
+}
+
+// v[j] = src[first + j]
+template <int P, bool FULL>
+__device__ __forceinline__ void load_run(const float* src, const Lane& ln, float (&v)[P]) {
+    src += ln.first;
+    if constexpr (FULL && P >= 4) {
 #pragma unroll
         for (int j = 0; j < P; j += 4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j < ln.n) {
-                v = *reinterpret_cast<const float4*>(src + j);
-                for (int q = 1; q < p.parts; ++q) {
-                    const float4 u = *reinterpret_cast<const float4*>(src + q * p.part_stride + j);
-                    v.x += u.x;
-                    v.y += u.y;
-                    v.z += u.z;
-                    v.w += u.w;
-                }
-            }
-            z[j] = v.x;
-            if (P >= 4) {
-                z[(j + 1) % P] = v.y;
-                z[(j + 2) % P] = v.z;
-                z[(j + 3) % P] = v.w;
-            }
+            const float4 f = *reinterpret_cast<const float4*>(src + j);
+            v[j] = f.x;
+            v[j + 1] = f.y;
+            v[j + 2] = f.z;
+            v[j + 3] = f.w;
         }
+    } else if constexpr (FULL && P == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[0] = f.x;
+        v[1] = f.y;
     } else {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            z[j] = 0.0f;
-            if (j < ln.n) {
-                z[j] = src[j];
-                for (int q = 1; q < p.parts; ++q) z[j] += src[q * p.part_stride + j];
-            }
-        }
+        for (int j = 0; j < P; ++j) v[j] = has<P, FULL>(ln, j) ? src[j] : 0.0f;
+    }
+}
+
+// z[j] = the token's logit of expert first + j: the partial-sum planes of a
+// K-split router GEMM added in plane order.
+template <int P, bool FULL>
+__device__ __forceinline__ void load_logits(const ScoredArgs& p, int64_t t, const Lane& ln, float (&z)[P]) {
+    load_run<P, FULL>(p.logits + t * p.E, ln, z);
+#pragma unroll 1
+    for (int q = 1; q < p.parts; ++q) {
+        float u[P];
+        load_run<P, FULL>(p.logits + q * p.part_stride + t * p.E, ln, u);
+#pragma unroll
+        for (int j = 0; j < P; ++j) z[j] += u[j];
     }
 }
 
@@ -126,12 +154,14 @@ struct Best2 {
     }
 };
 
-// The error of a binary32 choice value v against the formula's is at most half
-// of rel (ref or |v|) + 2^-22 |v|: two values further apart than that are in
-// the right order.  A sigmoid s is off by at most s (1 - s) 2^-23 (expf) +
-// 2^-24 s (the sum) + 2^-24 s (the quotient) < 2^-22 s; a softmax term by the
-// roundings of its sum of per_lane + 5 terms as well, 2^-24 each.  Without a
-// bias the value is the score (softmax: unnormalised) and ref is 0.
+// Two choice values further apart than (*this)(v) are in the right order.  A
+// binary32 value's error is at most half of rel (ref or |v|) + 2^-22 |v|.
+// With ex2.approx and its argument's rounding, |z| <= most:
+//   sigmoid      s (1 - s) (1.7 |z| 2^-24 + 2^-22) + s 2^-22: 2^-21 of 1 at
+//                most, or (most 2^-23 + 2^-21) of s
+//   softmax term e (2.7 |z - max| 2^-24 + 2^-22): with a bias 2^-21 of the
+//                largest and the roundings of the sum of per_lane + 5; without
+//                one unnormalised, so (most 2^-21 + 2^-22) of e
 struct Tolerance {
     float rel, ref;
     __device__ __forceinline__ float operator()(float v) const {
@@ -139,117 +169,85 @@ struct Tolerance {
     }
 };
 
-// Keys of the choice values (0: no expert) from the logits in z.  zm is the
-// largest logit, total the softmax denominator; both 1 and unused for sigmoid.
-template <int P>
+// Keys of the choice values (0: no expert) from the logits in z.  Without a
+// bias the value is the score (softmax: unnormalised).  zm is the largest
+// logit, total the softmax denominator (neither set for sigmoid).
+template <int P, bool FULL>
 __device__ __forceinline__ Tolerance choice_keys(const ScoredArgs& p, const Lane& ln, float (&z)[P],
                                                  uint32_t (&key)[P], float& zm, float& total, bool& finite) {
-    finite = true;
-    zm = -CUDART_INF_F;
+    float most = 0.0f, worst = 0.0f;
 #pragma unroll
-    for (int j = 0; j < P; ++j)
-        if (j < ln.n) {
-            finite = finite && isfinite(z[j]);
-            zm = fmaxf(zm, z[j]);
+    for (int j = 0; j < P; ++j) most = max_nan(most, fabsf(z[j]));  // (0 where there is no expert)
+    finite = most < CUDART_INF_F;
+    zm = total = 0.0f;
+    float factor = 1.0f;
+    if (p.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float e = exp2_fast(-kLog2e * fabsf(z[j]));
+            z[j] = (z[j] >= 0.0f ? 1.0f : e) * rcp_fast(1.0f + e);
         }
-    total = 1.0f;
-    if (!p.sigmoid) {
-        zm = warp_max(zm);
-        float sum = 0.0f;
+    } else {
+        zm = -CUDART_INF_F;
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            if (j < ln.n) {
-                z[j] = expf(z[j] - zm);
-                sum += z[j];
-            }
-        total = warp_sum(sum);
-    }
-    const float inv = 1.0f / total;
-    float top = 0.0f;
+            if (has<P, FULL>(ln, j)) zm = fmaxf(zm, z[j]);
+        zm = warp_max(zm);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        key[j] = 0u;
-        if (j < ln.n) {
-            float s = z[j];
-            if (p.sigmoid) {
-                const float e = expf(-fabsf(z[j]));
-                s = (z[j] >= 0.0f ? 1.0f : e) / (1.0f + e);
-            }
-            if (p.bias) {
-                if (!p.sigmoid) s *= inv;
-                top = fmaxf(top, s);
-                const float b = __ldg(p.bias + ln.first + j);
-                finite = finite && b < CUDART_INF_F;  // false for NaN too
-                s += b;
-            }
-            key[j] = order_key(s);
+        for (int j = 0; j < P; ++j) {
+            z[j] = has<P, FULL>(ln, j) ? exp2_fast(kLog2e * (z[j] - zm)) : 0.0f;
+            total += z[j];
+        }
+        total = warp_sum(total);
+        if (p.bias) factor = 1.0f / total;
+    }
+    if (p.bias) {
+        float b[P];
+        load_run<P, FULL>(p.bias, ln, b);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            z[j] = fmaf(z[j], factor, b[j]);
+            worst = max_nan(worst, z[j]);  // +inf or NaN where the bias is
         }
     }
-    finite = __all_sync(kFull, finite);
-    return Tolerance{p.sigmoid ? 0x1p-21f : (float)(p.per_lane + 12) * 0x1p-23f, p.bias ? warp_max(top) : 0.0f};
-}
-
-// The value itself in binary64 (softmax: total is the denominator with a
-// bias, 1 without).
-__device__ __forceinline__ double choice_in_64(const ScoredArgs& p, float z, int expert, float zm, double total) {
-    double s;
-    if (p.sigmoid) {
-        const double e = exp(-fabs((double)z));
-        s = (z >= 0.0f ? 1.0 : e) / (1.0 + e);
-    } else {
-        s = exp((double)z - (double)zm) / total;
-    }
-    return p.bias ? s + (double)p.bias[expert] : s;
-}
-
-// A group's best two (by all its lanes) and its score.
-template <class K>
-__device__ __forceinline__ K group_score(const ScoredArgs& p, const Lane& ln, K& k1, K& k2) {
-    for (int o = 1; o < p.lanes; o <<= 1) {
-        const K o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
-        k2 = max(min(k1, o1), max(k2, o2));
-        k1 = max(k1, o1);
-    }
-    const K score = p.group_top2 && k2 != 0 ? order_key(key_value(k1) + key_value(k2)) : k1;
-    return ln.g < p.n_groups ? score : (K)0;
-}
-
-// How many groups come before this lane's: larger, or as large and lower.
-template <class K>
-__device__ __forceinline__ int group_rank(const ScoredArgs& p, const Lane& ln, K score) {
-    int rank = 0;
-    for (int g = 0; g < p.n_groups; ++g) {
-        const K other = __shfl_sync(kFull, score, g * p.lanes);
-        rank += (other > score) || (other == score && g < ln.g);
-    }
-    return rank;
+#pragma unroll
+    for (int j = 0; j < P; ++j) key[j] = has<P, FULL>(ln, j) ? order_key(z[j]) : 0u;
+    finite = __all_sync(kFull, finite && worst < CUDART_INF_F);
+    most = __uint_as_float(warp_max(__float_as_uint(most)));
+    if (p.bias) return p.sigmoid ? Tolerance{0x1p-20f, 1.0f} : Tolerance{0x1p-18f + p.per_lane * 0x1p-23f, factor};
+    return Tolerance{p.sigmoid ? 0x1p-20f + most * 0x1p-22f : 0x1p-21f + most * 0x1p-20f, 0.0f};
 }
 
 // The k best of the lanes' keys.  Lane s < k gets the s-th pick's id; last is
-// the k-th pick's key, next the best left (0: none).  A lane offers its best
-// key; after a pick it falls back on its second, and looks through its run
-// again only when that is gone too.  Lane order is expert order, so the
-// lowest lane offering the largest key holds the lowest id.
-template <class K, int P>
-__device__ __forceinline__ int pick(const ScoredArgs& p, const K (&key)[P], const Best2<K>& best, const Lane& ln,
-                                    int lane, K& last, K& next) {
-    K offer = best.k1, second = best.k2;
+// the k-th pick's key, next the best left (0: none); a pick's own key goes to
+// its lane.  A lane offers its best key; after a pick it falls back on its
+// second, and looks through its run again only when that is gone too.  Lane
+// order is expert order, so the lowest lane offering the largest key holds
+// the lowest id.
+template <int P>
+__device__ __forceinline__ int pick(const ScoredArgs& p, const uint32_t (&key)[P], const Best2<uint32_t>& best,
+                                    const Lane& ln, int lane, uint32_t& my_key, uint32_t& last, uint32_t& next) {
+    uint32_t offer = best.k1, second = best.k2;
     int at = best.i1, at2 = best.i2, my_id = -1;
-    last = 0;
+    last = my_key = 0;
+#pragma unroll 1
     for (int s = 0; s < p.k; ++s) {
-        const K gk = warp_max(offer);
+        const uint32_t gk = warp_max(offer);
         if (gk == 0) break;  // fewer than k candidates (refused on the host)
         last = gk;
         const int owner = __ffs(__ballot_sync(kFull, offer == gk)) - 1;
         const int id = __shfl_sync(kFull, ln.first + at, owner);
-        if (lane == s) my_id = id;
+        if (lane == s) {
+            my_id = id;
+            my_key = gk;
+        }
         if (lane == owner) {
             if (second != 0) {
                 offer = second;
                 at = at2;
                 second = 0;
             } else {  // the best of what comes after (offer, at) in order
-                Best2<K> rest;
+                Best2<uint32_t> rest;
 #pragma unroll
                 for (int j = 0; j < P; ++j)
                     if (key[j] < offer || (key[j] == offer && j > at)) rest.add(key[j], j);
@@ -259,159 +257,137 @@ __device__ __forceinline__ int pick(const ScoredArgs& p, const K (&key)[P], cons
                 at2 = rest.i2;
             }
         }
+        __syncwarp();
     }
     next = warp_max(offer);
     return my_id;
 }
 
-// Shared memory of one warp for choose_close: the choice values' keys, and
-// the values in doubt with their keys in binary64.
+// --------------------------------------------------- what is too close --
+// Where binary32 cannot tell, what lies further from the decision than the
+// tolerance is settled, and only the values within it are listed and taken in
+// binary64 (which runs at 1/64 of binary32's rate or less: the whole choice
+// in it took a warp 30 us).
+
+// Shared memory of one warp: the listed experts and their values' keys.
 struct Scratch {
     uint64_t* exact;  // [E], by place in the list
-    uint32_t* key;    // [E]
-    int* list;        // [E]
-    static constexpr int kBytes = 16;  // per expert
+    int* list;        // [E], ascending
+    static constexpr int kBytes = 12;  // per expert
     __device__ Scratch(void* base, int E, int warp) {
-        char* at = static_cast<char*>(base) + (size_t)warp * E * kBytes;
+        char* at = static_cast<char*>(base) + (size_t)warp * ((E + 1) & ~1) * kBytes;
         exact = reinterpret_cast<uint64_t*>(at);
-        key = reinterpret_cast<uint32_t*>(at + 8 * (size_t)E);
-        list = reinterpret_cast<int*>(at + 12 * (size_t)E);
+        list = reinterpret_cast<int*>(at + 8 * (size_t)((E + 1) & ~1));
     }
+    static size_t bytes(int E, int warps) { return (size_t)warps * ((E + 1) & ~1) * kBytes; }
 };
 
-// The entry that follows (last, last_at) in the order of keys, largest first
-// and the lowest place among equals, of n keys in shared memory that `use`
-// admits; 0 if none.  Start with (all ones, -1).
-template <class K, class F>
-__device__ __forceinline__ void next_in_order(const K* keys, int n, int lane, K& last, int& last_at, F use) {
-    K best = 0;
-    int at = 0x7fffffff;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) {
-        const K c = keys[i];
-        if (c > best && (c < last || (c == last && i > last_at)) && use(i)) {
-            best = c;
-            at = i;
-        }
-    }
-    const K top = warp_max(best);
-    last_at = (int)__reduce_min_sync(kFull, best == top ? (unsigned)at : 0x7fffffffu);
-    last = top;
-}
-
-// The choice where binary32 cannot tell.  What lies further from a decision
-// than the tolerance is settled; the values within it are listed and taken in
-// binary64, 32 at a time (binary64 runs at 1/64 of binary32's rate or less,
-// so the whole choice in it would take a warp some 30 us).  Rare, so small:
-// loops over shared memory, nothing unrolled.  s.key holds the keys.
-__device__ __forceinline__ int choose_close(const ScoredArgs& p, int64_t t, int lane, const Scratch& s,
-                                            const Tolerance& tol, float zm) {
-    const int E = p.E, G = p.n_groups, gs = p.group_size;
+// The list's values in binary64.  zm: the largest logit (softmax).  No
+// exchange between lanes but the denominator's.
+__device__ __noinline__ void take_in_64(const ScoredArgs& p, int64_t t, int lane, const Scratch& s, int n, float zm) {
     double total = 1.0;
     if (!p.sigmoid && p.bias) {
-        double sum = 0.0;
+        total = 0.0;
 #pragma unroll 1
-        for (int e = lane; e < E; e += 32) sum += exp((double)logit_of(p, t, e) - (double)zm);
-        total = warp_sum(sum);
+        for (int e = lane; e < p.E; e += 32) total += exp((double)logit_of(p, t, e) - (double)zm);
+        total = warp_sum(total);
     }
-    auto take_in_64 = [&](int n) {
-        __syncwarp();
 #pragma unroll 1
-        for (int i = lane; i < n; i += 32) {
-            const int e = s.list[i];
-            s.exact[i] = order_key(choice_in_64(p, logit_of(p, t, e), e, zm, total));
-        }
-        __syncwarp();
-    };
-    uint32_t groups = kFull;  // the groups a token may choose from
-    if (p.top_groups < G) {
-        // lane g: group g
-        const bool is_group = lane < G;
-        uint32_t k1 = 0, k2 = 0;
-        if (is_group)
-#pragma unroll 1
-            for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
-                const uint32_t c = s.key[e];
-                k2 = max(k2, min(k1, c));
-                k1 = max(k1, c);
-            }
-        const bool two = p.group_top2 && k2 != 0;
-        const float v = two ? key_value(k1) + key_value(k2) : key_value(k1);
-        const uint32_t score = is_group ? order_key(v) : 0u;
-        int rank = 0;
-#pragma unroll 1
-        for (int g = 0; g < G; ++g) {
-            const uint32_t o = __shfl_sync(kFull, score, g);
-            rank += o > score || (o == score && g < lane);
-        }
-        const float edge = key_value(~warp_max(is_group && rank < p.top_groups ? ~score : 0u)), wide = 2.0f * tol(edge);
-        const bool sure = is_group && v > edge && !(v - edge <= wide);
-        const bool open = is_group && !sure && !(edge - v > wide);
-        const uint32_t sures = __ballot_sync(kFull, sure);
-        const uint32_t opens = __ballot_sync(kFull, open);
-        // the values that the open groups' scores may consist of
-        const float low = key_value(two ? k2 : k1), floor_of = low - tol(low);
-        int n = 0;
-#pragma unroll 1
-        for (int g = 0; g < G; ++g) {
-            if (!((opens >> g) & 1u)) continue;
-            const float floor_g = __shfl_sync(kFull, floor_of, g);
-#pragma unroll 1
-            for (int i = 0; i < gs; i += 32) {
-                const int e = g * gs + i + lane;
-                const bool in = i + lane < gs && !(key_value(s.key[e]) < floor_g);
-                const uint32_t ins = __ballot_sync(kFull, in);
-                if (in) s.list[n + __popc(ins & ((1u << lane) - 1u))] = e;
-                n += __popc(ins);
-            }
-        }
-        take_in_64(n);
-        uint64_t m1 = 0, m2 = 0;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i)
-            if (open && s.list[i] / gs == lane) {
-                const uint64_t c = s.exact[i];
-                m2 = max(m2, min(m1, c));
-                m1 = max(m1, c);
-            }
-        const uint64_t exact = open ? (p.group_top2 && m2 != 0 ? order_key(key_value(m1) + key_value(m2)) : m1) : 0;
-        rank = 0;
-#pragma unroll 1
-        for (int g = 0; g < G; ++g) {
-            const uint64_t o = __shfl_sync(kFull, exact, g);
-            rank += o > exact || (o == exact && g < lane);
-        }
-        groups = sures | __ballot_sync(kFull, open && rank < p.top_groups - __popc(sures));
+    for (int i = lane; i < n; i += 32) {
+        const int e = s.list[i];
+        const float z = logit_of(p, t, e);
+        double v = exp(p.sigmoid ? -fabs((double)z) : (double)z - (double)zm);
+        v = p.sigmoid ? (z >= 0.0f ? 1.0 : v) / (1.0 + v) : v / total;
+        if (p.bias) v += (double)p.bias[e];
+        s.exact[i] = order_key(v);
     }
-    auto allowed = [&](int e) { return ((groups >> (e / gs)) & 1u) != 0; };
-    // the k-th value, then what is above it beyond doubt and what is near it
-    uint32_t last = 0xffffffffu;
-    int at = -1;
-#pragma unroll 1
-    for (int i = 0; i < p.k; ++i) next_in_order(s.key, E, lane, last, at, allowed);
-    const float edge = key_value(last), wide = tol(edge);
-    int my_id = -1, n_sure = 0, n = 0;
-#pragma unroll 1
-    for (int i = 0; i < E; i += 32) {
-        const int e = i + lane;
-        const bool in = e < E && allowed(e);
-        const float v = in ? key_value(s.key[e]) : 0.0f;
-        const bool sure = in && v > edge && !(v - edge <= wide);
-        const bool open = in && !sure && !(edge - v > wide);
-        uint32_t sures = __ballot_sync(kFull, sure);
-        const uint32_t opens = __ballot_sync(kFull, open);
-        for (; sures != 0; sures &= sures - 1, ++n_sure)
-            if (lane == n_sure) my_id = i + __ffs(sures) - 1;
-        if (open) s.list[n + __popc(opens & ((1u << lane) - 1u))] = e;
-        n += __popc(opens);
+    __syncwarp();
+}
+
+// Lists the marked experts of all lanes (bit j: first + j) and takes them in
+// binary64; returns their number.
+__device__ __forceinline__ int list_in_64(const ScoredArgs& p, int64_t t, int lane, const Lane& ln, uint64_t bits,
+                                          const Scratch& s, float zm) {
+    const int mine = __popcll(bits);
+    int at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += u;
     }
-    take_in_64(n);
-    uint64_t last64 = ~0ull;
-    at = -1;
-#pragma unroll 1
+    const int n = __shfl_sync(kFull, at, 31);
+    at -= mine;
+    __syncwarp();
+    for (; bits != 0; bits &= bits - 1) s.list[at++] = ln.first + __ffsll((long long)bits) - 1;
+    __syncwarp();
+    take_in_64(p, t, lane, s, n, zm);
+    return n;
+}
+
+// Whether this lane's group stays, where the edge between kept and dropped
+// groups is too close.  k1, k2: the group's best two; score, edge: its score
+// and that of the last one kept.
+template <int P>
+__device__ __forceinline__ bool keep_close_group(const ScoredArgs& p, int64_t t, int lane, const Lane& ln,
+                                                 const uint32_t (&key)[P], uint32_t k1, uint32_t k2, uint32_t score,
+                                                 uint32_t edge_key, const Tolerance& tol, const Scratch& s, float zm) {
+    const float edge = key_value(edge_key), v = key_value(score), wide = 2.0f * tol(edge);
+    const bool is_group = ln.g < p.n_groups;
+    const bool sure = is_group && v > edge && !(v - edge <= wide);
+    const bool open = is_group && !sure && !(edge - v > wide);
+    const float low = key_value(p.group_top2 && k2 != 0 ? k2 : k1), floor = low - tol(low);
+    uint64_t bits = 0;  // the values an open group's score may consist of
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        if (open && key[j] != 0 && !(key_value(key[j]) < floor)) bits |= 1ull << j;
+    const int n = list_in_64(p, t, lane, ln, bits, s, zm);
+    uint64_t m1 = 0, m2 = 0;
+    for (int i = 0; i < n; ++i)
+        if (open && s.list[i] / p.group_size == ln.g) {
+            const uint64_t c = s.exact[i];
+            m2 = max(m2, min(m1, c));
+            m1 = max(m1, c);
+        }
+    const uint64_t exact = !open ? 0 : p.group_top2 && m2 != 0 ? order_key(key_value(m1) + key_value(m2)) : m1;
+    int rank = 0;
+    for (int g = 0; g < p.n_groups; ++g) {
+        const uint64_t o = __shfl_sync(kFull, exact, g * p.lanes);
+        rank += o > exact || (o == exact && g < ln.g);
+    }
+    const int slots = p.top_groups - __popc(__ballot_sync(kFull, sure && lane % p.lanes == 0));
+    return sure || (open && rank < slots);
+}
+
+// The k picks where the edge between the k-th and the next is too close:
+// my_id and my_key as pick() left them (the picks beyond doubt come first).
+template <int P>
+__device__ __forceinline__ int pick_close(const ScoredArgs& p, int64_t t, int lane, const Lane& ln,
+                                          const uint32_t (&key)[P], bool kept, int my_id, uint32_t my_key,
+                                          uint32_t edge_key, const Tolerance& tol, const Scratch& s, float zm) {
+    const float edge = key_value(edge_key), wide = tol(edge);
+    auto above = [&](uint32_t k) { return key_value(k) > edge && !(key_value(k) - edge <= wide); };
+    uint64_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        if (kept && key[j] != 0 && !above(key[j]) && !(edge - key_value(key[j]) > wide)) bits |= 1ull << j;
+    const int n_sure = __popc(__ballot_sync(kFull, my_id >= 0 && above(my_key)));
+    const int n = list_in_64(p, t, lane, ln, bits, s, zm);
+    uint64_t last = ~0ull;
+    int last_at = -1;
     for (int i = n_sure; i < p.k; ++i) {
-        next_in_order(s.exact, n, lane, last64, at, [](int) { return true; });
-        if (lane == i && at < n) my_id = s.list[at];
+        // what follows (last, last_at): largest first, the lowest on ties
+        uint64_t best = 0;
+        int at = 0x7fffffff;
+        for (int q = lane; q < n; q += 32) {
+            const uint64_t c = s.exact[q];
+            if (c > best && (c < last || (c == last && q > last_at))) {
+                best = c;
+                at = q;
+            }
+        }
+        last = warp_max(best);
+        last_at = (int)__reduce_min_sync(kFull, best == last ? (unsigned)at : 0x7fffffffu);
+        if (lane == i) my_id = last_at < n ? s.list[last_at] : -1;
     }
     __syncwarp();
     return my_id;
@@ -423,76 +399,81 @@ struct Pick {
     int id, slot;
     float w;
 };
-template <int P>
+template <int P, bool FULL>
 __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int lane, const Scratch& scratch) {
     const Lane ln(p, lane);
     float z[P];
-    load_logits<P>(p, t, ln, z);
+    load_logits<P, FULL>(p, t, ln, z);
     if (p.z_out) {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            if (j < ln.n) p.z_out[t * p.E + ln.first + j] = z[j];
+            if (has<P, FULL>(ln, j)) p.z_out[t * p.E + ln.first + j] = z[j];
     }
     uint32_t key[P];
     float zm, total;
     bool finite;
-    const Tolerance tol = choice_keys<P>(p, ln, z, key, zm, total, finite);
+    const Tolerance tol = choice_keys<P, FULL>(p, ln, z, key, zm, total, finite);
     if (!finite && lane == 0) atomicOr(p.err, DERR_NONFINITE_LOGIT);
     // close: a difference of infinities is NaN and never close, ties go by id
     auto close = [&](uint32_t a, uint32_t b, float times) {
-        return key_value(a) - key_value(b) <= times * tol(key_value(a));
+        return b != 0 && finite && key_value(a) - key_value(b) <= times * tol(key_value(a));
     };
     Best2<uint32_t> best;
 #pragma unroll
     for (int j = 0; j < P; ++j) best.add(key[j], j);
-    bool again = false;
+    bool kept = true;
     if (p.top_groups < p.n_groups) {
+        // the group's best two and score, by all its lanes
         uint32_t k1 = best.k1, k2 = best.k2;
-        const uint32_t score = group_score(p, ln, k1, k2);
-        const int rank = group_rank(p, ln, score);  // by every lane: it shuffles
-        const bool is_group = ln.g < p.n_groups, kept = is_group && rank < p.top_groups;
-        again = close(~warp_max(kept ? ~score : 0u), warp_max(is_group && !kept ? score : 0u), 2.0f);
+        for (int o = 1; o < p.lanes; o <<= 1) {
+            const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
+            k2 = max(min(k1, o1), max(k2, o2));
+            k1 = max(k1, o1);
+        }
+        const bool is_group = ln.g < p.n_groups;
+        uint32_t score = p.group_top2 && k2 != 0 ? order_key(key_value(k1) + key_value(k2)) : k1;
+        if (!is_group) score = 0;
+        int rank = 0;  // groups before this one: larger, or as large and lower
+        for (int g = 0; g < p.n_groups; ++g) {
+            const uint32_t other = __shfl_sync(kFull, score, g * p.lanes);
+            rank += other > score || (other == score && g < ln.g);
+        }
+        kept = is_group && rank < p.top_groups;
+        const uint32_t edge = ~warp_max(kept ? ~score : 0u), dropped = warp_max(is_group && !kept ? score : 0u);
+        if (close(edge, dropped, 2.0f))
+            kept = keep_close_group<P>(p, t, lane, ln, key, k1, k2, score, edge, tol, scratch, zm);
         if (!kept) best.k1 = best.k2 = 0;
     }
-    uint32_t last, next;
-    int my_id = pick<uint32_t, P>(p, key, best, ln, lane, last, next);
-    again = again || (next != 0 && close(last, next, 1.0f));
-    if (again && finite) {
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            if (j < ln.n) scratch.key[ln.first + j] = key[j];
-        __syncwarp();
-        my_id = choose_close(p, t, lane, scratch, tol, zm);
-    }
+    uint32_t my_key, last, next;
+    int my_id = pick<P>(p, key, best, ln, lane, my_key, last, next);
+    if (close(last, next, 1.0f))
+        my_id = pick_close<P>(p, t, lane, ln, key, kept, my_id, my_key, last, tol, scratch, zm);
 
     // weights, by lane s < k for its own pick
     const bool mine = lane < p.k && my_id >= 0;
     const float zc = mine ? logit_of(p, t, my_id) : -CUDART_INF_F;
     const bool out = !mine || (p.bias && p.bias[my_id] == -CUDART_INF_F);  // taken out: weight 0
-    float w = 0.0f;
-    if (p.renorm) {
-        // relative to the largest chosen score, so nothing underflows
-        const float top_z = warp_max(out ? -CUDART_INF_F : zc);
-        if (!out)
-            w = p.sigmoid ? expf(fminf(zc, 0.0f) - fminf(top_z, 0.0f)) / (1.0f + expf(-fabsf(zc)))
-                          : expf(zc - top_z);
-        const float sum = warp_sum(w);
-        w = sum > 0.0f ? w / sum * p.scale : 0.0f;
-    } else if (!out) {
-        const float e = expf(-fabsf(zc));
-        w = p.scale * (p.sigmoid ? (zc >= 0.0f ? 1.0f : e) / (1.0f + e) : expf(zc - zm) / total);
-    }
+    float top_z = zm, sum = total;
+    if (p.renorm) top_z = warp_max(out ? -CUDART_INF_F : zc);
+    // sigmoid: e^min(z, 0) / (1 + e^-|z|).  Renormalised, both kinds relative
+    // to the largest chosen one, so that nothing underflows.
+    const float shift = p.sigmoid ? (p.renorm ? fminf(top_z, 0.0f) : 0.0f) : top_z;
+    float w = out ? 0.0f : exp2_fast(kLog2e * ((p.sigmoid ? fminf(zc, 0.0f) : zc) - shift));
+    if (p.sigmoid) w *= rcp_fast(1.0f + exp2_fast(-kLog2e * fabsf(zc)));
+    if (p.renorm) sum = warp_sum(w);
+    if (p.renorm || !p.sigmoid) w *= sum > 0.0f ? rcp_fast(sum) : 0.0f;
+    w *= p.scale;
     // rank of my id among the chosen ids -> ascending-id slot
-    int rank = 0;
+    int slot = 0;
     for (int s = 0; s < p.k; ++s) {
         const int other = __shfl_sync(kFull, my_id, s);
-        rank += other >= 0 && other < my_id;
+        slot += other >= 0 && other < my_id;
     }
     if (mine) {
-        p.ids[t * p.k + rank] = my_id;
-        p.w[t * p.k + rank] = w;
+        p.ids[t * p.k + slot] = my_id;
+        p.w[t * p.k + slot] = w;
     }
-    return Pick{my_id, rank, w};
+    return Pick{my_id, slot, w};
 }
 
 // ------------------------------------------------------------- grouping --
@@ -617,7 +598,7 @@ __global__ void __launch_bounds__(kChunk) scored_place_kernel(const __grid_const
 // The cluster's choice for chunk `chunk`: ids and weights written, its pairs
 // counted by expert in `count` of the cluster's first block.  Dynamic shared
 // memory: Scratch of every warp.
-template <int P>
+template <int P, bool FULL>
 __device__ __forceinline__ void select_chunk(const ScoredArgs& p, int chunk, int rank, void* smem, int* count) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Scratch scratch(smem, p.E, warp);
@@ -627,7 +608,7 @@ __device__ __forceinline__ void select_chunk(const ScoredArgs& p, int chunk, int
     cluster_sync();
     const int end = min(p.T, (chunk + 1) * p.chunk_tokens);
     for (int t = chunk * p.chunk_tokens + rank * kSelectWarps + warp; t < end; t += kSelectCluster * kSelectWarps) {
-        const Pick pick = route_token<P>(p, t, lane, scratch);
+        const Pick pick = route_token<P, FULL>(p, t, lane, scratch);
         if (lane < p.k && pick.id >= 0) {
             uint32_t at;
             asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
@@ -641,27 +622,27 @@ __device__ __forceinline__ void select_chunk(const ScoredArgs& p, int chunk, int
     cluster_sync();
 }
 
-template <int P>
-__global__ void __launch_bounds__(32 * kSelectWarps) __cluster_dims__(kSelectCluster, 1, 1)
+template <int P, bool FULL>
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1) __cluster_dims__(kSelectCluster, 1, 1)
     scored_select_kernel(const __grid_constant__ ScoredArgs p) {
     extern __shared__ __align__(16) char smem[];
     __shared__ int count[DWDP_MAX_EXPERTS];
     const int chunk = blockIdx.x / kSelectCluster, rank = blockIdx.x % kSelectCluster;
-    select_chunk<P>(p, chunk, rank, smem, count);
+    select_chunk<P, FULL>(p, chunk, rank, smem, count);
     if (rank == 0)
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(int64_t)chunk * p.E + e] = count[e];
 }
 
 // One chunk: the cluster's first block also places the pairs, a round of 256
 // at a time; base[e] moves on by the round's pairs.
-template <int P>
-__global__ void __launch_bounds__(32 * kSelectWarps) __cluster_dims__(kSelectCluster, 1, 1)
+template <int P, bool FULL>
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1) __cluster_dims__(kSelectCluster, 1, 1)
     scored_one_kernel(const __grid_constant__ ScoredArgs p) {
     constexpr int kThreads = 32 * kSelectWarps, kPer = DWDP_MAX_EXPERTS / kThreads;
     extern __shared__ __align__(16) char smem[];
     __shared__ int base[DWDP_MAX_EXPERTS];
     __shared__ int tmp[32];
-    select_chunk<P>(p, 0, blockIdx.x, smem, base);
+    select_chunk<P, FULL>(p, 0, blockIdx.x, smem, base);
     if (blockIdx.x != 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* wc = reinterpret_cast<uint8_t*>(smem);  // [warps][E]; the scratch is done with
@@ -722,10 +703,10 @@ cudaError_t launch(F kernel, int grid, int threads, size_t smem, cudaStream_t s,
     return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
-template <int P>
-cudaError_t launch_per_lane(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
-    const size_t smem = (size_t)kSelectWarps * p.E * Scratch::kBytes;
-    auto kernel = n_chunks == 1 ? scored_one_kernel<P> : scored_select_kernel<P>;
+template <int P, bool FULL>
+cudaError_t launch_form(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
+    const size_t smem = Scratch::bytes(p.E, kSelectWarps);
+    auto kernel = n_chunks == 1 ? scored_one_kernel<P, FULL> : scored_select_kernel<P, FULL>;
     if (smem > 40 << 10) {  // beside the static part, beyond what a launch gets unasked
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -737,6 +718,13 @@ cudaError_t launch_per_lane(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
     e = launch_chunk_scan(p.hist, n_chunks, p.E, p.counts, p.offsets, s);
     if (e != cudaSuccess) return e;
     return launch(scored_place_kernel<true>, n_chunks, kChunk, (size_t)p.E * 36, s, p, n_chunks);
+}
+
+template <int P>
+cudaError_t launch_per_lane(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
+    if constexpr (P <= 16)
+        if (p.per_lane == P && 32 * P == p.E && p.lanes * P == p.group_size) return launch_form<P, true>(p, n_chunks, s);
+    return launch_form<P, false>(p, n_chunks, s);
 }
 
 }  // namespace
@@ -752,7 +740,6 @@ cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s) {
     while (p.lanes * 2 * p.n_groups <= 32) p.lanes *= 2;
     p.group_size = p.E / p.n_groups;
     p.per_lane = (p.group_size + p.lanes - 1) / p.lanes;
-    p.vector_loads = p.group_size % 4 == 0 && p.per_lane % 4 == 0;
     p.chunk_tokens = kChunk / p.k;
     const int n_chunks = (p.T + p.chunk_tokens - 1) / p.chunk_tokens;
     if (p.per_lane <= 1) return launch_per_lane<1>(p, n_chunks, s);

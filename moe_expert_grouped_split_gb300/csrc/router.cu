@@ -26,21 +26,25 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// MT m16 tiles of tokens x NT n8 tiles of experts.  A step is 32 elements of
-// K: thread q of a row's four takes 8 neighbours, 16 bytes, as the operands
-// of two MMAs (the order of k is free as long as both operands share it).
-template <int MT, int NT, int U>
+// MW x NW x KW warps, each MT m16 tiles of tokens x NT n8 tiles of experts x
+// its part of K.  A step is 32 elements of K: thread q of a row's four takes
+// 8 neighbours, 16 bytes, as the operands of two MMAs (the order of k is free
+// as long as both operands share it).
+template <int MW, int NW, int KW, int MT, int NT, int U>
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     router_small_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w, int T, int E, int H,
                         float* __restrict__ z) {
-    constexpr int kTile = MT * 16 * NT * 8;
-    __shared__ __align__(16) float part[kWarps][kTile];
+    static_assert(MW * NW * KW == kWarps, "");
+    constexpr int kRows = MW * MT * 16, kCols = NW * NT * 8, kTile = kRows * kCols;
+    __shared__ __align__(16) float part[KW][kTile];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int mw = warp % MW, nw = warp / MW % NW, kw = warp / (MW * NW);
     const int rank = blockIdx.x % kCluster;
-    const int t0 = (int)(blockIdx.x / kCluster) * MT * 16, e0 = (int)blockIdx.y * NT * 8;
+    const int t0 = (int)(blockIdx.x / kCluster) * kRows, e0 = (int)blockIdx.y * kCols;
+    const int tw = t0 + mw * MT * 16, ew = e0 + nw * NT * 8;  // this warp's first token and expert
     const int hv = H / 8, steps = H / 32;
-    const int at = rank * kWarps + warp;
-    const int step0 = steps * at / (kCluster * kWarps), step1 = steps * (at + 1) / (kCluster * kWarps);
+    const int at = rank * KW + kw;
+    const int step0 = steps * at / (kCluster * KW), step1 = steps * (at + 1) / (kCluster * KW);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float acc[MT][NT][4] = {};
@@ -52,12 +56,12 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
             const bool in = st + u < step1;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const int e = e0 + j * 8 + g;
+                const int e = ew + j * 8 + g;
                 wv[u][j] = in && e < E ? __ldg(w + (int64_t)e * hv + k) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
-                const int t = t0 + i * 8 + g;
+                const int t = tw + i * 8 + g;
                 xv[u][i] = in && t < T ? __ldg(x + (int64_t)t * hv + k) : make_uint4(0, 0, 0, 0);
             }
         }
@@ -78,14 +82,16 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2*>(&part[warp][(m * 16 + h * 8 + g) * NT * 8 + j * 8 + 2 * q]) =
+                *reinterpret_cast<float2*>(&part[kw][(tw - t0 + m * 16 + h * 8 + g) * kCols + ew - e0 + j * 8 + 2 * q]) =
                     make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile; i += kThreads) {
-        float s = part[0][i];
+    if constexpr (KW > 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kTile; i += kThreads) {
+            float s = part[0][i];
 #pragma unroll
-        for (int v = 1; v < kWarps; ++v) s += part[v][i];
-        part[0][i] = s;
+            for (int v = 1; v < KW; ++v) s += part[v][i];
+            part[0][i] = s;
+        }
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -100,34 +106,46 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
             s += v;
         }
-        const int t = t0 + i / (NT * 8), e = e0 + i % (NT * 8);
+        const int t = t0 + i / kCols, e = e0 + i % kCols;
         if (t < T && e < E) z[(int64_t)t * E + e] = s;
     }
+    __syncwarp();
     // nobody leaves while another rank may still read its shared memory
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int MT, int NT, int U>
+template <int MW, int NW, int KW, int MT, int NT, int U>
 cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
+    constexpr int kRows = MW * MT * 16, kCols = NW * NT * 8;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((T + MT * 16 - 1) / (MT * 16) * kCluster, (E + NT * 8 - 1) / (NT * 8));
+    c.gridDim = dim3((T + kRows - 1) / kRows * kCluster, (E + kCols - 1) / kCols);
     c.blockDim = dim3(kThreads);
     c.stream = s;
     c.attrs = &at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, router_small_kernel<MT, NT, U>, static_cast<const uint4*>(x),
+    return cudaLaunchKernelEx(&c, router_small_kernel<MW, NW, KW, MT, NT, U>, static_cast<const uint4*>(x),
                               static_cast<const uint4*>(w), T, E, H, z);
 }
 
 }  // namespace
 
-cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
-    if (T <= 16) return launch<1, 2, 4>(x, w, T, E, H, z, s);
-    return launch<2, 4, 2>(x, w, T, E, H, z, s);
+cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, int variant, cudaStream_t s) {
+    switch (variant) {
+        case 0: return launch<1, 1, 8, 1, 2, 4>(x, w, T, E, H, z, s);
+        case 1: return launch<1, 1, 8, 2, 4, 2>(x, w, T, E, H, z, s);
+        case 2: return launch<2, 2, 2, 2, 4, 2>(x, w, T, E, H, z, s);
+        case 3: return launch<2, 2, 2, 2, 4, 1>(x, w, T, E, H, z, s);
+        case 4: return launch<2, 2, 2, 1, 4, 4>(x, w, T, E, H, z, s);
+        case 5: return launch<2, 4, 1, 2, 4, 2>(x, w, T, E, H, z, s);
+        case 6: return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, s);
+        case 7: return launch<2, 4, 1, 2, 4, 1>(x, w, T, E, H, z, s);
+        case 8: return launch<1, 2, 4, 1, 2, 4>(x, w, T, E, H, z, s);
+        default: return launch<1, 2, 4, 1, 4, 4>(x, w, T, E, H, z, s);
+    }
 }
 
 }  // namespace dwdp
