@@ -93,6 +93,18 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, in
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows_box(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rows == 0) return false;
+    cuuint64_t dims[2] = {K, rows};
+    cuuint64_t strides[1] = {2 * K};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A weight buffer [slots][rows][K]: a 3-D map, box [1 x 128 rows x BK_BYTES];
 // slots are weight_slot_bytes apart (NVFP4: the codes of each slot, whose
 // block scales follow them).
@@ -202,8 +214,9 @@ WsLayout ws_layout(const dwdp_config& c, int64_t T) {
     WsLayout L;
     const int64_t H = c.hidden, I = c.inter, E = c.n_experts, k = c.top_k, S = c.n_shared;
     const int fmt = c.weight_dtype;
-    L.logits = 0;  // up to kRouterMaxSplit partial-sum planes of the router GEMM
-    L.group = align_up((size_t)(kRouterMaxSplit * T * E * 4), 256);
+    L.logits = 0;  // the partial-sum planes of the router GEMM
+    const int64_t planes = std::max(kRouterMaxSplit, router_pair_parts(T, E, H));
+    L.group = align_up((size_t)(planes * T * E * 4), 256);
     L.route_bytes = L.group + align_up(std::max(group_chunked_scratch_bytes((int)(T * k), (int)E),
                                                 scored_scratch_bytes(T, E, k)), 256);
     size_t o = 0;
@@ -849,14 +862,27 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     if (rc != DWDP_OK || empty) return rc;
     DWDP_CUDA(ctx, mark(ctx, 0, stream));
     ScoredArgs p{};
+    float* planes = reinterpret_cast<float*>(static_cast<char*>(ws) + ws_layout(c, T).logits);
     float* logits = nullptr;
-    if (T <= kRouterSmallTokens) {
+    if (router_is_small(T, c.n_experts)) {
         p.parts = 1;
-        logits = out->logits ? out->logits : reinterpret_cast<float*>(static_cast<char*>(ws) + ws_layout(c, T).logits);
+        logits = out->logits ? out->logits : planes;
         DWDP_CUDA(ctx, launch_router_small(x, w_router, T, c.n_experts, c.hidden, logits, stream));
     } else {
-        const int32_t rg = router_gemm(ctx, x, T, w_router, nullptr, out->logits, ws, stream, p.parts, logits);
-        if (rg != DWDP_OK) return rg;
+        RouterPairArgs r;
+        p.parts = router_pair_parts(T, c.n_experts, c.hidden);
+        logits = out->logits && p.parts == 1 ? out->logits : planes;
+        if (!encode_rows_box(&r.tm_x, x, T, c.hidden, 128) ||
+            !encode_rows_box(&r.tm_w, w_router, c.n_experts, c.hidden, router_pair_cols(c.n_experts) / 2))
+            return fail(ctx, DWDP_ERR_CUDA, "tensor map for the router GEMM");
+        r.z = logits;
+        r.part_stride = (int64_t)T * c.n_experts;
+        r.T = T;
+        r.E = c.n_experts;
+        r.H = c.hidden;
+        r.parts = p.parts;
+        r.err = ctx->d_err;
+        DWDP_CUDA(ctx, launch_router_pair(r, stream));
     }
     p.logits = logits;
     p.part_stride = (int64_t)T * c.n_experts;

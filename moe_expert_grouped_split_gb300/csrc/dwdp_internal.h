@@ -126,6 +126,8 @@ struct GemmArgs {
 // swizzled to BK_BYTES.  K counts elements of format fmt (bf16, E4M3 codes or
 // NVFP4 codes, two per byte); a weight slot is weight_slot_bytes apart.
 bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, int fmt = FMT_BF16);
+// The same bf16 matrix with boxes of box_rows rows.
+bool encode_rows_box(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, uint32_t box_rows);
 bool encode_slots(CUtensorMap* m, const void* base, uint64_t slots, uint64_t rows, uint64_t K,
                   int fmt = FMT_BF16);
 
@@ -217,9 +219,25 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* resi
                                const void* weight, float eps, int64_t rows, int H, void* out, void* codes,
                                float* row_scale, cudaStream_t s);
 
-// router.cu: z [T][E] = x [T][H] W [E][H]^T in fp32 for T <= kRouterSmallTokens.
-constexpr int kRouterSmallTokens = 256;
+// router.cu: z [T][E] = x [T][H] W [E][H]^T in fp32 on warp-level MMAs, for
+// router_is_small sizes.
+bool router_is_small(int64_t T, int64_t E);
 cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s);
+
+// router_pair.cu: the same for many tokens on tcgen05, as `parts` planes
+// part_stride apart whose sum is z.  tm_x: boxes of 128 rows x 64 elements;
+// tm_w: of router_pair_cols(E) / 2 rows x 64 elements.
+constexpr int kRouterPairMaxParts = 8;
+struct RouterPairArgs {
+    CUtensorMap tm_x, tm_w;
+    float* z;
+    int64_t part_stride;
+    int T, E, H, parts;
+    int* err;
+};
+int router_pair_cols(int E);
+int router_pair_parts(int64_t T, int64_t E, int64_t H);
+cudaError_t launch_router_pair(const RouterPairArgs& p, cudaStream_t s);
 
 // route_scored.cu: dwdp_route_scored from the logits on.  logits: `parts` fp32
 // planes [T][E] part_stride apart, summed in plane order; z_out, if not null,

@@ -2,10 +2,10 @@
 // z [T][E] = x W^T, fp32.
 //
 // Few tokens read W once and little else, so what counts is that the whole
-// GPU loads at once and how few round trips a launch needs: a tile of 16 or
-// 32 tokens x 16 or 32 experts is a cluster of 8 CTAs of 8 warps, 64 parts of
-// K, all of a part's loads issued before its first product; the parts meet in
-// shared memory, then across the cluster, in order.
+// GPU loads at once and how few round trips a launch needs: a tile of 16 to
+// 64 tokens x 16 to 64 experts is a cluster of 8 CTAs of 8 warps that share
+// K, operands straight from global memory, several steps' loads in flight;
+// the parts meet in shared memory, then across the cluster, in order.
 #include <cuda_bf16.h>
 
 #include "dwdp_internal.h"
@@ -133,19 +133,19 @@ cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, 
 
 }  // namespace
 
-cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, int variant, cudaStream_t s) {
-    switch (variant) {
-        case 0: return launch<1, 1, 8, 1, 2, 4>(x, w, T, E, H, z, s);
-        case 1: return launch<1, 1, 8, 2, 4, 2>(x, w, T, E, H, z, s);
-        case 2: return launch<2, 2, 2, 2, 4, 2>(x, w, T, E, H, z, s);
-        case 3: return launch<2, 2, 2, 2, 4, 1>(x, w, T, E, H, z, s);
-        case 4: return launch<2, 2, 2, 1, 4, 4>(x, w, T, E, H, z, s);
-        case 5: return launch<2, 4, 1, 2, 4, 2>(x, w, T, E, H, z, s);
-        case 6: return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, s);
-        case 7: return launch<2, 4, 1, 2, 4, 1>(x, w, T, E, H, z, s);
-        case 8: return launch<1, 2, 4, 1, 2, 4>(x, w, T, E, H, z, s);
-        default: return launch<1, 2, 4, 1, 4, 4>(x, w, T, E, H, z, s);
-    }
+// Where the tensor-core pairs (router_pair.cu) take over.
+bool router_is_small(int64_t T, int64_t E) { return T * E <= 128 << 10; }
+
+// The tile by the size of z: small tiles spread W over all SMs, larger ones
+// read x and W fewer times.  7168 x 256, us at 1 / 64 / 128 / 256 / 512
+// tokens: 16 x 16 3.1 / 5.2 / 9.5 / 18 / 34, 32 x 32 4.3 / 6.2 / 6.5 / 12 / 24,
+// 32 x 64 5.9 / 7.1 / 8.7 / 9.2 / 18, 64 x 64 8.5 / 11 / 11 / 13 / 14.
+cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
+    const int64_t n = (int64_t)T * E;
+    if (n <= 16 << 10) return launch<1, 1, 8, 1, 2, 4>(x, w, T, E, H, z, s);
+    if (n <= 32 << 10) return launch<1, 1, 8, 2, 4, 2>(x, w, T, E, H, z, s);
+    if (n <= 64 << 10) return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, s);
+    return launch<2, 2, 2, 2, 4, 2>(x, w, T, E, H, z, s);
 }
 
 }  // namespace dwdp

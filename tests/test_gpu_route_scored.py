@@ -132,6 +132,11 @@ CASES = [
     (31, 7168, 24, 3, how_of(SIG), False),
     (700, 7168, 512, 8, how_of(SIG, 8, 4, B.GROUP_TOP2), True),
     (33, 64, 7, 3, how_of(SOFT, 7, 3, B.GROUP_MAX), False),
+    (1100, 7168, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (3001, 576, 72, 6, how_of(SOFT, 8, 3, B.GROUP_MAX), True),
+    (1030, 192, 300, 7, how_of(SIG, 3, 2, B.GROUP_TOP2), True),
+    (2305, 128, 64, 6, how_of(SOFT, renorm=False), False),
+    (9000, 64, 16, 2, how_of(SOFT, 4, 2, B.GROUP_TOP2), False),
 ]
 
 
