@@ -218,7 +218,7 @@ WsLayout ws_layout(const dwdp_config& c, int64_t T) {
     const int64_t planes = std::max(kRouterMaxSplit, router_pair_parts(T, E, H));
     L.group = align_up((size_t)(planes * T * E * 4), 256);
     L.route_bytes = L.group + align_up(std::max(group_chunked_scratch_bytes((int)(T * k), (int)E),
-                                                scored_scratch_bytes(T, E, k)), 256);
+                                                (size_t)scored_chunks(T, k) * E * 4), 256);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -862,12 +862,16 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     if (rc != DWDP_OK || empty) return rc;
     DWDP_CUDA(ctx, mark(ctx, 0, stream));
     ScoredArgs p{};
-    float* planes = reinterpret_cast<float*>(static_cast<char*>(ws) + ws_layout(c, T).logits);
+    const WsLayout L = ws_layout(c, T);
+    float* planes = reinterpret_cast<float*>(static_cast<char*>(ws) + L.logits);
     float* logits = nullptr;
+    p.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.group);
+    const int chunks = scored_chunks(T, c.top_k);
+    const int64_t n_zero = chunks > 1 ? (int64_t)chunks * c.n_experts : 0;
     if (router_is_small(T, c.n_experts)) {
         p.parts = 1;
         logits = out->logits ? out->logits : planes;
-        DWDP_CUDA(ctx, launch_router_small(x, w_router, T, c.n_experts, c.hidden, logits, stream));
+        DWDP_CUDA(ctx, launch_router_small(x, w_router, T, c.n_experts, c.hidden, logits, p.hist, n_zero, stream));
     } else {
         RouterPairArgs r;
         p.parts = router_pair_parts(T, c.n_experts, c.hidden);
@@ -881,6 +885,8 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
         r.E = c.n_experts;
         r.H = c.hidden;
         r.parts = p.parts;
+        r.zero = p.hist;
+        r.n_zero = n_zero;
         r.err = ctx->d_err;
         DWDP_CUDA(ctx, launch_router_pair(r, stream));
     }
@@ -904,7 +910,6 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     p.offsets = out->offsets;
     p.perm = out->perm;
     p.inv_perm = out->inv_perm;
-    p.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + ws_layout(c, T).group);
     DWDP_CUDA(ctx, launch_scored_choice(p, stream));
     DWDP_CUDA(ctx, mark(ctx, 1, stream));
     return DWDP_OK;

@@ -220,9 +220,11 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* resi
                                float* row_scale, cudaStream_t s);
 
 // router.cu: z [T][E] = x [T][H] W [E][H]^T in fp32 on warp-level MMAs, for
-// router_is_small sizes.
+// router_is_small sizes.  The kernel also zeroes n_zero ints at `zero` (so
+// does router_pair.cu's), for whoever counts after it.
 bool router_is_small(int64_t T, int64_t E);
-cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s);
+cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, int32_t* zero,
+                                int64_t n_zero, cudaStream_t s);
 
 // router_pair.cu: the same for many tokens on tcgen05, as `parts` planes
 // part_stride apart whose sum is z.  tm_x: boxes of 128 rows x 64 elements;
@@ -233,6 +235,8 @@ struct RouterPairArgs {
     float* z;
     int64_t part_stride;
     int T, E, H, parts;
+    int32_t* zero;
+    int64_t n_zero;
     int* err;
 };
 int router_pair_cols(int E);
@@ -241,8 +245,9 @@ cudaError_t launch_router_pair(const RouterPairArgs& p, cudaStream_t s);
 
 // route_scored.cu: dwdp_route_scored from the logits on.  logits: `parts` fp32
 // planes [T][E] part_stride apart, summed in plane order; z_out, if not null,
-// receives the sums; hist: scored_scratch_bytes(T, E, k) of scratch.  The
-// members after `scale` are filled by launch_scored_choice.
+// receives the sums; hist: scored_chunks(T, k) x E counts, zero (unless there
+// is one chunk, which needs none).  The members after `scale` are filled by
+// launch_scored_choice.
 struct ScoredArgs {
     const float* logits;
     int64_t part_stride;
@@ -262,7 +267,7 @@ struct ScoredArgs {
     float scale;
     int lanes, group_size, per_lane, chunk_tokens;
 };
-size_t scored_scratch_bytes(int64_t T, int64_t E, int64_t k);
+int scored_chunks(int64_t T, int64_t k);
 cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s);
 // route.cu's chunk_scan_kernel on its own: hist [n_chunks][E] counts to each
 // chunk's first rows, counts [E] and offsets [E + 1].

@@ -80,7 +80,7 @@ struct Lane {
         g = lane / p.lanes;
         const int at = (lane % p.lanes) * p.per_lane;
         n = g < p.n_groups ? max(0, min(p.per_lane, p.group_size - at)) : 0;
-        first = g * p.group_size + at;
+        first = g * p.group_size + at;  // (beyond the experts where there are none)
     }
 };
 
@@ -136,21 +136,19 @@ __device__ __forceinline__ float logit_of(const ScoredArgs& p, int64_t t, int e)
     return v;
 }
 
-// A lane's two best keys with their places in its run (the lowest on ties).
-template <class K>
-struct Best2 {
-    K k1 = 0, k2 = 0;
-    int i1 = 0, i2 = 0;
-    __device__ __forceinline__ void add(K c, int j) {
-        if (c > k1) {
-            k2 = k1;
-            i2 = i1;
-            k1 = c;
-            i1 = j;
-        } else if (c > k2) {
-            k2 = c;
-            i2 = j;
-        }
+// A lane's three best keys with their places in its run (the lowest on
+// ties), without a branch.
+struct Best3 {
+    uint32_t k1 = 0, k2 = 0, k3 = 0;
+    int i1 = 0, i2 = 0, i3 = 0;
+    __device__ __forceinline__ void add(uint32_t c, int j) {
+        const bool g1 = c > k1, g2 = c > k2, g3 = c > k3;
+        k3 = g2 ? k2 : g3 ? c : k3;
+        i3 = g2 ? i2 : g3 ? j : i3;
+        k2 = g1 ? k1 : g2 ? c : k2;
+        i2 = g1 ? i1 : g2 ? j : i2;
+        k1 = g1 ? c : k1;
+        i1 = g1 ? j : i1;
     }
 };
 
@@ -220,46 +218,36 @@ __device__ __forceinline__ Tolerance choice_keys(const ScoredArgs& p, const Lane
 
 // The k best of the lanes' keys.  Lane s < k gets the s-th pick's id; last is
 // the k-th pick's key, next the best left (0: none); a pick's own key goes to
-// its lane.  A lane offers its best key; after a pick it falls back on its
-// second, and looks through its run again only when that is gone too.  Lane
-// order is expert order, so the lowest lane offering the largest key holds
-// the lowest id.
+// its lane.  A lane offers its best key, and after a pick the next of its
+// three; a lane picked three times (one token in five has one, at 8 of 16
+// lanes' 128) looks through its run again.  Lane order is expert order, so
+// the lowest lane offering the largest key holds the lowest id.
 template <int P>
-__device__ __forceinline__ int pick(const ScoredArgs& p, const uint32_t (&key)[P], const Best2<uint32_t>& best,
-                                    const Lane& ln, int lane, uint32_t& my_key, uint32_t& last, uint32_t& next) {
-    uint32_t offer = best.k1, second = best.k2;
-    int at = best.i1, at2 = best.i2, my_id = -1;
+__device__ __forceinline__ int pick(const ScoredArgs& p, const uint32_t (&key)[P], Best3 best, const Lane& ln,
+                                    int lane, uint32_t& my_key, uint32_t& last, uint32_t& next) {
+    int my_id = -1;
     last = my_key = 0;
 #pragma unroll 1
     for (int s = 0; s < p.k; ++s) {
-        const uint32_t gk = warp_max(offer);
-        if (gk == 0) break;  // fewer than k candidates (refused on the host)
-        last = gk;
-        const int owner = __ffs(__ballot_sync(kFull, offer == gk)) - 1;
-        const int id = __shfl_sync(kFull, ln.first + at, owner);
-        if (lane == s) {
-            my_id = id;
-            my_key = gk;
-        }
-        if (lane == owner) {
-            if (second != 0) {
-                offer = second;
-                at = at2;
-                second = 0;
-            } else {  // the best of what comes after (offer, at) in order
-                Best2<uint32_t> rest;
+        const uint32_t gk = last = warp_max(best.k1);  // never 0: the host refuses fewer than k candidates
+        const int owner = __ffs(__ballot_sync(kFull, best.k1 == gk)) - 1;
+        const int id = __shfl_sync(kFull, ln.first + best.i1, owner);
+        my_id = lane == s ? id : my_id;
+        my_key = lane == s ? gk : my_key;
+        const bool own = lane == owner;
+        const int at = best.i1;
+        best.k1 = own ? best.k2 : best.k1;
+        best.i1 = own ? best.i2 : best.i1;
+        best.k2 = own ? best.k3 : best.k2;
+        best.i2 = own ? best.i3 : best.i2;
+        best.k3 = own ? 0u : best.k3;
+        if (P > 3 && own && best.k1 == 0) {  // what comes after (gk, at) in order
 #pragma unroll
-                for (int j = 0; j < P; ++j)
-                    if (key[j] < offer || (key[j] == offer && j > at)) rest.add(key[j], j);
-                offer = rest.k1;
-                at = rest.i1;
-                second = rest.k2;
-                at2 = rest.i2;
-            }
+            for (int j = 0; j < P; ++j) best.add(key[j] < gk || (key[j] == gk && j > at) ? key[j] : 0u, j);
         }
         __syncwarp();
     }
-    next = warp_max(offer);
+    next = warp_max(best.k1);
     return my_id;
 }
 
@@ -418,7 +406,7 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
     auto close = [&](uint32_t a, uint32_t b, float times) {
         return b != 0 && finite && key_value(a) - key_value(b) <= times * tol(key_value(a));
     };
-    Best2<uint32_t> best;
+    Best3 best;
 #pragma unroll
     for (int j = 0; j < P; ++j) best.add(key[j], j);
     bool kept = true;
@@ -434,15 +422,19 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
         uint32_t score = p.group_top2 && k2 != 0 ? order_key(key_value(k1) + key_value(k2)) : k1;
         if (!is_group) score = 0;
         int rank = 0;  // groups before this one: larger, or as large and lower
-        for (int g = 0; g < p.n_groups; ++g) {
-            const uint32_t other = __shfl_sync(kFull, score, g * p.lanes);
-            rank += other > score || (other == score && g < ln.g);
+        for (int g0 = 0; g0 < p.n_groups; g0 += 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // (0 beyond the last group)
+                const int g = g0 + i;
+                const uint32_t other = g * p.lanes < 32 ? __shfl_sync(kFull, score, g * p.lanes) : 0u;
+                rank += other > score || (other == score && g < ln.g);
+            }
         }
         kept = is_group && rank < p.top_groups;
         const uint32_t edge = ~warp_max(kept ? ~score : 0u), dropped = warp_max(is_group && !kept ? score : 0u);
         if (close(edge, dropped, 2.0f))
             kept = keep_close_group<P>(p, t, lane, ln, key, k1, k2, score, edge, tol, scratch, zm);
-        if (!kept) best.k1 = best.k2 = 0;
+        if (!kept) best.k1 = best.k2 = best.k3 = 0;
     }
     uint32_t my_key, last, next;
     int my_id = pick<P>(p, key, best, ln, lane, my_key, last, next);
@@ -465,9 +457,10 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
     w *= p.scale;
     // rank of my id among the chosen ids -> ascending-id slot
     int slot = 0;
-    for (int s = 0; s < p.k; ++s) {
-        const int other = __shfl_sync(kFull, my_id, s);
-        slot += other >= 0 && other < my_id;
+    const unsigned order = mine ? (unsigned)my_id : 0xffffffffu;
+    for (int s0 = 0; s0 < p.k; s0 += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) slot += __shfl_sync(kFull, order, s0 + i) < order;
     }
     if (mine) {
         p.ids[t * p.k + slot] = my_id;
@@ -478,15 +471,16 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
 
 // ------------------------------------------------------------- grouping --
 // The pairs are taken in chunks of whole tokens, at most kChunk pairs each:
-//   select   a cluster of 8 blocks per chunk chooses, and counts its pairs
-//            by expert in its first block's shared memory: hist[chunk][e]
+//   select   a warp per token chooses, and counts its pairs by chunk and
+//            expert: hist[chunk][e], zeroed by the router GEMM's kernel
 //   place    a block per chunk adds up the counts of all chunks (its base is
 //            what lies before it), and ranks its own pairs
-// or, with one chunk, the cluster's first block does both.  Each pair's row is the stable one
-// (ascending flat index within an expert).
+// or, with one chunk, a cluster of 8 blocks chooses, counting in its first
+// block's shared memory, and that block places.  Each pair's row is the
+// stable one (ascending flat index within an expert).
 constexpr int kChunk = 1024;
-constexpr int kSelectCluster = 8;
 constexpr int kSelectWarps = 8;
+constexpr int kOneCluster = 8;  // blocks of the one-chunk kernel
 // Above this many chunks the sums over all of them, in every chunk's block,
 // cost more than a scan kernel between the two.
 constexpr int kSelfScanChunks = 128;
@@ -535,6 +529,7 @@ __device__ __forceinline__ void place_pairs(const ScoredArgs& p, int first, int 
     __syncthreads();
     if (valid) {
         int r = base[e] + in_warp;
+#pragma unroll 8
         for (int w = 0; w < warp; ++w) r += wc[w * p.E + e];
         p.perm[r] = first + threadIdx.x;
         p.inv_perm[first + threadIdx.x] = r;
@@ -566,7 +561,7 @@ __global__ void __launch_bounds__(kChunk) scored_place_kernel(const __grid_const
         const int parts = kChunk / ep, x = tid % ep, q = tid / ep;
         int all = 0, before = 0;
         if (x < p.E)
-#pragma unroll 4
+#pragma unroll 16
             for (int c = q; c < n_chunks; c += parts) {
                 const int h = p.hist[(int64_t)c * p.E + x];
                 all += h;
@@ -595,56 +590,47 @@ __global__ void __launch_bounds__(kChunk) scored_place_kernel(const __grid_const
     place_pairs(p, first, n, e, base, wc);
 }
 
-// The cluster's choice for chunk `chunk`: ids and weights written, its pairs
-// counted by expert in `count` of the cluster's first block.  Dynamic shared
-// memory: Scratch of every warp.
 template <int P, bool FULL>
-__device__ __forceinline__ void select_chunk(const ScoredArgs& p, int chunk, int rank, void* smem, int* count) {
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1)
+    scored_select_kernel(const __grid_constant__ ScoredArgs p) {
+    extern __shared__ __align__(16) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Scratch scratch(smem, p.E, warp);
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) count[e] = 0;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int t = blockIdx.x * kSelectWarps + warp;
+    if (t >= p.T) return;
+    const Pick pick = route_token<P, FULL>(p, t, lane, Scratch(smem, p.E, warp));
+    if (lane < p.k && pick.id >= 0) atomicAdd(p.hist + (int64_t)(t / p.chunk_tokens) * p.E + pick.id, 1);
+}
+
+// One chunk: the cluster's first block also places the pairs, a round of 256
+// at a time; base[e] moves on by the round's pairs.
+template <int P, bool FULL>
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1) __cluster_dims__(kOneCluster, 1, 1)
+    scored_one_kernel(const __grid_constant__ ScoredArgs p) {
+    constexpr int kThreads = 32 * kSelectWarps, kPer = DWDP_MAX_EXPERTS / kThreads;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ int base[DWDP_MAX_EXPERTS];
+    __shared__ int tmp[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int e = tid; e < p.E; e += kThreads) base[e] = 0;
     wait_for_previous_kernel();
     let_next_kernel_start();
     cluster_sync();
-    const int end = min(p.T, (chunk + 1) * p.chunk_tokens);
-    for (int t = chunk * p.chunk_tokens + rank * kSelectWarps + warp; t < end; t += kSelectCluster * kSelectWarps) {
-        const Pick pick = route_token<P, FULL>(p, t, lane, scratch);
+    for (int t = blockIdx.x * kSelectWarps + warp; t < p.T; t += kOneCluster * kSelectWarps) {
+        const Pick pick = route_token<P, FULL>(p, t, lane, Scratch(smem, p.E, warp));
         if (lane < p.k && pick.id >= 0) {
             uint32_t at;
             asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
                          : "=r"(at)
-                         : "r"((uint32_t)__cvta_generic_to_shared(count + pick.id)));
+                         : "r"((uint32_t)__cvta_generic_to_shared(base + pick.id)));
             asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], 1;" ::"r"(at) : "memory");
         }
         __syncwarp();
     }
     __syncwarp();
     cluster_sync();
-}
-
-template <int P, bool FULL>
-__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1) __cluster_dims__(kSelectCluster, 1, 1)
-    scored_select_kernel(const __grid_constant__ ScoredArgs p) {
-    extern __shared__ __align__(16) char smem[];
-    __shared__ int count[DWDP_MAX_EXPERTS];
-    const int chunk = blockIdx.x / kSelectCluster, rank = blockIdx.x % kSelectCluster;
-    select_chunk<P, FULL>(p, chunk, rank, smem, count);
-    if (rank == 0)
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(int64_t)chunk * p.E + e] = count[e];
-}
-
-// One chunk: the cluster's first block also places the pairs, a round of 256
-// at a time; base[e] moves on by the round's pairs.
-template <int P, bool FULL>
-__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1) __cluster_dims__(kSelectCluster, 1, 1)
-    scored_one_kernel(const __grid_constant__ ScoredArgs p) {
-    constexpr int kThreads = 32 * kSelectWarps, kPer = DWDP_MAX_EXPERTS / kThreads;
-    extern __shared__ __align__(16) char smem[];
-    __shared__ int base[DWDP_MAX_EXPERTS];
-    __shared__ int tmp[32];
-    select_chunk<P, FULL>(p, 0, blockIdx.x, smem, base);
     if (blockIdx.x != 0) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* wc = reinterpret_cast<uint8_t*>(smem);  // [warps][E]; the scratch is done with
     int mine[kPer], sum = 0;                         // experts kPer tid ...
 #pragma unroll
@@ -707,11 +693,12 @@ template <int P, bool FULL>
 cudaError_t launch_form(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
     const size_t smem = Scratch::bytes(p.E, kSelectWarps);
     auto kernel = n_chunks == 1 ? scored_one_kernel<P, FULL> : scored_select_kernel<P, FULL>;
+    const int grid = n_chunks == 1 ? kOneCluster : (p.T + kSelectWarps - 1) / kSelectWarps;
     if (smem > 40 << 10) {  // beside the static part, beyond what a launch gets unasked
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch(kernel, n_chunks * kSelectCluster, 32 * kSelectWarps, smem, s, p);
+    cudaError_t e = launch(kernel, grid, 32 * kSelectWarps, smem, s, p);
     if (e != cudaSuccess || n_chunks == 1) return e;
     if (n_chunks <= kSelfScanChunks)
         return launch(scored_place_kernel<false>, n_chunks, kChunk, (size_t)p.E * 36, s, p, n_chunks);
@@ -729,9 +716,9 @@ cudaError_t launch_per_lane(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
 
 }  // namespace
 
-size_t scored_scratch_bytes(int64_t T, int64_t E, int64_t k) {
+int scored_chunks(int64_t T, int64_t k) {
     const int64_t tokens = kChunk / k;
-    return (size_t)((T + tokens - 1) / tokens * E * 4);
+    return (int)((T + tokens - 1) / tokens);
 }
 
 cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s) {
@@ -741,7 +728,7 @@ cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s) {
     p.group_size = p.E / p.n_groups;
     p.per_lane = (p.group_size + p.lanes - 1) / p.lanes;
     p.chunk_tokens = kChunk / p.k;
-    const int n_chunks = (p.T + p.chunk_tokens - 1) / p.chunk_tokens;
+    const int n_chunks = scored_chunks(p.T, p.k);
     if (p.per_lane <= 1) return launch_per_lane<1>(p, n_chunks, s);
     if (p.per_lane <= 2) return launch_per_lane<2>(p, n_chunks, s);
     if (p.per_lane <= 4) return launch_per_lane<4>(p, n_chunks, s);

@@ -33,7 +33,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 template <int MW, int NW, int KW, int MT, int NT, int U>
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     router_small_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w, int T, int E, int H,
-                        float* __restrict__ z) {
+                        float* __restrict__ z, int32_t* __restrict__ zero, int64_t n_zero) {
     static_assert(MW * NW * KW == kWarps, "");
     constexpr int kRows = MW * MT * 16, kCols = NW * NT * 8, kTile = kRows * kCols;
     __shared__ __align__(16) float part[KW][kTile];
@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     const int step0 = steps * at / (kCluster * KW), step1 = steps * (at + 1) / (kCluster * KW);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t blocks = (int64_t)gridDim.x * gridDim.y, block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    for (int64_t i = block * kThreads + threadIdx.x; i < n_zero; i += blocks * kThreads) zero[i] = 0;
     float acc[MT][NT][4] = {};
     for (int st = step0; st < step1; st += U) {
         uint4 xv[U][2 * MT], wv[U][NT];
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
 }
 
 template <int MW, int NW, int KW, int MT, int NT, int U>
-cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
+cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, int32_t* zero, int64_t n_zero,
+                   cudaStream_t s) {
     constexpr int kRows = MW * MT * 16, kCols = NW * NT * 8;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -128,7 +131,7 @@ cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, 
     c.attrs = &at;
     c.numAttrs = 1;
     return cudaLaunchKernelEx(&c, router_small_kernel<MW, NW, KW, MT, NT, U>, static_cast<const uint4*>(x),
-                              static_cast<const uint4*>(w), T, E, H, z);
+                              static_cast<const uint4*>(w), T, E, H, z, zero, n_zero);
 }
 
 }  // namespace
@@ -140,12 +143,13 @@ bool router_is_small(int64_t T, int64_t E) { return T * E <= 128 << 10; }
 // read x and W fewer times.  7168 x 256, us at 1 / 64 / 128 / 256 / 512
 // tokens: 16 x 16 3.1 / 5.2 / 9.5 / 18 / 34, 32 x 32 4.3 / 6.2 / 6.5 / 12 / 24,
 // 32 x 64 5.9 / 7.1 / 8.7 / 9.2 / 18, 64 x 64 8.5 / 11 / 11 / 13 / 14.
-cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, cudaStream_t s) {
+cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, int32_t* zero,
+                                int64_t n_zero, cudaStream_t s) {
     const int64_t n = (int64_t)T * E;
-    if (n <= 16 << 10) return launch<1, 1, 8, 1, 2, 4>(x, w, T, E, H, z, s);
-    if (n <= 32 << 10) return launch<1, 1, 8, 2, 4, 2>(x, w, T, E, H, z, s);
-    if (n <= 64 << 10) return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, s);
-    return launch<2, 2, 2, 2, 4, 2>(x, w, T, E, H, z, s);
+    if (n <= 16 << 10) return launch<1, 1, 8, 1, 2, 4>(x, w, T, E, H, z, zero, n_zero, s);
+    if (n <= 32 << 10) return launch<1, 1, 8, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
+    if (n <= 64 << 10) return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
+    return launch<2, 2, 2, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
 }
 
 }  // namespace dwdp

@@ -119,6 +119,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = *tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp >= 2) {  // the epilogue's warps have nothing else to do yet
+        const int64_t blocks = (int64_t)gridDim.x * gridDim.y, block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        for (int64_t i = block * 128 + threadIdx.x - 64; i < p.n_zero; i += blocks * 128) p.zero[i] = 0;
+    }
 
     if (warp == 0) {
         if (lane == 0) {
