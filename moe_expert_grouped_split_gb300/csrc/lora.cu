@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dwdp_internal.h"
 
@@ -42,22 +43,20 @@ __device__ __forceinline__ void let_next_kernel_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// A float of another CTA of the cluster, at this CTA's address `p`.
-__device__ __forceinline__ float load_of_rank(const float* p, uint32_t rank) {
+// Stores v at this CTA's address `p` in another CTA of the cluster.
+__device__ __forceinline__ void store_to_rank(float* p, uint32_t rank, float v) {
     uint32_t at;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
 // A token's adapter as the kernels use it; what is not one is kNone.
@@ -68,40 +67,50 @@ __device__ __forceinline__ uint32_t adapter_of(const LoraArgs& p, int t, bool in
 }
 
 // x rows of one warp against A_i: TW x KW warps, MT m16 tiles a warp; NT
-// n8 tiles hold the rank.  G adapters share a pass over the warp's x.
+// n8 tiles hold the rank.  A step is 32 elements of K.
 template <int NT, int TW, int KW, int MT>
 struct Shrink {
     static constexpr int kRows = TW * MT * 16;
-    static constexpr int kSmem = KW * kRows * NT * 8 * 4;
+    static constexpr int kTile = kRows * NT * 8;
+    static constexpr int kSmem = (KW + 1) * kTile * 4;
 
+    // G adapters against the warp's rows, one reading of x, U steps' loads in
+    // flight.  Loads are in bounds without a predicate: a row without an
+    // adapter (or beyond the batch) reads some row of x, an adapter that is
+    // none adapter 0, a row of A beyond R the last one, and nothing of them
+    // is used.
     template <int G, int U>
     static __device__ __forceinline__ void pass(const LoraArgs& p, const uint4* const (&xr)[2 * MT],
                                                 const uint32_t (&cur)[G], int step0, int step1, int lane,
                                                 const uint32_t (&id)[2 * MT], float* part) {
         const int g = lane >> 2, q = lane & 3, kv = p.K / 8;
         float acc[G][MT][NT][4] = {};
-        const uint4* ar[G];
+        const uint4* xp[2 * MT];
+        const uint4* ap[G][NT];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) xp[i] = xr[i] + step0 * 4 + q;
 #pragma unroll
         for (int s = 0; s < G; ++s)
-            ar[s] = static_cast<const uint4*>(p.a) + (int64_t)(cur[s] == kNone ? 0 : cur[s]) * p.R * kv + (int64_t)g * kv;
-        for (int st = step0; st < step1; st += U) {
-            uint4 xv[U][2 * MT], av[U][G][NT];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = (st + u) * 4 + q;
-                const bool in = st + u < step1 && k < kv;
+            for (int j = 0; j < NT; ++j)
+                ap[s][j] = static_cast<const uint4*>(p.a) +
+                           ((int64_t)(cur[s] == kNone ? 0 : cur[s]) * p.R + min(j * 8 + g, p.R - 1)) * kv + step0 * 4 + q;
+        // n steps from `at`; `last`: the row's end may lie within them
+        auto steps = [&](auto count, int at, bool last) {
+            constexpr int N = decltype(count)::value;
+            uint4 xv[N][2 * MT], av[N][G][NT];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i)
-                    xv[u][i] = in && xr[i] ? __ldg(xr[i] + k) : make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < N; ++u) {
+                const bool in = !last || (at + u) * 4 + q < kv;
 #pragma unroll
                 for (int s = 0; s < G; ++s)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        av[u][s][j] = in && cur[s] != kNone && j * 8 + g < p.R ? __ldg(ar[s] + (int64_t)j * 8 * kv + k)
-                                                                                  : make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < NT; ++j) av[u][s][j] = in ? __ldg(ap[s][j] + 4 * u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) xv[u][i] = in ? __ldg(xp[i] + 4 * u) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < N; ++u)
 #pragma unroll
                 for (int s = 0; s < G; ++s)
 #pragma unroll
@@ -112,7 +121,17 @@ struct Shrink {
                             mma16816(acc[s][m][j], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
                             mma16816(acc[s][m][j], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
                         }
-        }
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) xp[i] += 4 * N;
+#pragma unroll
+            for (int s = 0; s < G; ++s)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) ap[s][j] += 4 * N;
+        };
+        const int whole = min(step1, kv / 4);  // steps that lie wholly in the row
+        int st = step0;
+        for (; st + U <= whole; st += U) steps(std::integral_constant<int, U>(), st, false);
+        for (; st < step1; ++st) steps(std::integral_constant<int, 1>(), st, st >= whole);
 #pragma unroll
         for (int s = 0; s < G; ++s)
 #pragma unroll
@@ -128,15 +147,19 @@ struct Shrink {
 };
 
 template <int NT, int TW, int KW, int MT>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+__global__ void __launch_bounds__(kThreads, MT > 1 ? 2 : 1) __cluster_dims__(kCluster, 1, 1)
     lora_shrink_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
     static_assert(TW * KW * 32 == kThreads, "one warp per (token part, K part)");
     using S = Shrink<NT, TW, KW, MT>;
-    constexpr int G = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;        // adapters a mixed pass takes at once
-    constexpr int U = MT * NT <= 4 ? 4 : MT * NT <= 16 ? 2 : 1;  // steps in flight
-    extern __shared__ float part[];                         // [KW][rows][NT * 8]
+    // adapters a mixed pass takes at once, and steps in flight with one and
+    // with several: what the registers hold (two blocks an SM for MT = 2)
+    constexpr int G = MT > 1 ? (NT <= 2 ? 2 : 1) : NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
+    constexpr int U1 = MT > 1 ? (NT <= 2 ? 2 : 1) : NT <= 2 ? 4 : NT <= 8 ? 2 : 1;
+    constexpr int UG = MT > 1 ? 1 : NT <= 2 ? 4 : 2;
+    extern __shared__ float part[];  // [KW][rows][NT * 8], then what the cluster sends [8][this rank's eighth]
     wait_for_previous_kernel();
     let_next_kernel_start();
+    cluster_arrive();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     const int tw = warp % TW, kw = warp / TW;
     const int t0 = (int)(blockIdx.x / kCluster) * tile_rows;
@@ -149,12 +172,12 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
         const int r = tw * MT * 16 + (i >> 1) * 16 + (i & 1) * 8 + g, t = t0 + r;
         const bool in = r < tile_rows && t < p.T;
         left[i] = id[i] = adapter_of(p, t, in);
-        xr[i] = id[i] != kNone ? static_cast<const uint4*>(p.x) + (int64_t)t * (p.x_stride / 8) : nullptr;
+        xr[i] = static_cast<const uint4*>(p.x) + (int64_t)(in ? t : t0) * (p.x_stride / 8);
         if (rank == 0 && kw == 0 && in && id[i] == kNone && p.ids[t] != -1) atomicOr(p.err, DERR_BAD_INDEX);
     }
     const int steps = (p.K + 31) / 32, at = (int)rank * KW + kw;
     const int step0 = steps * at / (kCluster * KW), step1 = steps * (at + 1) / (kCluster * KW);
-    float* mine = part + (kw * S::kRows + tw * MT * 16) * NT * 8;
+    float* mine = part + kw * S::kTile + tw * MT * 16 * NT * 8;
     // the lowest adapter among the rows not done yet
     auto next = [&] {
         uint32_t m = kNone;
@@ -171,94 +194,160 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
         const uint32_t a1 = next();
         if (G == 1 || a1 == kNone) {
             const uint32_t cur[1] = {a0};
-            S::template pass<1, U>(p, xr, cur, step0, step1, lane, id, mine);
+            S::template pass<1, U1>(p, xr, cur, step0, step1, lane, id, mine);
             a0 = a1;
         } else {
             uint32_t cur[G];
             cur[0] = a0;
 #pragma unroll
             for (int s = 1; s < G; ++s) cur[s] = s == 1 ? a1 : next();
-            S::template pass<G, (MT * NT <= 2 ? 2 : 1)>(p, xr, cur, step0, step1, lane, id, mine);
+            S::template pass<G, UG>(p, xr, cur, step0, step1, lane, id, mine);
             a0 = next();
         }
     }
+    // the K parts of the block, then of the cluster: rank e / kEighth gets
+    // element e of every rank, and adds them in order
+    constexpr int kEighth = S::kTile / kCluster;
+    float* sent = part + KW * S::kTile;
     __syncthreads();
-    const int n = S::kRows * NT * 8;
-    if constexpr (KW > 1) {
-        for (int e = threadIdx.x; e < n; e += kThreads) {
-            float s = part[e];
+    cluster_wait();  // everybody runs: its shared memory may be written
+    for (int e = threadIdx.x; e < S::kTile; e += kThreads) {
+        float s = part[e];
 #pragma unroll
-            for (int w = 1; w < KW; ++w) s += part[w * n + e];
-            part[e] = s;
-        }
+        for (int w = 1; w < KW; ++w) s += part[w * S::kTile + e];
+        store_to_rank(sent + rank * kEighth + e % kEighth, e / kEighth, s);
     }
-    cluster_sync();
-    // each rank finishes an eighth of the tile's rows
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     __nv_bfloat16* v = static_cast<__nv_bfloat16*>(p.ws);
-    for (int e = (int)rank * kThreads + threadIdx.x; e < n; e += kCluster * kThreads) {
-        const int r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
+    for (int i = threadIdx.x; i < kEighth; i += kThreads) {
+        const int e = (int)rank * kEighth + i, r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
         if (r >= tile_rows || c >= p.R) continue;
-        const uint32_t i = adapter_of(p, t, t < p.T);
-        if (i == kNone) continue;
-        float s = 0.0f;
+        const uint32_t a = adapter_of(p, t, t < p.T);
+        if (a == kNone) continue;
+        float s = sent[i];
 #pragma unroll
-        for (int k = 0; k < kCluster; ++k) s += load_of_rank(part + e, k);
-        v[(int64_t)t * p.R + c] = __float2bfloat16_rn(s * p.scale[i]);
+        for (int k = 1; k < kCluster; ++k) s += sent[k * kEighth + i];
+        v[(int64_t)t * p.R + c] = __float2bfloat16_rn(s * p.scale[a]);
     }
-    cluster_sync();  // nobody leaves while another rank may still read its shared memory
 }
 
 // out = base + v B_i^T: a warp takes MT m16 tiles and 32 columns.  Column
 // 2 q + e of n8 tile j is the warp's column 8 q + 2 j + e, so a thread's
-// results for a row are 8 neighbours: one 16-byte load and store.
+// results for a row are 8 neighbours: one 16-byte load and store.  base is
+// the accumulator's start, so a row's result does not depend on the tile's
+// other rows.
+template <int KS>
+struct Expand {
+    // B_i's rows of the warp's columns (columns beyond N read column 0)
+    static __device__ __forceinline__ void load_b(const LoraArgs& p, uint32_t i, int c0, int lane, uint2 (&f)[KS][4]) {
+        const int g = lane >> 2, q = lane & 3, rv = p.R / 4;
+        const uint2* b = static_cast<const uint2*>(p.b) + (int64_t)(i == kNone ? 0 : i) * p.N * rv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
+            const uint2* row = b + (int64_t)(c < p.N ? c : 0) * rv + q;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) f[s][j] = s * 4 + q < rv ? __ldg(row + s * 4) : make_uint2(0, 0);
+        }
+    }
+    // base (two rows' 8 columns) + v B
+    static __device__ __forceinline__ void product(const uint4 (&base)[2], const uint2 (&v)[2][KS], const uint2 (&b)[KS][4],
+                                                   float (&d)[4][4]) {
+        const __nv_bfloat162* lo = reinterpret_cast<const __nv_bfloat162*>(&base[0]);
+        const __nv_bfloat162* hi = reinterpret_cast<const __nv_bfloat162*>(&base[1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 l = __bfloat1622float2(lo[j]), h = __bfloat1622float2(hi[j]);
+            d[j][0] = l.x;
+            d[j][1] = l.y;
+            d[j][2] = h.x;
+            d[j][3] = h.y;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                mma16816(d[j], v[0][s].x, v[1][s].x, v[0][s].y, v[1][s].y, b[s][j].x, b[s][j].y);
+        }
+    }
+    static __device__ __forceinline__ uint4 round(const float (&d)[4][4], int h) {
+        uint4 o;
+        __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(&o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __floats2bfloat162_rn(d[j][2 * h], d[j][2 * h + 1]);
+        return o;
+    }
+};
+
 template <int KS, int MT>
 __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
+    using X = Expand<KS>;
     constexpr int G = MT > 1 ? 1 : KS <= 1 ? 4 : KS <= 2 ? 2 : 1;  // adapters whose B is loaded together
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int t0 = (int)blockIdx.x * tile_rows, c0 = ((int)blockIdx.y * (kThreads / 32) + warp) * 32;
+    if (c0 >= p.N) return;  // a whole warp beyond the columns
     const bool col_in = c0 + 8 * q < p.N;
+    const int rv = p.R / 4;
     // base and the ids do not come from the kernel before this one, which
     // lets this one start only after everything before it is done
-    uint32_t id[MT][2];
+    uint32_t id[MT][2], most = 0, least = kNone;
     uint4 bs[MT][2];
+    const uint4* base = static_cast<const uint4*>(p.base) + (int64_t)(t0 + g) * (p.base_stride / 8) + c0 / 8 + q;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = m * 16 + h * 8 + g, t = t0 + r;
-            const bool in = r < tile_rows && t < p.T;
+            const int r = m * 16 + h * 8, t = t0 + r + g;
+            const bool in = r + g < tile_rows && t < p.T;
+            bs[m][h] = in && col_in ? base[r * (p.base_stride / 8)] : make_uint4(0, 0, 0, 0);
             id[m][h] = adapter_of(p, t, in);
-            if (in && col_in)
-                bs[m][h] = *(static_cast<const uint4*>(p.base) + (int64_t)t * (p.base_stride / 8) + c0 / 8 + q);
+            most = max(most, id[m][h]);
+            least = min(least, id[m][h]);
         }
-    const uint2* bw = static_cast<const uint2*>(p.b);
-    const int rv = p.R / 4;
-    auto load_b = [&](uint32_t i, uint2 (&f)[KS][4]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                f[s][j] = i != kNone && c < p.N && s * 4 + q < rv
-                              ? __ldg(bw + ((int64_t)i * p.N + c) * rv + s * 4 + q) : make_uint2(0, 0);
-        }
-    };
-    wait_for_previous_kernel();
+    least = __reduce_min_sync(kFull, least);
+    most = __reduce_max_sync(kFull, most);
+    const uint2* v = static_cast<const uint2*>(p.ws) + (int64_t)(t0 + g) * rv + q;
+    uint4* out = static_cast<uint4*>(p.out) + (int64_t)(t0 + g) * (p.out_stride / 8) + c0 / 8 + q;
     uint2 bf[G][KS][4];
+    if (MT > 1 && least == most && least != kNone) {  // one adapter, every row in use
+        X::load_b(p, least, c0, lane, bf[0]);
+        wait_for_previous_kernel();
+        uint2 vf[MT][2][KS];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    vf[m][h][s] = s * 4 + q < rv ? v[(m * 16 + h * 8) * rv + s * 4] : make_uint2(0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float d[4][4];
+            X::product(bs[m], vf[m], bf[0], d);
+            if (col_in) {
+                out[m * 16 * (p.out_stride / 8)] = X::round(d, 0);
+                out[(m * 16 + 8) * (p.out_stride / 8)] = X::round(d, 1);
+            }
+        }
+        return;
+    }
     uint32_t held = kNone;  // G == 1: the adapter bf holds
-#pragma unroll
+    bool waited = false;
+#pragma unroll 1
     for (int m = 0; m < MT; ++m) {
+        uint32_t mid[2] = {id[0][0], id[0][1]};
+        uint4 mb[2] = {bs[0][0], bs[0][1]};
+#pragma unroll
+        for (int i = 1; i < MT; ++i)  // (constant indexes keep the arrays in registers)
+            if (i == m) {
+                mid[0] = id[i][0];
+                mid[1] = id[i][1];
+                mb[0] = bs[i][0];
+                mb[1] = bs[i][1];
+            }
+        uint32_t left[2] = {mid[0], mid[1]};
         uint2 vf[2][KS];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                vf[h][s] = id[m][h] != kNone && s * 4 + q < rv
-                               ? *(static_cast<const uint2*>(p.ws) + (int64_t)(t0 + m * 16 + h * 8 + g) * rv + s * 4 + q)
-                               : make_uint2(0, 0);
-        uint32_t left[2] = {id[m][0], id[m][1]};
-        float d[4][4];
-        for (;;) {
+        uint4 o[2] = {mb[0], mb[1]};  // a row without an adapter keeps base's bits
+        for (bool first = true;; first = false) {
             uint32_t cur[G];
 #pragma unroll
             for (int s = 0; s < G; ++s) {
@@ -269,45 +358,37 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_cons
             if (cur[0] == kNone) break;
             if (G > 1 || cur[0] != held) {
 #pragma unroll
-                for (int s = 0; s < G; ++s) load_b(cur[s], bf[s]);
+                for (int s = 0; s < G; ++s)
+                    if (s == 0 || cur[s] != kNone) X::load_b(p, cur[s], c0, lane, bf[s]);
                 held = cur[0];
             }
+            if (!waited) wait_for_previous_kernel();
+            waited = true;
+            if (first)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        vf[h][s] = mid[h] != kNone && s * 4 + q < rv ? v[(m * 16 + h * 8) * rv + s * 4]
+                                                                     : make_uint2(0, 0);
 #pragma unroll
             for (int s = 0; s < G; ++s) {
                 if (cur[s] == kNone) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-                        mma16816(e, vf[0][ks].x, vf[1][ks].x, vf[0][ks].y, vf[1][ks].y, bf[s][ks][j].x, bf[s][ks][j].y);
-                    if (id[m][0] == cur[s]) {
-                        d[j][0] = e[0];
-                        d[j][1] = e[1];
-                    }
-                    if (id[m][1] == cur[s]) {
-                        d[j][2] = e[2];
-                        d[j][3] = e[3];
-                    }
-                }
+                float d[4][4];
+                X::product(mb, vf, bf[s], d);
+                if (mid[0] == cur[s]) o[0] = X::round(d, 0);
+                if (mid[1] == cur[s]) o[1] = X::round(d, 1);
             }
         }
+        // a tile without adapters has waited for nothing: out may be base,
+        // which only this thread reads
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = m * 16 + h * 8 + g, t = t0 + r;
-            if (r >= tile_rows || t >= p.T || !col_in) continue;
-            uint4 o = bs[m][h];
-            if (id[m][h] != kNone) {
-                __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(&o);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = __bfloat1622float2(w[j]);
-                    w[j] = __floats2bfloat162_rn(f.x + d[j][2 * h], f.y + d[j][2 * h + 1]);
-                }
-            }
-            *(static_cast<uint4*>(p.out) + (int64_t)t * (p.out_stride / 8) + c0 / 8 + q) = o;
+            const int r = m * 16 + h * 8;
+            if (r + g < tile_rows && t0 + r + g < p.T && col_in) out[r * (p.out_stride / 8)] = o[h];
         }
     }
+    if (!waited) wait_for_previous_kernel();
 }
 
 cudaError_t launch(const void* kernel, dim3 grid, size_t smem, cudaStream_t s, const LoraArgs& p, int tile_rows) {
@@ -329,25 +410,31 @@ cudaError_t launch(const void* kernel, dim3 grid, size_t smem, cudaStream_t s, c
     return cudaLaunchKernelExC(&c, kernel, args);
 }
 
+template <int NT, int TW, int KW, int MT>
+cudaError_t launch_shrink(const LoraArgs& p, int rows, cudaStream_t s) {
+    return launch((const void*)lora_shrink_kernel<NT, TW, KW, MT>, dim3((p.T + rows - 1) / rows * kCluster),
+                  Shrink<NT, TW, KW, MT>::kSmem, s, p, rows);
+}
+
 template <int NT>
 cudaError_t launch_rank(const LoraArgs& p, cudaStream_t s) {
+    // shrink: the smallest tiles whose clusters still fit the GPU at once
+    // (then few tokens meet a block, with the most parts of K), or large ones
+    auto fits = [&](int rows) { return (int64_t)((p.T + rows - 1) / rows) * kCluster <= p.n_sms; };
+    int rows = 1;
+    while (rows < 64 && !fits(rows)) rows *= 2;
+    cudaError_t e;
+    if (rows <= 16) e = launch_shrink<NT, 1, 8, 1>(p, rows, s);
+    else if (rows == 32) e = launch_shrink<NT, 2, 4, 1>(p, rows, s);
+    else if (fits(rows) || NT > 8) e = launch_shrink<NT, 4, 2, 1>(p, rows, s);
+    else e = launch_shrink<NT, 4, 2, NT <= 8 ? 2 : 1>(p, NT <= 8 ? 128 : 64, s);
+    if (e != cudaSuccess) return e;
+    // expand: 64 tokens a warp where that leaves every SM two blocks
     constexpr int KS = NT / 2;
     const int cols = (p.N + 255) / 256;
-    cudaError_t e;
-    if (p.T >= 2048) {
-        using S = Shrink<NT, 4, 2, 2>;
-        e = launch((const void*)lora_shrink_kernel<NT, 4, 2, 2>, dim3((p.T + S::kRows - 1) / S::kRows * kCluster),
-                   S::kSmem, s, p, S::kRows);
-        if (e != cudaSuccess) return e;
+    if ((int64_t)((p.T + 63) / 64) * cols >= 2 * p.n_sms)
         return launch((const void*)lora_expand_kernel<KS, 4>, dim3((p.T + 63) / 64, cols), 0, s, p, 64);
-    }
-    // few tokens: tiles of 1 to 16 tokens, so that the clusters fill the GPU
-    int rows = 1;
-    while (rows < 16 && (int64_t)((p.T + rows - 1) / rows) * kCluster > p.n_sms) rows *= 2;
-    using S = Shrink<NT, 1, 8, 1>;
-    e = launch((const void*)lora_shrink_kernel<NT, 1, 8, 1>, dim3((p.T + rows - 1) / rows * kCluster), S::kSmem, s, p,
-               rows);
-    if (e != cudaSuccess) return e;
+    rows = std::min(rows, 16);
     return launch((const void*)lora_expand_kernel<KS, 1>, dim3((p.T + rows - 1) / rows, cols), 0, s, p, rows);
 }
 
