@@ -72,8 +72,8 @@ def test_rows(rows, H, residual, codes):
     check(call(x, w, r, codes), x, w, r)
 
 
-def test_many_rows():
-    rows, H = 5000, 1024
+@pytest.mark.parametrize("rows, H", [(5000, 1024), (2500, 512), (2501, 264), (2100, 7168), (2100, 6152), (2049, 8192)])
+def test_many_rows(rows, H):
     x = I.randn_bf16((rows, H), 1.0, 5, "cuda")
     r = I.randn_bf16((rows, H), 4.0, 6, "cuda")
     w = I.randn_bf16((H,), 1.0, 7, "cuda")
@@ -115,6 +115,18 @@ def test_zero_rows_and_zero_weights():
     check(o, x, w)
     o = call(x, torch.zeros_like(w))
     assert (o["out"] == 0).all() and (o["row_scale"] == 1.0).all()
+
+
+@pytest.mark.parametrize("rows, H", [(2200, 512), (2200, 7168), (3, 8), (40, 32768)])
+def test_squares_beyond_the_range_in_every_kernel(rows, H):
+    x = I.randn_bf16((rows, H), 1.0, 20, "cuda")
+    x[::3] *= 1e30
+    x[1::7, 0] = -3e38
+    w = I.randn_bf16((H,), 1.0, 21, "cuda")
+    o = call(x, w)
+    h, y, scale = formula(x, None, w)
+    assert (np.abs(f64(o["out"]) - y) <= (BF16_HALF + FP32) * np.abs(y) + 1e-38).all()
+    assert (np.abs(f64(o["row_scale"]) - scale) <= FP32 * scale).all()
 
 
 def test_range_ends():
