@@ -1,0 +1,451 @@
+// lora_tc.cu: dwdp_lora_add for many tokens, fed by TMA.
+//
+// Both halves stream: x once (shrink), base in and out once (expand); the
+// adapters stay in L2.  What counts is bytes in flight, so the loads are TMA
+// boxes into rings in shared memory, 100 KB and more an SM, and the arithmetic
+// is whatever keeps up: tcgen05 on the x tiles, warp MMAs on the base tiles.
+//   shrink  a cluster shares a tile of 128 tokens, each CTA a part of K; the
+//           parts meet in the owner's shared memory, in rank order
+//   expand  staying CTAs walk boxes of 32 tokens x 256 columns: load, add v B^T
+//           in place, store
+// A tile's tokens may have any adapters: shrink multiplies the tile by each
+// that occurs (several at a time) and keeps a row's own; expand does so by 16
+// rows.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "dwdp_internal.h"
+#include "lora_ops.h"
+#include "tc_ops.h"
+
+namespace dwdp {
+namespace {
+
+// ---------------------------------------------------------------- shrink --
+constexpr int kTokens = 128;    // tokens of a tile
+constexpr int kSlice = 64;      // elements of K per stage
+constexpr int kXBytes = kTokens * kSlice * 2;
+constexpr int kShrinkThreads = 192;
+
+// NR: the rank rounded up to 16 or a power of two (columns of one adapter's
+// accumulator); a pass takes kGroup adapters, kCols columns of TMEM.  Two CTAs
+// fit an SM up to NR = 64.
+template <int NR>
+struct ShrinkSmem {
+    static constexpr int kGroup = NR == 16 ? 4 : 1;
+    static constexpr int kStages = NR == 64 ? 3 : 4;
+    static constexpr int kCols = NR * kGroup < 32 ? 32 : NR * kGroup;
+    static constexpr int kABytes = NR * kSlice * 2;  // one adapter's rows of a slice
+    static constexpr int kStage = kXBytes + kGroup * kABytes;
+    static constexpr int kPart = kStages * kStage;         // float [128][NR]: this CTA's part of K
+    static constexpr int kList = kPart + kTokens * NR * 4;  // uint32 ids[128], distinct[128]
+    static constexpr int kBars = kList + 2 * kTokens * 4;   // full[S], empty[S], done
+    static constexpr int kMisc = kBars + 8 * (2 * kStages + 1);
+    static constexpr int kBytes = 1024 + kMisc + 32;
+    // what the cluster sends, float [C][128 / C][NR], goes where the stages were
+    static_assert(kTokens * NR * 4 <= kPart, "");
+    static_assert(NR == 128 || 2 * (kBytes + 1024) <= 227 << 10, "two CTAs an SM");
+};
+
+__device__ __forceinline__ void mma_rank(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+template <int NR>
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __grid_constant__ LoraTcArgs p) {
+    using S = ShrinkSmem<NR>;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* mem = raw + (base - smem_u32(raw));
+    float* part = reinterpret_cast<float*>(mem + S::kPart);
+    float* sent = reinterpret_cast<float*>(mem);
+    uint32_t* ids = reinterpret_cast<uint32_t*>(mem + S::kList);
+    uint32_t* distinct = ids + kTokens;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mem + S::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(mem + S::kMisc + 8);
+    int* n_distinct = reinterpret_cast<int*>(mem + S::kMisc + 16);
+    const uint32_t full0 = base + S::kBars, empty0 = full0 + 8 * S::kStages, done = empty0 + 8 * S::kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = p.parts;  // CTAs of the cluster
+    const uint32_t rank = C > 1 ? cluster_ctarank() : 0;
+    const int t0 = (int)(blockIdx.x / C) * kTokens;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tm_x);
+        prefetch_map(&p.tm_a);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(S::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    if (warp == 0) {
+        // the tile's adapters, and which occur, ascending
+        uint32_t left[kTokens / 32];
+#pragma unroll
+        for (int i = 0; i < kTokens / 32; ++i) {
+            const int r = 32 * i + lane, t = t0 + r;
+            left[i] = adapter_of(p.lora, t, t < p.lora.T);
+            ids[r] = left[i];
+            if (rank == 0 && t < p.lora.T && left[i] == kNoAdapter && p.lora.ids[t] != -1)
+                atomicOr(p.lora.err, DERR_BAD_INDEX);
+        }
+        int n = 0;
+        for (;; ++n) {
+            uint32_t m = kNoAdapter;
+#pragma unroll
+            for (int i = 0; i < kTokens / 32; ++i) m = min(m, left[i]);
+            m = __reduce_min_sync(0xffffffffu, m);
+            if (m == kNoAdapter) break;
+#pragma unroll
+            for (int i = 0; i < kTokens / 32; ++i)
+                if (left[i] == m) left[i] = kNoAdapter;
+            if (lane == 0) distinct[n] = m;
+        }
+        if (lane == 0) *n_distinct = n;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int n = *n_distinct;
+    const int slices = (p.lora.K + kSlice - 1) / kSlice;
+    const int s0 = slices * (int)rank / C, s1 = slices * ((int)rank + 1) / C;
+    // D fp32, A and B bf16, both K-major, N / 8 at bits 17-22, M / 16 at 24-28
+    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NR >> 3) << 17) | (8u << 24);
+
+    int stage = 0;  // of this thread's role; they go round together
+    uint32_t phase = 0, pass = 0;
+    bool ok = true;
+    for (int d0 = 0; d0 < n; d0 += S::kGroup, ++pass) {
+        const int group = min(S::kGroup, n - d0);
+        if (warp == 0 && lane == 0) {
+            for (int s = s0; s < s1 && ok; ++s) {
+                ok = mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.lora.err, DERR_PRODUCER_WAIT);
+                if (!ok) break;
+                const uint32_t bar = full0 + 8 * stage, dst = base + stage * S::kStage;
+                mbar_arrive_expect_tx(bar, kXBytes + group * p.lora.R * kSlice * 2);
+                tma_load_2d(dst, &p.tm_x, s * kSlice, t0, bar);
+                for (int a = 0; a < group; ++a)
+                    tma_load_2d(dst + kXBytes + a * S::kABytes, &p.tm_a, s * kSlice, (int)distinct[d0 + a] * p.lora.R, bar);
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) {  // loads still on their way land before this CTA may leave
+                const uint64_t t = global_timer();
+                while (global_timer() - t < 1000000ull) {}
+            }
+        } else if (warp == 1 && lane == 0) {
+            for (int s = s0; s < s1; ++s) {
+                if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, p.lora.err, DERR_MMA_FULL_WAIT)) break;
+                tc_fence_after();
+                const uint32_t at = base + stage * S::kStage;
+                const uint64_t x = smem_desc(at);
+                for (int a = 0; a < group; ++a) {
+                    const uint64_t w = smem_desc(at + kXBytes + a * S::kABytes);
+#pragma unroll
+                    for (int k = 0; k < kSlice / 16; ++k)  // 32 bytes of K further: + 2 in the start address
+                        mma_rank(tmem + a * NR, x + 2 * k, w + 2 * k, idesc, s > s0 || k > 0);
+                }
+                tc_commit(empty0 + 8 * stage);
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            tc_commit(done);
+        } else if (warp >= 2) {
+            const int q = warp & 3, r = 32 * q + lane;  // the TMEM lanes this warp may read; this thread's token
+            const bool got = s1 > s0 && __all_sync(0xffffffffu, mbar_wait(done, pass & 1u, abort_flag, p.lora.err, DERR_EPI_WAIT));
+            tc_fence_after();
+            for (int a = 0; a < group; ++a) {
+                const bool own = ids[r] == distinct[d0 + a];
+#pragma unroll
+                for (int c = 0; c < NR; c += 16) {
+                    uint32_t v[16];
+                    if (got) {
+                        tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + a * NR + c, v);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0u;
+                    }
+                    if (own) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4*>(part + r * NR + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        __syncthreads();  // the accumulators may be written again
+        tc_fence_after();
+    }
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+
+    // the cluster's parts: rank o finishes rows o * 128 / C ...
+    const int rows = kTokens / C, n_own = rows * NR;
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();  // nobody uses its stages any more
+        for (int e = threadIdx.x; e < kTokens * NR; e += kShrinkThreads)
+            store_to_rank(sent + rank * n_own + e % n_own, e / n_own, part[e]);
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
+    __nv_bfloat16* v = static_cast<__nv_bfloat16*>(p.lora.ws);
+    for (int i = threadIdx.x; i < n_own; i += kShrinkThreads) {
+        const int r = (int)rank * rows + i / NR, c = i % NR;
+        const uint32_t a = ids[r];
+        if (c >= p.lora.R || a == kNoAdapter) continue;
+        float s = C > 1 ? sent[i] : part[i];
+        for (int k = 1; k < C; ++k) s += sent[k * n_own + i];
+        v[(int64_t)(t0 + r) * p.lora.R + c] = __float2bfloat16_rn(s * p.lora.scale[a]);
+    }
+}
+
+template <int NR>
+cudaError_t launch_shrink(const LoraTcArgs& p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(lora_shrink_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         ShrinkSmem<NR>::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = p.parts;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((p.lora.T + kTokens - 1) / kTokens * p.parts);
+    c.blockDim = dim3(kShrinkThreads);
+    c.dynamicSmemBytes = ShrinkSmem<NR>::kBytes;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 2;
+    return cudaLaunchKernelEx(&c, lora_shrink_tc_kernel<NR>, p);
+}
+
+// ---------------------------------------------------------------- expand --
+constexpr int kBoxRows = 32, kBoxCols = 256;
+constexpr int kBoxBytes = kBoxRows * kBoxCols * 2;  // 16 KB
+constexpr int kExpandStages = 6;
+constexpr int kExpandThreads = 288;  // 8 warps of arithmetic, 1 of copies
+constexpr int kExpandBars = kExpandStages * kBoxBytes;  // full[S], ready[S]
+constexpr int kExpandSmem = 128 + kExpandBars + 8 * 2 * kExpandStages + 16;
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+// CTA c walks the boxes [c U / G, (c + 1) U / G) of all U, columns first, so a
+// warp keeps its rows' v over a run of boxes.  Warp w: rows 16 (w / 4) ...
+// of the box, columns 64 (w % 4) ...
+template <int KS>
+__global__ void __launch_bounds__(kExpandThreads, KS <= 2 ? 2 : 1) lora_expand_tc_kernel(const __grid_constant__ LoraTcArgs p) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 127u) & ~127u;
+    uint8_t* mem = raw + (base - smem_u32(raw));
+    const uint32_t full0 = base + kExpandBars, ready0 = full0 + 8 * kExpandStages;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(mem + kExpandBars + 16 * kExpandStages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int across = (p.lora.N + kBoxCols - 1) / kBoxCols;
+    const int64_t boxes = (int64_t)((p.lora.T + kBoxRows - 1) / kBoxRows) * across;
+    const int64_t first = boxes * blockIdx.x / gridDim.x;
+    const int count = (int)(boxes * (blockIdx.x + 1) / gridDim.x - first);  // this CTA's boxes
+    const int col0 = (int)(first % across) * kBoxCols, row0 = (int)(first / across) * kBoxRows;
+    const int width = across * kBoxCols;
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < kExpandStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(ready0 + 8 * s, 8);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tm_base);
+        prefetch_map(&p.tm_out);
+    }
+    __syncthreads();
+    if (warp == 8) {
+        if (lane == 0) {
+            // where the next load goes, and the next store
+            int load_x = col0, load_y = row0, load_s = 0, x = col0, y = row0, s = 0;
+            uint32_t phase = 0;
+            auto load = [&] {
+                mbar_arrive_expect_tx(full0 + 8 * load_s, kBoxBytes);
+                tma_load_2d(base + load_s * kBoxBytes, &p.tm_base, load_x, load_y, full0 + 8 * load_s);
+                if (++load_s == kExpandStages) load_s = 0;
+                if ((load_x += kBoxCols) == width) {
+                    load_x = 0;
+                    load_y += kBoxRows;
+                }
+            };
+            // base does not come from the kernel before this one, which lets
+            // this one start only after everything before it is done
+            for (int i = 0; i < min(count, kExpandStages); ++i) load();
+            bool ok = true;
+            for (int i = 0; i < count; ++i) {
+                ok = mbar_wait(ready0 + 8 * s, phase, abort_flag, p.lora.err, DERR_EPI_WAIT);
+                if (!ok) break;
+                tma_store_2d(&p.tm_out, x, y, base + s * kBoxBytes);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                // the store before this one has left its stage: fill it again
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                if (i > 0 && i - 1 + kExpandStages < count) load();
+                if ((x += kBoxCols) == width) {
+                    x = 0;
+                    y += kBoxRows;
+                }
+                if (++s == kExpandStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!ok) {  // loads still on their way land before this CTA may leave
+                const uint64_t t = global_timer();
+                while (global_timer() - t < 1000000ull) {}
+            }
+        }
+    } else {
+        const int r0 = 16 * (warp >> 2), c0 = 64 * (warp & 3);
+        const int rv = p.lora.R / 4;
+        wait_for_previous_kernel();
+        uint32_t id[2] = {kNoAdapter, kNoAdapter}, phase = 0;
+        uint2 v[2][KS];
+        int x = col0, t = row0 + r0 + g, s = 0;  // the box's column, this thread's first row, the stage
+        for (int i = 0; i < count; ++i) {
+            const int n0 = x + c0;
+            if (i == 0 || x == 0) {  // new rows
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    id[h] = adapter_of(p.lora, t + 8 * h, t + 8 * h < p.lora.T);
+                    const uint2* row = static_cast<const uint2*>(p.lora.ws) + (int64_t)(t + 8 * h) * rv + q;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        v[h][k] = id[h] != kNoAdapter && k * 4 + q < rv ? row[k * 4] : make_uint2(0, 0);
+                }
+            }
+            uint32_t left[2] = {id[0], id[1]};
+            auto next = [&] {
+                const uint32_t m = __reduce_min_sync(0xffffffffu, min(left[0], left[1]));
+                if (left[0] == m) left[0] = kNoAdapter;
+                if (left[1] == m) left[1] = kNoAdapter;
+                return m;
+            };
+            // the first adapter's B before the wait for the box
+            uint32_t cur = next();
+            uint2 bf[2][KS][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) Expand<KS>::load_b(p.lora, cur, n0 + 32 * h, lane, bf[h]);
+            if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, phase, abort_flag, p.lora.err, DERR_MMA_FULL_WAIT))) break;
+            // row g (and g + 8) of this warp's rows, columns 8 q ... of each half
+            uint4* at = reinterpret_cast<uint4*>(mem + s * kBoxBytes + (r0 + g) * kBoxCols * 2 + c0 * 2) + q;
+            constexpr int kRow8 = 8 * kBoxCols * 2 / 16;
+            uint4 bs[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                bs[h][0] = at[4 * h];
+                bs[h][1] = at[4 * h + kRow8];
+            }
+            while (cur != kNoAdapter) {
+                const uint32_t then = next();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float d[4][4];
+                    Expand<KS>::product(bs[h], v, bf[h], d);
+                    if (then != kNoAdapter) Expand<KS>::load_b(p.lora, then, n0 + 32 * h, lane, bf[h]);
+                    if (id[0] == cur) at[4 * h] = Expand<KS>::round(d, 0);
+                    if (id[1] == cur) at[4 * h + kRow8] = Expand<KS>::round(d, 1);
+                }
+                cur = then;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready0 + 8 * s);
+            if ((x += kBoxCols) == width) {
+                x = 0;
+                t += kBoxRows;
+            }
+            if (++s == kExpandStages) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+template <int KS>
+cudaError_t launch_expand(const LoraTcArgs& p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(lora_expand_tc_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t boxes = (int64_t)((p.lora.T + kBoxRows - 1) / kBoxRows) * ((p.lora.N + kBoxCols - 1) / kBoxCols);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)std::min<int64_t>(boxes, (KS <= 2 ? 2 : 1) * p.lora.n_sms));
+    c.blockDim = dim3(kExpandThreads);
+    c.dynamicSmemBytes = kExpandSmem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, lora_expand_tc_kernel<KS>, p);
+}
+
+}  // namespace
+
+// Parts of K per tile of 128 tokens: as many (at most 8) as the SMs' two CTAs
+// (one beyond rank 64) hold at once.
+int lora_tc_parts(int64_t T, int R, int n_sms) {
+    const int64_t tiles = (T + kTokens - 1) / kTokens;
+    int parts = 8;
+    while (parts > 1 && tiles * parts > (R > 64 ? 1 : 2) * n_sms) parts /= 2;
+    return parts;
+}
+
+bool lora_is_long(int64_t T) { return T >= 1024; }
+
+cudaError_t launch_lora_tc(const LoraTcArgs& p, cudaStream_t s) {
+    const int R = p.lora.R;
+    const cudaError_t e = R <= 16 ? launch_shrink<16>(p, s) : R <= 32 ? launch_shrink<32>(p, s)
+                          : R <= 64 ? launch_shrink<64>(p, s) : launch_shrink<128>(p, s);
+    if (e != cudaSuccess) return e;
+    return R <= 16 ? launch_expand<1>(p, s) : R <= 32 ? launch_expand<2>(p, s) : R <= 64 ? launch_expand<4>(p, s)
+                                                                                      : launch_expand<8>(p, s);
+}
+
+}  // namespace dwdp

@@ -84,7 +84,14 @@ def test_sizes(T, K, N, R, order):
     check(run(*args), *args)
 
 
-@pytest.mark.parametrize("T", [64, 200, 1000])
+@pytest.mark.parametrize("K, N, R", SIZES + [(72, 264, 16), (7168, 520, 16), (1000, 1000, 32)])
+@pytest.mark.parametrize("T", [1153, 2048])
+@pytest.mark.parametrize("order", ["one", "runs", "mixed"])
+def test_sizes_of_many_tokens(K, N, R, T, order):
+    test_sizes(T, K, N, R, order)
+
+
+@pytest.mark.parametrize("T", [64, 200, 1000, 1300])
 def test_every_token_its_own_adapter(T):
     n = 300
     ids = np.random.default_rng(T).permutation(np.resize(np.arange(n), T))
@@ -107,8 +114,9 @@ def test_nobody_has_an_adapter():
     assert torch.equal(run(*args), args[-1])
 
 
-def test_row_strides_and_in_place():
-    T, K, N = 200, 512, 768
+@pytest.mark.parametrize("T", [200, 1537])
+def test_row_strides_and_in_place(T):
+    K, N = 512, 768
     ids = np.random.default_rng(5).integers(-1, 4, T)
     x, a, b, scale, ids, base = case(T, K, N, 16, 4, ids, pad=512)
     wide = torch.full((T, N + 64), 5.0, dtype=torch.bfloat16, device="cuda")
@@ -120,18 +128,20 @@ def test_row_strides_and_in_place():
     assert torch.equal(same, out) and (full[:, N:] == 3.0).all()
 
 
-def test_ids_outside_the_bank_are_reported_and_skipped():
-    T, n = 40, 3
+@pytest.mark.parametrize("T", [40, 1200])
+def test_ids_outside_the_bank_are_reported_and_skipped(T):
+    n = 3
     ids = np.random.default_rng(6).integers(-1, n, T)
     ids[5], ids[30] = n, -2
     args = case(T, 256, 256, 16, n, ids)
     check(run(*args, status=-6), *args)
 
 
-def test_nan_stays_with_its_token_and_adapter():
+@pytest.mark.parametrize("T", [70, 1100])
+def test_nan_stays_with_its_token_and_adapter(T):
     """A NaN in one token's row, and adapters full of NaN that no token of
     the batch uses, or that its neighbours use."""
-    T, n = 70, 6
+    n = 6
     ids = np.random.default_rng(7).integers(0, 4, T)
     ids[10], ids[11] = 4, 0
     x, a, b, scale, ids, base = case(T, 256, 256, 16, n, ids)
@@ -147,9 +157,10 @@ def test_nan_stays_with_its_token_and_adapter():
     assert torch.equal(out[rest.cuda()], clean[rest.cuda()])
 
 
-def test_same_bits_every_time_and_on_another_stream():
-    ids = np.random.default_rng(8).integers(-1, 8, 777)
-    args = case(777, 1024, 1032, 32, 8, ids)
+@pytest.mark.parametrize("T", [777, 3000])
+def test_same_bits_every_time_and_on_another_stream(T):
+    ids = np.random.default_rng(8).integers(-1, 8, T)
+    args = case(T, 1024, 1032, 32, 8, ids)
     first = run(*args)
     assert torch.equal(first, run(*args)) and torch.equal(first, run(*args, stream=torch.cuda.Stream()))
 
