@@ -94,15 +94,15 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, in
 }
 
 bool encode_matrix(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t row_bytes,
-                   uint32_t box_rows, uint32_t box_cols, bool swizzle) {
+                   uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn || rows == 0) return false;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t box[2] = {64, box_rows};
     cuuint32_t es[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -878,9 +878,8 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
         p.parts = router_pair_parts(T, c.n_experts, c.hidden);
         logits = out->logits && p.parts == 1 ? out->logits : planes;
         const uint64_t row_bytes = 2ull * c.hidden;
-        if (!encode_matrix(&r.tm_x, x, T, c.hidden, row_bytes, 128, 64, true) ||
-            !encode_matrix(&r.tm_w, w_router, c.n_experts, c.hidden, row_bytes, router_pair_cols(c.n_experts) / 2, 64,
-                           true))
+        if (!encode_matrix(&r.tm_x, x, T, c.hidden, row_bytes, 128) ||
+            !encode_matrix(&r.tm_w, w_router, c.n_experts, c.hidden, row_bytes, router_pair_cols(c.n_experts) / 2))
             return fail(ctx, DWDP_ERR_CUDA, "tensor map for the router GEMM");
         r.z = logits;
         r.part_stride = (int64_t)T * c.n_experts;
@@ -990,17 +989,13 @@ int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T,
         DWDP_CUDA(ctx, launch_lora_add(p, stream));
         return DWDP_OK;
     }
-    for (const void* q : {x, a, base, static_cast<const void*>(out)})  // read or written through tensor maps
-        if (!is_device_memory_of(q, ctx->device))
-            return fail(ctx, DWDP_ERR_INVALID_ARG, "x, a, base and out must be device memory of the context's device (%d)",
-                        ctx->device);
+    if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(a, ctx->device))  // read through tensor maps
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and a must be device memory of the context's device (%d)", ctx->device);
     LoraTcArgs q;
     q.lora = p;
     q.parts = lora_tc_parts(T, R, ctx->n_sms);
-    if (!encode_matrix(&q.tm_x, x, T, K, 2ull * x_stride, 128, 64, true) ||
-        !encode_matrix(&q.tm_a, a, (uint64_t)n_adapters * R, K, 2ull * K, R, 64, true) ||
-        !encode_matrix(&q.tm_base, base, T, N, 2ull * base_stride, 32, 256, false) ||
-        !encode_matrix(&q.tm_out, out, T, N, 2ull * out_stride, 32, 256, false))
+    if (!encode_matrix(&q.tm_x, x, T, K, 2ull * x_stride, 128) ||
+        !encode_matrix(&q.tm_a, a, (uint64_t)n_adapters * R, K, 2ull * K, R))
         return fail(ctx, DWDP_ERR_CUDA, "tensor maps of the adapters");
     DWDP_CUDA(ctx, launch_lora_tc(q, stream));
     return DWDP_OK;

@@ -126,10 +126,10 @@ struct GemmArgs {
 // swizzled to BK_BYTES.  K counts elements of format fmt (bf16, E4M3 codes or
 // NVFP4 codes, two per byte); a weight slot is weight_slot_bytes apart.
 bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, int fmt = FMT_BF16);
-// A bf16 matrix whose rows are row_bytes apart, with boxes of box_rows x
-// box_cols (swizzle: box_cols = 64 elements in the 128-byte swizzle).
+// A bf16 matrix whose rows are row_bytes apart, with boxes of box_rows x 64
+// elements in the 128-byte swizzle.
 bool encode_matrix(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t row_bytes,
-                   uint32_t box_rows, uint32_t box_cols, bool swizzle);
+                   uint32_t box_rows);
 bool encode_slots(CUtensorMap* m, const void* base, uint64_t slots, uint64_t rows, uint64_t K,
                   int fmt = FMT_BF16);
 
@@ -296,12 +296,11 @@ struct LoraArgs {
 size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R);
 cudaError_t launch_lora_add(const LoraArgs& p, cudaStream_t s);
 
-// lora_tc.cu: the same, fed by TMA, for lora_is_long sizes.  Boxes: x 128 rows
-// x 64 elements, a ([n R][K]) R rows x 64 elements, both in the 128-byte
-// swizzle; base and out 32 rows x 256 elements, plain.
+// lora_tc.cu: the same, fed by bulk copies, for lora_is_long sizes.  Boxes: x
+// 128 rows, a ([n R][K]) R rows.
 struct LoraTcArgs {
     LoraArgs lora;
-    CUtensorMap tm_x, tm_a, tm_base, tm_out;
+    CUtensorMap tm_x, tm_a;
     int parts;  // lora_tc_parts
 };
 bool lora_is_long(int64_t T);

@@ -1,16 +1,16 @@
 // lora_tc.cu: dwdp_lora_add for many tokens, fed by TMA.
 //
 // Both halves stream: x once (shrink), base in and out once (expand); the
-// adapters stay in L2.  What counts is bytes in flight, so the loads are TMA
-// boxes into rings in shared memory, 100 KB and more an SM, and the arithmetic
-// is whatever keeps up: tcgen05 on the x tiles, warp MMAs on the base tiles.
+// adapters stay in L2.  What counts is bytes in flight and their order, so the
+// loads are bulk copies into rings in shared memory, 100 KB and more an SM, and
+// the arithmetic is whatever keeps up: tcgen05 on the x tiles, warp MMAs on
+// the base tiles.
 //   shrink  a cluster shares a tile of 128 tokens, each CTA a part of K; the
 //           parts meet in the owner's shared memory, in rank order
-//   expand  staying CTAs walk boxes of 32 tokens x 256 columns: load, add v B^T
-//           in place, store
+//   expand  staying CTAs walk stages of 16 tokens x 512 columns: load, add
+//           v B^T in place, store
 // A tile's tokens may have any adapters: shrink multiplies the tile by each
-// that occurs (several at a time) and keeps a row's own; expand does so by 16
-// rows.
+// that occurs (several at a time) and keeps a row's own; so does expand.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -258,149 +258,179 @@ cudaError_t launch_shrink(const LoraTcArgs& p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- expand --
-constexpr int kBoxRows = 32, kBoxCols = 256;
-constexpr int kBoxBytes = kBoxRows * kBoxCols * 2;  // 16 KB
-constexpr int kExpandStages = 6;
-constexpr int kExpandThreads = 288;  // 8 warps of arithmetic, 1 of copies
-constexpr int kExpandBars = kExpandStages * kBoxBytes;  // full[S], ready[S]
-constexpr int kExpandSmem = 128 + kExpandBars + 8 * 2 * kExpandStages + 16;
-
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"((uint64_t)map),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-}
-
-// CTA c walks the boxes [c U / G, (c + 1) U / G) of all U, columns first, so a
-// warp keeps its rows' v over a run of boxes.  Warp w: rows 16 (w / 4) ...
-// of the box, columns 64 (w % 4) ...
+// A stage holds 16 rows of base, kCols columns of each, fetched and put back
+// row by row (bulk copies of up to 1 KB; a multiple of 16 bytes, since rows
+// and N are).  The pitch of 64 bytes more keeps a warp's 16-byte accesses to
+// neighbouring rows in different banks.
 template <int KS>
-__global__ void __launch_bounds__(kExpandThreads, KS <= 2 ? 2 : 1) lora_expand_tc_kernel(const __grid_constant__ LoraTcArgs p) {
-    extern __shared__ uint8_t raw[];
-    const uint32_t base = (smem_u32(raw) + 127u) & ~127u;
-    uint8_t* mem = raw + (base - smem_u32(raw));
-    const uint32_t full0 = base + kExpandBars, ready0 = full0 + 8 * kExpandStages;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(mem + kExpandBars + 16 * kExpandStages);
+struct ExpandSmem {
+    static constexpr int kHalves = KS <= 4 ? 2 : 1;  // 32-column halves a warp holds B for
+    static constexpr int kCols = 8 * 32 * kHalves;
+    static constexpr int kPitch = kCols * 2 + 64;
+    static constexpr int kStage = 16 * kPitch;
+    static constexpr int kPerSm = KS <= 2 ? 2 : 1;
+    static constexpr int kStages = KS <= 2 ? 6 : 12;
+    static constexpr int kBars = kStages * kStage;  // full[S], ready[S]
+    static constexpr int kBytes = kBars + 16 * kStages + 16;
+};
+constexpr int kExpandThreads = 288;  // 8 warps of arithmetic, 1 of copies
+
+// Staying CTAs: CTA c takes the stages c, c + G, ... in the order of memory,
+// so what the GPU works on at one time lies close together (8192 x 7168 bf16
+// in and out: a copy in this order 37 us, with a run of stages per CTA 41,
+// with pieces of 512 bytes 51).  G is a multiple of the stages across a row:
+// a CTA stays in its columns, and B stays in registers while the adapter does.
+template <int KS>
+__global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
+    lora_expand_tc_kernel(const __grid_constant__ LoraArgs p) {
+    using S = ExpandSmem<KS>;
+    constexpr int NH = S::kHalves;
+    extern __shared__ __align__(128) uint8_t mem[];
+    const uint32_t base = smem_u32(mem), full0 = base + S::kBars, ready0 = full0 + 8 * S::kStages;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(mem + S::kBars + 16 * S::kStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int across = (p.lora.N + kBoxCols - 1) / kBoxCols;
-    const int64_t boxes = (int64_t)((p.lora.T + kBoxRows - 1) / kBoxRows) * across;
-    const int64_t first = boxes * blockIdx.x / gridDim.x;
-    const int count = (int)(boxes * (blockIdx.x + 1) / gridDim.x - first);  // this CTA's boxes
-    const int col0 = (int)(first % across) * kBoxCols, row0 = (int)(first / across) * kBoxRows;
-    const int width = across * kBoxCols;
+    const int across = (p.N + S::kCols - 1) / S::kCols, tiles = (p.T + 15) / 16;
+    const int64_t stages = (int64_t)tiles * across;
+    const int count = (int)((stages - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's
+    const int step_col = gridDim.x % across, step_tile = gridDim.x / across;
+    // the first stage's column and row tile, and the step to the next
+    const int col_first = blockIdx.x % across, tile_first = blockIdx.x / across;
+    auto advance = [&](int& col, int& tile) {
+        tile += step_tile;
+        if ((col += step_col) >= across) {
+            col -= across;
+            ++tile;
+        }
+    };
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int s = 0; s < kExpandStages; ++s) {
+        for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(ready0 + 8 * s, 8);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_map(&p.tm_base);
-        prefetch_map(&p.tm_out);
     }
     __syncthreads();
     if (warp == 8) {
-        if (lane == 0) {
-            // where the next load goes, and the next store
-            int load_x = col0, load_y = row0, load_s = 0, x = col0, y = row0, s = 0;
-            uint32_t phase = 0;
-            auto load = [&] {
-                mbar_arrive_expect_tx(full0 + 8 * load_s, kBoxBytes);
-                tma_load_2d(base + load_s * kBoxBytes, &p.tm_base, load_x, load_y, full0 + 8 * load_s);
-                if (++load_s == kExpandStages) load_s = 0;
-                if ((load_x += kBoxCols) == width) {
-                    load_x = 0;
-                    load_y += kBoxRows;
-                }
-            };
-            // base does not come from the kernel before this one, which lets
-            // this one start only after everything before it is done
-            for (int i = 0; i < min(count, kExpandStages); ++i) load();
-            bool ok = true;
-            for (int i = 0; i < count; ++i) {
-                ok = mbar_wait(ready0 + 8 * s, phase, abort_flag, p.lora.err, DERR_EPI_WAIT);
-                if (!ok) break;
-                tma_store_2d(&p.tm_out, x, y, base + s * kBoxBytes);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                // the store before this one has left its stage: fill it again
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                if (i > 0 && i - 1 + kExpandStages < count) load();
-                if ((x += kBoxCols) == width) {
-                    x = 0;
-                    y += kBoxRows;
-                }
-                if (++s == kExpandStages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            if (!ok) {  // loads still on their way land before this CTA may leave
-                const uint64_t t = global_timer();
-                while (global_timer() - t < 1000000ull) {}
+        // lane r < 16 copies row r
+        int load_col = col_first, load_tile = tile_first, load_s = 0, col = col_first, tile = tile_first, s = 0;
+        uint32_t phase = 0;
+        auto load = [&] {
+            const int bytes = 2 * min(S::kCols, p.N - load_col * S::kCols), t = load_tile * 16 + lane;
+            if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * load_s, bytes * min(16, p.T - load_tile * 16));
+            __syncwarp();
+            if (lane < 16 && t < p.T)
+                bulk_load(base + load_s * S::kStage + lane * S::kPitch,
+                          static_cast<const uint8_t*>(p.base) + 2 * (t * p.base_stride + (int64_t)load_col * S::kCols), bytes,
+                          full0 + 8 * load_s);
+            if (++load_s == S::kStages) load_s = 0;
+            advance(load_col, load_tile);
+        };
+        // base does not come from the kernel before this one, which lets
+        // this one start only after everything before it is done
+        for (int i = 0; i < min(count, S::kStages); ++i) load();
+        bool ok = true;
+        for (int i = 0; i < count; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait(ready0 + 8 * s, phase, abort_flag, p.err, DERR_EPI_WAIT));
+            if (!ok) break;
+            const int t = tile * 16 + lane;
+            if (lane < 16 && t < p.T)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 static_cast<uint8_t*>(p.out) + 2 * (t * p.out_stride + (int64_t)col * S::kCols)),
+                             "r"(base + s * S::kStage + lane * S::kPitch), "r"(2 * min(S::kCols, p.N - col * S::kCols))
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            // this lane's row of the stage before has left it: fill it again
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            if (i > 0 && i - 1 + S::kStages < count) load();
+            advance(col, tile);
+            if (++s == S::kStages) {
+                s = 0;
+                phase ^= 1u;
             }
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (!ok) {  // loads still on their way land before this CTA may leave
+            const uint64_t t = global_timer();
+            while (global_timer() - t < 1000000ull) {}
+        }
     } else {
-        const int r0 = 16 * (warp >> 2), c0 = 64 * (warp & 3);
-        const int rv = p.lora.R / 4;
+        const int rv = p.R / 4;
+        // this thread's first row and its chunk of the warp's first half
+        uint8_t* const chunk = mem + g * S::kPitch + warp * 64 * NH + q * 16;
         wait_for_previous_kernel();
-        uint32_t id[2] = {kNoAdapter, kNoAdapter}, phase = 0;
-        uint2 v[2][KS];
-        int x = col0, t = row0 + r0 + g, s = 0;  // the box's column, this thread's first row, the stage
-        for (int i = 0; i < count; ++i) {
-            const int n0 = x + c0;
-            if (i == 0 || x == 0) {  // new rows
+        int col = col_first, tile = tile_first, s = 0;
+        uint32_t phase = 0, held = kNoAdapter;
+        int held_col = -1;
+        uint2 bf[NH][KS][4];
+        uint32_t id_next[2];
+        uint2 v_next[2][KS];
+        auto fetch = [&](int tile_of) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    id[h] = adapter_of(p.lora, t + 8 * h, t + 8 * h < p.lora.T);
-                    const uint2* row = static_cast<const uint2*>(p.lora.ws) + (int64_t)(t + 8 * h) * rv + q;
+            for (int h = 0; h < 2; ++h) {
+                const int t = tile_of * 16 + 8 * h + g;
+                const bool in = t < p.T;
+                id_next[h] = adapter_of(p, t, in);
 #pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        v[h][k] = id[h] != kNoAdapter && k * 4 + q < rv ? row[k * 4] : make_uint2(0, 0);
-                }
+                for (int k = 0; k < KS; ++k)
+                    v_next[h][k] = in && k * 4 + q < rv ? static_cast<const uint2*>(p.ws)[(int64_t)t * rv + q + k * 4]
+                                                        : make_uint2(0, 0);
             }
-            uint32_t left[2] = {id[0], id[1]};
+        };
+        fetch(tile);
+        for (int i = 0; i < count; ++i) {
+            uint32_t id[2], left[2];
+            uint2 v[2][KS];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                left[h] = id[h] = id_next[h];
+#pragma unroll
+                for (int k = 0; k < KS; ++k) v[h][k] = v_next[h][k];
+            }
+            const int n0 = col * S::kCols + warp * 32 * NH;
+            const int col_now = col;
+            advance(col, tile);
+            if (i + 1 < count) fetch(tile);
             auto next = [&] {
                 const uint32_t m = __reduce_min_sync(0xffffffffu, min(left[0], left[1]));
                 if (left[0] == m) left[0] = kNoAdapter;
                 if (left[1] == m) left[1] = kNoAdapter;
                 return m;
             };
-            // the first adapter's B before the wait for the box
+            auto hold = [&](uint32_t a) {  // a's B in registers
+                if (a != kNoAdapter && (a != held || col_now != held_col)) {
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) Expand<KS>::load_b(p, a, n0 + 32 * h, lane, bf[h]);
+                    held = a;
+                    held_col = col_now;
+                }
+            };
             uint32_t cur = next();
-            uint2 bf[2][KS][4];
+            hold(cur);
+            if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, phase, abort_flag, p.err, DERR_MMA_FULL_WAIT))) break;
+            uint4* at = reinterpret_cast<uint4*>(chunk + s * S::kStage);
+            constexpr int kRow8 = 8 * S::kPitch / 16;
+            uint4 bs[NH][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) Expand<KS>::load_b(p.lora, cur, n0 + 32 * h, lane, bf[h]);
-            if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, phase, abort_flag, p.lora.err, DERR_MMA_FULL_WAIT))) break;
-            // row g (and g + 8) of this warp's rows, columns 8 q ... of each half
-            uint4* at = reinterpret_cast<uint4*>(mem + s * kBoxBytes + (r0 + g) * kBoxCols * 2 + c0 * 2) + q;
-            constexpr int kRow8 = 8 * kBoxCols * 2 / 16;
-            uint4 bs[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
                 bs[h][0] = at[4 * h];
                 bs[h][1] = at[4 * h + kRow8];
             }
             while (cur != kNoAdapter) {
-                const uint32_t then = next();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < NH; ++h) {
                     float d[4][4];
                     Expand<KS>::product(bs[h], v, bf[h], d);
-                    if (then != kNoAdapter) Expand<KS>::load_b(p.lora, then, n0 + 32 * h, lane, bf[h]);
                     if (id[0] == cur) at[4 * h] = Expand<KS>::round(d, 0);
                     if (id[1] == cur) at[4 * h + kRow8] = Expand<KS>::round(d, 1);
                 }
-                cur = then;
+                cur = next();
+                hold(cur);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(ready0 + 8 * s);
-            if ((x += kBoxCols) == width) {
-                x = 0;
-                t += kBoxRows;
-            }
-            if (++s == kExpandStages) {
+            if (++s == S::kStages) {
                 s = 0;
                 phase ^= 1u;
             }
@@ -409,17 +439,20 @@ __global__ void __launch_bounds__(kExpandThreads, KS <= 2 ? 2 : 1) lora_expand_t
 }
 
 template <int KS>
-cudaError_t launch_expand(const LoraTcArgs& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(lora_expand_tc_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
+cudaError_t launch_expand(const LoraArgs& p, cudaStream_t s) {
+    using S = ExpandSmem<KS>;
+    cudaError_t e = cudaFuncSetAttribute(lora_expand_tc_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (e != cudaSuccess) return e;
-    const int64_t boxes = (int64_t)((p.lora.T + kBoxRows - 1) / kBoxRows) * ((p.lora.N + kBoxCols - 1) / kBoxCols);
+    const int64_t across = (p.N + S::kCols - 1) / S::kCols, stages = (p.T + 15) / 16 * across;
+    int64_t grid = S::kPerSm * p.n_sms;
+    if (across <= grid) grid = grid / across * across;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)std::min<int64_t>(boxes, (KS <= 2 ? 2 : 1) * p.lora.n_sms));
+    c.gridDim = dim3((unsigned)std::min(stages, grid));
     c.blockDim = dim3(kExpandThreads);
-    c.dynamicSmemBytes = kExpandSmem;
+    c.dynamicSmemBytes = S::kBytes;
     c.stream = s;
     c.attrs = &at;
     c.numAttrs = 1;
@@ -444,8 +477,8 @@ cudaError_t launch_lora_tc(const LoraTcArgs& p, cudaStream_t s) {
     const cudaError_t e = R <= 16 ? launch_shrink<16>(p, s) : R <= 32 ? launch_shrink<32>(p, s)
                           : R <= 64 ? launch_shrink<64>(p, s) : launch_shrink<128>(p, s);
     if (e != cudaSuccess) return e;
-    return R <= 16 ? launch_expand<1>(p, s) : R <= 32 ? launch_expand<2>(p, s) : R <= 64 ? launch_expand<4>(p, s)
-                                                                                      : launch_expand<8>(p, s);
+    return R <= 16 ? launch_expand<1>(p.lora, s) : R <= 32 ? launch_expand<2>(p.lora, s)
+           : R <= 64 ? launch_expand<4>(p.lora, s) : launch_expand<8>(p.lora, s);
 }
 
 }  // namespace dwdp
