@@ -259,13 +259,19 @@ cudaError_t launch_shrink(const LoraTcArgs& p, cudaStream_t s) {
 
 // ---------------------------------------------------------------- expand --
 // A stage holds 16 rows of base, kCols columns of each, fetched and put back
-// row by row (bulk copies of up to 1 KB; a multiple of 16 bytes, since rows
-// and N are).  The pitch of 64 bytes more keeps a warp's 16-byte accesses to
+// row by row (bulk copies of up to 896 bytes; a multiple of 16, since rows and
+// N are).  The pitch of 64 bytes more keeps a warp's 16-byte accesses to
 // neighbouring rows in different banks.
+// 7 warps of arithmetic and 1 of copies: with two CTAs an SM 128 registers a
+// thread, which the arithmetic needs (8 + 1 warps spill at 96: 51 us for
+// 8192 x 7168 instead of 46; the copies alone take 40).
+constexpr int kExpandWarps = 7;
+constexpr int kExpandThreads = 32 * (kExpandWarps + 1);
+
 template <int KS>
 struct ExpandSmem {
     static constexpr int kHalves = KS <= 4 ? 2 : 1;  // 32-column halves a warp holds B for
-    static constexpr int kCols = 8 * 32 * kHalves;
+    static constexpr int kCols = kExpandWarps * 32 * kHalves;
     static constexpr int kPitch = kCols * 2 + 64;
     static constexpr int kStage = 16 * kPitch;
     static constexpr int kPerSm = KS <= 2 ? 2 : 1;
@@ -273,13 +279,10 @@ struct ExpandSmem {
     static constexpr int kBars = kStages * kStage;  // full[S], ready[S]
     static constexpr int kBytes = kBars + 16 * kStages + 16;
 };
-constexpr int kExpandThreads = 288;  // 8 warps of arithmetic, 1 of copies
-
-// Staying CTAs: CTA c takes the stages c, c + G, ... in the order of memory,
-// so what the GPU works on at one time lies close together (8192 x 7168 bf16
-// in and out: a copy in this order 37 us, with a run of stages per CTA 41,
-// with pieces of 512 bytes 51).  G is a multiple of the stages across a row:
-// a CTA stays in its columns, and B stays in registers while the adapter does.
+// Staying CTAs: the grid is groups of as many CTAs as stages lie across a row;
+// CTA c of group j takes column c of the group's row tiles, one after the
+// other, so that what a group works on at one time lies together in memory and
+// B stays in registers while the adapter does.
 template <int KS>
 __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
     lora_expand_tc_kernel(const __grid_constant__ LoraArgs p) {
@@ -290,60 +293,47 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(mem + S::kBars + 16 * S::kStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int across = (p.N + S::kCols - 1) / S::kCols, tiles = (p.T + 15) / 16;
-    const int64_t stages = (int64_t)tiles * across;
-    const int count = (int)((stages - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's
-    const int step_col = gridDim.x % across, step_tile = gridDim.x / across;
-    // the first stage's column and row tile, and the step to the next
-    const int col_first = blockIdx.x % across, tile_first = blockIdx.x / across;
-    auto advance = [&](int& col, int& tile) {
-        tile += step_tile;
-        if ((col += step_col) >= across) {
-            col -= across;
-            ++tile;
-        }
-    };
+    const int groups = gridDim.x / across, group = blockIdx.x / across, col = blockIdx.x % across;
+    const int tile0 = (int)((int64_t)tiles * group / groups), tile1 = (int)((int64_t)tiles * (group + 1) / groups);
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(ready0 + 8 * s, 8);
+            mbar_init(ready0 + 8 * s, kExpandWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    if (warp == 8) {
-        // lane r < 16 copies row r
-        int load_col = col_first, load_tile = tile_first, load_s = 0, col = col_first, tile = tile_first, s = 0;
+    if (warp == kExpandWarps) {
+        // lane r < 16 copies row r of a tile
+        const int bytes = 2 * min(S::kCols, p.N - col * S::kCols);
+        const uint8_t* src = static_cast<const uint8_t*>(p.base) + 2 * (lane * p.base_stride + (int64_t)col * S::kCols);
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + 2 * (lane * p.out_stride + (int64_t)col * S::kCols);
+        int load_s = 0, s = 0;
         uint32_t phase = 0;
-        auto load = [&] {
-            const int bytes = 2 * min(S::kCols, p.N - load_col * S::kCols), t = load_tile * 16 + lane;
-            if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * load_s, bytes * min(16, p.T - load_tile * 16));
+        auto load = [&](int tile) {
+            if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * load_s, bytes * min(16, p.T - tile * 16));
             __syncwarp();
-            if (lane < 16 && t < p.T)
-                bulk_load(base + load_s * S::kStage + lane * S::kPitch,
-                          static_cast<const uint8_t*>(p.base) + 2 * (t * p.base_stride + (int64_t)load_col * S::kCols), bytes,
+            if (lane < 16 && tile * 16 + lane < p.T)
+                bulk_load(base + load_s * S::kStage + lane * S::kPitch, src + 32 * tile * p.base_stride, bytes,
                           full0 + 8 * load_s);
             if (++load_s == S::kStages) load_s = 0;
-            advance(load_col, load_tile);
         };
         // base does not come from the kernel before this one, which lets
         // this one start only after everything before it is done
-        for (int i = 0; i < min(count, S::kStages); ++i) load();
+        for (int tile = tile0; tile < min(tile1, tile0 + S::kStages); ++tile) load(tile);
         bool ok = true;
-        for (int i = 0; i < count; ++i) {
+        for (int tile = tile0; tile < tile1; ++tile) {
             ok = __all_sync(0xffffffffu, mbar_wait(ready0 + 8 * s, phase, abort_flag, p.err, DERR_EPI_WAIT));
             if (!ok) break;
-            const int t = tile * 16 + lane;
-            if (lane < 16 && t < p.T)
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                 static_cast<uint8_t*>(p.out) + 2 * (t * p.out_stride + (int64_t)col * S::kCols)),
-                             "r"(base + s * S::kStage + lane * S::kPitch), "r"(2 * min(S::kCols, p.N - col * S::kCols))
+            if (lane < 16 && tile * 16 + lane < p.T)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + 32 * tile * p.out_stride),
+                             "r"(base + s * S::kStage + lane * S::kPitch), "r"(bytes)
                              : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            // this lane's row of the stage before has left it: fill it again
+            // this lane's row of the tile before has left its stage: fill it again
             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            if (i > 0 && i - 1 + S::kStages < count) load();
-            advance(col, tile);
+            if (tile > tile0 && tile - 1 + S::kStages < tile1) load(tile - 1 + S::kStages);
             if (++s == S::kStages) {
                 s = 0;
                 phase ^= 1u;
@@ -358,17 +348,17 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
         const int rv = p.R / 4;
         // this thread's first row and its chunk of the warp's first half
         uint8_t* const chunk = mem + g * S::kPitch + warp * 64 * NH + q * 16;
+        const int n0 = col * S::kCols + warp * 32 * NH;  // this warp's first column
         wait_for_previous_kernel();
-        int col = col_first, tile = tile_first, s = 0;
+        int s = 0;
         uint32_t phase = 0, held = kNoAdapter;
-        int held_col = -1;
         uint2 bf[NH][KS][4];
         uint32_t id_next[2];
         uint2 v_next[2][KS];
-        auto fetch = [&](int tile_of) {
+        auto fetch = [&](int tile) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int t = tile_of * 16 + 8 * h + g;
+                const int t = tile * 16 + 8 * h + g;
                 const bool in = t < p.T;
                 id_next[h] = adapter_of(p, t, in);
 #pragma unroll
@@ -377,8 +367,8 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
                                                         : make_uint2(0, 0);
             }
         };
-        fetch(tile);
-        for (int i = 0; i < count; ++i) {
+        fetch(tile0);
+        for (int tile = tile0; tile < tile1; ++tile) {
             uint32_t id[2], left[2];
             uint2 v[2][KS];
 #pragma unroll
@@ -387,10 +377,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
 #pragma unroll
                 for (int k = 0; k < KS; ++k) v[h][k] = v_next[h][k];
             }
-            const int n0 = col * S::kCols + warp * 32 * NH;
-            const int col_now = col;
-            advance(col, tile);
-            if (i + 1 < count) fetch(tile);
+            if (tile + 1 < tile1) fetch(tile + 1);
             auto next = [&] {
                 const uint32_t m = __reduce_min_sync(0xffffffffu, min(left[0], left[1]));
                 if (left[0] == m) left[0] = kNoAdapter;
@@ -398,11 +385,10 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
                 return m;
             };
             auto hold = [&](uint32_t a) {  // a's B in registers
-                if (a != kNoAdapter && (a != held || col_now != held_col)) {
+                if (a != kNoAdapter && a != held) {
 #pragma unroll
                     for (int h = 0; h < NH; ++h) Expand<KS>::load_b(p, a, n0 + 32 * h, lane, bf[h]);
                     held = a;
-                    held_col = col_now;
                 }
             };
             uint32_t cur = next();
@@ -443,14 +429,13 @@ cudaError_t launch_expand(const LoraArgs& p, cudaStream_t s) {
     using S = ExpandSmem<KS>;
     cudaError_t e = cudaFuncSetAttribute(lora_expand_tc_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (e != cudaSuccess) return e;
-    const int64_t across = (p.N + S::kCols - 1) / S::kCols, stages = (p.T + 15) / 16 * across;
-    int64_t grid = S::kPerSm * p.n_sms;
-    if (across <= grid) grid = grid / across * across;
+    const int across = (p.N + S::kCols - 1) / S::kCols;
+    const int groups = std::min((p.T + 15) / 16, std::max(1, S::kPerSm * p.n_sms / across));
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)std::min(stages, grid));
+    c.gridDim = dim3(groups * across);
     c.blockDim = dim3(kExpandThreads);
     c.dynamicSmemBytes = S::kBytes;
     c.stream = s;
