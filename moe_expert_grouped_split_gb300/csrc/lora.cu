@@ -14,7 +14,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "dwdp_internal.h"
 #include "lora_ops.h"
@@ -27,11 +26,11 @@ constexpr uint32_t kNone = kNoAdapter;  // a row without an adapter
 constexpr int kThreads = 256;
 constexpr int kCluster = 8;
 
-// x rows of one warp against A_i: TW x KW warps, MT m16 tiles a warp; NT
-// n8 tiles hold the rank.  A step is 32 elements of K.
-template <int NT, int TW, int KW, int MT>
+// 16 x rows of one warp against A_i: TW x KW warps; NT n8 tiles hold the rank.
+// A step is 32 elements of K.
+template <int NT, int TW, int KW>
 struct Shrink {
-    static constexpr int kRows = TW * MT * 16;
+    static constexpr int kRows = TW * 16;
     static constexpr int kTile = kRows * NT * 8;
     static constexpr int kSmem = (KW + 1) * kTile * 4;
 
@@ -41,82 +40,76 @@ struct Shrink {
     // none adapter 0, a row of A beyond R the last one, and nothing of them
     // is used.
     template <int G, int U>
-    static __device__ __forceinline__ void pass(const LoraArgs& p, const uint4* const (&xr)[2 * MT],
+    static __device__ __forceinline__ void pass(const LoraArgs& p, const uint4* const (&xr)[2],
                                                 const uint32_t (&cur)[G], int step0, int step1, int lane,
-                                                const uint32_t (&id)[2 * MT], float* part) {
+                                                const uint32_t (&id)[2], float* part) {
         const int g = lane >> 2, q = lane & 3, kv = p.K / 8;
-        float acc[G][MT][NT][4] = {};
-        const uint4* xp[2 * MT];
+        float acc[G][NT][4] = {};
+        const uint4* xp[2];
         const uint4* ap[G][NT];
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) xp[i] = xr[i] + step0 * 4 + q;
+        for (int i = 0; i < 2; ++i) xp[i] = xr[i] + step0 * 4 + q;
 #pragma unroll
         for (int s = 0; s < G; ++s)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 ap[s][j] = static_cast<const uint4*>(p.a) +
                            ((int64_t)(cur[s] == kNone ? 0 : cur[s]) * p.R + min(j * 8 + g, p.R - 1)) * kv + step0 * 4 + q;
-        // n steps from `at`; `last`: the row's end may lie within them
-        auto steps = [&](auto count, int at, bool last) {
-            constexpr int N = decltype(count)::value;
-            uint4 xv[N][2 * MT], av[N][G][NT];
+        // U steps from `at`; `last`: the part's or the row's end may lie within them
+        auto steps = [&](int at, bool last) {
+            uint4 xv[U][2], av[U][G][NT];
 #pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const bool in = !last || (at + u) * 4 + q < kv;
+            for (int u = 0; u < U; ++u) {
+                const bool in = !last || (at + u < step1 && (at + u) * 4 + q < kv);
 #pragma unroll
                 for (int s = 0; s < G; ++s)
 #pragma unroll
                     for (int j = 0; j < NT; ++j) av[u][s][j] = in ? __ldg(ap[s][j] + 4 * u) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) xv[u][i] = in ? __ldg(xp[i] + 4 * u) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 2; ++i) xv[u][i] = in ? __ldg(xp[i] + 4 * u) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int u = 0; u < N; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < G; ++s)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                    for (int j = 0; j < NT; ++j) {
+                        const uint4 &lo = xv[u][0], &hi = xv[u][1], &b = av[u][s][j];
+                        mma16816(acc[s][j], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+                        mma16816(acc[s][j], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+                    }
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const uint4 &lo = xv[u][2 * m], &hi = xv[u][2 * m + 1], &b = av[u][s][j];
-                            mma16816(acc[s][m][j], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-                            mma16816(acc[s][m][j], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-                        }
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) xp[i] += 4 * N;
+            for (int i = 0; i < 2; ++i) xp[i] += 4 * U;
 #pragma unroll
             for (int s = 0; s < G; ++s)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) ap[s][j] += 4 * N;
+                for (int j = 0; j < NT; ++j) ap[s][j] += 4 * U;
         };
-        const int whole = min(step1, kv / 4);  // steps that lie wholly in the row
-        int st = step0;
-        for (; st + U <= whole; st += U) steps(std::integral_constant<int, U>(), st, false);
-        for (; st < step1; ++st) steps(std::integral_constant<int, 1>(), st, st >= whole);
+        const int whole = min(step1, kv / 4);  // steps that lie wholly in the part and the row
+#pragma unroll 1
+        for (int st = step0; st < step1; st += U) steps(st, st + U > whole);
 #pragma unroll
         for (int s = 0; s < G; ++s)
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i)
+            for (int i = 0; i < 2; ++i)
                 if (id[i] != kNone && id[i] == cur[s]) {
-                    float* row = part + ((i >> 1) * 16 + (i & 1) * 8 + g) * NT * 8 + 2 * q;
+                    float* row = part + (i * 8 + g) * NT * 8 + 2 * q;
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
-                        *reinterpret_cast<float2*>(row + j * 8) =
-                            make_float2(acc[s][i >> 1][j][2 * (i & 1)], acc[s][i >> 1][j][2 * (i & 1) + 1]);
+                        *reinterpret_cast<float2*>(row + j * 8) = make_float2(acc[s][j][2 * i], acc[s][j][2 * i + 1]);
                 }
     }
 };
 
-template <int NT, int TW, int KW, int MT>
-__global__ void __launch_bounds__(kThreads, MT > 1 ? 2 : 1) __cluster_dims__(kCluster, 1, 1)
+template <int NT, int TW, int KW>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     lora_shrink_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
     static_assert(TW * KW * 32 == kThreads, "one warp per (token part, K part)");
-    using S = Shrink<NT, TW, KW, MT>;
+    using S = Shrink<NT, TW, KW>;
     // adapters a mixed pass takes at once, and steps in flight with one and
-    // with several: what the registers hold (two blocks an SM for MT = 2)
-    constexpr int G = MT > 1 ? (NT <= 2 ? 2 : 1) : NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
-    constexpr int U1 = MT > 1 ? (NT <= 2 ? 2 : 1) : NT <= 2 ? 4 : NT <= 8 ? 2 : 1;
-    constexpr int UG = MT > 1 ? 1 : NT <= 2 ? 4 : 2;
+    // with several: what the registers hold
+    constexpr int G = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
+    constexpr int U1 = NT <= 2 ? 4 : NT <= 8 ? 2 : 1, UG = NT <= 2 ? 4 : 2;
     extern __shared__ float part[];  // [KW][rows][NT * 8], then what the cluster sends [8][this rank's eighth]
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -126,11 +119,11 @@ __global__ void __launch_bounds__(kThreads, MT > 1 ? 2 : 1) __cluster_dims__(kCl
     const int t0 = (int)(blockIdx.x / kCluster) * tile_rows;
     const uint32_t rank = cluster_rank();
     // this warp's rows
-    uint32_t id[2 * MT], left[2 * MT];
-    const uint4* xr[2 * MT];
+    uint32_t id[2], left[2];
+    const uint4* xr[2];
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-        const int r = tw * MT * 16 + (i >> 1) * 16 + (i & 1) * 8 + g, t = t0 + r;
+    for (int i = 0; i < 2; ++i) {
+        const int r = tw * 16 + i * 8 + g, t = t0 + r;
         const bool in = r < tile_rows && t < p.T;
         left[i] = id[i] = adapter_of(p, t, in);
         xr[i] = static_cast<const uint4*>(p.x) + (int64_t)(in ? t : t0) * (p.x_stride / 8);
@@ -138,16 +131,12 @@ __global__ void __launch_bounds__(kThreads, MT > 1 ? 2 : 1) __cluster_dims__(kCl
     }
     const int steps = (p.K + 31) / 32, at = (int)rank * KW + kw;
     const int step0 = steps * at / (kCluster * KW), step1 = steps * (at + 1) / (kCluster * KW);
-    float* mine = part + kw * S::kTile + tw * MT * 16 * NT * 8;
+    float* mine = part + kw * S::kTile + tw * 16 * NT * 8;
     // the lowest adapter among the rows not done yet
     auto next = [&] {
-        uint32_t m = kNone;
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) m = min(m, left[i]);
-        m = __reduce_min_sync(kFull, m);
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i)
-            if (left[i] == m) left[i] = kNone;
+        const uint32_t m = __reduce_min_sync(kFull, min(left[0], left[1]));
+        if (left[0] == m) left[0] = kNone;
+        if (left[1] == m) left[1] = kNone;
         return m;
     };
     uint32_t a0 = next();
@@ -328,24 +317,22 @@ cudaError_t launch(const void* kernel, dim3 grid, size_t smem, cudaStream_t s, c
     return cudaLaunchKernelExC(&c, kernel, args);
 }
 
-template <int NT, int TW, int KW, int MT>
+template <int NT, int TW, int KW>
 cudaError_t launch_shrink(const LoraArgs& p, int rows, cudaStream_t s) {
-    return launch((const void*)lora_shrink_kernel<NT, TW, KW, MT>, dim3((p.T + rows - 1) / rows * kCluster),
-                  Shrink<NT, TW, KW, MT>::kSmem, s, p, rows);
+    return launch((const void*)lora_shrink_kernel<NT, TW, KW>, dim3((p.T + rows - 1) / rows * kCluster),
+                  Shrink<NT, TW, KW>::kSmem, s, p, rows);
 }
 
 template <int NT>
 cudaError_t launch_rank(const LoraArgs& p, cudaStream_t s) {
     // shrink: the smallest tiles whose clusters still fit the GPU at once
-    // (then few tokens meet a block, with the most parts of K), or large ones
-    auto fits = [&](int rows) { return (int64_t)((p.T + rows - 1) / rows) * kCluster <= p.n_sms; };
+    // (then few tokens meet a block, with the most parts of K)
     int rows = 1;
-    while (rows < 64 && !fits(rows)) rows *= 2;
+    while (rows < 64 && (int64_t)((p.T + rows - 1) / rows) * kCluster > p.n_sms) rows *= 2;
     cudaError_t e;
-    if (rows <= 16) e = launch_shrink<NT, 1, 8, 1>(p, rows, s);
-    else if (rows == 32) e = launch_shrink<NT, 2, 4, 1>(p, rows, s);
-    else if (fits(rows) || NT > 8) e = launch_shrink<NT, 4, 2, 1>(p, rows, s);
-    else e = launch_shrink<NT, 4, 2, NT <= 8 ? 2 : 1>(p, NT <= 8 ? 128 : 64, s);
+    if (rows <= 16) e = launch_shrink<NT, 1, 8>(p, rows, s);
+    else if (rows == 32) e = launch_shrink<NT, 2, 4>(p, rows, s);
+    else e = launch_shrink<NT, 4, 2>(p, rows, s);
     if (e != cudaSuccess) return e;
     // expand: 64 tokens a warp where that leaves every SM two blocks
     constexpr int KS = NT / 2;
