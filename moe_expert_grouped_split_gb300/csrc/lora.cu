@@ -3,8 +3,8 @@
 // adapter.  Memory-bound: x, base, out and the used adapters once.
 //
 // Two kernels, v = bf16(s_i x A_i^T) [T][R] between them:
-//   shrink  clusters of 8 CTAs per token tile, each CTA a part of K; the
-//           parts meet in distributed shared memory, in rank order
+//   shrink  a cluster of 2 to 8 CTAs per tile of up to 16 tokens, each warp a
+//           part of K; the parts meet in distributed shared memory, in order
 //   expand  token tile x 256 columns per CTA, base and out in 16-byte vectors
 // Both take 16 tokens at a time against each adapter that occurs among them
 // (mma m16n8k16) and give every row its own adapter's result, so tokens may
@@ -12,8 +12,6 @@
 // A step is at most 2 R flops a byte of x: far from the tensor rate, so the
 // warp-level MMA on operands straight from global memory is enough.
 #include <cuda_bf16.h>
-
-#include <algorithm>
 
 #include "dwdp_internal.h"
 #include "lora_ops.h"
@@ -24,15 +22,14 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kNone = kNoAdapter;  // a row without an adapter
 constexpr int kThreads = 256;
-constexpr int kCluster = 8;
+constexpr int kWarps = kThreads / 32;
 
-// 16 x rows of one warp against A_i: TW x KW warps; NT n8 tiles hold the rank.
-// A step is 32 elements of K.
-template <int NT, int TW, int KW>
+// 16 rows of x against A_i: a cluster of C blocks of 8 warps, each warp a part
+// of K; NT n8 tiles hold the rank.  A step is 32 elements of K.
+template <int NT, int C>
 struct Shrink {
-    static constexpr int kRows = TW * 16;
-    static constexpr int kTile = kRows * NT * 8;
-    static constexpr int kSmem = (KW + 1) * kTile * 4;
+    static constexpr int kTile = 16 * NT * 8;
+    static constexpr int kSmem = (kWarps + 1) * kTile * 4;
 
     // G adapters against the warp's rows, one reading of x, U steps' loads in
     // flight.  Loads are in bounds without a predicate: a row without an
@@ -101,37 +98,35 @@ struct Shrink {
     }
 };
 
-template <int NT, int TW, int KW>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+template <int NT, int C>
+__global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) __cluster_dims__(C, 1, 1)
     lora_shrink_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
-    static_assert(TW * KW * 32 == kThreads, "one warp per (token part, K part)");
-    using S = Shrink<NT, TW, KW>;
+    using S = Shrink<NT, C>;
     // adapters a mixed pass takes at once, and steps in flight with one and
     // with several: what the registers hold
     constexpr int G = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
-    constexpr int U1 = NT <= 2 ? 4 : NT <= 8 ? 2 : 1, UG = NT <= 2 ? 4 : 2;
-    extern __shared__ float part[];  // [KW][rows][NT * 8], then what the cluster sends [8][this rank's eighth]
+    constexpr int U1 = NT <= 2 ? 4 : NT <= 8 ? 2 : 1, UG = 2;
+    extern __shared__ float part[];  // [warps][16][NT * 8], then what the cluster sends [C][this rank's share]
     wait_for_previous_kernel();
     let_next_kernel_start();
     cluster_arrive();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int tw = warp % TW, kw = warp / TW;
-    const int t0 = (int)(blockIdx.x / kCluster) * tile_rows;
+    const int t0 = (int)(blockIdx.x / C) * tile_rows;
     const uint32_t rank = cluster_rank();
     // this warp's rows
     uint32_t id[2], left[2];
     const uint4* xr[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = tw * 16 + i * 8 + g, t = t0 + r;
+        const int r = i * 8 + g, t = t0 + r;
         const bool in = r < tile_rows && t < p.T;
         left[i] = id[i] = adapter_of(p, t, in);
         xr[i] = static_cast<const uint4*>(p.x) + (int64_t)(in ? t : t0) * (p.x_stride / 8);
-        if (rank == 0 && kw == 0 && in && id[i] == kNone && p.ids[t] != -1) atomicOr(p.err, DERR_BAD_INDEX);
+        if (rank == 0 && warp == 0 && in && id[i] == kNone && p.ids[t] != -1) atomicOr(p.err, DERR_BAD_INDEX);
     }
-    const int steps = (p.K + 31) / 32, at = (int)rank * KW + kw;
-    const int step0 = steps * at / (kCluster * KW), step1 = steps * (at + 1) / (kCluster * KW);
-    float* mine = part + kw * S::kTile + tw * 16 * NT * 8;
+    const int steps = (p.K + 31) / 32, at = (int)rank * kWarps + warp;
+    const int step0 = steps * at / (C * kWarps), step1 = steps * (at + 1) / (C * kWarps);
+    float* mine = part + warp * S::kTile;
     // the lowest adapter among the rows not done yet
     auto next = [&] {
         const uint32_t m = __reduce_min_sync(kFull, min(left[0], left[1]));
@@ -155,30 +150,30 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
             a0 = next();
         }
     }
-    // the K parts of the block, then of the cluster: rank e / kEighth gets
+    // the K parts of the block, then of the cluster: rank e / kShare gets
     // element e of every rank, and adds them in order
-    constexpr int kEighth = S::kTile / kCluster;
-    float* sent = part + KW * S::kTile;
+    constexpr int kShare = S::kTile / C;
+    float* sent = part + kWarps * S::kTile;
     __syncthreads();
     cluster_wait();  // everybody runs: its shared memory may be written
     for (int e = threadIdx.x; e < S::kTile; e += kThreads) {
         float s = part[e];
 #pragma unroll
-        for (int w = 1; w < KW; ++w) s += part[w * S::kTile + e];
-        store_to_rank(sent + rank * kEighth + e % kEighth, e / kEighth, s);
+        for (int w = 1; w < kWarps; ++w) s += part[w * S::kTile + e];
+        store_to_rank(sent + rank * kShare + e % kShare, e / kShare, s);
     }
     __syncwarp();
     cluster_arrive();
     cluster_wait();
     __nv_bfloat16* v = static_cast<__nv_bfloat16*>(p.ws);
-    for (int i = threadIdx.x; i < kEighth; i += kThreads) {
-        const int e = (int)rank * kEighth + i, r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
+    for (int i = threadIdx.x; i < kShare; i += kThreads) {
+        const int e = (int)rank * kShare + i, r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
         if (r >= tile_rows || c >= p.R) continue;
         const uint32_t a = adapter_of(p, t, t < p.T);
         if (a == kNone) continue;
         float s = sent[i];
 #pragma unroll
-        for (int k = 1; k < kCluster; ++k) s += sent[k * kEighth + i];
+        for (int k = 1; k < C; ++k) s += sent[k * kShare + i];
         v[(int64_t)t * p.R + c] = __float2bfloat16_rn(s * p.scale[a]);
     }
 }
@@ -188,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
 template <int KS, int MT>
 __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
     using X = Expand<KS>;
-    constexpr int G = MT > 1 ? 1 : KS <= 1 ? 4 : KS <= 2 ? 2 : 1;  // adapters whose B is loaded together
+    constexpr int G = MT > 1 || KS > 1 ? 1 : 2;  // adapters whose B is loaded together
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int t0 = (int)blockIdx.x * tile_rows, c0 = ((int)blockIdx.y * (kThreads / 32) + warp) * 32;
     if (c0 >= p.N) return;  // a whole warp beyond the columns
@@ -317,29 +312,32 @@ cudaError_t launch(const void* kernel, dim3 grid, size_t smem, cudaStream_t s, c
     return cudaLaunchKernelExC(&c, kernel, args);
 }
 
-template <int NT, int TW, int KW>
+template <int NT, int C>
 cudaError_t launch_shrink(const LoraArgs& p, int rows, cudaStream_t s) {
-    return launch((const void*)lora_shrink_kernel<NT, TW, KW>, dim3((p.T + rows - 1) / rows * kCluster),
-                  Shrink<NT, TW, KW>::kSmem, s, p, rows);
+    return launch((const void*)lora_shrink_kernel<NT, C>, dim3((p.T + rows - 1) / rows * C), Shrink<NT, C>::kSmem, s, p,
+                  rows);
 }
 
 template <int NT>
 cudaError_t launch_rank(const LoraArgs& p, cudaStream_t s) {
-    // shrink: the smallest tiles whose clusters still fit the GPU at once
-    // (then few tokens meet a block, with the most parts of K)
+    // shrink: the smallest tiles, then the fewest parts of K, whose clusters
+    // fit the GPU at once with a block per SM (a cluster that has to wait for
+    // another one's end costs more: 128 tokens of one adapter, rank 16, 8.0 us
+    // so, 5.1 us in one round).  Blocks of 8-block clusters that cannot share
+    // an SM (rank above 64) leave a fifth of the SMs in the gaps.
+    auto fits = [&](int rows, int C) {
+        return (int64_t)((p.T + rows - 1) / rows) * C <= p.n_sms * (NT == 16 && C == 8 ? 4 : 5) / 5;
+    };
     int rows = 1;
-    while (rows < 64 && (int64_t)((p.T + rows - 1) / rows) * kCluster > p.n_sms) rows *= 2;
-    cudaError_t e;
-    if (rows <= 16) e = launch_shrink<NT, 1, 8>(p, rows, s);
-    else if (rows == 32) e = launch_shrink<NT, 2, 4>(p, rows, s);
-    else e = launch_shrink<NT, 4, 2>(p, rows, s);
+    while (rows < 16 && !fits(rows, 8)) rows *= 2;
+    const cudaError_t e = fits(rows, 8) ? launch_shrink<NT, 8>(p, rows, s)
+                          : fits(rows, 4) ? launch_shrink<NT, 4>(p, rows, s) : launch_shrink<NT, 2>(p, rows, s);
     if (e != cudaSuccess) return e;
     // expand: 64 tokens a warp where that leaves every SM two blocks
     constexpr int KS = NT / 2;
     const int cols = (p.N + 255) / 256;
     if ((int64_t)((p.T + 63) / 64) * cols >= 2 * p.n_sms)
         return launch((const void*)lora_expand_kernel<KS, 4>, dim3((p.T + 63) / 64, cols), 0, s, p, 64);
-    rows = std::min(rows, 16);
     return launch((const void*)lora_expand_kernel<KS, 1>, dim3((p.T + rows - 1) / rows, cols), 0, s, p, rows);
 }
 

@@ -36,7 +36,9 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
                         float* __restrict__ z, int32_t* __restrict__ zero, int64_t n_zero) {
     static_assert(MW * NW * KW == kWarps, "");
     constexpr int kRows = MW * MT * 16, kCols = NW * NT * 8, kTile = kRows * kCols;
+    constexpr int kShare = kTile / kCluster;
     __shared__ __align__(16) float part[KW][kTile];
+    __shared__ float sent[kCluster][kShare];  // what the cluster's ranks send of this one's share
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int mw = warp % MW, nw = warp / MW % NW, kw = warp / (MW * NW);
     const int rank = blockIdx.x % kCluster;
@@ -47,6 +49,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     const int step0 = steps * at / (kCluster * KW), step1 = steps * (at + 1) / (kCluster * KW);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const int64_t blocks = (int64_t)gridDim.x * gridDim.y, block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     for (int64_t i = block * kThreads + threadIdx.x; i < n_zero; i += blocks * kThreads) zero[i] = 0;
     float acc[MT][NT][4] = {};
@@ -86,35 +89,28 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
             for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<float2*>(&part[kw][(tw - t0 + m * 16 + h * 8 + g) * kCols + ew - e0 + j * 8 + 2 * q]) =
                     make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-    if constexpr (KW > 1) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTile; i += kThreads) {
-            float s = part[0][i];
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // everybody runs: may be written to
+    for (int i = threadIdx.x; i < kTile; i += kThreads) {
+        float s = part[0][i];
 #pragma unroll
-            for (int v = 1; v < KW; ++v) s += part[v][i];
-            part[0][i] = s;
-        }
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    for (int i = rank * (kTile / kCluster) + threadIdx.x; i < (rank + 1) * (kTile / kCluster); i += kThreads) {
-        const uint32_t here = (uint32_t)__cvta_generic_to_shared(&part[0][i]);
-        float s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kCluster; ++c) {
-            uint32_t there;
-            float v;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(c));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
-            s += v;
-        }
-        const int t = t0 + i / kCols, e = e0 + i % kCols;
-        if (t < T && e < E) z[(int64_t)t * E + e] = s;
+        for (int v = 1; v < KW; ++v) s += part[v][i];
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"((uint32_t)__cvta_generic_to_shared(&sent[rank][i % kShare])), "r"(i / kShare));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(s) : "memory");
     }
     __syncwarp();
-    // nobody leaves while another rank may still read its shared memory
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int i = threadIdx.x; i < kShare; i += kThreads) {
+        float s = sent[0][i];
+#pragma unroll
+        for (int c = 1; c < kCluster; ++c) s += sent[c][i];
+        const int at = rank * kShare + i, t = t0 + at / kCols, e = e0 + at % kCols;
+        if (t < T && e < E) z[(int64_t)t * E + e] = s;
+    }
 }
 
 template <int MW, int NW, int KW, int MT, int NT, int U>

@@ -133,6 +133,13 @@ CASES = [
     (700, 7168, 512, 8, how_of(SIG, 8, 4, B.GROUP_TOP2), True),
     (33, 64, 7, 3, how_of(SOFT, 7, 3, B.GROUP_MAX), False),
     (1100, 7168, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (1024, 64, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),     # the most pairs one kernel takes
+    (1025, 64, 256, 8, how_of(SIG, 8, 4, B.GROUP_TOP2, True, 2.5), True),
+    (256, 64, 1024, 32, how_of(SOFT), True),
+    (257, 64, 1024, 32, how_of(SOFT, 16, 9, B.GROUP_TOP2), True),
+    (8191, 64, 48, 1, how_of(SIG, 3, 1, B.GROUP_MAX), True),
+    (8193, 64, 48, 1, how_of(SIG, 3, 1, B.GROUP_MAX), True),
+    (3, 64, 1020, 32, how_of(SIG, 17, 9, B.GROUP_TOP2), True),
     (3001, 576, 72, 6, how_of(SOFT, 8, 3, B.GROUP_MAX), True),
     (1030, 192, 300, 7, how_of(SIG, 3, 2, B.GROUP_TOP2), True),
     (2305, 128, 64, 6, how_of(SOFT, renorm=False), False),
