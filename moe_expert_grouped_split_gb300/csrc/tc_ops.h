@@ -1,5 +1,6 @@
-// tc_ops.h: the tcgen05 / TMA / mbarrier instructions that the tensor-core
-// kernels of libdwdp.so share, and their bounded waits.
+// tc_ops.h: the tcgen05 / TMA / mbarrier instructions of router_pair.cu and
+// lora_tc.cu, and their bounded waits.  (gemm.cu has its own: the committed DRAM
+// record of its kernels is keyed to its source.)
 #pragma once
 
 #include "dwdp_internal.h"
@@ -54,18 +55,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// Bounded wait that ignores the abort flag (used while draining).
-__device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, int* err, int code) {
-    const uint64_t t0 = global_timer();
-    while (!mbar_try_wait(bar, parity)) {
-        if (global_timer() - t0 > kWaitLimitNs) {
-            atomicOr(err, code);
-            return false;
-        }
-    }
-    return true;
-}
-
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -84,43 +73,12 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
-// As tma_load_3d, but the box lands at the same shared-memory offset in every
-// CTA of the cluster named in cta_mask, each completing its own mbarrier at
-// the same offset.
-__device__ __forceinline__ void tma_load_3d_mc(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                               uint32_t bar, uint16_t cta_mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(cta_mask)
-        : "memory");
-}
-
 // Untiled bulk copy of `bytes` (a multiple of 16, both addresses 16-byte
 // aligned) into this CTA's shared memory, completing on bar.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
         "l"((uint64_t)src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
-// As bulk_load, into the same offset of every CTA in cta_mask.
-__device__ __forceinline__ void bulk_load_mc(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
-                                             uint16_t cta_mask) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
-            dst),
-        "l"((uint64_t)src), "r"(bytes), "r"(bar), "h"(cta_mask)
         : "memory");
 }
 
@@ -140,18 +98,17 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
 }
 
-// Shared-memory matrix descriptor for a K-major operand tile written by TMA
-// with the swizzle that matches the slice width: rows of BK_BYTES bytes,
-// 8-row atoms 8 * BK_BYTES apart (stride byte offset), start address >> 4 in
-// bits 0-13, leading byte offset unused for these layouts (1), descriptor
-// version 1 at bits 46-47, swizzle mode at bits 61-63 (2 = 128-byte, 4 =
-// 64-byte).  The tile base is 1024-byte aligned.
+// Shared-memory matrix descriptor of a K-major operand tile written by TMA in
+// the 128-byte swizzle: rows of 128 bytes, 8-row atoms 1024 bytes apart (stride
+// byte offset), start address >> 4 in bits 0-13, leading byte offset unused
+// (1), descriptor version 1 at bits 46-47, swizzle mode 2 at bits 61-63.  The
+// tile base is 1024-byte aligned.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
     uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
     d |= (uint64_t)1 << 16;
-    d |= (uint64_t)((8 * BK_BYTES) >> 4) << 32;
+    d |= (uint64_t)(1024 >> 4) << 32;
     d |= (uint64_t)1 << 46;
-    d |= (uint64_t)(BK_BYTES == 128 ? 2 : 4) << 61;
+    d |= (uint64_t)2 << 61;
     return d;
 }
 
@@ -165,16 +122,6 @@ __device__ __forceinline__ void tc_fence_after() {
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-}
-
-// Commit that arrives on the mbarrier at the same offset in every CTA of
-// cta_mask once this thread's MMAs have finished reading shared memory.
-__device__ __forceinline__ void tc_commit_mc(uint32_t bar, uint16_t cta_mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            bar),
-        "h"(cta_mask)
         : "memory");
 }
 
