@@ -132,11 +132,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or type(t) is int else t.data_ptr()
 
 
 _current_raw_stream = None

@@ -98,22 +98,17 @@ struct Shrink {
     }
 };
 
+// The tile's partial sums over this block's part of K in part[0] ([16][NT * 8]
+// floats of shared memory for every warp); rows without an adapter hold
+// anything.  Ends with the block in step.
 template <int NT, int C>
-__global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) __cluster_dims__(C, 1, 1)
-    lora_shrink_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
+__device__ __forceinline__ void shrink_tile(const LoraArgs& p, int t0, int tile_rows, uint32_t rank, float* part) {
     using S = Shrink<NT, C>;
     // adapters a mixed pass takes at once, and steps in flight with one and
     // with several: what the registers hold
     constexpr int G = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
     constexpr int U1 = NT <= 2 ? 4 : NT <= 8 ? 2 : 1, UG = 2;
-    extern __shared__ float part[];  // [warps][16][NT * 8], then what the cluster sends [C][this rank's share]
-    wait_for_previous_kernel();
-    let_next_kernel_start();
-    cluster_arrive();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int t0 = (int)(blockIdx.x / C) * tile_rows;
-    const uint32_t rank = cluster_rank();
-    // this warp's rows
     uint32_t id[2], left[2];
     const uint4* xr[2];
 #pragma unroll
@@ -150,32 +145,103 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) __cluster_dims__(C,
             a0 = next();
         }
     }
-    // the K parts of the block, then of the cluster: rank e / kShare gets
-    // element e of every rank, and adds them in order
-    constexpr int kShare = S::kTile / C;
-    float* sent = part + kWarps * S::kTile;
     __syncthreads();
+}
+
+template <int NT, int C>
+__global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) __cluster_dims__(C, 1, 1)
+    lora_shrink_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
+    using S = Shrink<NT, C>;
+    extern __shared__ float part[];  // [warps][16][NT * 8], then what the cluster sends [C][this rank's share]
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    cluster_arrive();
+    const int t0 = (int)(blockIdx.x / C) * tile_rows;
+    const uint32_t rank = cluster_rank();
+    shrink_tile<NT, C>(p, t0, tile_rows, rank, part);
+    // the K parts of the block, then of the cluster: rank e / share gets
+    // element e of every rank, and adds them in order
+    const int n = tile_rows * NT * 8, share = n / C;
+    float* sent = part + kWarps * S::kTile;
     cluster_wait();  // everybody runs: its shared memory may be written
-    for (int e = threadIdx.x; e < S::kTile; e += kThreads) {
+    for (int e = threadIdx.x; e < n; e += kThreads) {
         float s = part[e];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) s += part[w * S::kTile + e];
-        store_to_rank(sent + rank * kShare + e % kShare, e / kShare, s);
+        store_to_rank(sent + rank * share + e % share, e / share, s);
     }
     __syncwarp();
     cluster_arrive();
     cluster_wait();
     __nv_bfloat16* v = static_cast<__nv_bfloat16*>(p.ws);
-    for (int i = threadIdx.x; i < kShare; i += kThreads) {
-        const int e = (int)rank * kShare + i, r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
-        if (r >= tile_rows || c >= p.R) continue;
+    for (int i = threadIdx.x; i < share; i += kThreads) {
+        const int e = (int)rank * share + i, r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
+        if (c >= p.R) continue;
         const uint32_t a = adapter_of(p, t, t < p.T);
         if (a == kNone) continue;
         float s = sent[i];
 #pragma unroll
-        for (int k = 1; k < C; ++k) s += sent[k * kShare + i];
+        for (int k = 1; k < C; ++k) s += sent[k * share + i];
         v[(int64_t)t * p.R + c] = __float2bfloat16_rn(s * p.scale[a]);
     }
+}
+
+// A handful of tokens in one kernel: a cluster of 8 blocks takes one token and
+// 2048 columns.  Its blocks share K for the first product, send every partial
+// sum to every block, and each goes on with 256 of the columns, whose base and
+// B it fetched at the start.  Other clusters compute the same v for other
+// columns.  One token, 7168 x 7168, rank 16: 3.6 us against the two kernels'
+// 4.4, and one launch less (2 us of a call from Python).
+template <int NT>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(8, 1, 1)
+    lora_one_kernel(const __grid_constant__ LoraArgs p, int) {
+    constexpr int C = 8, KS = NT / 2, kRank = NT * 8;
+    using X = Expand<KS>;
+    extern __shared__ float part[];  // [warps][16][NT * 8]
+    __shared__ float sent[C * kRank];  // what the cluster sends
+    __shared__ __align__(8) __nv_bfloat16 vs[kRank];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    cluster_arrive();
+    const uint32_t rank = cluster_rank();
+    const int wide = (p.N + 2047) / 2048, cluster = blockIdx.x / C, t = cluster / wide;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int c0 = ((cluster % wide) * C + (int)rank) * 256 + warp * 32;
+    const bool mine = g == 0 && c0 + 8 * q < p.N;  // the MMA's first row is the token's
+    const uint32_t id = adapter_of(p, t, true);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint4 bs[2] = {mine ? *(static_cast<const uint4*>(p.base) + t * (p.base_stride / 8) + c0 / 8 + q) : none, none};
+    uint2 bf[KS][4];
+    X::load_b(p, id, min(c0, p.N - 8), lane, bf);
+    shrink_tile<NT, C>(p, t, 1, rank, part);
+    cluster_wait();  // everybody runs: its shared memory may be written
+    for (int e = threadIdx.x; e < kRank; e += kThreads) {
+        float s = part[e];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) s += part[w * Shrink<NT, C>::kTile + e];
+#pragma unroll
+        for (int c = 0; c < C; ++c) store_to_rank(sent + rank * kRank + e, c, s);
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    for (int e = threadIdx.x; e < kRank; e += kThreads) {
+        float s = sent[e];
+#pragma unroll
+        for (int k = 1; k < C; ++k) s += sent[k * kRank + e];
+        vs[e] = __float2bfloat16_rn(id != kNone && e < p.R ? s * p.scale[id] : 0.0f);
+    }
+    __syncthreads();
+    uint2 vf[2][KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        vf[0][s] = g == 0 ? *reinterpret_cast<const uint2*>(vs + s * 16 + 4 * q) : make_uint2(0, 0);
+        vf[1][s] = make_uint2(0, 0);
+    }
+    float d[4][4];
+    X::product(bs, vf, bf, d);
+    // a token without an adapter keeps base's bits
+    if (mine) *(static_cast<uint4*>(p.out) + t * (p.out_stride / 8) + c0 / 8 + q) = id != kNone ? X::round(d, 0) : bs[0];
 }
 
 // A warp takes MT m16 tiles and 32 columns.  base is the accumulator's start,
@@ -320,6 +386,13 @@ cudaError_t launch_shrink(const LoraArgs& p, int rows, cudaStream_t s) {
 
 template <int NT>
 cudaError_t launch_rank(const LoraArgs& p, cudaStream_t s) {
+    if constexpr (NT <= 8) {
+        // one kernel while its clusters fit the GPU at once (rank 128 is slower so)
+        const int64_t blocks = (int64_t)p.T * ((p.N + 2047) / 2048) * 8;
+        if (p.T <= 16 && blocks <= p.n_sms * 4 / 5)
+            return launch((const void*)lora_one_kernel<NT>, dim3((unsigned)blocks),
+                          (size_t)kWarps * Shrink<NT, 8>::kTile * 4, s, p, 1);
+    }
     // shrink: the smallest tiles, then the fewest parts of K, whose clusters
     // fit the GPU at once with a block per SM (a cluster that has to wait for
     // another one's end costs more: 128 tokens of one adapter, rank 16, 8.0 us

@@ -603,33 +603,45 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 
     if (lane < p.k && pick.id >= 0) atomicAdd(p.hist + (int64_t)(t / p.chunk_tokens) * p.E + pick.id, 1);
 }
 
-// One chunk: the cluster's first block also places the pairs, a round of 256
-// at a time; base[e] moves on by the round's pairs.
-template <int P, bool FULL>
-__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1) __cluster_dims__(kOneCluster, 1, 1)
+// One chunk.  The blocks of a cluster (up to 8 tokens: a single block, ALONE)
+// send their picks to the first one's shared memory, which places the pairs,
+// a round of 256 at a time; base[e] moves on by the round's pairs.
+template <int P, bool FULL, bool ALONE>
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1)
     scored_one_kernel(const __grid_constant__ ScoredArgs p) {
     constexpr int kThreads = 32 * kSelectWarps, kPer = DWDP_MAX_EXPERTS / kThreads;
     extern __shared__ __align__(16) char smem[];
-    __shared__ int base[DWDP_MAX_EXPERTS];
+    __shared__ int base[DWDP_MAX_EXPERTS], sid[kChunk];
     __shared__ int tmp[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int e = tid; e < p.E; e += kThreads) base[e] = 0;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    cluster_sync();
-    for (int t = blockIdx.x * kSelectWarps + warp; t < p.T; t += kOneCluster * kSelectWarps) {
+    if constexpr (ALONE) __syncthreads();
+    else cluster_sync();
+    for (int t = blockIdx.x * kSelectWarps + warp; t < p.T; t += gridDim.x * kSelectWarps) {
         const Pick pick = route_token<P, FULL>(p, t, lane, Scratch(smem, p.E, warp));
         if (lane < p.k && pick.id >= 0) {
-            uint32_t at;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
-                         : "=r"(at)
-                         : "r"((uint32_t)__cvta_generic_to_shared(base + pick.id)));
-            asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], 1;" ::"r"(at) : "memory");
+            if constexpr (ALONE) {
+                atomicAdd(base + pick.id, 1);
+                sid[t * p.k + pick.slot] = pick.id;
+            } else {
+                uint32_t count_at, id_at;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                             : "=r"(count_at)
+                             : "r"((uint32_t)__cvta_generic_to_shared(base + pick.id)));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                             : "=r"(id_at)
+                             : "r"((uint32_t)__cvta_generic_to_shared(sid + t * p.k + pick.slot)));
+                asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], 1;" ::"r"(count_at) : "memory");
+                asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(id_at), "r"(pick.id) : "memory");
+            }
         }
         __syncwarp();
     }
     __syncwarp();
-    cluster_sync();
+    if constexpr (ALONE) __syncthreads();
+    else cluster_sync();
     if (blockIdx.x != 0) return;
     uint8_t* wc = reinterpret_cast<uint8_t*>(smem);  // [warps][E]; the scratch is done with
     int mine[kPer], sum = 0;                         // experts kPer tid ...
@@ -657,7 +669,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 
         for (int i = tid; i < kSelectWarps * p.E; i += kThreads) wc[i] = 0;
         __syncthreads();
         const int f = first + tid;
-        const int e = f < n ? p.ids[f] : -1;
+        const int e = f < n ? sid[f] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         const int in_warp = __popc(same & ((1u << lane) - 1u));
         if (e >= 0 && in_warp == 0) wc[warp * p.E + e] = (uint8_t)__popc(same);
@@ -675,36 +687,41 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 
 }
 
 template <class F, class... A>
-cudaError_t launch(F kernel, int grid, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch(F kernel, int grid, int threads, size_t smem, bool cluster, cudaStream_t s, A... args) {
+    if (smem > 36 << 10) {  // beside the static part, beyond what a launch gets unasked
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;  // the whole grid
+    at[1].val.clusterDim.x = grid;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(grid);
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    c.attrs = at;
+    c.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 template <int P, bool FULL>
 cudaError_t launch_form(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
+    constexpr int threads = 32 * kSelectWarps;
     const size_t smem = Scratch::bytes(p.E, kSelectWarps);
-    auto kernel = n_chunks == 1 ? scored_one_kernel<P, FULL> : scored_select_kernel<P, FULL>;
-    const int grid = n_chunks == 1 ? kOneCluster : (p.T + kSelectWarps - 1) / kSelectWarps;
-    if (smem > 40 << 10) {  // beside the static part, beyond what a launch gets unasked
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    cudaError_t e = launch(kernel, grid, 32 * kSelectWarps, smem, s, p);
-    if (e != cudaSuccess || n_chunks == 1) return e;
+    if (p.T <= kSelectWarps) return launch(scored_one_kernel<P, FULL, true>, 1, threads, smem, false, s, p);
+    if (n_chunks == 1) return launch(scored_one_kernel<P, FULL, false>, kOneCluster, threads, smem, true, s, p);
+    cudaError_t e =
+        launch(scored_select_kernel<P, FULL>, (p.T + kSelectWarps - 1) / kSelectWarps, threads, smem, false, s, p);
+    if (e != cudaSuccess) return e;
     if (n_chunks <= kSelfScanChunks)
-        return launch(scored_place_kernel<false>, n_chunks, kChunk, (size_t)p.E * 36, s, p, n_chunks);
+        return launch(scored_place_kernel<false>, n_chunks, kChunk, (size_t)p.E * 36, false, s, p, n_chunks);
     e = launch_chunk_scan(p.hist, n_chunks, p.E, p.counts, p.offsets, s);
     if (e != cudaSuccess) return e;
-    return launch(scored_place_kernel<true>, n_chunks, kChunk, (size_t)p.E * 36, s, p, n_chunks);
+    return launch(scored_place_kernel<true>, n_chunks, kChunk, (size_t)p.E * 36, false, s, p, n_chunks);
 }
 
 template <int P>
