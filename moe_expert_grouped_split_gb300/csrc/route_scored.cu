@@ -23,6 +23,18 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ (((k >> 31) - 1u) | 0x80000000u));
 }
+// Keys of a lane's run: the value's last log2 P bits, cut towards zero, make
+// room for the place j (lower places larger), so that no two keys of a lane
+// are alike and a pick needs no index beside it.  What the cut costs is part
+// of the tolerance below.
+template <int P>
+__device__ __forceinline__ uint32_t place_key(float x, int j) {
+    return (order_key(__uint_as_float(__float_as_uint(x) & ~(P - 1u))) & ~(P - 1u)) | (P - 1u - j);
+}
+template <int P>
+__device__ __forceinline__ float place_value(uint32_t k) {
+    return __uint_as_float(__float_as_uint(key_value(k)) & ~(P - 1u));
+}
 constexpr uint64_t kSign64 = 0x8000000000000000ull;
 __device__ __forceinline__ uint64_t order_key(double x) {
     const uint64_t u = (uint64_t)__double_as_longlong(x);
@@ -136,24 +148,19 @@ __device__ __forceinline__ float logit_of(const ScoredArgs& p, int64_t t, int e)
     return v;
 }
 
-// A lane's three best keys with their places in its run (the lowest on
-// ties), without a branch.
+// A lane's three best keys.
 struct Best3 {
     uint32_t k1 = 0, k2 = 0, k3 = 0;
-    int i1 = 0, i2 = 0, i3 = 0;
-    __device__ __forceinline__ void add(uint32_t c, int j) {
-        const bool g1 = c > k1, g2 = c > k2, g3 = c > k3;
-        k3 = g2 ? k2 : g3 ? c : k3;
-        i3 = g2 ? i2 : g3 ? j : i3;
-        k2 = g1 ? k1 : g2 ? c : k2;
-        i2 = g1 ? i1 : g2 ? j : i2;
-        k1 = g1 ? c : k1;
-        i1 = g1 ? j : i1;
+    __device__ __forceinline__ void add(uint32_t c) {
+        k3 = max(k3, min(k2, c));
+        k2 = max(k2, min(k1, c));
+        k1 = max(k1, c);
     }
 };
 
 // Two choice values further apart than (*this)(v) are in the right order.  A
-// binary32 value's error is at most half of rel (ref or |v|) + 2^-22 |v|.
+// binary32 value's error is at most half of rel (ref or |v|) + 2^-22 |v|, and
+// its key is cut by less than P - 1 units of 2^-23 |v|, always towards zero.
 // With ex2.approx and its argument's rounding, |z| <= most:
 //   sigmoid      s (1 - s) (1.7 |z| 2^-24 + 2^-22) + s 2^-22: 2^-21 of 1 at
 //                most, or (most 2^-23 + 2^-21) of s
@@ -161,18 +168,18 @@ struct Best3 {
 //                largest and the roundings of the sum of per_lane + 5; without
 //                one unnormalised, so (most 2^-21 + 2^-22) of e
 struct Tolerance {
-    float rel, ref;
+    float rel, ref, own;
     __device__ __forceinline__ float operator()(float v) const {
-        return rel * (ref > 0.0f ? ref : fabsf(v)) + 0x1p-22f * fabsf(v);
+        return rel * (ref > 0.0f ? ref : fabsf(v)) + own * fabsf(v);
     }
 };
 
-// Keys of the choice values (0: no expert) from the logits in z.  Without a
-// bias the value is the score (softmax: unnormalised).  zm is the largest
+// Keys of the choice values (0: no expert) from the logits in z and the bias
+// in b.  Without a bias the value is the score (softmax: unnormalised).  zm is the largest
 // logit, total the softmax denominator (neither set for sigmoid).
 template <int P, bool FULL>
 __device__ __forceinline__ Tolerance choice_keys(const ScoredArgs& p, const Lane& ln, float (&z)[P],
-                                                 uint32_t (&key)[P], float& zm, float& total, bool& finite) {
+                                                 const float (&b)[P], uint32_t (&key)[P], float& zm, float& total, bool& finite) {
     float most = 0.0f, worst = 0.0f;
 #pragma unroll
     for (int j = 0; j < P; ++j) most = max_nan(most, fabsf(z[j]));  // (0 where there is no expert)
@@ -200,8 +207,6 @@ __device__ __forceinline__ Tolerance choice_keys(const ScoredArgs& p, const Lane
         if (p.bias) factor = 1.0f / total;
     }
     if (p.bias) {
-        float b[P];
-        load_run<P, FULL>(p.bias, ln, b);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             z[j] = fmaf(z[j], factor, b[j]);
@@ -209,11 +214,12 @@ __device__ __forceinline__ Tolerance choice_keys(const ScoredArgs& p, const Lane
         }
     }
 #pragma unroll
-    for (int j = 0; j < P; ++j) key[j] = has<P, FULL>(ln, j) ? order_key(z[j]) : 0u;
+    for (int j = 0; j < P; ++j) key[j] = has<P, FULL>(ln, j) ? place_key<P>(z[j], j) : 0u;
     finite = __all_sync(kFull, finite && worst < CUDART_INF_F);
     most = __uint_as_float(warp_max(__float_as_uint(most)));
-    if (p.bias) return p.sigmoid ? Tolerance{0x1p-20f, 1.0f} : Tolerance{0x1p-18f + p.per_lane * 0x1p-23f, factor};
-    return Tolerance{p.sigmoid ? 0x1p-20f + most * 0x1p-22f : 0x1p-21f + most * 0x1p-20f, 0.0f};
+    constexpr float own = 0x1p-22f + (P - 1) * 0x1p-23f;
+    if (p.bias) return p.sigmoid ? Tolerance{0x1p-20f, 1.0f, own} : Tolerance{0x1p-18f + p.per_lane * 0x1p-23f, factor, own};
+    return Tolerance{p.sigmoid ? 0x1p-20f + most * 0x1p-22f : 0x1p-21f + most * 0x1p-20f, 0.0f, own};
 }
 
 // The k best of the lanes' keys.  Lane s < k gets the s-th pick's id; last is
@@ -225,30 +231,28 @@ __device__ __forceinline__ Tolerance choice_keys(const ScoredArgs& p, const Lane
 template <int P>
 __device__ __forceinline__ int pick(const ScoredArgs& p, const uint32_t (&key)[P], Best3 best, const Lane& ln,
                                     int lane, uint32_t& my_key, uint32_t& last, uint32_t& next) {
-    int my_id = -1;
+    int my_owner = 0;
     last = my_key = 0;
 #pragma unroll 1
     for (int s = 0; s < p.k; ++s) {
         const uint32_t gk = last = warp_max(best.k1);  // never 0: the host refuses fewer than k candidates
         const int owner = __ffs(__ballot_sync(kFull, best.k1 == gk)) - 1;
-        const int id = __shfl_sync(kFull, ln.first + best.i1, owner);
-        my_id = lane == s ? id : my_id;
+        my_owner = lane == s ? owner : my_owner;
         my_key = lane == s ? gk : my_key;
-        const bool own = lane == owner;
-        const int at = best.i1;
-        best.k1 = own ? best.k2 : best.k1;
-        best.i1 = own ? best.i2 : best.i1;
-        best.k2 = own ? best.k3 : best.k2;
-        best.i2 = own ? best.i3 : best.i2;
-        best.k3 = own ? 0u : best.k3;
-        if (P > 3 && own && best.k1 == 0) {  // what comes after (gk, at) in order
+        if (lane == owner) {
+            best.k1 = best.k2;
+            best.k2 = best.k3;
+            best.k3 = 0;
+            if (P > 3 && best.k1 == 0) {  // what comes after gk in order
 #pragma unroll
-            for (int j = 0; j < P; ++j) best.add(key[j] < gk || (key[j] == gk && j > at) ? key[j] : 0u, j);
+                for (int j = 0; j < P; ++j) best.add(key[j] < gk ? key[j] : 0u);
+            }
         }
         __syncwarp();
     }
     next = warp_max(best.k1);
-    return my_id;
+    const int first = __shfl_sync(kFull, ln.first, my_owner);
+    return lane < p.k ? first + (int)(P - 1u - (my_key & (P - 1u))) : -1;
 }
 
 // --------------------------------------------------- what is too close --
@@ -323,11 +327,11 @@ __device__ __forceinline__ bool keep_close_group(const ScoredArgs& p, int64_t t,
     const bool is_group = ln.g < p.n_groups;
     const bool sure = is_group && v > edge && !(v - edge <= wide);
     const bool open = is_group && !sure && !(edge - v > wide);
-    const float low = key_value(p.group_top2 && k2 != 0 ? k2 : k1), floor = low - tol(low);
+    const float low = place_value<P>(p.group_top2 && k2 != 0 ? k2 : k1), floor = low - tol(low);
     uint64_t bits = 0;  // the values an open group's score may consist of
 #pragma unroll
     for (int j = 0; j < P; ++j)
-        if (open && key[j] != 0 && !(key_value(key[j]) < floor)) bits |= 1ull << j;
+        if (open && key[j] != 0 && !(place_value<P>(key[j]) < floor)) bits |= 1ull << j;
     const int n = list_in_64(p, t, lane, ln, bits, s, zm);
     uint64_t m1 = 0, m2 = 0;
     for (int i = 0; i < n; ++i)
@@ -352,12 +356,12 @@ template <int P>
 __device__ __forceinline__ int pick_close(const ScoredArgs& p, int64_t t, int lane, const Lane& ln,
                                           const uint32_t (&key)[P], bool kept, int my_id, uint32_t my_key,
                                           uint32_t edge_key, const Tolerance& tol, const Scratch& s, float zm) {
-    const float edge = key_value(edge_key), wide = tol(edge);
-    auto above = [&](uint32_t k) { return key_value(k) > edge && !(key_value(k) - edge <= wide); };
+    const float edge = place_value<P>(edge_key), wide = tol(edge);
+    auto above = [&](uint32_t k) { return place_value<P>(k) > edge && !(place_value<P>(k) - edge <= wide); };
     uint64_t bits = 0;
 #pragma unroll
     for (int j = 0; j < P; ++j)
-        if (kept && key[j] != 0 && !above(key[j]) && !(edge - key_value(key[j]) > wide)) bits |= 1ull << j;
+        if (kept && key[j] != 0 && !above(key[j]) && !(edge - place_value<P>(key[j]) > wide)) bits |= 1ull << j;
     const int n_sure = __popc(__ballot_sync(kFull, my_id >= 0 && above(my_key)));
     const int n = list_in_64(p, t, lane, ln, bits, s, zm);
     uint64_t last = ~0ull;
@@ -388,8 +392,8 @@ struct Pick {
     float w;
 };
 template <int P, bool FULL>
-__device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int lane, const Scratch& scratch) {
-    const Lane ln(p, lane);
+__device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int lane, const Lane& ln,
+                                            const float (&b)[P], const Scratch& scratch) {
     float z[P];
     load_logits<P, FULL>(p, t, ln, z);
     if (p.z_out) {
@@ -400,15 +404,13 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
     uint32_t key[P];
     float zm, total;
     bool finite;
-    const Tolerance tol = choice_keys<P, FULL>(p, ln, z, key, zm, total, finite);
+    const Tolerance tol = choice_keys<P, FULL>(p, ln, z, b, key, zm, total, finite);
     if (!finite && lane == 0) atomicOr(p.err, DERR_NONFINITE_LOGIT);
     // close: a difference of infinities is NaN and never close, ties go by id
-    auto close = [&](uint32_t a, uint32_t b, float times) {
-        return b != 0 && finite && key_value(a) - key_value(b) <= times * tol(key_value(a));
-    };
+    auto close = [&](float a, float b, float times) { return finite && a - b <= times * tol(a); };
     Best3 best;
 #pragma unroll
-    for (int j = 0; j < P; ++j) best.add(key[j], j);
+    for (int j = 0; j < P; ++j) best.add(key[j]);
     bool kept = true;
     if (p.top_groups < p.n_groups) {
         // the group's best two and score, by all its lanes
@@ -419,7 +421,8 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
             k1 = max(k1, o1);
         }
         const bool is_group = ln.g < p.n_groups;
-        uint32_t score = p.group_top2 && k2 != 0 ? order_key(key_value(k1) + key_value(k2)) : k1;
+        const float top = place_value<P>(k1);
+        uint32_t score = order_key(p.group_top2 && k2 != 0 ? top + place_value<P>(k2) : top);
         if (!is_group) score = 0;
         int rank = 0;  // groups before this one: larger, or as large and lower
         for (int g0 = 0; g0 < p.n_groups; g0 += 8) {
@@ -432,13 +435,13 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
         }
         kept = is_group && rank < p.top_groups;
         const uint32_t edge = ~warp_max(kept ? ~score : 0u), dropped = warp_max(is_group && !kept ? score : 0u);
-        if (close(edge, dropped, 2.0f))
+        if (dropped != 0 && close(key_value(edge), key_value(dropped), 2.0f))
             kept = keep_close_group<P>(p, t, lane, ln, key, k1, k2, score, edge, tol, scratch, zm);
         if (!kept) best.k1 = best.k2 = best.k3 = 0;
     }
     uint32_t my_key, last, next;
     int my_id = pick<P>(p, key, best, ln, lane, my_key, last, next);
-    if (close(last, next, 1.0f))
+    if (next != 0 && close(place_value<P>(last), place_value<P>(next), 1.0f))
         my_id = pick_close<P>(p, t, lane, ln, key, kept, my_id, my_key, last, tol, scratch, zm);
 
     // weights, by lane s < k for its own pick
@@ -475,9 +478,10 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
 //            expert: hist[chunk][e], zeroed by the router GEMM's kernel
 //   place    a block per chunk adds up the counts of all chunks (its base is
 //            what lies before it), and ranks its own pairs
-// or, with one chunk, a cluster of 8 blocks chooses, counting in its first
-// block's shared memory, and that block places.  Each pair's row is the
-// stable one (ascending flat index within an expert).
+// or, with one chunk, one kernel for both: a block that chooses and places, a
+// warp per token, and above 8 tokens a cluster of 8 blocks that choose and
+// send their counts and ids to the first block, which places.  Each pair's
+// row is the stable one (ascending flat index within an expert).
 constexpr int kChunk = 1024;
 constexpr int kSelectWarps = 8;
 constexpr int kOneCluster = 8;  // blocks of the one-chunk kernel
@@ -590,16 +594,28 @@ __global__ void __launch_bounds__(kChunk) scored_place_kernel(const __grid_const
     place_pairs(p, first, n, e, base, wc);
 }
 
+// The lane's bias, before the kernel before this one (the router GEMM) is
+// done: it lets this one start only after everything before it is.
 template <int P, bool FULL>
-__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1)
+__device__ __forceinline__ void early_bias(const ScoredArgs& p, const Lane& ln, float (&b)[P]) {
+    if (p.bias) load_run<P, FULL>(p.bias, ln, b);
+}
+
+template <int P, bool FULL>
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 3 : P <= 16 ? 2 : 1)
     scored_select_kernel(const __grid_constant__ ScoredArgs p) {
     extern __shared__ __align__(16) char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Lane ln(p, lane);
+    float bias[P];
+    early_bias<P, FULL>(p, ln, bias);
     wait_for_previous_kernel();
-    let_next_kernel_start();
     const int t = blockIdx.x * kSelectWarps + warp;
     if (t >= p.T) return;
-    const Pick pick = route_token<P, FULL>(p, t, lane, Scratch(smem, p.E, warp));
+    const Pick pick = route_token<P, FULL>(p, t, lane, ln, bias, Scratch(smem, p.E, warp));
+    // not earlier: the placing blocks would take slots from waiting tokens
+    // (8192 tokens of 256 experts: 0.3 to 3 us of 48)
+    let_next_kernel_start();
     if (lane < p.k && pick.id >= 0) atomicAdd(p.hist + (int64_t)(t / p.chunk_tokens) * p.E + pick.id, 1);
 }
 
@@ -607,7 +623,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 
 // send their picks to the first one's shared memory, which places the pairs,
 // a round of 256 at a time; base[e] moves on by the round's pairs.
 template <int P, bool FULL, bool ALONE>
-__global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kSelectWarps, P <= 16 ? 2 : 1)
     scored_one_kernel(const __grid_constant__ ScoredArgs p) {
     constexpr int kThreads = 32 * kSelectWarps, kPer = DWDP_MAX_EXPERTS / kThreads;
     extern __shared__ __align__(16) char smem[];
@@ -615,12 +631,15 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 8 ? 4 : P <= 16 ? 2 : 
     __shared__ int tmp[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int e = tid; e < p.E; e += kThreads) base[e] = 0;
+    const Lane ln(p, lane);
+    float bias[P];
+    early_bias<P, FULL>(p, ln, bias);
     wait_for_previous_kernel();
     let_next_kernel_start();
     if constexpr (ALONE) __syncthreads();
     else cluster_sync();
     for (int t = blockIdx.x * kSelectWarps + warp; t < p.T; t += gridDim.x * kSelectWarps) {
-        const Pick pick = route_token<P, FULL>(p, t, lane, Scratch(smem, p.E, warp));
+        const Pick pick = route_token<P, FULL>(p, t, lane, ln, bias, Scratch(smem, p.E, warp));
         if (lane < p.k && pick.id >= 0) {
             if constexpr (ALONE) {
                 atomicAdd(base + pick.id, 1);
@@ -717,11 +736,12 @@ cudaError_t launch_form(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
     cudaError_t e =
         launch(scored_select_kernel<P, FULL>, (p.T + kSelectWarps - 1) / kSelectWarps, threads, smem, false, s, p);
     if (e != cudaSuccess) return e;
+    const size_t place_smem = (size_t)p.E * 36;
     if (n_chunks <= kSelfScanChunks)
-        return launch(scored_place_kernel<false>, n_chunks, kChunk, (size_t)p.E * 36, false, s, p, n_chunks);
+        return launch(scored_place_kernel<false>, n_chunks, kChunk, place_smem, false, s, p, n_chunks);
     e = launch_chunk_scan(p.hist, n_chunks, p.E, p.counts, p.offsets, s);
     if (e != cudaSuccess) return e;
-    return launch(scored_place_kernel<true>, n_chunks, kChunk, (size_t)p.E * 36, false, s, p, n_chunks);
+    return launch(scored_place_kernel<true>, n_chunks, kChunk, place_smem, false, s, p, n_chunks);
 }
 
 template <int P>

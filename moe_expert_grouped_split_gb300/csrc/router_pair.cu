@@ -9,8 +9,8 @@
 //   warp 0      TMA producer of its CTA; all loads complete on the leader's
 //               barrier
 //   warp 1      allocates TMEM; the leader's issues the pair's MMAs
-//   warps 2..5  epilogue: 32 TMEM lanes each, 32 x 32 blocks turned around in
-//               shared memory so that a row's stores are 128 bytes together
+//   warps 2..5  epilogue: 32 TMEM lanes each, a thread one token's row, stored
+//               in whole sectors of 32 bytes
 // K is cut into parts so that the pairs fill the GPU; the choice adds the
 // planes in order.
 #include <cuda_bf16.h>
@@ -33,8 +33,7 @@ template <int N>
 struct PairSmem {
     static constexpr int kWBytes = N / 2 * kSlice * 2;
     static constexpr int kStage = kRowsBytes + kWBytes;
-    static constexpr int kTurn = kPairStages * kStage;         // float [4 warps][32][33]
-    static constexpr int kBars = kTurn + 4 * 32 * 33 * 4;      // full[S], empty[S], done
+    static constexpr int kBars = kPairStages * kStage;         // full[S], empty[S], done
     static constexpr int kMisc = kBars + 8 * (2 * kPairStages + 1);
     static constexpr int kBytes = 1024 + kMisc + 16;           // base aligned to 1024 inside
 };
@@ -73,6 +72,12 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)0x3)
         : "memory");
+}
+
+__device__ __forceinline__ void store8(float* to, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 template <int N>
@@ -168,23 +173,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int q = warp & 3;  // the TMEM lane quarter this warp may read
         if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.err, DERR_EPI_WAIT))) {
             tc_fence_after();
-            float* turn = reinterpret_cast<float*>(mem + S::kTurn) + q * 32 * 33;
-            float* z = p.z + (int64_t)part * p.part_stride;
-            const int t0 = row0 + 32 * q;
+            const int t = row0 + 32 * q + lane;
+            float* row = p.z + (int64_t)part * p.part_stride + (int64_t)t * p.E + e0;
+            // whole sectors, where rows lie on them
+            const bool wide = p.E % 8 == 0 && (uint64_t)p.z % 32 == 0;
 #pragma unroll 1
             for (int c = 0; c < N; c += 32) {
                 uint32_t v[32];
                 tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
                 tmem_wait_ld();
-                __syncwarp();
+                if (t >= p.T) continue;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = __uint_as_float(v[j]);
-                __syncwarp();
-                const int e = e0 + c + lane;
-                if (e < p.E) {
-#pragma unroll 8
-                    for (int r = 0; r < 32; ++r)
-                        if (t0 + r < p.T) z[(int64_t)(t0 + r) * p.E + e] = turn[r * 33 + lane];
+                for (int j = 0; j < 32; j += 8) {
+                    const int e = c + j;
+                    if (wide && e0 + e < p.E) {
+                        store8(row + e, v + j);
+                    } else if (!wide) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (e0 + e + i < p.E) row[e + i] = __uint_as_float(v[j + i]);
+                    }
                 }
             }
         }
