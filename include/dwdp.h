@@ -547,10 +547,13 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
  * base_stride / t * out_stride, N of them; every stride a multiple of 8 and
  * no smaller than the row.  out may be base (equal strides); no other
  * overlap.  K, N multiples of 8, at most 2^20; R a multiple of 8,
- * 8..DWDP_MAX_LORA_RANK; T at most 2^30.  An id outside [-1, n_adapters) is not
- * followed: the token gets base and the device error word reports a bad index (DEVICE_CHECK).  ws: at least
+ * 8..DWDP_MAX_LORA_RANK; T at most 2^30; n_adapters * R below 2^31.  An id
+ * outside [-1, n_adapters) is not followed: the token gets base and the device
+ * error word reports a bad index (DEVICE_CHECK).  ws: at least
  * dwdp_lora_workspace_bytes(T, K, N, R) bytes, device.  All pointers 16-byte
- * aligned.  Enqueued on `stream`.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * aligned; from 1024 tokens on x and a must be device memory of the context's
+ * device (they are read through tensor maps).  Enqueued on `stream`.  Errors:
+ * INVALID_ARG, UNSUPPORTED, CUDA. */
 int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T, int32_t K, int32_t N,
                       const void* a, const void* b, const float* adapter_scale, int32_t n_adapters, int32_t R,
                       const int32_t* adapter_ids, const void* base, int64_t base_stride, void* out,

@@ -956,6 +956,8 @@ int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T,
     if (need == 0)
         return fail(ctx, DWDP_ERR_UNSUPPORTED, "K, N and R must be positive multiples of 8, K, N <= 2^20, R <= %d; T <= 2^30",
                     DWDP_MAX_LORA_RANK);
+    if ((int64_t)n_adapters * R > 0x7fffffff)  // rows of a's tensor map
+        return fail(ctx, DWDP_ERR_UNSUPPORTED, "n_adapters * R must stay below 2^31");
     if (x_stride < K || x_stride % 8 || base_stride < N || base_stride % 8 || out_stride < N || out_stride % 8)
         return fail(ctx, DWDP_ERR_INVALID_ARG, "strides must be multiples of 8, no smaller than the row");
     if (out == base && out_stride != base_stride)

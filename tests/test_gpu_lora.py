@@ -189,3 +189,41 @@ def test_no_tokens_and_refusals():
         assert rt.device_status() == 0 and (out == 0).all()
     finally:
         rt.close()
+
+
+@pytest.mark.parametrize("T", [1, 40, 1100])
+def test_row_strides_beyond_2_to_31_elements(T):
+    K, N, n = 512, 520, 4
+    stride = ((1 << 31) // max(T - 8, 1) + 7) // 8 * 8
+    x, a, b, scale, ids, base = case(T, K, N, 16, n, np.random.default_rng(9).integers(-1, n, T))
+    far = [torch.empty((T - 1) * stride + w, dtype=torch.bfloat16, device="cuda").as_strided((T, w), (stride, 1))
+           for w in (K, N, N)]
+    far[0].copy_(x)
+    far[1].copy_(base)
+    assert torch.equal(run(far[0], a, b, scale, ids, far[1], out=far[2]), run(x, a, b, scale, ids, base))
+    check(far[2], x, a, b, scale, ids, base)
+
+
+@pytest.mark.parametrize("T", [1, 40, 1100])
+def test_bank_beyond_2_to_31_elements(T):
+    K = N = 8192
+    n, used = (1 << 31) // (16 * K) + 6, 4
+    x, some_a, some_b, _, few, base = case(T, K, N, 16, used, np.random.default_rng(10).integers(0, used, T))
+    a = torch.empty((n, 16, K), dtype=torch.bfloat16, device="cuda")
+    b = torch.empty((n, N, 16), dtype=torch.bfloat16, device="cuda")
+    a[-used:], b[-used:] = some_a, some_b
+    scale, ids = torch.linspace(0.5, 2.0, n, device="cuda"), few + (n - used)
+    check(run(x, a, b, scale, ids, base), x, a, b, scale, ids, base)
+
+
+def test_bank_of_too_many_rows_is_refused():
+    x, a, b, scale, ids, base = case(4, 64, 64, 16, 1, [0] * 4)
+    rt = B.Runtime(64, 64, 1, 1, 0, 4, 1, 0, min_ws_bytes=B.dwdp_lora_workspace_bytes(4, 64, 64, 16))
+    try:
+        with pytest.raises(B.DwdpError) as ei:
+            B.dwdp_lora_add(rt.ctx, x=x, x_stride=64, T=4, K=64, N=64, a=a, b=b, adapter_scale=scale,
+                            n_adapters=1 << 27, R=16, adapter_ids=ids, base=base, base_stride=64,
+                            out=torch.empty_like(base), out_stride=64, ws=rt.ws, ws_bytes=rt.ws.numel())
+        assert ei.value.code == -5
+    finally:
+        rt.close()

@@ -172,3 +172,23 @@ def test_same_bits_every_time_and_on_another_stream():
     a, b = call(x, w, r), call(x, w, r, stream=torch.cuda.Stream())
     for name in a:
         assert torch.equal(a[name], b[name])
+
+
+@pytest.mark.parametrize("H", [512, 4096, 8192])
+def test_rows_beyond_2_to_31_elements(H):
+    rows, last = (1 << 31) // H + 20, 30
+    x, r = (torch.zeros((rows, H), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-last:] = I.randn_bf16((last, H), 1.0, 20, "cuda")
+    r[-last:] = I.randn_bf16((last, H), 4.0, 21, "cuda")
+    w = I.randn_bf16((H,), 1.0, 22, "cuda")
+    o = call(x, w, r)
+    check({name: t[-last:] for name, t in o.items()}, x[-last:], w, r[-last:])
+    assert not o["out"][:100].any() and (o["row_scale"][:100] == 1).all()
+
+
+def test_row_stride_beyond_2_to_31_elements():
+    rows, H, stride = 9, 512, (1 << 28) + 8
+    x = torch.empty(8 * stride + H, dtype=torch.bfloat16, device="cuda").as_strided((rows, H), (stride, 1))
+    x.copy_(I.randn_bf16((rows, H), 1.0, 23, "cuda"))
+    w = I.randn_bf16((H,), 1.0, 24, "cuda")
+    check(call(x, w), x, w)
