@@ -867,15 +867,16 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     float* planes = reinterpret_cast<float*>(static_cast<char*>(ws) + L.logits);
     float* logits = nullptr;
     p.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.group);
-    const int chunks = scored_chunks(T, c.top_k);
-    const int64_t n_zero = chunks > 1 ? (int64_t)chunks * c.n_experts : 0;
-    if (router_is_small(T, c.n_experts)) {
-        p.parts = 1;
+    const bool small = router_is_small(T, c.n_experts);
+    p.parts = small ? 1 : router_pair_parts(T, c.n_experts, c.hidden);
+    p.chunks = scored_chunks(T, c.top_k);
+    p.in_one = scored_in_one(T, c.top_k, p.parts);
+    const int64_t n_zero = p.in_one ? 0 : (int64_t)p.chunks * c.n_experts;
+    if (small) {
         logits = out->logits ? out->logits : planes;
         DWDP_CUDA(ctx, launch_router_small(x, w_router, T, c.n_experts, c.hidden, logits, p.hist, n_zero, stream));
     } else {
         RouterPairArgs r;
-        p.parts = router_pair_parts(T, c.n_experts, c.hidden);
         logits = out->logits && p.parts == 1 ? out->logits : planes;
         const uint64_t row_bytes = 2ull * c.hidden;
         if (!encode_matrix(&r.tm_x, x, T, c.hidden, row_bytes, 128) ||

@@ -247,9 +247,8 @@ cudaError_t launch_router_pair(const RouterPairArgs& p, cudaStream_t s);
 
 // route_scored.cu: dwdp_route_scored from the logits on.  logits: `parts` fp32
 // planes [T][E] part_stride apart, summed in plane order; z_out, if not null,
-// receives the sums; hist: scored_chunks(T, k) x E counts, zero (unless there
-// is one chunk, which needs none).  The members after `scale` are filled by
-// launch_scored_choice.
+// receives the sums; hist: chunks x E counts, zero (in_one: not used).  The
+// last four members are filled by launch_scored_choice.
 struct ScoredArgs {
     const float* logits;
     int64_t part_stride;
@@ -267,9 +266,12 @@ struct ScoredArgs {
     int n_groups, top_groups;
     bool sigmoid, group_top2, renorm;
     float scale;
+    int chunks;   // scored_chunks(T, k)
+    bool in_one;  // scored_in_one
     int lanes, group_size, per_lane, chunk_tokens;
 };
 int scored_chunks(int64_t T, int64_t k);
+bool scored_in_one(int64_t T, int64_t k, int parts);
 cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s);
 // route.cu's chunk_scan_kernel on its own: hist [n_chunks][E] counts to each
 // chunk's first rows, counts [E] and offsets [E + 1].

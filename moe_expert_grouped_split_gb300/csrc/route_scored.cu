@@ -481,10 +481,10 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
 //            expert: hist[chunk][e], zeroed by the router GEMM's kernel
 //   place    a block per chunk adds up the counts of all chunks (its base is
 //            what lies before it), and ranks its own pairs
-// or, with one chunk, one kernel for both: a block that chooses and places, a
-// warp per token, and above 8 tokens a cluster of 8 blocks that choose and
-// send their counts and ids to the first block, which places.  Each pair's
-// row is the stable one (ascending flat index within an expert).
+// or, for up to 64 tokens, one kernel for both: a block that chooses and
+// places, a warp per token, and above 8 tokens a cluster of 8 blocks that
+// choose and send their counts and ids to the first block, which places.
+// Each pair's row is the stable one (ascending flat index within an expert).
 constexpr int kChunk = 1024;
 constexpr int kSelectWarps = 8;
 constexpr int kOneCluster = 8;  // blocks of the one-chunk kernel
@@ -731,11 +731,12 @@ cudaError_t launch(F kernel, int grid, int threads, size_t smem, bool cluster, c
 }
 
 template <int P, bool FULL>
-cudaError_t launch_form(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
+cudaError_t launch_form(const ScoredArgs& p, cudaStream_t s) {
     constexpr int threads = 32 * kSelectWarps;
     const size_t smem = Scratch::bytes(p.E, kSelectWarps);
-    if (p.T <= kSelectWarps) return launch(scored_one_kernel<P, FULL, true>, 1, threads, smem, false, s, p);
-    if (n_chunks == 1) return launch(scored_one_kernel<P, FULL, false>, kOneCluster, threads, smem, true, s, p);
+    if (p.in_one && p.T <= kSelectWarps) return launch(scored_one_kernel<P, FULL, true>, 1, threads, smem, false, s, p);
+    if (p.in_one) return launch(scored_one_kernel<P, FULL, false>, kOneCluster, threads, smem, true, s, p);
+    const int n_chunks = p.chunks;
     cudaError_t e =
         launch(scored_select_kernel<P, FULL>, (p.T + kSelectWarps - 1) / kSelectWarps, threads, smem, false, s, p);
     if (e != cudaSuccess) return e;
@@ -748,10 +749,10 @@ cudaError_t launch_form(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
 }
 
 template <int P>
-cudaError_t launch_per_lane(const ScoredArgs& p, int n_chunks, cudaStream_t s) {
-    if constexpr (P <= 16)
-        if (p.per_lane == P && 32 * P == p.E && p.lanes * P == p.group_size) return launch_form<P, true>(p, n_chunks, s);
-    return launch_form<P, false>(p, n_chunks, s);
+cudaError_t launch_per_lane(const ScoredArgs& p, cudaStream_t s) {
+    if constexpr (P <= 32)
+        if (p.per_lane == P && 32 * P == p.E && p.lanes * P == p.group_size) return launch_form<P, true>(p, s);
+    return launch_form<P, false>(p, s);
 }
 
 }  // namespace
@@ -761,6 +762,14 @@ int scored_chunks(int64_t T, int64_t k) {
     return (int)((T + tokens - 1) / tokens);
 }
 
+// One kernel chooses and places: one chunk, one plane, and a token for each of
+// the cluster's 64 warps at most.  Routing to 8 of 256 experts, H = 7168, one
+// kernel / two, us: 32 tokens 9.5 / 9.7, 64 11.4 / 11.6, 128 16.9 / 14.3 (with
+// 8 planes 24); 2 of 16: 64 7.2 / 7.7, 512 18.1 / 9.0.
+bool scored_in_one(int64_t T, int64_t k, int parts) {
+    return parts == 1 && T <= kSelectWarps * kOneCluster && scored_chunks(T, k) == 1;
+}
+
 cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s) {
     if (p.T <= 0) return cudaSuccess;
     p.lanes = 1;
@@ -768,14 +777,13 @@ cudaError_t launch_scored_choice(ScoredArgs& p, cudaStream_t s) {
     p.group_size = p.E / p.n_groups;
     p.per_lane = (p.group_size + p.lanes - 1) / p.lanes;
     p.chunk_tokens = kChunk / p.k;
-    const int n_chunks = scored_chunks(p.T, p.k);
-    if (p.per_lane <= 1) return launch_per_lane<1>(p, n_chunks, s);
-    if (p.per_lane <= 2) return launch_per_lane<2>(p, n_chunks, s);
-    if (p.per_lane <= 4) return launch_per_lane<4>(p, n_chunks, s);
-    if (p.per_lane <= 8) return launch_per_lane<8>(p, n_chunks, s);
-    if (p.per_lane <= 16) return launch_per_lane<16>(p, n_chunks, s);
-    if (p.per_lane <= 32) return launch_per_lane<32>(p, n_chunks, s);
-    return launch_per_lane<64>(p, n_chunks, s);
+    if (p.per_lane <= 1) return launch_per_lane<1>(p, s);
+    if (p.per_lane <= 2) return launch_per_lane<2>(p, s);
+    if (p.per_lane <= 4) return launch_per_lane<4>(p, s);
+    if (p.per_lane <= 8) return launch_per_lane<8>(p, s);
+    if (p.per_lane <= 16) return launch_per_lane<16>(p, s);
+    if (p.per_lane <= 32) return launch_per_lane<32>(p, s);
+    return launch_per_lane<64>(p, s);
 }
 
 }  // namespace dwdp

@@ -2,8 +2,8 @@
 // z [T][E] = x W^T, fp32.
 //
 // Few tokens read W once and little else, so what counts is that the whole
-// GPU loads at once and how few round trips a launch needs: a tile of 16 to
-// 64 tokens x 16 to 64 experts is a cluster of 8 CTAs of 8 warps that share
+// GPU loads at once and how few round trips a launch needs: a tile of 16
+// or 32 tokens x 16 to 64 experts is a cluster of 8 CTAs of 8 warps that share
 // K, operands straight from global memory, several steps' loads in flight;
 // the parts meet in shared memory, then across the cluster, in order.
 #include <cuda_bf16.h>
@@ -132,20 +132,21 @@ cudaError_t launch(const void* x, const void* w, int T, int E, int H, float* z, 
 
 }  // namespace
 
-// Where the tensor-core pairs (router_pair.cu) take over.
-bool router_is_small(int64_t T, int64_t E) { return T * E <= 128 << 10; }
+// Where the tensor-core pairs (router_pair.cu) take over.  Routing to 8 of 256
+// experts, H = 7168, here / there, us: 192 tokens 17.1 / 19.1, 256 17.2 / 18.9,
+// 384 23.3 / 19.4, 512 21.9 / 19.0.
+bool router_is_small(int64_t T, int64_t E) { return T * E <= 64 << 10 && T <= 1 << 10; }
 
 // The tile by the size of z: small tiles spread W over all SMs, larger ones
 // read x and W fewer times.  7168 x 256, us at 1 / 64 / 128 / 256 / 512
 // tokens: 16 x 16 3.1 / 5.2 / 9.5 / 18 / 34, 32 x 32 4.3 / 6.2 / 6.5 / 12 / 24,
-// 32 x 64 5.9 / 7.1 / 8.7 / 9.2 / 18, 64 x 64 8.5 / 11 / 11 / 13 / 14.
+// 32 x 64 5.9 / 7.1 / 8.7 / 9.2 / 18.
 cudaError_t launch_router_small(const void* x, const void* w, int T, int E, int H, float* z, int32_t* zero,
                                 int64_t n_zero, cudaStream_t s) {
     const int64_t n = (int64_t)T * E;
     if (n <= 16 << 10) return launch<1, 1, 8, 1, 2, 4>(x, w, T, E, H, z, zero, n_zero, s);
     if (n <= 32 << 10) return launch<1, 1, 8, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
-    if (n <= 64 << 10) return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
-    return launch<2, 2, 2, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
+    return launch<1, 2, 4, 2, 4, 2>(x, w, T, E, H, z, zero, n_zero, s);
 }
 
 }  // namespace dwdp

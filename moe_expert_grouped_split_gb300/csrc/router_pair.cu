@@ -235,15 +235,18 @@ cudaError_t launch_n(const RouterPairArgs& p, cudaStream_t s) {
 int router_pair_cols(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
 
 // Parts of K: as many pairs as fill whole rounds of the GPU's 76 pairs of SMs
-// best, a part costing about 4% of a pass over x (its plane is written and
-// read again).  From the sizes alone, so the logits depend on nothing else.
+// best, in passes over all of K; a round costs 10% of one beside its work
+// (start and epilogue), a part's plane 1.5% (written and read again).  Of 7168
+// x 256, us of routing at 384 / 1024 / 2048 tokens: 8 parts 19.4 / 20.2 / 25.1,
+// 14 or as many as fit 20.3 / 22.4 / 24.8 (5 at 2048: 26.8).  From the sizes
+// alone, so the logits depend on nothing else.
 int router_pair_parts(int64_t T, int64_t E, int64_t H) {
     const int n = router_pair_cols((int)E);
     const int64_t tiles = (T + 255) / 256 * ((E + n - 1) / n);
     int best = 1;
     double least = 1e30;
-    for (int s = 1; s <= kRouterPairMaxParts && s * 2 <= H / kSlice; ++s) {
-        const double cost = (double)((tiles * s + 75) / 76) / s + 0.04 * s;
+    for (int s = 1; s == 1 || (s <= kRouterPairMaxParts && s * 4 <= H / kSlice); ++s) {
+        const double cost = (double)((tiles * s + 75) / 76) * (1.0 / s + 0.1) + 0.015 * s;
         if (cost < least - 1e-9) {
             least = cost;
             best = s;
