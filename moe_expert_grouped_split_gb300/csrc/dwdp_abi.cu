@@ -216,8 +216,7 @@ WsLayout ws_layout(const dwdp_config& c, int64_t T) {
     const int64_t H = c.hidden, I = c.inter, E = c.n_experts, k = c.top_k, S = c.n_shared;
     const int fmt = c.weight_dtype;
     L.logits = 0;  // the partial-sum planes of the router GEMM
-    const int64_t planes = std::max(kRouterMaxSplit, router_pair_parts(T, E, H));
-    L.group = align_up((size_t)(planes * T * E * 4), 256);
+    L.group = align_up((size_t)(std::max(kRouterMaxSplit * T, router_pair_plane_rows(T)) * router_pair_pitch(E) * 4), 256);
     L.route_bytes = L.group + align_up(std::max(group_chunked_scratch_bytes((int)(T * k), (int)E),
                                                 (size_t)scored_chunks(T, k) * E * 4), 256);
     size_t o = 0;
@@ -873,17 +872,21 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
     p.in_one = scored_in_one(T, c.top_k, p.parts);
     const int64_t n_zero = p.in_one ? 0 : (int64_t)p.chunks * c.n_experts;
     if (small) {
+        p.pitch = c.n_experts;
         logits = out->logits ? out->logits : planes;
         DWDP_CUDA(ctx, launch_router_small(x, w_router, T, c.n_experts, c.hidden, logits, p.hist, n_zero, stream));
     } else {
         RouterPairArgs r;
-        logits = out->logits && p.parts == 1 ? out->logits : planes;
+        p.pitch = router_pair_pitch(c.n_experts);
+        const bool straight = p.parts == 1 && p.pitch == c.n_experts;  // into out->logits
+        logits = out->logits && straight ? out->logits : planes;
+        p.z_out = straight ? nullptr : out->logits;
         const uint64_t row_bytes = 2ull * c.hidden;
         if (!encode_matrix(&r.tm_x, x, T, c.hidden, row_bytes, 128) ||
             !encode_matrix(&r.tm_w, w_router, c.n_experts, c.hidden, row_bytes, router_pair_cols(c.n_experts) / 2))
             return fail(ctx, DWDP_ERR_CUDA, "tensor map for the router GEMM");
         r.z = logits;
-        r.part_stride = (int64_t)T * c.n_experts;
+        r.pitch = p.pitch;
         r.T = T;
         r.E = c.n_experts;
         r.H = c.hidden;
@@ -894,11 +897,9 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
         DWDP_CUDA(ctx, launch_router_pair(r, stream));
     }
     p.logits = logits;
-    p.part_stride = (int64_t)T * c.n_experts;
     p.bias = choice_bias;
     p.ids = out->topk_ids;
     p.w = out->topk_w;
-    p.z_out = p.parts > 1 ? out->logits : nullptr;
     p.err = ctx->d_err;
     p.T = T;
     p.E = c.n_experts;

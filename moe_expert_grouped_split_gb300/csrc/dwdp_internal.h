@@ -235,23 +235,26 @@ constexpr int kRouterPairMaxParts = 8;
 struct RouterPairArgs {
     CUtensorMap tm_x, tm_w;
     float* z;
-    int64_t part_stride;
     int T, E, H, parts;
+    int pitch;  // of a row of z: E rounded up to router_pair_pitch
     int32_t* zero;
     int64_t n_zero;
     int* err;
 };
 int router_pair_cols(int E);
 int router_pair_parts(int64_t T, int64_t E, int64_t H);
+// Rows of all planes together are at most this many, for T tokens or fewer.
+int64_t router_pair_plane_rows(int64_t T);
+inline int64_t router_pair_pitch(int64_t E) { return (E + 7) / 8 * 8; }
 cudaError_t launch_router_pair(const RouterPairArgs& p, cudaStream_t s);
 
 // route_scored.cu: dwdp_route_scored from the logits on.  logits: `parts` fp32
-// planes [T][E] part_stride apart, summed in plane order; z_out, if not null,
+// planes [T][pitch], one after the other, summed in plane order; z_out [T][E], if not null,
 // receives the sums; hist: chunks x E counts, zero (in_one: not used).  The
 // last four members are filled by launch_scored_choice.
 struct ScoredArgs {
     const float* logits;
-    int64_t part_stride;
+    int pitch;
     const float* bias;
     int32_t* ids;
     float* w;

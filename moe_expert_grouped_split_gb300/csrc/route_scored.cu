@@ -135,19 +135,19 @@ __device__ __forceinline__ void load_run(const float* src, const Lane& ln, float
 // K-split router GEMM added in plane order.
 template <int P, bool FULL>
 __device__ __forceinline__ void load_logits(const ScoredArgs& p, int64_t t, const Lane& ln, float (&z)[P]) {
-    load_run<P, FULL>(p.logits + t * p.E, ln, z);
+    load_run<P, FULL>(p.logits + t * p.pitch, ln, z);
 #pragma unroll 1
     for (int q = 1; q < p.parts; ++q) {
         float u[P];
-        load_run<P, FULL>(p.logits + q * p.part_stride + t * p.E, ln, u);
+        load_run<P, FULL>(p.logits + (q * (int64_t)p.T + t) * p.pitch, ln, u);
 #pragma unroll
         for (int j = 0; j < P; ++j) z[j] += u[j];
     }
 }
 
 __device__ __forceinline__ float logit_of(const ScoredArgs& p, int64_t t, int e) {
-    float v = p.logits[t * p.E + e];
-    for (int q = 1; q < p.parts; ++q) v += p.logits[q * p.part_stride + t * p.E + e];
+    float v = p.logits[t * p.pitch + e];
+    for (int q = 1; q < p.parts; ++q) v += p.logits[(q * (int64_t)p.T + t) * p.pitch + e];
     return v;
 }
 

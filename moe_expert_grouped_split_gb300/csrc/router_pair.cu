@@ -1,5 +1,6 @@
 // router_pair.cu: the router's logits for many tokens (dwdp_route_scored):
-// planes z[part] [T][E] = x W^T over the part's K, fp32.
+// planes z[part] [T][pitch] = x W^T over the part's K, fp32 (zeros from expert
+// E on, so that a row is whole 32-byte sectors).
 //
 // What bounds it: 8192 x 7168 x 256 is 30 GFLOP, 16 us at the measured bf16
 // rate, and x comes from HBM once, 117 MB, 17 us; it takes about 28 us.  The
@@ -178,9 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.err, DERR_EPI_WAIT))) {
             tc_fence_after();
             const int t = row0 + 32 * q + lane;
-            float* row = p.z + (int64_t)part * p.part_stride + (int64_t)t * p.E + e0;
-            // whole sectors, where rows lie on them
-            const bool wide = p.E % 8 == 0 && (uint64_t)p.z % 32 == 0;
+            float* row = p.z + ((int64_t)part * p.T + t) * p.pitch + e0;
+            const bool wide = (uint64_t)p.z % 32 == 0;  // whole sectors
 #pragma unroll 1
             for (int c = 0; c < N; c += 32) {
                 uint32_t v[32];
@@ -189,13 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (t >= p.T) continue;
 #pragma unroll
                 for (int j = 0; j < 32; j += 8) {
-                    const int e = c + j;
-                    if (wide && e0 + e < p.E) {
-                        store8(row + e, v + j);
-                    } else if (!wide) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (e0 + e + i < p.E) row[e + i] = __uint_as_float(v[j + i]);
+                    if (e0 + c + j >= p.pitch) break;
+                    if (wide) {
+                        store8(row + c + j, v + j);
+                    } else {
+                        *reinterpret_cast<uint4*>(row + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        *reinterpret_cast<uint4*>(row + c + j + 4) = make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
                     }
                 }
             }
@@ -246,6 +245,7 @@ int router_pair_parts(int64_t T, int64_t E, int64_t H) {
     int best = 1;
     double least = 1e30;
     for (int s = 1; s == 1 || (s <= kRouterPairMaxParts && s * 4 <= H / kSlice); ++s) {
+        if (s > 4 && tiles * s > 76) break;  // (what router_pair_plane_rows counts on)
         const double cost = (double)((tiles * s + 75) / 76) * (1.0 / s + 0.1) + 0.015 * s;
         if (cost < least - 1e-9) {
             least = cost;
@@ -253,6 +253,11 @@ int router_pair_parts(int64_t T, int64_t E, int64_t H) {
         }
     }
     return best;
+}
+
+// More than 4 parts only where 256-token tiles x parts <= 76.
+int64_t router_pair_plane_rows(int64_t T) {
+    return std::max<int64_t>(4 * T, std::min<int64_t>(kRouterPairMaxParts * T, 76 * 256));
 }
 
 cudaError_t launch_router_pair(const RouterPairArgs& p, cudaStream_t s) {

@@ -284,3 +284,32 @@ def test_refusals():
         assert ei.value.code == -5
     finally:
         big.close()
+
+
+@pytest.mark.parametrize("H, E, k", [(64, 1020, 1), (7168, 256, 8), (2048, 60, 4)])
+def test_workspace_of_more_tokens_is_enough_for_fewer(H, E, k):
+    rt = B.Runtime(H, 64, E, k, 0, 30000, 1, 0)
+    try:
+        need = [B.lib().dwdp_workspace_bytes(rt.ctx, T) for T in list(range(1, 5000, 3)) + list(range(5000, 30000, 101))]
+        assert need == sorted(need)
+    finally:
+        rt.close()
+
+
+@pytest.mark.parametrize("T, H, E", [(600, 320, 148), (300, 64, 300), (1100, 1024, 20), (65, 576, 1020)])
+def test_logits_of_experts_that_are_no_whole_sectors(T, H, E):
+    x = I.randn_bf16((T, H), 1.0, 41, "cuda")
+    w = I.randn_bf16((E, H), I.sqrt_inv(H), 42, "cuda")
+    rt, rb = B.Runtime(H, 64, E, 4, 0, T, 1, 0), B.RouteBuffers(T, E, 4, keep_logits=True)
+    rb.logits.fill_(float("nan"))
+    try:
+        rt.route_scored(x, w, None, how_of(SIG), rb)
+        torch.cuda.synchronize()
+        assert rt.device_status() == 0
+    finally:
+        rt.close()
+    want = x.double() @ w.double().t()
+    # binary32 sums of H products
+    assert bool(((rb.logits.double() - want).abs() <= 2.0 ** -20 * (x.double().abs() @ w.double().abs().t())).all())
+    best = rb.logits.topk(4, dim=1).indices.sort(dim=1).values
+    assert torch.equal(best.int(), rb.topk_ids[:T])
