@@ -989,12 +989,12 @@ int32_t dwdp_lora_add(dwdp_ctx* ctx, const void* x, int64_t x_stride, int32_t T,
     p.ws = ws;
     p.err = ctx->d_err;
     p.n_sms = ctx->n_sms;
-    if (!lora_is_long(T)) {
+    if (T >= kLoraMapTokens && (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(a, ctx->device)))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and a must be device memory of the context's device (%d)", ctx->device);
+    if (!lora_is_long(T, K, N)) {
         DWDP_CUDA(ctx, launch_lora_add(p, stream));
         return DWDP_OK;
     }
-    if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(a, ctx->device))  // read through tensor maps
-        return fail(ctx, DWDP_ERR_INVALID_ARG, "x and a must be device memory of the context's device (%d)", ctx->device);
     LoraTcArgs q;
     q.lora = p;
     q.parts = lora_tc_parts(T, R, ctx->n_sms);

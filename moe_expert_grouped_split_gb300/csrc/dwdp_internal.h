@@ -308,7 +308,8 @@ struct LoraTcArgs {
     CUtensorMap tm_x, tm_a;
     int parts;  // lora_tc_parts
 };
-bool lora_is_long(int64_t T);
+constexpr int kLoraMapTokens = 1024;  // from here on x and a have to suit a tensor map
+bool lora_is_long(int64_t T, int64_t K, int64_t N);
 int lora_tc_parts(int64_t T, int R, int n_sms);
 cudaError_t launch_lora_tc(const LoraTcArgs& p, cudaStream_t s);
 

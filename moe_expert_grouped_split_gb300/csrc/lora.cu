@@ -2,8 +2,8 @@
 // (dwdp_lora_add): out[t] = base[t] + s_i (x[t] A_i^T) B_i^T, i the token's
 // adapter.  Memory-bound: x, base, out and the used adapters once.
 //
-// A handful of tokens: one kernel (lora_one_kernel).  More, below 1024: two
-// kernels, v = bf16(s_i x A_i^T) [T][R] between them:
+// A handful of tokens: one kernel (lora_one_kernel).  More, up to where
+// lora_tc.cu takes over: two kernels, v = bf16(s_i x A_i^T) [T][R] between them:
 //   shrink  a cluster of 2 to 8 CTAs per tile of up to 16 tokens, each warp a
 //           part of K; the parts meet in distributed shared memory, in order
 //   expand  token tile x 256 columns per CTA, base and out in 16-byte vectors

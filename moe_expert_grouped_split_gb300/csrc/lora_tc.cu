@@ -1,4 +1,4 @@
-// lora_tc.cu: dwdp_lora_add for many tokens, fed by TMA.
+// lora_tc.cu: dwdp_lora_add for many tokens (lora_is_long), fed by TMA.
 //
 // Both halves stream: x once (shrink), base in and out once (expand); the
 // adapters stay in L2.  What counts is bytes in flight and their order, so the
@@ -457,7 +457,13 @@ int lora_tc_parts(int64_t T, int R, int n_sms) {
     return parts;
 }
 
-bool lora_is_long(int64_t T) { return T >= 1024; }
+// Where these kernels take over from lora.cu's (here / there, us, 20 requests).
+// 2048 x 1536, rank 64: 2048 tokens 20.7 / 18.5, 3000 22.7 / 28.5; 520 x 6000,
+// rank 8: 18.7 / 16.5, 21.7 / 24.3; 7168 x 7168, rank 16: 1024 tokens 20.7 /
+// 23.1, 1300 22.4 / 25.3, 2048 25.5 / 31.0.
+bool lora_is_long(int64_t T, int64_t K, int64_t N) {
+    return T > 2048 || (T >= kLoraMapTokens && T * (K + N) > 16 << 20);
+}
 
 cudaError_t launch_lora_tc(const LoraTcArgs& p, cudaStream_t s) {
     const int R = p.lora.R;

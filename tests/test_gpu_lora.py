@@ -227,3 +227,32 @@ def test_bank_of_too_many_rows_is_refused():
         assert ei.value.code == -5
     finally:
         rt.close()
+
+
+@pytest.mark.parametrize("K, N, R", SIZES + [(72, 264, 16), (7168, 520, 16), (1000, 1000, 32)])
+@pytest.mark.parametrize("T", [2049, 2200])
+@pytest.mark.parametrize("order", ["one", "runs", "mixed"])
+def test_sizes_of_more_tokens(K, N, R, T, order):
+    test_sizes(T, K, N, R, order)
+
+
+@pytest.mark.parametrize("T, K, N", [(1024, 8192, 8192), (1023, 8192, 8200), (1100, 8, 16384)])
+@pytest.mark.parametrize("order", ["runs", "mixed"])
+def test_wide_rows_around_a_thousand_tokens(T, K, N, order):
+    test_sizes(T, K, N, 16, order)
+
+
+def test_many_strided_tokens_in_place():
+    test_row_strides_and_in_place(2500)
+
+
+def test_many_tokens_with_bad_ids():
+    test_ids_outside_the_bank_are_reported_and_skipped(2300)
+
+
+def test_nan_among_many_tokens():
+    test_nan_stays_with_its_token_and_adapter(2300)
+
+
+def test_many_tokens_each_its_own_adapter():
+    test_every_token_its_own_adapter(2100)
