@@ -542,7 +542,8 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
  * a: bf16 [n_adapters][R][K]; b: bf16 [n_adapters][N][R]; adapter_scale fp32
  * [n_adapters]; adapter_ids int32 [T] (all device).  Adapters of a smaller
  * rank are padded with zero rows (columns).  Tokens may come in any order;
- * tokens of one adapter next to each other are the cheap case.  x: row t at
+ * tokens of one adapter next to each other are the cheap case (above 2048
+ * tokens, or in banks of 256 adapters and more, the only one).  x: row t at
  * x + t * x_stride elements, K of them; base and out: row t at t *
  * base_stride / t * out_stride, N of them; every stride a multiple of 8 and
  * no smaller than the row.  out may be base (equal strides); no other

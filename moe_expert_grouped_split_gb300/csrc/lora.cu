@@ -17,6 +17,8 @@
 // the chain load, multiply, exchange in the cluster, launch, load, store.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "dwdp_internal.h"
 #include "lora_ops.h"
 
@@ -27,6 +29,94 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kNone = kNoAdapter;  // a row without an adapter
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+
+// ------------------------------------------------------ tokens by adapter --
+// A batch whose tokens' adapters change from token to token costs a tile as
+// many products as it has adapters.  So where they change at half of 32 places
+// or more, tiles of more than 4 tokens take the tokens in the order of their
+// adapters (stable, those without one last): every block finds the same order
+// and keeps its own tile's part.  A row's result does not depend on its tile.
+// 16 adapters at random, us without / with it: 7168 x 7168, rank 16: 128
+// tokens 12.8 / 11.6, 256 17.7 / 12.1, 1000 60 / 31; 2048 x 1536, rank 64: 256
+// 31 / 11.4, 1000 56 / 20.  Looking costs tokens that are in order 0.5 us (256
+// of 20 requests 8.1 / 8.6).
+constexpr int kOrderTokens = 2048;  // at most
+constexpr int kOrderBins = 256;  // adapters, and one for tokens without
+constexpr int kOrderRows = 64;   // of a tile at most
+
+// Shared memory: start[bins], count[bins], sums[warps], then the pairs by chunk
+// of 32 tokens and adapter, a byte each.
+__host__ __device__ inline int order_pitch(const LoraArgs& p) { return (p.n_adapters + 4) / 4 * 4; }
+bool may_order(const LoraArgs& p, int rows) {
+    return rows > 4 && p.T <= kOrderTokens && p.n_adapters < kOrderBins;
+}
+size_t order_bytes(const LoraArgs& p) {
+    return (2 * kOrderBins + kWarps) * 4 + (size_t)((p.T + 31) / 32) * order_pitch(p);
+}
+
+// Whether the tile at t0 takes tokens order[0 .. rows) (p.T: none) instead of
+// t0, t0 + 1, ...  Called by the whole block.
+__device__ __forceinline__ bool order_tile(const LoraArgs& p, int t0, int rows, void* mem, int* order) {
+    constexpr int kMine = kOrderTokens / kThreads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // neighbours at 32 places of the batch, the same for every warp; and the
+    // tile's own ids on their way
+    const int2 two = reinterpret_cast<const int2*>(p.ids)[(int64_t)lane * (p.T / 2) / 32];
+    const int own = p.ids[min(t0 + lane, p.T - 1)];
+    asm volatile("" ::"r"(own));
+    if (__popc(__ballot_sync(kFull, two.x != two.y)) < 16) return false;
+    int bin[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        bin[i] = -1;
+        if (i * kThreads >= p.T) continue;
+        const int t = (warp + kWarps * i) * 32 + lane;
+        bin[i] = t < p.T ? (int)min(adapter_of(p, t, true), (uint32_t)p.n_adapters) : -1;
+    }
+    int *const start = static_cast<int*>(mem), *const count = start + kOrderBins, *const sums = count + kOrderBins;
+    uint8_t* const in_chunk = reinterpret_cast<uint8_t*>(sums + kWarps);
+    const int pitch = order_pitch(p), words = (p.T + 31) / 32 * pitch / 4;
+    count[tid] = 0;
+    for (int i = tid; i < words; i += kThreads) reinterpret_cast<uint32_t*>(in_chunk)[i] = 0;
+    if (tid < rows) order[tid] = p.T;
+    __syncthreads();
+    int before[kMine] = {};  // of the same adapter in the chunk
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        if (i * kThreads >= p.T) continue;
+        const uint32_t same = __match_any_sync(kFull, bin[i]);
+        before[i] = __popc(same & ((1u << lane) - 1u));
+        if (bin[i] >= 0 && before[i] == 0) {
+            in_chunk[(warp + kWarps * i) * pitch + bin[i]] = (uint8_t)__popc(same);
+            atomicAdd(count + bin[i], __popc(same));
+        }
+    }
+    __syncthreads();
+    int at = count[tid];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += u;
+    }
+    if (lane == 31) sums[warp] = at;
+    __syncthreads();
+    at -= count[tid];
+    for (int w = 0; w < warp; ++w) at += sums[w];
+    start[tid] = at;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int b = max(bin[i], 0), chunk = warp + kWarps * i;
+        int r = start[b] - t0;
+        if (bin[i] >= 0 && r < rows && r + count[b] > 0) {
+            r += before[i];
+            for (int c = 0; c < chunk; ++c) r += in_chunk[c * pitch + b];
+            if (r >= 0 && r < rows) order[r] = chunk * 32 + lane;
+        }
+    }
+    __syncthreads();
+    return true;
+}
 
 // 16 rows of x against A_i: a cluster of C blocks of 8 warps, each warp a part
 // of K; NT n8 tiles hold the rank.  A step is 32 elements of K.
@@ -104,9 +194,10 @@ struct Shrink {
 
 // The tile's partial sums over this block's part of K in part[0] ([16][NT * 8]
 // floats of shared memory for every warp); rows without an adapter hold
-// anything.  Ends with the block in step.
-template <int NT, int C>
-__device__ __forceinline__ void shrink_tile(const LoraArgs& p, int t0, int tile_rows, uint32_t rank, float* part) {
+// anything.  token(r): the tile's r-th token, p.T or more: none.  Ends with the
+// block in step.
+template <int NT, int C, class Token>
+__device__ __forceinline__ void shrink_tile(const LoraArgs& p, Token token, int tile_rows, uint32_t rank, float* part) {
     using S = Shrink<NT, C>;
     // adapters a mixed pass takes at once, and steps in flight with one and
     // with several: what the registers hold
@@ -117,10 +208,10 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& p, int t0, int tile_
     const uint4* xr[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = i * 8 + g, t = t0 + r;
-        const bool in = r < tile_rows && t < p.T;
+        const int r = i * 8 + g, t = r < tile_rows ? token(r) : p.T;
+        const bool in = t < p.T;
         left[i] = id[i] = adapter_of(p, t, in);
-        xr[i] = static_cast<const uint4*>(p.x) + (int64_t)(in ? t : t0) * (p.x_stride / 8);
+        xr[i] = static_cast<const uint4*>(p.x) + (int64_t)(in ? t : 0) * (p.x_stride / 8);
         if (rank == 0 && warp == 0 && in && id[i] == kNone && p.ids[t] != -1) atomicOr(p.err, DERR_BAD_INDEX);
     }
     const int steps = (p.K + 31) / 32, at = (int)rank * kWarps + warp;
@@ -152,17 +243,20 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& p, int t0, int tile_
     __syncthreads();
 }
 
-template <int NT, int C>
+template <int NT, int C, bool ORDER>
 __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) __cluster_dims__(C, 1, 1)
     lora_shrink_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
     using S = Shrink<NT, C>;
     extern __shared__ float part[];  // [warps][16][NT * 8], then what the cluster sends [C][this rank's share]
+    __shared__ int order[kOrderRows];
     wait_for_previous_kernel();
     let_next_kernel_start();
     cluster_arrive();
     const int t0 = (int)(blockIdx.x / C) * tile_rows;
     const uint32_t rank = cluster_rank();
-    shrink_tile<NT, C>(p, t0, tile_rows, rank, part);
+    const bool ordered = ORDER && order_tile(p, t0, tile_rows, part, order);
+    auto token = [&](int r) { return ordered ? order[r] : t0 + r; };
+    shrink_tile<NT, C>(p, token, tile_rows, rank, part);
     // the K parts of the block, then of the cluster: rank e / share gets
     // element e of every rank, and adds them in order
     const int n = tile_rows * NT * 8, share = n / C;
@@ -179,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 8 ? 2 : 1) __cluster_dims__(C,
     cluster_wait();
     __nv_bfloat16* v = static_cast<__nv_bfloat16*>(p.ws);
     for (int i = threadIdx.x; i < share; i += kThreads) {
-        const int e = (int)rank * share + i, r = e / (NT * 8), c = e % (NT * 8), t = t0 + r;
+        const int e = (int)rank * share + i, r = e / (NT * 8), c = e % (NT * 8), t = token(r);
         if (c >= p.R) continue;
         const uint32_t a = adapter_of(p, t, t < p.T);
         if (a == kNone) continue;
@@ -218,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(8, 1, 1)
     const uint4 bs[2] = {mine ? *(static_cast<const uint4*>(p.base) + t * (p.base_stride / 8) + c0 / 8 + q) : none, none};
     uint2 bf[KS][4];
     X::load_b(p, id, min(c0, p.N - 8), lane, bf);
-    shrink_tile<NT, C>(p, t, 1, rank, part);
+    shrink_tile<NT, C>(p, [&](int) { return t; }, 1, rank, part);
     cluster_wait();  // everybody runs: its shared memory may be written
     for (int e = threadIdx.x; e < kRank; e += kThreads) {
         float s = part[e];
@@ -251,35 +345,46 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(8, 1, 1)
 
 // A warp takes MT m16 tiles and 32 columns.  base is the accumulator's start,
 // so a row's result does not depend on the tile's other rows.
-template <int KS, int MT>
+template <int KS, int MT, bool ORDER>
 __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_constant__ LoraArgs p, int tile_rows) {
     using X = Expand<KS>;
     constexpr int G = MT > 1 || KS > 1 ? 1 : 2;  // adapters whose B is loaded together
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int t0 = (int)blockIdx.x * tile_rows, c0 = ((int)blockIdx.y * (kThreads / 32) + warp) * 32;
-    if (c0 >= p.N) return;  // a whole warp beyond the columns
+    __shared__ int order[kOrderRows];
+    extern __shared__ int order_mem[];
     const bool col_in = c0 + 8 * q < p.N;
     const int rv = p.R / 4;
     // base and the ids do not come from the kernel before this one, which
     // lets this one start only after everything before it is done
     uint32_t id[MT][2], most = 0, least = kNone;
     uint4 bs[MT][2];
-    const uint4* base = static_cast<const uint4*>(p.base) + (int64_t)(t0 + g) * (p.base_stride / 8) + c0 / 8 + q;
+    int token[MT][2];  // p.T: none
+    const uint4* base = static_cast<const uint4*>(p.base) + c0 / 8 + q;
+    auto fetch = [&](auto of) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m * 16 + h * 8 + g, t = token[m][h] = r < tile_rows ? of(r) : p.T;
+                bs[m][h] = t < p.T && col_in ? base[t * (p.base_stride / 8)] : make_uint4(0, 0, 0, 0);
+                id[m][h] = adapter_of(p, t, t < p.T);
+            }
+    };
+    fetch([&](int r) { return min(t0 + r, p.T); });
+    if (ORDER && order_tile(p, t0, tile_rows, order_mem, order)) fetch([&](int r) { return order[r]; });
+    if (c0 >= p.N) return;  // a whole warp beyond the columns
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = m * 16 + h * 8, t = t0 + r + g;
-            const bool in = r + g < tile_rows && t < p.T;
-            bs[m][h] = in && col_in ? base[r * (p.base_stride / 8)] : make_uint4(0, 0, 0, 0);
-            id[m][h] = adapter_of(p, t, in);
             most = max(most, id[m][h]);
             least = min(least, id[m][h]);
         }
     least = __reduce_min_sync(kFull, least);
     most = __reduce_max_sync(kFull, most);
-    const uint2* v = static_cast<const uint2*>(p.ws) + (int64_t)(t0 + g) * rv + q;
-    uint4* out = static_cast<uint4*>(p.out) + (int64_t)(t0 + g) * (p.out_stride / 8) + c0 / 8 + q;
+    const uint2* v = static_cast<const uint2*>(p.ws) + q;
+    uint4* out = static_cast<uint4*>(p.out) + c0 / 8 + q;
     uint2 bf[G][KS][4];
     if (MT > 1 && least == most && least != kNone) {  // one adapter, every row in use
         X::load_b(p, least, c0, lane, bf[0]);
@@ -291,14 +396,14 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_cons
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                    vf[m][h][s] = s * 4 + q < rv ? v[(m * 16 + h * 8) * rv + s * 4] : make_uint2(0, 0);
+                    vf[m][h][s] = s * 4 + q < rv ? v[(int64_t)token[m][h] * rv + s * 4] : make_uint2(0, 0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             float d[4][4];
             X::product(bs[m], vf[m], bf[0], d);
             if (col_in) {
-                out[m * 16 * (p.out_stride / 8)] = X::round(d, 0);
-                out[(m * 16 + 8) * (p.out_stride / 8)] = X::round(d, 1);
+                out[token[m][0] * (p.out_stride / 8)] = X::round(d, 0);
+                out[token[m][1] * (p.out_stride / 8)] = X::round(d, 1);
             }
         }
         return;
@@ -309,6 +414,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_cons
     for (int m = 0; m < MT; ++m) {
         uint32_t mid[2] = {id[0][0], id[0][1]};
         uint4 mb[2] = {bs[0][0], bs[0][1]};
+        int mt[2] = {token[0][0], token[0][1]};
 #pragma unroll
         for (int i = 1; i < MT; ++i)  // (constant indexes keep the arrays in registers)
             if (i == m) {
@@ -316,6 +422,8 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_cons
                 mid[1] = id[i][1];
                 mb[0] = bs[i][0];
                 mb[1] = bs[i][1];
+                mt[0] = token[i][0];
+                mt[1] = token[i][1];
             }
         uint32_t left[2] = {mid[0], mid[1]};
         uint2 vf[2][KS];
@@ -342,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_cons
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int s = 0; s < KS; ++s)
-                        vf[h][s] = mid[h] != kNone && s * 4 + q < rv ? v[(m * 16 + h * 8) * rv + s * 4]
+                        vf[h][s] = mid[h] != kNone && s * 4 + q < rv ? v[(int64_t)mt[h] * rv + s * 4]
                                                                      : make_uint2(0, 0);
 #pragma unroll
             for (int s = 0; s < G; ++s) {
@@ -356,16 +464,14 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const __grid_cons
         // a tile without adapters has waited for nothing: out may be base,
         // which only this thread reads
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = m * 16 + h * 8;
-            if (r + g < tile_rows && t0 + r + g < p.T && col_in) out[r * (p.out_stride / 8)] = o[h];
-        }
+        for (int h = 0; h < 2; ++h)
+            if (mt[h] < p.T && col_in) out[mt[h] * (p.out_stride / 8)] = o[h];
     }
     if (!waited) wait_for_previous_kernel();
 }
 
 cudaError_t launch(const void* kernel, dim3 grid, size_t smem, cudaStream_t s, const LoraArgs& p, int tile_rows) {
-    if (smem > 48 << 10) {
+    if (smem > 40 << 10) {  // beside the static part, beyond what a launch gets unasked
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
@@ -385,8 +491,17 @@ cudaError_t launch(const void* kernel, dim3 grid, size_t smem, cudaStream_t s, c
 
 template <int NT, int C>
 cudaError_t launch_shrink(const LoraArgs& p, int rows, cudaStream_t s) {
-    return launch((const void*)lora_shrink_kernel<NT, C>, dim3((p.T + rows - 1) / rows * C), Shrink<NT, C>::kSmem, s, p,
-                  rows);
+    const bool order = may_order(p, rows);
+    const size_t smem = std::max((size_t)Shrink<NT, C>::kSmem, order ? order_bytes(p) : 0);
+    const void* kernel = order ? (const void*)lora_shrink_kernel<NT, C, true> : (const void*)lora_shrink_kernel<NT, C, false>;
+    return launch(kernel, dim3((p.T + rows - 1) / rows * C), smem, s, p, rows);
+}
+
+template <int KS, int MT>
+cudaError_t launch_expand(const LoraArgs& p, int rows, int cols, cudaStream_t s) {
+    const bool order = may_order(p, rows);
+    const void* kernel = order ? (const void*)lora_expand_kernel<KS, MT, true> : (const void*)lora_expand_kernel<KS, MT, false>;
+    return launch(kernel, dim3((p.T + rows - 1) / rows, cols), order ? order_bytes(p) : 0, s, p, rows);
 }
 
 template <int NT>
@@ -415,8 +530,8 @@ cudaError_t launch_rank(const LoraArgs& p, cudaStream_t s) {
     constexpr int KS = NT / 2;
     const int cols = (p.N + 255) / 256;
     if ((int64_t)((p.T + 63) / 64) * cols >= 2 * p.n_sms)
-        return launch((const void*)lora_expand_kernel<KS, 4>, dim3((p.T + 63) / 64, cols), 0, s, p, 64);
-    return launch((const void*)lora_expand_kernel<KS, 1>, dim3((p.T + rows - 1) / rows, cols), 0, s, p, rows);
+        return launch_expand<KS, 4>(p, 64, cols, s);
+    return launch_expand<KS, 1>(p, rows, cols, s);
 }
 
 }  // namespace

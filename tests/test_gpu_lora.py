@@ -256,3 +256,14 @@ def test_nan_among_many_tokens():
 
 def test_many_tokens_each_its_own_adapter():
     test_every_token_its_own_adapter(2100)
+
+
+@pytest.mark.parametrize("n", [3, 255, 256])
+@pytest.mark.parametrize("T", [39, 64, 65, 129, 257, 1000, 2047, 2048])
+def test_any_order_of_tokens(T, n):
+    ids = np.random.default_rng(T + n).integers(-1, n, T)
+    ids[-1] = n - 1
+    args = case(T, 520, 296, 16, n, ids, seed=T)
+    check(run(*args), *args)
+    base = args[-1].clone()
+    assert torch.equal(run(*args[:-1], base, out=base), run(*args))
