@@ -2,7 +2,10 @@
 //
 // Kernels live in gemm.cu (split-pointer grouped GEMM, tcgen05 + TMA) and
 // route.cu (top-k, grouping, row scatter into expert order, combine, and the
-// E4M3 / NVFP4 activation quantizers); dwdp_abi.cu is the C ABI.
+// E4M3 / NVFP4 activation quantizers); what surrounds the layer in a decoder
+// block in norm.cu (residual addition + norm), router.cu, router_pair.cu and
+// route_scored.cu (scored routing), lora.cu and lora_tc.cu (adapters);
+// dwdp_abi.cu is the C ABI.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap (type only; the driver is reached through an entry point)

@@ -12,8 +12,8 @@
 // come in any order, and values of one adapter never meet another's rows.
 // A step is at most 2 R flops a byte of x: far from the tensor rate, so the
 // warp-level MMA on operands straight from global memory is enough.
-// 64 tokens of 64 adapters, 7168 x 7168, rank 16 (32 MB): 9.5 us, 3.4 TB/s;
-// 517 tokens of 11 requests, 2048 x 1536, rank 64: 10.3 us.  What bounds both is
+// 64 tokens of 64 adapters, 7168 x 7168, rank 16 (32 MB): 9.6 us, 3.3 TB/s;
+// 517 tokens of 11 requests, 2048 x 1536, rank 64: 10.7 us.  What bounds both is
 // the chain load, multiply, exchange in the cluster, launch, load, store.
 #include <cuda_bf16.h>
 

@@ -9,7 +9,7 @@
 //           parts meet in the owner's shared memory, in rank order
 //   expand  staying CTAs walk stages of 16 tokens x 512 columns: load, add
 //           v B^T in place, store
-// 8192 tokens, 7168 x 7168, rank 16: 73.7 us for 360 MB, 4.9 TB/s (72% of the
+// 8192 tokens, 7168 x 7168, rank 16: 73.5 us for 360 MB, 4.9 TB/s (72% of the
 // copy rate): shrink 25 us, expand 46 us.
 // A tile's tokens may have any adapters: shrink multiplies the tile by each
 // that occurs (several at a time) and keeps a row's own; so does expand.

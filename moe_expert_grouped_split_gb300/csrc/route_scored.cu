@@ -1,9 +1,9 @@
 // route_scored.cu: what dwdp_route_scored does with the router's logits:
 // scores, choice values, groups of experts, top-k and weights, one warp per
 // token, and the grouping of the pairs by expert.  A few bytes a token: bound
-// by latency for few tokens and by instructions (about 900 a token of 256
+// by latency for few tokens and by instructions (about 1000 a token of 256
 // experts) for many.  8 of 256 experts in 4 of 8 groups, with the router GEMM
-// of H = 7168: 1 token 7.5 us, 256 tokens 17.8, 8192 tokens 47.5, of which the
+// of H = 7168: 1 token 7.5 us, 256 tokens 17.9, 8192 tokens 47.7, of which the
 // GEMM about 28, the choice 13 and the grouping 6.
 #include <cuda_bf16.h>
 #include <math_constants.h>
