@@ -29,6 +29,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+__device__ __forceinline__ float rcp(float a) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+
 __device__ __forceinline__ void unpack8(uint4 q, float (&f)[8]) {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
 #pragma unroll
@@ -52,24 +58,25 @@ __device__ __forceinline__ void copy16(uint4* to, const uint4* from) {
                  : "memory");
 }
 
+// m: magnitudes, whose order as floats is their bits' (a NaN is above +inf).
+template <bool MAX>
 __device__ __forceinline__ void warp_sum_max(float& s, float& m) {
+    if constexpr (MAX) m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 }
 
 // (sum, max) over the block; every thread gets them.
+template <bool MAX>
 __device__ __forceinline__ float2 block_sum_max(float s, float m, float2* red) {
-    warp_sum_max(s, m);
+    warp_sum_max<MAX>(s, m);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     if (lane == 0) red[warp] = make_float2(s, m);
     __syncthreads();
     const float2 v = lane < nw ? red[lane] : make_float2(0.0f, 0.0f);
     s = v.x;
     m = v.y;
-    warp_sum_max(s, m);
+    warp_sum_max<MAX>(s, m);
     __syncthreads();  // red may be written again
     return make_float2(s, m);
 }
@@ -87,7 +94,8 @@ struct NormArgs {
     const uint4* weight;
     float eps;
     int64_t rows;
-    int nv;  // vectors a row
+    int nv;         // vectors a row
+    float one_nth;  // 1 / H
     uint4* out;
     uint2* codes;
     float* row_scale;
@@ -134,15 +142,17 @@ __device__ __forceinline__ void give(const NormArgs& p, int64_t at, const float 
     }
 }
 
-// A row's two factors from its sums; `first` writes the row's scale.
+// A row's two factors from its sums; `first` writes the row's scale.  Every
+// thread does this, so by the approximate instructions: a few units in the
+// last place, where the roundings to come are 2^-8 and 2^-4.
 template <bool CODES>
 __device__ __forceinline__ void factors(const NormArgs& p, int64_t row, float ss, float mx, float eps, bool first,
                                         float& rs, float& inv) {
-    rs = 1.0f / sqrtf(ss / (float)(8 * p.nv) + eps);
+    rs = rsqrtf(fmaf(ss, p.one_nth, eps));
     inv = 0.0f;
     if constexpr (CODES) {
         const float m = mx == 0.0f ? 0.0f : max_nan(mx, kMinCodeMax);
-        inv = m == 0.0f ? 0.0f : 448.0f / m;
+        inv = m == 0.0f ? 0.0f : 448.0f * rcp(m);
         if (first) p.row_scale[row] = m == 0.0f ? 1.0f : m * rs / 448.0f;
     }
 }
@@ -188,12 +198,12 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant
             held = j + 1;
         }
     }
-    float2 sums = block_sum_max(ss, mx, red);
+    float2 sums = block_sum_max<CODES>(ss, mx, red);
     float eps = p.eps;
     if (!(sums.x < kSquaresLimit)) {  // rare; the whole block agrees
         take_scaled<VPT, CODES>(h, w, held, ss, mx);
         eps = p.eps * kDownScale * kDownScale;
-        sums = block_sum_max(ss, mx, red);
+        sums = block_sum_max<CODES>(ss, mx, red);
     }
     float rs, inv;
     factors<CODES>(p, row, sums.x, sums.y, eps, threadIdx.x == 0, rs, inv);
@@ -227,12 +237,12 @@ __global__ void __launch_bounds__(256) add_rmsnorm_warp_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
         if (j < held) take<RES, CODES>(p, row * p.nv + lane + 32 * j, x[j], r[j], w[j], h[j], ss, mx);
-    warp_sum_max(ss, mx);
+    warp_sum_max<CODES>(ss, mx);
     float eps = p.eps;
     if (!(ss < kSquaresLimit)) {
         take_scaled<VPT, CODES>(h, w, held, ss, mx);
         eps = p.eps * kDownScale * kDownScale;
-        warp_sum_max(ss, mx);
+        warp_sum_max<CODES>(ss, mx);
     }
     float rs, inv;
     factors<CODES>(p, row, ss, mx, eps, lane == 0, rs, inv);
@@ -273,13 +283,13 @@ __global__ void __launch_bounds__(1024, 1) add_rmsnorm_stream_kernel(const __gri
                              RES ? ring[(stage * kParts + 1) * n + tid] : make_uint4(0, 0, 0, 0), w[0], h[0], ss, mx);
         fetch(row + (int64_t)STAGES * gridDim.x, stage);
         auto block_sums = [&] {
-            warp_sum_max(ss, mx);
+            warp_sum_max<CODES>(ss, mx);
             if (lane == 0) red[half][warp] = make_float2(ss, mx);
             __syncthreads();
             const float2 v = lane < nw ? red[half][lane] : make_float2(0.0f, 0.0f);
             ss = v.x;
             mx = v.y;
-            warp_sum_max(ss, mx);
+            warp_sum_max<CODES>(ss, mx);
             half ^= 1;  // the next sums go to the other half: one barrier is enough
         };
         block_sums();
@@ -356,7 +366,7 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* resi
     if (rows <= 0) return cudaSuccess;
     const NormArgs p{static_cast<const uint4*>(x),      x_stride / 8, static_cast<const uint4*>(residual),
                      static_cast<uint4*>(residual_out), static_cast<const uint4*>(weight),
-                     eps,                               rows,         H / 8,
+                     eps,                               rows,         H / 8, 1.0f / (float)H,
                      static_cast<uint4*>(out),          static_cast<uint2*>(codes), row_scale};
     if (residual && codes) return launch_form<true, true>(p, s);
     if (residual) return launch_form<true, false>(p, s);
