@@ -251,25 +251,21 @@ __global__ void __launch_bounds__(256) add_rmsnorm_warp_kernel(const __grid_cons
         if (j < held) give<CODES>(p, row * p.nv + lane + 32 * j, h[j], w[j], rs, inv);
 }
 
-// Many rows: a block stays and takes rows blockIdx.x, + gridDim.x, ...; each
+// Many rows without a residual: a block stays and takes rows blockIdx.x, + gridDim.x, ...; each
 // thread fetches its own vectors of the rows STAGES ahead into shared memory
 // (cp.async: nobody else reads them, so nothing is waited for but the
 // thread's own copies), and keeps its part of the weight.
-template <int STAGES, bool RES, bool CODES>
-__global__ void __launch_bounds__(1024, 1) add_rmsnorm_stream_kernel(const __grid_constant__ NormArgs p) {
-    extern __shared__ uint4 ring[];  // [STAGES][RES ? 2 : 1][blockDim.x]
+template <int STAGES, bool CODES>
+__global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const __grid_constant__ NormArgs p) {
+    extern __shared__ uint4 ring[];  // [STAGES][blockDim.x]
     __shared__ float2 red[2][32];
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int tid = threadIdx.x, n = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = n >> 5;
-    constexpr int kParts = RES ? 2 : 1;
     const int held = tid < p.nv ? 1 : 0;
     uint4 w[1] = {held ? __ldg(p.weight + tid) : make_uint4(0, 0, 0, 0)};
     auto fetch = [&](int64_t row, int stage) {
-        if (held && row < p.rows) {
-            copy16(ring + stage * kParts * n + tid, p.x + row * p.x_vecs + tid);
-            if (RES) copy16(ring + (stage * kParts + 1) * n + tid, p.residual + row * p.nv + tid);
-        }
+        if (held && row < p.rows) copy16(ring + stage * n + tid, p.x + row * p.x_vecs + tid);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
@@ -279,8 +275,7 @@ __global__ void __launch_bounds__(1024, 1) add_rmsnorm_stream_kernel(const __gri
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         float h[1][8], ss = 0.0f, mx = 0.0f;
         if (held)
-            take<RES, CODES>(p, row * p.nv + tid, ring[stage * kParts * n + tid],
-                             RES ? ring[(stage * kParts + 1) * n + tid] : make_uint4(0, 0, 0, 0), w[0], h[0], ss, mx);
+            take<false, CODES>(p, row * p.nv + tid, ring[stage * n + tid], make_uint4(0, 0, 0, 0), w[0], h[0], ss, mx);
         fetch(row + (int64_t)STAGES * gridDim.x, stage);
         auto block_sums = [&] {
             warp_sum_max<CODES>(ss, mx);
@@ -340,20 +335,25 @@ template <bool RES, bool CODES>
 cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
     const int nv = p.nv, sms = current_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // Which kernel, with a residual and codes, us (a warp / a block per row /
-    // the staying blocks): 8192 x 512 7.8 / 8.7 / -, 64 x 512 1.9 / 1.6 / -,
-    // 8192 x 1024 14.7 / 13.1 / -; 8192 x 4096 - / 46 / 54, 1024 x 7168
-    // - / 14.7 / 14.8, 8192 x 7168 - / 88.6 / 84.3 (92% of the copy rate).
+    // Which kernel, us at 8192 rows (a warp / a block per row / the staying
+    // blocks).  Residual and codes: H = 512 5.1 / 8.7 / -, 1000 12.8 / 10.7 / -,
+    // 4096 - / 44.8 / 48.4, 7168 - / 84.5 / 85.1 (92% of the copy rate), 8192 -
+    // / 94.3 / 99.7.  Neither: 512 3.2 / 8.7 / -, 1000 4.7 / 8.8 / -, 4096 - /
+    // 27.7 / 29.5, 7168 - / 60 / 43.8.  512 x 64 rows, both: 1.9 / 1.6 / -.
     if (nv <= 64 && p.rows >= 8 * sms)
         return launch(add_rmsnorm_warp_kernel<2, RES, CODES>, p, (p.rows + 7) / 8, 256, 0, s);
+    if constexpr (!RES)
+        if (nv <= 128 && p.rows >= 8 * sms)
+            return launch(add_rmsnorm_warp_kernel<4, RES, CODES>, p, (p.rows + 7) / 8, 256, 0, s);
     const int threads = (nv + 31) / 32 * 32;
-    if (nv > 768 && nv <= 1024 && p.rows >= 12 * sms) {
-        constexpr int kStages = 3;
-        const size_t smem = (size_t)kStages * (RES ? 2 : 1) * threads * 16;
-        auto kernel = add_rmsnorm_stream_kernel<kStages, RES, CODES>;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        return e != cudaSuccess ? e : launch(kernel, p, sms, threads, smem, s);
-    }
+    if constexpr (!RES)
+        if (nv > 768 && nv <= 1024 && p.rows >= 12 * sms) {
+            constexpr int kStages = 3;
+            const size_t smem = (size_t)kStages * threads * 16;  // 48 KB at most, and the static part
+            const cudaError_t e = cudaFuncSetAttribute(rmsnorm_stream_kernel<kStages, CODES>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            return e != cudaSuccess ? e : launch(rmsnorm_stream_kernel<kStages, CODES>, p, sms, threads, smem, s);
+        }
     if (nv <= 1024) return launch(add_rmsnorm_kernel<1, RES, CODES>, p, p.rows, threads, 0, s);
     return launch(add_rmsnorm_kernel<4, RES, CODES>, p, p.rows, ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
 }

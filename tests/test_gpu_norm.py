@@ -192,3 +192,35 @@ def test_row_stride_beyond_2_to_31_elements():
     x.copy_(I.randn_bf16((rows, H), 1.0, 23, "cuda"))
     w = I.randn_bf16((H,), 1.0, 24, "cuda")
     check(call(x, w), x, w)
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("rows, H", [(5000, 1024), (2500, 512), (2501, 1000), (2100, 7168), (2100, 6152), (2049, 8192),
+                                     (1300, 904), (2000, 1032)])
+def test_many_rows_without_a_residual(rows, H, codes):
+    x = I.randn_bf16((rows, H), 1.0, 25, "cuda")
+    w = I.randn_bf16((H,), 1.0, 26, "cuda")
+    check(call(x, w, codes=codes), x, w)
+
+
+@pytest.mark.parametrize("rows, H", [(2200, 904), (2200, 7168), (2200, 8192)])
+def test_squares_beyond_the_range_without_a_residual(rows, H):
+    x = I.randn_bf16((rows, H), 1.0, 27, "cuda")
+    x[3::7] *= 2.0 ** 100
+    w = I.randn_bf16((H,), 1.0, 28, "cuda")
+    check(call(x, w), x, w)
+
+
+def test_nan_and_inf_stay_in_their_rows_of_many():
+    rows, H = 2200, 7168
+    x = I.randn_bf16((rows, H), 1.0, 29, "cuda")
+    w = I.randn_bf16((H,), 1.0, 30, "cuda")
+    clean = call(x, w)
+    x[5, 17], x[2000, 3] = float("nan"), float("inf")
+    o = call(x, w)
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[5] = rest[2000] = False
+    assert torch.isnan(o["out"][5]).all() and torch.isnan(o["row_scale"][5])
+    for name in o:
+        a, b = o[name][rest], clean[name][rest]
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
