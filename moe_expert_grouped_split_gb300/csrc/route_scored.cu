@@ -388,6 +388,33 @@ __device__ __forceinline__ int pick_close(const ScoredArgs& p, int64_t t, int la
     return my_id;
 }
 
+// The k picks where the last of them are experts taken out (-inf): those go
+// by id, but keys of different lanes order equal values by place first, and
+// a difference of infinities is no measure of closeness.
+template <int P>
+__device__ __forceinline__ int pick_taken_out(const ScoredArgs& p, int lane, const Lane& ln, const uint32_t (&key)[P],
+                                              bool kept, int my_id, uint32_t my_key, const Scratch& s) {
+    auto is_out = [](uint32_t k) { return place_value<P>(k) == -CUDART_INF_F; };
+    uint64_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        if (kept && key[j] != 0 && is_out(key[j])) bits |= 1ull << j;
+    const int n_left = __popc(__ballot_sync(kFull, my_id >= 0 && !is_out(my_key)));
+    const int mine = __popcll(bits);
+    int at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += u;
+    }
+    at -= mine;
+    for (; bits != 0 && at < p.k; bits &= bits - 1) s.list[at++] = ln.first + __ffsll((long long)bits) - 1;
+    __syncwarp();
+    if (lane >= n_left && lane < p.k) my_id = s.list[lane - n_left];
+    __syncwarp();
+    return my_id;
+}
+
 // One token by one warp: lane s < k gets the s-th pick's id, the slot it has
 // in ascending order of ids, and its weight.
 struct Pick {
@@ -409,7 +436,7 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
     bool finite;
     const Tolerance tol = choice_keys<P, FULL>(p, ln, z, b, key, zm, total, finite);
     if (!finite && lane == 0) atomicOr(p.err, DERR_NONFINITE_LOGIT);
-    // close: a difference of infinities is NaN and never close, ties go by id
+    // close: a difference of infinities is NaN and never close
     auto close = [&](float a, float b, float times) { return finite && a - b <= times * tol(a); };
     Best3 best;
 #pragma unroll
@@ -444,7 +471,9 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
     }
     uint32_t my_key, last, next;
     int my_id = pick<P>(p, key, best, ln, lane, my_key, last, next);
-    if (next != 0 && close(place_value<P>(last), place_value<P>(next), 1.0f))
+    if (place_value<P>(last) == -CUDART_INF_F)
+        my_id = pick_taken_out<P>(p, lane, ln, key, kept, my_id, my_key, scratch);
+    else if (next != 0 && close(place_value<P>(last), place_value<P>(next), 1.0f))
         my_id = pick_close<P>(p, t, lane, ln, key, kept, my_id, my_key, last, tol, scratch, zm);
 
     // weights, by lane s < k for its own pick

@@ -313,3 +313,21 @@ def test_logits_of_experts_that_are_no_whole_sectors(T, H, E):
     assert bool(((rb.logits.double() - want).abs() <= 2.0 ** -20 * (x.double().abs() @ w.double().abs().t())).all())
     best = rb.logits.topk(4, dim=1).indices.sort(dim=1).values
     assert torch.equal(best.int(), rb.topk_ids[:T])
+
+
+@pytest.mark.parametrize("E, G, top, gs", [(64, 1, 1, B.GROUP_MAX), (256, 1, 1, B.GROUP_MAX), (256, 8, 4, B.GROUP_MAX),
+                                           (256, 8, 4, B.GROUP_TOP2), (300, 5, 2, B.GROUP_TOP2),
+                                           (1020, 1, 1, B.GROUP_MAX), (1020, 17, 9, B.GROUP_TOP2)])
+@pytest.mark.parametrize("T", [1, 37, 300])
+def test_experts_taken_out_fill_up_from_the_lowest_id(T, E, G, top, gs):
+    """Lanes of several experts: fewer than k others are left, or none, and
+    what fills the choice up goes by id."""
+    H, k = 64, 8
+    rng = np.random.default_rng(E + G)
+    for left in (0, 1, 3, k - 1, 2 * k):
+        bias = np.full(E, -np.inf, np.float32)
+        bias[rng.permutation(E)[:left]] = rng.normal(0, 0.1, left)
+        for score, renorm in ((SIG, True), (SOFT, False)):
+            how = how_of(score, G, top, gs, renorm, 2.5)
+            _, _, rb = route(T, H, E, k, how, bias=bias, seed=left)
+            check(T, E, k, how, bias, rb)
