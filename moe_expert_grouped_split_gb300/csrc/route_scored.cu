@@ -164,6 +164,9 @@ struct Best3 {
 // Two choice values further apart than (*this)(v) are in the right order.  A
 // binary32 value's error is at most half of rel (ref or |v|) + 2^-22 |v|, and
 // its key is cut by less than P - 1 units of 2^-23 |v|, always towards zero.
+// Two groups' sums of two values are in the right order where they are further
+// apart than twice (*this)(m), m the larger of |first| + |second| of the two
+// groups: four values' errors, and cuts that go both ways where the signs differ.
 // With ex2.approx and its argument's rounding, |z| <= most:
 //   sigmoid      s (1 - s) (1.7 |z| 2^-24 + 2^-22) + s 2^-22: 2^-21 of 1 at
 //                most, or (most 2^-23 + 2^-21) of s
@@ -319,15 +322,26 @@ __device__ __forceinline__ int list_in_64(const ScoredArgs& p, int64_t t, int la
     return n;
 }
 
-// Whether this lane's group stays, where the edge between kept and dropped
-// groups is too close.  k1, k2: the group's best two; score, edge: its score
-// and that of the last one kept.
+// The largest of the warp's magnitudes (their order is their bits').
+__device__ __forceinline__ float warp_max_magnitude(float v) { return __uint_as_float(warp_max(__float_as_uint(v))); }
+
+// Whether this lane's group stays (kept: by the keys), where the edge between
+// kept and dropped groups is too close.  k1, k2: the group's best two; score,
+// edge, dropped: its score, that of the last one kept and of the first one
+// not; size: the magnitudes of what its score is the sum of; wide: the
+// tolerance by the largest size.
 template <int P>
 __device__ __forceinline__ bool keep_close_group(const ScoredArgs& p, int64_t t, int lane, const Lane& ln,
                                                  const uint32_t (&key)[P], uint32_t k1, uint32_t k2, uint32_t score,
-                                                 uint32_t edge_key, const Tolerance& tol, const Scratch& s, float zm) {
-    const float edge = key_value(edge_key), v = key_value(score), wide = 2.0f * tol(edge);
+                                                 float edge, float dropped, float size, float wide, bool kept,
+                                                 const Tolerance& tol, const Scratch& s, float zm) {
+    const float v = key_value(score);
     const bool is_group = ln.g < p.n_groups;
+    // Groups further from the edge than the largest size allows are settled;
+    // among the others only their own sizes count.
+    const bool near = is_group && !(v - edge > wide) && !(edge - v > wide);
+    wide = 2.0f * tol(warp_max_magnitude(near ? size : 0.0f));
+    if (edge - dropped > wide) return kept;
     const bool sure = is_group && v > edge && !(v - edge <= wide);
     const bool open = is_group && !sure && !(edge - v > wide);
     const float low = place_value<P>(p.group_top2 && k2 != 0 ? k2 : k1), floor = low - tol(low);
@@ -436,8 +450,8 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
     bool finite;
     const Tolerance tol = choice_keys<P, FULL>(p, ln, z, b, key, zm, total, finite);
     if (!finite && lane == 0) atomicOr(p.err, DERR_NONFINITE_LOGIT);
-    // close: a difference of infinities is NaN and never close
-    auto close = [&](float a, float b, float times) { return finite && a - b <= times * tol(a); };
+    // (a difference of infinities is NaN and never close)
+    auto close = [&](float a, float b) { return finite && a - b <= tol(a); };
     Best3 best;
 #pragma unroll
     for (int j = 0; j < P; ++j) best.add(key[j]);
@@ -451,9 +465,12 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
             k1 = max(k1, o1);
         }
         const bool is_group = ln.g < p.n_groups;
-        const float top = place_value<P>(k1);
-        uint32_t score = order_key(p.group_top2 && k2 != 0 ? top + place_value<P>(k2) : top);
+        const float top = place_value<P>(k1), second = p.group_top2 && k2 != 0 ? place_value<P>(k2) : 0.0f;
+        uint32_t score = order_key(p.group_top2 && k2 != 0 ? top + second : top);
+        // a sum is as uncertain as its terms are large, but one of -inf is certain
+        float size = fabsf(top) + fabsf(second);
         if (!is_group) score = 0;
+        if (!is_group || top == -CUDART_INF_F || second == -CUDART_INF_F) size = 0.0f;
         int rank = 0;  // groups before this one: larger, or as large and lower
         for (int g0 = 0; g0 < p.n_groups; g0 += 8) {
 #pragma unroll
@@ -464,16 +481,18 @@ __device__ __forceinline__ Pick route_token(const ScoredArgs& p, int64_t t, int 
             }
         }
         kept = is_group && rank < p.top_groups;
-        const uint32_t edge = ~warp_max(kept ? ~score : 0u), dropped = warp_max(is_group && !kept ? score : 0u);
-        if (dropped != 0 && close(key_value(edge), key_value(dropped), 2.0f))
-            kept = keep_close_group<P>(p, t, lane, ln, key, k1, k2, score, edge, tol, scratch, zm);
+        const uint32_t edge_key = ~warp_max(kept ? ~score : 0u), first_out = warp_max(is_group && !kept ? score : 0u);
+        const float edge = key_value(edge_key), dropped = key_value(first_out);
+        const float wide = 2.0f * tol(warp_max_magnitude(size));
+        if (first_out != 0 && finite && edge - dropped <= wide)
+            kept = keep_close_group<P>(p, t, lane, ln, key, k1, k2, score, edge, dropped, size, wide, kept, tol, scratch, zm);
         if (!kept) best.k1 = best.k2 = best.k3 = 0;
     }
     uint32_t my_key, last, next;
     int my_id = pick<P>(p, key, best, ln, lane, my_key, last, next);
     if (place_value<P>(last) == -CUDART_INF_F)
         my_id = pick_taken_out<P>(p, lane, ln, key, kept, my_id, my_key, scratch);
-    else if (next != 0 && close(place_value<P>(last), place_value<P>(next), 1.0f))
+    else if (next != 0 && close(place_value<P>(last), place_value<P>(next)))
         my_id = pick_close<P>(p, t, lane, ln, key, kept, my_id, my_key, last, tol, scratch, zm);
 
     // weights, by lane s < k for its own pick

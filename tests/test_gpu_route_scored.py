@@ -331,3 +331,34 @@ def test_experts_taken_out_fill_up_from_the_lowest_id(T, E, G, top, gs):
             how = how_of(score, G, top, gs, renorm, 2.5)
             _, _, rb = route(T, H, E, k, how, bias=bias, seed=left)
             check(T, E, k, how, bias, rb)
+
+
+@pytest.mark.parametrize("E, G, top", [(256, 8, 4), (128, 8, 4), (992, 31, 7)])
+@pytest.mark.parametrize("size", [8.0, 100.0, 1e3, 3e4])
+def test_group_scores_of_biases_that_cancel(size, E, G, top):
+    """One expert of each group at about +size, the others at about -size: the
+    sum of the best two is a small difference of large values, whose binary32
+    errors are those of the large ones."""
+    T, H, k = 4099, 64, 4
+    rng = np.random.default_rng(int(size) + E)
+    of_group = np.float32(size) * (1 + rng.random(G)).astype(np.float32)
+    bias = np.repeat(-of_group, E // G)
+    bias[np.arange(G) * (E // G) + rng.integers(0, E // G, G)] = of_group
+    for score in (SIG, SOFT):
+        how = how_of(score, G, top, B.GROUP_TOP2, True, 2.5)
+        _, _, rb = route(T, H, E, k, how, bias=bias, seed=E, std=0.5)
+        check(T, E, k, how, bias, rb)
+
+
+def test_group_scores_beside_experts_masked_with_large_negative_biases():
+    """Finite masks: groups whose second value is -1e30 are far below the
+    others and must not blur them."""
+    T, H, E, G, top, k = 1003, 64, 256, 8, 4, 4
+    rng = np.random.default_rng(3)
+    bias = rng.normal(0, 0.1, E).astype(np.float32)
+    bias[rng.permutation(E)[:100]] = -1e30
+    bias[3 * 32 + 1:4 * 32] = -1e30          # a group of one expert that is left
+    bias[6 * 32:7 * 32] = -1e30              # and one of none
+    how = how_of(SIG, G, top, B.GROUP_TOP2, True, 2.5)
+    _, _, rb = route(T, H, E, k, how, bias=bias)
+    check(T, E, k, how, bias, rb)
