@@ -41,6 +41,7 @@ constexpr int kWarps = kThreads / 32;
 // 31 / 11.4, 1000 56 / 20.  Looking costs tokens that are in order 0.5 us (256
 // of 20 requests 8.1 / 8.6).
 constexpr int kOrderTokens = 2048;  // at most
+constexpr int kOrderLeast = 5;      // fewer have nothing to gain
 constexpr int kOrderBins = 256;  // adapters, and one for tokens without
 constexpr int kOrderRows = 64;   // of a tile at most
 
@@ -48,8 +49,18 @@ constexpr int kOrderRows = 64;   // of a tile at most
 // of 32 tokens and adapter, a byte each.
 __host__ __device__ inline int order_pitch(const LoraArgs& p) { return (p.n_adapters + 4) / 4 * 4; }
 bool may_order(const LoraArgs& p, int rows) {
-    return rows > 4 && p.T <= kOrderTokens && p.n_adapters < kOrderBins;
+    return rows > 4 && p.T >= kOrderLeast && p.T <= kOrderTokens && p.n_adapters < kOrderBins;
 }
+// Lane l looks at ids 2 i and 2 i + 1, i = order_place(T, l): with 2 tokens or
+// more never beyond the last.
+__host__ __device__ constexpr int order_place(int T, int lane) { return (int)((int64_t)lane * (T / 2) / 32); }
+constexpr bool order_places_exist(int least, int most) {
+    for (int T = least; T <= most; ++T)
+        if (2 * order_place(T, 31) + 1 >= T) return false;
+    return true;
+}
+static_assert(order_places_exist(kOrderLeast, kOrderTokens), "");
+static_assert(!order_places_exist(1, 1) && order_places_exist(2, 2), "one token has no pair");
 size_t order_bytes(const LoraArgs& p) {
     return (2 * kOrderBins + kWarps) * 4 + (size_t)((p.T + 31) / 32) * order_pitch(p);
 }
@@ -61,7 +72,7 @@ __device__ __forceinline__ bool order_tile(const LoraArgs& p, int t0, int rows, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // neighbours at 32 places of the batch, the same for every warp; and the
     // tile's own ids on their way
-    const int2 two = reinterpret_cast<const int2*>(p.ids)[(int64_t)lane * (p.T / 2) / 32];
+    const int2 two = reinterpret_cast<const int2*>(p.ids)[order_place(p.T, lane)];
     const int own = p.ids[min(t0 + lane, p.T - 1)];
     asm volatile("" ::"r"(own));
     if (__popc(__ballot_sync(kFull, two.x != two.y)) < 16) return false;

@@ -267,3 +267,12 @@ def test_any_order_of_tokens(T, n):
     check(run(*args), *args)
     base = args[-1].clone()
     assert torch.equal(run(*args[:-1], base, out=base), run(*args))
+
+
+@pytest.mark.parametrize("N", [80000, 131072])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 17])
+def test_few_tokens_of_a_vocabulary_projection(T, N):
+    """Columns enough for the wide expand tiles although the tokens are few."""
+    for R in (16, 64):
+        args = case(T, 64, N, R, 4, np.random.default_rng(T).integers(-1, 4, T), seed=T + R)
+        check(run(*args), *args)
