@@ -350,8 +350,11 @@ cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
         if (nv > 768 && nv <= 1024 && p.rows >= 12 * sms) {
             constexpr int kStages = 3;
             const size_t smem = (size_t)kStages * threads * 16;  // 48 KB at most, and the static part
-            const cudaError_t e = cudaFuncSetAttribute(rmsnorm_stream_kernel<kStages, CODES>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            // the kernel's limit, not this call's size: another host thread
+            // may be about to launch a wider row
+            const cudaError_t e =
+                cudaFuncSetAttribute(rmsnorm_stream_kernel<kStages, CODES>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * 1024 * 16);
             return e != cudaSuccess ? e : launch(rmsnorm_stream_kernel<kStages, CODES>, p, sms, threads, smem, s);
         }
     if (nv <= 1024) return launch(add_rmsnorm_kernel<1, RES, CODES>, p, p.rows, threads, 0, s);

@@ -756,10 +756,13 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 16 ? 2 : 1)
     }
 }
 
+// most: what any call of the kernel may ask for.  The limit belongs to the
+// kernel, not to the launch: set to this call's size it could refuse another
+// host thread's larger launch.
 template <class F, class... A>
-cudaError_t launch(F kernel, int grid, int threads, size_t smem, bool cluster, cudaStream_t s, A... args) {
+cudaError_t launch(F kernel, int grid, int threads, size_t smem, size_t most, bool cluster, cudaStream_t s, A... args) {
     if (smem > 36 << 10) {  // beside the static part, beyond what a launch gets unasked
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute at[2]{};
@@ -781,19 +784,20 @@ cudaError_t launch(F kernel, int grid, int threads, size_t smem, bool cluster, c
 template <int P, bool FULL>
 cudaError_t launch_form(const ScoredArgs& p, cudaStream_t s) {
     constexpr int threads = 32 * kSelectWarps;
-    const size_t smem = Scratch::bytes(p.E, kSelectWarps);
-    if (p.in_one && p.T <= kSelectWarps) return launch(scored_one_kernel<P, FULL, true>, 1, threads, smem, false, s, p);
-    if (p.in_one) return launch(scored_one_kernel<P, FULL, false>, kOneCluster, threads, smem, true, s, p);
+    const size_t smem = Scratch::bytes(p.E, kSelectWarps), most = Scratch::bytes(DWDP_MAX_EXPERTS, kSelectWarps);
+    if (p.in_one && p.T <= kSelectWarps)
+        return launch(scored_one_kernel<P, FULL, true>, 1, threads, smem, most, false, s, p);
+    if (p.in_one) return launch(scored_one_kernel<P, FULL, false>, kOneCluster, threads, smem, most, true, s, p);
     const int n_chunks = p.chunks;
     cudaError_t e =
-        launch(scored_select_kernel<P, FULL>, (p.T + kSelectWarps - 1) / kSelectWarps, threads, smem, false, s, p);
+        launch(scored_select_kernel<P, FULL>, (p.T + kSelectWarps - 1) / kSelectWarps, threads, smem, most, false, s, p);
     if (e != cudaSuccess) return e;
-    const size_t place_smem = (size_t)p.E * 36;
+    const size_t place_smem = (size_t)p.E * 36, place_most = (size_t)DWDP_MAX_EXPERTS * 36;
     if (n_chunks <= kSelfScanChunks)
-        return launch(scored_place_kernel<false>, n_chunks, kChunk, place_smem, false, s, p, n_chunks);
+        return launch(scored_place_kernel<false>, n_chunks, kChunk, place_smem, place_most, false, s, p, n_chunks);
     e = launch_chunk_scan(p.hist, n_chunks, p.E, p.counts, p.offsets, s);
     if (e != cudaSuccess) return e;
-    return launch(scored_place_kernel<true>, n_chunks, kChunk, place_smem, false, s, p, n_chunks);
+    return launch(scored_place_kernel<true>, n_chunks, kChunk, place_smem, place_most, false, s, p, n_chunks);
 }
 
 template <int P>

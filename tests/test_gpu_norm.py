@@ -224,3 +224,33 @@ def test_nan_and_inf_stay_in_their_rows_of_many():
     for name in o:
         a, b = o[name][rest], clean[name][rest]
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_two_threads_with_different_widths():
+    """The same kernel with other sizes of shared memory from two host
+    threads: neither call is refused."""
+    import threading
+
+    failed = []
+    made = []
+    for H in (6400, 8192):
+        x = I.randn_bf16((2000, H), 1.0, H, "cuda")
+        made.append((x, torch.ones(H, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(x, w, out, stream):
+        try:
+            for i in range(3000):
+                B.dwdp_add_rmsnorm(x, x.shape[0], x.shape[1], w, EPS, out, stream=stream)
+                if i % 500 == 499:
+                    stream.synchronize()
+        except B.DwdpError as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed[0]

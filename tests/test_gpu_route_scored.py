@@ -362,3 +362,36 @@ def test_group_scores_beside_experts_masked_with_large_negative_biases():
     how = how_of(SIG, G, top, B.GROUP_TOP2, True, 2.5)
     _, _, rb = route(T, H, E, k, how, bias=bias)
     check(T, E, k, how, bias, rb)
+
+
+def test_two_threads_with_different_numbers_of_experts():
+    """The same kernel with other sizes of shared memory from two host
+    threads, a context each: neither call is refused."""
+    import threading
+
+    H, k, failed = 64, 4, []
+    made = []
+    for E in (400, 500):
+        rt = B.Runtime(H, 64, E, k, 0, 8, 1, 0)
+        made.append((rt, I.randn_bf16((8, H), 1.0, E, "cuda"), I.randn_bf16((E, H), 0.1, E + 1, "cuda"),
+                     B.RouteBuffers(8, E, k), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(rt, x, wr, rb, stream):
+        try:
+            for i in range(3000):
+                rt.route_scored(x, wr, None, how_of(SIG), rb, stream)
+                if i % 500 == 499:
+                    stream.synchronize()
+        except B.DwdpError as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for m in made:
+        m[0].close()
+    assert not failed, failed[0]
