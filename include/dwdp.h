@@ -475,9 +475,16 @@ int32_t dwdp_group_map(int32_t n_experts, int32_t n_ranks, int32_t rank, int32_t
  *   out = bf16(y)
  *   row_scale = max|y| / 448 (1 for an all-zero row),
  *   codes = E4M3(y / row_scale)                   (iff codes is given)
- * The codes come from the unrounded y: one rounding, to nearest even.  A row
- * whose largest |h weight| is below 2^-100 is quantized as if it were 2^-100.
- * The squares are summed in binary32, scaled where they would pass its range.
+ * The codes come from the unrounded y: one rounding, to nearest even (of
+ * y / row_scale by approximate reciprocals, so that a value next to the middle
+ * of two codes may take either).  A row whose largest |h weight| is below 2^-100
+ * is quantized as if it were 2^-100.
+ * The squares are summed in binary32, on scaled values where they would pass
+ * its range, or vanish below it with an eps that does not make up for them (eps
+ * below 2^-120, e.g. 0; an all-zero row of out is then NaN, 0 / 0).  The codes
+ * ask for weights of ordinary size: with an eps of 2^-120 or more, |h weight| has
+ * to stay in binary32's range, and a row whose squares pass it (|h| beyond 2^55)
+ * is quantized as if its largest |h weight| were at least 2^-20.
  * A NaN makes its row of out, and its row_scale, NaN.
  * x: bf16, row r at x + r * x_stride elements (x_stride >= H, a multiple of
  * 8); residual, residual_out, out: bf16 [rows][H]; weight: bf16 [H]; codes:

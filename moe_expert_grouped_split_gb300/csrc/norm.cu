@@ -8,6 +8,7 @@
 // max|h w|), in which rs cancels.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <math_constants.h>
 
 #include <atomic>
 
@@ -21,6 +22,13 @@ namespace {
 constexpr float kSquaresLimit = 1e38f;
 constexpr float kDownScale = 0x1p-80f;
 constexpr float kMinCodeMax = 0x1p-100f;
+// With an eps from here on squares that binary32 loses do not count.  Below it
+// (TINY, forms of their own: in the others this costs 8192 rows of 7168 with a
+// residual and codes 2%, of 8200 6%) a row whose mean + eps is lower is taken on
+// values scaled by 2^80 (bf16's least value is 2^-133); a row's sum then loses
+// at most 2^-30 of itself, 32768 additions to within 2^-150.
+constexpr float kEpsEnough = 0x1p-120f;
+constexpr float kUpScale = 0x1p80f;
 
 // The larger of two, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -93,6 +101,7 @@ struct NormArgs {
     uint4* residual_out;
     const uint4* weight;
     float eps;
+    float least;  // TINY: the least sum of squares that is taken as it is
     int64_t rows;
     int nv;         // vectors a row
     float one_nth;  // 1 / H
@@ -176,9 +185,56 @@ __device__ __forceinline__ void take_scaled(float (&h)[VPT][8], const uint4 (&w)
     }
 }
 
+// TINY: whether binary32 holds a row's squares and its products with the weight.
+template <bool CODES>
+__device__ __forceinline__ bool in_range(const NormArgs& p, float ss, float mx) {
+    return ss < kSquaresLimit && ss >= p.least && (!CODES || mx < CUDART_INF_F);
+}
+
+// TINY: a row that is not in range (or holds a NaN): h normalized in place,
+// from the squares of scaled values, and sums that say so: a mean of 1, no eps,
+// mx = max|y|.  An all-zero row keeps its zeros and its eps.  reduce(s, m):
+// over the row.
+template <int VPT, bool CODES, class Reduce>
+__device__ __forceinline__ void normalize(const NormArgs& p, float (&h)[VPT][8], const uint4 (&w)[VPT], int held, float& ss,
+                                          float& mx, float& eps, Reduce reduce) {
+    const float scale = !(ss < kSquaresLimit) ? kDownScale : ss < p.least ? kUpScale : 1.0f;
+    ss = mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (j >= held) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            h[j][c] *= scale;
+            ss = fmaf(h[j][c], h[j][c], ss);
+        }
+    }
+    reduce(ss, mx);
+    eps = eps * scale * scale;
+    const float rs = ss == 0.0f ? 1.0f : rsqrtf(fmaf(ss, p.one_nth, eps));
+    mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (j >= held) continue;
+        float f[8];
+        unpack8(w[j], f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            h[j][c] *= rs;
+            if constexpr (CODES) mx = max_nan(mx, fabsf(h[j][c] * f[c]));
+        }
+    }
+    float none = 0.0f;
+    if constexpr (CODES) reduce(none, mx);
+    if (ss != 0.0f) {
+        ss = (float)(p.nv * 8);
+        eps = 0.0f;
+    }
+}
+
 // One block per row; thread i holds the row's 16-byte vectors i, i + blockDim.x,
 // ... (VPT of them at most).
-template <int VPT, bool RES, bool CODES>
+template <int VPT, bool RES, bool CODES, bool TINY>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant__ NormArgs p) {
     __shared__ float2 red[32];
     wait_for_previous_kernel();
@@ -200,7 +256,15 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant
     }
     float2 sums = block_sum_max<CODES>(ss, mx, red);
     float eps = p.eps;
-    if (!(sums.x < kSquaresLimit)) {  // rare; the whole block agrees
+    if constexpr (TINY) {
+        if (!in_range<CODES>(p, sums.x, sums.y))
+            normalize<VPT, CODES>(p, h, w, held, sums.x, sums.y, eps,
+                                  [&](float& s, float& m) {
+                                      const float2 v = block_sum_max<CODES>(s, m, red);
+                                      s = v.x;
+                                      m = v.y;
+                                  });
+    } else if (!(sums.x < kSquaresLimit)) {  // rare; the whole block agrees
         take_scaled<VPT, CODES>(h, w, held, ss, mx);
         eps = p.eps * kDownScale * kDownScale;
         sums = block_sum_max<CODES>(ss, mx, red);
@@ -213,7 +277,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant
 }
 
 // One warp per row, 8 rows a block: rows of up to 32 VPT vectors.
-template <int VPT, bool RES, bool CODES>
+template <int VPT, bool RES, bool CODES, bool TINY>
 __global__ void __launch_bounds__(256) add_rmsnorm_warp_kernel(const __grid_constant__ NormArgs p) {
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -239,7 +303,10 @@ __global__ void __launch_bounds__(256) add_rmsnorm_warp_kernel(const __grid_cons
         if (j < held) take<RES, CODES>(p, row * p.nv + lane + 32 * j, x[j], r[j], w[j], h[j], ss, mx);
     warp_sum_max<CODES>(ss, mx);
     float eps = p.eps;
-    if (!(ss < kSquaresLimit)) {
+    if constexpr (TINY) {
+        if (!in_range<CODES>(p, ss, mx))
+            normalize<VPT, CODES>(p, h, w, held, ss, mx, eps, [](float& s, float& m) { warp_sum_max<CODES>(s, m); });
+    } else if (!(ss < kSquaresLimit)) {
         take_scaled<VPT, CODES>(h, w, held, ss, mx);
         eps = p.eps * kDownScale * kDownScale;
         warp_sum_max<CODES>(ss, mx);
@@ -255,7 +322,7 @@ __global__ void __launch_bounds__(256) add_rmsnorm_warp_kernel(const __grid_cons
 // thread fetches its own vectors of the rows STAGES ahead into shared memory
 // (cp.async: nobody else reads them, so nothing is waited for but the
 // thread's own copies), and keeps its part of the weight.
-template <int STAGES, bool CODES>
+template <int STAGES, bool CODES, bool TINY>
 __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const __grid_constant__ NormArgs p) {
     extern __shared__ uint4 ring[];  // [STAGES][blockDim.x]
     __shared__ float2 red[2][32];
@@ -277,22 +344,24 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const __grid_co
         if (held)
             take<false, CODES>(p, row * p.nv + tid, ring[stage * n + tid], make_uint4(0, 0, 0, 0), w[0], h[0], ss, mx);
         fetch(row + (int64_t)STAGES * gridDim.x, stage);
-        auto block_sums = [&] {
-            warp_sum_max<CODES>(ss, mx);
-            if (lane == 0) red[half][warp] = make_float2(ss, mx);
+        auto block_sums = [&](float& s, float& m) {
+            warp_sum_max<CODES>(s, m);
+            if (lane == 0) red[half][warp] = make_float2(s, m);
             __syncthreads();
             const float2 v = lane < nw ? red[half][lane] : make_float2(0.0f, 0.0f);
-            ss = v.x;
-            mx = v.y;
-            warp_sum_max<CODES>(ss, mx);
+            s = v.x;
+            m = v.y;
+            warp_sum_max<CODES>(s, m);
             half ^= 1;  // the next sums go to the other half: one barrier is enough
         };
-        block_sums();
+        block_sums(ss, mx);
         float eps = p.eps;
-        if (!(ss < kSquaresLimit)) {
+        if constexpr (TINY) {
+            if (!in_range<CODES>(p, ss, mx)) normalize<1, CODES>(p, h, w, held, ss, mx, eps, block_sums);
+        } else if (!(ss < kSquaresLimit)) {
             take_scaled<1, CODES>(h, w, held, ss, mx);
             eps = p.eps * kDownScale * kDownScale;
-            block_sums();
+            block_sums(ss, mx);
         }
         float rs, inv;
         factors<CODES>(p, row, ss, mx, eps, tid == 0, rs, inv);
@@ -331,7 +400,7 @@ int current_sms() {
     return n;
 }
 
-template <bool RES, bool CODES>
+template <bool RES, bool CODES, bool TINY>
 cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
     const int nv = p.nv, sms = current_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
@@ -341,10 +410,10 @@ cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
     // / 94.3 / 99.7.  Neither: 512 3.2 / 8.7 / -, 1000 4.7 / 8.8 / -, 4096 - /
     // 27.7 / 29.5, 7168 - / 60 / 43.8.  512 x 64 rows, both: 1.9 / 1.6 / -.
     if (nv <= 64 && p.rows >= 8 * sms)
-        return launch(add_rmsnorm_warp_kernel<2, RES, CODES>, p, (p.rows + 7) / 8, 256, 0, s);
+        return launch(add_rmsnorm_warp_kernel<2, RES, CODES, TINY>, p, (p.rows + 7) / 8, 256, 0, s);
     if constexpr (!RES)
         if (nv <= 128 && p.rows >= 8 * sms)
-            return launch(add_rmsnorm_warp_kernel<4, RES, CODES>, p, (p.rows + 7) / 8, 256, 0, s);
+            return launch(add_rmsnorm_warp_kernel<4, RES, CODES, TINY>, p, (p.rows + 7) / 8, 256, 0, s);
     const int threads = (nv + 31) / 32 * 32;
     if constexpr (!RES)
         if (nv > 768 && nv <= 1024 && p.rows >= 12 * sms) {
@@ -353,12 +422,17 @@ cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
             // the kernel's limit, not this call's size: another host thread
             // may be about to launch a wider row
             const cudaError_t e =
-                cudaFuncSetAttribute(rmsnorm_stream_kernel<kStages, CODES>,
+                cudaFuncSetAttribute(rmsnorm_stream_kernel<kStages, CODES, TINY>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * 1024 * 16);
-            return e != cudaSuccess ? e : launch(rmsnorm_stream_kernel<kStages, CODES>, p, sms, threads, smem, s);
+            return e != cudaSuccess ? e : launch(rmsnorm_stream_kernel<kStages, CODES, TINY>, p, sms, threads, smem, s);
         }
-    if (nv <= 1024) return launch(add_rmsnorm_kernel<1, RES, CODES>, p, p.rows, threads, 0, s);
-    return launch(add_rmsnorm_kernel<4, RES, CODES>, p, p.rows, ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
+    if (nv <= 1024) return launch(add_rmsnorm_kernel<1, RES, CODES, TINY>, p, p.rows, threads, 0, s);
+    return launch(add_rmsnorm_kernel<4, RES, CODES, TINY>, p, p.rows, ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
+}
+
+template <bool RES, bool CODES>
+cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
+    return p.eps < kEpsEnough ? launch_form<RES, CODES, true>(p, s) : launch_form<RES, CODES, false>(p, s);
 }
 
 }  // namespace
@@ -369,7 +443,8 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* resi
     if (rows <= 0) return cudaSuccess;
     const NormArgs p{static_cast<const uint4*>(x),      x_stride / 8, static_cast<const uint4*>(residual),
                      static_cast<uint4*>(residual_out), static_cast<const uint4*>(weight),
-                     eps,                               rows,         H / 8, 1.0f / (float)H,
+                     eps, (kEpsEnough - eps) * (float)H,
+                     rows, H / 8, 1.0f / (float)H,
                      static_cast<uint4*>(out),          static_cast<uint2*>(codes), row_scale};
     if (residual && codes) return launch_form<true, true>(p, s);
     if (residual) return launch_form<true, false>(p, s);

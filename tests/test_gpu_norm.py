@@ -254,3 +254,45 @@ def test_two_threads_with_different_widths():
         t.join()
     torch.cuda.synchronize()
     assert not failed, failed[0]
+
+
+# rows and widths that run every kernel, with and without a residual
+EVERY_KERNEL = [(2200, 512), (2200, 904), (2200, 7168), (3, 8), (130, 7168), (40, 32768)]
+
+
+@pytest.mark.parametrize("rows, H", EVERY_KERNEL)
+@pytest.mark.parametrize("residual, codes", [(False, False), (False, True), (True, True)])
+def test_squares_below_the_range(rows, H, residual, codes):
+    """Without an eps that carries them: rows whose squares binary32 does not
+    hold, down to the smallest values of bf16, among ordinary ones."""
+    x = I.randn_bf16((rows, H), 1.0, 31, "cuda")
+    r = I.randn_bf16((rows, H), 1.0, 32, "cuda") if residual else None
+    for t in (x, r) if residual else (x,):
+        t[0] *= 2.0 ** -100
+        t[1::4] *= 2.0 ** -75
+        t[2::8] *= 2.0 ** -124          # the upper end of bf16's own subnormal values
+    w = I.randn_bf16((H,), 1.0, 33, "cuda")
+    for eps in (0.0, 1e-38):
+        check(call(x, w, r, codes, eps), x, w, r, eps)
+
+
+@pytest.mark.parametrize("rows, H", EVERY_KERNEL)
+def test_codes_of_weights_at_the_ends_of_the_range(rows, H):
+    """Rows and weights whose products leave binary32's range although their
+    norm does not, and rows beyond the range of squares with small weights."""
+    for x_exp, w_exp in ((65, -95), (40, 100), (-40, -55), (100, 20), (-90, 110)):
+        x = I.randn_bf16((rows, H), 1.0, 34, "cuda") * 2.0 ** x_exp
+        w = I.randn_bf16((H,), 1.0, 35, "cuda") * 2.0 ** w_exp
+        check(call(x, w, eps=0.0), x, w, eps=0.0)
+
+
+@pytest.mark.parametrize("rows, H", EVERY_KERNEL)
+def test_zero_rows_without_eps(rows, H):
+    x = torch.zeros((rows, H), dtype=torch.bfloat16, device="cuda")
+    x[1] = 2.0 ** -120
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    o = call(x, w, eps=0.0)
+    zero = [t for t in range(rows) if t != 1]
+    assert (o["codes"][zero] == 0).all() and (o["row_scale"][zero] == 1).all()
+    assert torch.isnan(o["out"][zero].float()).all()        # 0 / 0
+    assert (o["out"][1] == 1).all()
