@@ -194,9 +194,9 @@ void dwdp_destroy(dwdp_ctx* ctx);
  * dwdp_create / host helper when ctx is NULL).  Never NULL. */
 const char* dwdp_last_error(const dwdp_ctx* ctx);
 
-/* Device workspace, in bytes, that dwdp_route and dwdp_moe_layer need for T
- * tokens (the larger of the two; both may share one buffer when they run in
- * order on one stream). */
+/* Device workspace, in bytes, that dwdp_route, dwdp_route_scored and
+ * dwdp_moe_layer (_codes) need for T tokens (the largest of them; they may
+ * share one buffer when they run in order on one stream). */
 size_t dwdp_workspace_bytes(const dwdp_ctx* ctx, int32_t T);
 
 /* Where dwdp_moe_layer keeps each intermediate of a T-token layer in its

@@ -6,6 +6,7 @@
 // launches of the kernels in gemm.cu and route.cu.  Citations ([DWDP] §n) are
 // to "DWDP: Distributed Weight Data Parallelism for High-Performance LLM
 // Inference on NVL72".
+#include <algorithm>
 #include <chrono>
 #include <cmath>
 #include <cstdarg>
@@ -200,15 +201,15 @@ struct NvtxRange {
 };
 
 struct WsLayout {
-    size_t logits = 0;  // route: fp32 [T][E] when the caller does not keep logits
-    size_t group = 0;   // route: scratch of the chunked grouping
+    size_t logits = 0;  // routing: partial-sum planes of the router GEMM
+    size_t group = 0, scored_group = 0;  // dwdp_route, dwdp_route_scored: scratch of the chunked grouping
     // moe offsets: gathered rows xp, activations a, expert outputs y; E4M3
     // and NVFP4 contexts also keep x's codes/scales (xq, sx), xp's scales
     // (sxp) and a's codes/scales (aq, sa); NVFP4 adds the block-scale chunks
     // of the two GEMMs' A tiles (sfx, sfa).
     size_t xp = 0, a = 0, y = 0, xq = 0, sx = 0, sxp = 0, aq = 0, sa = 0, sfx = 0, sfa = 0;
     int64_t sf_tiles = 0;  // A tiles sfx / sfa have room for
-    size_t route_bytes = 0, moe_bytes = 0;
+    size_t route_bytes = 0, scored_bytes = 0, moe_bytes = 0;
 };
 
 WsLayout ws_layout(const dwdp_config& c, int64_t T) {
@@ -216,9 +217,11 @@ WsLayout ws_layout(const dwdp_config& c, int64_t T) {
     const int64_t H = c.hidden, I = c.inter, E = c.n_experts, k = c.top_k, S = c.n_shared;
     const int fmt = c.weight_dtype;
     L.logits = 0;  // the partial-sum planes of the router GEMM
-    L.group = align_up((size_t)(std::max(kRouterMaxSplit * T, router_pair_plane_rows(T)) * router_pair_pitch(E) * 4), 256);
-    L.route_bytes = L.group + align_up(std::max(group_chunked_scratch_bytes((int)(T * k), (int)E),
-                                                (size_t)scored_chunks(T, k) * E * 4), 256);
+    L.group = align_up((size_t)(kRouterMaxSplit * T * E * 4), 256);
+    L.route_bytes = L.group + align_up(group_chunked_scratch_bytes((int)(T * k), (int)E), 256);
+    // (small sizes: one plane of pitch E, within the first of these)
+    L.scored_group = align_up((size_t)(router_pair_plane_rows(T) * router_pair_pitch(E) * 4), 256);
+    L.scored_bytes = L.scored_group + align_up((size_t)scored_chunks(T, k) * E * 4, 256);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -323,9 +326,10 @@ int32_t check_device_error_word(dwdp_ctx* ctx) {
 }
 
 // The argument checks dwdp_route and dwdp_route_scored share.  T = 0 is done
-// here (empty set): nothing is routed.
+// here (empty set): nothing is routed.  need: the call's workspace.
 int32_t check_route(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router, const float* bias,
-                    const dwdp_route_out* out, const void* ws, size_t ws_bytes, cudaStream_t stream, bool& empty) {
+                    const dwdp_route_out* out, const void* ws, size_t ws_bytes, size_t need, cudaStream_t stream,
+                    bool& empty) {
     const dwdp_config& c = ctx->cfg;
     if (T < 0 || T > c.max_tokens) return fail(ctx, DWDP_ERR_INVALID_ARG, "T=%d outside [0, max_tokens]", T);
     if (!out || !out->topk_ids || !out->topk_w || !out->counts || !out->offsets || !out->perm || !out->inv_perm)
@@ -345,7 +349,6 @@ int32_t check_route(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_route
     if (!is_device_memory_of(x, ctx->device) || !is_device_memory_of(w_router, ctx->device))
         return fail(ctx, DWDP_ERR_INVALID_ARG, "x and w_router must be device memory of the context's device (%d)",
                     ctx->device);
-    const size_t need = ws_layout(c, T).route_bytes;
     if (!ws || ws_bytes < need || !aligned16(ws))
         return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu) or unaligned", ws_bytes, need);
     return DWDP_OK;
@@ -634,7 +637,7 @@ void dwdp_destroy(dwdp_ctx* ctx) { delete ctx; }
 size_t dwdp_workspace_bytes(const dwdp_ctx* ctx, int32_t T) {
     if (!ctx || T < 0) return 0;
     const WsLayout L = ws_layout(ctx->cfg, T);
-    return std::max(L.route_bytes, L.moe_bytes);
+    return std::max({L.route_bytes, L.scored_bytes, L.moe_bytes});
 }
 
 int32_t dwdp_workspace_region(const dwdp_ctx* ctx, int32_t T, int32_t region, size_t* offset, size_t* bytes) {
@@ -819,9 +822,9 @@ int32_t dwdp_route(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_router
     if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
     const dwdp_config& c = ctx->cfg;
     bool empty = false;
-    const int32_t rc = check_route(ctx, x, T, w_router, logit_bias, out, ws, ws_bytes, stream, empty);
-    if (rc != DWDP_OK || empty) return rc;
     const WsLayout L = ws_layout(c, T);
+    const int32_t rc = check_route(ctx, x, T, w_router, logit_bias, out, ws, ws_bytes, L.route_bytes, stream, empty);
+    if (rc != DWDP_OK || empty) return rc;
     int32_t* group_scratch = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.group);
     DWDP_CUDA(ctx, mark(ctx, 0, stream));
     int parts = 1;
@@ -858,14 +861,14 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
         return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring: %d groups of %d experts hold fewer than k = %d", sc.top_groups,
                     c.n_experts / sc.n_groups, c.top_k);
     bool empty = false;
-    const int32_t rc = check_route(ctx, x, T, w_router, choice_bias, out, ws, ws_bytes, stream, empty);
+    const WsLayout L = ws_layout(c, T);
+    const int32_t rc = check_route(ctx, x, T, w_router, choice_bias, out, ws, ws_bytes, L.scored_bytes, stream, empty);
     if (rc != DWDP_OK || empty) return rc;
     DWDP_CUDA(ctx, mark(ctx, 0, stream));
     ScoredArgs p{};
-    const WsLayout L = ws_layout(c, T);
     float* planes = reinterpret_cast<float*>(static_cast<char*>(ws) + L.logits);
     float* logits = nullptr;
-    p.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.group);
+    p.hist = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.scored_group);
     const bool small = router_is_small(T, c.n_experts);
     p.parts = small ? 1 : router_pair_parts(T, c.n_experts, c.hidden);
     p.chunks = scored_chunks(T, c.top_k);

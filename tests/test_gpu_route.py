@@ -156,3 +156,28 @@ def test_routing_at_the_limits(T, H, E, k):
     # a four-n-tile router GEMM), E not a multiple of the warp, k beyond the
     # specialised widths
     _route_case(T, H, E, k, seed=8, router_std=0.05)
+
+
+@pytest.mark.parametrize("T, H, E, k", [(1, 256, 16, 2), (64, 7168, 256, 8), (300, 1024, 250, 4), (2432, 256, 256, 8)])
+def test_workspace_of_its_own_planes_is_enough(T, H, E, k):
+    """dwdp_route needs four planes of logits at most and the counts of the
+    chunked grouping, whatever the other calls on the workspace need."""
+    pad = lambda n: (n + 255) // 256 * 256
+    size = pad(4 * T * E * 4) + pad((T * k + 1023) // 1024 * E * 4)
+    rt = B.Runtime(H, 64, E, k, 0, T, 1, 0)
+    try:
+        x = I.randn_bf16((T, H), 1.0, 1, "cuda")
+        wr = I.randn_bf16((E, H), 0.05, 2, "cuda")
+        want, got = B.RouteBuffers(T, E, k), B.RouteBuffers(T, E, k)
+        rt.route(x, wr, None, want)
+        ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        B.dwdp_route(rt.ctx, x, T, wr, None, got.c, ws, size)
+        torch.cuda.synchronize()
+        assert rt.device_status() == 0 and (ws[size:] == 0xA5).all()
+        for name in ("topk_ids", "topk_w", "counts", "offsets", "perm", "inv_perm"):
+            assert torch.equal(getattr(want, name), getattr(got, name)), name
+        with pytest.raises(B.DwdpError) as ei:
+            B.dwdp_route(rt.ctx, x, T, wr, None, got.c, ws, size - 256)
+        assert ei.value.code == -1
+    finally:
+        rt.close()
