@@ -421,6 +421,9 @@ class Workload:
             e.record()
         self.gated_by = None      # the phase events of the last layer step
         self._phases_set = False
+        # weights and tokens are still being written on the current stream
+        for s in [self.compute] + self.copies:
+            s.wait_stream(torch.cuda.current_stream())
 
     def layer_step(self, layer, stage, T=None, x=None, out=None):
         T = self.shape.T if T is None else T
