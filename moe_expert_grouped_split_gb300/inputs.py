@@ -40,6 +40,14 @@ def _gen(device, seed: int) -> torch.Generator:
     return g
 
 
+def _written(device) -> None:
+    """Waits for what this stream still has to write: peer pools stand for
+    other ranks' memory, which any stream may copy from, and tokens for what
+    any stream may read."""
+    if torch.device(device).type == "cuda":
+        torch.cuda.current_stream(device).synchronize()
+
+
 def randn_bf16(shape, std: float, seed: int, device="cpu", out: torch.Tensor | None = None):
     """N(0, std^2) drawn in fp32, rounded to bf16 (RNE).  If ``out`` is given
     the values are written into it (a bf16 view of the right shape)."""
@@ -175,6 +183,7 @@ def make_layer(shape: LayerShape, placement: Placement, base_seed: int, layer: i
     bt = None
     if bias is not None:
         bt = torch.as_tensor(np.asarray(bias, dtype=np.float32)).to(device)
+    _written(device)
     return LayerWeights(shape, placement, wr, bt, lw13, lw2, pw13, pw2, sw13, sw2)
 
 
@@ -236,6 +245,7 @@ def make_layer_fp8(shape: LayerShape, placement: Placement, base_seed: int, laye
     bt = None
     if bias is not None:
         bt = torch.as_tensor(np.asarray(bias, dtype=np.float32)).to(device)
+    _written(device)
     return LayerWeightsFp8(shape, placement, wr, bt, lw13, lw2, pw13, pw2, sw13, sw2, s13, s2, ss13, ss2)
 
 
@@ -329,6 +339,7 @@ def make_layer_nvfp4(shape: LayerShape, placement: Placement, base_seed: int, la
     bt = None
     if bias is not None:
         bt = torch.as_tensor(np.asarray(bias, dtype=np.float32)).to(device)
+    _written(device)
     return LayerWeightsNvfp4(shape, placement, wr, bt, lw13, lw2, pw13, pw2, sw13, sw2, s13, s2, ss13, ss2)
 
 
@@ -365,7 +376,9 @@ def expert_scales(wdtype: str, base_seed: int, layer: int, E: int) -> tuple:
 
 def make_tokens(T: int, H: int, base_seed: int, step: int = 0, device="cpu") -> torch.Tensor:
     """Activations x ~ N(0, 1) as bf16 [T, H]."""
-    return randn_bf16((T, H), 1.0, seed_for(base_seed, "x", step), device)
+    x = randn_bf16((T, H), 1.0, seed_for(base_seed, "x", step), device)
+    _written(device)
+    return x
 
 
 def step_token_counts(n_steps: int, lo: int, hi: int, base_seed: int) -> list:
