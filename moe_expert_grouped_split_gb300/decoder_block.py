@@ -18,8 +18,16 @@ import torch
 from . import binding as B
 
 
+def _dense(name, t, shape, dtype) -> None:
+    """The library gets addresses only: what it would misread is refused here."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: {dtype} {list(shape)}, contiguous, is needed; "
+                         f"got {t.dtype} {list(t.shape)} with strides {list(t.stride())}")
+
+
 class DecoderBlockTail:
-    """One layer's weights and buffers.
+    """One layer's weights and buffers.  Tensors are contiguous, of the types
+    and shapes named here; others are refused (ValueError).
 
     rt             Runtime whose layer `layer` is mapped (Runtime.set_layer)
     w_o            [H, D] bf16, the attention's output projection
@@ -32,6 +40,14 @@ class DecoderBlockTail:
                  eps: float = 1e-6):
         H, T = rt.cfg["hidden"], rt.cfg["max_tokens"]
         dev = w_o.device
+        D, E, (n, R) = w_o.shape[1], rt.cfg["n_experts"], a.shape[:2]
+        for name, t, shape, dtype in (("w_o", w_o, (H, D), torch.bfloat16), ("a", a, (n, R, D), torch.bfloat16),
+                                      ("b", b, (n, H, R), torch.bfloat16), ("scale", scale, (n,), torch.float32),
+                                      ("norm_weight", norm_weight, (H,), torch.bfloat16),
+                                      ("w_router", w_router, (E, H), torch.bfloat16),
+                                      ("choice_bias", choice_bias, (E,), torch.float32)):
+            if t is not None:
+                _dense(name, t, shape, dtype)
         self.rt, self.layer, self.eps = rt, layer, eps
         self.w_o = w_o.view(1, *w_o.shape)  # a buffer of one slot
         self.a, self.b, self.scale = a, b, scale
@@ -53,8 +69,12 @@ class DecoderBlockTail:
         none); residual [T, H] bf16, updated in place.  Returns the expert
         layer's output [T, H], to be added to the residual by the next
         block's norm."""
-        T, D = attn.shape
-        H = self.y.shape[1]
+        T, H, D = attn.shape[0], self.y.shape[1], self.w_o.shape[2]
+        if T > self.y.shape[0]:
+            raise ValueError(f"{T} tokens in buffers for {self.y.shape[0]}")
+        _dense("attn", attn, (T, D), torch.bfloat16)
+        _dense("adapter_ids", adapter_ids, (T,), torch.int32)
+        _dense("residual", residual, (T, H), torch.bfloat16)
         y, x, out = self.y[:T], self.x[:T], self.out[:T]
         if T == 0:
             return out
