@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
             for (int c = 0; c < N; c += 32) {
                 uint32_t v[32];
+                __syncwarp();  // the load is the whole warp's; lanes beyond T are ahead here
                 tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
                 tmem_wait_ld();
                 if (t >= p.T) continue;

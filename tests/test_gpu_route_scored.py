@@ -395,3 +395,14 @@ def test_two_threads_with_different_numbers_of_experts():
     for m in made:
         m[0].close()
     assert not failed, failed[0]
+
+
+@pytest.mark.parametrize("T", [1025, 1055, 2049, 8205])
+@pytest.mark.parametrize("H, E", [(256, 256), (7168, 256), (192, 513), (64, 72)])
+def test_last_rows_of_a_warp_of_the_tensor_core_router(T, H, E):
+    """Token counts that end inside a warp's 32 rows: every column of the
+    rows that exist, and nothing beyond them."""
+    x, wr, rb = route(T, H, E, 4, how_of(SIG), seed=T)
+    ref, mag = x.double() @ wr.double().t(), x.double().abs() @ wr.double().abs().t()
+    assert bool(((rb.logits.double() - ref).abs() <= 2.0 ** -24 * H ** 0.5 * mag + 1e-30).all())
+    check(T, E, 4, how_of(SIG), None, rb)
