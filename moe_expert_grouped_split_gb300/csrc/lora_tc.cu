@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_tc_kernel(const __
 #pragma unroll
                 for (int c = 0; c < NR; c += 16) {
                     uint32_t v[16];
+                    __syncwarp();  // the load is the whole warp's; lanes of other adapters are ahead here
                     if (got) {
                         tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + a * NR + c, v);
                         tmem_wait_ld();

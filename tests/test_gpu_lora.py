@@ -276,3 +276,13 @@ def test_few_tokens_of_a_vocabulary_projection(T, N):
     for R in (16, 64):
         args = case(T, 64, N, R, 4, np.random.default_rng(T).integers(-1, 4, T), seed=T + R)
         check(run(*args), *args)
+
+
+@pytest.mark.parametrize("R", [8, 16, 24, 64, 128])
+@pytest.mark.parametrize("T", [2049, 2100])
+def test_lanes_of_a_warp_with_different_adapters(T, R):
+    """Each of a warp's 32 rows keeps another adapter's columns than its
+    neighbours, in every group of adapters the tile goes through."""
+    for ids in (np.arange(T) % 32, np.where(np.arange(T) % 3 == 0, -1, np.arange(T) % 7)):
+        args = case(T, 264, 136, R, 32, ids, seed=R)
+        check(run(*args), *args)
