@@ -687,6 +687,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps, P <= 16 ? 2 : 1)
     early_bias<P, FULL>(p, ln, bias);
     wait_for_previous_kernel();
     let_next_kernel_start();
+    __syncwarp();  // the cluster's barrier is the whole warp's; lanes zeroed more or fewer counts
     if constexpr (ALONE) __syncthreads();
     else cluster_sync();
     for (int t = blockIdx.x * kSelectWarps + warp; t < p.T; t += gridDim.x * kSelectWarps) {

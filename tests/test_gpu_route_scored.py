@@ -406,3 +406,10 @@ def test_last_rows_of_a_warp_of_the_tensor_core_router(T, H, E):
     ref, mag = x.double() @ wr.double().t(), x.double().abs() @ wr.double().abs().t()
     assert bool(((rb.logits.double() - ref).abs() <= 2.0 ** -24 * H ** 0.5 * mag + 1e-30).all())
     check(T, E, 4, how_of(SIG), None, rb)
+
+
+@pytest.mark.parametrize("T", [9, 33, 64])
+@pytest.mark.parametrize("E", [40, 270, 300, 513, 1001])
+def test_one_kernel_of_a_cluster_with_counts_that_end_inside_a_warp(T, E):
+    x, wr, rb = route(T, 64, E, 4, how_of(SIG), seed=E)
+    check(T, E, 4, how_of(SIG), None, rb)
