@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kExpandThreads, ExpandSmem<KS>::kPerSm)
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float d[4][4];
+                    __syncwarp();  // the products are the whole warp's; lanes of other adapters are ahead here
                     Expand<KS>::product(bs[h], v, bf[h], d);
                     if (id[0] == cur) at[4 * h] = Expand<KS>::round(d, 0);
                     if (id[1] == cur) at[4 * h + kRow8] = Expand<KS>::round(d, 1);
