@@ -132,7 +132,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t) -> int | None:
-    return t if t is None or type(t) is int else t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 _dtypes = None  # bfloat16, int32, float32, once torch is needed
