@@ -49,6 +49,18 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// The driver's call wants a current context.  A host thread has one from its
+// first runtime call that needs it, which may be none of those before this.
+template <class... A>
+bool encode_tiled(EncodeTiledFn fn, A... args) {
+    CUresult r = fn(args...);
+    int dev = 0;
+    if (r != CUDA_SUCCESS && r != CUDA_ERROR_INVALID_VALUE && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaSetDevice(dev) == cudaSuccess)
+        r = fn(args...);
+    return r == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct LayerMap {
@@ -89,9 +101,10 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, in
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {(cuuint32_t)(bytes ? BK_BYTES : BK_BYTES / 2), BM};
     cuuint32_t es[2] = {1, 1};
-    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, BK_BYTES == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(fn, m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        BK_BYTES == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool encode_matrix(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t row_bytes,
@@ -102,9 +115,9 @@ bool encode_matrix(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {64, box_rows};
     cuuint32_t es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(fn, m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // A weight buffer [slots][rows][K]: a 3-D map, box [1 x 128 rows x BK_BYTES];
@@ -119,9 +132,10 @@ bool encode_slots(CUtensorMap* m, const void* base, uint64_t slots, uint64_t row
     cuuint64_t strides[2] = {row_bytes, (uint64_t)weight_slot_bytes((int64_t)rows, (int64_t)K, fmt)};
     cuuint32_t box[3] = {(cuuint32_t)(bytes ? BK_BYTES : BK_BYTES / 2), BN / 2, 1};
     cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, BK_BYTES == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(fn, m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        BK_BYTES == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 void set_last_error(const char* msg) { g_last_error = msg; }
