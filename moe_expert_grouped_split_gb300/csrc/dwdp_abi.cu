@@ -400,7 +400,7 @@ int32_t router_gemm(dwdp_ctx* ctx, const void* x, int32_t T, const void* w_route
     a.split_stride = (int64_t)T * c.n_experts;
     a.err = ctx->d_err;
     a.bsrc[0] = make_int2(0, 0);
-    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_F32, FMT_BF16, a, ctx->n_sms, stream));
+    DWDP_CUDA(ctx, launch_grouped_gemm_in_turn(EPI_F32, FMT_BF16, a, ctx->n_sms, stream));
     return DWDP_OK;
 }
 
@@ -527,8 +527,8 @@ int32_t moe_layer(dwdp_ctx* ctx, int32_t layer, int32_t stage, const void* x, co
         a.bsrc[g] = m.bsrc[g];
         if (scaled) a.gscale[g] = m.scale13[g];
     }
-    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_SILU, fmt, a, ctx->n_sms, stream,
-                                       (c.flags & DWDP_FLAG_WIDE_EPILOGUE) != 0));
+    DWDP_CUDA(ctx, launch_grouped_gemm_in_turn(EPI_SILU, fmt, a, ctx->n_sms, stream,
+                                               (c.flags & DWDP_FLAG_WIDE_EPILOGUE) != 0));
     DWDP_CUDA(ctx, mark(ctx, 4, stream));
     // G2: y = a W_down (E4M3 / NVFP4: a's rows quantized first; this phase includes it).
     if (fmt == FMT_E4M3) DWDP_CUDA(ctx, launch_quantize_rows(act, rows_all, (int)I, aq, sa, stream));
@@ -552,7 +552,7 @@ int32_t moe_layer(dwdp_ctx* ctx, int32_t layer, int32_t stage, const void* x, co
     a.ldd = H;
     a.d_rows = rows_all;
     a.D = y;
-    DWDP_CUDA(ctx, launch_grouped_gemm(EPI_BF16, fmt, a, ctx->n_sms, stream));
+    DWDP_CUDA(ctx, launch_grouped_gemm_in_turn(EPI_BF16, fmt, a, ctx->n_sms, stream));
     DWDP_CUDA(ctx, mark(ctx, 5, stream));
     // The stage's weights have been read: the next prefetch into it may start.
     if (m.n_remote > 0) DWDP_CUDA(ctx, cudaEventRecord(ctx->freed[stage], stream));
@@ -1215,7 +1215,7 @@ int32_t dwdp_grouped_gemm(dwdp_ctx* ctx, int32_t epilogue, const void* a_ptr, in
     a.col_bias = nullptr;
     a.k_split = 1;
     a.err = ctx->d_err;
-    DWDP_CUDA(ctx, launch_grouped_gemm(epilogue, FMT_BF16, a, ctx->n_sms, stream));
+    DWDP_CUDA(ctx, launch_grouped_gemm_in_turn(epilogue, FMT_BF16, a, ctx->n_sms, stream));
     return DWDP_OK;
 }
 

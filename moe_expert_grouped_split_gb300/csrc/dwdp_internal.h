@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/dwdp.h"
 
 namespace dwdp {
@@ -160,6 +162,15 @@ inline bool is_device_memory_of(const void* p, int dev) {
 // warps instead of four (ignored otherwise).
 cudaError_t launch_grouped_gemm(int epi, int fmt, const GemmArgs& args, int n_sms, cudaStream_t stream,
                                 bool wide_epilogue = false);
+// The launch sets the kernel's shared-memory limit to its own size first, and
+// the limit is the kernel's: launches of several host threads (a context each)
+// take turns, or one could find it below its size and be refused.
+inline cudaError_t launch_grouped_gemm_in_turn(int epi, int fmt, const GemmArgs& args, int n_sms, cudaStream_t stream,
+                                               bool wide_epilogue = false) {
+    static std::mutex turn;
+    const std::lock_guard<std::mutex> lock(turn);
+    return launch_grouped_gemm(epi, fmt, args, n_sms, stream, wide_epilogue);
+}
 
 // K parts of the router GEMM (bf16, K = H) for T tokens and E experts: with
 // fewer 128-token tiles than SMs, as many parts as still fit one wave of

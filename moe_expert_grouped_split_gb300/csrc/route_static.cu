@@ -123,7 +123,7 @@ extern "C" int32_t dwdp_route_static(const void* x, int32_t T, int32_t hidden, i
     a.split_stride = (int64_t)T * n_experts;
     a.err = err;
     a.bsrc[0] = make_int2(0, 0);
-    e = launch_grouped_gemm(EPI_F32, FMT_BF16, a, n_sms, stream);
+    e = launch_grouped_gemm_in_turn(EPI_F32, FMT_BF16, a, n_sms, stream);
     if (e == cudaSuccess)
         e = launch_topk(logits, parts, (int64_t)T * n_experts, nullptr, T, n_experts, top_k, out->topk_ids,
                         out->topk_w, nullptr, err, stream);

@@ -110,3 +110,45 @@ def test_rejects_bad_arguments(rt):
         B.dwdp_grouped_gemm(rt.ctx, 0, a, 8, 64, 64, off, 1, [b], [0, 3], d)
     with pytest.raises(B.DwdpError):   # epilogue out of range
         B.dwdp_grouped_gemm(rt.ctx, 5, a, 8, 64, 64, off, 1, [b], [0, 0], d)
+
+
+def test_two_threads_with_different_numbers_of_groups():
+    """The same kernel with other sizes of shared memory from two host
+    threads, a context each: neither call is refused."""
+    import ctypes
+    import threading
+
+    failed, made = [], []
+    for G in (1, 1000):
+        r = B.Runtime(256, 128, 8, 2, 0, 64, 1, 0)
+        a = torch.ones((64, 64), dtype=torch.bfloat16, device="cuda")
+        w = torch.ones((1, 64, 64), dtype=torch.bfloat16, device="cuda")
+        off = torch.full((G + 1,), 64, dtype=torch.int32, device="cuda")
+        off[0] = 0
+        d = torch.zeros((64, 64), dtype=torch.bfloat16, device="cuda")
+        stream = torch.cuda.Stream()
+        bufs, slots = (B.dwdp_pool * 1)(B.pool(w, None)), (ctypes.c_int32 * (2 * G))()
+        made.append((r, d, (r.ctx, B.EPI_BF16, a.data_ptr(), 64, 64, 64, off.data_ptr(), G, bufs, 1, slots, d.data_ptr(),
+                            stream.cuda_stream), (a, w, off, stream)))
+    torch.cuda.synchronize()
+
+    def work(r, d, args, keep):
+        call = B.lib().dwdp_grouped_gemm
+        for i in range(6000):
+            if call(*args):
+                failed.append(B.dwdp_last_error(r.ctx))
+                return
+            if i % 500 == 499:
+                keep[3].synchronize()
+
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    status = [m[0].device_status() for m in made]
+    for m in made:
+        m[0].close()
+    assert not failed, failed[0]
+    assert status == [0, 0] and all((m[1] == 64).all() for m in made)
