@@ -527,7 +527,9 @@ typedef struct {
  *   (divided by their sum if renormalize) * scale.
  * Ties go to the lowest group and expert id.  choice_bias [E] fp32 (device)
  * steers the choice only, not the weights; -inf takes an expert out: it is
- * chosen only where fewer than k others are left, and then has weight 0.  The
+ * chosen only where fewer than k others are left, the lowest ids first, and
+ * then has weight 0.  Weights are right to a few units in the last place
+ * (approximate exponentials and reciprocals; 0 below 2^-126).  The
  * choice is the one these formulas give in binary64 on the fp32 logits (a
  * token whose decision binary32 cannot tell apart is decided again in
  * binary64), so it depends on the logits alone.  The logits are deterministic
@@ -549,8 +551,12 @@ int32_t dwdp_route_scored(dwdp_ctx* ctx, const void* x, int32_t T, const void* w
  * a: bf16 [n_adapters][R][K]; b: bf16 [n_adapters][N][R]; adapter_scale fp32
  * [n_adapters]; adapter_ids int32 [T] (all device).  Adapters of a smaller
  * rank are padded with zero rows (columns).  Tokens may come in any order;
- * tokens of one adapter next to each other are the cheap case (above 2048
- * tokens, or in banks of 256 adapters and more, the only one).  x: row t at
+ * tokens of one adapter next to each other are the cheap case.  Where adapters
+ * change from token to token (in half of 32 pairs of ids 2 i, 2 i + 1 spread
+ * over the batch), up to 2048 tokens, from 1024 on with T (K + N) up to 2^24,
+ * of a bank of up to 255 adapters are taken in the adapters' order; other such
+ * batches read x again for every few adapters of a tile of 16 to 128 tokens.
+ * x: row t at
  * x + t * x_stride elements, K of them; base and out: row t at t *
  * base_stride / t * out_stride, N of them; every stride a multiple of 8 and
  * no smaller than the row.  out may be base (equal strides); no other

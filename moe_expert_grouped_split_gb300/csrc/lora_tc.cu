@@ -12,7 +12,9 @@
 // 8192 tokens, 7168 x 7168, rank 16: 73.5 us for 360 MB, 4.9 TB/s (72% of the
 // copy rate): shrink 25 us, expand 46 us.
 // A tile's tokens may have any adapters: shrink multiplies the tile by each
-// that occurs (several at a time) and keeps a row's own; so does expand.
+// that occurs (4 at a time up to rank 16, else one) and keeps a row's own; so
+// does expand.  Every such step reads x again: 16 adapters at random instead of
+// in order, 8192 tokens, 7168 x 7168: rank 16 273 us (71), rank 64 865 (107).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -409,6 +409,8 @@ cudaError_t launch_form(const NormArgs& p, cudaStream_t s) {
     // 4096 - / 44.8 / 48.4, 7168 - / 84.5 / 85.1 (92% of the copy rate), 8192 -
     // / 94.3 / 99.7.  Neither: 512 3.2 / 8.7 / -, 1000 4.7 / 8.8 / -, 4096 - /
     // 27.7 / 29.5, 7168 - / 60 / 43.8.  512 x 64 rows, both: 1.9 / 1.6 / -.
+    // Wider rows, both: 8200 147 (60%), 16384 265 (67%), 32768 554 (64%); with
+    // codes that kernel spills 72 bytes a thread at its 64 registers.
     if (nv <= 64 && p.rows >= 8 * sms)
         return launch(add_rmsnorm_warp_kernel<2, RES, CODES, TINY>, p, (p.rows + 7) / 8, 256, 0, s);
     if constexpr (!RES)
