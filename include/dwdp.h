@@ -587,6 +587,138 @@ int32_t dwdp_moe_layer_codes(dwdp_ctx* ctx, int32_t layer, int32_t stage, const 
                              int32_t T, const dwdp_route_out* route, void* out, void* ws, size_t ws_bytes,
                              dwdp_stream_t stream);
 
+/* ---- training the block's norms and its router ---------------------------
+ * The calls below add what a decoder block's second half needs around
+ * dwdp_moe_layer when its norms, gates or router are trained or tuned: the
+ * norms before and after a block in one pass, with their gradients and with
+ * rows kept in 8 bits for them, the router's losses, and the gradient of its
+ * logits.  dwdp_sandwich_norm serves single tokens too.  All can be captured
+ * into CUDA graphs, and give the same bits from run to run. */
+
+/* What dwdp_sandwich_norm and its gradients share.
+ *   pre_weight, post_weight  bf16 [H] (device) or NULL: no such norm
+ *   gate          bf16 [n_groups][H] (device), or NULL (n_groups 0): 1
+ *   row_offsets   int32 [n_groups + 1] (device), non-decreasing: gate g is for
+ *                 rows row_offsets[g] .. row_offsets[g + 1] - 1, and rows outside
+ *                 [row_offsets[0], row_offsets[n_groups]) are left alone:
+ *                 not read, not written, no part of any sum.
+ *                 NULL: one gate for all rows (n_groups 1)
+ *   block_scale, residual_scale  finite constants
+ *   eps           of both norms, finite and at least 2^-100 */
+typedef struct {
+    const void* pre_weight;
+    const void* post_weight;
+    const void* gate;
+    const int32_t* row_offsets;
+    int32_t n_groups;
+    float block_scale;
+    float residual_scale;
+    float eps;
+} dwdp_sandwich;
+#define DWDP_MAX_GATES 32768
+
+/* The norm after a block, its gate, the residual addition and the next
+ * block's norm.  Per row of H elements, in binary32:
+ *   n = x rx post_weight,  rx = 1 / sqrt(mean(x^2) + eps)   (n = x without post_weight)
+ *   h = residual_scale residual + block_scale gate n        (residual NULL: 0)
+ *   residual_out = bf16(h)                                  (iff given)
+ *   y = h rh pre_weight,   rh = 1 / sqrt(mean(h^2) + eps)   from the unrounded h
+ *   out = bf16(y)                                           (iff pre_weight is given)
+ *   codes, row_scale: y as E4M3 rows, as in dwdp_add_rmsnorm (iff given)
+ * and what dwdp_sandwich_norm_grad takes (each iff given):
+ *   x_codes, x_scale: x as E4M3 rows, scale = max|x| / 448 (1 for a row of zeros)
+ *   h_codes, h_scale: the unrounded h, likewise
+ *   rstd [rows][2]: rx and rh (1 for a norm that is not there)
+ * The E4M3 rows are rounded once, to nearest even, by approximate reciprocals: a
+ * value next to the middle of two codes may take either; a row whose largest
+ * magnitude (codes: of h pre_weight) is below 2^-100 is quantized as if it were
+ * 2^-100.  h and h pre_weight have to stay in binary32's range; squares may pass
+ * it.  A NaN makes its row NaN where it goes.
+ * x: bf16, row r at x + r * x_stride elements (x_stride >= H, a multiple of 8);
+ * residual, residual_out, out bf16 [rows][H]; codes, x_codes, h_codes E4M3
+ * bytes [rows][H]; row_scale, x_scale, h_scale fp32 [rows]; rstd fp32.  Codes
+ * and their scale go together; out and codes need pre_weight.  residual_out may
+ * be residual, and out may be x when x_stride == H; no other overlap.  H a
+ * multiple of 8, 8 <= H <= 32768; rows in [0, 2^31); at most DWDP_MAX_GATES
+ * groups.  All pointers device, 16-byte aligned.  Enqueued on `stream`; needs no
+ * context.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int32_t dwdp_sandwich_norm(const dwdp_sandwich* how, const void* x, int64_t x_stride, const void* residual,
+                           int64_t rows, int32_t H, void* residual_out, void* out, void* codes, float* row_scale,
+                           void* x_codes, float* x_scale, void* h_codes, float* h_scale, float* rstd,
+                           dwdp_stream_t stream);
+
+/* The gradients of dwdp_sandwich_norm (without post_weight and gate: of
+ * dwdp_add_rmsnorm).  From x and h (bf16 rows, or E4M3 codes where x_scale /
+ * h_scale is given), rstd as the forward call wrote it, and the gradients of
+ * out (dout) and residual_out (dresidual_out; NULL = 0), both bf16 [rows][H]:
+ *   hhat = h rh,  gy = dout pre_weight
+ *   dh = dresidual_out + rh (gy - hhat mean(gy hhat))       (dh = dresidual_out without pre_weight)
+ *   dresidual = residual_scale dh,  dn = block_scale gate dh
+ *   xhat = x rx,  gn = dn post_weight
+ *   dx = rx (gn - xhat mean(gn xhat))                       (dx = dn without post_weight)
+ *   dpre_weight = sum over rows of dout hhat,  dpost_weight = sum of dn xhat
+ *   dgate[g] = sum over its rows of block_scale dh xhat post_weight
+ * in binary32; dx and dresidual are rounded once to bf16 [rows][H], the sums
+ * are fp32 ([H], [H], [n_groups][H]), written whole (zeros where there are no
+ * rows).  Each output may be NULL.  x may be NULL without post_weight and
+ * dgate, and h without pre_weight, which also has no dout.  x_stride (in
+ * elements) holds for x's codes too; h is dense.  dresidual may be
+ * dresidual_out and dx may be dout; no other overlap.  H at most 8192, the
+ * rest as for dwdp_sandwich_norm.  ws: dwdp_sandwich_grad_workspace_bytes(rows,
+ * H) bytes (device), needed for the sums only.  Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA. */
+int32_t dwdp_sandwich_norm_grad(const dwdp_sandwich* how, const void* x, int64_t x_stride, const float* x_scale,
+                                const void* h, const float* h_scale, const float* rstd, const void* dout,
+                                const void* dresidual_out, int64_t rows, int32_t H, void* dx, void* dresidual,
+                                float* dpost_weight, float* dpre_weight, float* dgate, void* ws, size_t ws_bytes,
+                                dwdp_stream_t stream);
+
+/* Workspace of dwdp_sandwich_norm_grad; 0 for sizes it refuses. */
+size_t dwdp_sandwich_grad_workspace_bytes(int64_t rows, int32_t H);
+
+/* How evenly the experts were used, per sequence.  Sequence b has tokens
+ * seq_offsets[b] .. seq_offsets[b + 1] - 1, T_b of them (seq_offsets: int32
+ * [n_seqs + 1], device, non-decreasing; NULL: one sequence of all T tokens);
+ * tokens outside [seq_offsets[0], seq_offsets[n_seqs]) are in none.  From the
+ * router's logits z [T][E] fp32 and choices topk_ids [T][k]
+ * (dwdp_route_scored's logits and topk_ids), with the token's shares p =
+ * softmax(z), or s / sum(s) with s = sigmoid(z):
+ *   counts [n_seqs][E]  tokens of the sequence that chose the expert (int32)
+ *   mean_p [n_seqs][E]  mean of p over the sequence
+ *   balance [n_seqs]    E / (k T_b) sum_e counts mean_p (1 when all is even)
+ *   z [n_seqs]          mean of logsumexp(z)^2; NULL = not computed
+ * all zero for a sequence without tokens.  Sums are binary32, shares right to
+ * a few units in the last place times the logits' spread (approximate
+ * exponentials).  Of `scoring` only score is used.  A NaN or infinite logit may
+ * make its sequence's mean_p, balance and z NaN.  An id outside [0, E) is not
+ * counted; the device error word reports it (DEVICE_CHECK).  T at most
+ * max_tokens and 2^30.  ws: dwdp_balance_workspace_bytes(T, E, n_seqs) bytes,
+ * device.  All pointers 16-byte aligned.  Enqueued on `stream`.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int32_t dwdp_balance_loss(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, int32_t T,
+                          const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring, int32_t* counts,
+                          float* mean_p, float* balance, float* z, void* ws, size_t ws_bytes, dwdp_stream_t stream);
+
+/* Workspace of dwdp_balance_loss; 0 for sizes it refuses. */
+size_t dwdp_balance_workspace_bytes(int32_t T, int32_t E, int32_t n_seqs);
+
+/* The gradient of dwdp_route_scored's logits, from that of its weights and
+ * from dwdp_balance_loss's losses:
+ *   dlogits = d/dz ( sum dtopk_w topk_w + sum_b dbalance[b] balance[b] + dz[b] z[b] )
+ * with the choice and the counts held fixed.  dtopk_w fp32 [T][k], dbalance and
+ * dz fp32 [n_seqs] (device): each NULL = 0.  counts as dwdp_balance_loss wrote them
+ * (needed with dbalance; counts added up over several devices, with dbalance to
+ * match, serve as well).  Tokens in no sequence get the weights' part only.
+ * score, renormalize and scale of `scoring` are used.  The ids of a token are distinct.
+ * dlogits [T][E]: fp32, or bf16 when dlogits_bf16 is 1; every element is written.
+ * A NaN or infinite logit may make its token's gradient NaN; an id outside [0,
+ * E) is skipped and reported as above.  Other arguments as for dwdp_balance_loss;
+ * dlogits overlaps none of them.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int32_t dwdp_route_scored_grad(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, const float* dtopk_w,
+                               int32_t T, const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring,
+                               const int32_t* counts, const float* dbalance, const float* dz, void* dlogits,
+                               int32_t dlogits_bf16, dwdp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

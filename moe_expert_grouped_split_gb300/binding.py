@@ -23,6 +23,7 @@ DTYPE_BF16, DTYPE_E4M3, DTYPE_NVFP4 = 0, 1, 2
 FLAG_WIDE_EPILOGUE = 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
+MAX_GATES = 32768
 
 
 def weight_slot_bytes(rows: int, K: int, weight_dtype: int) -> int:
@@ -60,6 +61,12 @@ class dwdp_route_out(ctypes.Structure):
 class dwdp_scoring(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
                 ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class dwdp_sandwich(ctypes.Structure):
+    _fields_ = [("pre_weight", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("row_offsets", ctypes.c_void_p), ("n_groups", ctypes.c_int32), ("block_scale", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class dwdp_copy_slice(ctypes.Structure):
@@ -109,6 +116,16 @@ SIGNATURES = [
     ("dwdp_lora_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
     ("dwdp_moe_layer_codes", _I32, [_VP, _I32, _I32, _VP, _VP, _I32, ctypes.POINTER(dwdp_route_out), _VP, _VP,
                                     ctypes.c_size_t, _VP]),
+    ("dwdp_sandwich_norm", _I32, [ctypes.POINTER(dwdp_sandwich), _VP, ctypes.c_int64, _VP, ctypes.c_int64, _I32] +
+     [_VP] * 10),
+    ("dwdp_sandwich_norm_grad", _I32, [ctypes.POINTER(dwdp_sandwich), _VP, ctypes.c_int64] + [_VP] * 6 +
+     [ctypes.c_int64, _I32] + [_VP] * 6 + [ctypes.c_size_t, _VP]),
+    ("dwdp_sandwich_grad_workspace_bytes", ctypes.c_size_t, [ctypes.c_int64, _I32]),
+    ("dwdp_balance_loss", _I32, [_VP, _VP, _VP, _I32, _VP, _I32, ctypes.POINTER(dwdp_scoring), _VP, _VP, _VP, _VP, _VP,
+                                 ctypes.c_size_t, _VP]),
+    ("dwdp_balance_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32]),
+    ("dwdp_route_scored_grad", _I32, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, ctypes.POINTER(dwdp_scoring), _VP, _VP, _VP,
+                                      _VP, _I32, _VP]),
     ("dwdp_plan_prefetch", _I32, [_I32, _I32, _I32, _I32, _I32P, _I32P, _I32P, _I32, ctypes.c_size_t,
                                   ctypes.POINTER(dwdp_copy_slice), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
 ]
@@ -143,6 +160,31 @@ def _load_dtypes():
     import torch
     _dtypes = torch.bfloat16, torch.int32, torch.float32
     return _dtypes
+
+
+_current_device = None
+
+
+def _device() -> int:
+    """The current CUDA device's index."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        torch.cuda.init()
+        _current_device = torch._C._cuda_getDevice
+    return _current_device()
+
+
+def _like(call, device, name, t, dtypes, shape) -> int | None:
+    """t's address; ValueError unless it is None or a dense tensor of one of
+    `dtypes` and of `shape` on the current device: the library gets addresses
+    only.  (0.5 us a tensor.)"""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{call}: {name} {t.dtype} {list(t.shape)} strides {list(t.stride())} on {t.device}: "
+                         f"{' or '.join(str(d) for d in dtypes)} {list(shape)}, dense, on cuda:{device} is needed")
+    return t.data_ptr()
 
 
 _current_raw_stream = None
@@ -279,6 +321,54 @@ def dwdp_lora_add(ctx, x, x_stride, T, K, N, a, b, adapter_scale, n_adapters, R,
                                     _ptr(ws), ws_bytes, _stream(stream)))
 
 
+def sandwich(pre_weight=None, post_weight=None, gate=None, row_offsets=None, n_groups=0, block_scale=1.0,
+             residual_scale=1.0, eps=1e-6) -> dwdp_sandwich:
+    return dwdp_sandwich(_ptr(pre_weight), _ptr(post_weight), _ptr(gate), _ptr(row_offsets), n_groups, block_scale,
+                         residual_scale, eps)
+
+
+def dwdp_sandwich_norm(how: dwdp_sandwich, x, rows, H, residual=None, residual_out=None, out=None, codes=None,
+                       row_scale=None, x_codes=None, x_scale=None, h_codes=None, h_scale=None, rstd=None,
+                       x_stride=None, stream=None) -> None:
+    """x_stride: elements between x's rows (None: H)."""
+    _check(None, lib().dwdp_sandwich_norm(ctypes.byref(how), _ptr(x), H if x_stride is None else x_stride,
+                                          _ptr(residual), rows, H, _ptr(residual_out), _ptr(out), _ptr(codes),
+                                          _ptr(row_scale), _ptr(x_codes), _ptr(x_scale), _ptr(h_codes), _ptr(h_scale),
+                                          _ptr(rstd), _stream(stream)))
+
+
+def dwdp_sandwich_norm_grad(how: dwdp_sandwich, x, h, rstd, dout, dresidual_out, rows, H, dx=None, dresidual=None,
+                            dpost_weight=None, dpre_weight=None, dgate=None, ws=None, ws_bytes=0, x_scale=None,
+                            h_scale=None, x_stride=None, stream=None) -> None:
+    """x_stride: elements between x's rows (None: H)."""
+    _check(None, lib().dwdp_sandwich_norm_grad(
+        ctypes.byref(how), _ptr(x), H if x_stride is None else x_stride, _ptr(x_scale), _ptr(h), _ptr(h_scale),
+        _ptr(rstd), _ptr(dout), _ptr(dresidual_out), rows, H, _ptr(dx), _ptr(dresidual), _ptr(dpost_weight),
+        _ptr(dpre_weight), _ptr(dgate), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dwdp_sandwich_grad_workspace_bytes(rows, H) -> int:
+    return lib().dwdp_sandwich_grad_workspace_bytes(rows, H)
+
+
+def dwdp_balance_loss(ctx, logits, topk_ids, T, seq_offsets, n_seqs, how: dwdp_scoring, counts, mean_p, balance, z, ws,
+                      ws_bytes, stream=None) -> None:
+    _check(ctx, lib().dwdp_balance_loss(ctx, _ptr(logits), _ptr(topk_ids), T, _ptr(seq_offsets), n_seqs,
+                                        ctypes.byref(how), _ptr(counts), _ptr(mean_p), _ptr(balance), _ptr(z), _ptr(ws),
+                                        ws_bytes, _stream(stream)))
+
+
+def dwdp_balance_workspace_bytes(T, E, n_seqs) -> int:
+    return lib().dwdp_balance_workspace_bytes(T, E, n_seqs)
+
+
+def dwdp_route_scored_grad(ctx, logits, topk_ids, dtopk_w, T, seq_offsets, n_seqs, how: dwdp_scoring, counts, dbalance,
+                           dz, dlogits, dlogits_bf16=0, stream=None) -> None:
+    _check(ctx, lib().dwdp_route_scored_grad(ctx, _ptr(logits), _ptr(topk_ids), _ptr(dtopk_w), T, _ptr(seq_offsets),
+                                             n_seqs, ctypes.byref(how), _ptr(counts), _ptr(dbalance), _ptr(dz),
+                                             _ptr(dlogits), dlogits_bf16, _stream(stream)))
+
+
 def dwdp_wait_stage(ctx, stage, timeout_ms) -> int:
     """Returns the status code (OK or TIMEOUT) instead of raising on TIMEOUT."""
     rc = lib().dwdp_wait_stage(ctx, stage, timeout_ms)
@@ -409,6 +499,127 @@ class RouteBuffers:
                            self.logits)
 
 
+class BalanceBuffers:
+    """Device tensors for dwdp_balance_loss's outputs (allocation only)."""
+
+    def __init__(self, n_seqs: int, E: int, z: bool = True, device="cuda"):
+        import torch
+        f32 = dict(dtype=torch.float32, device=device)
+        self.n_seqs, self.E = n_seqs, E
+        self.counts = torch.empty((n_seqs, E), dtype=torch.int32, device=device)
+        self.mean_p = torch.empty((n_seqs, E), **f32)
+        self.balance = torch.empty(n_seqs, **f32)
+        self.z = torch.empty(n_seqs, **f32) if z else None
+
+
+class SandwichNorm:
+    """The weights and constants of dwdp_sandwich_norm, and the workspace of its
+    gradients for up to max_rows rows.  forward and grad look at every tensor's
+    type, shape and device (ValueError) and forward to the C ABI; outputs
+    that are not asked for stay None.  pre_weight, post_weight: bf16 [H] or None.
+    gate: bf16 [H] or [groups, H], with row_offsets int32 [groups + 1], up to
+    max_groups of them."""
+
+    def __init__(self, H, max_rows, pre_weight=None, post_weight=None, block_scale=1.0, residual_scale=1.0, eps=1e-6,
+                 max_groups=1, device="cuda"):
+        import torch
+        self.H, self.max_rows, self.max_groups = H, max_rows, max_groups
+        self.pre_weight, self.post_weight = pre_weight, post_weight
+        self._bf16, self._i32, self._f32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
+        self._e4m3, self._kept = (torch.float8_e4m3fn, torch.uint8), None
+        self._row = torch.Size((H,))
+        for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
+            _like("SandwichNorm", _device(), name, w, self._bf16, self._row)
+        self._how = sandwich(pre_weight, post_weight, None, None, 0, block_scale, residual_scale, eps)
+        self.ws_bytes = dwdp_sandwich_grad_workspace_bytes(max_rows, H)
+        self._device_name, self._ws = device, None
+
+    @property
+    def ws(self):
+        """The gradients' workspace, made when first used."""
+        if self._ws is None:
+            import torch
+            self._ws = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=self._device_name)
+        return self._ws
+
+    def _rows_of(self, call, device, x, codes=False):
+        """(rows, stride, address) of x, whose rows may lie apart."""
+        if (x.dim() != 2 or x.shape[1] != self.H or x.dtype not in (self._e4m3 if codes else self._bf16)
+                or x.stride(1) != 1 or x.get_device() != device or x.shape[0] > self.max_rows):
+            raise ValueError(f"{call}: x {x.dtype} {list(x.shape)} strides {list(x.stride())} on {x.device}: "
+                             f"{'E4M3' if codes else 'bf16'} rows of {self.H}, {self.max_rows} at most, on cuda:{device} "
+                             "are needed")
+        rows = x.shape[0]
+        return rows, x.stride(0) if rows > 1 else self.H, x.data_ptr()
+
+    def _set_groups(self, call, device, gate, row_offsets) -> int:
+        how = self._how
+        if gate is None:
+            if row_offsets is not None:
+                raise ValueError(f"{call}: row_offsets go with a gate")
+            how.gate, how.row_offsets, how.n_groups = None, None, 0
+            return 0
+        G = 1 if gate.dim() == 1 else gate.shape[0]
+        if G > max(1, self.max_groups) or (row_offsets is None and G != 1):
+            raise ValueError(f"{call}: {G} gates; max_groups is {self.max_groups}, and more than one need row_offsets")
+        how.gate = _like(call, device, "gate", gate, self._bf16, (self.H,) if gate.dim() == 1 else (G, self.H))
+        how.row_offsets = _like(call, device, "row_offsets", row_offsets, self._i32, (G + 1,))
+        how.n_groups = G
+        return G
+
+    def forward(self, x, residual=None, residual_out=None, out=None, gate=None, row_offsets=None, codes=None,
+                row_scale=None, x_codes=None, x_scale=None, h_codes=None, h_scale=None, rstd=None, stream=None) -> None:
+        """x [rows, H] bf16 (rows may lie apart); residual, residual_out, out
+        [rows, H] bf16; codes, x_codes, h_codes [rows, H] E4M3 (or uint8);
+        row_scale, x_scale, h_scale [rows] and rstd [rows, 2] fp32."""
+        device, call = _device(), "sandwich norm"
+        rows, stride, xp = self._rows_of(call, device, x)
+        self._set_groups(call, device, gate, row_offsets)
+        bf16, e4m3, f32, full, one = self._bf16, self._e4m3, self._f32, (rows, self.H), (rows,)
+        like = _like
+        rc = lib().dwdp_sandwich_norm(
+            self._how, xp, stride, like(call, device, "residual", residual, bf16, full), rows, self.H,
+            like(call, device, "residual_out", residual_out, bf16, full), like(call, device, "out", out, bf16, full),
+            like(call, device, "codes", codes, e4m3, full), like(call, device, "row_scale", row_scale, f32, one),
+            like(call, device, "x_codes", x_codes, e4m3, full), like(call, device, "x_scale", x_scale, f32, one),
+            like(call, device, "h_codes", h_codes, e4m3, full), like(call, device, "h_scale", h_scale, f32, one),
+            like(call, device, "rstd", rstd, f32, (rows, 2)), _stream(stream))
+        if rc:
+            _check(None, rc)
+
+    def grad(self, x, h, rstd, dout, dresidual_out=None, dx=None, dresidual=None, dpost_weight=None, dpre_weight=None,
+             dgate=None, gate=None, row_offsets=None, x_scale=None, h_scale=None, stream=None) -> None:
+        """x [rows, H] bf16 or, with x_scale [rows] fp32, E4M3 (rows may lie
+        apart); h likewise, dense; rstd [rows, 2] fp32; dout, dresidual_out, dx,
+        dresidual [rows, H] bf16; dpost_weight, dpre_weight [H] and dgate (of
+        gate's shape) fp32."""
+        device, call = _device(), "sandwich norm's gradient"
+        first = next((t for t in (x, dout, dresidual_out) if t is not None), None)
+        if first is None:
+            raise ValueError(f"{call}: neither x nor dout nor dresidual_out")
+        rows, stride, xp = first.shape[0], self.H, None
+        if x is not None:
+            rows, stride, xp = self._rows_of(call, device, x, x_scale is not None)
+        elif rows > self.max_rows:
+            raise ValueError(f"{call}: {rows} rows; max_rows is {self.max_rows}")
+        G = self._set_groups(call, device, gate, row_offsets)
+        bf16, f32, full, one, row = self._bf16, self._f32, (rows, self.H), (rows,), self._row
+        like = _like
+        ws = self.ws
+        rc = lib().dwdp_sandwich_norm_grad(
+            self._how, xp, stride, like(call, device, "x_scale", x_scale, f32, one),
+            like(call, device, "h", h, bf16 if h_scale is None else self._e4m3, full),
+            like(call, device, "h_scale", h_scale, f32, one), like(call, device, "rstd", rstd, f32, (rows, 2)),
+            like(call, device, "dout", dout, bf16, full), like(call, device, "dresidual_out", dresidual_out, bf16, full),
+            rows, self.H, like(call, device, "dx", dx, bf16, full), like(call, device, "dresidual", dresidual, bf16, full),
+            like(call, device, "dpost_weight", dpost_weight, f32, row),
+            like(call, device, "dpre_weight", dpre_weight, f32, row),
+            like(call, device, "dgate", dgate, f32, gate.shape if gate is not None else (G, self.H)), ws.data_ptr(),
+            self.ws_bytes, _stream(stream))
+        if rc:
+            _check(None, rc)
+
+
 class Runtime:
     """One dwdp context with its stage buffers (two by default) and a
     workspace (torch allocations; at least min_ws_bytes, e.g. what
@@ -482,6 +693,50 @@ class Runtime:
         rc = lib().dwdp_lora_add(self.ctx, x.data_ptr(), xs, T, K, N, a.data_ptr(), b.data_ptr(),
                                  adapter_scale.data_ptr(), n, R, adapter_ids.data_ptr(), base.data_ptr(), bs,
                                  out.data_ptr(), os, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        if rc:
+            _check(self.ctx, rc)
+
+    def _router(self, call, device, logits, topk_ids, seq_offsets, n_seqs):
+        """(tokens, addresses of logits, topk_ids and seq_offsets)."""
+        bf16, i32, f32 = _dtypes or _load_dtypes()
+        T, E, k = logits.shape[0], self.cfg["n_experts"], self.cfg["top_k"]
+        if seq_offsets is None and n_seqs != 1:
+            raise ValueError(f"{call}: {n_seqs} sequences need seq_offsets")
+        return (T, _like(call, device, "logits", logits, (f32,), (T, E)),
+                _like(call, device, "topk_ids", topk_ids, (i32,), (T, k)),
+                _like(call, device, "seq_offsets", seq_offsets, (i32,), (n_seqs + 1,)))
+
+    def balance_loss(self, logits, topk_ids, how: dwdp_scoring, out: BalanceBuffers, seq_offsets=None,
+                     stream=None) -> None:
+        """logits [T, E] fp32 and topk_ids [T, k] int32 as route_scored gives
+        them (RouteBuffers' first T rows); seq_offsets int32 [out.n_seqs + 1] or
+        None (one sequence).  The workspace: Runtime(min_ws_bytes=
+        dwdp_balance_workspace_bytes(...))."""
+        device, call = _device(), "balance_loss"
+        T, lp, ip, op = self._router(call, device, logits, topk_ids, seq_offsets, out.n_seqs)
+        if out.E != self.cfg["n_experts"]:
+            raise ValueError(f"{call}: buffers for {out.E} experts")
+        rc = lib().dwdp_balance_loss(self.ctx, lp, ip, T, op, out.n_seqs, how, out.counts.data_ptr(),
+                                     out.mean_p.data_ptr(), out.balance.data_ptr(), _ptr(out.z), self.ws.data_ptr(),
+                                     self.ws_bytes, _stream(stream))
+        if rc:
+            _check(self.ctx, rc)
+
+    def route_scored_grad(self, logits, topk_ids, how: dwdp_scoring, dlogits, dtopk_w=None, counts=None, dbalance=None,
+                          dz=None, seq_offsets=None, stream=None) -> None:
+        """dlogits [T, E] fp32 or bf16, from dtopk_w [T, k], dbalance and dz
+        [n_seqs] fp32 (each may be None) and balance_loss's counts [n_seqs, E]."""
+        device, call = _device(), "route_scored_grad"
+        bf16, i32, f32 = _dtypes or _load_dtypes()
+        n_seqs = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        T, lp, ip, op = self._router(call, device, logits, topk_ids, seq_offsets, n_seqs)
+        E, of_f32, each = self.cfg["n_experts"], (f32,), (n_seqs,)
+        rc = lib().dwdp_route_scored_grad(
+            self.ctx, lp, ip, _like(call, device, "dtopk_w", dtopk_w, of_f32, (T, self.cfg["top_k"])), T, op, n_seqs, how,
+            _like(call, device, "counts", counts, (i32,), (n_seqs, E)),
+            _like(call, device, "dbalance", dbalance, of_f32, each), _like(call, device, "dz", dz, of_f32, each),
+            _like(call, device, "dlogits", dlogits, (f32, bf16), (T, E)), 1 if dlogits.dtype is bf16 else 0,
+            _stream(stream))
         if rc:
             _check(self.ctx, rc)
 

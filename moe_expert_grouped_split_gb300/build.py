@@ -21,7 +21,7 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = PKG / "libdwdp.so"
 SOURCES = ["gemm.cu", "route.cu", "dwdp_abi.cu", "route_static.cu", "norm.cu", "router.cu", "router_pair.cu", "route_scored.cu", "lora.cu",
-           "lora_tc.cu"]
+           "lora_tc.cu", "sandwich.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 

@@ -957,6 +957,227 @@ int32_t dwdp_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, 
     return e == cudaSuccess ? DWDP_OK : cuda_fail(nullptr, e, "dwdp_add_rmsnorm");
 }
 
+// What both directions of the sandwich norm ask of their common part.
+static int32_t check_sandwich(const dwdp_sandwich* how, const void* x, int64_t x_stride, int64_t rows, int32_t H,
+                              int32_t most_H) {
+    if (!how) return fail(nullptr, DWDP_ERR_INVALID_ARG, "how is NULL");
+    if (rows < 0 || rows >= ((int64_t)1 << 31)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "rows outside [0, 2^31)");
+    if (H <= 0 || H % 8 || H > most_H)
+        return fail(nullptr, DWDP_ERR_UNSUPPORTED, "H must be a multiple of 8 in 8..%d", most_H);
+    if (x && (x_stride < H || x_stride % 8))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least H");
+    if (!std::isfinite(how->block_scale) || !std::isfinite(how->residual_scale))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "block_scale and residual_scale must be finite");
+    if (!std::isfinite(how->eps) || how->eps < 0x1p-100f)
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "eps must be finite and at least 2^-100");
+    if (how->gate ? how->n_groups < 1 || (!how->row_offsets && how->n_groups != 1) : how->n_groups || how->row_offsets)
+        return fail(nullptr, DWDP_ERR_INVALID_ARG,
+                    "n_groups and row_offsets go with gate: no gate, no groups; no row_offsets, one group");
+    if (how->n_groups > DWDP_MAX_GATES)
+        return fail(nullptr, DWDP_ERR_UNSUPPORTED, "at most %d groups", DWDP_MAX_GATES);
+    if (!aligned16(how->pre_weight) || !aligned16(how->post_weight) || !aligned16(how->gate) ||
+        !aligned16(how->row_offsets) || !aligned16(x))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    return DWDP_OK;
+}
+
+int32_t dwdp_sandwich_norm(const dwdp_sandwich* how, const void* x, int64_t x_stride, const void* residual,
+                           int64_t rows, int32_t H, void* residual_out, void* out, void* codes, float* row_scale,
+                           void* x_codes, float* x_scale, void* h_codes, float* h_scale, float* rstd,
+                           dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_sandwich_norm rows=%lld", (long long)rows);
+    const int32_t rc = check_sandwich(how, x, x_stride, rows, H, 32768);
+    if (rc != DWDP_OK) return rc;
+    if (!codes != !row_scale || !x_codes != !x_scale || !h_codes != !h_scale)
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "codes and their scale go together");
+    if (!how->pre_weight && (out || codes)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "out and codes need pre_weight");
+    if (rows == 0) return DWDP_OK;
+    if (!x || (how->pre_weight && !out) || (!out && !residual_out))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG,
+                    "x must be non-NULL, and out with pre_weight, residual_out without");
+    for (const void* q : {residual, (const void*)residual_out, (const void*)out, (const void*)codes,
+                          (const void*)row_scale, (const void*)x_codes, (const void*)x_scale, (const void*)h_codes,
+                          (const void*)h_scale, (const void*)rstd})
+        if (!aligned16(q)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    SandwichArgs p{};
+    p.x = static_cast<const uint4*>(x);
+    p.x_vecs = x_stride / 8;
+    p.residual = static_cast<const uint4*>(residual);
+    p.post = static_cast<const uint4*>(how->post_weight);
+    p.gate = static_cast<const uint4*>(how->gate);
+    p.row_offsets = how->row_offsets;
+    p.pre = static_cast<const uint4*>(how->pre_weight);
+    p.n_groups = how->n_groups;
+    p.block_scale = how->block_scale;
+    p.residual_scale = how->residual_scale;
+    p.eps = how->eps;
+    p.rows = rows;
+    p.nv = H / 8;
+    p.one_nth = 1.0f / (float)H;
+    p.residual_out = static_cast<uint4*>(residual_out);
+    p.out = static_cast<uint4*>(out);
+    p.codes = static_cast<uint2*>(codes);
+    p.row_scale = row_scale;
+    p.x_codes = static_cast<uint2*>(x_codes);
+    p.x_scale = x_scale;
+    p.h_codes = static_cast<uint2*>(h_codes);
+    p.h_scale = h_scale;
+    p.rstd = reinterpret_cast<float2*>(rstd);
+    const cudaError_t e = launch_sandwich_norm(p, stream);
+    return e == cudaSuccess ? DWDP_OK : cuda_fail(nullptr, e, "dwdp_sandwich_norm");
+}
+
+size_t dwdp_sandwich_grad_workspace_bytes(int64_t rows, int32_t H) {
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || H <= 0 || H % 8 || H > 8192) return 0;
+    return std::max<size_t>(256, sandwich_grad_bytes(rows, H));
+}
+
+int32_t dwdp_sandwich_norm_grad(const dwdp_sandwich* how, const void* x, int64_t x_stride, const float* x_scale,
+                                const void* h, const float* h_scale, const float* rstd, const void* dout,
+                                const void* dresidual_out, int64_t rows, int32_t H, void* dx, void* dresidual,
+                                float* dpost_weight, float* dpre_weight, float* dgate, void* ws, size_t ws_bytes,
+                                dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_sandwich_norm_grad rows=%lld", (long long)rows);
+    const int32_t rc = check_sandwich(how, x, x_stride, rows, H, 8192);
+    if (rc != DWDP_OK) return rc;
+    if ((x_scale && !x) || (h_scale && !h)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "a scale needs its codes");
+    if ((dpost_weight && !how->post_weight) || (dpre_weight && !how->pre_weight) || (dgate && !how->gate))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "the gradient of a weight or gate that is not there");
+    if (!how->pre_weight && (h || dout)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "h and dout need pre_weight");
+    const bool sums = dpost_weight || dpre_weight || dgate;
+    if (rows > 0 && ((how->pre_weight && (!h || !dout)) || (!dout && !dresidual_out) ||
+                     ((how->post_weight || dgate) && !x) || ((how->post_weight || how->pre_weight) && !rstd)))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG,
+                    "x (with post_weight or dgate), h and dout (with pre_weight), rstd (with either) and one of dout "
+                    "and dresidual_out must be non-NULL");
+    if (!dx && !dresidual && !sums) return DWDP_OK;
+    if (rows == 0 && !sums) return DWDP_OK;
+    for (const void* q : {(const void*)x_scale, h, (const void*)h_scale, (const void*)rstd, dout, dresidual_out,
+                          (const void*)dx, (const void*)dresidual, (const void*)dpost_weight, (const void*)dpre_weight,
+                          (const void*)dgate, (const void*)ws})
+        if (!aligned16(q)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    const size_t need = dwdp_sandwich_grad_workspace_bytes(rows, H);
+    if (sums && (!ws || ws_bytes < need))
+        return fail(nullptr, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws ? ws_bytes : 0, need);
+    SandwichGradArgs p{};
+    p.x = x;
+    p.x_vecs = x_stride / 8;
+    p.x_scale = x_scale;
+    p.h = h;
+    p.h_scale = h_scale;
+    p.rstd = reinterpret_cast<const float2*>(rstd);
+    p.dout = static_cast<const uint4*>(dout);
+    p.dres = static_cast<const uint4*>(dresidual_out);
+    p.post = static_cast<const uint4*>(how->post_weight);
+    p.gate = static_cast<const uint4*>(how->gate);
+    p.row_offsets = how->row_offsets;
+    p.pre = static_cast<const uint4*>(how->pre_weight);
+    p.n_groups = how->n_groups;
+    p.block_scale = how->block_scale;
+    p.residual_scale = how->residual_scale;
+    p.rows = rows;
+    p.nv = H / 8;
+    p.one_nth = 1.0f / (float)H;
+    p.dx = static_cast<uint4*>(dx);
+    p.dresidual = static_cast<uint4*>(dresidual);
+    p.dpost = dpost_weight;
+    p.dpre = dpre_weight;
+    p.dgate = dgate;
+    p.partial = static_cast<float*>(ws);
+    const cudaError_t e = launch_sandwich_grad(p, stream);
+    return e == cudaSuccess ? DWDP_OK : cuda_fail(nullptr, e, "dwdp_sandwich_norm_grad");
+}
+
+size_t dwdp_balance_workspace_bytes(int32_t T, int32_t E, int32_t n_seqs) {
+    if (T < 0 || T > (1 << 30) || E < 1 || E > DWDP_MAX_EXPERTS || n_seqs < 1) return 0;
+    return std::max<size_t>(256, balance_bytes(T, E));
+}
+
+// What dwdp_balance_loss and dwdp_route_scored_grad ask of what they share.
+static int32_t check_balance(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, int32_t T,
+                             const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring) {
+    if (!ctx) return fail(nullptr, DWDP_ERR_INVALID_ARG, "ctx is NULL");
+    if (T < 0 || T > ctx->cfg.max_tokens) return fail(ctx, DWDP_ERR_INVALID_ARG, "T=%d outside [0, max_tokens]", T);
+    if (T > (1 << 30)) return fail(ctx, DWDP_ERR_UNSUPPORTED, "at most 2^30 tokens");
+    if (!scoring || (scoring->score != DWDP_SCORE_SOFTMAX && scoring->score != DWDP_SCORE_SIGMOID))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring is NULL, or its score unknown");
+    if (n_seqs < 1 || (!seq_offsets && n_seqs != 1))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "n_seqs >= 1, and 1 without seq_offsets");
+    if (T > 0 && (!logits || !topk_ids))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "logits and topk_ids must be non-NULL");
+    if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(seq_offsets))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    return DWDP_OK;
+}
+
+int32_t dwdp_balance_loss(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, int32_t T,
+                          const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring, int32_t* counts,
+                          float* mean_p, float* balance, float* z, void* ws, size_t ws_bytes, dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_balance_loss T=%d", T);
+    const int32_t rc = check_balance(ctx, logits, topk_ids, T, seq_offsets, n_seqs, scoring);
+    if (rc != DWDP_OK) return rc;
+    if (!counts || !mean_p || !balance)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "counts, mean_p and balance must be non-NULL");
+    if (!aligned16(counts) || !aligned16(mean_p) || !aligned16(balance) || !aligned16(z) || !aligned16(ws))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    const size_t need = dwdp_balance_workspace_bytes(T, ctx->cfg.n_experts, n_seqs);
+    if (!ws || ws_bytes < need)
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "workspace too small (%zu < %zu)", ws ? ws_bytes : 0, need);
+    BalanceArgs p{};
+    p.logits = logits;
+    p.ids = topk_ids;
+    p.offsets = seq_offsets;
+    p.T = T;
+    p.E = ctx->cfg.n_experts;
+    p.k = ctx->cfg.top_k;
+    p.n_seqs = n_seqs;
+    p.sigmoid = scoring->score == DWDP_SCORE_SIGMOID;
+    p.counts = counts;
+    p.mean_p = mean_p;
+    p.balance = balance;
+    p.z = z;
+    p.err = ctx->d_err;
+    DWDP_CUDA(ctx, launch_balance(p, ws, stream));
+    return DWDP_OK;
+}
+
+int32_t dwdp_route_scored_grad(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, const float* dtopk_w,
+                               int32_t T, const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring,
+                               const int32_t* counts, const float* dbalance, const float* dz, void* dlogits,
+                               int32_t dlogits_bf16, dwdp_stream_t stream) {
+    const NvtxRange nvtx("dwdp_route_scored_grad T=%d", T);
+    const int32_t rc = check_balance(ctx, logits, topk_ids, T, seq_offsets, n_seqs, scoring);
+    if (rc != DWDP_OK) return rc;
+    if ((scoring->renormalize != 0 && scoring->renormalize != 1) || !std::isfinite(scoring->scale) ||
+        !(scoring->scale > 0.0f) || (dlogits_bf16 != 0 && dlogits_bf16 != 1))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "scoring: bad renormalize or scale; or dlogits_bf16 is not 0 or 1");
+    if (dbalance && !counts) return fail(ctx, DWDP_ERR_INVALID_ARG, "dbalance needs counts");
+    if (T == 0) return DWDP_OK;
+    if (!dlogits) return fail(ctx, DWDP_ERR_INVALID_ARG, "dlogits must be non-NULL");
+    if (!aligned16(dtopk_w) || !aligned16(counts) || !aligned16(dbalance) || !aligned16(dz) || !aligned16(dlogits))
+        return fail(ctx, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
+    RouterGradArgs p{};
+    p.logits = logits;
+    p.ids = topk_ids;
+    p.dw = dtopk_w;
+    p.offsets = seq_offsets;
+    p.counts = counts;
+    p.dbalance = dbalance;
+    p.dz = dz;
+    p.T = T;
+    p.E = ctx->cfg.n_experts;
+    p.k = ctx->cfg.top_k;
+    p.n_seqs = n_seqs;
+    p.sigmoid = scoring->score == DWDP_SCORE_SIGMOID;
+    p.renorm = scoring->renormalize == 1;
+    p.half = dlogits_bf16 == 1;
+    p.scale = scoring->scale;
+    p.dlogits = dlogits;
+    p.err = ctx->d_err;
+    DWDP_CUDA(ctx, launch_router_grad(p, stream));
+    return DWDP_OK;
+}
+
 size_t dwdp_lora_workspace_bytes(int32_t T, int32_t K, int32_t N, int32_t R) {
     if (T < 0 || T > (1 << 30) || K <= 0 || N <= 0 || K > (1 << 20) || N > (1 << 20) || K % 8 || N % 8 || R <= 0 ||
         R % 8 || R > DWDP_MAX_LORA_RANK)

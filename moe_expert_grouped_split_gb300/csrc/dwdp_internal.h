@@ -3,7 +3,8 @@
 // Kernels live in gemm.cu (split-pointer grouped GEMM, tcgen05 + TMA) and
 // route.cu (top-k, grouping, row scatter into expert order, combine, and the
 // E4M3 / NVFP4 activation quantizers); what surrounds the layer in a decoder
-// block in norm.cu (residual addition + norm), router.cu, router_pair.cu and
+// block in norm.cu (residual addition + norm), sandwich.cu (the norms around a
+// block, with gradients), balance.cu (the router's losses and gradients), router.cu, router_pair.cu and
 // route_scored.cu (scored routing), lora.cu and lora_tc.cu (adapters);
 // dwdp_abi.cu is the C ABI.
 #pragma once
@@ -234,6 +235,99 @@ cudaError_t launch_combine(const void* y, int H, const int32_t* inv, const float
 cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, void* residual_out,
                                const void* weight, float eps, int64_t rows, int H, void* out, void* codes,
                                float* row_scale, cudaStream_t s);
+
+// sandwich.cu: dwdp_sandwich_norm and dwdp_sandwich_norm_grad (arguments as
+// there, checked; the last members of SandwichGradArgs are filled by
+// launch_sandwich_grad).  Rows in vectors of 8 elements.
+struct SandwichArgs {
+    const uint4* x;
+    int64_t x_vecs;  // between x's rows
+    const uint4* residual;
+    const uint4* post;
+    const uint4* gate;
+    const int32_t* row_offsets;
+    const uint4* pre;
+    int n_groups;
+    float block_scale, residual_scale, eps;
+    int64_t rows;
+    int nv;         // vectors a row
+    float one_nth;  // 1 / H
+    uint4* residual_out;
+    uint4* out;
+    uint2* codes;
+    float* row_scale;
+    uint2* x_codes;
+    float* x_scale;
+    uint2* h_codes;
+    float* h_scale;
+    float2* rstd;
+};
+cudaError_t launch_sandwich_norm(const SandwichArgs& p, cudaStream_t s);
+struct SandwichGradArgs {
+    const void* x;  // bf16, or E4M3 codes where x_scale is given; h likewise
+    int64_t x_vecs;
+    const float* x_scale;
+    const void* h;
+    const float* h_scale;
+    const float2* rstd;
+    const uint4* dout;
+    const uint4* dres;
+    const uint4* post;
+    const uint4* gate;
+    const int32_t* row_offsets;
+    const uint4* pre;
+    int n_groups;
+    float block_scale, residual_scale;
+    int64_t rows;
+    int nv;
+    float one_nth;
+    uint4* dx;
+    uint4* dresidual;
+    float* dpost;
+    float* dpre;
+    float* dgate;
+    float* partial;
+    int64_t blocks, chunk;
+};
+size_t sandwich_grad_bytes(int64_t rows, int H);
+cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s);
+
+// balance.cu: dwdp_balance_loss and dwdp_route_scored_grad (arguments as
+// there, checked; the last members of both are filled by the launches).
+struct BalanceArgs {
+    const float* logits;
+    const int32_t* ids;
+    const int32_t* offsets;  // null: one sequence of all tokens
+    int T, E, k, n_seqs;
+    bool sigmoid;
+    int32_t* counts;
+    float* mean_p;
+    float* balance;
+    float* z;
+    int* err;
+    int chunk;  // tokens a block
+    float* part_p;
+    int32_t* part_counts;
+    float* part_z;
+};
+size_t balance_bytes(int64_t T, int E);
+cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s);
+struct RouterGradArgs {
+    const float* logits;
+    const int32_t* ids;
+    const float* dw;
+    const int32_t* offsets;
+    const int32_t* counts;
+    const float* dbalance;
+    const float* dz;
+    int T, E, k, n_seqs;
+    bool sigmoid, renorm, half;
+    float scale;
+    void* dlogits;
+    int* err;
+    int chunk;
+};
+cudaError_t launch_router_grad(RouterGradArgs& p, cudaStream_t s);
 
 // router.cu: z [T][E] = x [T][H] W [E][H]^T in fp32 on warp-level MMAs, for
 // router_is_small sizes.  The kernel also zeroes n_zero ints at `zero` (so

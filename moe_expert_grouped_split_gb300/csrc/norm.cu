@@ -6,13 +6,12 @@
 // outputs need: y = h rs w with rs = 1 / sqrt(mean + eps), max|y| =
 // max|h w| rs, and the code's argument y / (max|y| / 448) = h w (448 /
 // max|h w|), in which rs cancels.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <math_constants.h>
 
 #include <atomic>
 
 #include "dwdp_internal.h"
+#include "row_ops.h"
 
 namespace dwdp {
 namespace {
@@ -30,50 +29,6 @@ constexpr float kMinCodeMax = 0x1p-100f;
 constexpr float kEpsEnough = 0x1p-120f;
 constexpr float kUpScale = 0x1p80f;
 
-// The larger of two, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float rcp(float a) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
-    return r;
-}
-
-__device__ __forceinline__ void unpack8(uint4 q, float (&f)[8]) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = __bfloat1622float2(h[i]);
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    uint4 q;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    return q;
-}
-
-__device__ __forceinline__ void copy16(uint4* to, const uint4* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
-                 : "memory");
-}
-
-// m: magnitudes, whose order as floats is their bits' (a NaN is above +inf).
-template <bool MAX>
-__device__ __forceinline__ void warp_sum_max(float& s, float& m) {
-    if constexpr (MAX) m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-}
-
 // (sum, max) over the block; every thread gets them.
 template <bool MAX>
 __device__ __forceinline__ float2 block_sum_max(float s, float m, float2* red) {
@@ -87,11 +42,6 @@ __device__ __forceinline__ float2 block_sum_max(float s, float m, float2* red) {
     warp_sum_max<MAX>(s, m);
     __syncthreads();  // red may be written again
     return make_float2(s, m);
-}
-
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 struct NormArgs {
@@ -370,21 +320,9 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const __grid_co
     }
 }
 
-// Programmatic dependent launch: the block's start overlaps the end of the
-// kernel before it (0.1 to 0.4 us of a small call).
 template <class K>
 cudaError_t launch(K kernel, const NormArgs& p, int64_t grid, int threads, size_t smem, cudaStream_t s) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)grid);
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, p);
+    return launch_dependent(kernel, p, dim3((unsigned)grid), threads, smem, s);
 }
 
 // SMs of the current device, looked up once per device.
