@@ -233,68 +233,76 @@ __global__ void __launch_bounds__(1024) sandwich_norm_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------ gradients --
+using eight = float[8];  // a vector's elements
 
-__device__ __forceinline__ void values8(uint2 q, float scale, float (&f)[8]) {
-    const uint32_t w[2] = {q.x, q.y};
+// How a row was kept.
+enum Kept : int { KEPT_NOT, KEPT_BF16, KEPT_E4M3 };
+__host__ __device__ constexpr int kept_bytes(int k) { return k == KEPT_E4M3 ? 8 : k == KEPT_BF16 ? 16 : 0; }
+
+// 8 elements of a kept row times `by`.
+template <int K>
+__device__ __forceinline__ void values(const char* at, float by, eight& f) {
+    if constexpr (K == KEPT_E4M3) {
+        const uint2 q = *reinterpret_cast<const uint2*>(at);
+        const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw v =
-            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> ((i & 1) * 16)), __NV_E4M3);
-        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&v));
-        f[2 * i] = t.x * scale;
-        f[2 * i + 1] = t.y * scale;
-    }
-}
-
-// 8 elements of a kept row, bf16 or E4M3 codes, times `by`.
-template <bool K8>
-__device__ __forceinline__ void kept8(const void* base, int vec, float by, float (&f)[8]) {
-    if constexpr (K8) {
-        values8(static_cast<const uint2*>(base)[vec], by, f);
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw v =
+                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> ((i & 1) * 16)), __NV_E4M3);
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&v));
+            f[2 * i] = t.x * by;
+            f[2 * i + 1] = t.y * by;
+        }
     } else {
-        unpack8(static_cast<const uint4*>(base)[vec], f);
+        unpack8(*reinterpret_cast<const uint4*>(at), f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) f[c] *= by;
     }
 }
 
-// Copies 16 bytes (8 for codes) of this thread's into shared memory; nobody
-// else reads them, so nothing is waited for but the thread's own copies.
-template <bool K8>
-__device__ __forceinline__ void fetch8(void* to, const void* base, int64_t vec) {
+// Copies a vector of this thread's into shared memory; nobody else reads it,
+// so nothing is waited for but the thread's own copies.
+template <int K>
+__device__ __forceinline__ void fetch_vec(char* to, const char* from) {
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (K8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(static_cast<const uint2*>(base) + vec)
-                     : "memory");
+    if constexpr (K == KEPT_E4M3)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
     else
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(static_cast<const uint4*>(base) + vec)
-                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
 }
 
-// The block's sum of s, for every thread; `turn` alternates between two
-// buffers, so one barrier a sum is enough.
-__device__ __forceinline__ float block_sum(float s, float (*red)[32], int& turn) {
-    float none = 0.0f;
-    warp_sum_max<false>(s, none);
-    const int nw = blockDim.x >> 5;
-    if (nw == 1) return s;
-    float* r = red[turn];
-    turn ^= 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) r[warp] = s;
-    __syncthreads();
-    s = (lane & 15) < nw ? r[lane & 15] : 0.0f;  // 16 warps at most
+// The block's sums of a, b and c, for every thread.  A warp's three sums
+// together: half of the lanes go on with each value.  `turn` alternates
+// between two buffers, so one barrier is enough.  16 warps at most.
+__device__ __forceinline__ float3 block_sums(float a, float b, float c, float (*red)[64], int& turn) {
+    constexpr uint32_t all = 0xffffffffu;
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const bool upper = lane & 16, odd = lane & 8;
+    float u = (upper ? c : a) + __shfl_xor_sync(all, upper ? a : c, 16);
+    float v = (upper ? 0.0f : b) + __shfl_xor_sync(all, upper ? b : 0.0f, 16);
+    float s = (odd ? v : u) + __shfl_xor_sync(all, odd ? u : v, 8);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(all, s, o);
+    // lanes 8 i .. 8 i + 7: value i
+    if (nw > 1) {
+        float* r = red[turn];
+        turn ^= 1;
+        const int warp = threadIdx.x >> 5, w = lane & 7, i = lane >> 3;
+        if (w == 0) r[warp * 4 + i] = s;
+        __syncthreads();
+        s = (w < nw ? r[w * 4 + i] : 0.0f) + (w + 8 < nw ? r[(w + 8) * 4 + i] : 0.0f);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(all, s, o);
+    }
+    return make_float3(__shfl_sync(all, s, 0), __shfl_sync(all, s, 8), __shfl_sync(all, s, 16));
 }
 
-__device__ __forceinline__ void store8(float* to, const float (&f)[8]) {
+__device__ __forceinline__ void store8(float* to, const eight& f) {
     reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
     reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-__device__ __forceinline__ void load8(const float* from, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(from)[0], b = reinterpret_cast<const float4*>(from)[1];
+__device__ __forceinline__ void load8(const float4* at, int apart, eight& f) {
+    const float4 a = at[0], b = at[apart];
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
@@ -305,76 +313,104 @@ constexpr int kGradStages = 3, kGradVecs = 2;
 // gradients only two sums a column have to be kept while rows go by: dout
 // hhat, and S = dh xhat since the group began, as dgate = c post S and
 // dpost_weight = sum over groups of c gate S.  The rows kGradStages ahead are
-// on their way into shared memory.
+// on their way into shared memory.  One reduction a row: with e = dres + rh gy
+// and q = c gate post xhat,
+//   mean(gn xhat) = mean(q e) - rh mean(gy hhat) mean(q hhat).
 // partial [blocks][4][H]: the sums for pre and post, and S of the group that
 // was begun before the block's rows and of the one that goes on after them
 // (a group whose rows are all here goes to dgate at once).
-template <bool X8, bool H8>
+// X, HK: how x and h were kept (HK KEPT_NOT: no pre norm); POST: a post norm.
+template <int X, int HK, bool POST>
 __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_constant__ SandwichGradArgs p) {
-    constexpr int VPT = kGradVecs;
+    constexpr int VPT = kGradVecs, kX = kept_bytes(X), kH = kept_bytes(HK);
+    constexpr bool PRE = HK != KEPT_NOT;
     extern __shared__ __align__(16) char smem[];
-    __shared__ float red[2][32];
+    __shared__ float red[2][64];
     const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31;
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int64_t lo = (int64_t)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.rows);
     const int H = p.nv * 8;
-    // the stages, each x, h, dout and dres of a row; then c gate post
-    const int x_bytes = X8 ? 8 : 16, h_bytes = H8 ? 8 : 16, stage_bytes = n * VPT * (x_bytes + h_bytes + 32);
+    // a stage: vectors of dout, dres, x and h; behind the stages c gate post
+    const int vecs = n * VPT, stage_bytes = vecs * (kX + kH + 32);
+    char* const own = smem + tid * 16;
+    char* const own_x = smem + vecs * 32 + tid * kX;
+    char* const own_h = smem + vecs * (32 + kX) + tid * kH;
     // (vector j's two halves n 16 bytes apart: no two lanes on one bank)
-    float4* gw = reinterpret_cast<float4*>(smem + kGradStages * stage_bytes) + tid;
-    auto fetch = [&](int64_t row, int stage) {
+    float4* const gw = reinterpret_cast<float4*>(smem + kGradStages * stage_bytes) + tid;
+    const bool held[VPT] = {tid < p.nv, tid + n < p.nv};
+    auto fetch = [&](int64_t row, int at) {
         if (row < hi) {
-            char* at = smem + stage * stage_bytes;
+            const int64_t vec = row * p.nv + tid, x_vec = row * p.x_vecs + tid;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = tid + j * n;
-                if (i >= p.nv) continue;
-                if (p.x) fetch8<X8>(at + i * x_bytes, p.x, row * p.x_vecs + i);
-                if (p.pre) {
-                    fetch8<H8>(at + n * VPT * x_bytes + i * h_bytes, p.h, row * p.nv + i);
-                    fetch8<false>(at + n * VPT * (x_bytes + h_bytes) + i * 16, p.dout, row * p.nv + i);
+                if (!held[j]) continue;
+                if constexpr (X != KEPT_NOT)
+                    fetch_vec<X>(own_x + at + j * n * kX, static_cast<const char*>(p.x) + (x_vec + j * n) * kX);
+                if constexpr (PRE) {
+                    fetch_vec<HK>(own_h + at + j * n * kH, static_cast<const char*>(p.h) + (vec + j * n) * kH);
+                    fetch_vec<KEPT_BF16>(own + at + j * n * 16, reinterpret_cast<const char*>(p.dout + vec + j * n));
                 }
-                if (p.dres) fetch8<false>(at + n * VPT * (x_bytes + h_bytes + 16) + i * 16, p.dres, row * p.nv + i);
+                if (p.dres)
+                    fetch_vec<KEPT_BF16>(own + at + (VPT + j) * n * 16, reinterpret_cast<const char*>(p.dres + vec + j * n));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // what is never fetched is zero, so that the arithmetic need not ask
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (held[j] && p.dres) continue;
+        for (int at = 0; at < kGradStages * stage_bytes; at += stage_bytes) {
+            *reinterpret_cast<uint4*>(own + at + (VPT + j) * n * 16) = zero;
+            if (held[j]) continue;
+            *reinterpret_cast<uint4*>(own + at + j * n * 16) = zero;
+            if (kX == 16) *reinterpret_cast<uint4*>(own_x + at + j * n * kX) = zero;
+            if (kX == 8) *reinterpret_cast<uint2*>(own_x + at + j * n * kX) = make_uint2(0, 0);
+            if (kH == 16) *reinterpret_cast<uint4*>(own_h + at + j * n * kH) = zero;
+            if (kH == 8) *reinterpret_cast<uint2*>(own_h + at + j * n * kH) = make_uint2(0, 0);
+        }
+        if (!held[j]) gw[2 * j * n] = gw[(2 * j + 1) * n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     // what a row has once: 1 / rms of both norms, and what x's and h's values are to be multiplied by
     auto row_factors = [&](int64_t row) {
         if (row >= hi) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const float2 r = p.rstd ? p.rstd[row] : make_float2(1.0f, 1.0f);
-        return make_float4(r.x, r.y, X8 ? p.x_scale[row] * r.x : r.x, H8 ? p.h_scale[row] * r.y : r.y);
+        return make_float4(r.x, r.y, X == KEPT_E4M3 ? p.x_scale[row] * r.x : r.x, HK == KEPT_E4M3 ? p.h_scale[row] * r.y : r.y);
     };
 #pragma unroll
-    for (int s = 0; s < kGradStages; ++s) fetch(lo + s, s);
+    for (int s = 0; s < kGradStages; ++s) fetch(lo + s, s * stage_bytes);
     float4 mine = row_factors(lo + lane), later = row_factors(lo + 32 + lane);  // of 32 rows, a lane each
-    float dpre[VPT][8] = {}, sum[VPT][8] = {};
+    eight dpre[VPT] = {}, sum[VPT] = {};
     uint4 pre[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) pre[j] = p.pre && tid + j * n < p.nv ? __ldg(p.pre + tid + j * n) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < VPT; ++j) pre[j] = PRE && tid + j * n < p.nv ? __ldg(p.pre + tid + j * n) : make_uint4(0, 0, 0, 0);
     float* partial = p.partial + (int64_t)blockIdx.x * 4 * H;
-    int group = 0, stage = 0, turn = 0;
+    const bool to_dx[VPT] = {held[0] && p.dx, held[1] && p.dx};
+    const bool to_dresidual[VPT] = {held[0] && p.dresidual, held[1] && p.dresidual};
+    int group = 0, in = 0, turn = 0;
     int64_t begin = 0, end = p.rows;  // of the group
     bool open = !p.row_offsets, any = false;
-    auto weight_of = [&](const uint4* w, int64_t vec, float (&f)[8]) {
-        if (w) {
-            unpack8(__ldg(w + vec), f);
-        } else {
+    // block_scale times a weight's or gate's elements (1 where there is none)
+    auto scaled = [&](const uint4* w, int64_t vec, eight& f) {
+        if (w) unpack8(__ldg(w + vec), f);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] = 1.0f;
-        }
+        for (int c = 0; c < 8; ++c) f[c] = p.block_scale * (w ? f[c] : 1.0f);
     };
     auto open_group = [&]() {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = tid + j * n;
             if (i >= p.nv) continue;
-            float g[8], w[8];
-            weight_of(p.gate, (int64_t)group * p.nv + i, g);
-            weight_of(p.post, i, w);
+            eight g;
+            scaled(p.gate, (int64_t)group * p.nv + i, g);
+            if constexpr (POST) {
+                eight w;
+                unpack8(__ldg(p.post + i), w);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) g[c] *= p.block_scale * w[c];
+                for (int c = 0; c < 8; ++c) g[c] *= w[c];
+            }
             gw[2 * j * n] = make_float4(g[0], g[1], g[2], g[3]);
             gw[(2 * j + 1) * n] = make_float4(g[4], g[5], g[6], g[7]);
         }
@@ -385,20 +421,21 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
         for (int j = 0; j < VPT; ++j) {
             const int i = tid + j * n;
             if (i >= p.nv) continue;
-            if (p.dpost) {
-                float g[8], before[8] = {};
-                weight_of(p.gate, (int64_t)group * p.nv + i, g);
-                if (any) load8(partial + H + 8 * i, before);
+            if (POST && p.dpost) {
+                eight g, before = {};
+                scaled(p.gate, (int64_t)group * p.nv + i, g);
+                float* to = partial + H + 8 * i;
+                if (any) load8(reinterpret_cast<const float4*>(to), 1, before);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) before[c] = fmaf(p.block_scale * g[c], sum[j][c], before[c]);
-                store8(partial + H + 8 * i, before);
+                for (int c = 0; c < 8; ++c) before[c] = fmaf(g[c], sum[j][c], before[c]);
+                store8(to, before);
             }
             if (p.dgate) {
                 if (whole) {
-                    float w[8];
-                    weight_of(p.post, i, w);
+                    eight w;
+                    scaled(POST ? p.post : nullptr, i, w);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) sum[j][c] *= p.block_scale * w[c];
+                    for (int c = 0; c < 8; ++c) sum[j][c] *= w[c];
                 }
                 store8((whole ? p.dgate + (int64_t)group * H : partial + (begin < lo ? 2 : 3) * H) + 8 * i, sum[j]);
             }
@@ -408,103 +445,102 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
         any = true;
     };
     if (open) open_group();
-    for (int64_t row = lo; row < hi; ++row) {
-        const int at = (int)(row - lo) & 31;
-        if (at == 0 && row != lo) {
+    const int rows = (int)(hi - lo);
+    int change = open ? rows : 0;  // the row at which the group has to be looked up again
+    for (int r = 0; r < rows; ++r) {
+        const int at = r & 31;
+        if (at == 0 && r != 0) {
             mine = later;
-            later = row_factors(row + 32 + lane);
+            later = row_factors(lo + r + 32 + lane);
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 1) : "memory");
-        if (p.row_offsets && (!open || row >= end)) {
+        if (r == change) {
             if (open) close_group();
-            group = group_of(p.row_offsets, p.n_groups, row);
+            group = group_of(p.row_offsets, p.n_groups, lo + r);
             open = group >= 0;
+            change = r + 1;
             if (open) {
                 begin = max(p.row_offsets[group], 0);
                 end = min((int64_t)p.row_offsets[group + 1], p.rows);
+                change = (int)min(max(end - lo, (int64_t)change), (int64_t)rows);
                 open_group();
             }
         }
-        const char* in = smem + stage * stage_bytes;
         if (open) {
             const float rx = __shfl_sync(0xffffffffu, mine.x, at), rh = __shfl_sync(0xffffffffu, mine.y, at);
             const float x_by = __shfl_sync(0xffffffffu, mine.z, at), h_by = __shfl_sync(0xffffffffu, mine.w, at);
-            float gy[VPT][8] = {}, hh[VPT][8] = {};
-            float dot = 0.0f;
-            if (p.pre) {
+            eight e[VPT], hh[VPT], xx[VPT];
+            float by_h = 0.0f, q_e = 0.0f, q_h = 0.0f;  // the sums of gy hhat, q e and q hhat
 #pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int i = tid + j * n;
-                    if (i >= p.nv) continue;
-                    float w[8], dy[8];
-                    kept8<H8>(in + n * VPT * x_bytes, i, h_by, hh[j]);
-                    unpack8(*reinterpret_cast<const uint4*>(in + n * VPT * (x_bytes + h_bytes) + i * 16), dy);
+            for (int j = 0; j < VPT; ++j) {
+                unpack8(*reinterpret_cast<const uint4*>(own + in + (VPT + j) * n * 16), e[j]);
+                if constexpr (PRE) {
+                    eight w, dy;
+                    values<HK>(own_h + in + j * n * kH, h_by, hh[j]);
+                    unpack8(*reinterpret_cast<const uint4*>(own + in + j * n * 16), dy);
                     unpack8(pre[j], w);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         dpre[j][c] = fmaf(dy[c], hh[j][c], dpre[j][c]);
-                        gy[j][c] = dy[c] * w[c];
-                        dot = fmaf(gy[j][c], hh[j][c], dot);
+                        const float gy = dy[c] * w[c];
+                        by_h = fmaf(gy, hh[j][c], by_h);
+                        e[j][c] = fmaf(rh, gy, e[j][c]);
                     }
                 }
-                dot = block_sum(dot, red, turn) * p.one_nth * rh;
+                if constexpr (X != KEPT_NOT) values<X>(own_x + in + j * n * kX, x_by, xx[j]);
+                if constexpr (POST) {
+                    eight w;
+                    load8(gw + 2 * j * n, n, w);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float q = w[c] * xx[j][c];
+                        q_e = fmaf(q, e[j][c], q_e);
+                        if constexpr (PRE) q_h = fmaf(q, hh[j][c], q_h);
+                    }
+                }
             }
-            float xx[VPT][8];
-            float dot2 = 0.0f;
+            float m = 0.0f, m2 = 0.0f;
+            const int64_t vec = (lo + r) * p.nv + tid;
+            if constexpr (PRE || POST) {
+                const float3 sums = block_sums(by_h, q_e, q_h, red, turn);
+                m = rh * sums.x * p.one_nth;
+                m2 = rx * (sums.y - m * sums.z) * p.one_nth;
+            }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = tid + j * n;
-                if (i >= p.nv) continue;
-                float d[8] = {}, w[8];
-                if (p.dres) unpack8(*reinterpret_cast<const uint4*>(in + n * VPT * (x_bytes + h_bytes + 16) + i * 16), d);
-                if (p.pre) {
+                eight t;
+                if constexpr (PRE) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) d[c] = fmaf(rh, gy[j][c], fmaf(-dot, hh[j][c], d[c]));
+                    for (int c = 0; c < 8; ++c) e[j][c] = fmaf(-m, hh[j][c], e[j][c]);
                 }
-                if (p.dresidual) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) w[c] = p.residual_scale * d[c];
-                    p.dresidual[row * p.nv + i] = pack8(w);
+                for (int c = 0; c < 8; ++c) t[c] = p.residual_scale * e[j][c];
+                if (to_dresidual[j]) p.dresidual[vec + j * n] = pack8(t);
+                if constexpr (X != KEPT_NOT) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) sum[j][c] = fmaf(e[j][c], xx[j][c], sum[j][c]);
                 }
-                {
-                    const float4 a = gw[2 * j * n], b = gw[(2 * j + 1) * n];
-                    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-                }
-                if (p.x) kept8<X8>(in, i, x_by, xx[j]);
+                load8(gw + 2 * j * n, n, t);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    gy[j][c] = d[c] * w[c];
-                    if (p.x) {
-                        sum[j][c] = fmaf(d[c], xx[j][c], sum[j][c]);
-                        dot2 = fmaf(gy[j][c], xx[j][c], dot2);
-                    }
+                    t[c] *= e[j][c];
+                    if constexpr (POST) t[c] = fmaf(rx, t[c], -m2 * xx[j][c]);
                 }
-            }
-            if (p.post) dot2 = block_sum(dot2, red, turn) * p.one_nth * rx;
-            if (p.dx) {
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int i = tid + j * n;
-                    if (i >= p.nv) continue;
-                    if (p.post) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) gy[j][c] = fmaf(rx, gy[j][c], -dot2 * xx[j][c]);
-                    }
-                    p.dx[row * p.nv + i] = pack8(gy[j]);
-                }
+                if (to_dx[j]) p.dx[vec + j * n] = pack8(t);
             }
         }
-        fetch(row + kGradStages, stage);
-        if (++stage == kGradStages) stage = 0;
+        fetch(lo + r + kGradStages, in);
+        in += stage_bytes;
+        if (in == kGradStages * stage_bytes) in = 0;
     }
     if (open) close_group();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = tid + j * n;
         if (i >= p.nv) continue;
-        const float none[8] = {};
-        if (p.dpre) store8(partial + 8 * i, dpre[j]);
-        if (p.dpost && !any) store8(partial + H + 8 * i, none);
+        const eight none = {};
+        if (PRE && p.dpre) store8(partial + 8 * i, dpre[j]);
+        if (POST && p.dpost && !any) store8(partial + H + 8 * i, none);
     }
 }
 
@@ -572,15 +608,21 @@ int64_t grad_blocks(int64_t rows, int nv, size_t smem) {
     return std::max<int64_t>(1, std::min(rows, most));
 }
 
-template <bool X8, bool H8>
+template <int X, int HK, bool POST>
 cudaError_t launch_grad(const SandwichGradArgs& p, cudaStream_t s) {
-    const auto kernel = sandwich_grad_kernel<X8, H8>;
+    const auto kernel = sandwich_grad_kernel<X, HK, POST>;
     // the kernel's limit, not this call's size (norm.cu)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)grad_smem(1024, X8 ? 8 : 16, H8 ? 8 : 16));
+                                               (int)grad_smem(1024, kept_bytes(X), kept_bytes(HK)));
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, p, dim3((unsigned)p.blocks), grad_threads(p.nv),
-                            grad_smem(p.nv, X8 ? 8 : 16, H8 ? 8 : 16), s);
+                            grad_smem(p.nv, kept_bytes(X), kept_bytes(HK)), s);
+}
+template <int X, bool POST>
+cudaError_t launch_grad(const SandwichGradArgs& p, int h, cudaStream_t s) {
+    return h == KEPT_NOT    ? launch_grad<X, KEPT_NOT, POST>(p, s)
+           : h == KEPT_BF16 ? launch_grad<X, KEPT_BF16, POST>(p, s)
+                            : launch_grad<X, KEPT_E4M3, POST>(p, s);
 }
 
 }  // namespace
@@ -596,13 +638,23 @@ cudaError_t launch_sandwich_norm(const SandwichArgs& p, cudaStream_t s) {
 size_t sandwich_grad_bytes(int64_t rows, int H) { return (size_t)grad_blocks(rows, H / 8, 0) * 4 * H * sizeof(float); }
 
 cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s) {
-    const int H = p.nv * 8;
-    const bool x8 = p.x_scale != nullptr, h8 = p.h_scale != nullptr;
-    p.blocks = grad_blocks(p.rows, p.nv, grad_smem(p.nv, x8 ? 8 : 16, h8 ? 8 : 16));
-    p.chunk = std::max<int64_t>(1, (p.rows + p.blocks - 1) / p.blocks);
-    p.blocks = std::max<int64_t>(1, (p.rows + p.chunk - 1) / p.chunk);  // none without rows, but for one
-    const cudaError_t e = x8 ? (h8 ? launch_grad<true, true>(p, s) : launch_grad<true, false>(p, s))
-                             : (h8 ? launch_grad<false, true>(p, s) : launch_grad<false, false>(p, s));
+    const int H = p.nv * 8, x = !p.x ? KEPT_NOT : p.x_scale ? KEPT_E4M3 : KEPT_BF16,
+              h = !p.pre ? KEPT_NOT : p.h_scale ? KEPT_E4M3 : KEPT_BF16;
+    if (p.rows == 0) {
+        const size_t row = H * sizeof(float);
+        cudaError_t e = cudaSuccess;
+        if (p.dpre) e = cudaMemsetAsync(p.dpre, 0, row, s);
+        if (p.dpost && e == cudaSuccess) e = cudaMemsetAsync(p.dpost, 0, row, s);
+        if (p.dgate && e == cudaSuccess) e = cudaMemsetAsync(p.dgate, 0, row * p.n_groups, s);
+        return e;
+    }
+    p.blocks = grad_blocks(p.rows, p.nv, grad_smem(p.nv, kept_bytes(x), kept_bytes(h)));
+    p.chunk = (p.rows + p.blocks - 1) / p.blocks;
+    p.blocks = (p.rows + p.chunk - 1) / p.chunk;
+    const cudaError_t e = x == KEPT_NOT ? launch_grad<KEPT_NOT, false>(p, h, s)
+                          : x == KEPT_BF16
+                              ? (p.post ? launch_grad<KEPT_BF16, true>(p, h, s) : launch_grad<KEPT_BF16, false>(p, h, s))
+                              : (p.post ? launch_grad<KEPT_E4M3, true>(p, h, s) : launch_grad<KEPT_E4M3, false>(p, h, s));
     if (e != cudaSuccess || (!p.dpre && !p.dpost && !p.dgate)) return e;
     const dim3 grid((unsigned)((H + 31) / 32), (unsigned)(2 + (p.dgate ? p.n_groups : 0)));
     return launch_dependent(sandwich_sums_kernel, p, grid, 256, 0, s);
