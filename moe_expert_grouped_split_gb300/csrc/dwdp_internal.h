@@ -237,8 +237,7 @@ cudaError_t launch_add_rmsnorm(const void* x, int64_t x_stride, const void* resi
                                float* row_scale, cudaStream_t s);
 
 // sandwich.cu: dwdp_sandwich_norm and dwdp_sandwich_norm_grad (arguments as
-// there, checked; the last members of SandwichGradArgs are filled by
-// launch_sandwich_grad).  Rows in vectors of 8 elements.
+// there, checked; the last members are filled by the launches).  Rows in vectors of 8 elements.
 struct SandwichArgs {
     const uint4* x;
     int64_t x_vecs;  // between x's rows
@@ -261,8 +260,9 @@ struct SandwichArgs {
     uint2* h_codes;
     float* h_scale;
     float2* rstd;
+    int64_t chunk;
 };
-cudaError_t launch_sandwich_norm(const SandwichArgs& p, cudaStream_t s);
+cudaError_t launch_sandwich_norm(SandwichArgs& p, cudaStream_t s);
 struct SandwichGradArgs {
     const void* x;  // bf16, or E4M3 codes where x_scale is given; h likewise
     int64_t x_vecs;

@@ -42,25 +42,28 @@ __device__ __forceinline__ int group_of(const int32_t* offsets, int n_groups, in
     return lo < n_groups ? lo : -1;
 }
 
-// (sum, max, max) over the block; every thread gets them.
-__device__ __forceinline__ float3 block_sum_max2(float s, float a, float b, float4* red) {
+// (sum, max, max) over the block; every thread gets them.  `turn` alternates
+// between two buffers, so one barrier is enough.
+__device__ __forceinline__ float3 block_sum_max2(float s, float a, float b, float4 (*red)[32], int& turn) {
     warp_sum_max<false>(s, a);
     a = warp_max(a);
     b = warp_max(b);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0) red[warp] = make_float4(s, a, b, 0.0f);
+    const int nw = blockDim.x >> 5;
+    if (nw == 1) return make_float3(s, a, b);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float4* r = red[turn];
+    turn ^= 1;
+    if (lane == 0) r[warp] = make_float4(s, a, b, 0.0f);
     __syncthreads();
-    const float4 v = lane < nw ? red[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 v = lane < nw ? r[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     s = v.x;
-    a = v.y;
     warp_sum_max<false>(s, a);
-    a = warp_max(a);
-    b = warp_max(v.z);
-    __syncthreads();  // red may be written again
-    return make_float3(s, a, b);
+    return make_float3(s, warp_max(v.y), warp_max(v.z));
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+using eight = float[8];  // a vector's elements
+
+__device__ __forceinline__ uint2 codes8(const eight& v, float inv) {
     uint32_t q[2] = {0u, 0u};
 #pragma unroll
     for (int c = 0; c < 8; c += 2) {
@@ -81,26 +84,167 @@ __device__ __forceinline__ float code_factor(float m, float& scale) {
     return 448.0f * rcp(m);
 }
 
-// One block per row; thread i holds the row's 16-byte vectors i, i + blockDim.x,
-// ... (VPT of them at most).
-template <int VPT>
-__global__ void __launch_bounds__(1024) sandwich_norm_kernel(const __grid_constant__ SandwichArgs p) {
-    __shared__ float4 red[32];
+// Copies a vector of this thread's into shared memory; nobody else reads it,
+// so nothing is waited for but the thread's own copies.
+template <int BYTES>
+__device__ __forceinline__ void fetch_vec(char* to, const void* from) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void load8(const float4* at, int apart, eight& f) {
+    const float4 a = at[0], b = at[apart];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// What is asked of a forward call (the rest are pointers that may be null).
+template <bool POST_, bool PRE_, bool CODES_, bool KEPT_>
+struct Asked {
+    static constexpr bool POST = POST_, PRE = PRE_, CODES = CODES_, KEPT = KEPT_;
+};
+
+// c gate post of a vector's elements.
+__device__ __forceinline__ void block_factor(const SandwichArgs& p, const uint4* gate, const uint4* post, int i, eight& f) {
+    eight w;
+    if (gate) unpack8(__ldg(gate + i), f);
+    if (post) unpack8(__ldg(post + i), w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] = p.block_scale * (gate ? f[c] : 1.0f) * (post ? w[c] : 1.0f);
+}
+
+// One row of which the thread has VPT vectors: x and the residual (zeros where
+// there is nothing), factor(j, f) = c gate post and pre.  vec: the first
+// one's place among all vectors, the others n on each; held[j]: to be stored.
+template <class ASK, int VPT, class Factor>
+__device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row, int64_t vec, int n, const bool (&held)[VPT],
+                                             const uint4 (&x)[VPT], const uint4 (&r)[VPT], const uint4 (&pre)[VPT],
+                                             Factor factor, float4 (*red)[32], int& turn) {
+    float rx = 1.0f, x_inv = 0.0f;
+    const bool first = threadIdx.x == 0;
+    if constexpr (ASK::POST || ASK::KEPT) {
+        float ss = 0.0f, ax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            eight f;
+            unpack8(x[j], f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if constexpr (ASK::POST) ss = fmaf(f[c], f[c], ss);
+                if constexpr (ASK::KEPT) ax = max_nan(ax, fabsf(f[c]));
+            }
+        }
+        float3 sums = block_sum_max2(ss, ax, 0.0f, red, turn);
+        if constexpr (ASK::POST) {
+            float scaled = 1.0f;
+            if (!(sums.x < kSquaresLimit)) {  // rare; the whole block agrees
+                scaled = kDownScale;
+                ss = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    eight f;
+                    unpack8(x[j], f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) ss = fmaf(f[c] * scaled, f[c] * scaled, ss);
+                }
+                sums.x = block_sum_max2(ss, 0.0f, 0.0f, red, turn).x;
+            }
+            rx = rsqrtf(fmaf(sums.x, p.one_nth, p.eps * scaled * scaled)) * scaled;
+        }
+        if constexpr (ASK::KEPT) {
+            float scale;
+            x_inv = code_factor(sums.y, scale);
+            if (first && p.x_scale) p.x_scale[row] = scale;
+        }
+    }
+    eight h[VPT];
+    float ss = 0.0f, ah = 0.0f, ay = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        eight f, w;
+        unpack8(x[j], f);
+        if (ASK::KEPT && p.x_codes && held[j]) p.x_codes[vec + j * n] = codes8(f, x_inv);
+        factor(j, w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] *= ASK::POST ? rx * w[c] : w[c];
+        unpack8(r[j], w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            h[j][c] = fmaf(p.residual_scale, w[c], f[c]);
+            if constexpr (ASK::PRE) ss = fmaf(h[j][c], h[j][c], ss);
+            if constexpr (ASK::KEPT) ah = max_nan(ah, fabsf(h[j][c]));
+        }
+        if constexpr (ASK::CODES) {
+            unpack8(pre[j], w);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) ay = max_nan(ay, fabsf(h[j][c] * w[c]));
+        }
+        if (p.residual_out && held[j]) p.residual_out[vec + j * n] = pack8(h[j]);
+    }
+    float rh = 1.0f, h_inv = 0.0f, y_inv = 0.0f;
+    if constexpr (ASK::PRE || ASK::KEPT) {
+        float3 sums = block_sum_max2(ss, ah, ay, red, turn);
+        if constexpr (ASK::PRE) {
+            float scaled = 1.0f;
+            if (!(sums.x < kSquaresLimit)) {
+                scaled = kDownScale;
+                ss = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) ss = fmaf(h[j][c] * scaled, h[j][c] * scaled, ss);
+                sums.x = block_sum_max2(ss, 0.0f, 0.0f, red, turn).x;
+            }
+            rh = rsqrtf(fmaf(sums.x, p.one_nth, p.eps * scaled * scaled)) * scaled;
+        }
+        if constexpr (ASK::KEPT) {
+            float scale;
+            h_inv = code_factor(sums.y, scale);
+            if (first && p.h_scale) p.h_scale[row] = scale;
+        }
+        if constexpr (ASK::CODES) {
+            float scale;
+            y_inv = code_factor(sums.z, scale);
+            if (first) p.row_scale[row] = sums.z == 0.0f ? 1.0f : scale * rh;
+        }
+    }
+    if (first && p.rstd) p.rstd[row] = make_float2(rx, rh);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (ASK::KEPT && p.h_codes && held[j]) p.h_codes[vec + j * n] = codes8(h[j], h_inv);
+        if constexpr (ASK::PRE) {
+            eight w, y;
+            unpack8(pre[j], w);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                w[c] *= h[j][c];
+                y[c] = w[c] * rh;
+            }
+            if (held[j]) p.out[vec + j * n] = pack8(y);
+            if (ASK::CODES && held[j]) p.codes[vec + j * n] = codes8(w, y_inv);
+        }
+    }
+}
+
+// One block per row; thread i holds the row's vectors i, i + blockDim.x, ...
+template <class ASK, int VPT>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 1024) sandwich_norm_kernel(const __grid_constant__ SandwichArgs p) {
+    __shared__ float4 red[2][32];
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int64_t row = blockIdx.x;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 x[VPT], r[VPT], post[VPT];
-    int held = 0;
+    uint4 x[VPT], r[VPT], pre[VPT];
+    bool held[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = threadIdx.x + j * blockDim.x;
-        if (i < p.nv) {
-            x[j] = p.x[row * p.x_vecs + i];
-            r[j] = p.residual ? p.residual[row * p.nv + i] : zero;
-            post[j] = p.post ? __ldg(p.post + i) : zero;
-            held = j + 1;
-        }
+        held[j] = i < p.nv;
+        x[j] = held[j] ? p.x[row * p.x_vecs + i] : zero;
+        r[j] = held[j] && p.residual ? p.residual[row * p.nv + i] : zero;
+        pre[j] = ASK::PRE && held[j] ? __ldg(p.pre + i) : zero;
     }
     const uint4* gate = p.gate;
     if (p.row_offsets) {
@@ -108,133 +252,102 @@ __global__ void __launch_bounds__(1024) sandwich_norm_kernel(const __grid_consta
         if (g < 0) return;  // the whole block
         gate += (int64_t)g * p.nv;
     }
-    float rx = 1.0f;
-    const bool keep_x = p.x_codes != nullptr;
-    if (p.post || keep_x) {
-        float ss = 0.0f, ax = 0.0f;
+    auto factor = [&](int j, eight& f) {
+        if (held[j]) {
+            block_factor(p, gate, ASK::POST ? p.post : nullptr, threadIdx.x + j * blockDim.x, f);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) f[c] = 0.0f;
+        }
+    };
+    int turn = 0;
+    sandwich_row<ASK, VPT>(p, row, row * p.nv + threadIdx.x, blockDim.x, held, x, r, pre, factor, red, turn);
+}
+
+// Many rows: a block stays and takes rows [blockIdx.x chunk, + chunk) in order.
+// The rows STAGES - 1 ahead are on their way into shared memory, where c gate
+// post of the group lies too; what is never fetched is zero there.
+constexpr int kNormVecs = 2, kNormStayRows = 8;
+template <class ASK, int STAGES>
+__global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_constant__ SandwichArgs p) {
+    constexpr int VPT = kNormVecs;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float4 red[2][32];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int tid = threadIdx.x, n = blockDim.x;
+    const int64_t lo = (int64_t)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.rows);
+    const bool held[VPT] = {tid < p.nv, tid + n < p.nv};
+    const int stage_bytes = 2 * VPT * n * 16;
+    char* const own = smem + tid * 16;
+    float4* const factors = reinterpret_cast<float4*>(smem + STAGES * stage_bytes) + tid;
+    auto fetch = [&](int64_t row, int at) {
+        if (row < hi) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (!held[j]) continue;
+                fetch_vec<16>(own + at + j * n * 16, p.x + row * p.x_vecs + tid + j * n);
+                if (p.residual) fetch_vec<16>(own + at + (VPT + j) * n * 16, p.residual + row * p.nv + tid + j * n);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint4 pre[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        pre[j] = ASK::PRE && held[j] ? __ldg(p.pre + tid + j * n) : zero;
+        if (held[j] && p.residual) continue;
+        for (int at = 0; at < STAGES * stage_bytes; at += stage_bytes) {
+            *reinterpret_cast<uint4*>(own + at + (VPT + j) * n * 16) = zero;
+            if (!held[j]) *reinterpret_cast<uint4*>(own + at + j * n * 16) = zero;
+        }
+        if (!held[j]) factors[2 * j * n] = factors[(2 * j + 1) * n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) fetch(lo + s, s * stage_bytes);
+    auto open_group = [&](int group) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (j >= held) continue;
-            float f[8];
-            unpack8(x[j], f);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                ss = fmaf(f[c], f[c], ss);
-                ax = max_nan(ax, fabsf(f[c]));
+            if (!held[j]) continue;
+            eight f;
+            block_factor(p, p.gate ? p.gate + (int64_t)group * p.nv : nullptr, ASK::POST ? p.post : nullptr, tid + j * n, f);
+            factors[2 * j * n] = make_float4(f[0], f[1], f[2], f[3]);
+            factors[(2 * j + 1) * n] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    };
+    bool open = !p.row_offsets;
+    if (open) open_group(0);
+    const int rows = (int)(hi - lo);
+    int change = open ? rows : 0, in = 0, turn = 0;
+    for (int i = 0; i < rows; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        if (i == change) {
+            const int group = group_of(p.row_offsets, p.n_groups, lo + i);
+            open = group >= 0;
+            change = i + 1;
+            if (open) {
+                change = (int)min(max((int64_t)p.row_offsets[group + 1] - lo, (int64_t)change), (int64_t)rows);
+                open_group(group);
             }
         }
-        float3 sums = block_sum_max2(ss, ax, 0.0f, red);
-        float scaled = 1.0f;
-        if (p.post && !(sums.x < kSquaresLimit)) {  // rare; the whole block agrees
-            scaled = kDownScale;
-            ss = 0.0f;
+        uint4 x[VPT], r[VPT];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (j >= held) continue;
-                float f[8];
-                unpack8(x[j], f);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) ss = fmaf(f[c] * scaled, f[c] * scaled, ss);
-            }
-            sums.x = block_sum_max2(ss, 0.0f, 0.0f, red).x;
+        for (int j = 0; j < VPT; ++j) {
+            x[j] = *reinterpret_cast<const uint4*>(own + in + j * n * 16);
+            r[j] = *reinterpret_cast<const uint4*>(own + in + (VPT + j) * n * 16);
         }
-        if (p.post) rx = rsqrtf(fmaf(sums.x, p.one_nth, p.eps * scaled * scaled)) * scaled;
-        if (keep_x) {
-            float scale;
-            const float inv = code_factor(sums.y, scale);
-            if (threadIdx.x == 0) p.x_scale[row] = scale;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (j >= held) continue;
-                float f[8];
-                unpack8(x[j], f);
-                p.x_codes[row * p.nv + threadIdx.x + j * blockDim.x] = codes8(f, inv);
-            }
-        }
-    }
-    float h[VPT][8];
-    uint4 pre[VPT];
-    float ss = 0.0f, ah = 0.0f, ay = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        if (j >= held) continue;
-        const int i = threadIdx.x + j * blockDim.x;
-        float f[8], w[8];
-        unpack8(x[j], f);
-        if (p.post) {
-            unpack8(post[j], w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] = f[c] * rx * w[c];
-        }
-        if (gate) {
-            unpack8(__ldg(gate + i), w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] *= w[c];
-        }
-        unpack8(r[j], w);
-        pre[j] = p.pre ? __ldg(p.pre + i) : zero;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            h[j][c] = fmaf(p.block_scale, f[c], p.residual_scale * w[c]);
-            ss = fmaf(h[j][c], h[j][c], ss);
-            ah = max_nan(ah, fabsf(h[j][c]));
-        }
-        unpack8(pre[j], w);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) ay = max_nan(ay, fabsf(h[j][c] * w[c]));
-        if (p.residual_out) p.residual_out[row * p.nv + i] = pack8(h[j]);
-    }
-    if (!p.pre && !p.h_codes) {
-        if (p.rstd && threadIdx.x == 0) p.rstd[row] = make_float2(rx, 1.0f);
-        return;
-    }
-    float3 sums = block_sum_max2(ss, ah, ay, red);
-    float rh = 1.0f;
-    if (p.pre) {
-        float scaled = 1.0f;
-        if (!(sums.x < kSquaresLimit)) {
-            scaled = kDownScale;
-            ss = 0.0f;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (j >= held) continue;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) ss = fmaf(h[j][c] * scaled, h[j][c] * scaled, ss);
-            }
-            sums.x = block_sum_max2(ss, 0.0f, 0.0f, red).x;
-        }
-        rh = rsqrtf(fmaf(sums.x, p.one_nth, p.eps * scaled * scaled)) * scaled;
-    }
-    if (p.rstd && threadIdx.x == 0) p.rstd[row] = make_float2(rx, rh);
-    float h_scale, y_scale;
-    const float h_inv = code_factor(sums.y, h_scale), y_inv = code_factor(sums.z, y_scale);
-    if (threadIdx.x == 0) {
-        if (p.h_codes) p.h_scale[row] = h_scale;
-        if (p.codes) p.row_scale[row] = sums.z == 0.0f ? 1.0f : y_scale * rh;
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        if (j >= held) continue;
-        const int64_t at = row * p.nv + threadIdx.x + j * blockDim.x;
-        if (p.h_codes) p.h_codes[at] = codes8(h[j], h_inv);
-        if (p.pre) {
-            float w[8], y[8];
-            unpack8(pre[j], w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) y[c] = h[j][c] * rh * w[c];
-            p.out[at] = pack8(y);
-            if (p.codes) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) y[c] = h[j][c] * w[c];
-                p.codes[at] = codes8(y, y_inv);
-            }
-        }
+        fetch(lo + i + STAGES, in);
+        in += stage_bytes;
+        if (in == STAGES * stage_bytes) in = 0;
+        if (open)
+            sandwich_row<ASK, VPT>(
+                p, lo + i, (lo + i) * p.nv + tid, n, held, x, r, pre, [&](int j, eight& f) { load8(factors + 2 * j * n, n, f); }, red,
+                turn);
     }
 }
 
 // ------------------------------------------------------------ gradients --
-using eight = float[8];  // a vector's elements
-
 // How a row was kept.
 enum Kept : int { KEPT_NOT, KEPT_BF16, KEPT_E4M3 };
 __host__ __device__ constexpr int kept_bytes(int k) { return k == KEPT_E4M3 ? 8 : k == KEPT_BF16 ? 16 : 0; }
@@ -258,17 +371,6 @@ __device__ __forceinline__ void values(const char* at, float by, eight& f) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) f[c] *= by;
     }
-}
-
-// Copies a vector of this thread's into shared memory; nobody else reads it,
-// so nothing is waited for but the thread's own copies.
-template <int K>
-__device__ __forceinline__ void fetch_vec(char* to, const char* from) {
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (K == KEPT_E4M3)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
 }
 
 // The block's sums of a, b and c, for every thread.  A warp's three sums
@@ -301,11 +403,6 @@ __device__ __forceinline__ void store8(float* to, const eight& f) {
     reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
     reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-__device__ __forceinline__ void load8(const float4* at, int apart, eight& f) {
-    const float4 a = at[0], b = at[apart];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-
 constexpr int kGradStages = 3, kGradVecs = 2;
 
 // A block takes rows [blockIdx.x chunk, + chunk) in order; thread i holds the
@@ -346,13 +443,13 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
             for (int j = 0; j < VPT; ++j) {
                 if (!held[j]) continue;
                 if constexpr (X != KEPT_NOT)
-                    fetch_vec<X>(own_x + at + j * n * kX, static_cast<const char*>(p.x) + (x_vec + j * n) * kX);
+                    fetch_vec<kX>(own_x + at + j * n * kX, static_cast<const char*>(p.x) + (x_vec + j * n) * kX);
                 if constexpr (PRE) {
-                    fetch_vec<HK>(own_h + at + j * n * kH, static_cast<const char*>(p.h) + (vec + j * n) * kH);
-                    fetch_vec<KEPT_BF16>(own + at + j * n * 16, reinterpret_cast<const char*>(p.dout + vec + j * n));
+                    fetch_vec<kH>(own_h + at + j * n * kH, static_cast<const char*>(p.h) + (vec + j * n) * kH);
+                    fetch_vec<16>(own + at + j * n * 16, p.dout + vec + j * n);
                 }
                 if (p.dres)
-                    fetch_vec<KEPT_BF16>(own + at + (VPT + j) * n * 16, reinterpret_cast<const char*>(p.dres + vec + j * n));
+                    fetch_vec<16>(own + at + (VPT + j) * n * 16, p.dres + vec + j * n);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -625,14 +722,40 @@ cudaError_t launch_grad(const SandwichGradArgs& p, int h, cudaStream_t s) {
                             : launch_grad<X, KEPT_E4M3, POST>(p, s);
 }
 
+template <class ASK>
+cudaError_t launch_norm(SandwichArgs& p, cudaStream_t s) {
+    const int nv = p.nv;
+    // Staying blocks, two an SM, from a few rows each on.
+    if (nv <= 1024 && p.rows >= 152 * kNormStayRows) {
+        const int threads = ((nv + kNormVecs - 1) / kNormVecs + 31) / 32 * 32;
+        auto bytes = [&](int stages) { return (size_t)threads * kNormVecs * (stages * 32 + 32); };
+        const int stages = bytes(3) <= (228 << 10) / 2 - 2048 ? 3 : 2;
+        const int64_t most = 152 * std::min<int64_t>(1024 / threads, (228 << 10) / (bytes(stages) + 2048));
+        p.chunk = (p.rows + most - 1) / most;
+        const dim3 grid((unsigned)((p.rows + p.chunk - 1) / p.chunk));
+        const auto kernel = stages == 3 ? sandwich_stream_kernel<ASK, 3> : sandwich_stream_kernel<ASK, 2>;
+        // the kernel's limit, not this call's size (norm.cu)
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (228 << 10) / 2 - 2048);
+        return e != cudaSuccess ? e : launch_dependent(kernel, p, grid, threads, bytes(stages), s);
+    }
+    const dim3 grid((unsigned)p.rows);
+    if (nv <= 1024) return launch_dependent(sandwich_norm_kernel<ASK, 1>, p, grid, (nv + 31) / 32 * 32, 0, s);
+    return launch_dependent(sandwich_norm_kernel<ASK, 4>, p, grid, ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
+}
+
+template <bool POST, bool KEPT>
+cudaError_t launch_norm(SandwichArgs& p, cudaStream_t s) {
+    if (!p.pre) return launch_norm<Asked<POST, false, false, KEPT>>(p, s);
+    return p.codes ? launch_norm<Asked<POST, true, true, KEPT>>(p, s) : launch_norm<Asked<POST, true, false, KEPT>>(p, s);
+}
+
 }  // namespace
 
-cudaError_t launch_sandwich_norm(const SandwichArgs& p, cudaStream_t s) {
+cudaError_t launch_sandwich_norm(SandwichArgs& p, cudaStream_t s) {
     if (p.rows <= 0) return cudaSuccess;
-    const int nv = p.nv;
-    if (nv <= 1024)
-        return launch_dependent(sandwich_norm_kernel<1>, p, dim3((unsigned)p.rows), (nv + 31) / 32 * 32, 0, s);
-    return launch_dependent(sandwich_norm_kernel<4>, p, dim3((unsigned)p.rows), ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
+    const bool kept = p.x_codes || p.h_codes;
+    if (p.post) return kept ? launch_norm<true, true>(p, s) : launch_norm<true, false>(p, s);
+    return kept ? launch_norm<false, true>(p, s) : launch_norm<false, false>(p, s);
 }
 
 size_t sandwich_grad_bytes(int64_t rows, int H) { return (size_t)grad_blocks(rows, H / 8, 0) * 4 * H * sizeof(float); }
