@@ -663,8 +663,8 @@ int32_t dwdp_sandwich_norm(const dwdp_sandwich* how, const void* x, int64_t x_st
  * rows).  Each output may be NULL.  x may be NULL without post_weight and
  * dgate, and h without pre_weight, which also has no dout.  x_stride (in
  * elements) holds for x's codes too; h is dense.  dresidual may be
- * dresidual_out and dx may be dout; no other overlap.  H at most 8192, the
- * rest as for dwdp_sandwich_norm.  ws: dwdp_sandwich_grad_workspace_bytes(rows,
+ * dresidual_out and dx may be dout; no other overlap.  The rest as for
+ * dwdp_sandwich_norm.  ws: dwdp_sandwich_grad_workspace_bytes(rows,
  * H) bytes (device), needed for the sums only.  Errors: INVALID_ARG,
  * UNSUPPORTED, CUDA. */
 int32_t dwdp_sandwich_norm_grad(const dwdp_sandwich* how, const void* x, int64_t x_stride, const float* x_scale,

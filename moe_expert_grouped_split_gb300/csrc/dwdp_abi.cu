@@ -958,12 +958,11 @@ int32_t dwdp_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, 
 }
 
 // What both directions of the sandwich norm ask of their common part.
-static int32_t check_sandwich(const dwdp_sandwich* how, const void* x, int64_t x_stride, int64_t rows, int32_t H,
-                              int32_t most_H) {
+static int32_t check_sandwich(const dwdp_sandwich* how, const void* x, int64_t x_stride, int64_t rows, int32_t H) {
     if (!how) return fail(nullptr, DWDP_ERR_INVALID_ARG, "how is NULL");
     if (rows < 0 || rows >= ((int64_t)1 << 31)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "rows outside [0, 2^31)");
-    if (H <= 0 || H % 8 || H > most_H)
-        return fail(nullptr, DWDP_ERR_UNSUPPORTED, "H must be a multiple of 8 in 8..%d", most_H);
+    if (H <= 0 || H % 8 || H > 32768)
+        return fail(nullptr, DWDP_ERR_UNSUPPORTED, "H must be a multiple of 8 in 8..32768");
     if (x && (x_stride < H || x_stride % 8))
         return fail(nullptr, DWDP_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least H");
     if (!std::isfinite(how->block_scale) || !std::isfinite(how->residual_scale))
@@ -986,7 +985,7 @@ int32_t dwdp_sandwich_norm(const dwdp_sandwich* how, const void* x, int64_t x_st
                            void* x_codes, float* x_scale, void* h_codes, float* h_scale, float* rstd,
                            dwdp_stream_t stream) {
     const NvtxRange nvtx("dwdp_sandwich_norm rows=%lld", (long long)rows);
-    const int32_t rc = check_sandwich(how, x, x_stride, rows, H, 32768);
+    const int32_t rc = check_sandwich(how, x, x_stride, rows, H);
     if (rc != DWDP_OK) return rc;
     if (!codes != !row_scale || !x_codes != !x_scale || !h_codes != !h_scale)
         return fail(nullptr, DWDP_ERR_INVALID_ARG, "codes and their scale go together");
@@ -1028,7 +1027,7 @@ int32_t dwdp_sandwich_norm(const dwdp_sandwich* how, const void* x, int64_t x_st
 }
 
 size_t dwdp_sandwich_grad_workspace_bytes(int64_t rows, int32_t H) {
-    if (rows < 0 || rows >= ((int64_t)1 << 31) || H <= 0 || H % 8 || H > 8192) return 0;
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || H <= 0 || H % 8 || H > 32768) return 0;
     return std::max<size_t>(256, sandwich_grad_bytes(rows, H));
 }
 
@@ -1038,7 +1037,7 @@ int32_t dwdp_sandwich_norm_grad(const dwdp_sandwich* how, const void* x, int64_t
                                 float* dpost_weight, float* dpre_weight, float* dgate, void* ws, size_t ws_bytes,
                                 dwdp_stream_t stream) {
     const NvtxRange nvtx("dwdp_sandwich_norm_grad rows=%lld", (long long)rows);
-    const int32_t rc = check_sandwich(how, x, x_stride, rows, H, 8192);
+    const int32_t rc = check_sandwich(how, x, x_stride, rows, H);
     if (rc != DWDP_OK) return rc;
     if ((x_scale && !x) || (h_scale && !h)) return fail(nullptr, DWDP_ERR_INVALID_ARG, "a scale needs its codes");
     if ((dpost_weight && !how->post_weight) || (dpre_weight && !how->pre_weight) || (dgate && !how->gate))

@@ -287,7 +287,8 @@ struct SandwichGradArgs {
     float* dpre;
     float* dgate;
     float* partial;
-    int64_t blocks, chunk;
+    int64_t units, chunk;  // rows at once; rows a unit
+    int size, share;       // blocks that share a row, vectors a block
 };
 size_t sandwich_grad_bytes(int64_t rows, int H);
 cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s);

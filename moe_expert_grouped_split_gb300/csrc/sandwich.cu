@@ -348,13 +348,53 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------ gradients --
+// Two binary32 values in one 64-bit register, one instruction for both.
+using pair = unsigned long long;
+__device__ __forceinline__ pair two(float a, float b) {
+    pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ pair two(float a) { return two(a, a); }
+__device__ __forceinline__ float2 apart(pair v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
+    pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ pair mul2(pair a, pair b) {
+    pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+using four = pair[4];  // a vector's 8 elements
+__device__ __forceinline__ void unpack4(uint4 q, four& f) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack4(const four& f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = apart(f[i]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // How a row was kept.
 enum Kept : int { KEPT_NOT, KEPT_BF16, KEPT_E4M3 };
 __host__ __device__ constexpr int kept_bytes(int k) { return k == KEPT_E4M3 ? 8 : k == KEPT_BF16 ? 16 : 0; }
 
 // 8 elements of a kept row times `by`.
 template <int K>
-__device__ __forceinline__ void values(const char* at, float by, eight& f) {
+__device__ __forceinline__ void values(const char* at, pair by, four& f) {
     if constexpr (K == KEPT_E4M3) {
         const uint2 q = *reinterpret_cast<const uint2*>(at);
         const uint32_t w[2] = {q.x, q.y};
@@ -363,20 +403,33 @@ __device__ __forceinline__ void values(const char* at, float by, eight& f) {
             const __half2_raw v =
                 __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> ((i & 1) * 16)), __NV_E4M3);
             const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&v));
-            f[2 * i] = t.x * by;
-            f[2 * i + 1] = t.y * by;
+            f[i] = two(t.x, t.y);
         }
     } else {
-        unpack8(*reinterpret_cast<const uint4*>(at), f);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] *= by;
+        unpack4(*reinterpret_cast<const uint4*>(at), f);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], by);
 }
 
-// The block's sums of a, b and c, for every thread.  A warp's three sums
-// together: half of the lanes go on with each value.  `turn` alternates
-// between two buffers, so one barrier is enough.  16 warps at most.
-__device__ __forceinline__ float3 block_sums(float a, float b, float c, float (*red)[64], int& turn) {
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of the cluster; what was written to any block's shared memory
+// before is seen after it.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The sums of a, b and c over the `size` blocks (4 at most) that share a row,
+// for every thread.  A warp's three sums together: half of the lanes go on
+// with each value, and eight lanes end with each, one of them for each block.
+// Rows take the two halves of red ([2][size][warps][4]) in turn, so one
+// barrier is enough.  16 warps at most.
+template <bool SHARED>
+__device__ __forceinline__ float3 row_sums(float a, float b, float c, float* red, int& turn, int size) {
     constexpr uint32_t all = 0xffffffffu;
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const bool upper = lane & 16, odd = lane & 8;
@@ -386,10 +439,23 @@ __device__ __forceinline__ float3 block_sums(float a, float b, float c, float (*
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(all, s, o);
     // lanes 8 i .. 8 i + 7: value i
-    if (nw > 1) {
-        float* r = red[turn];
+    const int warp = threadIdx.x >> 5, w = lane & 7, i = lane >> 3;
+    if (SHARED) {
+        float* r = red + turn * size * nw * 4;
         turn ^= 1;
-        const int warp = threadIdx.x >> 5, w = lane & 7, i = lane >> 3;
+        if (w < size) {
+            uint32_t at = (uint32_t)__cvta_generic_to_shared(r + (cluster_rank() * nw + warp) * 4 + i);
+            asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(w));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(s) : "memory");
+        }
+        cluster_barrier();
+        s = 0.0f;
+        for (int e = w; e < size * nw; e += 8) s += r[e * 4 + i];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(all, s, o);
+    } else if (nw > 1) {
+        float* r = red + turn * 64;
+        turn ^= 1;
         if (w == 0) r[warp * 4 + i] = s;
         __syncthreads();
         s = (w < nw ? r[w * 4 + i] : 0.0f) + (w + 8 < nw ? r[(w + 8) * 4 + i] : 0.0f);
@@ -399,46 +465,55 @@ __device__ __forceinline__ float3 block_sums(float a, float b, float c, float (*
     return make_float3(__shfl_sync(all, s, 0), __shfl_sync(all, s, 8), __shfl_sync(all, s, 16));
 }
 
-__device__ __forceinline__ void store8(float* to, const eight& f) {
-    reinterpret_cast<float4*>(to)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(to)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store4(float* to, const four& f) {
+    reinterpret_cast<ulonglong2*>(to)[0] = make_ulonglong2(f[0], f[1]);
+    reinterpret_cast<ulonglong2*>(to)[1] = make_ulonglong2(f[2], f[3]);
 }
-constexpr int kGradStages = 3, kGradVecs = 2;
+__device__ __forceinline__ void load4(const ulonglong2* at, int far, four& f) {
+    const ulonglong2 a = at[0], b = at[far];
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
 
-// A block takes rows [blockIdx.x chunk, + chunk) in order; thread i holds the
-// row's vectors i and i + blockDim.x and their columns' sums.  Of the weights'
+constexpr int kGradVecs = 2, kGradSmem = 227 << 10;
+
+// A block takes rows [unit chunk, + chunk) in order; thread i holds the row's
+// vectors i and i + blockDim.x and their columns' sums.  Rows of more than
+// 8192 elements are shared by a cluster of blocks, each with its part of the
+// columns (SHARED).  Of the weights'
 // gradients only two sums a column have to be kept while rows go by: dout
 // hhat, and S = dh xhat since the group began, as dgate = c post S and
-// dpost_weight = sum over groups of c gate S.  The rows kGradStages ahead are
+// dpost_weight = sum over groups of c gate S.  The rows STAGES ahead are
 // on their way into shared memory.  One reduction a row: with e = dres + rh gy
 // and q = c gate post xhat,
 //   mean(gn xhat) = mean(q e) - rh mean(gy hhat) mean(q hhat).
-// partial [blocks][4][H]: the sums for pre and post, and S of the group that
-// was begun before the block's rows and of the one that goes on after them
+// partial [units][4][H]: the sums for pre and post, and S of the group that
+// was begun before the unit's rows and of the one that goes on after them
 // (a group whose rows are all here goes to dgate at once).
 // X, HK: how x and h were kept (HK KEPT_NOT: no pre norm); POST: a post norm.
-template <int X, int HK, bool POST>
+template <int X, int HK, bool POST, int STAGES, bool SHARED>
 __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_constant__ SandwichGradArgs p) {
     constexpr int VPT = kGradVecs, kX = kept_bytes(X), kH = kept_bytes(HK);
     constexpr bool PRE = HK != KEPT_NOT;
     extern __shared__ __align__(16) char smem[];
-    __shared__ float red[2][64];
     const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31;
+    const int size = SHARED ? p.size : 1, rank = SHARED ? (int)cluster_rank() : 0, unit = blockIdx.x / size;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    const int64_t lo = (int64_t)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.rows);
-    const int H = p.nv * 8;
+    const int64_t lo = (int64_t)unit * p.chunk, hi = min(lo + p.chunk, p.rows);
+    const int H = p.nv * 8, own_vecs = SHARED ? min(p.nv - rank * p.share, p.share) : p.nv;
+    const int first = SHARED ? rank * p.share + tid : tid;  // this thread's first vector
     // a stage: vectors of dout, dres, x and h; behind the stages c gate post
     const int vecs = n * VPT, stage_bytes = vecs * (kX + kH + 32);
     char* const own = smem + tid * 16;
     char* const own_x = smem + vecs * 32 + tid * kX;
     char* const own_h = smem + vecs * (32 + kX) + tid * kH;
     // (vector j's two halves n 16 bytes apart: no two lanes on one bank)
-    float4* const gw = reinterpret_cast<float4*>(smem + kGradStages * stage_bytes) + tid;
-    const bool held[VPT] = {tid < p.nv, tid + n < p.nv};
+    ulonglong2* const gw = reinterpret_cast<ulonglong2*>(smem + STAGES * stage_bytes) + tid;
+    float* const red = reinterpret_cast<float*>(smem + STAGES * stage_bytes + vecs * 32);
+    const bool held[VPT] = {tid < own_vecs, tid + n < own_vecs};
     auto fetch = [&](int64_t row, int at) {
         if (row < hi) {
-            const int64_t vec = row * p.nv + tid, x_vec = row * p.x_vecs + tid;
+            const int64_t vec = row * p.nv + first, x_vec = row * p.x_vecs + first;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (!held[j]) continue;
@@ -459,7 +534,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
     for (int j = 0; j < VPT; ++j) {
         const uint4 zero = make_uint4(0, 0, 0, 0);
         if (held[j] && p.dres) continue;
-        for (int at = 0; at < kGradStages * stage_bytes; at += stage_bytes) {
+        for (int at = 0; at < STAGES * stage_bytes; at += stage_bytes) {
             *reinterpret_cast<uint4*>(own + at + (VPT + j) * n * 16) = zero;
             if (held[j]) continue;
             *reinterpret_cast<uint4*>(own + at + j * n * 16) = zero;
@@ -468,7 +543,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
             if (kH == 16) *reinterpret_cast<uint4*>(own_h + at + j * n * kH) = zero;
             if (kH == 8) *reinterpret_cast<uint2*>(own_h + at + j * n * kH) = make_uint2(0, 0);
         }
-        if (!held[j]) gw[2 * j * n] = gw[(2 * j + 1) * n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!held[j]) gw[2 * j * n] = gw[(2 * j + 1) * n] = make_ulonglong2(0, 0);
     }
     // what a row has once: 1 / rms of both norms, and what x's and h's values are to be multiplied by
     auto row_factors = [&](int64_t row) {
@@ -477,71 +552,77 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
         return make_float4(r.x, r.y, X == KEPT_E4M3 ? p.x_scale[row] * r.x : r.x, HK == KEPT_E4M3 ? p.h_scale[row] * r.y : r.y);
     };
 #pragma unroll
-    for (int s = 0; s < kGradStages; ++s) fetch(lo + s, s * stage_bytes);
+    for (int s = 0; s < STAGES; ++s) fetch(lo + s, s * stage_bytes);
     float4 mine = row_factors(lo + lane), later = row_factors(lo + 32 + lane);  // of 32 rows, a lane each
-    eight dpre[VPT] = {}, sum[VPT] = {};
+    four dpre[VPT] = {}, sum[VPT] = {};
     uint4 pre[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) pre[j] = PRE && tid + j * n < p.nv ? __ldg(p.pre + tid + j * n) : make_uint4(0, 0, 0, 0);
-    float* partial = p.partial + (int64_t)blockIdx.x * 4 * H;
+    for (int j = 0; j < VPT; ++j) pre[j] = PRE && held[j] ? __ldg(p.pre + first + j * n) : make_uint4(0, 0, 0, 0);
+    float* partial = p.partial + (int64_t)unit * 4 * H;
     const bool to_dx[VPT] = {held[0] && p.dx, held[1] && p.dx};
     const bool to_dresidual[VPT] = {held[0] && p.dresidual, held[1] && p.dresidual};
     int group = 0, in = 0, turn = 0;
     int64_t begin = 0, end = p.rows;  // of the group
     bool open = !p.row_offsets, any = false;
     // block_scale times a weight's or gate's elements (1 where there is none)
-    auto scaled = [&](const uint4* w, int64_t vec, eight& f) {
-        if (w) unpack8(__ldg(w + vec), f);
+    auto scaled = [&](const uint4* w, int64_t vec, four& f) {
+        if (w) {
+            unpack4(__ldg(w + vec), f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = p.block_scale * (w ? f[c] : 1.0f);
+            for (int c = 0; c < 4; ++c) f[c] = mul2(f[c], two(p.block_scale));
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) f[c] = two(p.block_scale);
+        }
     };
     auto open_group = [&]() {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = tid + j * n;
-            if (i >= p.nv) continue;
-            eight g;
+            const int i = first + j * n;
+            if (!held[j]) continue;
+            four g;
             scaled(p.gate, (int64_t)group * p.nv + i, g);
             if constexpr (POST) {
-                eight w;
-                unpack8(__ldg(p.post + i), w);
+                four w;
+                unpack4(__ldg(p.post + i), w);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) g[c] *= w[c];
+                for (int c = 0; c < 4; ++c) g[c] = mul2(g[c], w[c]);
             }
-            gw[2 * j * n] = make_float4(g[0], g[1], g[2], g[3]);
-            gw[(2 * j + 1) * n] = make_float4(g[4], g[5], g[6], g[7]);
+            gw[2 * j * n] = make_ulonglong2(g[0], g[1]);
+            gw[(2 * j + 1) * n] = make_ulonglong2(g[2], g[3]);
         }
     };
     auto close_group = [&]() {
         const bool whole = begin >= lo && end <= hi;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = tid + j * n;
-            if (i >= p.nv) continue;
+            const int i = first + j * n;
+            if (!held[j]) continue;
             if (POST && p.dpost) {
-                eight g, before = {};
+                four g, before = {};
                 scaled(p.gate, (int64_t)group * p.nv + i, g);
                 float* to = partial + H + 8 * i;
-                if (any) load8(reinterpret_cast<const float4*>(to), 1, before);
+                if (any) load4(reinterpret_cast<const ulonglong2*>(to), 1, before);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) before[c] = fmaf(g[c], sum[j][c], before[c]);
-                store8(to, before);
+                for (int c = 0; c < 4; ++c) before[c] = fma2(g[c], sum[j][c], before[c]);
+                store4(to, before);
             }
             if (p.dgate) {
                 if (whole) {
-                    eight w;
+                    four w;
                     scaled(POST ? p.post : nullptr, i, w);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) sum[j][c] *= w[c];
+                    for (int c = 0; c < 4; ++c) sum[j][c] = mul2(sum[j][c], w[c]);
                 }
-                store8((whole ? p.dgate + (int64_t)group * H : partial + (begin < lo ? 2 : 3) * H) + 8 * i, sum[j]);
+                store4((whole ? p.dgate + (int64_t)group * H : partial + (begin < lo ? 2 : 3) * H) + 8 * i, sum[j]);
             }
 #pragma unroll
-            for (int c = 0; c < 8; ++c) sum[j][c] = 0.0f;
+            for (int c = 0; c < 4; ++c) sum[j][c] = 0;
         }
         any = true;
     };
     if (open) open_group();
+    if (SHARED) cluster_barrier();  // all blocks are there to be written to
     const int rows = (int)(hi - lo);
     int change = open ? rows : 0;  // the row at which the group has to be looked up again
     for (int r = 0; r < rows; ++r) {
@@ -550,7 +631,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
             mine = later;
             later = row_factors(lo + r + 32 + lane);
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         if (r == change) {
             if (open) close_group();
             group = group_of(p.row_offsets, p.n_groups, lo + r);
@@ -566,90 +647,92 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
         if (open) {
             const float rx = __shfl_sync(0xffffffffu, mine.x, at), rh = __shfl_sync(0xffffffffu, mine.y, at);
             const float x_by = __shfl_sync(0xffffffffu, mine.z, at), h_by = __shfl_sync(0xffffffffu, mine.w, at);
-            eight e[VPT], hh[VPT], xx[VPT];
-            float by_h = 0.0f, q_e = 0.0f, q_h = 0.0f;  // the sums of gy hhat, q e and q hhat
+            four e[VPT], hh[VPT], xx[VPT];
+            pair by_h = 0, q_e = 0, q_h = 0;  // the sums of gy hhat, q e and q hhat
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                unpack8(*reinterpret_cast<const uint4*>(own + in + (VPT + j) * n * 16), e[j]);
+                unpack4(*reinterpret_cast<const uint4*>(own + in + (VPT + j) * n * 16), e[j]);
                 if constexpr (PRE) {
-                    eight w, dy;
-                    values<HK>(own_h + in + j * n * kH, h_by, hh[j]);
-                    unpack8(*reinterpret_cast<const uint4*>(own + in + j * n * 16), dy);
-                    unpack8(pre[j], w);
+                    four w, dy;
+                    values<HK>(own_h + in + j * n * kH, two(h_by), hh[j]);
+                    unpack4(*reinterpret_cast<const uint4*>(own + in + j * n * 16), dy);
+                    unpack4(pre[j], w);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        dpre[j][c] = fmaf(dy[c], hh[j][c], dpre[j][c]);
-                        const float gy = dy[c] * w[c];
-                        by_h = fmaf(gy, hh[j][c], by_h);
-                        e[j][c] = fmaf(rh, gy, e[j][c]);
+                    for (int c = 0; c < 4; ++c) {
+                        dpre[j][c] = fma2(dy[c], hh[j][c], dpre[j][c]);
+                        const pair gy = mul2(dy[c], w[c]);
+                        by_h = fma2(gy, hh[j][c], by_h);
+                        e[j][c] = fma2(two(rh), gy, e[j][c]);
                     }
                 }
-                if constexpr (X != KEPT_NOT) values<X>(own_x + in + j * n * kX, x_by, xx[j]);
+                if constexpr (X != KEPT_NOT) values<X>(own_x + in + j * n * kX, two(x_by), xx[j]);
                 if constexpr (POST) {
-                    eight w;
-                    load8(gw + 2 * j * n, n, w);
+                    four w;
+                    load4(gw + 2 * j * n, n, w);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float q = w[c] * xx[j][c];
-                        q_e = fmaf(q, e[j][c], q_e);
-                        if constexpr (PRE) q_h = fmaf(q, hh[j][c], q_h);
+                    for (int c = 0; c < 4; ++c) {
+                        const pair t = mul2(w[c], xx[j][c]);
+                        q_e = fma2(t, e[j][c], q_e);
+                        if constexpr (PRE) q_h = fma2(t, hh[j][c], q_h);
                     }
                 }
             }
             float m = 0.0f, m2 = 0.0f;
-            const int64_t vec = (lo + r) * p.nv + tid;
+            const int64_t vec = (lo + r) * p.nv + first;
             if constexpr (PRE || POST) {
-                const float3 sums = block_sums(by_h, q_e, q_h, red, turn);
+                const float2 s0 = apart(by_h), s1 = apart(q_e), s2 = apart(q_h);
+                const float3 sums = row_sums<SHARED>(s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, red, turn, size);
                 m = rh * sums.x * p.one_nth;
                 m2 = rx * (sums.y - m * sums.z) * p.one_nth;
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                eight t;
+                four t;
                 if constexpr (PRE) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) e[j][c] = fmaf(-m, hh[j][c], e[j][c]);
+                    for (int c = 0; c < 4; ++c) e[j][c] = fma2(two(-m), hh[j][c], e[j][c]);
                 }
 #pragma unroll
-                for (int c = 0; c < 8; ++c) t[c] = p.residual_scale * e[j][c];
-                if (to_dresidual[j]) p.dresidual[vec + j * n] = pack8(t);
+                for (int c = 0; c < 4; ++c) t[c] = mul2(two(p.residual_scale), e[j][c]);
+                if (to_dresidual[j]) p.dresidual[vec + j * n] = pack4(t);
                 if constexpr (X != KEPT_NOT) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) sum[j][c] = fmaf(e[j][c], xx[j][c], sum[j][c]);
+                    for (int c = 0; c < 4; ++c) sum[j][c] = fma2(e[j][c], xx[j][c], sum[j][c]);
                 }
-                load8(gw + 2 * j * n, n, t);
+                load4(gw + 2 * j * n, n, t);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    t[c] *= e[j][c];
-                    if constexpr (POST) t[c] = fmaf(rx, t[c], -m2 * xx[j][c]);
+                for (int c = 0; c < 4; ++c) {
+                    t[c] = mul2(t[c], e[j][c]);
+                    if constexpr (POST) t[c] = fma2(two(rx), t[c], mul2(two(-m2), xx[j][c]));
                 }
-                if (to_dx[j]) p.dx[vec + j * n] = pack8(t);
+                if (to_dx[j]) p.dx[vec + j * n] = pack4(t);
             }
         }
-        fetch(lo + r + kGradStages, in);
+        fetch(lo + r + STAGES, in);
         in += stage_bytes;
-        if (in == kGradStages * stage_bytes) in = 0;
+        if (in == STAGES * stage_bytes) in = 0;
     }
     if (open) close_group();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int i = tid + j * n;
-        if (i >= p.nv) continue;
-        const eight none = {};
-        if (PRE && p.dpre) store8(partial + 8 * i, dpre[j]);
-        if (POST && p.dpost && !any) store8(partial + H + 8 * i, none);
+        const int i = first + j * n;
+        if (!held[j]) continue;
+        const four none = {};
+        if (PRE && p.dpre) store4(partial + 8 * i, dpre[j]);
+        if (POST && p.dpost && !any) store4(partial + H + 8 * i, none);
     }
+    if (SHARED) cluster_barrier();  // no block leaves while another may write to it
 }
 
-// Adds up the blocks' sums: blockIdx.y 0 pre, 1 post, 2 + g group g's gate;
-// 32 columns a block, the row blocks dealt to 8 warps.
+// Adds up the units' sums: blockIdx.y 0 pre, 1 post, 2 + g group g's gate;
+// 32 columns a block, the units dealt to 8 warps.
 __global__ void __launch_bounds__(256) sandwich_sums_kernel(const __grid_constant__ SandwichGradArgs p) {
     __shared__ float red[8][32];
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int H = p.nv * 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
     const int what = blockIdx.y;
-    int64_t first = 0, last = p.blocks - 1;
+    int64_t first = 0, last = p.units - 1;
     float* to;
     if (what < 2) {
         to = what == 0 ? p.dpre : p.dpost;
@@ -667,7 +750,7 @@ __global__ void __launch_bounds__(256) sandwich_sums_kernel(const __grid_constan
             } else {
                 last = -1;
             }
-        } else if (p.blocks == 1) {
+        } else if (p.units == 1) {
             return;
         }
     }
@@ -692,34 +775,51 @@ __global__ void __launch_bounds__(256) sandwich_sums_kernel(const __grid_constan
     }
 }
 
-// The gradients' kernel: threads of a block, its shared memory with kept rows
-// of x_bytes and h_bytes a vector, and how many blocks.
-int grad_threads(int nv) { return ((nv + kGradVecs - 1) / kGradVecs + 31) / 32 * 32; }
-size_t grad_smem(int nv, int x_bytes, int h_bytes) {
-    return (size_t)grad_threads(nv) * kGradVecs * (kGradStages * (x_bytes + h_bytes + 32) + 32);
-}
-// As many blocks as a GB300's 152 SMs hold at 128 registers a thread and
-// `smem` bytes a block (the workspace: 0).
-int64_t grad_blocks(int64_t rows, int nv, size_t smem) {
-    const int64_t by_smem = (228 << 10) / (smem + 1024 + 256), most = 152 * std::min<int64_t>(512 / grad_threads(nv), by_smem);
-    return std::max<int64_t>(1, std::min(rows, most));
-}
+// How the gradients' kernel is launched for rows of nv vectors.
+struct GradShape {
+    int size, share, threads;  // blocks that share a row, vectors a block, threads
+    explicit GradShape(int nv)
+        : size((nv + 1023) / 1024), share((nv + size - 1) / size), threads(((share + kGradVecs - 1) / kGradVecs + 31) / 32 * 32) {}
+    size_t smem(int stages, int x_bytes, int h_bytes) const {
+        return (size_t)threads * kGradVecs * (stages * (x_bytes + h_bytes + 32) + 32) + std::max(size * threads, 512);
+    }
+    // As many units (rows at once) as a GB300's 152 SMs hold at 128 registers
+    // a thread and `smem` bytes a block (the workspace: 0).
+    int64_t units(int64_t rows, size_t smem) const {
+        const int64_t blocks = std::min<int64_t>(512 / threads, (228 << 10) / (smem + 1024));
+        return std::max<int64_t>(1, std::min(rows, 152 * blocks / size));
+    }
+};
 
-template <int X, int HK, bool POST>
-cudaError_t launch_grad(const SandwichGradArgs& p, cudaStream_t s) {
-    const auto kernel = sandwich_grad_kernel<X, HK, POST>;
+template <int X, int HK, bool POST, int STAGES, bool SHARED>
+cudaError_t launch_grad(const SandwichGradArgs& p, const GradShape& g, cudaStream_t s) {
+    const auto kernel = sandwich_grad_kernel<X, HK, POST, STAGES, SHARED>;
     // the kernel's limit, not this call's size (norm.cu)
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)grad_smem(1024, kept_bytes(X), kept_bytes(HK)));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, p, dim3((unsigned)p.blocks), grad_threads(p.nv),
-                            grad_smem(p.nv, kept_bytes(X), kept_bytes(HK)), s);
+    return launch_dependent(kernel, p, dim3((unsigned)(p.units * g.size)), g.threads,
+                            g.smem(STAGES, kept_bytes(X), kept_bytes(HK)), s, g.size);
+}
+template <int X, int HK, bool POST>
+cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
+    const GradShape g(p.nv);
+    // three stages where they fit an SM
+    const size_t smem = g.smem(3, kept_bytes(X), kept_bytes(HK));
+    const bool three = smem <= kGradSmem;
+    p.size = g.size;
+    p.share = g.share;
+    p.units = g.units(p.rows, three ? smem : g.smem(2, kept_bytes(X), kept_bytes(HK)));
+    p.chunk = (p.rows + p.units - 1) / p.units;
+    p.units = (p.rows + p.chunk - 1) / p.chunk;
+    if (g.size == 1)
+        return three ? launch_grad<X, HK, POST, 3, false>(p, g, s) : launch_grad<X, HK, POST, 2, false>(p, g, s);
+    return three ? launch_grad<X, HK, POST, 3, true>(p, g, s) : launch_grad<X, HK, POST, 2, true>(p, g, s);
 }
 template <int X, bool POST>
-cudaError_t launch_grad(const SandwichGradArgs& p, int h, cudaStream_t s) {
-    return h == KEPT_NOT    ? launch_grad<X, KEPT_NOT, POST>(p, s)
-           : h == KEPT_BF16 ? launch_grad<X, KEPT_BF16, POST>(p, s)
-                            : launch_grad<X, KEPT_E4M3, POST>(p, s);
+cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
+    return !p.pre        ? launch_grad<X, KEPT_NOT, POST>(p, s)
+           : !p.h_scale ? launch_grad<X, KEPT_BF16, POST>(p, s)
+                        : launch_grad<X, KEPT_E4M3, POST>(p, s);
 }
 
 template <class ASK>
@@ -758,11 +858,12 @@ cudaError_t launch_sandwich_norm(SandwichArgs& p, cudaStream_t s) {
     return kept ? launch_norm<false, true>(p, s) : launch_norm<false, false>(p, s);
 }
 
-size_t sandwich_grad_bytes(int64_t rows, int H) { return (size_t)grad_blocks(rows, H / 8, 0) * 4 * H * sizeof(float); }
+size_t sandwich_grad_bytes(int64_t rows, int H) {
+    return (size_t)GradShape(H / 8).units(rows, 0) * 4 * H * sizeof(float);
+}
 
 cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s) {
-    const int H = p.nv * 8, x = !p.x ? KEPT_NOT : p.x_scale ? KEPT_E4M3 : KEPT_BF16,
-              h = !p.pre ? KEPT_NOT : p.h_scale ? KEPT_E4M3 : KEPT_BF16;
+    const int H = p.nv * 8;
     if (p.rows == 0) {
         const size_t row = H * sizeof(float);
         cudaError_t e = cudaSuccess;
@@ -771,13 +872,9 @@ cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s) {
         if (p.dgate && e == cudaSuccess) e = cudaMemsetAsync(p.dgate, 0, row * p.n_groups, s);
         return e;
     }
-    p.blocks = grad_blocks(p.rows, p.nv, grad_smem(p.nv, kept_bytes(x), kept_bytes(h)));
-    p.chunk = (p.rows + p.blocks - 1) / p.blocks;
-    p.blocks = (p.rows + p.chunk - 1) / p.chunk;
-    const cudaError_t e = x == KEPT_NOT ? launch_grad<KEPT_NOT, false>(p, h, s)
-                          : x == KEPT_BF16
-                              ? (p.post ? launch_grad<KEPT_BF16, true>(p, h, s) : launch_grad<KEPT_BF16, false>(p, h, s))
-                              : (p.post ? launch_grad<KEPT_E4M3, true>(p, h, s) : launch_grad<KEPT_E4M3, false>(p, h, s));
+    const cudaError_t e = !p.x         ? launch_grad<KEPT_NOT, false>(p, s)
+                          : !p.x_scale ? (p.post ? launch_grad<KEPT_BF16, true>(p, s) : launch_grad<KEPT_BF16, false>(p, s))
+                                       : (p.post ? launch_grad<KEPT_E4M3, true>(p, s) : launch_grad<KEPT_E4M3, false>(p, s));
     if (e != cudaSuccess || (!p.dpre && !p.dpost && !p.dgate)) return e;
     const dim3 grid((unsigned)((H + 31) / 32), (unsigned)(2 + (p.dgate ? p.n_groups : 0)));
     return launch_dependent(sandwich_sums_kernel, p, grid, 256, 0, s);

@@ -351,7 +351,7 @@ class Grads:
             near(o[name], want, tol, self.m.inside if name in ("dx", "dresidual") else None)
 
 
-@pytest.mark.parametrize("H", [8, 64, 520, 1536, 4096, 4104, 7168, 8192])
+@pytest.mark.parametrize("H", [8, 64, 520, 1536, 4096, 4104, 7168, 8192, 8200, 20008, 32768])
 @pytest.mark.parametrize("form", FORMS, ids=str)
 def test_gradients(H, form):
     g = Grads(Made(77, H, **form))
@@ -359,7 +359,7 @@ def test_gradients(H, form):
 
 
 @pytest.mark.parametrize("x8, h8", [(False, True), (True, False), (True, True)])
-@pytest.mark.parametrize("H", [8, 520, 7168])
+@pytest.mark.parametrize("H", [8, 520, 7168, 16392])
 def test_gradients_from_rows_in_8_bits(H, x8, h8):
     g = Grads(Made(161, H, groups=[0, 3, 3, 100, 160, 161]), x8, h8)
     g.check(g.run())
@@ -367,7 +367,7 @@ def test_gradients_from_rows_in_8_bits(H, x8, h8):
     g.check(g.run())
 
 
-@pytest.mark.parametrize("rows, H", [(1, 7168), (2, 8), (152, 7168), (153, 7168), (1003, 2048), (3000, 512), (20000, 256), (305, 8192)])
+@pytest.mark.parametrize("rows, H", [(1, 7168), (2, 8), (152, 7168), (153, 7168), (1003, 2048), (3000, 512), (20000, 256), (305, 8192), (700, 12296)])
 @pytest.mark.parametrize("x8", [False, True])
 def test_gradients_of_many_rows(rows, H, x8):
     g = Grads(Made(rows, H, groups=1 if rows < 3 else [0, rows // 3, rows - 1, rows], pad=0 if x8 else 64), x8, x8)
