@@ -474,7 +474,7 @@ __device__ __forceinline__ void load4(const ulonglong2* at, int far, four& f) {
     f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 
-constexpr int kGradVecs = 2, kGradSmem = 227 << 10;
+constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = 227 << 10;
 
 // A block takes rows [unit chunk, + chunk) in order; thread i holds the row's
 // vectors i and i + blockDim.x and their columns' sums.  Rows of more than
@@ -482,18 +482,23 @@ constexpr int kGradVecs = 2, kGradSmem = 227 << 10;
 // columns (SHARED).  Of the weights'
 // gradients only two sums a column have to be kept while rows go by: dout
 // hhat, and S = dh xhat since the group began, as dgate = c post S and
-// dpost_weight = sum over groups of c gate S.  The rows STAGES ahead are
+// dpost_weight = sum over groups of c gate S.  The rows kGradStages ahead are
 // on their way into shared memory.  One reduction a row: with e = dres + rh gy
 // and q = c gate post xhat,
 //   mean(gn xhat) = mean(q e) - rh mean(gy hhat) mean(q hhat).
 // partial [units][4][H]: the sums for pre and post, and S of the group that
 // was begun before the unit's rows and of the one that goes on after them
 // (a group whose rows are all here goes to dgate at once).
-// X, HK: how x and h were kept (HK KEPT_NOT: no pre norm); POST: a post norm.
-template <int X, int HK, bool POST, int STAGES, bool SHARED>
-__global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_constant__ SandwichGradArgs p) {
+// X, HK: how x and h were kept (HK KEPT_NOT: no pre norm); POST: a post norm;
+// THREADS at most (448: the compiler's order of things is 5% faster than for 512).
+template <int X, int HK, bool POST, int THREADS, bool SHARED>
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad_kernel(const __grid_constant__ SandwichGradArgs p) {
     constexpr int VPT = kGradVecs, kX = kept_bytes(X), kH = kept_bytes(HK);
     constexpr bool PRE = HK != KEPT_NOT;
+    // the row kGradStages ahead is asked for as soon as a thread has taken its part of this one, where a block is alone on its
+    // SM (8192 x 7168 from 8 bits: 132 us; 138 if after the
+    // reduction), and after it where four share one (16384 x 2048: 74 us; 77 if before)
+    constexpr bool kEarly = THREADS > 256;
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31;
     const int size = SHARED ? p.size : 1, rank = SHARED ? (int)cluster_rank() : 0, unit = blockIdx.x / size;
@@ -503,28 +508,30 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
     const int H = p.nv * 8, own_vecs = SHARED ? min(p.nv - rank * p.share, p.share) : p.nv;
     const int first = SHARED ? rank * p.share + tid : tid;  // this thread's first vector
     // a stage: vectors of dout, dres, x and h; behind the stages c gate post
-    const int vecs = n * VPT, stage_bytes = vecs * (kX + kH + 32);
+    const int vecs = n * VPT, stage_bytes = vecs * (kX + kH + 32), all_stages = kGradStages * stage_bytes;
     char* const own = smem + tid * 16;
     char* const own_x = smem + vecs * 32 + tid * kX;
     char* const own_h = smem + vecs * (32 + kX) + tid * kH;
     // (vector j's two halves n 16 bytes apart: no two lanes on one bank)
-    ulonglong2* const gw = reinterpret_cast<ulonglong2*>(smem + STAGES * stage_bytes) + tid;
-    float* const red = reinterpret_cast<float*>(smem + STAGES * stage_bytes + vecs * 32);
+    ulonglong2* const gw = reinterpret_cast<ulonglong2*>(smem + all_stages) + tid;
+    float* const red = reinterpret_cast<float*>(smem + all_stages + vecs * 32);
     const bool held[VPT] = {tid < own_vecs, tid + n < own_vecs};
     auto fetch = [&](int64_t row, int at) {
         if (row < hi) {
-            const int64_t vec = row * p.nv + first, x_vec = row * p.x_vecs + first;
+            const char* const x = static_cast<const char*>(p.x) + row * p.x_vecs * kX;
+            const char* const h = static_cast<const char*>(p.h) + row * p.nv * kH;
+            const char* const dout = reinterpret_cast<const char*>(p.dout) + row * p.nv * 16;
+            const char* const dres = reinterpret_cast<const char*>(p.dres) + row * p.nv * 16;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (!held[j]) continue;
-                if constexpr (X != KEPT_NOT)
-                    fetch_vec<kX>(own_x + at + j * n * kX, static_cast<const char*>(p.x) + (x_vec + j * n) * kX);
+                const uint32_t place = first + j * n;
+                if constexpr (X != KEPT_NOT) fetch_vec<kX>(own_x + at + j * n * kX, x + place * kX);
                 if constexpr (PRE) {
-                    fetch_vec<kH>(own_h + at + j * n * kH, static_cast<const char*>(p.h) + (vec + j * n) * kH);
-                    fetch_vec<16>(own + at + j * n * 16, p.dout + vec + j * n);
+                    fetch_vec<kH>(own_h + at + j * n * kH, h + place * kH);
+                    fetch_vec<16>(own + at + j * n * 16, dout + place * 16);
                 }
-                if (p.dres)
-                    fetch_vec<16>(own + at + (VPT + j) * n * 16, p.dres + vec + j * n);
+                if (p.dres) fetch_vec<16>(own + at + (VPT + j) * n * 16, dres + place * 16);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
     for (int j = 0; j < VPT; ++j) {
         const uint4 zero = make_uint4(0, 0, 0, 0);
         if (held[j] && p.dres) continue;
-        for (int at = 0; at < STAGES * stage_bytes; at += stage_bytes) {
+        for (int at = 0; at < all_stages; at += stage_bytes) {
             *reinterpret_cast<uint4*>(own + at + (VPT + j) * n * 16) = zero;
             if (held[j]) continue;
             *reinterpret_cast<uint4*>(own + at + j * n * 16) = zero;
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
         return make_float4(r.x, r.y, X == KEPT_E4M3 ? p.x_scale[row] * r.x : r.x, HK == KEPT_E4M3 ? p.h_scale[row] * r.y : r.y);
     };
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) fetch(lo + s, s * stage_bytes);
+    for (int s = 0; s < kGradStages; ++s) fetch(lo + s, s * stage_bytes);
     float4 mine = row_factors(lo + lane), later = row_factors(lo + 32 + lane);  // of 32 rows, a lane each
     four dpre[VPT] = {}, sum[VPT] = {};
     uint4 pre[VPT];
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
             mine = later;
             later = row_factors(lo + r + 32 + lane);
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 1) : "memory");
         if (r == change) {
             if (open) close_group();
             group = group_of(p.row_offsets, p.n_groups, lo + r);
@@ -677,6 +684,7 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
                     }
                 }
             }
+            if constexpr (kEarly) fetch(lo + r + kGradStages, in);
             float m = 0.0f, m2 = 0.0f;
             const int64_t vec = (lo + r) * p.nv + first;
             if constexpr (PRE || POST) {
@@ -708,9 +716,9 @@ __global__ void __launch_bounds__(512, 1) sandwich_grad_kernel(const __grid_cons
                 if (to_dx[j]) p.dx[vec + j * n] = pack4(t);
             }
         }
-        fetch(lo + r + STAGES, in);
+        if (!kEarly || !open) fetch(lo + r + kGradStages, in);
         in += stage_bytes;
-        if (in == STAGES * stage_bytes) in = 0;
+        if (in == all_stages) in = 0;
     }
     if (open) close_group();
 #pragma unroll
@@ -780,8 +788,8 @@ struct GradShape {
     int size, share, threads;  // blocks that share a row, vectors a block, threads
     explicit GradShape(int nv)
         : size((nv + 1023) / 1024), share((nv + size - 1) / size), threads(((share + kGradVecs - 1) / kGradVecs + 31) / 32 * 32) {}
-    size_t smem(int stages, int x_bytes, int h_bytes) const {
-        return (size_t)threads * kGradVecs * (stages * (x_bytes + h_bytes + 32) + 32) + std::max(size * threads, 512);
+    size_t smem(int x_bytes, int h_bytes) const {  // 226 KB at most
+        return (size_t)threads * kGradVecs * (kGradStages * (x_bytes + h_bytes + 32) + 32) + std::max(size * threads, 512);
     }
     // As many units (rows at once) as a GB300's 152 SMs hold at 128 registers
     // a thread and `smem` bytes a block (the workspace: 0).
@@ -791,29 +799,27 @@ struct GradShape {
     }
 };
 
-template <int X, int HK, bool POST, int STAGES, bool SHARED>
-cudaError_t launch_grad(const SandwichGradArgs& p, const GradShape& g, cudaStream_t s) {
-    const auto kernel = sandwich_grad_kernel<X, HK, POST, STAGES, SHARED>;
+template <int X, int HK, bool POST, int THREADS, bool SHARED>
+cudaError_t launch_grad(const SandwichGradArgs& p, const GradShape& g, size_t smem, cudaStream_t s) {
+    const auto kernel = sandwich_grad_kernel<X, HK, POST, THREADS, SHARED>;
     // the kernel's limit, not this call's size (norm.cu)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, p, dim3((unsigned)(p.units * g.size)), g.threads,
-                            g.smem(STAGES, kept_bytes(X), kept_bytes(HK)), s, g.size);
+    return launch_dependent(kernel, p, dim3((unsigned)(p.units * g.size)), g.threads, smem, s, g.size);
 }
 template <int X, int HK, bool POST>
 cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
     const GradShape g(p.nv);
-    // three stages where they fit an SM
-    const size_t smem = g.smem(3, kept_bytes(X), kept_bytes(HK));
-    const bool three = smem <= kGradSmem;
+    const size_t smem = g.smem(kept_bytes(X), kept_bytes(HK));
     p.size = g.size;
     p.share = g.share;
-    p.units = g.units(p.rows, three ? smem : g.smem(2, kept_bytes(X), kept_bytes(HK)));
+    p.units = g.units(p.rows, smem);
     p.chunk = (p.rows + p.units - 1) / p.units;
     p.units = (p.rows + p.chunk - 1) / p.chunk;
-    if (g.size == 1)
-        return three ? launch_grad<X, HK, POST, 3, false>(p, g, s) : launch_grad<X, HK, POST, 2, false>(p, g, s);
-    return three ? launch_grad<X, HK, POST, 3, true>(p, g, s) : launch_grad<X, HK, POST, 2, true>(p, g, s);
+    if (g.size > 1) return launch_grad<X, HK, POST, 512, true>(p, g, smem, s);
+    return g.threads <= 256   ? launch_grad<X, HK, POST, 256, false>(p, g, smem, s)
+           : g.threads <= 448 ? launch_grad<X, HK, POST, 448, false>(p, g, smem, s)
+                              : launch_grad<X, HK, POST, 512, false>(p, g, smem, s);
 }
 template <int X, bool POST>
 cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
