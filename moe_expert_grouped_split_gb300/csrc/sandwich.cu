@@ -732,55 +732,68 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
     if (SHARED) cluster_barrier();  // no block leaves while another may write to it
 }
 
-// Adds up the units' sums: blockIdx.y 0 pre, 1 post, 2 + g group g's gate;
-// 32 columns a block, the units dealt to 8 warps.
-__global__ void __launch_bounds__(256) sandwich_sums_kernel(const __grid_constant__ SandwichGradArgs p) {
-    __shared__ float red[8][32];
+// Adds up the units' sums, 64 columns a block.  blockIdx.y 0: pre, 1: post,
+// the units dealt to 16 warps; beyond, the groups' gates: 16 groups a block, a
+// warp each (PER_WARP), or one, its units dealt to the warps.  8 loads a lane
+// are on their way.
+constexpr int kSumWarps = 16;
+template <bool PER_WARP>
+__global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __grid_constant__ SandwichGradArgs p) {
+    __shared__ float2 red[kSumWarps][32];
+    const int H = p.nv * 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 64 + 2 * lane;
+    const bool gates = blockIdx.y >= 2, alone = PER_WARP && gates;
+    const int group = !gates ? 0 : PER_WARP ? (blockIdx.y - 2) * kSumWarps + warp : blockIdx.y - 2;
+    float* to = gates ? p.dgate + (int64_t)group * H : blockIdx.y == 0 ? p.dpre : p.dpost;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    const int H = p.nv * 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-    const int what = blockIdx.y;
-    int64_t first = 0, last = p.units - 1;
-    float* to;
-    if (what < 2) {
-        to = what == 0 ? p.dpre : p.dpost;
-        if (!to) return;
-    } else {
-        if (!p.dgate) return;
-        const int g = what - 2;
-        to = p.dgate + (int64_t)g * H;
-        if (p.row_offsets) {
-            const int64_t begin = max(p.row_offsets[g], 0), end = min((int64_t)p.row_offsets[g + 1], p.rows);
-            if (begin < end) {
-                first = begin / p.chunk;
-                last = (end - 1) / p.chunk;
-                if (first == last) return;  // written already
-            } else {
-                last = -1;
-            }
-        } else if (p.units == 1) {
-            return;
+    if (!gates && !to) return;
+    uint32_t first = 0, last = (uint32_t)p.units;  // one behind the last unit
+    bool wanted = col < H;
+    if (gates) {
+        if (group >= p.n_groups) {
+            wanted = false;
+        } else if (p.row_offsets) {
+            const uint32_t begin = max(p.row_offsets[group], 0), chunk = (uint32_t)p.chunk;
+            const uint32_t end = min((uint32_t)max(p.row_offsets[group + 1], 0), (uint32_t)p.rows);
+            first = begin / chunk;
+            last = begin < end ? (end - 1) / chunk + 1 : 0;
         }
+        if (last == first + 1) wanted = false;  // written already
     }
-    float s = 0.0f;
-    if (col < H) {
+    float2 s = make_float2(0.0f, 0.0f);
+    if (wanted) {
+        const float* from = p.partial + (gates ? 2 : blockIdx.y) * (int64_t)H + col;
+        const uint32_t step = alone ? 1 : kSumWarps;
 #pragma unroll 8
-        for (int64_t b = first + warp; b <= last; b += 8) {
-            const int slot = what < 2 ? what : b == first ? 3 : 2;
-            s += p.partial[(b * 4 + slot) * H + col];
+        for (uint32_t b = first + (alone ? 0 : warp); b < last; b += step) {
+            // the group begun in its first unit lies in the slot behind
+            const float2 v = *reinterpret_cast<const float2*>(from + ((int64_t)b * 4 + (gates && b == first)) * H);
+            s.x += v.x;
+            s.y += v.y;
         }
     }
-    red[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && col < H) {
+    if (!alone) {
+        red[warp][lane] = s;
+        __syncthreads();
+        if (warp != 0) return;
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += red[w][lane];
-        if (what >= 2) {
-            s *= p.block_scale;
-            if (p.post) s *= __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.post)[col]);
+        for (int w = 1; w < kSumWarps; ++w) {
+            s.x += red[w][lane].x;
+            s.y += red[w][lane].y;
         }
-        to[col] = s;
     }
+    if (!wanted) return;
+    if (gates) {
+        float2 by = make_float2(p.block_scale, p.block_scale);
+        if (p.post) {
+            const float2 w = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(p.post)[col / 2]);
+            by.x *= w.x;
+            by.y *= w.y;
+        }
+        s.x *= by.x;
+        s.y *= by.y;
+    }
+    *reinterpret_cast<float2*>(to + col) = s;
 }
 
 // How the gradients' kernel is launched for rows of nv vectors.
@@ -792,10 +805,11 @@ struct GradShape {
         return (size_t)threads * kGradVecs * (kGradStages * (x_bytes + h_bytes + 32) + 32) + std::max(size * threads, 512);
     }
     // As many units (rows at once) as a GB300's 152 SMs hold at 128 registers
-    // a thread and `smem` bytes a block (the workspace: 0).
+    // a thread and `smem` bytes a block (the workspace: 0), but no more than one
+    // an SM for less than two rows each (1003 x 2048: 19.6 us, 22.4 otherwise).
     int64_t units(int64_t rows, size_t smem) const {
         const int64_t blocks = std::min<int64_t>(512 / threads, (228 << 10) / (smem + 1024));
-        return std::max<int64_t>(1, std::min(rows, 152 * blocks / size));
+        return std::max<int64_t>(1, std::min({rows, 152 * blocks / size, std::max<int64_t>(152 / size, rows / 2)}));
     }
 };
 
@@ -882,8 +896,12 @@ cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s) {
                           : !p.x_scale ? (p.post ? launch_grad<KEPT_BF16, true>(p, s) : launch_grad<KEPT_BF16, false>(p, s))
                                        : (p.post ? launch_grad<KEPT_E4M3, true>(p, s) : launch_grad<KEPT_E4M3, false>(p, s));
     if (e != cudaSuccess || (!p.dpre && !p.dpost && !p.dgate)) return e;
-    const dim3 grid((unsigned)((H + 31) / 32), (unsigned)(2 + (p.dgate ? p.n_groups : 0)));
-    return launch_dependent(sandwich_sums_kernel, p, grid, 256, 0, s);
+    const unsigned tiles = (H + 63) / 64;
+    // a warp each from few units a group on (1003 x 2048, 11 groups of 45 units: 20 us, 38 with a warp each)
+    if (!p.dgate || p.n_groups * 8 < p.units)
+        return launch_dependent(sandwich_sums_kernel<false>, p, dim3(tiles, 2 + (p.dgate ? p.n_groups : 0)), 32 * kSumWarps, 0, s);
+    return launch_dependent(sandwich_sums_kernel<true>, p, dim3(tiles, 2 + (p.n_groups + kSumWarps - 1) / kSumWarps),
+                            32 * kSumWarps, 0, s);
 }
 
 }  // namespace dwdp
