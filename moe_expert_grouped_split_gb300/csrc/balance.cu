@@ -8,10 +8,11 @@
 // for the largest logit: with exp(z) (softmax) or s = 1 / (1 + exp(-z))
 // (sigmoid) as they are, the sum says whether binary32 held them, and only a
 // token whose sum lies outside [kLeast, kMost] is taken again relative to its
-// largest logit.  For the sigmoid with c = min(that, 0):
-//   a = exp(c - z),  u = 1 / (a + exp(c)) = exp(-c) s,  p = u / sum u,
-//   1 - s = a u
-// so neither small scores nor scores next to 1 lose their digits.
+// largest logit.  For the sigmoid with c = min(that, 0), else 0:
+//   t = exp(z - c),  r = 1 / (1 + t exp(c)) = 1 - s,  u = t r = exp(-c) s,
+//   p = u / sum u
+// so neither small scores nor scores next to 1 lose their digits, and sum t
+// serves the log-sum-exp as well.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -22,8 +23,11 @@
 namespace dwdp {
 namespace {
 
-constexpr int kWarps = 8;  // of a block
-constexpr float kLeast = 1e-20f, kMost = 1e35f;
+constexpr int kWarps = 16, kGradWarps = 8;  // of a block: the losses', the gradients'
+// A token's choices in each of its lanes, for the most that E experts can have.
+__host__ __device__ constexpr int choices_a_lane(int lanes) { return lanes >= 32 ? 1 : lanes == 16 ? 2 : 4; }
+constexpr float kLeast = 1e-20f, kMost = 1e34f;
+constexpr float kTop = 88.0f;  // exp(88) is 1.7e38; from 79 on a sum is beyond kMost
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -75,11 +79,6 @@ __device__ __forceinline__ void load_token(const float* row, int E, int lane, fl
     }
 }
 
-template <int LANES, int V>
-__device__ __forceinline__ bool column(int v, int i, int lane, int E) {
-    return 4 * (v * LANES + lane) + i < E;
-}
-
 // A token's exp(z - c) and their sum.
 template <int LANES, int V>
 __device__ __forceinline__ float soft_terms(const float (&z)[4 * V], float (&e)[4 * V], float& c) {
@@ -109,21 +108,25 @@ __device__ __forceinline__ float soft_terms(const float (&z)[4 * V], float (&e)[
     return sum;
 }
 
-// A token's u and their sum (a u = 1 - s).  Columns beyond E get u = 0.
+// A token's u and r and the sum of u; z_sum, where asked for, gets sum t, and
+// z_c its c.  Columns beyond E get u = 0.
 template <int LANES, int V>
-__device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], int lane, int E, float (&a)[4 * V],
-                                               float (&u)[4 * V], float& c) {
+__device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&u)[4 * V], float (&r)[4 * V], float& c,
+                                               bool want_z, float& z_sum, float& z_c) {
     c = 0.0f;
-    float sum = 0.0f, one = 1.0f;
+    float sum, one = 1.0f;
     auto terms = [&]() {
-        sum = 0.0f;
+        sum = z_sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
-            a[i] = exp_fast(min_nan(c - z[i], 87.0f));
-            u[i] = column<LANES, V>(i / 4, i % 4, lane, E) ? rcp(a[i] + one) : 0.0f;
+            const float t = exp_fast(min_nan(z[i] - c, kTop));
+            r[i] = rcp(fmaf(t, one, 1.0f));
+            u[i] = t * r[i];
             sum += u[i];
+            z_sum += t;
         }
         sum = token_sum<LANES>(sum);
+        if (want_z) z_sum = token_sum<LANES>(z_sum);
     };
     terms();
     const bool lost = !(sum >= kLeast);
@@ -135,6 +138,11 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], int lane
         if (lost) c = min_nan(m, 0.0f);
         one = exp_fast(c);
         terms();
+    }
+    z_c = c;
+    if (want_z && __any_sync(0xffffffffu, !(z_sum <= kMost))) {  // logits of 79 and more
+        float e[4 * V];
+        z_sum = soft_terms<LANES, V>(z, e, z_c);
     }
     return sum;
 }
@@ -191,20 +199,101 @@ __device__ __forceinline__ void finish_sequence(const BalanceArgs& p, int b, int
     __syncthreads();
 }
 
-// A block takes tokens [blockIdx.x chunk, + chunk), sequence by sequence.  A
-// sequence whose tokens are all here is finished here; one that began before
-// leaves its sums in slot 0, one that goes on in slot 1.
+// What a lane has summed up over its tokens.
+template <int V>
+struct TokenSums {
+    float p[4 * V];
+    float z;
+};
+
+// Adds up tokens `first`, first + step, ... below `to` for a warp (first: of
+// its first LANES lanes, the next tokens for the others), and counts their
+// choices in hist.  The next token's logits and choices are on their way while
+// one is worked on.
+template <int LANES, int V, bool VEC>
+__device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int to, int step, int* hist, TokenSums<V>& sums) {
+    constexpr int KPL = choices_a_lane(LANES);
+    const int lane = threadIdx.x % LANES, sub = (threadIdx.x & 31) / LANES;
+    float next[4 * V];
+    int next_id[KPL];
+    auto load = [&](int t0) {  // a token of the warp at least is there
+        const int t = min(t0 + sub, to - 1);
+        load_token<LANES, V, VEC>(p.logits + (int64_t)t * p.E, p.E, lane, next);
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) next_id[j] = lane + j * LANES < p.k ? __ldg(p.ids + (int64_t)t * p.k + lane + j * LANES) : 0;
+    };
+    if (first < to) load(first);
+    for (int t0 = first; t0 < to; t0 += step) {  // whole warps together
+        const bool in = t0 + sub < to;
+        float z[4 * V], e[4 * V], c, sum;
+        int id[KPL];
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) z[i] = next[i];
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) id[j] = next_id[j];
+        if (t0 + step < to) load(t0 + step);
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) {
+            if (!in || lane + j * LANES >= p.k) continue;
+            if (id[j] >= 0 && id[j] < p.E)
+                atomicAdd(hist + id[j], 1);
+            else
+                atomicOr(p.err, DERR_BAD_INDEX);
+        }
+        float z_sum, z_c;
+        if (p.sigmoid) {
+            float r[4 * V];
+            sum = sigmoid_terms<LANES, V>(z, e, r, c, p.z != nullptr, z_sum, z_c);
+        } else {
+            z_sum = sum = soft_terms<LANES, V>(z, e, c);
+            z_c = c;
+        }
+        const float f = 1.0f / sum;
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < 4 * V; ++i) sums.p[i] = fmaf(e[i], f, sums.p[i]);
+            if (p.z) {
+                const float l = log_of(z_sum, z_c);
+                sums.z = fmaf(l, l, sums.z);
+            }
+        }
+    }
+}
+
+// A lane's sums to `rows` [tokens at once][columns]; afterwards (a barrier on)
+// total_p(e) is the block's sum of column e.
+template <int LANES, int V>
+__device__ __forceinline__ void leave(const TokenSums<V>& sums, float* rows, float* z_rows) {
+    constexpr int kCols = 4 * V * LANES;
+    const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        reinterpret_cast<float4*>(rows + slot * kCols)[v * LANES + lane] =
+            make_float4(sums.p[4 * v], sums.p[4 * v + 1], sums.p[4 * v + 2], sums.p[4 * v + 3]);
+    if (lane == 0) z_rows[slot] = sums.z;
+}
+template <int TOKENS, int COLS>
+__device__ __forceinline__ float total_p(const float* rows, int e) {
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < TOKENS; ++i) s += rows[i * COLS + e];
+    return s;
+}
+
+// Many tokens: a block takes tokens [blockIdx.x chunk, + chunk), sequence by
+// sequence.  A sequence whose tokens are all here is finished here; one that
+// began before leaves its sums in slot 0, one that goes on in slot 1.
 template <int LANES, int V, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_constant__ BalanceArgs p) {
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];
     constexpr int kTokens = 32 / LANES * kWarps;  // at once
     constexpr int kCols = 4 * V * LANES;
-    float* sums = smem;                                     // [kTokens][kCols]
+    float* rows = smem;                                          // [kTokens][kCols]
     int* hist = reinterpret_cast<int*>(smem + kTokens * kCols);  // [kCols]
-    __shared__ float red[32], z_red[kTokens];
+    __shared__ float red[32], z_rows[kTokens];
     wait_for_previous_kernel();
     let_next_kernel_start();
-    const int tid = threadIdx.x, lane = tid % LANES, slot = tid / LANES;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.T);
     int b = p.offsets ? seq_of(p.offsets, p.n_seqs, lo) : 0;
     if (b < 0) b = p.offsets[0] > lo ? 0 : p.n_seqs;
@@ -215,56 +304,14 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
         if (from >= to) continue;
         for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
-        for (int64_t i = (int64_t)from * p.k + tid; i < (int64_t)to * p.k; i += blockDim.x) {
-            const int id = p.ids[i];
-            if (id >= 0 && id < p.E)
-                atomicAdd(hist + id, 1);
-            else
-                atomicOr(p.err, DERR_BAD_INDEX);
-        }
-        float sum_p[4 * V] = {}, z_sum = 0.0f;
-        for (int t0 = from; t0 < to; t0 += kTokens) {  // whole warps together
-            const int t = t0 + slot;
-            const bool in = t < to;
-            float z[4 * V], e[4 * V], c;
-            load_token<LANES, V, VEC>(p.logits + (int64_t)(in ? t : to - 1) * p.E, p.E, lane, z);
-            float sum;
-            if (p.sigmoid) {
-                float u[4 * V];
-                sum = sigmoid_terms<LANES, V>(z, lane, p.E, e, u, c);
-                const float f = in ? 1.0f / sum : 0.0f;
-                if (in) {
-#pragma unroll
-                    for (int i = 0; i < 4 * V; ++i) sum_p[i] = fmaf(u[i], f, sum_p[i]);
-                }
-                if (p.z) sum = soft_terms<LANES, V>(z, e, c);
-            } else {
-                sum = soft_terms<LANES, V>(z, e, c);
-                const float f = 1.0f / sum;
-                if (in) {
-#pragma unroll
-                    for (int i = 0; i < 4 * V; ++i) sum_p[i] = fmaf(e[i], f, sum_p[i]);
-                }
-            }
-            if (p.z && in) {
-                const float l = log_of(sum, c);
-                z_sum = fmaf(l, l, z_sum);
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            reinterpret_cast<float4*>(sums + slot * kCols)[v * LANES + lane] =
-                make_float4(sum_p[4 * v], sum_p[4 * v + 1], sum_p[4 * v + 2], sum_p[4 * v + 3]);
-        if (lane == 0) z_red[slot] = z_sum;
+        TokenSums<V> sums{};
+        add_tokens<LANES, V, VEC>(p, from + warp * (32 / LANES), to, kTokens, hist, sums);
+        leave<LANES, V>(sums, rows, z_rows);
         __syncthreads();
-        auto sum_of = [&](int e) {
-            float s = 0.0f;
-            for (int i = 0; i < kTokens; ++i) s += sums[i * kCols + e];
-            return s;
-        };
         float z_all = 0.0f;
         if (tid == 0)
-            for (int i = 0; i < kTokens; ++i) z_all += z_red[i];
+            for (int i = 0; i < kTokens; ++i) z_all += z_rows[i];
+        auto sum_of = [&](int e) { return total_p<kTokens, kCols>(rows, e); };
         if (begin >= lo && end <= hi) {
             finish_sequence(p, b, end - begin, z_all, sum_of, [&](int e) { return hist[e]; }, red);
         } else {
@@ -277,6 +324,71 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
             __syncthreads();
         }
     }
+}
+
+// Few tokens: a cluster of 8 blocks takes a sequence, adds its blocks' sums up
+// through shared memory and finishes it, in one kernel.
+constexpr int kFewBlocks = 8;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t from_rank(const void* own, int rank) {
+    uint32_t at = (uint32_t)__cvta_generic_to_shared(own), v;
+    asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+template <int LANES, int V, bool VEC>
+__global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps)
+    balance_few_kernel(const __grid_constant__ BalanceArgs p) {
+    extern __shared__ __align__(16) float smem[];
+    constexpr int kTokens = 32 / LANES * kWarps, kCols = 4 * V * LANES;
+    float* rows = smem;
+    int* hist = reinterpret_cast<int*>(smem + kTokens * kCols);
+    float* total = smem + (kTokens + 1) * kCols;  // [kCols], and z's
+    __shared__ float red[32], z_rows[kTokens];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int tid = threadIdx.x, warp = tid >> 5, b = blockIdx.x / kFewBlocks, rank = blockIdx.x % kFewBlocks;
+    const int begin = seq_begin(p, b), end = seq_end(p, b);
+    for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    TokenSums<V> sums{};
+    add_tokens<LANES, V, VEC>(p, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
+    leave<LANES, V>(sums, rows, z_rows);
+    __syncthreads();
+    for (int e = tid; e < p.E; e += blockDim.x) total[e] = total_p<kTokens, kCols>(rows, e);
+    if (tid == 0) {
+        float z = 0.0f;
+        for (int i = 0; i < kTokens; ++i) z += z_rows[i];
+        z_rows[0] = z;
+    }
+    cluster_sync();
+    if (rank == 0) {
+        float z = 0.0f;
+        if (tid == 0)
+            for (int i = 0; i < kFewBlocks; ++i) z += __uint_as_float(from_rank(z_rows, i));
+        finish_sequence(
+            p, b, max(end - begin, 0), z,
+            [&](int e) {
+                float v[kFewBlocks], s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kFewBlocks; ++i) v[i] = __uint_as_float(from_rank(total + e, i));
+#pragma unroll
+                for (int i = 0; i < kFewBlocks; ++i) s += v[i];
+                return s;
+            },
+            [&](int e) {
+                int v[kFewBlocks], s = 0;
+#pragma unroll
+                for (int i = 0; i < kFewBlocks; ++i) v[i] = (int)from_rank(hist + e, i);
+#pragma unroll
+                for (int i = 0; i < kFewBlocks; ++i) s += v[i];
+                return s;
+            },
+            red);
+    }
+    cluster_sync();  // the others' shared memory stays until it has been read
 }
 
 // The sequences that no block finished alone: those of several blocks, and
@@ -299,6 +411,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
     if (part < parts) {
         float s = 0.0f;
         int n = 0;
+#pragma unroll 8
         for (int i = first + part; i <= last; i += parts) {
             const int64_t at = ((int64_t)i * 2 + (i == first ? 1 : 0)) * p.E + e;
             s += p.part_p[at];
@@ -344,60 +457,61 @@ __device__ __forceinline__ void store4(void* out, int64_t at, float a, float b, 
     }
 }
 
-// The gradients of a token's chosen logits from those of its weights: lane
-// holds choices lane, lane + LANES, ... (KPL of them).  direct: added to the
-// chosen logits; through: d loss / d s of the chosen, to go through all
-// shares (softmax over all, not renormalized).
+// What the gradients of a token's chosen weights add to the chosen logits: lane
+// holds choices lane, lane + LANES, ... (KPL of them): z, their logits (-inf
+// where there is none), dw.  c: the token's own (soft_terms, sigmoid_terms).
 template <int LANES, int KPL>
-__device__ __forceinline__ void choice_terms(const RouterGradArgs& p, const float* row, const int (&id)[KPL],
-                                             const float (&dw)[KPL], float c, float (&direct)[KPL]) {
-    float e[KPL], a[KPL];
-    float sum = 0.0f, m = -CUDART_INF_F;
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-        const float z = id[j] >= 0 ? __ldg(row + id[j]) : -CUDART_INF_F;
-        e[j] = z;
-        m = max_nan(m, z);
-    }
-    if (p.renorm) m = token_max<LANES>(m);
-    const float shift = !p.renorm ? c : p.sigmoid ? min_nan(m, 0.0f) : m, one = exp_fast(shift);
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-        if (p.sigmoid) {
-            a[j] = exp_fast(min_nan(shift - e[j], 87.0f));
-            e[j] = id[j] >= 0 ? rcp(a[j] + one) : 0.0f;  // exp(-shift) s
-            a[j] *= e[j];                                // 1 - s
-        } else {
-            e[j] = id[j] >= 0 ? exp_fast(e[j] - shift) : 0.0f;
-            a[j] = 1.0f;
-        }
-        sum += e[j];
-    }
-    if (p.renorm) {
-        sum = 1.0f / token_sum<LANES>(sum);
-        float dot = 0.0f;
+__device__ __forceinline__ void choice_terms(const RouterGradArgs& p, const float (&z)[KPL], const float (&dw)[KPL], float c,
+                                             float (&add)[KPL]) {
+    float e[KPL], r[KPL], sum, one;
+    auto terms = [&]() {
+        one = p.sigmoid ? exp_fast(c) : 0.0f;  // softmax: r = 1
+        sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
-            e[j] *= sum;
-            dot = fmaf(e[j], dw[j], dot);
+            e[j] = exp_fast(min_nan(z[j] - c, kTop));
+            r[j] = rcp(fmaf(e[j], one, 1.0f));  // 1 - s
+            e[j] *= r[j];                        // exp(-c) s
+            sum += e[j];
         }
-        dot = token_sum<LANES>(dot);
+    };
+    terms();
+    if (!p.renorm) {  // sigmoid, each on its own
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) direct[j] = p.scale * a[j] * e[j] * (dw[j] - dot);
-    } else {
-        // sigmoid, each on its own
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) direct[j] = p.scale * a[j] * e[j] * one * dw[j];
+        for (int j = 0; j < KPL; ++j) add[j] = p.scale * r[j] * e[j] * one * dw[j];
+        return;
     }
+    sum = token_sum<LANES>(sum);
+    const bool lost = !(sum >= kLeast && sum <= kMost);  // chosen against the scores, or logits of 79 and more
+    if (__any_sync(0xffffffffu, lost)) {
+        float m = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) m = max_nan(m, z[j]);
+        m = token_max<LANES>(m);
+        if (lost) c = p.sigmoid ? min_nan(m, 0.0f) : m;
+        terms();
+        sum = token_sum<LANES>(sum);
+    }
+    const float one_sum = 1.0f / sum;
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+        e[j] *= one_sum;
+        dot = fmaf(e[j], dw[j], dot);
+    }
+    dot = token_sum<LANES>(dot);
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) add[j] = p.scale * r[j] * e[j] * (dw[j] - dot);
 }
 
 // LANES lanes a token; a block takes tokens [blockIdx.x chunk, + chunk), its
-// warps in turn.
+// warps in turn.  The next token's logits, choices and weights are on their way
+// while one is worked on.
 template <int LANES, int V, bool VEC, bool HALF>
-__global__ void __launch_bounds__(32 * kWarps) router_grad_kernel(const __grid_constant__ RouterGradArgs p) {
-    constexpr int kTokens = 32 / LANES * kWarps, kCols = 4 * V * LANES;
-    constexpr int KPL = LANES >= 32 ? 1 : LANES == 16 ? 2 : 4;
-    extern __shared__ float smem[];  // [kTokens][kCols]: what the choices add, zero between tokens
+__global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __grid_constant__ RouterGradArgs p) {
+    constexpr int kTokens = 32 / LANES * kGradWarps, kCols = 4 * V * LANES;
+    constexpr int KPL = choices_a_lane(LANES);
+    extern __shared__ __align__(16) float smem[];  // [kTokens][kCols]: what the choices add, zero between tokens
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int tid = threadIdx.x, lane = tid % LANES, slot = tid / LANES;
@@ -406,58 +520,99 @@ __global__ void __launch_bounds__(32 * kWarps) router_grad_kernel(const __grid_c
     for (int v = 0; v < V; ++v) reinterpret_cast<float4*>(mine)[v * LANES + lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
     const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.T);
+    const bool losses = p.dbalance || p.dz, direct = p.renorm || p.sigmoid;
+    float next[4 * V], next_dw[KPL], next_chosen[KPL];
+    int next_id[KPL];
+    auto load = [&](int t0) {
+        const int t = min(t0 + slot, hi - 1);
+        load_token<LANES, V, VEC>(p.logits + (int64_t)t * p.E, p.E, lane, next);
+        if (!p.dw) return;
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) {
+            const int i = lane + j * LANES;
+            next_id[j] = i < p.k ? __ldg(p.ids + (int64_t)t * p.k + i) : -1;
+            next_dw[j] = i < p.k ? __ldg(p.dw + (int64_t)t * p.k + i) : 0.0f;
+        }
+    };
+    // the chosen experts' logits, once the choices are there
+    auto load_chosen = [&](int t0) {
+        if (!p.dw) return;
+        const float* row = p.logits + (int64_t)min(t0 + slot, hi - 1) * p.E;
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) {
+            if (lane + j * LANES < p.k && (next_id[j] < 0 || next_id[j] >= p.E)) {
+                atomicOr(p.err, DERR_BAD_INDEX);
+                next_id[j] = -1;
+            }
+            if (next_id[j] < 0) next_dw[j] = 0.0f;
+            next_chosen[j] = next_id[j] >= 0 ? __ldg(row + next_id[j]) : -CUDART_INF_F;
+        }
+    };
+    int from = 0, to = 0;  // the tokens of the sequence at hand; none yet
+    float by_p = 0.0f, by_z = 0.0f;
+    float of_counts[V <= 2 ? 4 * V : 1];  // d loss / d p of its balance loss, where registers allow
+    const int32_t* counts = p.counts;
+    load(lo);
+    load_chosen(lo);
     for (int t0 = lo; t0 < hi; t0 += kTokens) {  // whole warps together
         const int t = min(t0 + slot, hi - 1);
         const bool in = t0 + slot < hi;
-        const float* row = p.logits + (int64_t)t * p.E;
-        float z[4 * V], e[4 * V], a[4 * V], g[4 * V] = {};
-        load_token<LANES, V, VEC>(row, p.E, lane, z);
-        int b = -1, tokens = 0;
-        if (p.dbalance || p.dz) {
-            b = p.offsets ? seq_of(p.offsets, p.n_seqs, t) : 0;
-            if (b >= 0) tokens = p.offsets ? min(p.offsets[b + 1], p.T) - max(p.offsets[b], 0) : p.T;
+        float z[4 * V], e[4 * V], r[4 * V], g[4 * V], dw[KPL], chosen_z[KPL];
+        int id[KPL];
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) z[i] = next[i];
+#pragma unroll
+        for (int j = 0; j < KPL; ++j) {
+            id[j] = next_id[j];
+            dw[j] = next_dw[j];
+            chosen_z[j] = next_chosen[j];
         }
-        const float per_token = b >= 0 ? 1.0f / (float)tokens : 0.0f;
-        // d loss / d p: the balance losses' part
-        float by_p = 0.0f;
-        if (p.dbalance && b >= 0) {
-            by_p = p.dbalance[b] * ((float)p.E / (float)p.k) * per_token * per_token;
+        const bool more = t0 + kTokens < hi;
+        if (more) load(t0 + kTokens);
+        if (losses && (t < from || t >= to)) {  // another sequence
+            const int b = p.offsets ? seq_of(p.offsets, p.n_seqs, t) : 0;
+            from = t;
+            to = t + 1;
+            by_p = by_z = 0.0f;
+            if (b >= 0) {
+                from = p.offsets ? max(p.offsets[b], 0) : 0;
+                to = p.offsets ? min(p.offsets[b + 1], p.T) : p.T;
+                const float per_token = 1.0f / (float)(to - from);
+                if (p.dbalance) by_p = p.dbalance[b] * ((float)p.E / (float)p.k) * per_token * per_token;
+                if (p.dz) by_z = 2.0f * p.dz[b] * per_token;
+                counts = p.counts + (int64_t)b * p.E;
+            }
+            if constexpr (V <= 2) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = 4 * (v * LANES + lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i < p.E) g[4 * v + i] = by_p * (float)__ldg(p.counts + (int64_t)b * p.E + c + i);
+                for (int i = 0; i < 4 * V; ++i) {
+                    const int c = 4 * (i / 4 * LANES + lane) + i % 4;
+                    of_counts[i] = by_p != 0.0f && c < p.E ? by_p * (float)__ldg(counts + c) : 0.0f;
+                }
             }
         }
-        float c = 0.0f, sum;
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) {
+            if constexpr (V <= 2) {
+                g[i] = losses ? of_counts[i] : 0.0f;
+            } else {
+                const int c = 4 * (i / 4 * LANES + lane) + i % 4;
+                g[i] = by_p != 0.0f && c < p.E ? by_p * (float)__ldg(counts + c) : 0.0f;
+            }
+        }
+        float c, sum, z_sum, z_c;
         if (p.sigmoid) {
-            sum = sigmoid_terms<LANES, V>(z, lane, p.E, a, e, c);
+            sum = sigmoid_terms<LANES, V>(z, e, r, c, p.dz != nullptr, z_sum, z_c);
         } else {
-            sum = soft_terms<LANES, V>(z, e, c);
+            z_sum = sum = soft_terms<LANES, V>(z, e, c);
+            z_c = c;
         }
         const float one_sum = 1.0f / sum;
-        // the chosen experts' weights
-        int id[KPL];
-        float dw[KPL];
-        bool direct_terms = false;
+        float d[4 * V];
         if (p.dw) {
-#pragma unroll
-            for (int j = 0; j < KPL; ++j) {
-                const int i = lane + j * LANES;
-                id[j] = i < p.k ? p.ids[(int64_t)t * p.k + i] : -1;
-                dw[j] = i < p.k ? p.dw[(int64_t)t * p.k + i] : 0.0f;
-                if (i < p.k && (id[j] < 0 || id[j] >= p.E)) {
-                    atomicOr(p.err, DERR_BAD_INDEX);
-                    id[j] = -1;
-                }
-                if (id[j] < 0) dw[j] = 0.0f;
-            }
-            direct_terms = p.renorm || p.sigmoid;
             float add[KPL];
-            if (direct_terms) {
-                choice_terms<LANES, KPL>(p, row, id, dw, c, add);
-            } else {
+            if (direct) {
+                choice_terms<LANES, KPL>(p, chosen_z, dw, c, add);
+            } else {  // softmax over all: through the shares, with the losses' part
 #pragma unroll
                 for (int j = 0; j < KPL; ++j) add[j] = p.scale * dw[j];
             }
@@ -465,54 +620,46 @@ __global__ void __launch_bounds__(32 * kWarps) router_grad_kernel(const __grid_c
             for (int j = 0; j < KPL; ++j)
                 if (id[j] >= 0) mine[id[j]] = add[j];
             __syncwarp();
-        }
-        float chosen[4 * V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float4 q = reinterpret_cast<const float4*>(mine)[v * LANES + lane];
-            chosen[4 * v] = q.x;
-            chosen[4 * v + 1] = q.y;
-            chosen[4 * v + 2] = q.z;
-            chosen[4 * v + 3] = q.w;
-        }
-        if (p.dw) {
+            for (int v = 0; v < V; ++v) {
+                const float4 q = reinterpret_cast<const float4*>(mine)[v * LANES + lane];
+                d[4 * v] = q.x;
+                d[4 * v + 1] = q.y;
+                d[4 * v + 2] = q.z;
+                d[4 * v + 3] = q.w;
+            }
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < KPL; ++j)
                 if (id[j] >= 0) mine[id[j]] = 0.0f;
+            __syncwarp();
+            if (!direct) {
+#pragma unroll
+                for (int i = 0; i < 4 * V; ++i) {
+                    g[i] += d[i];
+                    d[i] = 0.0f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * V; ++i) d[i] = 0.0f;
         }
-        // softmax over all: the weights' gradients go through the shares too
-        if (!direct_terms) {
+        if (more) load_chosen(t0 + kTokens);
+        if (p.dbalance || !direct) {
+            float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
-                g[i] += chosen[i];
-                chosen[i] = 0.0f;
+                e[i] *= one_sum;
+                dot = fmaf(e[i], g[i], dot);
             }
-        }
-        float dot = 0.0f;
+            dot = token_sum<LANES>(dot);
 #pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-            e[i] *= one_sum;
-            dot = fmaf(e[i], g[i], dot);
-        }
-        dot = token_sum<LANES>(dot);
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-            float d = e[i] * (g[i] - dot);
-            if (p.sigmoid) d *= a[i] * (e[i] * sum);  // 1 - s
-            chosen[i] += d;
+            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(p.sigmoid ? e[i] * r[i] : e[i], g[i] - dot, d[i]);
         }
         if (p.dz) {
-            if (p.sigmoid) {
-                sum = soft_terms<LANES, V>(z, e, c);
+            const float by = by_z * log_of(z_sum, z_c), one_z = 1.0f / z_sum;
 #pragma unroll
-                for (int i = 0; i < 4 * V; ++i) e[i] *= 1.0f / sum;
-            }
-            if (b >= 0) {
-                const float by = 2.0f * p.dz[b] * per_token * log_of(sum, c);
-#pragma unroll
-                for (int i = 0; i < 4 * V; ++i) chosen[i] = fmaf(by, e[i], chosen[i]);
-            }
+            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(by, exp_fast(z[i] - z_c) * one_z, d[i]);
         }
         if (in) {
 #pragma unroll
@@ -520,16 +667,15 @@ __global__ void __launch_bounds__(32 * kWarps) router_grad_kernel(const __grid_c
                 const int col = 4 * (v * LANES + lane);
                 const int64_t at = (int64_t)t * p.E + col;
                 if constexpr (VEC) {
-                    if (col < p.E)
-                        store4<HALF>(p.dlogits, at, chosen[4 * v], chosen[4 * v + 1], chosen[4 * v + 2], chosen[4 * v + 3]);
+                    if (col < p.E) store4<HALF>(p.dlogits, at, d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (col + i >= p.E) continue;
                         if constexpr (HALF)
-                            static_cast<__nv_bfloat16*>(p.dlogits)[at + i] = __float2bfloat16_rn(chosen[4 * v + i]);
+                            static_cast<__nv_bfloat16*>(p.dlogits)[at + i] = __float2bfloat16_rn(d[4 * v + i]);
                         else
-                            static_cast<float*>(p.dlogits)[at + i] = chosen[4 * v + i];
+                            static_cast<float*>(p.dlogits)[at + i] = d[4 * v + i];
                     }
                 }
             }
@@ -539,7 +685,8 @@ __global__ void __launch_bounds__(32 * kWarps) router_grad_kernel(const __grid_c
 
 template <int L, int N, bool W>
 struct Form {
-    static constexpr int LANES = L, V = N, kCols = 4 * V * LANES, kTokens = 32 / LANES * kWarps;
+    static constexpr int LANES = L, V = N, kCols = 4 * V * LANES, kTokens = 32 / LANES * kWarps,
+                         kGradTokens = 32 / LANES * kGradWarps;
     static constexpr bool VEC = W;
 };
 
@@ -556,11 +703,13 @@ cudaError_t by_experts(int E, F f) {
     return vec ? f(Form<32, 8, true>()) : f(Form<32, 8, false>());
 }
 
-// Tokens of a block of the losses' kernel: few enough to give every SM of a
-// GB300 (152) a block, whole rounds of the block's warps, 16 rounds at most.
+// Few tokens: one kernel of a cluster a sequence.
+bool balance_is_few(int64_t T, int n_seqs) { return T <= 4096 && n_seqs <= 4096; }
+// Tokens of a block of the losses' kernel: two blocks an SM of a GB300's 152,
+// whole rounds of a block's warps.
 int balance_chunk(int64_t T, int E) {
     const int at_once = kWarps * std::max(1, 32 / std::max(4, (E + 3) / 4));
-    const int64_t want = (T + 152 * 4 - 1) / (152 * 4);
+    const int64_t want = (T + 152 * 2 - 1) / (152 * 2);
     return (int)std::max<int64_t>(at_once, (want + at_once - 1) / at_once * at_once);
 }
 
@@ -589,28 +738,38 @@ cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s) {
     p.part_p = reinterpret_cast<float*>(base + L.p);
     p.part_counts = reinterpret_cast<int32_t*>(base + L.counts);
     p.part_z = reinterpret_cast<float*>(base + L.z);
-    if (p.T > 0) {
-        const cudaError_t e = by_experts(p.E, [&](auto form) {
+    if (balance_is_few(p.T, p.n_seqs))
+        return by_experts(p.E, [&](auto form) {
             using F = decltype(form);
-            return launch_dependent(balance_kernel<F::LANES, F::V, F::VEC>, p, dim3((unsigned)L.blocks), 32 * kWarps,
-                                    (F::kTokens + 1) * F::kCols * sizeof(float), s);
+            const auto kernel = balance_few_kernel<F::LANES, F::V, F::VEC>;
+            const size_t smem = (F::kTokens + 2) * F::kCols * sizeof(float);
+            cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                              : cudaSuccess;
+            return e != cudaSuccess ? e : launch_dependent(kernel, p, dim3((unsigned)p.n_seqs * kFewBlocks), 32 * kWarps, smem, s);
         });
-        if (e != cudaSuccess) return e;
-    }
-    return launch_dependent(balance_finish_kernel, p, dim3((unsigned)p.n_seqs), 1024, 0, s);
+    const cudaError_t e = by_experts(p.E, [&](auto form) {
+        using F = decltype(form);
+        const auto kernel = balance_kernel<F::LANES, F::V, F::VEC>;
+        const size_t smem = (F::kTokens + 1) * F::kCols * sizeof(float);
+        cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                          : cudaSuccess;
+        return e != cudaSuccess ? e : launch_dependent(kernel, p, dim3((unsigned)L.blocks), 32 * kWarps, smem, s);
+    });
+    return e != cudaSuccess ? e : launch_dependent(balance_finish_kernel, p, dim3((unsigned)p.n_seqs), 1024, 0, s);
 }
 
 cudaError_t launch_router_grad(RouterGradArgs& p, cudaStream_t s) {
     if (p.T <= 0) return cudaSuccess;
     return by_experts(p.E, [&](auto form) {
         using F = decltype(form);
-        const int64_t want = (p.T + 152 * 8 - 1) / (152 * 8);
-        p.chunk = (int)std::max<int64_t>(F::kTokens, (want + F::kTokens - 1) / F::kTokens * F::kTokens);
+        // four blocks an SM, whole rounds of their warps
+        const int64_t want = (p.T + 152 * 4 - 1) / (152 * 4);
+        p.chunk = (int)std::max<int64_t>(F::kGradTokens, (want + F::kGradTokens - 1) / F::kGradTokens * F::kGradTokens);
         const dim3 grid((unsigned)((p.T + p.chunk - 1) / p.chunk));
-        const size_t smem = F::kTokens * F::kCols * sizeof(float);
+        const size_t smem = F::kGradTokens * F::kCols * sizeof(float);
         if (p.half)
-            return launch_dependent(router_grad_kernel<F::LANES, F::V, F::VEC, true>, p, grid, 32 * kWarps, smem, s);
-        return launch_dependent(router_grad_kernel<F::LANES, F::V, F::VEC, false>, p, grid, 32 * kWarps, smem, s);
+            return launch_dependent(router_grad_kernel<F::LANES, F::V, F::VEC, true>, p, grid, 32 * kGradWarps, smem, s);
+        return launch_dependent(router_grad_kernel<F::LANES, F::V, F::VEC, false>, p, grid, 32 * kGradWarps, smem, s);
     });
 }
 
