@@ -27,7 +27,8 @@ constexpr int kWarps = 16, kGradWarps = 8;  // of a block: the losses', the grad
 // A token's choices in each of its lanes, for the most that E experts can have.
 __host__ __device__ constexpr int choices_a_lane(int lanes) { return lanes >= 32 ? 1 : lanes == 16 ? 2 : 4; }
 constexpr float kLeast = 1e-20f, kMost = 1e34f;
-constexpr float kTop = 88.0f;  // exp(88) is 1.7e38; from 79 on a sum is beyond kMost
+// exp(kTop) is 2^125.99, so that its reciprocal is no subnormal; from 79 on a sum is beyond kMost
+constexpr float kTop = 87.33f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -37,13 +38,19 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 }
 
 // exp by the approximate power of two: its argument's rounding makes the
-// relative error |x| 2^-23 or 2^-22, whichever is more.
-__device__ __forceinline__ float exp_fast(float x) {
+// relative error |x| 2^-23 or 2^-22, whichever is more; 0 below 2^-126.
+__device__ __forceinline__ float exp2_fast(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x * kLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
+// 1 / x, 0 below 2^-126.
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * kLog2e); }
 // Sums and maxima over the LANES lanes of a token.
 template <int LANES>
 __device__ __forceinline__ float token_sum(float v) {
@@ -58,15 +65,18 @@ __device__ __forceinline__ float token_max(float v) {
     return v;
 }
 
+// How rows lie: any E; a multiple of 4 (16-byte aligned rows); every column of
+// every lane there.
+enum Rows : int { ROWS_ANY, ROWS_VEC, ROWS_FULL };
+
 // A lane's logits of one token: columns 4 (v LANES + lane) .. + 3, -inf beyond E.
-// VEC: E is a multiple of 4, so rows are 16-byte aligned.
-template <int LANES, int V, bool VEC>
+template <int LANES, int V, int ROWS>
 __device__ __forceinline__ void load_token(const float* row, int E, int lane, float (&z)[4 * V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = 4 * (v * LANES + lane);
-        if constexpr (VEC) {
-            const float4 q = c < E ? __ldg(reinterpret_cast<const float4*>(row + c))
+        if constexpr (ROWS != ROWS_ANY) {
+            const float4 q = ROWS == ROWS_FULL || c < E ? __ldg(reinterpret_cast<const float4*>(row + c))
                                    : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
             z[4 * v] = q.x;
             z[4 * v + 1] = q.y;
@@ -82,8 +92,8 @@ __device__ __forceinline__ void load_token(const float* row, int E, int lane, fl
 // A token's exp(z - c) and their sum.
 template <int LANES, int V>
 __device__ __forceinline__ float soft_terms(const float (&z)[4 * V], float (&e)[4 * V], float& c) {
-    c = 0.0f;
     float sum = 0.0f;
+    c = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) {
         e[i] = exp_fast(z[i]);
@@ -97,13 +107,14 @@ __device__ __forceinline__ float soft_terms(const float (&z)[4 * V], float (&e)[
         for (int i = 0; i < 4 * V; ++i) m = max_nan(m, z[i]);
         m = token_max<LANES>(m);
         if (lost) c = m;
-        float again = 0.0f;
+        // from the difference itself: of large logits, their product with
+        // kLog2e alone would be off by more than 1
 #pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-            e[i] = exp_fast(z[i] - c);
-            again += e[i];
-        }
-        sum = token_sum<LANES>(again);
+        for (int i = 0; i < 4 * V; ++i) e[i] = exp_fast(z[i] - c);
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) sum += e[i];
+        sum = token_sum<LANES>(sum);
     }
     return sum;
 }
@@ -114,13 +125,14 @@ template <int LANES, int V>
 __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&u)[4 * V], float (&r)[4 * V], float& c,
                                                bool want_z, float& z_sum, float& z_c) {
     c = 0.0f;
-    float sum, one = 1.0f;
-    auto terms = [&]() {
+    float sum;
+    // far: relative to c, from the difference itself (as in soft_terms)
+    auto terms = [&](bool far, float one) {
         sum = z_sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
-            const float t = exp_fast(min_nan(z[i] - c, kTop));
-            r[i] = rcp(fmaf(t, one, 1.0f));
+            const float t = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp2_fast(min_nan(z[i] * kLog2e, kTop * kLog2e));
+            r[i] = rcp_fast(far ? fmaf(t, one, 1.0f) : t + 1.0f);
             u[i] = t * r[i];
             sum += u[i];
             z_sum += t;
@@ -128,7 +140,7 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         sum = token_sum<LANES>(sum);
         if (want_z) z_sum = token_sum<LANES>(z_sum);
     };
-    terms();
+    terms(false, 1.0f);
     const bool lost = !(sum >= kLeast);
     if (__any_sync(0xffffffffu, lost)) {
         float m = -CUDART_INF_F;
@@ -136,8 +148,7 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         for (int i = 0; i < 4 * V; ++i) m = max_nan(m, z[i]);
         m = token_max<LANES>(m);
         if (lost) c = min_nan(m, 0.0f);
-        one = exp_fast(c);
-        terms();
+        terms(true, exp_fast(c));
     }
     z_c = c;
     if (want_z && __any_sync(0xffffffffu, !(z_sum <= kMost))) {  // logits of 79 and more
@@ -210,7 +221,7 @@ struct TokenSums {
 // its first LANES lanes, the next tokens for the others), and counts their
 // choices in hist.  The next token's logits and choices are on their way while
 // one is worked on.
-template <int LANES, int V, bool VEC>
+template <int LANES, int V, int ROWS>
 __device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int to, int step, int* hist, TokenSums<V>& sums) {
     constexpr int KPL = choices_a_lane(LANES);
     const int lane = threadIdx.x % LANES, sub = (threadIdx.x & 31) / LANES;
@@ -218,7 +229,7 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int 
     int next_id[KPL];
     auto load = [&](int t0) {  // a token of the warp at least is there
         const int t = min(t0 + sub, to - 1);
-        load_token<LANES, V, VEC>(p.logits + (int64_t)t * p.E, p.E, lane, next);
+        load_token<LANES, V, ROWS>(p.logits + (int64_t)t * p.E, p.E, lane, next);
 #pragma unroll
         for (int j = 0; j < KPL; ++j) next_id[j] = lane + j * LANES < p.k ? __ldg(p.ids + (int64_t)t * p.k + lane + j * LANES) : 0;
     };
@@ -248,10 +259,10 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int 
             z_sum = sum = soft_terms<LANES, V>(z, e, c);
             z_c = c;
         }
-        const float f = 1.0f / sum;
-        if (in) {
+        const float f = in ? rcp_fast(sum) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4 * V; ++i) sums.p[i] = fmaf(e[i], f, sums.p[i]);
+        for (int i = 0; i < 4 * V; ++i) sums.p[i] = fmaf(e[i], f, sums.p[i]);
+        if (in) {
             if (p.z) {
                 const float l = log_of(z_sum, z_c);
                 sums.z = fmaf(l, l, sums.z);
@@ -283,7 +294,7 @@ __device__ __forceinline__ float total_p(const float* rows, int e) {
 // Many tokens: a block takes tokens [blockIdx.x chunk, + chunk), sequence by
 // sequence.  A sequence whose tokens are all here is finished here; one that
 // began before leaves its sums in slot 0, one that goes on in slot 1.
-template <int LANES, int V, bool VEC>
+template <int LANES, int V, int ROWS>
 __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_constant__ BalanceArgs p) {
     extern __shared__ __align__(16) float smem[];
     constexpr int kTokens = 32 / LANES * kWarps;  // at once
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
         for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
         TokenSums<V> sums{};
-        add_tokens<LANES, V, VEC>(p, from + warp * (32 / LANES), to, kTokens, hist, sums);
+        add_tokens<LANES, V, ROWS>(p, from + warp * (32 / LANES), to, kTokens, hist, sums);
         leave<LANES, V>(sums, rows, z_rows);
         __syncthreads();
         float z_all = 0.0f;
@@ -338,7 +349,7 @@ __device__ __forceinline__ uint32_t from_rank(const void* own, int rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
-template <int LANES, int V, bool VEC>
+template <int LANES, int V, int ROWS>
 __global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps)
     balance_few_kernel(const __grid_constant__ BalanceArgs p) {
     extern __shared__ __align__(16) float smem[];
@@ -354,7 +365,7 @@ __global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps
     for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
     TokenSums<V> sums{};
-    add_tokens<LANES, V, VEC>(p, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
+    add_tokens<LANES, V, ROWS>(p, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
     leave<LANES, V>(sums, rows, z_rows);
     __syncthreads();
     for (int e = tid; e < p.E; e += blockDim.x) total[e] = total_p<kTokens, kCols>(rows, e);
@@ -444,9 +455,8 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
 
 // ------------------------------------------------------------ gradients --
 
-template <bool HALF>
-__device__ __forceinline__ void store4(void* out, int64_t at, float a, float b, float c, float d) {
-    if constexpr (HALF) {
+__device__ __forceinline__ void store4(void* out, bool half, int64_t at, float a, float b, float c, float d) {
+    if (half) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
         uint2 q;
         q.x = *reinterpret_cast<const uint32_t*>(&lo);
@@ -460,17 +470,17 @@ __device__ __forceinline__ void store4(void* out, int64_t at, float a, float b, 
 // What the gradients of a token's chosen weights add to the chosen logits: lane
 // holds choices lane, lane + LANES, ... (KPL of them): z, their logits (-inf
 // where there is none), dw.  c: the token's own (soft_terms, sigmoid_terms).
-template <int LANES, int KPL>
+template <int LANES, int KPL, bool SIGMOID>
 __device__ __forceinline__ void choice_terms(const RouterGradArgs& p, const float (&z)[KPL], const float (&dw)[KPL], float c,
                                              float (&add)[KPL]) {
     float e[KPL], r[KPL], sum, one;
     auto terms = [&]() {
-        one = p.sigmoid ? exp_fast(c) : 0.0f;  // softmax: r = 1
+        one = SIGMOID ? exp_fast(c) : 0.0f;  // softmax: r = 1
         sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
             e[j] = exp_fast(min_nan(z[j] - c, kTop));
-            r[j] = rcp(fmaf(e[j], one, 1.0f));  // 1 - s
+            r[j] = SIGMOID ? rcp_fast(fmaf(e[j], one, 1.0f)) : 1.0f;  // 1 - s
             e[j] *= r[j];                        // exp(-c) s
             sum += e[j];
         }
@@ -488,11 +498,11 @@ __device__ __forceinline__ void choice_terms(const RouterGradArgs& p, const floa
 #pragma unroll
         for (int j = 0; j < KPL; ++j) m = max_nan(m, z[j]);
         m = token_max<LANES>(m);
-        if (lost) c = p.sigmoid ? min_nan(m, 0.0f) : m;
+        if (lost) c = SIGMOID ? min_nan(m, 0.0f) : m;
         terms();
         sum = token_sum<LANES>(sum);
     }
-    const float one_sum = 1.0f / sum;
+    const float one_sum = rcp_fast(sum);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < KPL; ++j) {
@@ -507,8 +517,8 @@ __device__ __forceinline__ void choice_terms(const RouterGradArgs& p, const floa
 // LANES lanes a token; a block takes tokens [blockIdx.x chunk, + chunk), its
 // warps in turn.  The next token's logits, choices and weights are on their way
 // while one is worked on.
-template <int LANES, int V, bool VEC, bool HALF>
-__global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __grid_constant__ RouterGradArgs p) {
+template <int LANES, int V, int ROWS, bool SIGMOID>
+__global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_kernel(const __grid_constant__ RouterGradArgs p) {
     constexpr int kTokens = 32 / LANES * kGradWarps, kCols = 4 * V * LANES;
     constexpr int KPL = choices_a_lane(LANES);
     extern __shared__ __align__(16) float smem[];  // [kTokens][kCols]: what the choices add, zero between tokens
@@ -520,12 +530,12 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __gr
     for (int v = 0; v < V; ++v) reinterpret_cast<float4*>(mine)[v * LANES + lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
     const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.T);
-    const bool losses = p.dbalance || p.dz, direct = p.renorm || p.sigmoid;
+    const bool losses = p.dbalance || p.dz, direct = p.renorm || SIGMOID;
     float next[4 * V], next_dw[KPL], next_chosen[KPL];
     int next_id[KPL];
     auto load = [&](int t0) {
         const int t = min(t0 + slot, hi - 1);
-        load_token<LANES, V, VEC>(p.logits + (int64_t)t * p.E, p.E, lane, next);
+        load_token<LANES, V, ROWS>(p.logits + (int64_t)t * p.E, p.E, lane, next);
         if (!p.dw) return;
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
@@ -550,7 +560,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __gr
     };
     int from = 0, to = 0;  // the tokens of the sequence at hand; none yet
     float by_p = 0.0f, by_z = 0.0f;
-    float of_counts[V <= 2 ? 4 * V : 1];  // d loss / d p of its balance loss, where registers allow
+    float of_counts[V <= 2 ? 4 * V : 1] = {};  // d loss / d p of its balance loss, where registers allow
     const int32_t* counts = p.counts;
     load(lo);
     load_chosen(lo);
@@ -593,25 +603,25 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __gr
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
             if constexpr (V <= 2) {
-                g[i] = losses ? of_counts[i] : 0.0f;
+                g[i] = of_counts[i];
             } else {
                 const int c = 4 * (i / 4 * LANES + lane) + i % 4;
                 g[i] = by_p != 0.0f && c < p.E ? by_p * (float)__ldg(counts + c) : 0.0f;
             }
         }
         float c, sum, z_sum, z_c;
-        if (p.sigmoid) {
+        if constexpr (SIGMOID) {
             sum = sigmoid_terms<LANES, V>(z, e, r, c, p.dz != nullptr, z_sum, z_c);
         } else {
             z_sum = sum = soft_terms<LANES, V>(z, e, c);
             z_c = c;
         }
-        const float one_sum = 1.0f / sum;
+        const float one_sum = rcp_fast(sum);
         float d[4 * V];
         if (p.dw) {
             float add[KPL];
             if (direct) {
-                choice_terms<LANES, KPL>(p, chosen_z, dw, c, add);
+                choice_terms<LANES, KPL, SIGMOID>(p, chosen_z, dw, c, add);
             } else {  // softmax over all: through the shares, with the losses' part
 #pragma unroll
                 for (int j = 0; j < KPL; ++j) add[j] = p.scale * dw[j];
@@ -654,10 +664,10 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __gr
             }
             dot = token_sum<LANES>(dot);
 #pragma unroll
-            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(p.sigmoid ? e[i] * r[i] : e[i], g[i] - dot, d[i]);
+            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(SIGMOID ? e[i] * r[i] : e[i], g[i] - dot, d[i]);
         }
         if (p.dz) {
-            const float by = by_z * log_of(z_sum, z_c), one_z = 1.0f / z_sum;
+            const float by = by_z * log_of(z_sum, z_c), one_z = rcp_fast(z_sum);
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(by, exp_fast(z[i] - z_c) * one_z, d[i]);
         }
@@ -666,13 +676,14 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __gr
             for (int v = 0; v < V; ++v) {
                 const int col = 4 * (v * LANES + lane);
                 const int64_t at = (int64_t)t * p.E + col;
-                if constexpr (VEC) {
-                    if (col < p.E) store4<HALF>(p.dlogits, at, d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
+                if constexpr (ROWS != ROWS_ANY) {
+                    if (ROWS == ROWS_FULL || col < p.E)
+                        store4(p.dlogits, p.half, at, d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (col + i >= p.E) continue;
-                        if constexpr (HALF)
+                        if (p.half)
                             static_cast<__nv_bfloat16*>(p.dlogits)[at + i] = __float2bfloat16_rn(d[4 * v + i]);
                         else
                             static_cast<float*>(p.dlogits)[at + i] = d[4 * v + i];
@@ -683,24 +694,27 @@ __global__ void __launch_bounds__(32 * kGradWarps) router_grad_kernel(const __gr
     }
 }
 
-template <int L, int N, bool W>
+template <int L, int N, int W>
 struct Form {
     static constexpr int LANES = L, V = N, kCols = 4 * V * LANES, kTokens = 32 / LANES * kWarps,
                          kGradTokens = 32 / LANES * kGradWarps;
-    static constexpr bool VEC = W;
+    static constexpr int ROWS = W;
 };
 
+template <int L, int V, class F>
+cudaError_t by_rows(int E, F f) {
+    return E == 4 * V * L ? f(Form<L, V, ROWS_FULL>()) : E % 4 == 0 ? f(Form<L, V, ROWS_VEC>()) : f(Form<L, V, ROWS_ANY>());
+}
 // f(Form) for E experts.
 template <class F>
 cudaError_t by_experts(int E, F f) {
-    const bool vec = E % 4 == 0;
-    if (E <= 16) return vec ? f(Form<4, 1, true>()) : f(Form<4, 1, false>());
-    if (E <= 32) return vec ? f(Form<8, 1, true>()) : f(Form<8, 1, false>());
-    if (E <= 64) return vec ? f(Form<16, 1, true>()) : f(Form<16, 1, false>());
-    if (E <= 128) return vec ? f(Form<32, 1, true>()) : f(Form<32, 1, false>());
-    if (E <= 256) return vec ? f(Form<32, 2, true>()) : f(Form<32, 2, false>());
-    if (E <= 512) return vec ? f(Form<32, 4, true>()) : f(Form<32, 4, false>());
-    return vec ? f(Form<32, 8, true>()) : f(Form<32, 8, false>());
+    if (E <= 16) return by_rows<4, 1>(E, f);
+    if (E <= 32) return by_rows<8, 1>(E, f);
+    if (E <= 64) return by_rows<16, 1>(E, f);
+    if (E <= 128) return by_rows<32, 1>(E, f);
+    if (E <= 256) return by_rows<32, 2>(E, f);
+    if (E <= 512) return by_rows<32, 4>(E, f);
+    return by_rows<32, 8>(E, f);
 }
 
 // Few tokens: one kernel of a cluster a sequence.
@@ -741,7 +755,7 @@ cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s) {
     if (balance_is_few(p.T, p.n_seqs))
         return by_experts(p.E, [&](auto form) {
             using F = decltype(form);
-            const auto kernel = balance_few_kernel<F::LANES, F::V, F::VEC>;
+            const auto kernel = balance_few_kernel<F::LANES, F::V, F::ROWS>;
             const size_t smem = (F::kTokens + 2) * F::kCols * sizeof(float);
             cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                               : cudaSuccess;
@@ -749,7 +763,7 @@ cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s) {
         });
     const cudaError_t e = by_experts(p.E, [&](auto form) {
         using F = decltype(form);
-        const auto kernel = balance_kernel<F::LANES, F::V, F::VEC>;
+        const auto kernel = balance_kernel<F::LANES, F::V, F::ROWS>;
         const size_t smem = (F::kTokens + 1) * F::kCols * sizeof(float);
         cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                           : cudaSuccess;
@@ -767,9 +781,9 @@ cudaError_t launch_router_grad(RouterGradArgs& p, cudaStream_t s) {
         p.chunk = (int)std::max<int64_t>(F::kGradTokens, (want + F::kGradTokens - 1) / F::kGradTokens * F::kGradTokens);
         const dim3 grid((unsigned)((p.T + p.chunk - 1) / p.chunk));
         const size_t smem = F::kGradTokens * F::kCols * sizeof(float);
-        if (p.half)
-            return launch_dependent(router_grad_kernel<F::LANES, F::V, F::VEC, true>, p, grid, 32 * kGradWarps, smem, s);
-        return launch_dependent(router_grad_kernel<F::LANES, F::V, F::VEC, false>, p, grid, 32 * kGradWarps, smem, s);
+        if (p.sigmoid)
+            return launch_dependent(router_grad_kernel<F::LANES, F::V, F::ROWS, true>, p, grid, 32 * kGradWarps, smem, s);
+        return launch_dependent(router_grad_kernel<F::LANES, F::V, F::ROWS, false>, p, grid, 32 * kGradWarps, smem, s);
     });
 }
 
