@@ -65,6 +65,22 @@ __device__ __forceinline__ float token_max(float v) {
     return v;
 }
 
+// Four sums over the LANES lanes of a token: halves, then quarters of the lanes
+// go on with some of the values each, and everybody gets all at the end.
+template <int LANES>
+__device__ __forceinline__ float4 token_sums(float a, float b, float c, float d) {
+    constexpr uint32_t all = 0xffffffffu;
+    const int lane = threadIdx.x % LANES;
+    const bool upper = lane & (LANES / 2), odd = lane & (LANES / 4);
+    const float u = (upper ? c : a) + __shfl_xor_sync(all, upper ? a : c, LANES / 2);
+    const float v = (upper ? d : b) + __shfl_xor_sync(all, upper ? b : d, LANES / 2);
+    float s = (odd ? v : u) + __shfl_xor_sync(all, odd ? u : v, LANES / 4);
+#pragma unroll
+    for (int o = LANES / 8; o > 0; o >>= 1) s += __shfl_xor_sync(all, s, o);
+    return make_float4(__shfl_sync(all, s, 0, LANES), __shfl_sync(all, s, LANES / 4, LANES),
+                       __shfl_sync(all, s, LANES / 2, LANES), __shfl_sync(all, s, 3 * LANES / 4, LANES));
+}
+
 // How rows lie: any E; a multiple of 4 (16-byte aligned rows); every column of
 // every lane there.
 enum Rows : int { ROWS_ANY, ROWS_VEC, ROWS_FULL };
@@ -467,53 +483,6 @@ __device__ __forceinline__ void store4(void* out, bool half, int64_t at, float a
     }
 }
 
-// What the gradients of a token's chosen weights add to the chosen logits: lane
-// holds choices lane, lane + LANES, ... (KPL of them): z, their logits (-inf
-// where there is none), dw.  c: the token's own (soft_terms, sigmoid_terms).
-template <int LANES, int KPL, bool SIGMOID>
-__device__ __forceinline__ void choice_terms(const RouterGradArgs& p, const float (&z)[KPL], const float (&dw)[KPL], float c,
-                                             float (&add)[KPL]) {
-    float e[KPL], r[KPL], sum, one;
-    auto terms = [&]() {
-        one = SIGMOID ? exp_fast(c) : 0.0f;  // softmax: r = 1
-        sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            e[j] = exp_fast(min_nan(z[j] - c, kTop));
-            r[j] = SIGMOID ? rcp_fast(fmaf(e[j], one, 1.0f)) : 1.0f;  // 1 - s
-            e[j] *= r[j];                        // exp(-c) s
-            sum += e[j];
-        }
-    };
-    terms();
-    if (!p.renorm) {  // sigmoid, each on its own
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) add[j] = p.scale * r[j] * e[j] * one * dw[j];
-        return;
-    }
-    sum = token_sum<LANES>(sum);
-    const bool lost = !(sum >= kLeast && sum <= kMost);  // chosen against the scores, or logits of 79 and more
-    if (__any_sync(0xffffffffu, lost)) {
-        float m = -CUDART_INF_F;
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) m = max_nan(m, z[j]);
-        m = token_max<LANES>(m);
-        if (lost) c = SIGMOID ? min_nan(m, 0.0f) : m;
-        terms();
-        sum = token_sum<LANES>(sum);
-    }
-    const float one_sum = rcp_fast(sum);
-    float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) {
-        e[j] *= one_sum;
-        dot = fmaf(e[j], dw[j], dot);
-    }
-    dot = token_sum<LANES>(dot);
-#pragma unroll
-    for (int j = 0; j < KPL; ++j) add[j] = p.scale * r[j] * e[j] * (dw[j] - dot);
-}
-
 // LANES lanes a token; a block takes tokens [blockIdx.x chunk, + chunk), its
 // warps in turn.  The next token's logits, choices and weights are on their way
 // while one is worked on.
@@ -567,16 +536,35 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
     for (int t0 = lo; t0 < hi; t0 += kTokens) {  // whole warps together
         const int t = min(t0 + slot, hi - 1);
         const bool in = t0 + slot < hi;
-        float z[4 * V], e[4 * V], r[4 * V], g[4 * V], dw[KPL], chosen_z[KPL];
+        float z[4 * V], e[4 * V], r[4 * V], g[4 * V], d[4 * V], dw[KPL], chosen_z[KPL];
         int id[KPL];
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) z[i] = next[i];
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
-            id[j] = next_id[j];
-            dw[j] = next_dw[j];
-            chosen_z[j] = next_chosen[j];
+            id[j] = p.dw ? next_id[j] : -1;
+            dw[j] = p.dw ? next_dw[j] : 0.0f;
+            chosen_z[j] = p.dw ? next_chosen[j] : 0.0f;
         }
+        // what the choices have left in shared memory; then none of it is there
+        auto gather = [&](float (&v)[4 * V]) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float4 q = reinterpret_cast<const float4*>(mine)[i * LANES + lane];
+                v[4 * i] = q.x;
+                v[4 * i + 1] = q.y;
+                v[4 * i + 2] = q.z;
+                v[4 * i + 3] = q.w;
+            }
+            __syncwarp();
+        };
+        auto clear = [&]() {
+#pragma unroll
+            for (int j = 0; j < KPL; ++j)
+                if (id[j] >= 0) mine[id[j]] = 0.0f;
+            __syncwarp();
+        };
         const bool more = t0 + kTokens < hi;
         if (more) load(t0 + kTokens);
         if (losses && (t < from || t >= to)) {  // another sequence
@@ -609,64 +597,91 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
                 g[i] = by_p != 0.0f && c < p.E ? by_p * (float)__ldg(counts + c) : 0.0f;
             }
         }
-        float c, sum, z_sum, z_c;
-        if constexpr (SIGMOID) {
-            sum = sigmoid_terms<LANES, V>(z, e, r, c, p.dz != nullptr, z_sum, z_c);
-        } else {
-            z_sum = sum = soft_terms<LANES, V>(z, e, c);
-            z_c = c;
+        // softmax over all: the weights' gradients go through the shares, with the losses' part
+        if (p.dw && !direct) {
+#pragma unroll
+            for (int j = 0; j < KPL; ++j)
+                if (id[j] >= 0) mine[id[j]] = p.scale * dw[j];
+            gather(d);
+#pragma unroll
+            for (int i = 0; i < 4 * V; ++i) g[i] += d[i];
+            clear();
         }
-        const float one_sum = rcp_fast(sum);
-        float d[4 * V];
-        if (p.dw) {
-            float add[KPL];
-            if (direct) {
-                choice_terms<LANES, KPL, SIGMOID>(p, chosen_z, dw, c, add);
-            } else {  // softmax over all: through the shares, with the losses' part
+        // u = exp(-c) s and r = 1 - s (softmax: 1) of every expert and of the
+        // chosen ones, and all sums at once: of u, u g, and the chosen ones' u, u dw
+        float c = 0.0f, chosen_c = 0.0f, chosen_u[KPL], chosen_r[KPL], z_sum, chosen_one;
+        float4 sums;
+        auto terms = [&](bool far) {
+            const float one = far && SIGMOID ? exp_fast(c) : 1.0f;
+            chosen_one = far && SIGMOID ? exp_fast(chosen_c) : 1.0f;
+            float a = 0.0f, b = 0.0f, chosen_a = 0.0f, chosen_b = 0.0f;
+            z_sum = 0.0f;
 #pragma unroll
-                for (int j = 0; j < KPL; ++j) add[j] = p.scale * dw[j];
-            }
-#pragma unroll
-            for (int j = 0; j < KPL; ++j)
-                if (id[j] >= 0) mine[id[j]] = add[j];
-            __syncwarp();
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float4 q = reinterpret_cast<const float4*>(mine)[v * LANES + lane];
-                d[4 * v] = q.x;
-                d[4 * v + 1] = q.y;
-                d[4 * v + 2] = q.z;
-                d[4 * v + 3] = q.w;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < KPL; ++j)
-                if (id[j] >= 0) mine[id[j]] = 0.0f;
-            __syncwarp();
-            if (!direct) {
-#pragma unroll
-                for (int i = 0; i < 4 * V; ++i) {
-                    g[i] += d[i];
-                    d[i] = 0.0f;
+            for (int i = 0; i < 4 * V; ++i) {
+                e[i] = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp2_fast(min_nan(z[i] * kLog2e, kTop * kLog2e));
+                z_sum += e[i];
+                if constexpr (SIGMOID) {
+                    r[i] = rcp_fast(far ? fmaf(e[i], one, 1.0f) : e[i] + 1.0f);
+                    e[i] *= r[i];
                 }
+                a += e[i];
+                b = fmaf(e[i], g[i], b);
             }
+#pragma unroll
+            for (int j = 0; j < KPL; ++j) {
+                chosen_u[j] = exp_fast(min_nan(chosen_z[j] - chosen_c, kTop));
+                if constexpr (SIGMOID) {
+                    chosen_r[j] = rcp_fast(fmaf(chosen_u[j], chosen_one, 1.0f));
+                    chosen_u[j] *= chosen_r[j];
+                }
+                chosen_a += chosen_u[j];
+                chosen_b = fmaf(chosen_u[j], dw[j], chosen_b);
+            }
+            sums = token_sums<LANES>(a, b, chosen_a, chosen_b);
+        };
+        terms(false);
+        {
+            const bool lost = !(sums.x >= kLeast && sums.x <= kMost);
+            const bool chosen_lost = p.dw && p.renorm && !(sums.z >= kLeast && sums.z <= kMost);
+            if (__any_sync(0xffffffffu, lost || chosen_lost)) {
+                float m = -CUDART_INF_F, chosen_m = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < 4 * V; ++i) m = max_nan(m, z[i]);
+#pragma unroll
+                for (int j = 0; j < KPL; ++j) chosen_m = max_nan(chosen_m, chosen_z[j]);
+                m = token_max<LANES>(m);
+                chosen_m = token_max<LANES>(chosen_m);
+                if (lost) c = SIGMOID ? min_nan(m, 0.0f) : m;
+                if (chosen_lost) chosen_c = SIGMOID ? min_nan(chosen_m, 0.0f) : chosen_m;
+                terms(true);
+            }
+        }
+        const float one_sum = rcp_fast(sums.x);
+        if (p.dw && direct) {
+            const float by = p.renorm ? p.scale * rcp_fast(sums.z) : p.scale * chosen_one;
+            const float mean = p.renorm ? sums.w * rcp_fast(sums.z) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < KPL; ++j)
+                if (id[j] >= 0) mine[id[j]] = by * chosen_u[j] * (dw[j] - mean) * (SIGMOID ? chosen_r[j] : 1.0f);
+            gather(d);
+            clear();
         } else {
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) d[i] = 0.0f;
         }
         if (more) load_chosen(t0 + kTokens);
         if (p.dbalance || !direct) {
-            float dot = 0.0f;
+            const float mean = sums.y * one_sum;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
-                e[i] *= one_sum;
-                dot = fmaf(e[i], g[i], dot);
+                const float p_i = SIGMOID ? e[i] * r[i] : e[i];
+                d[i] = fmaf(p_i * one_sum, g[i] - mean, d[i]);
             }
-            dot = token_sum<LANES>(dot);
-#pragma unroll
-            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(SIGMOID ? e[i] * r[i] : e[i], g[i] - dot, d[i]);
         }
         if (p.dz) {
+            float z_c = c;
+            z_sum = token_sum<LANES>(z_sum);
+            if (__any_sync(0xffffffffu, !(z_sum <= kMost))) z_sum = soft_terms<LANES, V>(z, e, z_c);  // logits of 79 and more
             const float by = by_z * log_of(z_sum, z_c), one_z = rcp_fast(z_sum);
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(by, exp_fast(z[i] - z_c) * one_z, d[i]);
@@ -776,8 +791,8 @@ cudaError_t launch_router_grad(RouterGradArgs& p, cudaStream_t s) {
     if (p.T <= 0) return cudaSuccess;
     return by_experts(p.E, [&](auto form) {
         using F = decltype(form);
-        // four blocks an SM, whole rounds of their warps
-        const int64_t want = (p.T + 152 * 4 - 1) / (152 * 4);
+        // three blocks an SM, whole rounds of their warps
+        const int64_t want = (p.T + 152 * 3 - 1) / (152 * 3);
         p.chunk = (int)std::max<int64_t>(F::kGradTokens, (want + F::kGradTokens - 1) / F::kGradTokens * F::kGradTokens);
         const dim3 grid((unsigned)((p.T + p.chunk - 1) / p.chunk));
         const size_t smem = F::kGradTokens * F::kCols * sizeof(float);
