@@ -81,6 +81,17 @@ __device__ __forceinline__ float4 token_sums(float a, float b, float c, float d)
                        __shfl_sync(all, s, LANES / 2, LANES), __shfl_sync(all, s, 3 * LANES / 4, LANES));
 }
 
+// Two of them.
+template <int LANES>
+__device__ __forceinline__ float2 token_sums(float a, float b) {
+    constexpr uint32_t all = 0xffffffffu;
+    const bool upper = threadIdx.x % LANES & (LANES / 2);
+    float s = (upper ? b : a) + __shfl_xor_sync(all, upper ? a : b, LANES / 2);
+#pragma unroll
+    for (int o = LANES / 4; o > 0; o >>= 1) s += __shfl_xor_sync(all, s, o);
+    return make_float2(__shfl_sync(all, s, 0, LANES), __shfl_sync(all, s, LANES / 2, LANES));
+}
+
 // How rows lie: any E; a multiple of 4 (16-byte aligned rows); every column of
 // every lane there.
 enum Rows : int { ROWS_ANY, ROWS_VEC, ROWS_FULL };
@@ -147,17 +158,22 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         sum = z_sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
-            const float t = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp2_fast(min_nan(z[i] * kLog2e, kTop * kLog2e));
+            const float t = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
             r[i] = rcp_fast(far ? fmaf(t, one, 1.0f) : t + 1.0f);
             u[i] = t * r[i];
             sum += u[i];
             z_sum += t;
         }
-        sum = token_sum<LANES>(sum);
-        if (want_z) z_sum = token_sum<LANES>(z_sum);
+        if (want_z) {
+            const float2 both = token_sums<LANES>(sum, z_sum);
+            sum = both.x;
+            z_sum = both.y;
+        } else {
+            sum = token_sum<LANES>(sum);
+        }
     };
     terms(false, 1.0f);
-    const bool lost = !(sum >= kLeast);
+    const bool lost = !(sum >= kLeast);  // too small, or a logit so large that u is inf 0
     if (__any_sync(0xffffffffu, lost)) {
         float m = -CUDART_INF_F;
 #pragma unroll
@@ -175,20 +191,6 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
 }
 
 __device__ __forceinline__ float log_of(float sum, float c) { return c + __log2f(sum) * kLn2; }
-
-// The last sequence whose tokens start at t or before; -1 or n_seqs - 1 and
-// beyond it where t is in none.  One thread.
-__device__ __forceinline__ int seq_of(const int32_t* offsets, int n_seqs, int t) {
-    int lo = 0, hi = n_seqs + 1;  // offsets[lo - 1] <= t < offsets[hi]
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (offsets[mid] <= t)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo - 1 < n_seqs ? lo - 1 : -1;
-}
 
 __device__ __forceinline__ int seq_begin(const BalanceArgs& p, int b) {
     return p.offsets ? min(max(p.offsets[b], 0), p.T) : 0;
@@ -250,6 +252,7 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int 
         for (int j = 0; j < KPL; ++j) next_id[j] = lane + j * LANES < p.k ? __ldg(p.ids + (int64_t)t * p.k + lane + j * LANES) : 0;
     };
     if (first < to) load(first);
+#pragma unroll 2
     for (int t0 = first; t0 < to; t0 += step) {  // whole warps together
         const bool in = t0 + sub < to;
         float z[4 * V], e[4 * V], c, sum;
@@ -322,8 +325,7 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
     let_next_kernel_start();
     const int tid = threadIdx.x, warp = tid >> 5;
     const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.T);
-    int b = p.offsets ? seq_of(p.offsets, p.n_seqs, lo) : 0;
-    if (b < 0) b = p.offsets[0] > lo ? 0 : p.n_seqs;
+    int b = p.offsets ? max(last_not_above(p.offsets, p.n_seqs + 1, lo), 0) : 0;
     for (; b < p.n_seqs; ++b) {
         const int begin = seq_begin(p, b), end = seq_end(p, b);
         if (begin >= hi) break;
@@ -424,8 +426,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
     __shared__ float sums[4][DWDP_MAX_EXPERTS];
     __shared__ int counts[4][DWDP_MAX_EXPERTS];
     __shared__ float red[32];
-    wait_for_previous_kernel();
-    let_next_kernel_start();
+    // (the kernel before let this one start when everything before it was done)
     const int b = blockIdx.x;
     const int begin = seq_begin(p, b), end = seq_end(p, b);
     int first = 0, last = -1;
@@ -434,6 +435,8 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
         last = (end - 1) / p.chunk;
         if (first == last) return;
     }
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     const int parts = min(4, 1024 / p.E), part = threadIdx.x / p.E, e = threadIdx.x % p.E;
     if (part < parts) {
         float s = 0.0f;
@@ -527,7 +530,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             next_chosen[j] = next_id[j] >= 0 ? __ldg(row + next_id[j]) : -CUDART_INF_F;
         }
     };
-    int from = 0, to = 0;  // the tokens of the sequence at hand; none yet
+    // the sequence at hand, and where its tokens end; none yet
+    int seq = losses && p.offsets ? last_not_above(p.offsets, p.n_seqs + 1, lo) : 0, to = 0;
     float by_p = 0.0f, by_z = 0.0f;
     float of_counts[V <= 2 ? 4 * V : 1] = {};  // d loss / d p of its balance loss, where registers allow
     const int32_t* counts = p.counts;
@@ -567,18 +571,20 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
         };
         const bool more = t0 + kTokens < hi;
         if (more) load(t0 + kTokens);
-        if (losses && (t < from || t >= to)) {  // another sequence
-            const int b = p.offsets ? seq_of(p.offsets, p.n_seqs, t) : 0;
-            from = t;
-            to = t + 1;
+        if (losses && t >= to) {  // another sequence
+            int from = 0;
+            to = p.T;
+            if (p.offsets) {
+                while (seq < p.n_seqs && p.offsets[seq + 1] <= t) ++seq;
+                from = seq >= 0 ? max(p.offsets[seq], 0) : 0;
+                to = seq < p.n_seqs ? min(p.offsets[seq + 1], p.T) : p.T;
+            }
             by_p = by_z = 0.0f;
-            if (b >= 0) {
-                from = p.offsets ? max(p.offsets[b], 0) : 0;
-                to = p.offsets ? min(p.offsets[b + 1], p.T) : p.T;
+            if (seq >= 0 && seq < p.n_seqs) {
                 const float per_token = 1.0f / (float)(to - from);
-                if (p.dbalance) by_p = p.dbalance[b] * ((float)p.E / (float)p.k) * per_token * per_token;
-                if (p.dz) by_z = 2.0f * p.dz[b] * per_token;
-                counts = p.counts + (int64_t)b * p.E;
+                if (p.dbalance) by_p = p.dbalance[seq] * ((float)p.E / (float)p.k) * per_token * per_token;
+                if (p.dz) by_z = 2.0f * p.dz[seq] * per_token;
+                counts = p.counts + (int64_t)seq * p.E;
             }
             if constexpr (V <= 2) {
 #pragma unroll
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             z_sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
-                e[i] = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp2_fast(min_nan(z[i] * kLog2e, kTop * kLog2e));
+                e[i] = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
                 z_sum += e[i];
                 if constexpr (SIGMOID) {
                     r[i] = rcp_fast(far ? fmaf(e[i], one, 1.0f) : e[i] + 1.0f);
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
         };
         terms(false);
         {
-            const bool lost = !(sums.x >= kLeast && sums.x <= kMost);
+            const bool lost = !(sums.x >= kLeast && sums.x <= kMost);  // a sigmoid's u is inf 0 of a large logit
             const bool chosen_lost = p.dw && p.renorm && !(sums.z >= kLeast && sums.z <= kMost);
             if (__any_sync(0xffffffffu, lost || chosen_lost)) {
                 float m = -CUDART_INF_F, chosen_m = -CUDART_INF_F;

@@ -57,6 +57,22 @@ __device__ __forceinline__ void warp_sum_max(float& s, float& m) {
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 }
 
+// The last of n non-decreasing values that is at most v; -1 where there is
+// none.  The whole warp together: 32 values a step.
+__device__ __forceinline__ int last_not_above(const int32_t* values, int n, int64_t v) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (true) {
+        const int step = (n + 31) / 32, i = lane * step;
+        const uint32_t at = __ballot_sync(0xffffffffu, i < n && (int64_t)values[lo + i] <= v);
+        if (at == 0) return lo - 1;
+        const int j = (31 - __clz(at)) * step;
+        lo += j;
+        n = min(step, n - j);
+        if (n == 1) return lo;
+    }
+}
+
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -27,19 +27,10 @@ constexpr float kDownScale = 0x1p-80f;
 constexpr float kMinCodeMax = 0x1p-100f;
 
 // The group of `row`: offsets[g] <= row < offsets[g + 1], the last such g; -1
-// where there is none.  The whole warp together: 32 offsets a step.
+// where there is none.  The whole warp together.
 __device__ __forceinline__ int group_of(const int32_t* offsets, int n_groups, int64_t row) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = n_groups + 1;
-    while (n > 1) {
-        const int step = (n + 31) / 32, i = lane * step;
-        const uint32_t at = __ballot_sync(0xffffffffu, i < n && (int64_t)offsets[lo + i] <= row);
-        if (at == 0) return -1;
-        const int j = (31 - __clz(at)) * step;
-        lo += j;
-        n = min(step, n - j);
-    }
-    return lo < n_groups ? lo : -1;
+    const int g = last_not_above(offsets, n_groups + 1, row);
+    return g < n_groups ? g : -1;
 }
 
 // (sum, max, max) over the block; every thread gets them.  `turn` alternates
@@ -744,9 +735,8 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __g
     const bool gates = blockIdx.y >= 2, alone = PER_WARP && gates;
     const int group = !gates ? 0 : PER_WARP ? (blockIdx.y - 2) * kSumWarps + warp : blockIdx.y - 2;
     float* to = gates ? p.dgate + (int64_t)group * H : blockIdx.y == 0 ? p.dpre : p.dpost;
-    wait_for_previous_kernel();
-    let_next_kernel_start();
     if (!gates && !to) return;
+    // (the kernel before let this one start when everything before it was done)
     uint32_t first = 0, last = (uint32_t)p.units;  // one behind the last unit
     bool wanted = col < H;
     if (gates) {
@@ -760,6 +750,8 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __g
         }
         if (last == first + 1) wanted = false;  // written already
     }
+    wait_for_previous_kernel();
+    let_next_kernel_start();
     float2 s = make_float2(0.0f, 0.0f);
     if (wanted) {
         const float* from = p.partial + (gates ? 2 : blockIdx.y) * (int64_t)H + col;
