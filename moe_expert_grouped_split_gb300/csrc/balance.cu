@@ -96,25 +96,64 @@ __device__ __forceinline__ float2 token_sums(float a, float b) {
 // every lane there.
 enum Rows : int { ROWS_ANY, ROWS_VEC, ROWS_FULL };
 
-// A lane's logits of one token: columns 4 (v LANES + lane) .. + 3, -inf beyond E.
-template <int LANES, int V, int ROWS>
-__device__ __forceinline__ void load_token(const float* row, int E, int lane, float (&z)[4 * V]) {
+// A token's lanes' place in shared memory: tokens on their way (depth() of them),
+// each with its logits, columns 4 (v LANES + lane) .. + 3 of a lane, its choices
+// and, for the gradients, their weights' gradients.  Every lane copies what it
+// reads itself, but for the chosen logits.
+template <int LANES, int V, bool DW>
+struct Ring {
+    static constexpr int kCols = 4 * V * LANES, kPer = choices_a_lane(LANES), kChoices = kPer * LANES;
+    static constexpr int kDepth = V > 2 ? 2 : 4;
+    static constexpr int kStage = kCols + kChoices * (DW ? 2 : 1);  // 4-byte values
+    static constexpr int kFloats = kDepth * kStage;
+    float* at;  // of this token's lanes
+
+    // -inf where there is no column; nothing is copied there
+    __device__ __forceinline__ void clear(int E, int lane) const {
+        for (int s = 0; s < kDepth; ++s)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = 4 * (v * LANES + lane);
-        if constexpr (ROWS != ROWS_ANY) {
-            const float4 q = ROWS == ROWS_FULL || c < E ? __ldg(reinterpret_cast<const float4*>(row + c))
-                                   : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+            for (int i = 0; i < 4 * V; ++i) {
+                const int c = 4 * (i / 4 * LANES + lane) + i % 4;
+                if (c >= E) at[s * kStage + c] = -CUDART_INF_F;
+            }
+    }
+    template <int ROWS>
+    __device__ __forceinline__ void fetch(int s, const float* logits, const int32_t* ids, const float* dw, int64_t t, int E, int k,
+                                          int lane) const {
+        float* const to = at + s * kStage;
+        const float* const row = logits + t * E;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = 4 * (v * LANES + lane);
+            if constexpr (ROWS != ROWS_ANY) {
+                if (ROWS == ROWS_FULL || c < E) copy_async<16>(to + c, row + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < E) copy_async<4>(to + c + i, row + c + i);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = lane + j * LANES;
+            if (i >= k || !ids) continue;
+            copy_async<4>(to + kCols + i, ids + t * k + i);
+            if constexpr (DW) copy_async<4>(to + kCols + kChoices + i, dw + t * k + i);
+        }
+    }
+    __device__ __forceinline__ void take(int s, int lane, float (&z)[4 * V]) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float4 q = reinterpret_cast<const float4*>(at + s * kStage)[v * LANES + lane];
             z[4 * v] = q.x;
             z[4 * v + 1] = q.y;
             z[4 * v + 2] = q.z;
             z[4 * v + 3] = q.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[4 * v + i] = c + i < E ? __ldg(row + c + i) : -CUDART_INF_F;
         }
     }
-}
+    __device__ __forceinline__ int choice(int s, int i) const { return __float_as_int(at[s * kStage + kCols + i]); }
+    __device__ __forceinline__ float dw(int s, int i) const { return at[s * kStage + kCols + kChoices + i]; }
+};
 
 // A token's exp(z - c) and their sum.
 template <int LANES, int V>
@@ -237,39 +276,35 @@ struct TokenSums {
 
 // Adds up tokens `first`, first + step, ... below `to` for a warp (first: of
 // its first LANES lanes, the next tokens for the others), and counts their
-// choices in hist.  The next token's logits and choices are on their way while
-// one is worked on.
+// choices in hist.
 template <int LANES, int V, int ROWS>
-__device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int to, int step, int* hist, TokenSums<V>& sums) {
-    constexpr int KPL = choices_a_lane(LANES);
+__device__ __forceinline__ void add_tokens(const BalanceArgs& p, const Ring<LANES, V, false>& ring, int first, int to, int step,
+                                           int* hist, TokenSums<V>& sums) {
+    using R = Ring<LANES, V, false>;
     const int lane = threadIdx.x % LANES, sub = (threadIdx.x & 31) / LANES;
-    float next[4 * V];
-    int next_id[KPL];
-    auto load = [&](int t0) {  // a token of the warp at least is there
-        const int t = min(t0 + sub, to - 1);
-        load_token<LANES, V, ROWS>(p.logits + (int64_t)t * p.E, p.E, lane, next);
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) next_id[j] = lane + j * LANES < p.k ? __ldg(p.ids + (int64_t)t * p.k + lane + j * LANES) : 0;
+    auto fetch = [&](int64_t t0, int s) {  // a token of the warp at least is there
+        if (t0 < to) ring.template fetch<ROWS>(s, p.logits, p.ids, nullptr, min((int)t0 + sub, to - 1), p.E, p.k, lane);
+        end_copies();
     };
-    if (first < to) load(first);
-#pragma unroll 2
+#pragma unroll
+    for (int s = 0; s < R::kDepth; ++s) fetch(first + (int64_t)s * step, s);
+    int s = 0;
     for (int t0 = first; t0 < to; t0 += step) {  // whole warps together
+        wait_copies<R::kDepth - 1>();
         const bool in = t0 + sub < to;
         float z[4 * V], e[4 * V], c, sum;
-        int id[KPL];
+        ring.take(s, lane, z);
 #pragma unroll
-        for (int i = 0; i < 4 * V; ++i) z[i] = next[i];
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) id[j] = next_id[j];
-        if (t0 + step < to) load(t0 + step);
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) {
+        for (int j = 0; j < R::kPer; ++j) {
             if (!in || lane + j * LANES >= p.k) continue;
-            if (id[j] >= 0 && id[j] < p.E)
-                atomicAdd(hist + id[j], 1);
+            const int id = ring.choice(s, lane + j * LANES);
+            if (id >= 0 && id < p.E)
+                atomicAdd(hist + id, 1);
             else
                 atomicOr(p.err, DERR_BAD_INDEX);
         }
+        fetch(t0 + (int64_t)R::kDepth * step, s);
+        s = s + 1 == R::kDepth ? 0 : s + 1;
         float z_sum, z_c;
         if (p.sigmoid) {
             float r[4 * V];
@@ -279,34 +314,34 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& p, int first, int 
             z_c = c;
         }
         const float f = in ? rcp_fast(sum) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) sums.p[i] = fmaf(e[i], f, sums.p[i]);
         if (in) {
+#pragma unroll
+            for (int i = 0; i < 4 * V; ++i) sums.p[i] = fmaf(e[i], f, sums.p[i]);
             if (p.z) {
                 const float l = log_of(z_sum, z_c);
                 sums.z = fmaf(l, l, sums.z);
             }
         }
     }
+    wait_copies<0>();
 }
 
-// A lane's sums to `rows` [tokens at once][columns]; afterwards (a barrier on)
-// total_p(e) is the block's sum of column e.
+// A lane's sums to its token's first stage; afterwards (a barrier on)
+// total_p(rings, e) is the block's sum of column e.
 template <int LANES, int V>
-__device__ __forceinline__ void leave(const TokenSums<V>& sums, float* rows, float* z_rows) {
-    constexpr int kCols = 4 * V * LANES;
+__device__ __forceinline__ void leave(const TokenSums<V>& sums, const Ring<LANES, V, false>& ring, float* z_rows) {
     const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        reinterpret_cast<float4*>(rows + slot * kCols)[v * LANES + lane] =
+        reinterpret_cast<float4*>(ring.at)[v * LANES + lane] =
             make_float4(sums.p[4 * v], sums.p[4 * v + 1], sums.p[4 * v + 2], sums.p[4 * v + 3]);
     if (lane == 0) z_rows[slot] = sums.z;
 }
-template <int TOKENS, int COLS>
-__device__ __forceinline__ float total_p(const float* rows, int e) {
+template <int LANES, int V>
+__device__ __forceinline__ float total_p(const float* rings, int e) {
     float s = 0.0f;
 #pragma unroll 8
-    for (int i = 0; i < TOKENS; ++i) s += rows[i * COLS + e];
+    for (int i = 0; i < 32 / LANES * kWarps; ++i) s += rings[i * Ring<LANES, V, false>::kFloats + e];
     return s;
 }
 
@@ -317,9 +352,9 @@ template <int LANES, int V, int ROWS>
 __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_constant__ BalanceArgs p) {
     extern __shared__ __align__(16) float smem[];
     constexpr int kTokens = 32 / LANES * kWarps;  // at once
-    constexpr int kCols = 4 * V * LANES;
-    float* rows = smem;                                          // [kTokens][kCols]
-    int* hist = reinterpret_cast<int*>(smem + kTokens * kCols);  // [kCols]
+    using R = Ring<LANES, V, false>;
+    const R ring{smem + threadIdx.x / LANES * R::kFloats};
+    int* hist = reinterpret_cast<int*>(smem + kTokens * R::kFloats);  // [kCols]
     __shared__ float red[32], z_rows[kTokens];
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -332,15 +367,16 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
         const int from = max(begin, lo), to = min(end, hi);
         if (from >= to) continue;
         for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
+        ring.clear(p.E, tid % LANES);
         __syncthreads();
         TokenSums<V> sums{};
-        add_tokens<LANES, V, ROWS>(p, from + warp * (32 / LANES), to, kTokens, hist, sums);
-        leave<LANES, V>(sums, rows, z_rows);
+        add_tokens<LANES, V, ROWS>(p, ring, from + warp * (32 / LANES), to, kTokens, hist, sums);
+        leave<LANES, V>(sums, ring, z_rows);
         __syncthreads();
         float z_all = 0.0f;
         if (tid == 0)
             for (int i = 0; i < kTokens; ++i) z_all += z_rows[i];
-        auto sum_of = [&](int e) { return total_p<kTokens, kCols>(rows, e); };
+        auto sum_of = [&](int e) { return total_p<LANES, V>(smem, e); };
         if (begin >= lo && end <= hi) {
             finish_sequence(p, b, end - begin, z_all, sum_of, [&](int e) { return hist[e]; }, red);
         } else {
@@ -371,22 +407,24 @@ template <int LANES, int V, int ROWS>
 __global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps)
     balance_few_kernel(const __grid_constant__ BalanceArgs p) {
     extern __shared__ __align__(16) float smem[];
-    constexpr int kTokens = 32 / LANES * kWarps, kCols = 4 * V * LANES;
-    float* rows = smem;
-    int* hist = reinterpret_cast<int*>(smem + kTokens * kCols);
-    float* total = smem + (kTokens + 1) * kCols;  // [kCols], and z's
+    using R = Ring<LANES, V, false>;
+    constexpr int kTokens = 32 / LANES * kWarps;
+    const R ring{smem + threadIdx.x / LANES * R::kFloats};
+    int* hist = reinterpret_cast<int*>(smem + kTokens * R::kFloats);
+    float* total = smem + kTokens * R::kFloats + R::kCols;  // [kCols]
     __shared__ float red[32], z_rows[kTokens];
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int tid = threadIdx.x, warp = tid >> 5, b = blockIdx.x / kFewBlocks, rank = blockIdx.x % kFewBlocks;
     const int begin = seq_begin(p, b), end = seq_end(p, b);
     for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
+    ring.clear(p.E, tid % LANES);
     __syncthreads();
     TokenSums<V> sums{};
-    add_tokens<LANES, V, ROWS>(p, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
-    leave<LANES, V>(sums, rows, z_rows);
+    add_tokens<LANES, V, ROWS>(p, ring, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
+    leave<LANES, V>(sums, ring, z_rows);
     __syncthreads();
-    for (int e = tid; e < p.E; e += blockDim.x) total[e] = total_p<kTokens, kCols>(rows, e);
+    for (int e = tid; e < p.E; e += blockDim.x) total[e] = total_p<LANES, V>(smem, e);
     if (tid == 0) {
         float z = 0.0f;
         for (int i = 0; i < kTokens; ++i) z += z_rows[i];
@@ -491,65 +529,60 @@ __device__ __forceinline__ void store4(void* out, bool half, int64_t at, float a
 // while one is worked on.
 template <int LANES, int V, int ROWS, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_kernel(const __grid_constant__ RouterGradArgs p) {
-    constexpr int kTokens = 32 / LANES * kGradWarps, kCols = 4 * V * LANES;
-    constexpr int KPL = choices_a_lane(LANES);
-    extern __shared__ __align__(16) float smem[];  // [kTokens][kCols]: what the choices add, zero between tokens
+    using R = Ring<LANES, V, true>;
+    constexpr int kTokens = 32 / LANES * kGradWarps, kCols = R::kCols, KPL = R::kPer;
+    extern __shared__ __align__(16) float smem[];  // [kTokens][kCols]: what the choices add, zero between tokens; the rings
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int tid = threadIdx.x, lane = tid % LANES, slot = tid / LANES;
     float* mine = smem + slot * kCols;
+    const R ring{smem + kTokens * kCols + slot * R::kFloats};
+    ring.clear(p.E, lane);
 #pragma unroll
     for (int v = 0; v < V; ++v) reinterpret_cast<float4*>(mine)[v * LANES + lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
     const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.T);
     const bool losses = p.dbalance || p.dz, direct = p.renorm || SIGMOID;
-    float next[4 * V], next_dw[KPL], next_chosen[KPL];
-    int next_id[KPL];
-    auto load = [&](int t0) {
-        const int t = min(t0 + slot, hi - 1);
-        load_token<LANES, V, ROWS>(p.logits + (int64_t)t * p.E, p.E, lane, next);
-        if (!p.dw) return;
-#pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            const int i = lane + j * LANES;
-            next_id[j] = i < p.k ? __ldg(p.ids + (int64_t)t * p.k + i) : -1;
-            next_dw[j] = i < p.k ? __ldg(p.dw + (int64_t)t * p.k + i) : 0.0f;
-        }
+    auto fetch = [&](int64_t t0, int s) {
+        if (t0 < hi)
+            ring.template fetch<ROWS>(s, p.logits, p.dw ? p.ids : nullptr, p.dw, min((int)t0 + slot, hi - 1), p.E, p.k, lane);
+        end_copies();
     };
-    // the chosen experts' logits, once the choices are there
-    auto load_chosen = [&](int t0) {
-        if (!p.dw) return;
-        const float* row = p.logits + (int64_t)min(t0 + slot, hi - 1) * p.E;
 #pragma unroll
-        for (int j = 0; j < KPL; ++j) {
-            if (lane + j * LANES < p.k && (next_id[j] < 0 || next_id[j] >= p.E)) {
-                atomicOr(p.err, DERR_BAD_INDEX);
-                next_id[j] = -1;
-            }
-            if (next_id[j] < 0) next_dw[j] = 0.0f;
-            next_chosen[j] = next_id[j] >= 0 ? __ldg(row + next_id[j]) : -CUDART_INF_F;
-        }
-    };
+    for (int s = 0; s < R::kDepth; ++s) fetch(lo + s * kTokens, s);
+    int s = 0;
     // the sequence at hand, and where its tokens end; none yet
     int seq = losses && p.offsets ? last_not_above(p.offsets, p.n_seqs + 1, lo) : 0, to = 0;
     float by_p = 0.0f, by_z = 0.0f;
     float of_counts[V <= 2 ? 4 * V : 1] = {};  // d loss / d p of its balance loss, where registers allow
     const int32_t* counts = p.counts;
-    load(lo);
-    load_chosen(lo);
     for (int t0 = lo; t0 < hi; t0 += kTokens) {  // whole warps together
         const int t = min(t0 + slot, hi - 1);
         const bool in = t0 + slot < hi;
         float z[4 * V], e[4 * V], r[4 * V], g[4 * V], d[4 * V], dw[KPL], chosen_z[KPL];
         int id[KPL];
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) z[i] = next[i];
+        wait_copies<R::kDepth - 1>();
+        __syncwarp();  // the chosen logits are other lanes' copies
+        ring.take(s, lane, z);
 #pragma unroll
         for (int j = 0; j < KPL; ++j) {
-            id[j] = p.dw ? next_id[j] : -1;
-            dw[j] = p.dw ? next_dw[j] : 0.0f;
-            chosen_z[j] = p.dw ? next_chosen[j] : 0.0f;
+            const int i = lane + j * LANES;
+            id[j] = -1;
+            dw[j] = 0.0f;
+            if (p.dw && i < p.k) {
+                id[j] = ring.choice(s, i);
+                if (id[j] >= 0 && id[j] < p.E) {
+                    dw[j] = ring.dw(s, i);
+                } else {
+                    atomicOr(p.err, DERR_BAD_INDEX);
+                    id[j] = -1;
+                }
+            }
+            chosen_z[j] = id[j] >= 0 ? ring.at[s * R::kStage + id[j]] : -CUDART_INF_F;
         }
+        __syncwarp();  // everybody has read this stage
+        fetch(t0 + (int64_t)R::kDepth * kTokens, s);
+        s = s + 1 == R::kDepth ? 0 : s + 1;
         // what the choices have left in shared memory; then none of it is there
         auto gather = [&](float (&v)[4 * V]) {
             __syncwarp();
@@ -569,8 +602,6 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
                 if (id[j] >= 0) mine[id[j]] = 0.0f;
             __syncwarp();
         };
-        const bool more = t0 + kTokens < hi;
-        if (more) load(t0 + kTokens);
         if (losses && t >= to) {  // another sequence
             int from = 0;
             to = p.T;
@@ -675,7 +706,6 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) d[i] = 0.0f;
         }
-        if (more) load_chosen(t0 + kTokens);
         if (p.dbalance || !direct) {
             const float mean = sums.y * one_sum;
 #pragma unroll
@@ -777,7 +807,7 @@ cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s) {
         return by_experts(p.E, [&](auto form) {
             using F = decltype(form);
             const auto kernel = balance_few_kernel<F::LANES, F::V, F::ROWS>;
-            const size_t smem = (F::kTokens + 2) * F::kCols * sizeof(float);
+            const size_t smem = (F::kTokens * Ring<F::LANES, F::V, false>::kFloats + 2 * F::kCols) * sizeof(float);
             cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                               : cudaSuccess;
             return e != cudaSuccess ? e : launch_dependent(kernel, p, dim3((unsigned)p.n_seqs * kFewBlocks), 32 * kWarps, smem, s);
@@ -785,7 +815,7 @@ cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s) {
     const cudaError_t e = by_experts(p.E, [&](auto form) {
         using F = decltype(form);
         const auto kernel = balance_kernel<F::LANES, F::V, F::ROWS>;
-        const size_t smem = (F::kTokens + 1) * F::kCols * sizeof(float);
+        const size_t smem = (F::kTokens * Ring<F::LANES, F::V, false>::kFloats + F::kCols) * sizeof(float);
         cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                           : cudaSuccess;
         return e != cudaSuccess ? e : launch_dependent(kernel, p, dim3((unsigned)L.blocks), 32 * kWarps, smem, s);
@@ -801,10 +831,12 @@ cudaError_t launch_router_grad(RouterGradArgs& p, cudaStream_t s) {
         const int64_t want = (p.T + 152 * 3 - 1) / (152 * 3);
         p.chunk = (int)std::max<int64_t>(F::kGradTokens, (want + F::kGradTokens - 1) / F::kGradTokens * F::kGradTokens);
         const dim3 grid((unsigned)((p.T + p.chunk - 1) / p.chunk));
-        const size_t smem = F::kGradTokens * F::kCols * sizeof(float);
-        if (p.sigmoid)
-            return launch_dependent(router_grad_kernel<F::LANES, F::V, F::ROWS, true>, p, grid, 32 * kGradWarps, smem, s);
-        return launch_dependent(router_grad_kernel<F::LANES, F::V, F::ROWS, false>, p, grid, 32 * kGradWarps, smem, s);
+        const size_t smem = F::kGradTokens * (F::kCols + Ring<F::LANES, F::V, true>::kFloats) * sizeof(float);
+        const auto kernel = p.sigmoid ? router_grad_kernel<F::LANES, F::V, F::ROWS, true> : router_grad_kernel<F::LANES, F::V, F::ROWS, false>;
+        const cudaError_t e = smem > (48 << 10)
+                                  ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                  : cudaSuccess;
+        return e != cudaSuccess ? e : launch_dependent(kernel, p, grid, 32 * kGradWarps, smem, s);
     });
 }
 

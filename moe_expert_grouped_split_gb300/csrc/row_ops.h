@@ -45,6 +45,22 @@ __device__ __forceinline__ void copy16(uint4* to, const uint4* from) {
                  : "memory");
 }
 
+// Copies BYTES (4, 8 or 16) into shared memory, to be waited for.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most PENDING groups of this thread's copies are on their way.
+template <int PENDING>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // m: magnitudes, whose order as floats is their bits' (a NaN is above +inf).
 __device__ __forceinline__ float warp_max(float m) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));

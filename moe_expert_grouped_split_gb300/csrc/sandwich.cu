@@ -75,17 +75,6 @@ __device__ __forceinline__ float code_factor(float m, float& scale) {
     return 448.0f * rcp(m);
 }
 
-// Copies a vector of this thread's into shared memory; nobody else reads it,
-// so nothing is waited for but the thread's own copies.
-template <int BYTES>
-__device__ __forceinline__ void fetch_vec(char* to, const void* from) {
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (BYTES == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
-}
-
 __device__ __forceinline__ void load8(const float4* at, int apart, eight& f) {
     const float4 a = at[0], b = at[apart];
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
@@ -256,7 +245,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 1024) sandwich_norm_kernel(c
 }
 
 // Many rows: a block stays and takes rows [blockIdx.x chunk, + chunk) in order.
-// The rows STAGES - 1 ahead are on their way into shared memory, where c gate
+// The rows STAGES - 1 ahead are on their way into shared memory (each thread
+// copies what it will read itself, and waits for its own copies only), where c gate
 // post of the group lies too; what is never fetched is zero there.
 constexpr int kNormVecs = 2, kNormStayRows = 8;
 template <class ASK, int STAGES>
@@ -277,11 +267,11 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (!held[j]) continue;
-                fetch_vec<16>(own + at + j * n * 16, p.x + row * p.x_vecs + tid + j * n);
-                if (p.residual) fetch_vec<16>(own + at + (VPT + j) * n * 16, p.residual + row * p.nv + tid + j * n);
+                copy_async<16>(own + at + j * n * 16, p.x + row * p.x_vecs + tid + j * n);
+                if (p.residual) copy_async<16>(own + at + (VPT + j) * n * 16, p.residual + row * p.nv + tid + j * n);
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        end_copies();
     };
     uint4 pre[VPT];
 #pragma unroll
@@ -312,7 +302,7 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
     const int rows = (int)(hi - lo);
     int change = open ? rows : 0, in = 0, turn = 0;
     for (int i = 0; i < rows; ++i) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        wait_copies<STAGES - 1>();
         if (i == change) {
             const int group = group_of(p.row_offsets, p.n_groups, lo + i);
             open = group >= 0;
@@ -517,15 +507,15 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
             for (int j = 0; j < VPT; ++j) {
                 if (!held[j]) continue;
                 const uint32_t place = first + j * n;
-                if constexpr (X != KEPT_NOT) fetch_vec<kX>(own_x + at + j * n * kX, x + place * kX);
+                if constexpr (X != KEPT_NOT) copy_async<kX>(own_x + at + j * n * kX, x + place * kX);
                 if constexpr (PRE) {
-                    fetch_vec<kH>(own_h + at + j * n * kH, h + place * kH);
-                    fetch_vec<16>(own + at + j * n * 16, dout + place * 16);
+                    copy_async<kH>(own_h + at + j * n * kH, h + place * kH);
+                    copy_async<16>(own + at + j * n * 16, dout + place * 16);
                 }
-                if (p.dres) fetch_vec<16>(own + at + (VPT + j) * n * 16, dres + place * 16);
+                if (p.dres) copy_async<16>(own + at + (VPT + j) * n * 16, dres + place * 16);
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        end_copies();
     };
     // what is never fetched is zero, so that the arithmetic need not ask
 #pragma unroll
@@ -629,7 +619,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
             mine = later;
             later = row_factors(lo + r + 32 + lane);
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 1) : "memory");
+        wait_copies<kGradStages - 1>();
         if (r == change) {
             if (open) close_group();
             group = group_of(p.row_offsets, p.n_groups, lo + r);
