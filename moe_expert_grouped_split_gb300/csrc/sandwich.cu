@@ -209,8 +209,8 @@ __device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row,
 }
 
 // One block per row; thread i holds the row's vectors i, i + blockDim.x, ...
-template <class ASK, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 1024) sandwich_norm_kernel(const __grid_constant__ SandwichArgs p) {
+template <class ASK, int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 448 ? 2 : 1) sandwich_norm_kernel(const __grid_constant__ SandwichArgs p) {
     __shared__ float4 red[2][32];
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 1024) sandwich_norm_kernel(c
     sandwich_row<ASK, VPT>(p, row, row * p.nv + threadIdx.x, blockDim.x, held, x, r, pre, factor, red, turn);
 }
 
-// Many rows: a block stays and takes rows [blockIdx.x chunk, + chunk) in order.
+// Many wide rows: a block stays and takes rows [blockIdx.x chunk, + chunk) in order.
 // The rows STAGES - 1 ahead are on their way into shared memory (each thread
 // copies what it will read itself, and waits for its own copies only), where c gate
 // post of the group lies too; what is never fetched is zero there.
-constexpr int kNormVecs = 2, kNormStayRows = 8;
+constexpr int kNormVecs = 2, kNormSmem = (228 << 10) / 2 - 2048;  // of a block: two fit an SM
 template <class ASK, int STAGES>
 __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_constant__ SandwichArgs p) {
     constexpr int VPT = kNormVecs;
@@ -824,25 +824,38 @@ cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
                         : launch_grad<X, KEPT_E4M3, POST>(p, s);
 }
 
+// Which kernel.  us with a post norm, kept rows and no codes: a block a row, one
+// vector a thread / the same, two a thread / staying blocks.
+//   rows   H 512               2048                7168
+//    152   2.3 / 2.6 / 3.5     2.4 / 2.8 / 3.8      3.8 /  4.2 /  4.7
+//    608   2.5 / 2.7 / 3.5     3.6 / 5.0 / 5.5     16.1 / 12.2 / 12.1
+//   1216   2.8 / 3.2 / 3.9     8.1 / 8.1 / 9.7     30.3 / 21.6 / 20.5
+//   4864   7.7 / 7.3 / 9.2    24.8 / 20.6 / 23.7    112 / 72.6 / 63.1
+//  16384         18 / 19             60 / 61               232 / 193
+// So one vector a thread while all rows' blocks are on the SMs at once (64
+// registers a thread), then two; staying blocks for many wide rows.
 template <class ASK>
 cudaError_t launch_norm(SandwichArgs& p, cudaStream_t s) {
-    const int nv = p.nv;
-    // Staying blocks, two an SM, from a few rows each on.
-    if (nv <= 1024 && p.rows >= 152 * kNormStayRows) {
-        const int threads = ((nv + kNormVecs - 1) / kNormVecs + 31) / 32 * 32;
-        auto bytes = [&](int stages) { return (size_t)threads * kNormVecs * (stages * 32 + 32); };
-        const int stages = bytes(3) <= (228 << 10) / 2 - 2048 ? 3 : 2;
-        const int64_t most = 152 * std::min<int64_t>(1024 / threads, (228 << 10) / (bytes(stages) + 2048));
+    const int nv = p.nv, threads1 = (nv + 31) / 32 * 32, threads2 = ((nv + 1) / 2 + 31) / 32 * 32;
+    const dim3 grid((unsigned)p.rows);
+    if (nv <= 1024 && p.rows <= 152 * (1024 / threads1))
+        return launch_dependent(sandwich_norm_kernel<ASK, 1, 1024>, p, grid, threads1, 0, s);
+    if (nv <= 896 && (nv <= 448 || p.rows < 8 * 152))
+        return launch_dependent(sandwich_norm_kernel<ASK, 2, 448>, p, grid, threads2, 0, s);
+    if (nv <= 1024) {
+        // two an SM
+        auto bytes = [&](int stages) { return (size_t)threads2 * kNormVecs * (stages * 32 + 32); };
+        const int stages = bytes(3) <= kNormSmem ? 3 : 2;
+        const int64_t most = 152 * std::min<int64_t>(1024 / threads2, (228 << 10) / (bytes(stages) + 2048));
         p.chunk = (p.rows + most - 1) / most;
-        const dim3 grid((unsigned)((p.rows + p.chunk - 1) / p.chunk));
+        const dim3 blocks((unsigned)((p.rows + p.chunk - 1) / p.chunk));
         const auto kernel = stages == 3 ? sandwich_stream_kernel<ASK, 3> : sandwich_stream_kernel<ASK, 2>;
         // the kernel's limit, not this call's size (norm.cu)
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (228 << 10) / 2 - 2048);
-        return e != cudaSuccess ? e : launch_dependent(kernel, p, grid, threads, bytes(stages), s);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+        return e != cudaSuccess ? e : launch_dependent(kernel, p, blocks, threads2, bytes(stages), s);
     }
-    const dim3 grid((unsigned)p.rows);
-    if (nv <= 1024) return launch_dependent(sandwich_norm_kernel<ASK, 1>, p, grid, (nv + 31) / 32 * 32, 0, s);
-    return launch_dependent(sandwich_norm_kernel<ASK, 4>, p, grid, ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
+    if (nv <= 2048) return launch_dependent(sandwich_norm_kernel<ASK, 2, 1024>, p, grid, threads2, 0, s);
+    return launch_dependent(sandwich_norm_kernel<ASK, 4, 1024>, p, grid, ((nv + 3) / 4 + 31) / 32 * 32, 0, s);
 }
 
 template <bool POST, bool KEPT>
