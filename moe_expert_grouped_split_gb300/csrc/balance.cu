@@ -103,7 +103,7 @@ enum Rows : int { ROWS_ANY, ROWS_VEC, ROWS_FULL };
 template <int LANES, int V, bool DW>
 struct Ring {
     static constexpr int kCols = 4 * V * LANES, kPer = choices_a_lane(LANES), kChoices = kPer * LANES;
-    static constexpr int kDepth = V > 2 ? 2 : 4;
+    static constexpr int kDepth = 2;
     static constexpr int kStage = kCols + kChoices * (DW ? 2 : 1);  // 4-byte values
     static constexpr int kFloats = kDepth * kStage;
     float* at;  // of this token's lanes
@@ -276,18 +276,20 @@ struct TokenSums {
 
 // Adds up tokens `first`, first + step, ... below `to` for a warp (first: of
 // its first LANES lanes, the next tokens for the others), and counts their
-// choices in hist.
+// choices in hist.  asked: the first tokens are on their way already.
 template <int LANES, int V, int ROWS>
-__device__ __forceinline__ void add_tokens(const BalanceArgs& p, const Ring<LANES, V, false>& ring, int first, int to, int step,
-                                           int* hist, TokenSums<V>& sums) {
+__device__ __forceinline__ void add_tokens(const BalanceArgs& p, const Ring<LANES, V, false>& ring, bool asked, int first, int to,
+                                           int step, int* hist, TokenSums<V>& sums) {
     using R = Ring<LANES, V, false>;
     const int lane = threadIdx.x % LANES, sub = (threadIdx.x & 31) / LANES;
     auto fetch = [&](int64_t t0, int s) {  // a token of the warp at least is there
         if (t0 < to) ring.template fetch<ROWS>(s, p.logits, p.ids, nullptr, min((int)t0 + sub, to - 1), p.E, p.k, lane);
         end_copies();
     };
+    if (!asked) {
 #pragma unroll
-    for (int s = 0; s < R::kDepth; ++s) fetch(first + (int64_t)s * step, s);
+        for (int s = 0; s < R::kDepth; ++s) fetch(first + (int64_t)s * step, s);
+    }
     int s = 0;
     for (int t0 = first; t0 < to; t0 += step) {  // whole warps together
         wait_copies<R::kDepth - 1>();
@@ -360,6 +362,16 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
     let_next_kernel_start();
     const int tid = threadIdx.x, warp = tid >> 5;
     const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.T);
+    // the block's first tokens, before it is known which sequence they are in
+    ring.clear(p.E, tid % LANES);
+#pragma unroll
+    for (int s = 0; s < R::kDepth; ++s) {
+        const int t0 = lo + warp * (32 / LANES) + s * kTokens;
+        if (t0 < hi)
+            ring.template fetch<ROWS>(s, p.logits, p.ids, nullptr, min(t0 + (tid & 31) / LANES, hi - 1), p.E, p.k, tid % LANES);
+        end_copies();
+    }
+    bool asked = true;
     int b = p.offsets ? max(last_not_above(p.offsets, p.n_seqs + 1, lo), 0) : 0;
     for (; b < p.n_seqs; ++b) {
         const int begin = seq_begin(p, b), end = seq_end(p, b);
@@ -367,10 +379,15 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
         const int from = max(begin, lo), to = min(end, hi);
         if (from >= to) continue;
         for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
-        ring.clear(p.E, tid % LANES);
+        if (!asked || from != lo) {
+            wait_copies<0>();
+            ring.clear(p.E, tid % LANES);
+            asked = false;
+        }
         __syncthreads();
         TokenSums<V> sums{};
-        add_tokens<LANES, V, ROWS>(p, ring, from + warp * (32 / LANES), to, kTokens, hist, sums);
+        add_tokens<LANES, V, ROWS>(p, ring, asked, from + warp * (32 / LANES), to, kTokens, hist, sums);
+        asked = false;
         leave<LANES, V>(sums, ring, z_rows);
         __syncthreads();
         float z_all = 0.0f;
@@ -403,40 +420,17 @@ __device__ __forceinline__ uint32_t from_rank(const void* own, int rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
-template <int LANES, int V, int ROWS>
-__global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps)
-    balance_few_kernel(const __grid_constant__ BalanceArgs p) {
-    extern __shared__ __align__(16) float smem[];
-    using R = Ring<LANES, V, false>;
-    constexpr int kTokens = 32 / LANES * kWarps;
-    const R ring{smem + threadIdx.x / LANES * R::kFloats};
-    int* hist = reinterpret_cast<int*>(smem + kTokens * R::kFloats);
-    float* total = smem + kTokens * R::kFloats + R::kCols;  // [kCols]
-    __shared__ float red[32], z_rows[kTokens];
-    wait_for_previous_kernel();
-    let_next_kernel_start();
-    const int tid = threadIdx.x, warp = tid >> 5, b = blockIdx.x / kFewBlocks, rank = blockIdx.x % kFewBlocks;
-    const int begin = seq_begin(p, b), end = seq_end(p, b);
-    for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
-    ring.clear(p.E, tid % LANES);
-    __syncthreads();
-    TokenSums<V> sums{};
-    add_tokens<LANES, V, ROWS>(p, ring, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
-    leave<LANES, V>(sums, ring, z_rows);
-    __syncthreads();
-    for (int e = tid; e < p.E; e += blockDim.x) total[e] = total_p<LANES, V>(smem, e);
-    if (tid == 0) {
-        float z = 0.0f;
-        for (int i = 0; i < kTokens; ++i) z += z_rows[i];
-        z_rows[0] = z;
-    }
+// finish_sequence by a cluster whose blocks have their sums in total [E], hist
+// [E] and *z each.
+__device__ __forceinline__ void finish_cluster(const BalanceArgs& p, int b, int tokens, const float* total, const int* hist,
+                                               const float* z, int rank, float* red) {
     cluster_sync();
     if (rank == 0) {
-        float z = 0.0f;
-        if (tid == 0)
-            for (int i = 0; i < kFewBlocks; ++i) z += __uint_as_float(from_rank(z_rows, i));
+        float z_sum = 0.0f;
+        if (threadIdx.x == 0 && p.z)
+            for (int i = 0; i < kFewBlocks; ++i) z_sum += __uint_as_float(from_rank(z, i));
         finish_sequence(
-            p, b, max(end - begin, 0), z,
+            p, b, max(tokens, 0), z_sum,
             [&](int e) {
                 float v[kFewBlocks], s = 0.0f;
 #pragma unroll
@@ -457,30 +451,63 @@ __global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps
     }
     cluster_sync();  // the others' shared memory stays until it has been read
 }
+template <int LANES, int V, int ROWS>
+__global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps)
+    balance_few_kernel(const __grid_constant__ BalanceArgs p) {
+    extern __shared__ __align__(16) float smem[];
+    using R = Ring<LANES, V, false>;
+    constexpr int kTokens = 32 / LANES * kWarps;
+    const R ring{smem + threadIdx.x / LANES * R::kFloats};
+    int* hist = reinterpret_cast<int*>(smem + kTokens * R::kFloats);
+    float* total = smem + kTokens * R::kFloats + R::kCols;  // [kCols]
+    __shared__ float red[32], z_rows[kTokens];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int tid = threadIdx.x, warp = tid >> 5, b = blockIdx.x / kFewBlocks, rank = blockIdx.x % kFewBlocks;
+    const int begin = seq_begin(p, b), end = seq_end(p, b);
+    for (int e = tid; e < p.E; e += blockDim.x) hist[e] = 0;
+    ring.clear(p.E, tid % LANES);
+    __syncthreads();
+    TokenSums<V> sums{};
+    add_tokens<LANES, V, ROWS>(p, ring, false, begin + (rank * kWarps + warp) * (32 / LANES), end, kFewBlocks * kTokens, hist, sums);
+    leave<LANES, V>(sums, ring, z_rows);
+    __syncthreads();
+    for (int e = tid; e < p.E; e += blockDim.x) total[e] = total_p<LANES, V>(smem, e);
+    if (tid == 0) {
+        float z = 0.0f;
+        for (int i = 0; i < kTokens; ++i) z += z_rows[i];
+        z_rows[0] = z;
+    }
+    finish_cluster(p, b, end - begin, total, hist, z_rows, rank, red);
+}
 
 // The sequences that no block finished alone: those of several blocks, and
-// those without tokens.  A block each; 4 threads a column at most.
+// those without tokens.  A block each (CLUSTER: 8, where a sequence has many
+// blocks' sums: an SM takes in 600 KB in 6 us); 4 threads a column at most.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_constant__ BalanceArgs p) {
     __shared__ float sums[4][DWDP_MAX_EXPERTS];
     __shared__ int counts[4][DWDP_MAX_EXPERTS];
-    __shared__ float red[32];
+    __shared__ float red[32], z_all;
+    constexpr int kBlocks = CLUSTER ? kFewBlocks : 1;
     // (the kernel before let this one start when everything before it was done)
-    const int b = blockIdx.x;
+    const int b = blockIdx.x / kBlocks, rank = blockIdx.x % kBlocks;
     const int begin = seq_begin(p, b), end = seq_end(p, b);
     int first = 0, last = -1;
     if (begin < end) {
         first = begin / p.chunk;
         last = (end - 1) / p.chunk;
-        if (first == last) return;
     }
+    // (before any return: who comes next waits for this kernel only)
     wait_for_previous_kernel();
     let_next_kernel_start();
+    if (first == last) return;  // finished already; the whole cluster
     const int parts = min(4, 1024 / p.E), part = threadIdx.x / p.E, e = threadIdx.x % p.E;
     if (part < parts) {
         float s = 0.0f;
         int n = 0;
 #pragma unroll 8
-        for (int i = first + part; i <= last; i += parts) {
+        for (int i = first + rank * parts + part; i <= last; i += kBlocks * parts) {
             const int64_t at = ((int64_t)i * 2 + (i == first ? 1 : 0)) * p.E + e;
             s += p.part_p[at];
             n += p.part_counts[at];
@@ -488,26 +515,35 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
         sums[part][e] = s;
         counts[part][e] = n;
     }
-    float z = 0.0f;
     if (p.z && threadIdx.x < 32) {
-        float none = 0.0f;
-        for (int i = first + threadIdx.x; i <= last; i += 32) z += p.part_z[(int64_t)i * 2 + (i == first ? 1 : 0)];
+        float z = 0.0f, none = 0.0f;
+        for (int i = first + rank * 32 + threadIdx.x; i <= last; i += 32 * kBlocks)
+            z += p.part_z[(int64_t)i * 2 + (i == first ? 1 : 0)];
         warp_sum_max<false>(z, none);
+        if (threadIdx.x == 0) z_all = z;
     }
     __syncthreads();
-    finish_sequence(
-        p, b, max(end - begin, 0), z,
-        [&](int c) {
-            float s = 0.0f;
-            for (int i = 0; i < parts; ++i) s += sums[i][c];
-            return s;
-        },
-        [&](int c) {
-            int n = 0;
-            for (int i = 0; i < parts; ++i) n += counts[i][c];
-            return n;
-        },
-        red);
+    auto own_p = [&](int c) {
+        float s = 0.0f;
+        for (int i = 0; i < parts; ++i) s += sums[i][c];
+        return s;
+    };
+    auto own_count = [&](int c) {
+        int n = 0;
+        for (int i = 0; i < parts; ++i) n += counts[i][c];
+        return n;
+    };
+    if constexpr (CLUSTER) {
+        for (int c = threadIdx.x; c < p.E; c += blockDim.x) {
+            const float s = own_p(c);
+            const int n = own_count(c);
+            sums[0][c] = s;
+            counts[0][c] = n;
+        }
+        finish_cluster(p, b, end - begin, sums[0], counts[0], &z_all, rank, red);
+    } else {
+        finish_sequence(p, b, max(end - begin, 0), p.z ? z_all : 0.0f, own_p, own_count, red);
+    }
 }
 
 // ------------------------------------------------------------ gradients --
@@ -820,7 +856,10 @@ cudaError_t launch_balance(BalanceArgs& p, void* ws, cudaStream_t s) {
                                           : cudaSuccess;
         return e != cudaSuccess ? e : launch_dependent(kernel, p, dim3((unsigned)L.blocks), 32 * kWarps, smem, s);
     });
-    return e != cudaSuccess ? e : launch_dependent(balance_finish_kernel, p, dim3((unsigned)p.n_seqs), 1024, 0, s);
+    if (e != cudaSuccess) return e;
+    if (L.blocks / p.n_seqs >= 64)
+        return launch_dependent(balance_finish_kernel<true>, p, dim3((unsigned)p.n_seqs * kFewBlocks), 1024, 0, s, kFewBlocks);
+    return launch_dependent(balance_finish_kernel<false>, p, dim3((unsigned)p.n_seqs), 1024, 0, s);
 }
 
 cudaError_t launch_router_grad(RouterGradArgs& p, cudaStream_t s) {

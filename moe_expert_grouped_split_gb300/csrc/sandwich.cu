@@ -725,7 +725,6 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __g
     const bool gates = blockIdx.y >= 2, alone = PER_WARP && gates;
     const int group = !gates ? 0 : PER_WARP ? (blockIdx.y - 2) * kSumWarps + warp : blockIdx.y - 2;
     float* to = gates ? p.dgate + (int64_t)group * H : blockIdx.y == 0 ? p.dpre : p.dpost;
-    if (!gates && !to) return;
     // (the kernel before let this one start when everything before it was done)
     uint32_t first = 0, last = (uint32_t)p.units;  // one behind the last unit
     bool wanted = col < H;
@@ -740,8 +739,10 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __g
         }
         if (last == first + 1) wanted = false;  // written already
     }
+    // (before any return: who comes next waits for this kernel only)
     wait_for_previous_kernel();
     let_next_kernel_start();
+    if (!gates && !to) return;
     float2 s = make_float2(0.0f, 0.0f);
     if (wanted) {
         const float* from = p.partial + (gates ? 2 : blockIdx.y) * (int64_t)H + col;
