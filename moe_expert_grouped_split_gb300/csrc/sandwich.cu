@@ -15,6 +15,7 @@
 
 #include "dwdp_internal.h"
 #include "row_ops.h"
+#include "tc_ops.h"
 
 namespace dwdp {
 namespace {
@@ -393,16 +394,6 @@ __device__ __forceinline__ void values(const char* at, pair by, four& f) {
     for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], by);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// Every thread of the cluster; what was written to any block's shared memory
-// before is seen after it.
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // The sums of a, b and c over the `size` blocks (4 at most) that share a row,
 // for every thread.  A warp's three sums together: half of the lanes go on
@@ -425,11 +416,11 @@ __device__ __forceinline__ float3 row_sums(float a, float b, float c, float* red
         float* r = red + turn * size * nw * 4;
         turn ^= 1;
         if (w < size) {
-            uint32_t at = (uint32_t)__cvta_generic_to_shared(r + (cluster_rank() * nw + warp) * 4 + i);
+            uint32_t at = (uint32_t)__cvta_generic_to_shared(r + (cluster_ctarank() * nw + warp) * 4 + i);
             asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(w));
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(s) : "memory");
         }
-        cluster_barrier();
+        cluster_sync();
         s = 0.0f;
         for (int e = w; e < size * nw; e += 8) s += r[e * 4 + i];
 #pragma unroll
@@ -455,7 +446,7 @@ __device__ __forceinline__ void load4(const ulonglong2* at, int far, four& f) {
     f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 
-constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = 227 << 10;
+constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = (227 << 10) - 1024;
 
 // A block takes rows [unit chunk, + chunk) in order; thread i holds the row's
 // vectors i and i + blockDim.x and their columns' sums.  Rows of more than
@@ -472,17 +463,18 @@ constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = 227 << 10;
 // (a group whose rows are all here goes to dgate at once).
 // X, HK: how x and h were kept (HK KEPT_NOT: no pre norm); POST: a post norm;
 // THREADS at most (448: the compiler's order of things is 5% faster than for 512).
-template <int X, int HK, bool POST, int THREADS, bool SHARED>
+// BULK: one thread asks for whole rows (16-byte addresses and sizes: bf16, or
+// codes of H a multiple of 16), at the end of the row whose stage they take; else
+// every thread copies what it will read itself, as soon as it has taken its
+// part of that row.
+template <int X, int HK, bool POST, int THREADS, bool SHARED, bool BULK>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad_kernel(const __grid_constant__ SandwichGradArgs p) {
     constexpr int VPT = kGradVecs, kX = kept_bytes(X), kH = kept_bytes(HK);
     constexpr bool PRE = HK != KEPT_NOT;
-    // the row kGradStages ahead is asked for as soon as a thread has taken its part of this one, where a block is alone on its
-    // SM (8192 x 7168 from 8 bits: 132 us; 138 if after the
-    // reduction), and after it where four share one (16384 x 2048: 74 us; 77 if before)
-    constexpr bool kEarly = THREADS > 256;
     extern __shared__ __align__(16) char smem[];
+    __shared__ uint64_t full_bars[kGradStages];  // BULK: of the stages, when their rows have come
     const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31;
-    const int size = SHARED ? p.size : 1, rank = SHARED ? (int)cluster_rank() : 0, unit = blockIdx.x / size;
+    const int size = SHARED ? p.size : 1, rank = SHARED ? (int)cluster_ctarank() : 0, unit = blockIdx.x / size;
     wait_for_previous_kernel();
     let_next_kernel_start();
     const int64_t lo = (int64_t)unit * p.chunk, hi = min(lo + p.chunk, p.rows);
@@ -497,7 +489,23 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
     ulonglong2* const gw = reinterpret_cast<ulonglong2*>(smem + all_stages) + tid;
     float* const red = reinterpret_cast<float*>(smem + all_stages + vecs * 32);
     const bool held[VPT] = {tid < own_vecs, tid + n < own_vecs};
-    auto fetch = [&](int64_t row, int at) {
+    const uint32_t full = smem_u32(full_bars);
+    const int row_bytes = p.nv * (kX + kH + (PRE ? 16 : 0) + (p.dres ? 16 : 0));
+    // asks for a row into stage `stage`, which begins at `at`
+    auto fetch = [&](int64_t row, int stage, int at) {
+        if (BULK) {
+            if (tid != 0 || row >= hi) return;
+            const uint32_t to = smem_u32(smem) + at, bar = full + 8 * stage;
+            mbar_arrive_expect_tx(bar, row_bytes);
+            if constexpr (X != KEPT_NOT)
+                bulk_load(to + vecs * 32, static_cast<const char*>(p.x) + row * p.x_vecs * kX, p.nv * kX, bar);
+            if constexpr (PRE) {
+                bulk_load(to + vecs * (32 + kX), static_cast<const char*>(p.h) + row * p.nv * kH, p.nv * kH, bar);
+                bulk_load(to, p.dout + row * p.nv, p.nv * 16, bar);
+            }
+            if (p.dres) bulk_load(to + vecs * 16, p.dres + row * p.nv, p.nv * 16, bar);
+            return;
+        }
         if (row < hi) {
             const char* const x = static_cast<const char*>(p.x) + row * p.x_vecs * kX;
             const char* const h = static_cast<const char*>(p.h) + row * p.nv * kH;
@@ -539,8 +547,15 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         const float2 r = p.rstd ? p.rstd[row] : make_float2(1.0f, 1.0f);
         return make_float4(r.x, r.y, X == KEPT_E4M3 ? p.x_scale[row] * r.x : r.x, HK == KEPT_E4M3 ? p.h_scale[row] * r.y : r.y);
     };
+    if (BULK) {
+        if (tid == 0) {
+            for (int s = 0; s < kGradStages; ++s) mbar_init(full + 8 * s, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncthreads();
+    }
 #pragma unroll
-    for (int s = 0; s < kGradStages; ++s) fetch(lo + s, s * stage_bytes);
+    for (int s = 0; s < kGradStages; ++s) fetch(lo + s, s, s * stage_bytes);
     float4 mine = row_factors(lo + lane), later = row_factors(lo + 32 + lane);  // of 32 rows, a lane each
     four dpre[VPT] = {}, sum[VPT] = {};
     uint4 pre[VPT];
@@ -549,9 +564,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
     float* partial = p.partial + (int64_t)unit * 4 * H;
     const bool to_dx[VPT] = {held[0] && p.dx, held[1] && p.dx};
     const bool to_dresidual[VPT] = {held[0] && p.dresidual, held[1] && p.dresidual};
-    int group = 0, in = 0, turn = 0;
+    int group = 0, in = 0, turn = 0, stage = 0, parity = 0;
     int64_t begin = 0, end = p.rows;  // of the group
-    bool open = !p.row_offsets, any = false;
+    bool open = !p.row_offsets, any = false, lost = false;
     // block_scale times a weight's or gate's elements (1 where there is none)
     auto scaled = [&](const uint4* w, int64_t vec, four& f) {
         if (w) {
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         any = true;
     };
     if (open) open_group();
-    if (SHARED) cluster_barrier();  // all blocks are there to be written to
+    if (SHARED) cluster_sync();  // all blocks are there to be written to
     const int rows = (int)(hi - lo);
     int change = open ? rows : 0;  // the row at which the group has to be looked up again
     for (int r = 0; r < rows; ++r) {
@@ -619,7 +634,15 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
             mine = later;
             later = row_factors(lo + r + 32 + lane);
         }
-        wait_copies<kGradStages - 1>();
+        if (BULK) {
+            // 2 s at most, and then for no other row: what is written from here on is NaN
+            if (!lost && !mbar_try_wait(full + 8 * stage, parity)) {
+                const uint64_t since = global_timer();
+                while (!lost && !mbar_try_wait(full + 8 * stage, parity)) lost = global_timer() - since > kWaitLimitNs;
+            }
+        } else {
+            wait_copies<kGradStages - 1>();
+        }
         if (r == change) {
             if (open) close_group();
             group = group_of(p.row_offsets, p.n_groups, lo + r);
@@ -665,7 +688,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
                     }
                 }
             }
-            if constexpr (kEarly) fetch(lo + r + kGradStages, in);
+            if (!BULK) fetch(lo + r + kGradStages, stage, in);
             float m = 0.0f, m2 = 0.0f;
             const int64_t vec = (lo + r) * p.nv + first;
             if constexpr (PRE || POST) {
@@ -674,6 +697,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
                 m = rh * sums.x * p.one_nth;
                 m2 = rx * (sums.y - m * sums.z) * p.one_nth;
             }
+            if (BULK && lost) m = m2 = CUDART_NAN_F;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 four t;
@@ -697,9 +721,27 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
                 if (to_dx[j]) p.dx[vec + j * n] = pack4(t);
             }
         }
-        if (!kEarly || !open) fetch(lo + r + kGradStages, in);
+        if (BULK) {
+            // everybody has taken his part of the stage: they were at the row's
+            // barrier since, where it has one (and nobody is a phase of the
+            // stage's own barrier behind)
+            if (!open || !(PRE || POST))
+                __syncthreads();
+            else
+                __syncwarp();  // a block of one warp
+        }
+        if (BULK || !open) fetch(lo + r + kGradStages, stage, in);
         in += stage_bytes;
-        if (in == all_stages) in = 0;
+        if (++stage == kGradStages) {
+            stage = in = 0;
+            parity ^= 1;
+        }
+    }
+    if (lost) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) dpre[j][c] = sum[j][c] = two(CUDART_NAN_F);
     }
     if (open) close_group();
 #pragma unroll
@@ -710,7 +752,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         if (PRE && p.dpre) store4(partial + 8 * i, dpre[j]);
         if (POST && p.dpost && !any) store4(partial + H + 8 * i, none);
     }
-    if (SHARED) cluster_barrier();  // no block leaves while another may write to it
+    if (SHARED) cluster_sync();  // no block leaves while another may write to it
 }
 
 // Adds up the units' sums, 64 columns a block.  blockIdx.y 0: pre, 1: post,
@@ -796,9 +838,9 @@ struct GradShape {
     }
 };
 
-template <int X, int HK, bool POST, int THREADS, bool SHARED>
+template <int X, int HK, bool POST, int THREADS, bool SHARED, bool BULK>
 cudaError_t launch_grad(const SandwichGradArgs& p, const GradShape& g, size_t smem, cudaStream_t s) {
-    const auto kernel = sandwich_grad_kernel<X, HK, POST, THREADS, SHARED>;
+    const auto kernel = sandwich_grad_kernel<X, HK, POST, THREADS, SHARED, BULK>;
     // the kernel's limit, not this call's size (norm.cu)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
     if (e != cudaSuccess) return e;
@@ -813,10 +855,12 @@ cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
     p.units = g.units(p.rows, smem);
     p.chunk = (p.rows + p.units - 1) / p.units;
     p.units = (p.rows + p.chunk - 1) / p.chunk;
-    if (g.size > 1) return launch_grad<X, HK, POST, 512, true>(p, g, smem, s);
-    return g.threads <= 256   ? launch_grad<X, HK, POST, 256, false>(p, g, smem, s)
-           : g.threads <= 448 ? launch_grad<X, HK, POST, 448, false>(p, g, smem, s)
-                              : launch_grad<X, HK, POST, 512, false>(p, g, smem, s);
+    if (g.size > 1) return launch_grad<X, HK, POST, 512, true, false>(p, g, smem, s);
+    if constexpr (X == KEPT_E4M3 || HK == KEPT_E4M3)
+        if (p.nv % 2 || (X == KEPT_E4M3 && p.x_vecs % 2)) return launch_grad<X, HK, POST, 512, false, false>(p, g, smem, s);
+    return g.threads <= 256   ? launch_grad<X, HK, POST, 256, false, true>(p, g, smem, s)
+           : g.threads <= 448 ? launch_grad<X, HK, POST, 448, false, true>(p, g, smem, s)
+                              : launch_grad<X, HK, POST, 512, false, true>(p, g, smem, s);
 }
 template <int X, bool POST>
 cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
