@@ -53,283 +53,6 @@ __device__ __forceinline__ float3 block_sum_max2(float s, float a, float b, floa
     return make_float3(s, warp_max(v.y), warp_max(v.z));
 }
 
-using eight = float[8];  // a vector's elements
-
-__device__ __forceinline__ uint2 codes8(const eight& v, float inv) {
-    uint32_t q[2] = {0u, 0u};
-#pragma unroll
-    for (int c = 0; c < 8; c += 2) {
-        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[c] * inv, v[c + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        q[c >> 2] |= two << ((c & 2) * 8);
-    }
-    return make_uint2(q[0], q[1]);
-}
-
-// 448 / the largest magnitude, and the scale that goes with it (1 for zeros).
-__device__ __forceinline__ float code_factor(float m, float& scale) {
-    if (m == 0.0f) {
-        scale = 1.0f;
-        return 0.0f;
-    }
-    m = max_nan(m, kMinCodeMax);
-    scale = m / 448.0f;
-    return 448.0f * rcp(m);
-}
-
-__device__ __forceinline__ void load8(const float4* at, int apart, eight& f) {
-    const float4 a = at[0], b = at[apart];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-
-// What is asked of a forward call (the rest are pointers that may be null).
-template <bool POST_, bool PRE_, bool CODES_, bool KEPT_>
-struct Asked {
-    static constexpr bool POST = POST_, PRE = PRE_, CODES = CODES_, KEPT = KEPT_;
-};
-
-// c gate post of a vector's elements.
-__device__ __forceinline__ void block_factor(const SandwichArgs& p, const uint4* gate, const uint4* post, int i, eight& f) {
-    eight w;
-    if (gate) unpack8(__ldg(gate + i), f);
-    if (post) unpack8(__ldg(post + i), w);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] = p.block_scale * (gate ? f[c] : 1.0f) * (post ? w[c] : 1.0f);
-}
-
-// One row of which the thread has VPT vectors: x and the residual (zeros where
-// there is nothing), factor(j, f) = c gate post and pre.  vec: the first
-// one's place among all vectors, the others n on each; held[j]: to be stored.
-template <class ASK, int VPT, class Factor>
-__device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row, int64_t vec, int n, const bool (&held)[VPT],
-                                             const uint4 (&x)[VPT], const uint4 (&r)[VPT], const uint4 (&pre)[VPT],
-                                             Factor factor, float4 (*red)[32], int& turn) {
-    float rx = 1.0f, x_inv = 0.0f;
-    const bool first = threadIdx.x == 0;
-    if constexpr (ASK::POST || ASK::KEPT) {
-        float ss = 0.0f, ax = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            eight f;
-            unpack8(x[j], f);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if constexpr (ASK::POST) ss = fmaf(f[c], f[c], ss);
-                if constexpr (ASK::KEPT) ax = max_nan(ax, fabsf(f[c]));
-            }
-        }
-        float3 sums = block_sum_max2(ss, ax, 0.0f, red, turn);
-        if constexpr (ASK::POST) {
-            float scaled = 1.0f;
-            if (!(sums.x < kSquaresLimit)) {  // rare; the whole block agrees
-                scaled = kDownScale;
-                ss = 0.0f;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    eight f;
-                    unpack8(x[j], f);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) ss = fmaf(f[c] * scaled, f[c] * scaled, ss);
-                }
-                sums.x = block_sum_max2(ss, 0.0f, 0.0f, red, turn).x;
-            }
-            rx = rsqrtf(fmaf(sums.x, p.one_nth, p.eps * scaled * scaled)) * scaled;
-        }
-        if constexpr (ASK::KEPT) {
-            float scale;
-            x_inv = code_factor(sums.y, scale);
-            if (first && p.x_scale) p.x_scale[row] = scale;
-        }
-    }
-    eight h[VPT];
-    float ss = 0.0f, ah = 0.0f, ay = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        eight f, w;
-        unpack8(x[j], f);
-        if (ASK::KEPT && p.x_codes && held[j]) p.x_codes[vec + j * n] = codes8(f, x_inv);
-        factor(j, w);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] *= ASK::POST ? rx * w[c] : w[c];
-        unpack8(r[j], w);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            h[j][c] = fmaf(p.residual_scale, w[c], f[c]);
-            if constexpr (ASK::PRE) ss = fmaf(h[j][c], h[j][c], ss);
-            if constexpr (ASK::KEPT) ah = max_nan(ah, fabsf(h[j][c]));
-        }
-        if constexpr (ASK::CODES) {
-            unpack8(pre[j], w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) ay = max_nan(ay, fabsf(h[j][c] * w[c]));
-        }
-        if (p.residual_out && held[j]) p.residual_out[vec + j * n] = pack8(h[j]);
-    }
-    float rh = 1.0f, h_inv = 0.0f, y_inv = 0.0f;
-    if constexpr (ASK::PRE || ASK::KEPT) {
-        float3 sums = block_sum_max2(ss, ah, ay, red, turn);
-        if constexpr (ASK::PRE) {
-            float scaled = 1.0f;
-            if (!(sums.x < kSquaresLimit)) {
-                scaled = kDownScale;
-                ss = 0.0f;
-#pragma unroll
-                for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) ss = fmaf(h[j][c] * scaled, h[j][c] * scaled, ss);
-                sums.x = block_sum_max2(ss, 0.0f, 0.0f, red, turn).x;
-            }
-            rh = rsqrtf(fmaf(sums.x, p.one_nth, p.eps * scaled * scaled)) * scaled;
-        }
-        if constexpr (ASK::KEPT) {
-            float scale;
-            h_inv = code_factor(sums.y, scale);
-            if (first && p.h_scale) p.h_scale[row] = scale;
-        }
-        if constexpr (ASK::CODES) {
-            float scale;
-            y_inv = code_factor(sums.z, scale);
-            if (first) p.row_scale[row] = sums.z == 0.0f ? 1.0f : scale * rh;
-        }
-    }
-    if (first && p.rstd) p.rstd[row] = make_float2(rx, rh);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        if (ASK::KEPT && p.h_codes && held[j]) p.h_codes[vec + j * n] = codes8(h[j], h_inv);
-        if constexpr (ASK::PRE) {
-            eight w, y;
-            unpack8(pre[j], w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                w[c] *= h[j][c];
-                y[c] = w[c] * rh;
-            }
-            if (held[j]) p.out[vec + j * n] = pack8(y);
-            if (ASK::CODES && held[j]) p.codes[vec + j * n] = codes8(w, y_inv);
-        }
-    }
-}
-
-// One block per row; thread i holds the row's vectors i, i + blockDim.x, ...
-template <class ASK, int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS <= 448 ? 2 : 1) sandwich_norm_kernel(const __grid_constant__ SandwichArgs p) {
-    __shared__ float4 red[2][32];
-    wait_for_previous_kernel();
-    let_next_kernel_start();
-    const int64_t row = blockIdx.x;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 x[VPT], r[VPT], pre[VPT];
-    bool held[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int i = threadIdx.x + j * blockDim.x;
-        held[j] = i < p.nv;
-        x[j] = held[j] ? p.x[row * p.x_vecs + i] : zero;
-        r[j] = held[j] && p.residual ? p.residual[row * p.nv + i] : zero;
-        pre[j] = ASK::PRE && held[j] ? __ldg(p.pre + i) : zero;
-    }
-    const uint4* gate = p.gate;
-    if (p.row_offsets) {
-        const int g = group_of(p.row_offsets, p.n_groups, row);
-        if (g < 0) return;  // the whole block
-        gate += (int64_t)g * p.nv;
-    }
-    auto factor = [&](int j, eight& f) {
-        if (held[j]) {
-            block_factor(p, gate, ASK::POST ? p.post : nullptr, threadIdx.x + j * blockDim.x, f);
-        } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] = 0.0f;
-        }
-    };
-    int turn = 0;
-    sandwich_row<ASK, VPT>(p, row, row * p.nv + threadIdx.x, blockDim.x, held, x, r, pre, factor, red, turn);
-}
-
-// Many wide rows: a block stays and takes rows [blockIdx.x chunk, + chunk) in order.
-// The rows STAGES - 1 ahead are on their way into shared memory (each thread
-// copies what it will read itself, and waits for its own copies only), where c gate
-// post of the group lies too; what is never fetched is zero there.
-constexpr int kNormVecs = 2, kNormSmem = (228 << 10) / 2 - 2048;  // of a block: two fit an SM
-template <class ASK, int STAGES>
-__global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_constant__ SandwichArgs p) {
-    constexpr int VPT = kNormVecs;
-    extern __shared__ __align__(16) char smem[];
-    __shared__ float4 red[2][32];
-    wait_for_previous_kernel();
-    let_next_kernel_start();
-    const int tid = threadIdx.x, n = blockDim.x;
-    const int64_t lo = (int64_t)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.rows);
-    const bool held[VPT] = {tid < p.nv, tid + n < p.nv};
-    const int stage_bytes = 2 * VPT * n * 16;
-    char* const own = smem + tid * 16;
-    float4* const factors = reinterpret_cast<float4*>(smem + STAGES * stage_bytes) + tid;
-    auto fetch = [&](int64_t row, int at) {
-        if (row < hi) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (!held[j]) continue;
-                copy_async<16>(own + at + j * n * 16, p.x + row * p.x_vecs + tid + j * n);
-                if (p.residual) copy_async<16>(own + at + (VPT + j) * n * 16, p.residual + row * p.nv + tid + j * n);
-            }
-        }
-        end_copies();
-    };
-    uint4 pre[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        pre[j] = ASK::PRE && held[j] ? __ldg(p.pre + tid + j * n) : zero;
-        if (held[j] && p.residual) continue;
-        for (int at = 0; at < STAGES * stage_bytes; at += stage_bytes) {
-            *reinterpret_cast<uint4*>(own + at + (VPT + j) * n * 16) = zero;
-            if (!held[j]) *reinterpret_cast<uint4*>(own + at + j * n * 16) = zero;
-        }
-        if (!held[j]) factors[2 * j * n] = factors[(2 * j + 1) * n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) fetch(lo + s, s * stage_bytes);
-    auto open_group = [&](int group) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (!held[j]) continue;
-            eight f;
-            block_factor(p, p.gate ? p.gate + (int64_t)group * p.nv : nullptr, ASK::POST ? p.post : nullptr, tid + j * n, f);
-            factors[2 * j * n] = make_float4(f[0], f[1], f[2], f[3]);
-            factors[(2 * j + 1) * n] = make_float4(f[4], f[5], f[6], f[7]);
-        }
-    };
-    bool open = !p.row_offsets;
-    if (open) open_group(0);
-    const int rows = (int)(hi - lo);
-    int change = open ? rows : 0, in = 0, turn = 0;
-    for (int i = 0; i < rows; ++i) {
-        wait_copies<STAGES - 1>();
-        if (i == change) {
-            const int group = group_of(p.row_offsets, p.n_groups, lo + i);
-            open = group >= 0;
-            change = i + 1;
-            if (open) {
-                change = (int)min(max((int64_t)p.row_offsets[group + 1] - lo, (int64_t)change), (int64_t)rows);
-                open_group(group);
-            }
-        }
-        uint4 x[VPT], r[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            x[j] = *reinterpret_cast<const uint4*>(own + in + j * n * 16);
-            r[j] = *reinterpret_cast<const uint4*>(own + in + (VPT + j) * n * 16);
-        }
-        fetch(lo + i + STAGES, in);
-        in += stage_bytes;
-        if (in == STAGES * stage_bytes) in = 0;
-        if (open)
-            sandwich_row<ASK, VPT>(
-                p, lo + i, (lo + i) * p.nv + tid, n, held, x, r, pre, [&](int j, eight& f) { load8(factors + 2 * j * n, n, f); }, red,
-                turn);
-    }
-}
-
-// ------------------------------------------------------------ gradients --
 // Two binary32 values in one 64-bit register, one instruction for both.
 using pair = unsigned long long;
 __device__ __forceinline__ pair two(float a, float b) {
@@ -370,6 +93,314 @@ __device__ __forceinline__ uint4 pack4(const four& f) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ void load4(const ulonglong2* at, int far, four& f) {
+    const ulonglong2 a = at[0], b = at[far];
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+__device__ __forceinline__ float sum_of(pair v) {
+    const float2 f = apart(v);
+    return f.x + f.y;
+}
+__device__ __forceinline__ float max_of(const four& v, float m) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float2 f = apart(v[c]);
+        m = max_nan(max_nan(m, fabsf(f.x)), fabsf(f.y));
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint2 codes8(const four& v, float inv) {
+    uint32_t q[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) q[c] = __nv_cvt_float2_to_fp8x2(apart(mul2(v[c], two(inv))), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+}
+
+// 448 / the largest magnitude (0 for zeros), and the scale that goes with it.
+__device__ __forceinline__ float code_factor(float m) { return m == 0.0f ? 0.0f : 448.0f * rcp(max_nan(m, kMinCodeMax)); }
+__device__ __forceinline__ float code_scale(float m) { return m == 0.0f ? 1.0f : max_nan(m, kMinCodeMax) / 448.0f; }
+
+// What is asked of a forward call (the rest are pointers that may be null).
+template <bool POST_, bool PRE_, bool CODES_, bool KEPT_>
+struct Asked {
+    static constexpr bool POST = POST_, PRE = PRE_, CODES = CODES_, KEPT = KEPT_;
+};
+
+// c gate post of a vector's elements.
+__device__ __forceinline__ void block_factor(const SandwichArgs& p, const uint4* gate, const uint4* post, int i, four& f) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[c] = two(p.block_scale);
+    four w;
+    if (gate) {
+        unpack4(__ldg(gate + i), w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] = mul2(f[c], w[c]);
+    }
+    if (post) {
+        unpack4(__ldg(post + i), w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] = mul2(f[c], w[c]);
+    }
+}
+
+// One row of which the thread has VPT vectors: x and the residual (zeros where
+// there is nothing), factor(j, f) = c gate post and pre.  vec: the first
+// one's place among all vectors, the others n on each; held[j]: to be stored.
+template <class ASK, int VPT, class Factor>
+__device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row, int64_t vec, int n, const bool (&held)[VPT],
+                                             const uint4 (&x)[VPT], const uint4 (&r)[VPT], const uint4 (&pre)[VPT],
+                                             Factor factor, float4 (*red)[32], int& turn) {
+    float rx = 1.0f, x_inv = 0.0f;
+    const bool first = threadIdx.x == 0;
+    // 1 / rms from the sum of squares; where that passes the limit it is taken
+    // again on scaled values, squares(by): rare, and the whole block agrees
+    auto rms = [&](float ss, auto squares) {
+        float scaled = 1.0f;
+        if (!(ss < kSquaresLimit)) {
+            scaled = kDownScale;
+            pair again = 0;
+            squares(two(scaled), again);
+            ss = block_sum_max2(sum_of(again), 0.0f, 0.0f, red, turn).x;
+        }
+        return rsqrtf(fmaf(ss, p.one_nth, p.eps * scaled * scaled)) * scaled;
+    };
+    if constexpr (ASK::POST || ASK::KEPT) {
+        pair ss = 0;
+        float ax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            four f;
+            unpack4(x[j], f);
+            if constexpr (ASK::POST) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ss = fma2(f[c], f[c], ss);
+            }
+            if constexpr (ASK::KEPT) ax = max_of(f, ax);
+        }
+        const float3 sums = block_sum_max2(sum_of(ss), ax, 0.0f, red, turn);
+        if constexpr (ASK::POST)
+            rx = rms(sums.x, [&](pair by, pair& again) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    four f;
+                    unpack4(x[j], f);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        f[c] = mul2(f[c], by);
+                        again = fma2(f[c], f[c], again);
+                    }
+                }
+            });
+        if constexpr (ASK::KEPT) {
+            x_inv = code_factor(sums.y);
+            if (first && p.x_scale) p.x_scale[row] = code_scale(sums.y);
+        }
+    }
+    four h[VPT];
+    pair ss = 0;
+    float ah = 0.0f, ay = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        four f, w;
+        unpack4(x[j], f);
+        if (ASK::KEPT && p.x_codes && held[j]) p.x_codes[vec + j * n] = codes8(f, x_inv);
+        factor(j, w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] = mul2(f[c], ASK::POST ? mul2(two(rx), w[c]) : w[c]);
+        unpack4(r[j], w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            h[j][c] = fma2(two(p.residual_scale), w[c], f[c]);
+            if constexpr (ASK::PRE) ss = fma2(h[j][c], h[j][c], ss);
+        }
+        if constexpr (ASK::KEPT) ah = max_of(h[j], ah);
+        if constexpr (ASK::CODES) {
+            unpack4(pre[j], w);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c] = mul2(h[j][c], w[c]);
+            ay = max_of(w, ay);
+        }
+        if (p.residual_out && held[j]) p.residual_out[vec + j * n] = pack4(h[j]);
+    }
+    float rh = 1.0f, h_inv = 0.0f, y_inv = 0.0f;
+    if constexpr (ASK::PRE || ASK::KEPT) {
+        const float3 sums = block_sum_max2(sum_of(ss), ah, ay, red, turn);
+        if constexpr (ASK::PRE)
+            rh = rms(sums.x, [&](pair by, pair& again) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const pair v = mul2(h[j][c], by);
+                        again = fma2(v, v, again);
+                    }
+            });
+        if constexpr (ASK::KEPT) {
+            h_inv = code_factor(sums.y);
+            if (first && p.h_scale) p.h_scale[row] = code_scale(sums.y);
+        }
+        if constexpr (ASK::CODES) {
+            y_inv = code_factor(sums.z);
+            if (first) p.row_scale[row] = sums.z == 0.0f ? 1.0f : code_scale(sums.z) * rh;
+        }
+    }
+    if (first && p.rstd) p.rstd[row] = make_float2(rx, rh);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        if (ASK::KEPT && p.h_codes && held[j]) p.h_codes[vec + j * n] = codes8(h[j], h_inv);
+        if constexpr (ASK::PRE) {
+            four w, y;
+            unpack4(pre[j], w);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[c] = mul2(w[c], h[j][c]);
+                y[c] = mul2(w[c], two(rh));
+            }
+            if (held[j]) p.out[vec + j * n] = pack4(y);
+            if (ASK::CODES && held[j]) p.codes[vec + j * n] = codes8(w, y_inv);
+        }
+    }
+}
+
+// One block per row; thread i holds the row's vectors i, i + blockDim.x, ...
+template <class ASK, int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 448 ? 2 : 1) sandwich_norm_kernel(const __grid_constant__ SandwichArgs p) {
+    __shared__ float4 red[2][32];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int64_t row = blockIdx.x;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 x[VPT], r[VPT], pre[VPT];
+    bool held[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = threadIdx.x + j * blockDim.x;
+        held[j] = i < p.nv;
+        x[j] = held[j] ? p.x[row * p.x_vecs + i] : zero;
+        r[j] = held[j] && p.residual ? p.residual[row * p.nv + i] : zero;
+        pre[j] = ASK::PRE && held[j] ? __ldg(p.pre + i) : zero;
+    }
+    const uint4* gate = p.gate;
+    if (p.row_offsets) {
+        const int g = group_of(p.row_offsets, p.n_groups, row);
+        if (g < 0) return;  // the whole block
+        gate += (int64_t)g * p.nv;
+    }
+    auto factor = [&](int j, four& f) {
+        if (held[j]) {
+            block_factor(p, gate, ASK::POST ? p.post : nullptr, threadIdx.x + j * blockDim.x, f);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) f[c] = 0;
+        }
+    };
+    int turn = 0;
+    sandwich_row<ASK, VPT>(p, row, row * p.nv + threadIdx.x, blockDim.x, held, x, r, pre, factor, red, turn);
+}
+
+// Many wide rows: a block stays and takes rows [blockIdx.x chunk, + chunk) in order.
+// One thread asks for whole rows, STAGES - 1 ahead, into shared memory, where c
+// gate post of the group lies too; what is never fetched is zero there.
+constexpr int kNormVecs = 2, kNormSmem = (228 << 10) / 2 - 2048;  // of a block: two fit an SM
+template <class ASK, int STAGES>
+__global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_constant__ SandwichArgs p) {
+    constexpr int VPT = kNormVecs;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float4 red[2][32];  // 16 warps at most: its end holds the stages' barriers, that their rows have come
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int tid = threadIdx.x, n = blockDim.x;
+    const int64_t lo = (int64_t)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.rows);
+    const bool held[VPT] = {tid < p.nv, tid + n < p.nv};
+    const int stage_bytes = 2 * VPT * n * 16;
+    char* const own = smem + tid * 16;
+    ulonglong2* const factors = reinterpret_cast<ulonglong2*>(smem + STAGES * stage_bytes) + tid;
+    const uint32_t full = smem_u32(&red[1][30]);
+    auto fetch = [&](int64_t row, int stage) {
+        if (tid != 0 || row >= hi) return;
+        const uint32_t to = smem_u32(smem) + stage * stage_bytes, bar = full + 8 * stage, bytes = p.nv * 16;
+        mbar_arrive_expect_tx(bar, p.residual ? 2 * bytes : bytes);
+        bulk_load(to, p.x + row * p.x_vecs, bytes, bar);
+        if (p.residual) bulk_load(to + VPT * n * 16, p.residual + row * p.nv, bytes, bar);
+    };
+    uint4 pre[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        pre[j] = ASK::PRE && held[j] ? __ldg(p.pre + tid + j * n) : zero;
+        if (held[j] && p.residual) continue;
+        for (int at = 0; at < STAGES * stage_bytes; at += stage_bytes) {
+            *reinterpret_cast<uint4*>(own + at + (VPT + j) * n * 16) = zero;
+            if (!held[j]) *reinterpret_cast<uint4*>(own + at + j * n * 16) = zero;
+        }
+        if (!held[j]) factors[2 * j * n] = factors[(2 * j + 1) * n] = make_ulonglong2(0, 0);
+    }
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(full + 8 * s, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) fetch(lo + s, s);
+    auto open_group = [&](int group) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (!held[j]) continue;
+            four f;
+            block_factor(p, p.gate ? p.gate + (int64_t)group * p.nv : nullptr, ASK::POST ? p.post : nullptr, tid + j * n, f);
+            factors[2 * j * n] = make_ulonglong2(f[0], f[1]);
+            factors[(2 * j + 1) * n] = make_ulonglong2(f[2], f[3]);
+        }
+    };
+    bool open = !p.row_offsets, lost = false;
+    if (open) open_group(0);
+    const int rows = (int)(hi - lo);
+    int change = open ? rows : 0, stage = 0, parity = 0, turn = 0;
+    for (int i = 0; i < rows; ++i) {
+        // 2 s at most, and then for no other row: what is written from here on is NaN
+        if (!lost && !mbar_try_wait(full + 8 * stage, parity)) {
+            const uint64_t since = global_timer();
+            while (!lost && !mbar_try_wait(full + 8 * stage, parity)) lost = global_timer() - since > kWaitLimitNs;
+        }
+        if (i == change) {
+            const int group = group_of(p.row_offsets, p.n_groups, lo + i);
+            open = group >= 0;
+            change = i + 1;
+            if (open) {
+                change = (int)min(max((int64_t)p.row_offsets[group + 1] - lo, (int64_t)change), (int64_t)rows);
+                open_group(group);
+            }
+        }
+        if (open) {
+            const char* const in = own + stage * stage_bytes;
+            uint4 x[VPT], r[VPT];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                x[j] = *reinterpret_cast<const uint4*>(in + j * n * 16);
+                r[j] = *reinterpret_cast<const uint4*>(in + (VPT + j) * n * 16);
+                if (lost) x[j].x = r[j].x = 0xffffffffu;
+            }
+            sandwich_row<ASK, VPT>(
+                p, lo + i, (lo + i) * p.nv + tid, n, held, x, r, pre, [&](int j, four& f) { load4(factors + 2 * j * n, n, f); }, red,
+                turn);
+        }
+        // everybody has taken his part of the stage: they were at a barrier of
+        // the row since, where it has one (and nobody is a phase of the stage's
+        // own barrier behind)
+        if (!open || !(ASK::POST || ASK::PRE || ASK::KEPT))
+            __syncthreads();
+        else
+            __syncwarp();  // a block of one warp
+        fetch(lo + i + STAGES, stage);
+        if (++stage == STAGES) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+}
+
+// ------------------------------------------------------------ gradients --
 // How a row was kept.
 enum Kept : int { KEPT_NOT, KEPT_BF16, KEPT_E4M3 };
 __host__ __device__ constexpr int kept_bytes(int k) { return k == KEPT_E4M3 ? 8 : k == KEPT_BF16 ? 16 : 0; }
@@ -441,11 +472,6 @@ __device__ __forceinline__ void store4(float* to, const four& f) {
     reinterpret_cast<ulonglong2*>(to)[0] = make_ulonglong2(f[0], f[1]);
     reinterpret_cast<ulonglong2*>(to)[1] = make_ulonglong2(f[2], f[3]);
 }
-__device__ __forceinline__ void load4(const ulonglong2* at, int far, four& f) {
-    const ulonglong2 a = at[0], b = at[far];
-    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
-}
-
 constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = (227 << 10) - 1024;
 
 // A block takes rows [unit chunk, + chunk) in order; thread i holds the row's
