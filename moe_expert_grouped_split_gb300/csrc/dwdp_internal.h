@@ -289,6 +289,7 @@ struct SandwichGradArgs {
     float* partial;
     int64_t units, chunk;  // rows at once; rows a unit
     int size, share;       // blocks that share a row, vectors a block
+    int sum_warps;         // that add up a group's gate
 };
 size_t sandwich_grad_bytes(int64_t rows, int H);
 cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s);

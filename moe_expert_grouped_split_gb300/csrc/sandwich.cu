@@ -486,7 +486,8 @@ constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = (227 << 10) - 1024;
 //   mean(gn xhat) = mean(q e) - rh mean(gy hhat) mean(q hhat).
 // partial [units][4][H]: the sums for pre and post, and S of the group that
 // was begun before the unit's rows and of the one that goes on after them
-// (a group whose rows are all here goes to dgate at once).
+// (a group whose rows are all here goes to dgate at once).  With one group
+// for all rows its S takes post's place.
 // X, HK: how x and h were kept (HK KEPT_NOT: no pre norm); POST: a post norm;
 // THREADS at most (448: the compiler's order of things is 5% faster than for 512).
 // BULK: one thread asks for whole rows (16-byte addresses and sizes: bf16, or
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
     const bool to_dx[VPT] = {held[0] && p.dx, held[1] && p.dx};
     const bool to_dresidual[VPT] = {held[0] && p.dresidual, held[1] && p.dresidual};
     int group = 0, in = 0, turn = 0, stage = 0, parity = 0;
-    int64_t begin = 0, end = p.rows;  // of the group
+    int64_t begin = 0, end = p.rows, next_end = 0;  // of the group; of the one behind it
     bool open = !p.row_offsets, any = false, lost = false;
     // block_scale times a weight's or gate's elements (1 where there is none)
     auto scaled = [&](const uint4* w, int64_t vec, four& f) {
@@ -622,6 +623,14 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         }
     };
     auto close_group = [&]() {
+        if (!p.row_offsets) {  // one group: S is all that both gradients need
+            if (p.dpost || p.dgate) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if (held[j]) store4(partial + H + 8 * (first + j * n), sum[j]);
+            }
+            return;
+        }
         const bool whole = begin >= lo && end <= hi;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -671,14 +680,27 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         }
         if (r == change) {
             if (open) close_group();
-            group = group_of(p.row_offsets, p.n_groups, lo + r);
-            open = group >= 0;
+            const int64_t row = lo + r;
+            if (open && row == end && row < next_end) {  // the next group
+                ++group;
+            } else {
+                group = group_of(p.row_offsets, p.n_groups, row);
+                open = group >= 0;
+                next_end = open ? min((int64_t)p.row_offsets[group + 1], p.rows) : 0;
+            }
             change = r + 1;
             if (open) {
-                begin = max(p.row_offsets[group], 0);
-                end = min((int64_t)p.row_offsets[group + 1], p.rows);
+                begin = any ? row : max(p.row_offsets[group], 0);
+                end = next_end;
+                next_end = min((int64_t)p.row_offsets[min(group + 2, p.n_groups)], p.rows);
                 change = (int)min(max(end - lo, (int64_t)change), (int64_t)rows);
                 open_group();
+                if (group + 1 < p.n_groups && end < hi) {  // its gate on its way
+#pragma unroll
+                    for (int j = 0; j < VPT; ++j)
+                        if (held[j])
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.gate + (int64_t)(group + 1) * p.nv + first + j * n));
+                }
             }
         }
         if (open) {
@@ -776,30 +798,30 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         if (!held[j]) continue;
         const four none = {};
         if (PRE && p.dpre) store4(partial + 8 * i, dpre[j]);
-        if (POST && p.dpost && !any) store4(partial + H + 8 * i, none);
+        if (POST && p.dpost && p.row_offsets && !any) store4(partial + H + 8 * i, none);
     }
     if (SHARED) cluster_sync();  // no block leaves while another may write to it
 }
 
-// Adds up the units' sums, 64 columns a block.  blockIdx.y 0: pre, 1: post,
-// the units dealt to 16 warps; beyond, the groups' gates: 16 groups a block, a
-// warp each (PER_WARP), or one, its units dealt to the warps.  8 loads a lane
-// are on their way.
-constexpr int kSumWarps = 16;
-template <bool PER_WARP>
+// Adds up the units' sums, 64 columns a block of 16 warps.  blockIdx.y 0: pre,
+// 1: post (with one group for all rows, its S: post and the gate); beyond, the groups' gates, p.sum_warps warps a group.  A sum's units
+// are dealt to its warps, kSumLoads of each on their way.
+constexpr int kSumWarps = 16, kSumLoads = 12;
 __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __grid_constant__ SandwichGradArgs p) {
     __shared__ float2 red[kSumWarps][32];
     const int H = p.nv * 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 64 + 2 * lane;
-    const bool gates = blockIdx.y >= 2, alone = PER_WARP && gates;
-    const int group = !gates ? 0 : PER_WARP ? (blockIdx.y - 2) * kSumWarps + warp : blockIdx.y - 2;
+    const bool gates = blockIdx.y >= 2;
+    const uint32_t warps = gates ? p.sum_warps : kSumWarps, part = warp % warps;
+    const int group = gates ? (blockIdx.y - 2) * (kSumWarps / warps) + warp / warps : 0;
     float* to = gates ? p.dgate + (int64_t)group * H : blockIdx.y == 0 ? p.dpre : p.dpost;
     // (the kernel before let this one start when everything before it was done)
     uint32_t first = 0, last = (uint32_t)p.units;  // one behind the last unit
-    bool wanted = col < H;
+    const bool single = blockIdx.y == 1 && !p.row_offsets;
+    bool wanted = col < H && (to != nullptr || (single && p.dgate));
     if (gates) {
         if (group >= p.n_groups) {
             wanted = false;
-        } else if (p.row_offsets) {
+        } else {
             const uint32_t begin = max(p.row_offsets[group], 0), chunk = (uint32_t)p.chunk;
             const uint32_t end = min((uint32_t)max(p.row_offsets[group + 1], 0), (uint32_t)p.rows);
             first = begin / chunk;
@@ -810,40 +832,42 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __g
     // (before any return: who comes next waits for this kernel only)
     wait_for_previous_kernel();
     let_next_kernel_start();
-    if (!gates && !to) return;
     float2 s = make_float2(0.0f, 0.0f);
     if (wanted) {
         const float* from = p.partial + (gates ? 2 : blockIdx.y) * (int64_t)H + col;
-        const uint32_t step = alone ? 1 : kSumWarps;
-#pragma unroll 8
-        for (uint32_t b = first + (alone ? 0 : warp); b < last; b += step) {
-            // the group begun in its first unit lies in the slot behind
-            const float2 v = *reinterpret_cast<const float2*>(from + ((int64_t)b * 4 + (gates && b == first)) * H);
-            s.x += v.x;
-            s.y += v.y;
-        }
-    }
-    if (!alone) {
-        red[warp][lane] = s;
-        __syncthreads();
-        if (warp != 0) return;
+        for (uint32_t b0 = first + part; b0 < last; b0 += kSumLoads * warps) {
+            float2 v[kSumLoads];
 #pragma unroll
-        for (int w = 1; w < kSumWarps; ++w) {
-            s.x += red[w][lane].x;
-            s.y += red[w][lane].y;
+            for (int i = 0; i < kSumLoads; ++i) {
+                const uint32_t b = b0 + i * warps;
+                // the group begun in its first unit lies in the slot behind
+                v[i] = b < last ? *reinterpret_cast<const float2*>(from + ((int64_t)b * 4 + (gates && b == first)) * H)
+                                : make_float2(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < kSumLoads; ++i) {
+                s.x += v[i].x;
+                s.y += v[i].y;
+            }
         }
     }
-    if (!wanted) return;
-    if (gates) {
-        float2 by = make_float2(p.block_scale, p.block_scale);
-        if (p.post) {
-            const float2 w = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(p.post)[col / 2]);
-            by.x *= w.x;
-            by.y *= w.y;
-        }
-        s.x *= by.x;
-        s.y *= by.y;
+    red[warp][lane] = s;
+    __syncthreads();
+    if (part != 0 || !wanted) return;
+    for (int w = warp + 1; w < warp + (int)warps; ++w) {
+        s.x += red[w][lane].x;
+        s.y += red[w][lane].y;
     }
+    auto times = [&](const uint4* w) {  // c w S
+        const float2 f = w ? __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(w)[col / 2]) : make_float2(1.0f, 1.0f);
+        return make_float2(s.x * p.block_scale * f.x, s.y * p.block_scale * f.y);
+    };
+    if (single) {
+        if (p.dpost) *reinterpret_cast<float2*>(p.dpost + col) = times(p.gate);
+        if (p.dgate) *reinterpret_cast<float2*>(p.dgate + col) = times(p.post);
+        return;
+    }
+    if (gates) s = times(p.post);
     *reinterpret_cast<float2*>(to + col) = s;
 }
 
@@ -897,14 +921,16 @@ cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
 
 // Which kernel.  us with a post norm, kept rows and no codes: a block a row, one
 // vector a thread / the same, two a thread / staying blocks.
-//   rows   H 512               2048                7168
-//    152   2.3 / 2.6 / 3.5     2.4 / 2.8 / 3.8      3.8 /  4.2 /  4.7
-//    608   2.5 / 2.7 / 3.5     3.6 / 5.0 / 5.5     16.1 / 12.2 / 12.1
-//   1216   2.8 / 3.2 / 3.9     8.1 / 8.1 / 9.7     30.3 / 21.6 / 20.5
-//   4864   7.7 / 7.3 / 9.2    24.8 / 20.6 / 23.7    112 / 72.6 / 63.1
-//  16384         18 / 19             60 / 61               232 / 193
+//   rows   H 512               2048                4096                7168
+//    152   2.3 / 2.6 /  3.4    2.5 / 2.8 /  3.6    2.8 / 3.1 /  3.8     3.7 /  3.7 /  4.4
+//    608   2.5 / 2.7 /  3.4    3.6 / 4.3 /  5.0    8.2 / 8.4 /  9.0    15.5 / 11.2 / 11.3
+//   1216   2.8 / 3.1 /  3.7    7.7 / 7.6 /  9.1   14.7 / 13.0 / 13.4   29.4 / 19.8 / 19.0
+//   4864   7.4 / 6.8 /  8.8   24.2 / 19.0 / 22.4  49.4 / 39.5 / 37.0    107 / 65.3 / 61.1
+//  16384  19.1 / 17.5 / 19.1  72.7 / 55.4 / 60.5   157 / 121 / 113      355 / 209 / 190
 // So one vector a thread while all rows' blocks are on the SMs at once (64
-// registers a thread), then two; staying blocks for many wide rows.
+// registers a thread), then two; staying blocks for many wide rows (16384 x
+// 7168: 92% of the copy rate).  Wider rows than 8192 are read by a block a row:
+// 4864 x 12288 156 us (57%), x 16384 197 (60%), x 32768 700 (34%: spills).
 template <class ASK>
 cudaError_t launch_norm(SandwichArgs& p, cudaStream_t s) {
     const int nv = p.nv, threads1 = (nv + 31) / 32 * 32, threads2 = ((nv + 1) / 2 + 31) / 32 * 32;
@@ -962,12 +988,14 @@ cudaError_t launch_sandwich_grad(SandwichGradArgs& p, cudaStream_t s) {
                           : !p.x_scale ? (p.post ? launch_grad<KEPT_BF16, true>(p, s) : launch_grad<KEPT_BF16, false>(p, s))
                                        : (p.post ? launch_grad<KEPT_E4M3, true>(p, s) : launch_grad<KEPT_E4M3, false>(p, s));
     if (e != cudaSuccess || (!p.dpre && !p.dpost && !p.dgate)) return e;
-    const unsigned tiles = (H + 63) / 64;
-    // a warp each from few units a group on (1003 x 2048, 11 groups of 45 units: 20 us, 38 with a warp each)
-    if (!p.dgate || p.n_groups * 8 < p.units)
-        return launch_dependent(sandwich_sums_kernel<false>, p, dim3(tiles, 2 + (p.dgate ? p.n_groups : 0)), 32 * kSumWarps, 0, s);
-    return launch_dependent(sandwich_sums_kernel<true>, p, dim3(tiles, 2 + (p.n_groups + kSumWarps - 1) / kSumWarps),
-                            32 * kSumWarps, 0, s);
+    // a warp for every 8 units of a group, on average
+    int blocks = 2;
+    p.sum_warps = 1;
+    if (p.dgate && p.row_offsets) {
+        while (p.sum_warps < kSumWarps && (int64_t)p.sum_warps * 8 * p.n_groups < p.units) p.sum_warps *= 2;
+        blocks += (p.n_groups * p.sum_warps + kSumWarps - 1) / kSumWarps;
+    }
+    return launch_dependent(sandwich_sums_kernel, p, dim3((H + 63) / 64, blocks), 32 * kSumWarps, 0, s);
 }
 
 }  // namespace dwdp
