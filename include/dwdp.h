@@ -464,7 +464,7 @@ int32_t dwdp_group_map(int32_t n_experts, int32_t n_ranks, int32_t rank, int32_t
  * The three calls below surround dwdp_moe_layer in a decoder block: the
  * adapters of the attention's output projection (the projection itself is
  * dwdp_grouped_gemm with one group), the residual addition with the norm, and
- * the router of the R1 models.  They serve (no gradients), for one token as
+ * the router of the R1 models.  They serve, for one token as
  * for many, and can be captured into CUDA graphs. */
 
 /* Residual addition and root-mean-square norm, optionally also as E4M3 rows

@@ -518,7 +518,8 @@ class SandwichNorm:
     type, shape and device (ValueError) and forward to the C ABI; outputs
     that are not asked for stay None.  pre_weight, post_weight: bf16 [H] or None.
     gate: bf16 [H] or [groups, H], with row_offsets int32 [groups + 1], up to
-    max_groups of them."""
+    max_groups of them.  One object serves one host thread, and its gradients,
+    captured ones too, one stream at a time (they share its workspace)."""
 
     def __init__(self, H, max_rows, pre_weight=None, post_weight=None, block_scale=1.0, residual_scale=1.0, eps=1e-6,
                  max_groups=1, device="cuda"):
@@ -714,8 +715,8 @@ class Runtime:
         dwdp_balance_workspace_bytes(...))."""
         device, call = _device(), "balance_loss"
         T, lp, ip, op = self._router(call, device, logits, topk_ids, seq_offsets, out.n_seqs)
-        if out.E != self.cfg["n_experts"]:
-            raise ValueError(f"{call}: buffers for {out.E} experts")
+        if out.E != self.cfg["n_experts"] or out.counts.get_device() != device:
+            raise ValueError(f"{call}: buffers for {out.E} experts on {out.counts.device}")
         rc = lib().dwdp_balance_loss(self.ctx, lp, ip, T, op, out.n_seqs, how, out.counts.data_ptr(),
                                      out.mean_p.data_ptr(), out.balance.data_ptr(), _ptr(out.z), self.ws.data_ptr(),
                                      self.ws_bytes, _stream(stream))

@@ -4,11 +4,10 @@
 //
 // Forward, per row: x stays in registers for its sum of squares, h for its
 // own; two reductions a row, which also carry the largest magnitudes that the
-// E4M3 rows' scales need.  Backward, per row: two reductions, the means of
-// (dout pre) h and of (dn post) x; the weights' and gates' gradients are sums
-// over rows, which each block keeps in registers for the rows it takes, one
-// after the other, and a second kernel adds up in the blocks' order: the same
-// bits from run to run.
+// E4M3 rows' scales need.  Backward, per row: one reduction; the weights' and
+// gates' gradients are sums over rows, which each block keeps in registers for
+// the rows it takes, one after the other, and a second kernel adds up in the
+// blocks' order: the same bits from run to run.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -425,7 +424,6 @@ __device__ __forceinline__ void values(const char* at, pair by, four& f) {
     for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], by);
 }
 
-
 // The sums of a, b and c over the `size` blocks (4 at most) that share a row,
 // for every thread.  A warp's three sums together: half of the lanes go on
 // with each value, and eight lanes end with each, one of them for each block.
@@ -472,14 +470,15 @@ __device__ __forceinline__ void store4(float* to, const four& f) {
     reinterpret_cast<ulonglong2*>(to)[0] = make_ulonglong2(f[0], f[1]);
     reinterpret_cast<ulonglong2*>(to)[1] = make_ulonglong2(f[2], f[3]);
 }
+
 constexpr int kGradVecs = 2, kGradStages = 3, kGradSmem = (227 << 10) - 1024;
 
 // A block takes rows [unit chunk, + chunk) in order; thread i holds the row's
 // vectors i and i + blockDim.x and their columns' sums.  Rows of more than
 // 8192 elements are shared by a cluster of blocks, each with its part of the
-// columns (SHARED).  Of the weights'
-// gradients only two sums a column have to be kept while rows go by: dout
-// hhat, and S = dh xhat since the group began, as dgate = c post S and
+// columns (SHARED).  Of the weights' gradients only two sums a column have to
+// be kept while rows go by (HBM bounds this only if a row costs a warp few
+// enough instructions: 128 registers a thread leave an SM 16 warps): dout hhat, and S = dh xhat since the group began, as dgate = c post S and
 // dpost_weight = sum over groups of c gate S.  The rows kGradStages ahead are
 // on their way into shared memory.  One reduction a row: with e = dres + rh gy
 // and q = c gate post xhat,
@@ -867,7 +866,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sums_kernel(const __g
         if (p.dgate) *reinterpret_cast<float2*>(p.dgate + col) = times(p.post);
         return;
     }
-    if (gates) s = times(p.post);
+    if (gates && first < last) s = times(p.post);  // (a group without rows: zeros)
     *reinterpret_cast<float2*>(to + col) = s;
 }
 
@@ -930,7 +929,7 @@ cudaError_t launch_grad(SandwichGradArgs& p, cudaStream_t s) {
 // So one vector a thread while all rows' blocks are on the SMs at once (64
 // registers a thread), then two; staying blocks for many wide rows (16384 x
 // 7168: 92% of the copy rate).  Wider rows than 8192 are read by a block a row:
-// 4864 x 12288 156 us (57%), x 16384 197 (60%), x 32768 700 (34%: spills).
+// 4864 x 12288 143 us (62%), x 16384 177 (67%), x 32768 359 (66%).
 template <class ASK>
 cudaError_t launch_norm(SandwichArgs& p, cudaStream_t s) {
     const int nv = p.nv, threads1 = (nv + 31) / 32 * 32, threads2 = ((nv + 1) / 2 + 31) / 32 * 32;

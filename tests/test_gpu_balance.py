@@ -405,7 +405,7 @@ def test_refuses_what_it_would_misread():
     f()
     for bad in (dict(logits=m.z.bfloat16()), dict(logits=m.z[:, :32]), dict(logits=m.z.cpu()), dict(topk_ids=m.ids.long()),
                 dict(topk_ids=m.ids[:8]), dict(topk_ids=m.ids[:, :2]), dict(seq_offsets=m.offsets.long()), dict(seq_offsets=None),
-                dict(seq_offsets=m.offsets[:2]), dict(out=B.BalanceBuffers(2, 32)), dict(out=B.BalanceBuffers(3, 64))):
+                dict(seq_offsets=m.offsets[:2]), dict(out=B.BalanceBuffers(2, 32)), dict(out=B.BalanceBuffers(3, 64)), dict(out=B.BalanceBuffers(2, 64, device="cpu"))):
         with pytest.raises(ValueError):
             f(**bad)
     with pytest.raises(B.DwdpError):  # more than max_tokens

@@ -193,6 +193,52 @@ def test_in_place(H):
     assert torch.equal(x, apart["out"]) and torch.equal(r, apart["residual_out"])
 
 
+def test_in_place_with_rows_fetched_ahead():
+    m = Made(1300, 7168, groups=[0, 5, 700, 1300])
+    apart = m.forward(kept=False)
+    x, r = m.x.clone(), m.residual.clone()
+    m.norm.forward(x, r, gate=m.gate, row_offsets=m.offsets, residual_out=r, out=x)
+    torch.cuda.synchronize()
+    assert torch.equal(x, apart["out"]) and torch.equal(r, apart["residual_out"])
+    g = Grads(m)
+    o = g.run()
+    g.call(dx=g.dout, dresidual=g.dres)
+    torch.cuda.synchronize()
+    assert torch.equal(g.dout, o["dx"]) and torch.equal(g.dres, o["dresidual"])
+
+
+@pytest.mark.parametrize("H", [512, 7168, 8192, 12296])
+@pytest.mark.parametrize("form", [dict(), dict(pre=False), dict(post=False), dict(post=False, pre=False)], ids=str)
+def test_many_rows_of_which_some_are_in_no_group(H, form):
+    """Blocks that pass over rows, at their start, at their end, and altogether."""
+    rows = 6000 if H == 512 else 2500
+    m = Made(rows, H, groups=[700, 705, 705, rows - 903, rows - 31], **form)
+    o = m.forward()
+    m.check_forward(o)
+    out = ~m.inside
+    for name, t in m.outputs().items():
+        assert torch.equal(o[name][out].view(torch.uint8), t[out].view(torch.uint8)), name
+    for x8 in (False, True):
+        g = Grads(m, x8, x8 and m.pre is not None)
+        b = g.run()
+        g.check(b)
+        for n in ("dx", "dresidual"):
+            assert torch.isnan(b[n][out]).all()
+
+
+@pytest.mark.parametrize("pad", [8, 16, 64])
+@pytest.mark.parametrize("H", [64, 2048, 7168])
+def test_gradients_from_codes_whose_rows_lie_apart(H, pad):
+    g = Grads(Made(330, H, groups=[0, 100, 330]), True, True)
+    o = g.run()
+    wide = torch.full((330, H + pad), 3.0, device="cuda").to(F8)
+    wide[:, :H] = g.x
+    g.x = wide[:, :H]
+    again = g.run()
+    for n in o:
+        near(again[n], *g.formula()[n], g.m.inside if n in ("dx", "dresidual") else None)
+
+
 def test_is_add_rmsnorm_without_its_extras():
     m = Made(65, 1536, post=False, groups=None)
     m.norm = B.SandwichNorm(m.H, m.rows, m.pre, None, 1.0, 1.0, EPS)
