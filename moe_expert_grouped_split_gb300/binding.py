@@ -178,10 +178,12 @@ def _device() -> int:
 def _like(call, device, name, t, dtypes, shape) -> int | None:
     """t's address; ValueError unless it is None or a dense tensor of one of
     `dtypes` and of `shape` on the current device: the library gets addresses
-    only.  (0.5 us a tensor.)"""
+    only.  (0.35 us a tensor.)"""
     if t is None:
         return None
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+    d = t.dtype
+    if ((d is not dtypes[0] and d not in dtypes) or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != device):
         raise ValueError(f"{call}: {name} {t.dtype} {list(t.shape)} strides {list(t.stride())} on {t.device}: "
                          f"{' or '.join(str(d) for d in dtypes)} {list(shape)}, dense, on cuda:{device} is needed")
     return t.data_ptr()
@@ -545,13 +547,16 @@ class SandwichNorm:
 
     def _rows_of(self, call, device, x, codes=False):
         """(rows, stride, address) of x, whose rows may lie apart."""
-        if (x.dim() != 2 or x.shape[1] != self.H or x.dtype not in (self._e4m3 if codes else self._bf16)
-                or x.stride(1) != 1 or x.get_device() != device or x.shape[0] > self.max_rows):
+        shape, H = x.shape, self.H
+        rows = shape[0] if len(shape) == 2 else -1
+        stride = x.stride(0) if rows > 1 else H
+        if (rows < 0 or shape[1] != H or x.dtype not in (self._e4m3 if codes else self._bf16)
+                or x.get_device() != device or rows > self.max_rows
+                or not (x.is_contiguous() or x.stride(1) == 1)):
             raise ValueError(f"{call}: x {x.dtype} {list(x.shape)} strides {list(x.stride())} on {x.device}: "
                              f"{'E4M3' if codes else 'bf16'} rows of {self.H}, {self.max_rows} at most, on cuda:{device} "
                              "are needed")
-        rows = x.shape[0]
-        return rows, x.stride(0) if rows > 1 else self.H, x.data_ptr()
+        return rows, stride, x.data_ptr()
 
     def _set_groups(self, call, device, gate, row_offsets) -> int:
         how = self._how
@@ -575,16 +580,29 @@ class SandwichNorm:
         row_scale, x_scale, h_scale [rows] and rstd [rows, 2] fp32."""
         device, call = _device(), "sandwich norm"
         rows, stride, xp = self._rows_of(call, device, x)
-        self._set_groups(call, device, gate, row_offsets)
-        bf16, e4m3, f32, full, one = self._bf16, self._e4m3, self._f32, (rows, self.H), (rows,)
-        like = _like
-        rc = lib().dwdp_sandwich_norm(
-            self._how, xp, stride, like(call, device, "residual", residual, bf16, full), rows, self.H,
-            like(call, device, "residual_out", residual_out, bf16, full), like(call, device, "out", out, bf16, full),
-            like(call, device, "codes", codes, e4m3, full), like(call, device, "row_scale", row_scale, f32, one),
-            like(call, device, "x_codes", x_codes, e4m3, full), like(call, device, "x_scale", x_scale, f32, one),
-            like(call, device, "h_codes", h_codes, e4m3, full), like(call, device, "h_scale", h_scale, f32, one),
-            like(call, device, "rstd", rstd, f32, (rows, 2)), _stream(stream))
+        if gate is not None or row_offsets is not None or self._how.n_groups:
+            self._set_groups(call, device, gate, row_offsets)
+        like, bf16, full = _like, self._bf16, (rows, self.H)
+        rp = rop = op = cp = rsp = xcp = xsp = hcp = hsp = sp = None
+        if residual is not None:
+            rp = like(call, device, "residual", residual, bf16, full)
+        if residual_out is not None:
+            rop = like(call, device, "residual_out", residual_out, bf16, full)
+        if out is not None:
+            op = like(call, device, "out", out, bf16, full)
+        if codes is not None or row_scale is not None:
+            cp = like(call, device, "codes", codes, self._e4m3, full)
+            rsp = like(call, device, "row_scale", row_scale, self._f32, (rows,))
+        if x_codes is not None or x_scale is not None:
+            xcp = like(call, device, "x_codes", x_codes, self._e4m3, full)
+            xsp = like(call, device, "x_scale", x_scale, self._f32, (rows,))
+        if h_codes is not None or h_scale is not None:
+            hcp = like(call, device, "h_codes", h_codes, self._e4m3, full)
+            hsp = like(call, device, "h_scale", h_scale, self._f32, (rows,))
+        if rstd is not None:
+            sp = like(call, device, "rstd", rstd, self._f32, (rows, 2))
+        rc = (_lib or lib()).dwdp_sandwich_norm(self._how, xp, stride, rp, rows, self.H, rop, op, cp, rsp, xcp, xsp, hcp,
+                                                hsp, sp, _stream(stream))
         if rc:
             _check(None, rc)
 
