@@ -880,10 +880,11 @@ struct GradShape {
     }
     // As many units (rows at once) as a GB300's 152 SMs hold at 128 registers
     // a thread and `smem` bytes a block (the workspace: 0), but no more than one
-    // an SM for less than two rows each (1003 x 2048: 19.6 us, 22.4 otherwise).
+    // an SM for less than three rows each (1003 x 2048, 11 gates, 8 bits: 16.3 us;
+    // one row each 18.2, six 18.7).
     int64_t units(int64_t rows, size_t smem) const {
         const int64_t blocks = std::min<int64_t>(512 / threads, (228 << 10) / (smem + 1024));
-        return std::max<int64_t>(1, std::min({rows, 152 * blocks / size, std::max<int64_t>(152 / size, rows / 2)}));
+        return std::max<int64_t>(1, std::min({rows, 152 * blocks / size, std::max<int64_t>(152 / size, rows / 3)}));
     }
 };
 
