@@ -804,8 +804,11 @@ cudaError_t by_experts(int E, F f) {
     return by_rows<32, 8>(E, f);
 }
 
-// Few tokens: one kernel of a cluster a sequence.
-bool balance_is_few(int64_t T, int n_seqs) { return T <= 4096 && n_seqs <= 4096; }
+// Few tokens: one kernel of a cluster a sequence.  us for 256 experts, sigmoid, z
+// loss, one kernel / two: 256 tokens in 1 sequence 4.4 / 6.6, 768 in 1 6.5 / 8.1, 1024
+// in 1 7.6 / 6.7, 2048 in 1 12.2 / 7.6, in 4 5.7 / 7.0, 8192 in 16 7.4 / 8.8, 16384 in
+// 64 11.0 / 10.5.
+bool balance_is_few(int64_t T, int n_seqs) { return T <= 8192 && T <= 768 * (int64_t)n_seqs && n_seqs <= 4096; }
 // Tokens of a block of the losses' kernel: two blocks an SM of a GB300's 152,
 // whole rounds of a block's warps.
 int balance_chunk(int64_t T, int E) {
