@@ -485,7 +485,7 @@ __global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(32 * kWarps
 // those without tokens.  A block each (CLUSTER: 8, where a sequence has many
 // blocks' sums: an SM takes in 600 KB in 6 us); 4 threads a column at most.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_constant__ BalanceArgs p) {
+__global__ void __launch_bounds__(1024, 1) balance_finish_kernel(const __grid_constant__ BalanceArgs p) {
     __shared__ float sums[4][DWDP_MAX_EXPERTS];
     __shared__ int counts[4][DWDP_MAX_EXPERTS];
     __shared__ float red[32], z_all;
@@ -506,11 +506,22 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
     if (part < parts) {
         float s = 0.0f;
         int n = 0;
-#pragma unroll 8
-        for (int i = first + rank * parts + part; i <= last; i += kBlocks * parts) {
-            const int64_t at = ((int64_t)i * 2 + (i == first ? 1 : 0)) * p.E + e;
-            s += p.part_p[at];
-            n += p.part_counts[at];
+        constexpr int kLoads = 6;  // of each on their way
+        for (int i0 = first + rank * parts + part; i0 <= last; i0 += kLoads * kBlocks * parts) {
+            float v[kLoads];
+            int m[kLoads];
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int i = i0 + j * kBlocks * parts;
+                const int64_t at = ((int64_t)i * 2 + (i == first ? 1 : 0)) * p.E + e;
+                v[j] = i <= last ? p.part_p[at] : 0.0f;
+                m[j] = i <= last ? p.part_counts[at] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                s += v[j];
+                n += m[j];
+            }
         }
         sums[part][e] = s;
         counts[part][e] = n;
