@@ -693,17 +693,15 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
         }
         // u = exp(-c) s and r = 1 - s (softmax: 1) of every expert and of the
         // chosen ones, and all sums at once: of u, u g, and the chosen ones' u, u dw
-        float c = 0.0f, chosen_c = 0.0f, chosen_u[KPL], chosen_r[KPL], z_sum, chosen_one;
+        float c = 0.0f, chosen_c = 0.0f, chosen_u[KPL], chosen_r[KPL], chosen_one;
         float4 sums;
         auto terms = [&](bool far) {
             const float one = far && SIGMOID ? exp_fast(c) : 1.0f;
             chosen_one = far && SIGMOID ? exp_fast(chosen_c) : 1.0f;
             float a = 0.0f, b = 0.0f, chosen_a = 0.0f, chosen_b = 0.0f;
-            z_sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
                 e[i] = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
-                z_sum += e[i];
                 if constexpr (SIGMOID) {
                     r[i] = rcp_fast(far ? fmaf(e[i], one, 1.0f) : e[i] + 1.0f);
                     e[i] *= r[i];
@@ -754,6 +752,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             for (int i = 0; i < 4 * V; ++i) d[i] = 0.0f;
         }
         if (p.dbalance || !direct) {
+            // (shares first: one_sum twice could pass binary32's range)
             const float mean = sums.y * one_sum;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
@@ -762,12 +761,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             }
         }
         if (p.dz) {
-            float z_c = c;
-            z_sum = token_sum<LANES>(z_sum);
-            if (__any_sync(0xffffffffu, !(z_sum <= kMost))) z_sum = soft_terms<LANES, V>(z, e, z_c);  // logits of 79 and more
-            const float by = by_z * log_of(z_sum, z_c), one_z = rcp_fast(z_sum);
+            float z_c;
+            const float z_sum = soft_terms<LANES, V>(z, e, z_c), by = by_z * log_of(z_sum, z_c) * rcp_fast(z_sum);
 #pragma unroll
-            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(by, exp_fast(z[i] - z_c) * one_z, d[i]);
+            for (int i = 0; i < 4 * V; ++i) d[i] = fmaf(by, e[i], d[i]);
         }
         if (in) {
 #pragma unroll
