@@ -665,8 +665,8 @@ int32_t dwdp_sandwich_norm(const dwdp_sandwich* how, const void* x, int64_t x_st
  * elements) holds for x's codes too; h is dense.  dresidual may be
  * dresidual_out and dx may be dout; no other overlap.  The rest as for
  * dwdp_sandwich_norm.  ws: dwdp_sandwich_grad_workspace_bytes(rows,
- * H) bytes (device), needed for the sums only.  Errors: INVALID_ARG,
- * UNSUPPORTED, CUDA. */
+ * H) bytes (device), needed for the sums only; calls that may overlap, replays of
+ * captured ones too, need one each.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int32_t dwdp_sandwich_norm_grad(const dwdp_sandwich* how, const void* x, int64_t x_stride, const float* x_scale,
                                 const void* h, const float* h_scale, const float* rstd, const void* dout,
                                 const void* dresidual_out, int64_t rows, int32_t H, void* dx, void* dresidual,
@@ -693,7 +693,7 @@ size_t dwdp_sandwich_grad_workspace_bytes(int64_t rows, int32_t H);
  * make its sequence's mean_p, balance and z NaN.  An id outside [0, E) is not
  * counted; the device error word reports it (DEVICE_CHECK).  T at most
  * max_tokens and 2^30.  ws: dwdp_balance_workspace_bytes(T, E, n_seqs) bytes,
- * device.  All pointers 16-byte aligned.  Enqueued on `stream`.
+ * device, one for each of calls that may overlap.  All pointers 16-byte aligned.  Enqueued on `stream`.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int32_t dwdp_balance_loss(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, int32_t T,
                           const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring, int32_t* counts,
