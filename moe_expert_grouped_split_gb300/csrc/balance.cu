@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(32 * kWarps) balance_kernel(const __grid_const
 // through shared memory and finishes it, in one kernel.
 constexpr int kFewBlocks = 8;
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // the barrier is the whole warp's; lanes took more or fewer columns
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t from_rank(const void* own, int rank) {
