@@ -449,6 +449,7 @@ __device__ __forceinline__ float3 row_sums(float a, float b, float c, float* red
             asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(w));
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(s) : "memory");
         }
+        __syncwarp();  // the cluster's barrier is the whole warp's
         cluster_sync();
         s = 0.0f;
         for (int e = w; e < size * nw; e += 8) s += r[e * 4 + i];
@@ -659,7 +660,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         any = true;
     };
     if (open) open_group();
-    if (SHARED) cluster_sync();  // all blocks are there to be written to
+    if (SHARED) {
+        __syncwarp();
+        cluster_sync();  // all blocks are there to be written to
+    }
     const int rows = (int)(hi - lo);
     int change = open ? rows : 0;  // the row at which the group has to be looked up again
     for (int r = 0; r < rows; ++r) {
@@ -799,7 +803,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         if (PRE && p.dpre) store4(partial + 8 * i, dpre[j]);
         if (POST && p.dpost && p.row_offsets && !any) store4(partial + H + 8 * i, none);
     }
-    if (SHARED) cluster_sync();  // no block leaves while another may write to it
+    if (SHARED) {
+        __syncwarp();
+        cluster_sync();  // no block leaves while another may write to it
+    }
 }
 
 // Adds up the units' sums, 64 columns a block of 16 warps.  blockIdx.y 0: pre,
