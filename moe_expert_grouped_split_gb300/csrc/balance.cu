@@ -27,7 +27,8 @@ constexpr int kWarps = 16, kGradWarps = 8;  // of a block: the losses', the grad
 // A token's choices in each of its lanes, for the most that E experts can have.
 __host__ __device__ constexpr int choices_a_lane(int lanes) { return lanes >= 32 ? 1 : lanes == 16 ? 2 : 4; }
 constexpr float kLeast = 1e-20f, kMost = 1e34f;
-// exp(kTop) is 2^125.99, so that its reciprocal is no subnormal; from 79 on a sum is beyond kMost
+// exp(kTop) is 2^125.99, the most whose reciprocal is no subnormal, which
+// would be taken for 0: a sigmoid's exponents stop there, where 1 - s is 2^-126.
 constexpr float kTop = 87.33f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -197,7 +198,7 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         sum = z_sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
-            const float t = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
+            const float t = exp_fast(min_nan(far ? z[i] - c : z[i], kTop));
             r[i] = rcp_fast(far ? fmaf(t, one, 1.0f) : t + 1.0f);
             u[i] = t * r[i];
             sum += u[i];
@@ -212,7 +213,7 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         }
     };
     terms(false, 1.0f);
-    const bool lost = !(sum >= kLeast);  // too small, or a logit so large that u is inf 0
+    const bool lost = !(sum >= kLeast);
     if (__any_sync(0xffffffffu, lost)) {
         float m = -CUDART_INF_F;
 #pragma unroll
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             float a = 0.0f, b = 0.0f, chosen_a = 0.0f, chosen_b = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
-                e[i] = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
+                e[i] = far || SIGMOID ? exp_fast(min_nan(far ? z[i] - c : z[i], kTop)) : exp_fast(z[i]);
                 if constexpr (SIGMOID) {
                     r[i] = rcp_fast(far ? fmaf(e[i], one, 1.0f) : e[i] + 1.0f);
                     e[i] *= r[i];
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
         };
         terms(false);
         {
-            const bool lost = !(sums.x >= kLeast && sums.x <= kMost);  // a sigmoid's u is inf 0 of a large logit
+            const bool lost = !(sums.x >= kLeast && sums.x <= kMost);
             const bool chosen_lost = p.dw && p.renorm && !(sums.z >= kLeast && sums.z <= kMost);
             if (__any_sync(0xffffffffu, lost || chosen_lost)) {
                 float m = -CUDART_INF_F, chosen_m = -CUDART_INF_F;
