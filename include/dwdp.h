@@ -705,7 +705,9 @@ size_t dwdp_balance_workspace_bytes(int32_t T, int32_t E, int32_t n_seqs);
 /* The gradient of dwdp_route_scored's logits, from that of its weights and
  * from dwdp_balance_loss's losses:
  *   dlogits = d/dz ( sum dtopk_w topk_w + sum_b dbalance[b] balance[b] + dz[b] z[b] )
- * with the choice and the counts held fixed.  dtopk_w fp32 [T][k], dbalance and
+ * with the choice and the counts held fixed, for a routing without choice_bias or
+ * with one that took no expert out (-inf; else dwdp_route_scored_biased_grad).
+ * dtopk_w fp32 [T][k], dbalance and
  * dz fp32 [n_seqs] (device): each NULL = 0.  counts as dwdp_balance_loss wrote them
  * (needed with dbalance; counts added up over several devices, with dbalance to
  * match, serve as well).  Tokens in no sequence get the weights' part only.
@@ -718,6 +720,16 @@ int32_t dwdp_route_scored_grad(dwdp_ctx* ctx, const float* logits, const int32_t
                                int32_t T, const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring,
                                const int32_t* counts, const float* dbalance, const float* dz, void* dlogits,
                                int32_t dlogits_bf16, dwdp_stream_t stream);
+
+/* The same where choice_bias (fp32 [E], device, or NULL), as dwdp_route_scored
+ * got it, takes experts out: one that filled a choice up has the weight 0, no
+ * part of the sum that the others are divided by, and no gradient from its
+ * weight.  (In counts, and so in the balance loss, it is a chosen one.) */
+int32_t dwdp_route_scored_biased_grad(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids,
+                                      const float* dtopk_w, const float* choice_bias, int32_t T,
+                                      const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring,
+                                      const int32_t* counts, const float* dbalance, const float* dz, void* dlogits,
+                                      int32_t dlogits_bf16, dwdp_stream_t stream);
 
 #ifdef __cplusplus
 }

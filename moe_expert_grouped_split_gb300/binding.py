@@ -126,6 +126,8 @@ SIGNATURES = [
     ("dwdp_balance_workspace_bytes", ctypes.c_size_t, [_I32, _I32, _I32]),
     ("dwdp_route_scored_grad", _I32, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, ctypes.POINTER(dwdp_scoring), _VP, _VP, _VP,
                                       _VP, _I32, _VP]),
+    ("dwdp_route_scored_biased_grad", _I32, [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _I32, ctypes.POINTER(dwdp_scoring),
+                                             _VP, _VP, _VP, _VP, _I32, _VP]),
     ("dwdp_plan_prefetch", _I32, [_I32, _I32, _I32, _I32, _I32P, _I32P, _I32P, _I32, ctypes.c_size_t,
                                   ctypes.POINTER(dwdp_copy_slice), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
 ]
@@ -365,10 +367,11 @@ def dwdp_balance_workspace_bytes(T, E, n_seqs) -> int:
 
 
 def dwdp_route_scored_grad(ctx, logits, topk_ids, dtopk_w, T, seq_offsets, n_seqs, how: dwdp_scoring, counts, dbalance,
-                           dz, dlogits, dlogits_bf16=0, stream=None) -> None:
-    _check(ctx, lib().dwdp_route_scored_grad(ctx, _ptr(logits), _ptr(topk_ids), _ptr(dtopk_w), T, _ptr(seq_offsets),
-                                             n_seqs, ctypes.byref(how), _ptr(counts), _ptr(dbalance), _ptr(dz),
-                                             _ptr(dlogits), dlogits_bf16, _stream(stream)))
+                           dz, dlogits, dlogits_bf16=0, stream=None, choice_bias=None) -> None:
+    """choice_bias: dwdp_route_scored's, where it takes experts out (-inf)."""
+    _check(ctx, lib().dwdp_route_scored_biased_grad(
+        ctx, _ptr(logits), _ptr(topk_ids), _ptr(dtopk_w), _ptr(choice_bias), T, _ptr(seq_offsets), n_seqs,
+        ctypes.byref(how), _ptr(counts), _ptr(dbalance), _ptr(dz), _ptr(dlogits), dlogits_bf16, _stream(stream)))
 
 
 def dwdp_wait_stage(ctx, stage, timeout_ms) -> int:
@@ -742,16 +745,18 @@ class Runtime:
             _check(self.ctx, rc)
 
     def route_scored_grad(self, logits, topk_ids, how: dwdp_scoring, dlogits, dtopk_w=None, counts=None, dbalance=None,
-                          dz=None, seq_offsets=None, stream=None) -> None:
+                          dz=None, seq_offsets=None, stream=None, choice_bias=None) -> None:
         """dlogits [T, E] fp32 or bf16, from dtopk_w [T, k], dbalance and dz
-        [n_seqs] fp32 (each may be None) and balance_loss's counts [n_seqs, E]."""
+        [n_seqs] fp32 (each may be None) and balance_loss's counts [n_seqs, E].
+        choice_bias [E] fp32: route_scored's, where it takes experts out (-inf)."""
         device, call = _device(), "route_scored_grad"
         bf16, i32, f32 = _dtypes or _load_dtypes()
         n_seqs = 1 if seq_offsets is None else seq_offsets.numel() - 1
         T, lp, ip, op = self._router(call, device, logits, topk_ids, seq_offsets, n_seqs)
         E, of_f32, each = self.cfg["n_experts"], (f32,), (n_seqs,)
-        rc = lib().dwdp_route_scored_grad(
-            self.ctx, lp, ip, _like(call, device, "dtopk_w", dtopk_w, of_f32, (T, self.cfg["top_k"])), T, op, n_seqs, how,
+        rc = lib().dwdp_route_scored_biased_grad(
+            self.ctx, lp, ip, _like(call, device, "dtopk_w", dtopk_w, of_f32, (T, self.cfg["top_k"])),
+            _like(call, device, "choice_bias", choice_bias, of_f32, (E,)), T, op, n_seqs, how,
             _like(call, device, "counts", counts, (i32,), (n_seqs, E)),
             _like(call, device, "dbalance", dbalance, of_f32, each), _like(call, device, "dz", dz, of_f32, each),
             _like(call, device, "dlogits", dlogits, (f32, bf16), (T, E)), 1 if dlogits.dtype is bf16 else 0,

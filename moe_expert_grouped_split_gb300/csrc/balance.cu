@@ -620,11 +620,13 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             dw[j] = 0.0f;
             if (p.dw && i < p.k) {
                 id[j] = ring.choice(s, i);
-                if (id[j] >= 0 && id[j] < p.E) {
-                    dw[j] = ring.dw(s, i);
-                } else {
+                if (id[j] < 0 || id[j] >= p.E) {
                     atomicOr(p.err, DERR_BAD_INDEX);
                     id[j] = -1;
+                } else if (p.bias && __ldg(p.bias + id[j]) == -CUDART_INF_F) {
+                    id[j] = -1;  // taken out: its weight is 0 whatever its logit
+                } else {
+                    dw[j] = ring.dw(s, i);
                 }
             }
             chosen_z[j] = id[j] >= 0 ? ring.at[s * R::kStage + id[j]] : -CUDART_INF_F;

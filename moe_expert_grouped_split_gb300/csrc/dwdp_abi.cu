@@ -1144,6 +1144,15 @@ int32_t dwdp_route_scored_grad(dwdp_ctx* ctx, const float* logits, const int32_t
                                int32_t T, const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring,
                                const int32_t* counts, const float* dbalance, const float* dz, void* dlogits,
                                int32_t dlogits_bf16, dwdp_stream_t stream) {
+    return dwdp_route_scored_biased_grad(ctx, logits, topk_ids, dtopk_w, nullptr, T, seq_offsets, n_seqs, scoring,
+                                         counts, dbalance, dz, dlogits, dlogits_bf16, stream);
+}
+
+int32_t dwdp_route_scored_biased_grad(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids,
+                                      const float* dtopk_w, const float* choice_bias, int32_t T,
+                                      const int32_t* seq_offsets, int32_t n_seqs, const dwdp_scoring* scoring,
+                                      const int32_t* counts, const float* dbalance, const float* dz, void* dlogits,
+                                      int32_t dlogits_bf16, dwdp_stream_t stream) {
     const NvtxRange nvtx("dwdp_route_scored_grad T=%d", T);
     const int32_t rc = check_balance(ctx, logits, topk_ids, T, seq_offsets, n_seqs, scoring);
     if (rc != DWDP_OK) return rc;
@@ -1153,12 +1162,14 @@ int32_t dwdp_route_scored_grad(dwdp_ctx* ctx, const float* logits, const int32_t
     if (dbalance && !counts) return fail(ctx, DWDP_ERR_INVALID_ARG, "dbalance needs counts");
     if (T == 0) return DWDP_OK;
     if (!dlogits) return fail(ctx, DWDP_ERR_INVALID_ARG, "dlogits must be non-NULL");
-    if (!aligned16(dtopk_w) || !aligned16(counts) || !aligned16(dbalance) || !aligned16(dz) || !aligned16(dlogits))
+    if (!aligned16(dtopk_w) || !aligned16(choice_bias) || !aligned16(counts) || !aligned16(dbalance) || !aligned16(dz) ||
+        !aligned16(dlogits))
         return fail(ctx, DWDP_ERR_INVALID_ARG, "every pointer must be 16-byte aligned");
     RouterGradArgs p{};
     p.logits = logits;
     p.ids = topk_ids;
     p.dw = dtopk_w;
+    p.bias = choice_bias;
     p.offsets = seq_offsets;
     p.counts = counts;
     p.dbalance = dbalance;

@@ -318,6 +318,7 @@ struct RouterGradArgs {
     const float* logits;
     const int32_t* ids;
     const float* dw;
+    const float* bias;  // of the choice; null: no expert was taken out
     const int32_t* offsets;
     const int32_t* counts;
     const float* dbalance;

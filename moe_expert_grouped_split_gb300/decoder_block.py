@@ -175,7 +175,7 @@ class DecoderBlockTail:
                                 losses.mean_p, losses.balance, losses.z, ws, ws.numel())
             dlogits = torch.empty((T, E), **bf16)
             self.rt.route_scored_grad(rb.logits, rb.topk_ids, self.how, dlogits, dtopk_w=dtopk_w, counts=losses.counts,
-                                      dbalance=dbalance, dz=dz, seq_offsets=seq_offsets)
+                                      dbalance=dbalance, dz=dz, seq_offsets=seq_offsets, choice_bias=self.choice_bias)
             # the GEMM takes rows of multiples of 64 elements
             up = lambda n: -(-n // 64) * 64  # noqa: E731
             left, w_t = torch.zeros((T, up(E)), **bf16), torch.zeros((1, H, up(E)), **bf16)

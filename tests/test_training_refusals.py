@@ -110,3 +110,8 @@ def test_calls_without_a_context(lib):
     sc = B.scoring()
     assert lib.dwdp_balance_loss(None, P, P, 4, None, 1, ctypes.byref(sc), P, P, P, P, P, 1 << 20, None) == INVALID
     assert lib.dwdp_route_scored_grad(None, P, P, P, 4, None, 1, ctypes.byref(sc), P, P, P, P, 0, None) == INVALID
+
+
+def test_biased_gradient_without_a_context(lib):
+    sc = B.scoring()
+    assert lib.dwdp_route_scored_biased_grad(None, P, P, P, P, 4, None, 1, ctypes.byref(sc), P, P, P, P, 0, None) == INVALID
