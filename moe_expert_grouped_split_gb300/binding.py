@@ -722,25 +722,30 @@ class Runtime:
         """(tokens, addresses of logits, topk_ids and seq_offsets)."""
         bf16, i32, f32 = _dtypes or _load_dtypes()
         T, E, k = logits.shape[0], self.cfg["n_experts"], self.cfg["top_k"]
-        if seq_offsets is None and n_seqs != 1:
-            raise ValueError(f"{call}: {n_seqs} sequences need seq_offsets")
+        if n_seqs < 1 or (seq_offsets is None and n_seqs != 1):
+            raise ValueError(f"{call}: {n_seqs} sequences; at least one, and more need seq_offsets")
         return (T, _like(call, device, "logits", logits, (f32,), (T, E)),
                 _like(call, device, "topk_ids", topk_ids, (i32,), (T, k)),
                 _like(call, device, "seq_offsets", seq_offsets, (i32,), (n_seqs + 1,)))
 
     def balance_loss(self, logits, topk_ids, how: dwdp_scoring, out: BalanceBuffers, seq_offsets=None,
-                     stream=None) -> None:
+                     stream=None, ws=None) -> None:
         """logits [T, E] fp32 and topk_ids [T, k] int32 as route_scored gives
         them (RouteBuffers' first T rows); seq_offsets int32 [out.n_seqs + 1] or
-        None (one sequence).  The workspace: Runtime(min_ws_bytes=
-        dwdp_balance_workspace_bytes(...))."""
+        None (one sequence).  The workspace: ws, uint8, or the context's own, of
+        Runtime(min_ws_bytes=dwdp_balance_workspace_bytes(...))."""
         device, call = _device(), "balance_loss"
         T, lp, ip, op = self._router(call, device, logits, topk_ids, seq_offsets, out.n_seqs)
         if out.E != self.cfg["n_experts"] or out.counts.get_device() != device:
             raise ValueError(f"{call}: buffers for {out.E} experts on {out.counts.device}")
+        if ws is None:
+            wp, ws_bytes = self.ws.data_ptr(), self.ws_bytes
+        else:
+            import torch
+            wp, ws_bytes = _like(call, device, "ws", ws, (torch.uint8,), (ws.numel(),)), ws.numel()
         rc = lib().dwdp_balance_loss(self.ctx, lp, ip, T, op, out.n_seqs, how, out.counts.data_ptr(),
-                                     out.mean_p.data_ptr(), out.balance.data_ptr(), _ptr(out.z), self.ws.data_ptr(),
-                                     self.ws_bytes, _stream(stream))
+                                     out.mean_p.data_ptr(), out.balance.data_ptr(), _ptr(out.z), wp, ws_bytes,
+                                     _stream(stream))
         if rc:
             _check(self.ctx, rc)
 

@@ -169,10 +169,11 @@ class DecoderBlockTail:
                 raise ValueError("no tokens")
             bf16, f32 = dict(dtype=torch.bfloat16, device=dev), dict(dtype=torch.float32, device=dev)
             S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+            if S < 1:
+                raise ValueError(f"seq_offsets: {seq_offsets.numel()} elements; two at least are needed")
             rb, losses = kept.rb, B.BalanceBuffers(S, E, device=dev)
             ws = torch.empty(B.dwdp_balance_workspace_bytes(T, E, S), dtype=torch.uint8, device=dev)
-            B.dwdp_balance_loss(self.rt.ctx, rb.logits, rb.topk_ids, T, seq_offsets, S, self.how, losses.counts,
-                                losses.mean_p, losses.balance, losses.z, ws, ws.numel())
+            self.rt.balance_loss(rb.logits, rb.topk_ids, self.how, losses, seq_offsets=seq_offsets, ws=ws)
             dlogits = torch.empty((T, E), **bf16)
             self.rt.route_scored_grad(rb.logits, rb.topk_ids, self.how, dlogits, dtopk_w=dtopk_w, counts=losses.counts,
                                       dbalance=dbalance, dz=dz, seq_offsets=seq_offsets, choice_bias=self.choice_bias)
