@@ -41,7 +41,7 @@ class Kept:
     def __init__(self, T: int, H: int, E: int, k: int, device="cuda"):
         e4m3 = dict(dtype=torch.float8_e4m3fn, device=device)
         f32 = dict(dtype=torch.float32, device=device)
-        self.T = T
+        self.T, self.of = T, (T, H, E, k)
         self.y_codes, self.h_codes = torch.empty((T, H), **e4m3), torch.empty((T, H), **e4m3)
         self.y_scale, self.h_scale, self.rstd = torch.empty(T, **f32), torch.empty(T, **f32), torch.empty((T, 2), **f32)
         self.x = torch.empty((T, H), dtype=torch.bfloat16, device=device)
@@ -110,6 +110,12 @@ class DecoderBlockTail:
         """Room for what a call of T tokens leaves for balance_grad."""
         return Kept(T, self.y.shape[1], self.rt.cfg["n_experts"], self.rt.cfg["top_k"], self.y.device)
 
+    def _kept_here(self, kept, T) -> None:
+        of = (T, self.y.shape[1], self.rt.cfg["n_experts"], self.rt.cfg["top_k"])
+        if kept is not None and (kept.of != of or kept.x.device != self.y.device):
+            raise ValueError(f"kept is for tokens, width, experts, choices {kept.of} on {kept.x.device}; "
+                             f"{of} on {self.y.device} are needed")
+
     def __call__(self, attn, adapter_ids, residual, stage: int = 0, stream=None, gate=None, row_offsets=None,
                  kept: Kept | None = None):
         """attn [T, D]: the attention's output; adapter_ids [T] int32 (-1:
@@ -123,6 +129,7 @@ class DecoderBlockTail:
         _dense("attn", attn, (T, D), torch.bfloat16)
         _dense("adapter_ids", adapter_ids, (T,), torch.int32)
         _dense("residual", residual, (T, H), torch.bfloat16)
+        self._kept_here(kept, T)
         y, x, out = self.y[:T], self.x[:T], self.out[:T]
         if T == 0:
             return out
@@ -132,8 +139,6 @@ class DecoderBlockTail:
                         self.lora_ws, self.lora_ws.numel(), stream)
         rb = self.rb
         if kept is not None:
-            if kept.T != T:
-                raise ValueError(f"{T} tokens; kept is for {kept.T}")
             x, rb = kept.x, kept.rb
         if self.plain and gate is None and kept is None:
             B.dwdp_add_rmsnorm(y, T, H, self.norm_weight, self.eps, x, residual=residual, residual_out=residual,
@@ -167,6 +172,7 @@ class DecoderBlockTail:
             T, H, E, dev = kept.T, self.y.shape[1], self.rt.cfg["n_experts"], self.y.device
             if T == 0:
                 raise ValueError("no tokens")
+            self._kept_here(kept, T)
             bf16, f32 = dict(dtype=torch.bfloat16, device=dev), dict(dtype=torch.float32, device=dev)
             S = 1 if seq_offsets is None else seq_offsets.numel() - 1
             if S < 1:

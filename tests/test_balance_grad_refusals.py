@@ -72,3 +72,22 @@ def test_workspace(block, bad):
         call(torch.zeros(1 << 16, dtype=torch.uint8))
     with pytest.raises(ValueError, match="ws"):
         call(bad)
+
+
+@pytest.mark.parametrize("of", [(T - 1, H, E, 2), (T + 1, H, E, 2), (T, H // 2, E, 2), (T, H, E // 2, 2), (T, H, 2 * E, 2),
+                                (T, H, E, 1), (T, H, E, 3)], ids=str)
+def test_a_call_that_would_leave_its_rows_in_another_blocks(block, of, monkeypatch):
+    """Refused before the first call of the library, which here takes everything."""
+    called = []
+    calls = types.SimpleNamespace(**{n: (lambda *a, n=n: called.append(n) or 0) for n, _, _ in B.SIGNATURES})
+    block.norm  # asks for its workspace's size
+    block.rt.ws, block.rt.ws_bytes = torch.empty(256, dtype=torch.uint8), 256
+    monkeypatch.setattr(B, "_lib", calls)
+    monkeypatch.setattr(B, "lib", lambda: calls)
+    args = (torch.zeros((T, D), dtype=torch.bfloat16), torch.zeros(T, dtype=torch.int32), torch.zeros((T, H), dtype=torch.bfloat16))
+    block(*args, kept=block.keep(T))
+    assert "dwdp_sandwich_norm" in called and "dwdp_route_scored" in called
+    called.clear()
+    with pytest.raises(ValueError, match="kept"):
+        block(*args, kept=Kept(*of, "cpu"))
+    assert not called
