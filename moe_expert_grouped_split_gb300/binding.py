@@ -524,7 +524,8 @@ class SandwichNorm:
     that are not asked for stay None.  pre_weight, post_weight: bf16 [H] or None.
     gate: bf16 [H] or [groups, H], with row_offsets int32 [groups + 1], up to
     max_groups of them.  One object serves one host thread, and its gradients,
-    captured ones too, one stream at a time (they share its workspace)."""
+    captured ones too, one stream at a time (they share its workspace).  It
+    belongs to the device that is current when it is made."""
 
     def __init__(self, H, max_rows, pre_weight=None, post_weight=None, block_scale=1.0, residual_scale=1.0, eps=1e-6,
                  max_groups=1, device="cuda"):
@@ -534,8 +535,9 @@ class SandwichNorm:
         self._bf16, self._i32, self._f32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
         self._e4m3, self._kept = (torch.float8_e4m3fn, torch.uint8), None
         self._row = torch.Size((H,))
+        self._index = _device()
         for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
-            _like("SandwichNorm", _device(), name, w, self._bf16, self._row)
+            _like("SandwichNorm", self._index, name, w, self._bf16, self._row)
         self._how = sandwich(pre_weight, post_weight, None, None, 0, block_scale, residual_scale, eps)
         self.ws_bytes = dwdp_sandwich_grad_workspace_bytes(max_rows, H)
         self._device_name, self._ws = device, None
@@ -547,6 +549,13 @@ class SandwichNorm:
             import torch
             self._ws = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=self._device_name)
         return self._ws
+
+    def _device_of(self, call) -> int:
+        """The current device; ValueError where the weights are on another."""
+        device = _device()
+        if device != self._index:
+            raise ValueError(f"{call}: made on cuda:{self._index}, called on cuda:{device}")
+        return device
 
     def _rows_of(self, call, device, x, codes=False):
         """(rows, stride, address) of x, whose rows may lie apart."""
@@ -581,7 +590,8 @@ class SandwichNorm:
         """x [rows, H] bf16 (rows may lie apart); residual, residual_out, out
         [rows, H] bf16; codes, x_codes, h_codes [rows, H] E4M3 (or uint8);
         row_scale, x_scale, h_scale [rows] and rstd [rows, 2] fp32."""
-        device, call = _device(), "sandwich norm"
+        call = "sandwich norm"
+        device = self._device_of(call)
         rows, stride, xp = self._rows_of(call, device, x)
         if gate is not None or row_offsets is not None or self._how.n_groups:
             self._set_groups(call, device, gate, row_offsets)
@@ -615,7 +625,8 @@ class SandwichNorm:
         apart); h likewise, dense; rstd [rows, 2] fp32; dout, dresidual_out, dx,
         dresidual [rows, H] bf16; dpost_weight, dpre_weight [H] and dgate (of
         gate's shape) fp32."""
-        device, call = _device(), "sandwich norm's gradient"
+        call = "sandwich norm's gradient"
+        device = self._device_of(call)
         first = next((t for t in (x, dout, dresidual_out) if t is not None), None)
         if first is None:
             raise ValueError(f"{call}: neither x nor dout nor dresidual_out")
@@ -720,6 +731,8 @@ class Runtime:
 
     def _router(self, call, device, logits, topk_ids, seq_offsets, n_seqs):
         """(tokens, addresses of logits, topk_ids and seq_offsets)."""
+        if device != self.ws.get_device():
+            raise ValueError(f"{call}: the context is on {self.ws.device}, the current device is cuda:{device}")
         bf16, i32, f32 = _dtypes or _load_dtypes()
         T, E, k = logits.shape[0], self.cfg["n_experts"], self.cfg["top_k"]
         if n_seqs < 1 or (seq_offsets is None and n_seqs != 1):

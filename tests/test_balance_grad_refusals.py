@@ -19,6 +19,7 @@ def block(monkeypatch):
     monkeypatch.setattr(B, "_stream", lambda s: None)
     rt = object.__new__(B.Runtime)
     rt.ctx, rt.weight_dtype, rt.cfg = None, B.DTYPE_BF16, dict(hidden=H, max_tokens=T, n_experts=E, top_k=2)
+    rt.ws, rt.ws_bytes = torch.empty(256, dtype=torch.uint8), 256
     bf16 = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     return DecoderBlockTail(rt, 0, bf16(H, D), bf16(N, R, D), bf16(N, H, R), torch.ones(N), bf16(H), bf16(E, H),
                             torch.zeros(E), B.scoring())
@@ -81,7 +82,6 @@ def test_a_call_that_would_leave_its_rows_in_another_blocks(block, of, monkeypat
     called = []
     calls = types.SimpleNamespace(**{n: (lambda *a, n=n: called.append(n) or 0) for n, _, _ in B.SIGNATURES})
     block.norm  # asks for its workspace's size
-    block.rt.ws, block.rt.ws_bytes = torch.empty(256, dtype=torch.uint8), 256
     monkeypatch.setattr(B, "_lib", calls)
     monkeypatch.setattr(B, "lib", lambda: calls)
     args = (torch.zeros((T, D), dtype=torch.bfloat16), torch.zeros(T, dtype=torch.int32), torch.zeros((T, H), dtype=torch.bfloat16))
