@@ -540,14 +540,27 @@ class SandwichNorm:
             _like("SandwichNorm", self._index, name, w, self._bf16, self._row)
         self._how = sandwich(pre_weight, post_weight, None, None, 0, block_scale, residual_scale, eps)
         self.ws_bytes = dwdp_sandwich_grad_workspace_bytes(max_rows, H)
-        self._device_name, self._ws = device, None
+        self._device_name, self._ws, self._ws_streams = device, None, set()
 
     @property
     def ws(self):
         """The gradients' workspace, made when first used."""
-        if self._ws is None:
+        return self._workspace(None, _stream(None))
+
+    def _workspace(self, stream, handle):
+        """The workspace for a call on `stream`: made there when first used (memory
+        that another stream freed may still be in use by it), and given back
+        only when every stream that it was used on is done with it."""
+        if handle not in self._ws_streams:
             import torch
-            self._ws = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=self._device_name)
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            if self._ws is None:
+                with torch.cuda.stream(stream):  # None: the current one
+                    self._ws = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=self._device_name)
+            else:
+                self._ws.record_stream(stream or torch.cuda.current_stream())
+            self._ws_streams.add(handle)
         return self._ws
 
     def _device_of(self, call) -> int:
@@ -637,8 +650,8 @@ class SandwichNorm:
             raise ValueError(f"{call}: {rows} rows; max_rows is {self.max_rows}")
         G = self._set_groups(call, device, gate, row_offsets)
         bf16, f32, full, one, row = self._bf16, self._f32, (rows, self.H), (rows,), self._row
-        like = _like
-        ws = self.ws
+        like, handle = _like, _stream(stream)
+        ws = self._workspace(stream, handle)
         rc = lib().dwdp_sandwich_norm_grad(
             self._how, xp, stride, like(call, device, "x_scale", x_scale, f32, one),
             like(call, device, "h", h, bf16 if h_scale is None else self._e4m3, full),
@@ -648,7 +661,7 @@ class SandwichNorm:
             like(call, device, "dpost_weight", dpost_weight, f32, row),
             like(call, device, "dpre_weight", dpre_weight, f32, row),
             like(call, device, "dgate", dgate, f32, gate.shape if gate is not None else (G, self.H)), ws.data_ptr(),
-            self.ws_bytes, _stream(stream))
+            self.ws_bytes, handle)
         if rc:
             _check(None, rc)
 
