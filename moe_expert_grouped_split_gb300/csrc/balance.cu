@@ -26,7 +26,8 @@ namespace {
 constexpr int kWarps = 16, kGradWarps = 8;  // of a block: the losses', the gradients'
 // A token's choices in each of its lanes, for the most that E experts can have.
 __host__ __device__ constexpr int choices_a_lane(int lanes) { return lanes >= 32 ? 1 : lanes == 16 ? 2 : 4; }
-constexpr float kLeast = 1e-20f, kMost = 1e34f;
+// (kMost: the sums times gradients of up to 2^90, a loss' scale in them, stay in binary32's range)
+constexpr float kLeast = 1e-20f, kMost = 0x1p36f;
 // exp(kTop) is 2^125.99, the most whose reciprocal is no subnormal, which
 // would be taken for 0: a sigmoid's exponents stop there, where 1 - s is 2^-126.
 constexpr float kTop = 87.33f;
@@ -223,7 +224,7 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         terms(true, exp_fast(c));
     }
     z_c = c;
-    if (want_z && __any_sync(0xffffffffu, !(z_sum <= kMost))) {  // logits of 79 and more
+    if (want_z && __any_sync(0xffffffffu, !(z_sum <= kMost))) {
         float e[4 * V];
         z_sum = soft_terms<LANES, V>(z, e, z_c);
     }

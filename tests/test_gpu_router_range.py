@@ -71,3 +71,20 @@ def test_logits_whose_exponentials_reciprocal_is_subnormal(how, E, k):
             check_grad(m, out.counts, **parts)
         m.z[:] = large[:, None]
     m.close()
+
+
+@pytest.mark.parametrize("how", HOWS, ids=str)
+@pytest.mark.parametrize("E, k", [(9, 3), (24, 4), (256, 8), (600, 8)])
+def test_large_logits_and_scaled_losses(how, E, k):
+    """Logits around 20 to 79, under gradients of a loss times 2^24: their product
+    is beyond binary32 where neither factor is."""
+    T = 60
+    m = Made(T, E, k, [0, 30, T], how, seed=E)
+    m.z += 20 + torch.arange(T, device="cuda")[:, None]
+    m.dw *= 2.0 ** 24
+    m.db *= 2.0 ** 24
+    m.dz *= 2.0 ** 24
+    counts = m.losses().counts
+    for parts in (dict(), dict(w=False, z=False), dict(b=False, z=False), dict(b=False, w=False)):
+        check_grad(m, counts, **parts)
+    m.close()
