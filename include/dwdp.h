@@ -687,10 +687,11 @@ size_t dwdp_sandwich_grad_workspace_bytes(int64_t rows, int32_t H);
  *   mean_p [n_seqs][E]  mean of p over the sequence
  *   balance [n_seqs]    E / (k T_b) sum_e counts mean_p (1 when all is even)
  *   z [n_seqs]          mean of logsumexp(z)^2; NULL = not computed
- * all zero for a sequence without tokens.  Sums are binary32, shares right to
- * a few units in the last place times the logits' spread (approximate
- * exponentials).  Of `scoring` only score is used.  A NaN or infinite logit may
- * make its sequence's mean_p, balance and z NaN.  An id outside [0, E) is not
+ * all zero for a sequence without tokens.  Sums are binary32; a share is right
+ * to (2 m + 24) 2^-23 of itself, m the logits' spread where the sum of exp(z)
+ * (softmax) or s lies outside 2^-36 .. 2^36, else at most 32 more (approximate
+ * exponentials of the logits as they are).  Of `scoring` only score is used.  A
+ * NaN or infinite logit may make its sequence's mean_p, balance and z NaN.  An id outside [0, E) is not
  * counted; the device error word reports it (DEVICE_CHECK).  T at most
  * max_tokens and 2^30.  ws: dwdp_balance_workspace_bytes(T, E, n_seqs) bytes,
  * device, one for each of calls that may overlap.  All pointers 16-byte aligned.  Enqueued on `stream`.

@@ -8,7 +8,8 @@
 // for the largest logit: with exp(z) (softmax) or s = 1 / (1 + exp(-z))
 // (sigmoid) as they are, the sum says whether binary32 held them, and only a
 // token whose sum lies outside [kLeast, kMost] is taken again relative to its
-// largest logit.  For the sigmoid with c = min(that, 0), else 0:
+// largest logit.  (An exponential's relative error goes with its argument: so
+// that is at most 32 more than the logits' spread.)  For the sigmoid with c = min(that, 0), else 0:
 //   t = exp(z - c),  r = 1 / (1 + t exp(c)) = 1 - s,  u = t r = exp(-c) s,
 //   p = u / sum u
 // so neither small scores nor scores next to 1 lose their digits, and sum t
@@ -27,7 +28,7 @@ constexpr int kWarps = 16, kGradWarps = 8;  // of a block: the losses', the grad
 // A token's choices in each of its lanes, for the most that E experts can have.
 __host__ __device__ constexpr int choices_a_lane(int lanes) { return lanes >= 32 ? 1 : lanes == 16 ? 2 : 4; }
 // (kMost: the sums times gradients of up to 2^90, a loss' scale in them, stay in binary32's range)
-constexpr float kLeast = 1e-20f, kMost = 0x1p36f;
+constexpr float kLeast = 0x1p-36f, kMost = 0x1p36f;
 // exp(kTop) is 2^125.99, the most whose reciprocal is no subnormal, which
 // would be taken for 0: a sigmoid's exponents stop there, where 1 - s is 2^-126.
 constexpr float kTop = 87.33f;

@@ -88,3 +88,20 @@ def test_large_logits_and_scaled_losses(how, E, k):
     for parts in (dict(), dict(w=False, z=False), dict(b=False, z=False), dict(b=False, w=False)):
         check_grad(m, counts, **parts)
     m.close()
+
+
+@pytest.mark.parametrize("how", HOWS, ids=str)
+@pytest.mark.parametrize("at", [-85.0, -46.0, 33.0, 70.0])
+def test_logits_far_from_zero_and_near_each_other(how, at):
+    """A share's error goes with the logits' spread (0.5), not with where they
+    lie: exponentials of at most 0.5 are off by 2^-22, and a sum over 64 experts
+    (4 terms, 4 exchanges) with its reciprocal and one product by 10 2^-24; as
+    much for 1 - s, and half an ulp of the quotient that the oracle is not off by.
+    s next to 1 is off by the error of 1 - s only."""
+    T, E, k = 200, 64, 4
+    m = Made(T, E, k, list(range(T + 1)), how, seed=3)
+    g = torch.Generator("cuda").manual_seed(4)
+    m.z = at + 0.5 * torch.rand((T, E), generator=g, device="cuda")
+    p = m.shares(m.z.double())
+    near(m.losses().mean_p, p, (2 * 2.0 ** -22 + 11 * 2.0 ** -24) * p)
+    m.close()
