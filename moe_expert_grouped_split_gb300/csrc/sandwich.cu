@@ -126,6 +126,33 @@ struct Asked {
     static constexpr bool POST = POST_, PRE = PRE_, CODES = CODES_, KEPT = KEPT_;
 };
 
+// Waits for the bulk copies of row r of `rows`, in stage `stage`, 2 s at most.
+// A thread whose wait ran out gets a `poison` of NaN, else 0: it waits for no
+// other row, all that it writes from there on is NaN (these calls have no error
+// word), and the one that asks for rows asks for no more.  That one also gives
+// those that are on their way 2 s to land, as the shared memory goes to another block
+// after this one.
+template <int STAGES>
+__device__ __forceinline__ void wait_row(uint32_t full, int r, int rows, int stage, uint32_t parity, float& poison) {
+    if (poison != 0.0f || mbar_try_wait(full + 8 * stage, parity)) return;
+    uint64_t since = global_timer();
+    while (!mbar_try_wait(full + 8 * stage, parity)) {
+        if (global_timer() - since <= kWaitLimitNs) continue;
+        poison = CUDART_NAN_F;
+        if (threadIdx.x != 0) return;
+        since = global_timer();
+        for (const int to = min(r + STAGES, rows); r < to; ++r) {
+            while (!mbar_try_wait(full + 8 * stage, parity) && global_timer() - since <= kWaitLimitNs) {
+            }
+            if (++stage == STAGES) {
+                stage = 0;
+                parity ^= 1;
+            }
+        }
+        return;
+    }
+}
+
 // c gate post of a vector's elements.
 __device__ __forceinline__ void block_factor(const SandwichArgs& p, const uint4* gate, const uint4* post, int i, four& f) {
 #pragma unroll
@@ -146,10 +173,11 @@ __device__ __forceinline__ void block_factor(const SandwichArgs& p, const uint4*
 // One row of which the thread has VPT vectors: x and the residual (zeros where
 // there is nothing), factor(j, f) = c gate post and pre.  vec: the first
 // one's place among all vectors, the others n on each; held[j]: to be stored.
+// poison: 0, or NaN for all outputs.
 template <class ASK, int VPT, class Factor>
 __device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row, int64_t vec, int n, const bool (&held)[VPT],
                                              const uint4 (&x)[VPT], const uint4 (&r)[VPT], const uint4 (&pre)[VPT],
-                                             Factor factor, float4 (*red)[32], int& turn) {
+                                             Factor factor, float4 (*red)[32], int& turn, float poison = 0.0f) {
     float rx = 1.0f, x_inv = 0.0f;
     const bool first = threadIdx.x == 0;
     // 1 / rms from the sum of squares; where that passes the limit it is taken
@@ -158,15 +186,15 @@ __device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row,
         float scaled = 1.0f;
         if (!(ss < kSquaresLimit)) {
             scaled = kDownScale;
-            pair again = 0;
+            pair again = two(poison);
             squares(two(scaled), again);
             ss = block_sum_max2(sum_of(again), 0.0f, 0.0f, red, turn).x;
         }
         return rsqrtf(fmaf(ss, p.one_nth, p.eps * scaled * scaled)) * scaled;
     };
     if constexpr (ASK::POST || ASK::KEPT) {
-        pair ss = 0;
-        float ax = 0.0f;
+        pair ss = two(poison);
+        float ax = poison;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             four f;
@@ -196,6 +224,7 @@ __device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row,
             if (first && p.x_scale) p.x_scale[row] = code_scale(sums.y);
         }
     }
+    const pair by_residual = two(p.residual_scale + poison);
     four h[VPT];
     pair ss = 0;
     float ah = 0.0f, ay = 0.0f;
@@ -210,7 +239,7 @@ __device__ __forceinline__ void sandwich_row(const SandwichArgs& p, int64_t row,
         unpack4(r[j], w);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            h[j][c] = fma2(two(p.residual_scale), w[c], f[c]);
+            h[j][c] = fma2(by_residual, w[c], f[c]);
             if constexpr (ASK::PRE) ss = fma2(h[j][c], h[j][c], ss);
         }
         if constexpr (ASK::KEPT) ah = max_of(h[j], ah);
@@ -316,8 +345,9 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
     char* const own = smem + tid * 16;
     ulonglong2* const factors = reinterpret_cast<ulonglong2*>(smem + STAGES * stage_bytes) + tid;
     const uint32_t full = smem_u32(&red[1][30]);
+    float poison = 0.0f;
     auto fetch = [&](int64_t row, int stage) {
-        if (tid != 0 || row >= hi) return;
+        if (tid != 0 || row >= hi || poison != 0.0f) return;
         const uint32_t to = smem_u32(smem) + stage * stage_bytes, bar = full + 8 * stage, bytes = p.nv * 16;
         mbar_arrive_expect_tx(bar, p.residual ? 2 * bytes : bytes);
         bulk_load(to, p.x + row * p.x_vecs, bytes, bar);
@@ -352,16 +382,12 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
             factors[(2 * j + 1) * n] = make_ulonglong2(f[2], f[3]);
         }
     };
-    bool open = !p.row_offsets, lost = false;
+    bool open = !p.row_offsets;
     if (open) open_group(0);
     const int rows = (int)(hi - lo);
     int change = open ? rows : 0, stage = 0, parity = 0, turn = 0;
     for (int i = 0; i < rows; ++i) {
-        // 2 s at most, and then for no other row: what is written from here on is NaN
-        if (!lost && !mbar_try_wait(full + 8 * stage, parity)) {
-            const uint64_t since = global_timer();
-            while (!lost && !mbar_try_wait(full + 8 * stage, parity)) lost = global_timer() - since > kWaitLimitNs;
-        }
+        wait_row<STAGES>(full, i, rows, stage, parity, poison);
         if (i == change) {
             const int group = group_of(p.row_offsets, p.n_groups, lo + i);
             open = group >= 0;
@@ -378,11 +404,10 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
             for (int j = 0; j < VPT; ++j) {
                 x[j] = *reinterpret_cast<const uint4*>(in + j * n * 16);
                 r[j] = *reinterpret_cast<const uint4*>(in + (VPT + j) * n * 16);
-                if (lost) x[j].x = r[j].x = 0xffffffffu;
             }
             sandwich_row<ASK, VPT>(
                 p, lo + i, (lo + i) * p.nv + tid, n, held, x, r, pre, [&](int j, four& f) { load4(factors + 2 * j * n, n, f); }, red,
-                turn);
+                turn, poison);
         }
         // everybody has taken his part of the stage: they were at a barrier of
         // the row since, where it has one (and nobody is a phase of the stage's
@@ -400,6 +425,22 @@ __global__ void __launch_bounds__(512, 2) sandwich_stream_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------ gradients --
+// As wait_row above for the gradients' rows, in two parts and without a value to
+// poison with: one form for both kernels costs either the norm 8% (8192 x 7168,
+// rows kept: 107 us for 99) or the gradients 20% (138 for 113, spills).
+__device__ __forceinline__ void wait_row(uint32_t bar, uint32_t parity, bool& lost) {
+    if (lost || mbar_try_wait(bar, parity)) return;
+    const uint64_t since = global_timer();
+    while (!lost && !mbar_try_wait(bar, parity)) lost = global_timer() - since > kWaitLimitNs;
+}
+// For the thread that asked for them, at the end: rows `from` .. `to` - 1 were never seen.
+__device__ __forceinline__ void wait_lost_rows(uint32_t full, int stages, int from, int to) {
+    const uint64_t since = global_timer();
+    for (int r = from; r < to; ++r)
+        while (!mbar_try_wait(full + 8 * (r % stages), r / stages & 1) && global_timer() - since <= kWaitLimitNs) {
+        }
+}
+
 // How a row was kept.
 enum Kept : int { KEPT_NOT, KEPT_BF16, KEPT_E4M3 };
 __host__ __device__ constexpr int kept_bytes(int k) { return k == KEPT_E4M3 ? 8 : k == KEPT_BF16 ? 16 : 0; }
@@ -518,10 +559,12 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
     const bool held[VPT] = {tid < own_vecs, tid + n < own_vecs};
     const uint32_t full = smem_u32(full_bars);
     const int row_bytes = p.nv * (kX + kH + (PRE ? 16 : 0) + (p.dres ? 16 : 0));
+    bool lost = false;
+    int lost_at = 0;
     // asks for a row into stage `stage`, which begins at `at`
     auto fetch = [&](int64_t row, int stage, int at) {
         if (BULK) {
-            if (tid != 0 || row >= hi) return;
+            if (tid != 0 || row >= hi || lost) return;
             const uint32_t to = smem_u32(smem) + at, bar = full + 8 * stage;
             mbar_arrive_expect_tx(bar, row_bytes);
             if constexpr (X != KEPT_NOT)
@@ -593,7 +636,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
     const bool to_dresidual[VPT] = {held[0] && p.dresidual, held[1] && p.dresidual};
     int group = 0, in = 0, turn = 0, stage = 0, parity = 0;
     int64_t begin = 0, end = p.rows, next_end = 0;  // of the group; of the one behind it
-    bool open = !p.row_offsets, any = false, lost = false;
+    bool open = !p.row_offsets, any = false;
     // block_scale times a weight's or gate's elements (1 where there is none)
     auto scaled = [&](const uint4* w, int64_t vec, four& f) {
         if (w) {
@@ -673,11 +716,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
             later = row_factors(lo + r + 32 + lane);
         }
         if (BULK) {
-            // 2 s at most, and then for no other row: what is written from here on is NaN
-            if (!lost && !mbar_try_wait(full + 8 * stage, parity)) {
-                const uint64_t since = global_timer();
-                while (!lost && !mbar_try_wait(full + 8 * stage, parity)) lost = global_timer() - since > kWaitLimitNs;
-            }
+            wait_row(full + 8 * stage, parity, lost);
+            lost_at += !lost;
         } else {
             wait_copies<kGradStages - 1>();
         }
@@ -714,6 +754,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 unpack4(*reinterpret_cast<const uint4*>(own + in + (VPT + j) * n * 16), e[j]);
+                if constexpr (BULK && !PRE) {
+                    if (lost) e[j][0] = e[j][1] = e[j][2] = e[j][3] = two(CUDART_NAN_F);
+                }
                 if constexpr (PRE) {
                     four w, dy;
                     values<HK>(own_h + in + j * n * kH, two(h_by), hh[j]);
@@ -744,11 +787,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
             const int64_t vec = (lo + r) * p.nv + first;
             if constexpr (PRE || POST) {
                 const float2 s0 = apart(by_h), s1 = apart(q_e), s2 = apart(q_h);
-                const float3 sums = row_sums<SHARED>(s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, red, turn, size);
+                // (lost: m and m2 of the whole block, and with m e below)
+                const float3 sums = row_sums<SHARED>(BULK && lost ? CUDART_NAN_F : s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, red, turn, size);
                 m = rh * sums.x * p.one_nth;
                 m2 = rx * (sums.y - m * sums.z) * p.one_nth;
             }
-            if (BULK && lost) m = m2 = CUDART_NAN_F;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 four t;
@@ -788,11 +831,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
             parity ^= 1;
         }
     }
-    if (lost) {
+    if (BULK && lost) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) dpre[j][c] = sum[j][c] = two(CUDART_NAN_F);
+            for (int c = 0; c < 4; ++c) dpre[j][c] = two(CUDART_NAN_F);
     }
     if (open) close_group();
 #pragma unroll
@@ -803,6 +846,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) sandwich_grad
         if (PRE && p.dpre) store4(partial + 8 * i, dpre[j]);
         if (POST && p.dpost && p.row_offsets && !any) store4(partial + H + 8 * i, none);
     }
+    if (BULK && lost && tid == 0) wait_lost_rows(full, kGradStages, lost_at, min(lost_at + kGradStages, rows));
     if (SHARED) {
         __syncwarp();
         cluster_sync();  // no block leaves while another may write to it
