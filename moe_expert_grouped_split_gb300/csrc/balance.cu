@@ -795,6 +795,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
     }
 }
 
+// kTokens, kGradTokens: of a block at once, the losses' and the gradients' kernel.
 template <int L, int N, int W>
 struct Form {
     static constexpr int LANES = L, V = N, kCols = 4 * V * LANES, kTokens = 32 / LANES * kWarps,
@@ -826,7 +827,11 @@ bool balance_is_few(int64_t T, int n_seqs) { return T <= 8192 && T <= 768 * (int
 // Tokens of a block of the losses' kernel: two blocks an SM of a GB300's 152,
 // whole rounds of a block's warps.
 int balance_chunk(int64_t T, int E) {
-    const int at_once = kWarps * std::max(1, 32 / std::max(4, (E + 3) / 4));
+    int at_once = 0;
+    by_experts(E, [&](auto form) {
+        at_once = decltype(form)::kTokens;
+        return cudaSuccess;
+    });
     const int64_t want = (T + 152 * 2 - 1) / (152 * 2);
     return (int)std::max<int64_t>(at_once, (want + at_once - 1) / at_once * at_once);
 }
