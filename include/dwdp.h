@@ -600,8 +600,9 @@ int32_t dwdp_moe_layer_codes(dwdp_ctx* ctx, int32_t layer, int32_t stage, const 
  *   gate          bf16 [n_groups][H] (device), or NULL (n_groups 0): 1
  *   row_offsets   int32 [n_groups + 1] (device), non-decreasing: gate g is for
  *                 rows row_offsets[g] .. row_offsets[g + 1] - 1, and rows outside
- *                 [row_offsets[0], row_offsets[n_groups]) are left alone:
- *                 not read, not written, no part of any sum.
+ *                 [row_offsets[0], row_offsets[n_groups]) are left alone: not
+ *                 written, no part of any sum, whatever they hold (they may be
+ *                 read, so every array has all its rows)
  *                 NULL: one gate for all rows (n_groups 1)
  *   block_scale, residual_scale  finite constants
  *   eps           of both norms, finite and at least 2^-100 */
