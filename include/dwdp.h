@@ -692,7 +692,8 @@ size_t dwdp_sandwich_grad_workspace_bytes(int64_t rows, int32_t H);
  * to (2 m + 24) 2^-23 of itself, m the logits' spread where the sum of exp(z)
  * (softmax) or s lies outside 2^-36 .. 2^36, else at most 32 more (approximate
  * exponentials of the logits as they are).  Of `scoring` only score is used.  A
- * NaN or infinite logit may make its sequence's mean_p, balance and z NaN.  An id outside [0, E) is not
+ * NaN or infinite logit may make its sequence's mean_p, balance and z NaN; -inf
+ * is a share of 0 where the token has a finite one.  An id outside [0, E) is not
  * counted; the device error word reports it (DEVICE_CHECK).  T at most
  * max_tokens and 2^30.  ws: dwdp_balance_workspace_bytes(T, E, n_seqs) bytes,
  * device, one for each of calls that may overlap.  All pointers 16-byte aligned.  Enqueued on `stream`.
@@ -715,7 +716,8 @@ size_t dwdp_balance_workspace_bytes(int32_t T, int32_t E, int32_t n_seqs);
  * match, serve as well).  Tokens in no sequence get the weights' part only.
  * score, renormalize and scale of `scoring` are used.  The ids of a token are distinct.
  * dlogits [T][E]: fp32, or bf16 when dlogits_bf16 is 1; every element is written.
- * A NaN or infinite logit may make its token's gradient NaN; an id outside [0,
+ * A NaN or infinite logit may make its token's gradient NaN; -inf has a gradient
+ * of 0 where the token, and with renormalize its choice, has a finite one; an id outside [0,
  * E) is skipped and reported as above.  Other arguments as for dwdp_balance_loss;
  * dlogits overlaps none of them.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int32_t dwdp_route_scored_grad(dwdp_ctx* ctx, const float* logits, const int32_t* topk_ids, const float* dtopk_w,
