@@ -10,9 +10,9 @@
 // token whose sum lies outside [kLeast, kMost] is taken again relative to its
 // largest logit.  (An exponential's relative error goes with its argument: so
 // that is at most 32 more than the logits' spread.)  For the sigmoid with c = min(that, 0), else 0:
-//   t = exp(z - c),  r = 1 / (1 + t exp(c)) = 1 - s,  u = t r = exp(-c) s,
+//   t = exp(z - c),  r = 16 / (1 + t exp(c)) = 16 (1 - s),  u = t r = 16 exp(-c) s,
 //   p = u / sum u
-// so neither small scores nor scores next to 1 lose their digits, and sum t
+// (16: the reciprocal of the largest t would be subnormal, and taken for 0) so neither small scores nor scores next to 1 lose their digits, and sum t
 // serves the log-sum-exp as well.
 #include <math_constants.h>
 
@@ -29,9 +29,10 @@ constexpr int kWarps = 16, kGradWarps = 8;  // of a block: the losses', the grad
 __host__ __device__ constexpr int choices_a_lane(int lanes) { return lanes >= 32 ? 1 : lanes == 16 ? 2 : 4; }
 // (kMost: the sums times gradients of up to 2^90, a loss' scale in them, stay in binary32's range)
 constexpr float kLeast = 0x1p-36f, kMost = 0x1p36f;
-// exp(kTop) is 2^125.99, the most whose reciprocal is no subnormal, which
-// would be taken for 0: a sigmoid's exponents stop there, where 1 - s is 2^-126.
+// exp(kTop) is 2^125.99, the most whose reciprocal is no subnormal: a sigmoid's
+// exponents stop there where exp(z) would pass binary32's range.
 constexpr float kTop = 87.33f;
+constexpr float kSigmoidUnit = 16.0f;  // of u and r above
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -188,6 +189,11 @@ __device__ __forceinline__ float soft_terms(const float (&z)[4 * V], float (&e)[
     return sum;
 }
 
+// 16 / (1 + t one)
+__device__ __forceinline__ float sigmoid_rest(float t, float one) {
+    return rcp_fast(fmaf(t, one * (1.0f / kSigmoidUnit), 1.0f / kSigmoidUnit));
+}
+
 // A token's u and r and the sum of u; z_sum, where asked for, gets sum t, and
 // z_c its c.  Columns beyond E get u = 0.
 template <int LANES, int V>
@@ -200,8 +206,8 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         sum = z_sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
-            const float t = exp_fast(min_nan(far ? z[i] - c : z[i], kTop));
-            r[i] = rcp_fast(far ? fmaf(t, one, 1.0f) : t + 1.0f);
+            const float t = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
+            r[i] = sigmoid_rest(t, one);
             u[i] = t * r[i];
             sum += u[i];
             z_sum += t;
@@ -215,7 +221,7 @@ __device__ __forceinline__ float sigmoid_terms(const float (&z)[4 * V], float (&
         }
     };
     terms(false, 1.0f);
-    const bool lost = !(sum >= kLeast);
+    const bool lost = !(sum >= kSigmoidUnit * kLeast);  // too small, or a logit so large that u is inf 0
     if (__any_sync(0xffffffffu, lost)) {
         float m = -CUDART_INF_F;
 #pragma unroll
@@ -697,8 +703,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             for (int i = 0; i < 4 * V; ++i) g[i] += d[i];
             clear();
         }
-        // u = exp(-c) s and r = 1 - s (softmax: 1) of every expert and of the
-        // chosen ones, and all sums at once: of u, u g, and the chosen ones' u, u dw
+        // u = exp(-c) s and r = 1 - s (softmax: r = 1) of every expert, each times 16,
+        // and of the chosen ones, as they are; and all sums at once: of u, u g, and
+        // the chosen ones' u, u dw
         float c = 0.0f, chosen_c = 0.0f, chosen_u[KPL], chosen_r[KPL], chosen_one;
         float4 sums;
         auto terms = [&](bool far) {
@@ -707,9 +714,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
             float a = 0.0f, b = 0.0f, chosen_a = 0.0f, chosen_b = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
-                e[i] = far || SIGMOID ? exp_fast(min_nan(far ? z[i] - c : z[i], kTop)) : exp_fast(z[i]);
+                e[i] = far ? exp_fast(min_nan(z[i] - c, kTop)) : exp_fast(z[i]);
                 if constexpr (SIGMOID) {
-                    r[i] = rcp_fast(far ? fmaf(e[i], one, 1.0f) : e[i] + 1.0f);
+                    r[i] = sigmoid_rest(e[i], one);
                     e[i] *= r[i];
                 }
                 a += e[i];
@@ -729,7 +736,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
         };
         terms(false);
         {
-            const bool lost = !(sums.x >= kLeast && sums.x <= kMost);
+            const bool lost = !(sums.x >= (SIGMOID ? kSigmoidUnit : 1.0f) * kLeast && sums.x <= kMost);  // a sigmoid's u is inf 0 of a large logit
             const bool chosen_lost = p.dw && p.renorm && !(sums.z >= kLeast && sums.z <= kMost);
             if (__any_sync(0xffffffffu, lost || chosen_lost)) {
                 float m = -CUDART_INF_F, chosen_m = -CUDART_INF_F;
@@ -759,11 +766,11 @@ __global__ void __launch_bounds__(32 * kGradWarps, V <= 2 ? 3 : 1) router_grad_k
         }
         if (p.dbalance || !direct) {
             // (shares first: one_sum twice could pass binary32's range)
-            const float mean = sums.y * one_sum;
+            const float mean = sums.y * one_sum, by_sum = SIGMOID ? one_sum * (1.0f / kSigmoidUnit) : one_sum;
 #pragma unroll
             for (int i = 0; i < 4 * V; ++i) {
                 const float p_i = SIGMOID ? e[i] * r[i] : e[i];
-                d[i] = fmaf(p_i * one_sum, g[i] - mean, d[i]);
+                d[i] = fmaf(p_i * by_sum, g[i] - mean, d[i]);
             }
         }
         if (p.dz) {
