@@ -931,8 +931,8 @@ struct GradShape {
     }
     // As many units (rows at once) as a GB300's 152 SMs hold at 128 registers
     // a thread and `smem` bytes a block (the workspace: 0), but no more than one
-    // an SM for less than three rows each (1003 x 2048, 11 gates, 8 bits: 16.3 us;
-    // one row each 18.2, six 18.7).
+    // an SM for less than rows / 3 units (1003 x 2048, 11 gates, 8 bits: four rows
+    // each 16.3 us; two 18.2, seven 18.7).
     int64_t units(int64_t rows, size_t smem) const {
         const int64_t blocks = std::min<int64_t>(512 / threads, (228 << 10) / (smem + 1024));
         return std::max<int64_t>(1, std::min({rows, 152 * blocks / size, std::max<int64_t>(152 / size, rows / 3)}));

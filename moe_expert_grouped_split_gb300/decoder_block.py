@@ -10,9 +10,9 @@ experts the norm's codes go straight to the expert layer
 
 The time of the expert layer, and what has to be staged for it, depend on how
 evenly the router uses the experts.  DecoderBlockTail.balance_grad gives the
-gradients of the router's balance and z losses (and of its weights) by all that
-lies before the experts, which stay as they are: the router's weight, the
-norms', the gates, the projection's output and the residual.  A forward call
+gradients of the router's balance and z losses (and of its weights) by the
+router's weight, the norms', the gates, the projection's output and the
+residual; the experts, the projection's weight and the adapters stay as they are.  A forward call
 that is to be followed by it keeps its rows in 8 bits (Kept).
 
     python -m moe_expert_grouped_split_gb300.decoder_block [tokens]
